@@ -17,6 +17,14 @@
  *                       leaf of a model, in one launch (PSK-Realize, Parameter
  *                       trees; presk "The language", The optimizer).
  *
+ * Around them stand the operators with which a language model's training
+ * step begins and ends: psk_embed and psk_embed_backward (token embedding and
+ * its leaf gradient), psk_dropout, psk_norm_backward (the norm regions'
+ * backward), psk_token_logp and psk_policy_loss (log-probabilities and the
+ * clipped policy loss over vocabulary rows, with its gradient).  Their f32
+ * sums run over fixed trees, not over a declared order: one call's bits
+ * repeat on one device.
+ *
  * Conventions for every call:
  * - Pointers named ptr/x/y/theta/m/v/grad/gamma/beta/workspace are DEVICE
  *   pointers owned by the caller; descriptor structs and arrays of them are
@@ -58,8 +66,9 @@ extern "C" {
 
 /* ------------------------------------------------------- storage types */
 /* PSK_I32 (32-bit integers) is a fusion group's input type for SELECT
- * conditions only; every other argument of every entry point refuses it. */
-typedef enum { PSK_F32 = 0, PSK_BF16 = 1, PSK_I32 = 2 } psk_dtype;
+ * conditions, and with PSK_I64 (64-bit) the type of token ids; every other
+ * argument of every entry point refuses both. */
+typedef enum { PSK_F32 = 0, PSK_BF16 = 1, PSK_I32 = 2, PSK_I64 = 3 } psk_dtype;
 
 /* ======================================================== psk_group_run
  * Program format (postfix; one uint32 token per item; opcode in bits 31..24,
@@ -402,6 +411,105 @@ int psk_adamw_clip_scale(const float* group_sums, const int64_t* groups_per_leaf
                          float* scale, void* stream);
 int psk_adamw_tree_scaled(const psk_leaf* leaves, int32_t n_leaves, const psk_adamw_hparams* hp,
                           const psk_adamw_schedule* sched, const float* scale, void* stream);
+
+/* ======================================================= psk_embed
+ * The token embedding: y[i, :] = RN(RN(table[ids[i], :] * scale)) rounded to
+ * yt, i < tokens; an id outside [0, vocab) marks padding and gives a zero
+ * row.  scale is rounded once to f32.  ids: DEVICE, PSK_I32 or PSK_I64.
+ * table: vocab rows, y: tokens rows of cols elements (f32 or bf16), leading
+ * dimensions ldt, ldy >= cols.  y must not overlap table or ids.  tokens and
+ * vocab < 2^31; tokens or cols == 0 launches nothing. */
+int psk_embed(const void* ids, int32_t idt, int64_t tokens, const void* table, int32_t tt, int64_t vocab,
+              int64_t cols, int64_t ldt, double scale, void* y, int32_t yt, int64_t ldy, void* stream);
+
+/* The embedding's backward: the gradient leaf
+ *   dtable[v, :] = RN(scale * S_v), S_v = the sum of ct[i, :] over ids[i] = v,
+ * zero rows for ids that do not occur; with accumulate != 0
+ * RN(dtable[v, :] + RN(scale * S_v)) where v occurs and other rows left as
+ * they are (a leaf that the output head shares).  Padding positions are not
+ * read into any sum.  No atomics: the positions are sorted by id, in order,
+ * the sorted list is cut into runs of 32 entries, a run's entries of one id
+ * are added left to right in f32, and an id's run sums left to right; the
+ * bits depend on the ids and ct alone.  ct: tokens rows (f32 or bf16, ldc >=
+ * cols); dtable: vocab rows (f32 or bf16, ldd >= cols), overlapping nothing
+ * else.  workspace: 16-byte aligned DEVICE scratch of at least
+ * psk_embed_workspace bytes, no initialisation, one per concurrent call
+ * (calls and captured graphs that may overlap in time must not share it). */
+int psk_embed_workspace(int64_t tokens, int64_t vocab, int64_t cols, uint64_t* bytes);
+int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, const void* ct, int32_t ct_t, int64_t ldc,
+                       double scale, void* dtable, int32_t dt, int64_t vocab, int64_t cols, int64_t ldd,
+                       int32_t accumulate, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* ====================================================== psk_dropout
+ * Dropout of rows x cols elements with a mask that is never stored:
+ *   y[r, c] = [residual[r, c] +] (keep(r, c) ? RN(x[r, c] * s) : +0),
+ * s = RN_f32(1 / (1 - p)), the sum one f32 rounding, the result rounded to yt.
+ * A dropped element's x (a NaN or an infinity too) never reaches the result.
+ * keep(r, c): word c mod 4 of Philox4x32-10 (Salmon et al., "Parallel random
+ * numbers: as easy as 1, 2, 3", 2011) with counter words (c / 4, r, offset's
+ * low and high half) and key words (seed's low and high half) is at least
+ * RN(p 2^32).  The mask depends on r, c, seed and offset only: the backward
+ * is the same call on the cotangent, without residual (the residual's own
+ * gradient is the cotangent), and calls with other offsets are independent.
+ * counter: NULL, or a DEVICE uint64 added to offset (mod 2^64) when the
+ * kernel runs, so that a captured graph's replays can draw new masks.
+ * 0 <= p <= 1.  residual may be NULL.  y may be x or the residual in place
+ * (same type and leading dimension), no other overlap.  rows <= 2^32,
+ * cols <= 2^34; rows or cols == 0 launches nothing. */
+int psk_dropout(const void* x, int32_t xt, const void* residual, int32_t rt, void* y, int32_t yt, int64_t rows,
+                int64_t cols, int64_t ldx, int64_t ldr, int64_t ldy, double p, uint64_t seed, uint64_t offset,
+                const uint64_t* counter, void* stream);
+
+/* ================================================ psk_norm_backward
+ * The backward of psk_norm_region over rows of cols elements, recomputing the
+ * statistics from x: with d = sqrt(mean((x - mu)^2) + eps), xh = (x - mu) / d
+ * (mu = 0 for RMSNorm), g = ct * gamma and row means,
+ *   dx     = (g - [mean g] - xh mean(g xh)) / d      ([.] LayerNorm only)
+ *   dgamma = sum over rows of ct xh;   dbeta = sum over rows of ct
+ * in f32, dx rounded to dxt, dgamma and dbeta to grad_dtype.  gamma may be NULL
+ * (ones); dgamma and dbeta may be NULL (not wanted); RMSNorm takes no dbeta.
+ * x, ct, dx: f32 or bf16 rows, leading dimensions ldx, ldc, ldd >= cols; dx
+ * may be x or ct in place (same type and leading dimension), no other overlap.
+ * cols up to 49152; rows == 0 writes zero dgamma and dbeta.  workspace: as for
+ * psk_embed_backward, psk_norm_backward_workspace bytes. */
+int psk_norm_backward_workspace(int64_t rows, int64_t cols, uint64_t* bytes);
+int psk_norm_backward(const void* x, int32_t xt, const void* ct, int32_t ct_t, void* dx, int32_t dxt, int64_t rows,
+                      int64_t cols, int64_t ldx, int64_t ldc, int64_t ldd, int32_t kind, double eps,
+                      const void* gamma, int32_t param_dtype, void* dgamma, void* dbeta, int32_t grad_dtype,
+                      void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* ================================== psk_token_logp, psk_policy_loss
+ * Over rows of cols logits (f32 or bf16, ldl >= cols), z = scale * x (scale in
+ * [1e-30, 1e30]: the inverse sampling temperature), t = targets[r] (DEVICE,
+ * PSK_I32 or PSK_I64):
+ *   logp[r] = z_t - log(sum_j exp(z_j)).
+ * A target outside [0, cols) marks padding: its row is not read, logp 0.
+ *
+ * psk_policy_loss, per row with weight w (weight[r]; NULL: 1 / rows),
+ * advantage A, ratio = exp(logp - old_logp[r]), q = ref_logp[r] - logp:
+ *   term = -min(ratio A, clamp(ratio, 1 - clip_low, 1 + clip_high) A)
+ *   k    = exp(q) - q - 1                              (0 without ref_logp)
+ *   loss[0] = sum w (term + kl_coef k),   loss[1] = sum w k
+ *   dlogits[r, j] = scale w (-A ratio [ratio A is the minimum]
+ *                            - kl_coef (exp(q) - 1)) ([j = t] - softmax(z)_j)
+ * A row of weight 0 or of a padding target is left out: its logits are not
+ * read, its logp is 0 and its gradient row zero.  A row holding a NaN or +inf
+ * logit, or only -inf, gives NaN; -inf logits otherwise have probability 0.
+ * A zero advantage gives zero terms whatever the (non-NaN) ratio.  Each row's
+ * logp carries an absolute error of a few 1e-7.
+ * logp may be NULL; ref_logp may be NULL if kl_coef is 0; dlogits NULL computes
+ * the loss alone, else rows (type gt, ldg >= cols) written whole, in place of
+ * the logits if wanted (same type and leading dimension).  No other overlap.
+ * cols < 2^31; rows == 0 gives a zero loss.  clip_low in [0, 1], clip_high >=
+ * 0.  workspace: as for psk_embed_backward, psk_policy_loss_workspace bytes. */
+int psk_token_logp(const void* logits, int32_t lt, int64_t rows, int64_t cols, int64_t ldl, double scale,
+                   const void* targets, int32_t tt, float* logp, void* stream);
+int psk_policy_loss_workspace(int64_t rows, int64_t cols, uint64_t* bytes);
+int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int64_t cols, int64_t ldl, double scale,
+                    const void* targets, int32_t tt, const float* old_logp, const float* ref_logp,
+                    const float* advantage, const float* weight, double clip_low, double clip_high, double kl_coef,
+                    float* loss, float* logp, void* dlogits, int32_t gt, int64_t ldg, void* workspace,
+                    uint64_t workspace_bytes, void* stream);
 
 /* Host-only, synchronous: the device status word of the pipelined kernels of
  * the current device (0 = no bounded wait ever timed out; bit 0 = a wait gave

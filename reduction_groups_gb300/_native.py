@@ -12,7 +12,7 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libpsk.so")
 
-PSK_F32, PSK_BF16, PSK_I32 = 0, 1, 2
+PSK_F32, PSK_BF16, PSK_I32, PSK_I64 = 0, 1, 2, 3
 PSK_ORDER_SEQUENTIAL, PSK_ORDER_BLOCKED, PSK_ORDER_INTERLEAVED = 0, 1, 2
 PSK_EXP_EXACT, PSK_EXP_FAST = 0, 1
 PSK_NORM_RMS, PSK_NORM_LAYER = 0, 1
@@ -29,6 +29,9 @@ EXPORTS = ("psk_group_run", "psk_group_run_ex", "psk_group_run_interp", "psk_gro
            "psk_softmax_backward", "psk_norm_region",
            "psk_adamw_tree", "psk_adamw_tree_ex", "psk_adamw_tree_static", "psk_adamw_lr", "psk_adamw_workspace",
            "psk_adamw_scalars", "psk_adamw_group_sqsums", "psk_adamw_clip_scale", "psk_adamw_tree_scaled",
+           "psk_embed", "psk_embed_workspace", "psk_embed_backward", "psk_dropout",
+           "psk_norm_backward_workspace", "psk_norm_backward",
+           "psk_token_logp", "psk_policy_loss_workspace", "psk_policy_loss",
            "psk_device_status", "psk_test_drop_row", "psk_test_fast_exp", "psk_last_error")
 
 
@@ -121,6 +124,18 @@ def lib() -> ctypes.CDLL:
                                            ctypes.c_void_p, ctypes.c_void_p]
         L.psk_adamw_tree_scaled.argtypes = [P(psk_leaf), ctypes.c_int32, P(psk_adamw_hparams),
                                             P(psk_adamw_schedule), ctypes.c_void_p, ctypes.c_void_p]
+        V, I32, I64, U64, F64 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_double)
+        L.psk_embed.argtypes = [V, I32, I64, V, I32, I64, I64, I64, F64, V, I32, I64, V]
+        L.psk_embed_workspace.argtypes = [I64, I64, I64, P(U64)]
+        L.psk_embed_backward.argtypes = [V, I32, I64, V, I32, I64, F64, V, I32, I64, I64, I64, I32, V, U64, V]
+        L.psk_dropout.argtypes = [V, I32, V, I32, V, I32, I64, I64, I64, I64, I64, F64, U64, U64, V, V]
+        L.psk_norm_backward_workspace.argtypes = [I64, I64, P(U64)]
+        L.psk_norm_backward.argtypes = [V, I32, V, I32, V, I32, I64, I64, I64, I64, I64, I32, F64, V, I32, V, V, I32,
+                                        V, U64, V]
+        L.psk_token_logp.argtypes = [V, I32, I64, I64, I64, F64, V, I32, V, V]
+        L.psk_policy_loss_workspace.argtypes = [I64, I64, P(U64)]
+        L.psk_policy_loss.argtypes = [V, I32, I64, I64, I64, F64, V, I32, V, V, V, V, F64, F64, F64, V, V, V, I32, I64,
+                                      V, U64, V]
         L.psk_last_error.restype = ctypes.c_char_p
         for f in ("psk_group_run", "psk_group_run_ex", "psk_group_run_interp", "psk_group_check", "psk_group_prepare", "psk_group_prepare_ex",
                   "psk_softmax_region", "psk_norm_region",
@@ -129,6 +144,9 @@ def lib() -> ctypes.CDLL:
                   "psk_adamw_scalars", "psk_adamw_lr", "psk_adamw_workspace", "psk_adamw_tree_ex",
                   "psk_adamw_tree_static",
                   "psk_adamw_group_sqsums", "psk_adamw_clip_scale", "psk_adamw_tree_scaled",
+                  "psk_embed", "psk_embed_workspace", "psk_embed_backward", "psk_dropout",
+                  "psk_norm_backward_workspace", "psk_norm_backward",
+                  "psk_token_logp", "psk_policy_loss_workspace", "psk_policy_loss",
                   "psk_device_status", "psk_test_drop_row", "psk_test_fast_exp"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L

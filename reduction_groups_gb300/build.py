@@ -27,7 +27,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
-CU_SOURCES = ["group.cu", "regions.cu", "lanes.cu", "adamw.cu"]
+CU_SOURCES = ["group.cu", "regions.cu", "lanes.cu", "adamw.cu", "dropout.cu", "embed.cu", "norm_bwd.cu",
+              "loss.cu"]
 CPP_SOURCES = ["api.cpp"]
 
 NVCC_FLAGS = [

@@ -1,6 +1,7 @@
 """Python binding of the C ABI with the same names: psk_group_run,
-psk_softmax_region, psk_norm_region, psk_adamw_tree (plus the host-only psk_group_check and
-psk_adamw_scalars).  Each function marshals torch tensors (device memory and
+psk_softmax_region, psk_norm_region, psk_adamw_tree, the training step's psk_embed,
+psk_dropout, psk_norm_backward and psk_policy_loss (plus the host-only psk_group_check,
+psk_adamw_scalars and the workspace sizes).  Each function marshals torch tensors (device memory and
 the current stream) or plain host arrays into the C structs and calls the
 library; every step of the hot path runs in the library's kernels.
 """
@@ -324,3 +325,206 @@ def psk_adamw_tree_static(leaves, hp, kind="constant", warmup=0, total=1, grad_c
     arr, n = _leaf_table(leaves)
     h, sc = _hparams(hp), _schedule(kind, warmup, total, grad_clip)
     N.check(N.lib().psk_adamw_tree_static(arr, n, ctypes.byref(h), ctypes.byref(sc), _stream_handle(stream)))
+
+
+# ------------------------------------------- the training step's two ends
+
+_CODES = {}
+
+
+def _code(t, what: str, ids: bool = False) -> int:
+    """The psk_dtype of a value tensor (f32, bf16) or, with ids, of an id tensor (int32, int64)."""
+    if not _CODES:
+        import torch
+
+        _CODES.update({torch.float32: N.PSK_F32, torch.bfloat16: N.PSK_BF16, torch.int32: N.PSK_I32,
+                       torch.int64: N.PSK_I64})
+    c = _CODES.get(t.dtype, -1)
+    if (c in (N.PSK_I32, N.PSK_I64)) if ids else (c in (N.PSK_F32, N.PSK_BF16)):
+        return c
+    raise TypeError(f"{what}: storage type {t.dtype} is not {'int32 or int64' if ids else 'f32 or bf16'}")
+
+
+def _same_device(stream, *ts) -> int:
+    """The stream's handle, the tensors checked to live on the device it runs on (the current one)."""
+    import torch
+
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("the tensors must live on one device")
+    if dev.type != "cuda":
+        raise ValueError("the tensors must live on a CUDA device")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors live on {dev}, which is not the current device")
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if stream.device != dev:
+        raise ValueError(f"the stream runs on {stream.device}, the tensors live on {dev}")
+    return stream.cuda_stream
+
+
+def _matrix(t, what: str, shape=None) -> int:
+    """The leading dimension of a 2-D tensor of contiguous rows."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{what} must be a 2-D tensor with contiguous rows")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    rows, cols = t.shape
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{what} has rows that overlap")
+    return max(t.stride(0), cols)
+
+
+def _vector(t, what: str, n: int, f32: bool = False):
+    """The address of a contiguous 1-D tensor of n elements (None: NULL)."""
+    if t is None:
+        return None
+    if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous vector of {n} elements")
+    if f32:
+        import torch
+
+        if t.dtype != torch.float32:
+            raise TypeError(f"{what} must be f32")
+    return t.data_ptr()
+
+
+def _scratch(t):
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _bytes(f, *sizes) -> int:
+    out = ctypes.c_uint64(0)
+    N.check(f(*[int(v) for v in sizes], ctypes.byref(out)))
+    return int(out.value)
+
+
+def psk_embed(ids, table, y, scale: float = 1.0, stream=None) -> None:
+    """y[i, :] = table[ids[i], :] * scale; ids: int32 or int64, one outside the
+    table's rows marks padding and gives a zero row."""
+    s = _same_device(stream, table, ids, y)
+    n, (vocab, cols) = ids.numel(), table.shape
+    ldt, ldy = _matrix(table, "table"), _matrix(y, "y", (n, cols))
+    N.check(N.lib().psk_embed(_vector(ids, "ids", n), _code(ids, "ids", True), n, table.data_ptr(),
+                              _code(table, "table"), vocab, cols, ldt, scale, y.data_ptr(), _code(y, "y"), ldy, s))
+
+
+def psk_embed_workspace(tokens: int, vocab: int, cols: int) -> int:
+    """Device workspace bytes psk_embed_backward needs."""
+    return _bytes(N.lib().psk_embed_workspace, tokens, vocab, cols)
+
+
+def psk_embed_backward(ids, ct, dtable, scale: float = 1.0, accumulate: bool = False, workspace=None,
+                       stream=None) -> None:
+    """dtable[v, :] = scale * (sum of ct[i, :] over ids[i] == v), every row
+    written; with accumulate added to the rows that occur, the others left as
+    they are.  workspace: a device tensor of at least psk_embed_workspace
+    bytes."""
+    s = _same_device(stream, dtable, ids, ct, workspace)
+    n, (vocab, cols) = ids.numel(), dtable.shape
+    ldd, ldc = _matrix(dtable, "dtable"), _matrix(ct, "ct", (n, cols))
+    ws, wb = _scratch(workspace)
+    N.check(N.lib().psk_embed_backward(_vector(ids, "ids", n), _code(ids, "ids", True), n, ct.data_ptr(),
+                                       _code(ct, "ct"), ldc, scale, dtable.data_ptr(), _code(dtable, "dtable"), vocab,
+                                       cols, ldd, 1 if accumulate else 0, ws, wb, s))
+
+
+def psk_dropout(x, y, p: float, seed: int, offset: int = 0, residual=None, counter=None, stream=None) -> None:
+    """y = [residual +] dropout(x) of 2-D tensors (a 1-D tensor as one row),
+    the mask drawn from (row, column, seed, offset) and never stored: the
+    backward is psk_dropout(ct, dx, p, seed, offset).  counter: a one-element
+    int64 device tensor added to offset when the kernel runs (for captured
+    graphs)."""
+    import torch
+
+    s = _same_device(stream, x, y, residual, counter)
+    if x.dim() == 1:
+        if y.dim() != 1 or (residual is not None and residual.dim() != 1):
+            raise ValueError("x, y and the residual must have the same shape")
+        x, y = x[None], y[None]
+        residual = None if residual is None else residual[None]
+    ldx, ldy = _matrix(x, "x"), _matrix(y, "y", x.shape)
+    ldr = 0 if residual is None else _matrix(residual, "residual", x.shape)
+    if counter is not None and (counter.dtype != torch.int64 or counter.numel() != 1):
+        raise TypeError("counter must be a one-element int64 tensor")
+    for v, what in ((seed, "seed"), (offset, "offset")):
+        if not 0 <= v < 1 << 64:
+            raise ValueError(f"{what} must be in [0, 2^64)")
+    rows, cols = x.shape
+    N.check(N.lib().psk_dropout(x.data_ptr(), _code(x, "x"), None if residual is None else residual.data_ptr(),
+                                0 if residual is None else _code(residual, "residual"), y.data_ptr(), _code(y, "y"),
+                                rows, cols, ldx, ldr, ldy, p, seed, offset,
+                                None if counter is None else counter.data_ptr(), s))
+
+
+_NORM = {"rms": N.PSK_NORM_RMS, "layer": N.PSK_NORM_LAYER}
+
+
+def psk_norm_backward_workspace(rows: int, cols: int) -> int:
+    """Device workspace bytes psk_norm_backward needs."""
+    return _bytes(N.lib().psk_norm_backward_workspace, rows, cols)
+
+
+def psk_norm_backward(x, ct, dx, kind: str, eps: float, gamma=None, dgamma=None, dbeta=None, workspace=None,
+                      stream=None) -> None:
+    """The backward of psk_norm_region(x, y, kind, eps, gamma, beta): dx from
+    the cotangent ct of y, and the gradients of gamma and beta (1-D, one
+    storage type; None: not wanted).  workspace: a device tensor of at least
+    psk_norm_backward_workspace bytes."""
+    s = _same_device(stream, x, ct, dx, gamma, dgamma, dbeta, workspace)
+    rows, cols = x.shape
+    ldx, ldc, ldd = _matrix(x, "x"), _matrix(ct, "ct", x.shape), _matrix(dx, "dx", x.shape)
+    g = dgamma if dgamma is not None else dbeta
+    if dgamma is not None and dbeta is not None and dgamma.dtype != dbeta.dtype:
+        raise TypeError("dgamma and dbeta must share one storage type")
+    ws, wb = _scratch(workspace)
+    N.check(N.lib().psk_norm_backward(x.data_ptr(), _code(x, "x"), ct.data_ptr(), _code(ct, "ct"), dx.data_ptr(),
+                                      _code(dx, "dx"), rows, cols, ldx, ldc, ldd, _NORM[kind], eps,
+                                      _vector(gamma, "gamma", cols), 0 if gamma is None else _code(gamma, "gamma"),
+                                      _vector(dgamma, "dgamma", cols), _vector(dbeta, "dbeta", cols),
+                                      0 if g is None else _code(g, "dgamma"), ws, wb, s))
+
+
+def psk_token_logp(logits, targets, logp, scale: float = 1.0, stream=None) -> None:
+    """logp[r] = log softmax(scale * logits[r])[targets[r]] (f32); targets:
+    int32 or int64, one outside the row marks padding (logp 0)."""
+    s = _same_device(stream, logits, targets, logp)
+    rows, cols = logits.shape
+    ldl = _matrix(logits, "logits")
+    N.check(N.lib().psk_token_logp(logits.data_ptr(), _code(logits, "logits"), rows, cols, ldl, scale,
+                                   _vector(targets, "targets", rows), _code(targets, "targets", True),
+                                   _vector(logp, "logp", rows, True), s))
+
+
+def psk_policy_loss_workspace(rows: int, cols: int) -> int:
+    """Device workspace bytes psk_policy_loss needs."""
+    return _bytes(N.lib().psk_policy_loss_workspace, rows, cols)
+
+
+def psk_policy_loss(logits, targets, old_logp, advantage, weight, loss, logp=None, dlogits=None, ref_logp=None,
+                    clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0, scale: float = 1.0,
+                    workspace=None, stream=None) -> None:
+    """The clipped policy loss with a KL term over rows of vocabulary logits:
+    loss (two f32: loss, weighted KL sum), logp (f32 per row; None: not
+    wanted) and, unless None, dlogits (may be the logits in place).  weight:
+    f32 per row (0 leaves a row out), None: 1 / rows.  workspace: a device
+    tensor of at least psk_policy_loss_workspace bytes."""
+    s = _same_device(stream, logits, targets, old_logp, advantage, weight, loss, logp, dlogits, ref_logp, workspace)
+    rows, cols = logits.shape
+    ldl = _matrix(logits, "logits")
+    ldg = 0 if dlogits is None else _matrix(dlogits, "dlogits", logits.shape)
+    ws, wb = _scratch(workspace)
+    N.check(N.lib().psk_policy_loss(logits.data_ptr(), _code(logits, "logits"), rows, cols, ldl, scale,
+                                    _vector(targets, "targets", rows), _code(targets, "targets", True),
+                                    _vector(old_logp, "old_logp", rows, True),
+                                    _vector(ref_logp, "ref_logp", rows, True),
+                                    _vector(advantage, "advantage", rows, True),
+                                    _vector(weight, "weight", rows, True), clip_low, clip_high, kl_coef,
+                                    _vector(loss, "loss", 2, True), _vector(logp, "logp", rows, True),
+                                    None if dlogits is None else dlogits.data_ptr(),
+                                    0 if dlogits is None else _code(dlogits, "dlogits"), ldg, ws, wb, s))
