@@ -500,7 +500,7 @@ int psk_norm_backward(const void* x, int32_t xt, const void* ct, int32_t ct_t, v
  * logp may be NULL; ref_logp may be NULL if kl_coef is 0; dlogits NULL computes
  * the loss alone, else rows (type gt, ldg >= cols) written whole, in place of
  * the logits if wanted (same type and leading dimension).  No other overlap.
- * cols < 2^31; rows == 0 gives a zero loss.  clip_low in [0, 1], clip_high >=
+ * rows, cols < 2^31; rows == 0 gives a zero loss.  clip_low in [0, 1], clip_high >=
  * 0.  workspace: as for psk_embed_backward, psk_policy_loss_workspace bytes. */
 int psk_token_logp(const void* logits, int32_t lt, int64_t rows, int64_t cols, int64_t ldl, double scale,
                    const void* targets, int32_t tt, float* logp, void* stream);

@@ -92,6 +92,8 @@ extern "C" int psk_dropout(const void* x, int32_t xt, const void* residual, int3
   if (cols > (1LL << 34)) return fail(PSK_E_SHAPE, "cols %lld above 2^34", (long long)cols);
   if (rows == 0 || cols == 0) return PSK_OK;
   if (!x || !y) return fail(PSK_E_NULL, "x or y is NULL");
+  if ((uintptr_t)x % dtype_size(xt) || (uintptr_t)y % dtype_size(yt) || (residual && (uintptr_t)residual % dtype_size(rt)))
+    return fail(PSK_E_ARG, "x, y or the residual is not aligned to its type");
   if (ldx < cols || ldy < cols || (residual && ldr < cols)) return fail(PSK_E_SHAPE, "leading dimension below cols");
   if (!rows_addressable(rows, ldx) || !rows_addressable(rows, ldy) || (residual && !rows_addressable(rows, ldr)))
     return fail(PSK_E_SHAPE, "rows x leading dimension too large");

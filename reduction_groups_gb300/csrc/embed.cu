@@ -354,6 +354,8 @@ extern "C" int psk_embed(const void* ids, int32_t idt, int64_t tokens, const voi
   if (!(scale >= -3.4e38 && scale <= 3.4e38)) return fail(PSK_E_ARG, "scale is not a finite f32 value");
   if (tokens == 0 || cols == 0) return PSK_OK;
   if (!ids || !y || (!table && vocab > 0)) return fail(PSK_E_NULL, "ids, table or y is NULL");
+  if ((uintptr_t)table % dtype_size(tt) || (uintptr_t)y % dtype_size(yt))
+    return fail(PSK_E_ARG, "table or y is not aligned to its type");
   if (ldt < cols || ldy < cols) return fail(PSK_E_SHAPE, "leading dimension below cols");
   if (!rows_addressable(tokens, ldy) || !rows_addressable(vocab, ldt))
     return fail(PSK_E_SHAPE, "rows x leading dimension too large");
@@ -410,6 +412,8 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
   if (!(scale >= -3.4e38 && scale <= 3.4e38)) return fail(PSK_E_ARG, "scale is not a finite f32 value");
   if (vocab == 0 || cols == 0 || (tokens == 0 && accumulate)) return PSK_OK;
   if (!dtable || (tokens > 0 && (!ids || !ct))) return fail(PSK_E_NULL, "ids, ct or the gradient is NULL");
+  if ((uintptr_t)dtable % dtype_size(dt) || (tokens > 0 && (uintptr_t)ct % dtype_size(ct_t)))
+    return fail(PSK_E_ARG, "ct or the gradient is not aligned to its type");
   if (ldd < cols || (tokens > 0 && ldc < cols)) return fail(PSK_E_SHAPE, "leading dimension below cols");
   if (!rows_addressable(tokens, ldc) || !rows_addressable(vocab, ldd))
     return fail(PSK_E_SHAPE, "rows x leading dimension too large");

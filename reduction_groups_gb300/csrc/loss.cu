@@ -5,13 +5,17 @@
 //   k     = e^q - q - 1, q = ref - logp                    (a KL estimate >= 0)
 //   loss  = sum w (term + beta k)
 //   dx_j  = scale w (dterm/dlogp - beta (e^q - 1)) ([j = t] - softmax_j)
-// A row is one pass for its maximum and sum (each thread keeps a running
-// maximum and rescales its sum when that grows) and, for the gradient, one
-// more over the row, which then comes from L2.  Row sums are joined across
-// threads in pairs of floats (sum and rounding error), so that 1 - p of a
-// nearly certain token keeps its digits; logp is formed in 64 bits.
+// Sums of 2^(c (x - m)) about a running maximum m (c = scale log2 e; the
+// maximum's own term is exactly 1), rescaled when the maximum grows, joined
+// across threads in pairs of floats (sum and rounding error), so that 1 - p of
+// a nearly certain token keeps its digits; logp is formed in 64 bits, and the
+// ratio and the KL term from it with an exp of extra digits (exp_tier1_core),
+// since their sum over rows cancels.
 #include "vec8.cuh"
 #include "crmath.cuh"
+#include "pair.cuh"
+#include "pipe.cuh"
+#include "trainops.h"
 
 namespace psk {
 
@@ -46,6 +50,11 @@ struct LossParams {
 __device__ __forceinline__ float ex2_approx(float t) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 __device__ __forceinline__ float max_nan2(float a, float b) {
@@ -108,26 +117,38 @@ __device__ __forceinline__ void add8(RowSum& v, const float* x, int n, float c) 
 }
 
 // e^q - q - 1 >= 0: its series where the difference would cancel.
-__device__ __forceinline__ float kl_term(float q, float em1) {
+__device__ __forceinline__ double kl_term(double q, double em1) {
+  const float f = (float)q;
   if (em1 == INFINITY) return em1;
-  if (!(fabsf(q) < 0.5f)) return em1 - q;
-  float h = 1.0f / 3628800.0f;   // sum q^(n-2) / n!, n = 2..10
-  h = fmaf(h, q, 1.0f / 362880.0f);
-  h = fmaf(h, q, 1.0f / 40320.0f);
-  h = fmaf(h, q, 1.0f / 5040.0f);
-  h = fmaf(h, q, 1.0f / 720.0f);
-  h = fmaf(h, q, 1.0f / 120.0f);
-  h = fmaf(h, q, 1.0f / 24.0f);
-  h = fmaf(h, q, 1.0f / 6.0f);
-  h = fmaf(h, q, 0.5f);
-  return q * q * h;
+  if (!(fabsf(f) < 0.25f)) return em1 - q;
+  float h = 1.0f / 362880.0f;    // sum q^(n-2) / n!, n = 2..9 (the next below 2^-36)
+  h = fmaf(h, f, 1.0f / 40320.0f);
+  h = fmaf(h, f, 1.0f / 5040.0f);
+  h = fmaf(h, f, 1.0f / 720.0f);
+  h = fmaf(h, f, 1.0f / 120.0f);
+  h = fmaf(h, f, 1.0f / 24.0f);
+  h = fmaf(h, f, 1.0f / 6.0f);
+  h = fmaf(h, f, 0.5f);
+  return q * q * (double)h;
 }
 
 // What a row's logp leads to.
 struct RowLoss {
-  float term, k;      // loss terms
+  double term, k;     // loss terms
   float d;            // d(term + beta k) / dlogp
 };
+
+// e^v to a relative error below 2^-40 for |v| <= 87: tier 1 of the correctly
+// rounded exp, before its rounding, at v's f32 part, times 1 + the rest.
+__device__ __forceinline__ double exp_wide(double v) {
+  const float hi = (float)v;
+  if (!(fabsf(hi) <= 87.0f)) return (double)expf(hi);
+  const float lo = (float)(v - (double)hi);
+  float R, d;
+  int n;
+  exp_tier1_core(hi, psk_exp_tab2, R, d, n);
+  return ((double)R + (double)fmaf(R, lo, d)) * __hiloint2double((1023 + n) << 20, 0);
+}
 
 __device__ __forceinline__ double row_logp(float xt, const RowSum& v, float scale) {
   float R, d;
@@ -138,19 +159,20 @@ __device__ __forceinline__ double row_logp(float xt, const RowSum& v, float scal
 
 __device__ __forceinline__ RowLoss row_loss(const LossParams& P, double logp, float old, float ref, float adv) {
   RowLoss o;
-  const float ratio = expf((float)(logp - (double)old));
-  const float bound = fminf(fmaxf(ratio, P.low), P.high);
+  const double ratio = exp_wide(logp - (double)old), a = (double)adv;
+  const double low = (double)P.low, high = (double)P.high;
+  const double bound = ratio < low ? low : ratio > high ? high : ratio;
   // A zero advantage gives zero terms even where the ratio overflows.
-  const float free_term = adv == 0.0f && ratio == ratio ? 0.0f : ratio * adv, bound_term = bound * adv;
+  const double free_term = adv == 0.0f && ratio == ratio ? 0.0 : ratio * a, bound_term = bound * a;
   const bool clipped = bound_term < free_term;
   o.term = -(clipped ? bound_term : free_term);
-  o.d = clipped ? 0.0f : -free_term;
-  o.k = 0.0f;
+  o.d = clipped ? 0.0f : -(float)free_term;
+  o.k = 0.0;
   if (P.ref_logp) {
-    const float q = (float)((double)ref - logp);
-    const float em1 = expm1f(q);
+    const double q = (double)ref - logp;
+    const double em1 = exp_wide(q) - 1.0;
     o.k = kl_term(q, em1);
-    if (P.beta != 0.0f) o.d = fmaf(-P.beta, em1, o.d);
+    if (P.beta != 0.0f) o.d = fmaf(-P.beta, (float)em1, o.d);
   }
   return o;
 }
@@ -159,12 +181,20 @@ __device__ __forceinline__ int64_t row_target(const LossParams& P, int64_t r) {
   return P.targets64 ? ((const int64_t*)P.targets)[r] : (int64_t)((const int32_t*)P.targets)[r];
 }
 
-template <int LT, bool VEC>
+template <int LT>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
   return LT == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)p)[i]) : ((const float*)p)[i];
 }
+template <int LT>
+__device__ __forceinline__ void store1(void* p, int64_t i, float v) {
+  if (LT == PSK_BF16) ((uint16_t*)p)[i] = f32_to_bf16_bits(v);
+  else ((float*)p)[i] = v;
+}
 
-// A CTA per row, CTAs over rows in turn.
+// Any row: a CTA per row, CTAs over rows in turn, the row read from global
+// memory for its sums and (from L2) again for its gradient.  Rows that the
+// resident kernel below cannot take: longer than a cluster's shared memory,
+// gradients of another type or alignment than the logits.
 template <int LT, int GT, int MODE, bool VEC>
 __global__ void __launch_bounds__(LOSS_THREADS) loss_rows_kernel(const __grid_constant__ LossParams P) {
   __shared__ RowSum red[LOSS_WARPS];
@@ -185,7 +215,7 @@ __global__ void __launch_bounds__(LOSS_THREADS) loss_rows_kernel(const __grid_co
       continue;
     }
     const int64_t xo = r * P.ldx;
-    const float xt = load1<LT, VEC>(P.x, xo + t);       // read before the row may be overwritten in place
+    const float xt = load1<LT>(P.x, xo + t);       // read before the row may be overwritten in place
     RowSum v{-INFINITY, 0.0f, 0.0f};
     for (int64_t q0 = threadIdx.x; q0 < groups; q0 += 4 * LOSS_THREADS) {
       float x[4][8];
@@ -210,8 +240,8 @@ __global__ void __launch_bounds__(LOSS_THREADS) loss_rows_kernel(const __grid_co
           coef[0] = -a / v.s;                           // times 2^(c (x - m)): -a softmax
           coef[1] = a * -expm1f((float)logp);           // a (1 - softmax_t)
         }
-        loss_sum += (double)w * ((double)o.term + (P.beta != 0.0f ? (double)P.beta * (double)o.k : 0.0));
-        kl_sum += (double)w * (double)o.k;
+        loss_sum += (double)w * (o.term + (P.beta != 0.0f ? (double)P.beta * o.k : 0.0));
+        kl_sum += (double)w * o.k;
       }
     }
     __syncthreads();
@@ -234,14 +264,432 @@ __global__ void __launch_bounds__(LOSS_THREADS) loss_rows_kernel(const __grid_co
   }
 }
 
-// The CTAs' sums joined: two warps, lanes over CTAs in turn.
-__global__ void __launch_bounds__(64) loss_finish_kernel(const double* part, int n, float* loss) {
-  const int lane = threadIdx.x & 31, which = threadIdx.x >> 5;
+// ------------------------------------------------------ the resident kernel
+//
+// A row is read from memory once: its body (the 16-byte groups between an
+// unaligned head and tail of a few elements) is copied by TMA into shared
+// memory, a row slice per CTA of a cluster (one CTA where the row fits, up to
+// eight for rows of up to 8 x 72 KB or to spread a call of few rows), and
+// stays there for the sums and for the gradient, which goes straight to
+// memory: the floor of one read and one write per logit.  A producer warp
+// keeps the ring of slices full (rows ahead of the consumers), and hands each
+// row's scalars along with it.  Teams of consumer warps take rows in turn, so
+// that one team's barriers and scalar section (logarithm, ratio, KL term)
+// overlap another's exponentials; the CTAs of a cluster exchange their
+// slices' maxima and sums through distributed shared memory.
+
+constexpr int RES_CONSUMERS = 576;             // at most (teams of 32 to 512 threads)
+constexpr int RES_THREADS = RES_CONSUMERS + 32;
+constexpr int RES_MAX_TEAMS = 16;
+constexpr int RES_MAX_SLOTS = 32;
+constexpr int RES_MAX_CLUSTER = 8;
+constexpr int RES_SMEM = 216 * 1024;          // ring
+constexpr int RES_SLICE = 72 * 1024;          // largest slice: three in the ring
+
+struct ResParams {
+  LossParams L;
+  int32_t slice_groups;     // 16-byte groups of a CTA's slice (the last may be short)
+  int32_t slots, slot_bytes;
+  int32_t team_threads, teams;   // slots is a multiple of teams: a slot's phases are all one team's, which
+                                 // visits them in order (a parity wait must never run ahead of its barrier)
+  int32_t cluster;
+};
+
+// A row's scalars, from the producer to the teams.
+struct RowInfo {
+  int32_t live, target;
+  float w, xt, old, ref, adv;
+};
+
+struct ResShared {
+  uint64_t full[RES_MAX_SLOTS], empty[RES_MAX_SLOTS];
+  uint64_t xbar[RES_MAX_TEAMS][2];
+  RowInfo info[RES_MAX_SLOTS];
+  RowSum red[2][RES_CONSUMERS / 32];            // per warp
+  RowSum xchg[RES_MAX_TEAMS][2][RES_MAX_CLUSTER];
+  float4 coef[RES_MAX_TEAMS];
+  volatile int abort_flag;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void peer_store(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void peer_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// mbar_wait with the cluster's writes acquired.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  do {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (ok) return true;
+  } while (clock64() - t0 < PIPE_WAIT_CYCLES);
+  atomicOr(&g_pipe_status, PIPE_TIMEOUT);
+  return false;
+}
+
+// Elements of a 16-byte group.
+template <int LT>
+struct GroupOf {
+  static constexpr int N = LT == PSK_BF16 ? 8 : 4;
+  static constexpr int PER_STEP = LT == PSK_BF16 ? 2 : 4;     // groups of a step: sixteen elements
+};
+
+__device__ __forceinline__ f2 unpack_bf16(uint32_t u) {
+  return f2{__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)};
+}
+
+// A step's sixteen elements and their maximum (groups past the end: -inf).
+template <int LT>
+__device__ __forceinline__ void load_step(const unsigned char* s, int i, int n, int stride, f2* x, float& m) {
+  if constexpr (LT == PSK_BF16) {
+    uint4 u[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      u[q] = i + q * stride < n ? *(const uint4*)(s + (size_t)(i + q * stride) * 16)
+                                : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+    uint32_t h = bf16x2_max(bf16x2_max(bf16x2_max(u[0].x, u[0].y), bf16x2_max(u[0].z, u[0].w)),
+                            bf16x2_max(bf16x2_max(u[1].x, u[1].y), bf16x2_max(u[1].z, u[1].w)));
+    const f2 e = unpack_bf16(h);
+    m = max_nan2(e.x, e.y);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      x[4 * q] = unpack_bf16(u[q].x), x[4 * q + 1] = unpack_bf16(u[q].y);
+      x[4 * q + 2] = unpack_bf16(u[q].z), x[4 * q + 3] = unpack_bf16(u[q].w);
+    }
+  } else {
+    m = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 v = i + q * stride < n ? *(const float4*)(s + (size_t)(i + q * stride) * 16)
+                                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      x[2 * q] = f2{v.x, v.y}, x[2 * q + 1] = f2{v.z, v.w};
+      m = max_nan2(m, max_nan2(max_nan2(v.x, v.y), max_nan2(v.z, v.w)));
+    }
+  }
+}
+
+template <int LT, int MODE>
+__global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __grid_constant__ ResParams P) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ __align__(16) ResShared S;
+  constexpr int G = GroupOf<LT>::N;
+  constexpr int ESZ = 16 / G;
+  const LossParams& L = P.L;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const uint32_t K = (uint32_t)P.cluster;
+  const uint32_t rank = K > 1 ? cluster_rank() : 0;
+  const int64_t cid = blockIdx.x / K, ncl = gridDim.x / K;
+  const int n_local = cid < L.rows ? (int)((L.rows - 1 - cid) / ncl + 1) : 0;
+  const int slots = P.slots;
+  const int64_t cols = L.cols;
+  const uintptr_t base = (uintptr_t)L.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < slots; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], P.team_threads / 32);
+    for (int t = 0; t < P.teams; ++t) mbar_init(&S.xbar[t][0], K), mbar_init(&S.xbar[t][1], K);
+    S.abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (K > 1) cluster_barrier();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the finishing kernel may be set up
+
+  // Row r: elements before its first 16-byte boundary, full groups after.
+  auto head_of = [&](int64_t r) {
+    const int a = (int)(((base + (uintptr_t)(r * L.ldx) * ESZ) & 15u) / ESZ);
+    const int64_t h = a ? G - a : 0;
+    return (int)(h < cols ? h : cols);
+  };
+
+  if (tid >= P.teams * P.team_threads) {
+    // ---------------- producer: lanes fetch 32 rows' scalars at once, lane 0 issues
+    const long long drop = g_pipe_drop_row;
+    int issued = 0;
+    bool stop = false;
+    for (int j0 = 0; j0 < n_local && !stop; j0 += 32) {
+      RowInfo info{};
+      const int64_t mine = cid + (int64_t)(j0 + lane) * ncl;
+      if (j0 + lane < n_local) {
+        const int64_t t = row_target(L, mine);
+        info.w = MODE == LOSS_LOGP ? 1.0f : L.weight ? L.weight[mine] : L.uniform;
+        info.live = t >= 0 && t < cols && !(info.w == 0.0f);
+        if (info.live) {
+          info.target = (int32_t)t;
+          info.xt = load1<LT>(L.x, mine * L.ldx + t);
+          if (MODE != LOSS_LOGP) {
+            info.old = L.old_logp[mine], info.adv = L.adv[mine];
+            info.ref = L.ref_logp ? L.ref_logp[mine] : 0.0f;
+          }
+        }
+      }
+      for (int k = 0; k < 32 && j0 + k < n_local; ++k) {
+        const int j = j0 + k, s = j % slots;
+        if (lane == k) {
+          bool ok = j != drop && !S.abort_flag;
+          if (ok && j >= slots && !mbar_wait(&S.empty[s], (uint32_t)((j / slots) - 1) & 1u)) {
+            S.abort_flag = 1;
+            ok = false;
+          }
+          if (ok) {
+            S.info[s] = info;
+            const int head = head_of(mine);
+            const int64_t body = (cols - head) / G;
+            const int64_t first = (int64_t)rank * P.slice_groups;
+            int64_t n = body - first;
+            n = n < 0 || !info.live ? 0 : n < P.slice_groups ? n : P.slice_groups;
+            mbar_arrive_expect_tx(&S.full[s], (uint32_t)n * 16u);
+            if (n > 0)
+              bulk_copy_g2s(ring + (size_t)s * P.slot_bytes,
+                            (const unsigned char*)L.x + (mine * L.ldx + head) * ESZ + first * 16, (uint32_t)n * 16u,
+                            &S.full[s]);
+            ++issued;
+          }
+          stop = !ok;
+        }
+        stop = __shfl_sync(0xFFFFFFFFu, stop, k);
+        if (stop) break;
+      }
+    }
+    // Wind-down after a timeout: copies still in flight land before the CTA retires.
+    for (int o = 16; o > 0; o >>= 1) issued += __shfl_xor_sync(0xFFFFFFFFu, issued, o);
+    if (stop && lane == 0)
+      for (int j = issued > slots ? issued - slots : 0; j < issued; ++j)
+        mbar_wait(&S.full[j % slots], (uint32_t)(j / slots) & 1u);
+  } else {
+    // ---------------- teams.  After a timeout (`dead`) a thread skips waits
+    // and work but keeps meeting its team's barriers.
+    const int TT = P.team_threads, team = tid / TT, tt = tid - team * TT, tw = tt >> 5, nw = TT / 32;
+    const float c = L.c;
+    bool dead = false;
+    double loss_sum = 0.0, kl_sum = 0.0;
+    uint32_t rows_done = 0, exchanges = 0;
+    auto team_barrier = [&]() {
+      if (TT == 32) __syncwarp();
+      else named_barrier(1 + team, TT);
+    };
+    for (int j = team; j < n_local; j += P.teams, ++rows_done) {
+      const int s = j % slots;
+      const int64_t r = cid + (int64_t)j * ncl;
+      const unsigned char* x = ring + (size_t)s * P.slot_bytes;
+      const int head = head_of(r);
+      const int64_t body = (cols - head) / G;
+      const int tail = (int)(cols - head - body * G);
+      const int64_t first = (int64_t)rank * P.slice_groups;
+      const int n = body <= first ? 0 : body - first < P.slice_groups ? (int)(body - first) : P.slice_groups;
+      // The head's and tail's elements: one each for the first threads of the first CTA's team.
+      const int64_t edge = rank != 0 || tt >= 16 ? -1
+                           : tt < 8 ? (tt < head ? tt : -1)
+                                    : (tt - 8 < tail ? cols - tail + (tt - 8) : -1);
+      dead = dead || S.abort_flag;
+      if (!dead && !mbar_wait(&S.full[s], (uint32_t)(j / slots) & 1u)) { S.abort_flag = 1; dead = true; }
+      RowInfo info{};
+      if (!dead) info = S.info[s];
+      const bool live = !dead && info.live;
+      const float xe = live && edge >= 0 ? load1<LT>(L.x, r * L.ldx + edge) : -INFINITY;
+
+      RowSum v{-INFINITY, 0.0f, 0.0f};
+      if (live) {
+        f2 sum{0.0f, 0.0f};
+        constexpr int STEP = GroupOf<LT>::PER_STEP;
+        for (int i = tt; i < n; i += STEP * TT) {
+          f2 e[8];
+          float m;
+          load_step<LT>(x, i, n, TT, e, m);
+          if (!(m <= v.m)) {                       // grows, or NaN
+            m = max_nan2(m, v.m);
+            const float f = ex2_approx((v.m - m) * c);
+            sum.x *= f, sum.y *= f;
+            v.m = m;
+          }
+          const f2 nm = f2_splat(v.m == -INFINITY ? 0.0f : -v.m);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) e[q] = f2_mul(f2_add(e[q], nm), f2_splat(c));
+#pragma unroll
+          for (int q = 0; q < 8; ++q) e[q].x = ex2_approx(e[q].x), e[q].y = ex2_approx(e[q].y);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) sum = f2_add(sum, e[q]);
+        }
+        v.s = __fadd_rn(sum.x, sum.y);
+        if (edge >= 0) {
+          if (!(xe <= v.m)) {
+            const float m = max_nan2(xe, v.m);
+            v.s *= ex2_approx((v.m - m) * c);
+            v.m = m;
+          }
+          v.s += v.m == -INFINITY ? 0.0f : ex2_approx((xe - v.m) * c);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          RowSum u;
+          u.m = __shfl_xor_sync(0xFFFFFFFFu, v.m, o);
+          u.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
+          u.e = __shfl_xor_sync(0xFFFFFFFFu, v.e, o);
+          v = join(v, u, c);
+        }
+        if (lane == 0) S.red[rows_done & 1][tid >> 5] = v;
+      }
+      __syncwarp();
+      if (MODE != LOSS_GRAD && !dead && lane == 0) mbar_arrive(&S.empty[s]);
+      team_barrier();
+      if (tw == 0 && live) {
+        v = lane < nw ? S.red[rows_done & 1][team * nw + lane] : RowSum{-INFINITY, 0.0f, 0.0f};
+        for (int o = 1; o < nw; o <<= 1) {
+          RowSum u;
+          u.m = __shfl_xor_sync(0xFFFFFFFFu, v.m, o);
+          u.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
+          u.e = __shfl_xor_sync(0xFFFFFFFFu, v.e, o);
+          v = join(v, u, c);
+        }
+        if (K > 1) {
+          v.m = __shfl_sync(0xFFFFFFFFu, v.m, 0);
+          v.s = __shfl_sync(0xFFFFFFFFu, v.s, 0);
+          v.e = __shfl_sync(0xFFFFFFFFu, v.e, 0);
+          const uint32_t p = exchanges & 1;
+          if ((uint32_t)lane < K) {
+            const uint32_t to = peer_addr(&S.xchg[team][p][rank], lane);
+            peer_store(to, v.m);
+            peer_store(to + 4, v.s);
+            peer_store(to + 8, v.e);
+            peer_arrive(peer_addr(&S.xbar[team][p], lane));
+          }
+          bool ok = true;
+          if (lane == 0) ok = mbar_wait_cluster(&S.xbar[team][p], (exchanges >> 1) & 1u);
+          ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+          ++exchanges;
+          if (!ok) { S.abort_flag = 1; dead = true; }
+          // every lane acquires what the peers wrote
+          if (ok && lane != 0) mbar_wait_cluster(&S.xbar[team][p], ((exchanges - 1) >> 1) & 1u);
+          v = ok && (uint32_t)lane < K ? S.xchg[team][p][lane] : RowSum{-INFINITY, 0.0f, 0.0f};
+          for (uint32_t o = 1; o < K; o <<= 1) {
+            RowSum u;
+            u.m = __shfl_xor_sync(0xFFFFFFFFu, v.m, o);
+            u.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
+            u.e = __shfl_xor_sync(0xFFFFFFFFu, v.e, o);
+            v = join(v, u, c);
+          }
+        }
+        if (lane == 0 && !dead) {
+          const double logp = row_logp(info.xt, v, L.scale);
+          if (L.logp && rank == 0) L.logp[r] = (float)logp;
+          if (MODE != LOSS_LOGP) {
+            const RowLoss o = row_loss(L, logp, info.old, info.ref, info.adv);
+            if (MODE == LOSS_GRAD) {
+              const float a = info.w * o.d * L.scale;
+              S.coef[team] = make_float4(-a / v.s, a * -expm1f((float)logp), v.m, 0.0f);
+            }
+            loss_sum += (double)info.w * (o.term + (L.beta != 0.0f ? (double)L.beta * o.k : 0.0));
+            kl_sum += (double)info.w * o.k;
+          }
+        }
+        __syncwarp();
+      } else if (tt == 0 && !dead && rank == 0 && L.logp) {
+        L.logp[r] = 0.0f;                        // a row left out
+      }
+      if (MODE == LOSS_GRAD) {
+        team_barrier();
+        unsigned char* g = (unsigned char*)L.grad + (r * L.ldg + head) * ESZ + first * 16;
+        if (live) {
+          const float4 k = S.coef[team];
+          const f2 f{k.x, k.x}, nm = f2_splat(-k.z);
+          for (int i = tt; i < n; i += TT) {
+            if constexpr (LT == PSK_BF16) {
+              const uint4 u = *(const uint4*)(x + (size_t)i * 16);
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+              uint32_t o[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                f2 e = f2_mul(f2_add(unpack_bf16(w[q]), nm), f2_splat(c));
+                e = f2_mul(f2{ex2_approx(e.x), ex2_approx(e.y)}, f);
+                o[q] = f32x2_to_bf16x2(e.x, e.y);
+              }
+              *(uint4*)(g + (size_t)i * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+              const float4 u = *(const float4*)(x + (size_t)i * 16);
+              f2 a = f2_mul(f2_add(f2{u.x, u.y}, nm), f2_splat(c)), b = f2_mul(f2_add(f2{u.z, u.w}, nm), f2_splat(c));
+              a = f2_mul(f2{ex2_approx(a.x), ex2_approx(a.y)}, f);
+              b = f2_mul(f2{ex2_approx(b.x), ex2_approx(b.y)}, f);
+              *(float4*)(g + (size_t)i * 16) = make_float4(a.x, a.y, b.x, b.y);
+            }
+          }
+          if (edge >= 0) {
+            const float e = edge == info.target ? k.y : ex2_approx((xe - k.z) * c) * k.x;
+            store1<LT>(L.grad, r * L.ldg + edge, e);
+          }
+          // The target's own element, over what its thread has just stored.
+          const int64_t at = ((int64_t)info.target - head) / G - first;
+          if (info.target >= head && at >= 0 && at < n && (int)at % TT == tt)
+            store1<LT>(L.grad, r * L.ldg + info.target, k.y);
+        } else if (!dead) {
+          for (int i = tt; i < n; i += TT) *(uint4*)(g + (size_t)i * 16) = make_uint4(0, 0, 0, 0);
+          if (edge >= 0) store1<LT>(L.grad, r * L.ldg + edge, 0.0f);
+        }
+        __syncwarp();
+        if (!dead && lane == 0) mbar_arrive(&S.empty[s]);
+      }
+    }
+    if (MODE != LOSS_LOGP && tt == 0 && rank == 0) {
+      L.part[2 * (cid * P.teams + team)] = loss_sum;
+      L.part[2 * (cid * P.teams + team) + 1] = kl_sum;
+    }
+  }
+  __syncwarp();
+  if (K > 1) cluster_barrier();     // no CTA leaves while a peer may still write to it
+}
+
+// The partial sums joined, 256 threads over them in turn for each of the two.
+constexpr int FINISH_THREADS = 512;
+__global__ void __launch_bounds__(FINISH_THREADS) loss_finish_kernel(const double* part, int n, float* loss) {
+  __shared__ double sums[FINISH_THREADS / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int half = FINISH_THREADS / 2, which = threadIdx.x / half, t = threadIdx.x - which * half;
   double s = 0.0;
-  for (int i = lane; i < n; i += 32) s += part[2 * i + which];
+  for (int i = t; i < n; i += half) s += part[2 * i + which];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  if (lane == 0) loss[which] = (float)s;
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (t == 0) {
+    const int w0 = which * (half / 32);
+    for (int w = 1; w < half / 32; ++w) s += sums[w0 + w];
+    loss[which] = (float)s;
+  }
+}
+
+// Launched so that its set-up overlaps the kernel before it, whose sums it
+// waits for.
+static int loss_finish(const double* part, int n, float* loss, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(FINISH_THREADS);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, loss_finish_kernel, part, n, loss);
+  return check_launch("policy loss finishing kernel");
 }
 
 static int loss_check_rows(const void* logits, int32_t lt, int64_t rows, int64_t cols, int64_t ldl, double scale,
@@ -249,13 +697,15 @@ static int loss_check_rows(const void* logits, int32_t lt, int64_t rows, int64_t
   if (!dtype_ok(lt)) return fail(PSK_E_DTYPE, "logits dtype %d", lt);
   if (tt != PSK_I32 && tt != PSK_I64) return fail(PSK_E_DTYPE, "target dtype %d", tt);
   if (rows < 0 || cols < 0) return fail(PSK_E_SHAPE, "rows %lld, cols %lld", (long long)rows, (long long)cols);
-  if (cols > (1LL << 31)) return fail(PSK_E_SHAPE, "cols %lld above 2^31", (long long)cols);
+  if (rows > 0x7FFFFFFFll || cols > 0x7FFFFFFFll)
+    return fail(PSK_E_SHAPE, "rows %lld or cols %lld above 2^31 - 1", (long long)rows, (long long)cols);
   if (rows > 0 && cols == 0) return fail(PSK_E_SHAPE, "rows of no logits");
   if (!(scale >= 1e-30 && scale <= 1e30)) return fail(PSK_E_ARG, "scale %g is not in [1e-30, 1e30]", scale);
   if (rows == 0) return PSK_OK;
   if (!logits || !targets) return fail(PSK_E_NULL, "logits or targets is NULL");
   if (ldl < cols) return fail(PSK_E_SHAPE, "leading dimension below cols");
   if (!rows_addressable(rows, ldl)) return fail(PSK_E_SHAPE, "rows x leading dimension too large");
+  if ((uintptr_t)logits % dtype_size(lt) != 0) return fail(PSK_E_ARG, "logits are not aligned to their type");
   if ((uintptr_t)targets % (tt == PSK_I64 ? 8 : 4) != 0) return fail(PSK_E_ARG, "targets are not aligned to their type");
   return PSK_OK;
 }
@@ -268,6 +718,105 @@ static LossParams loss_params(const void* logits, int64_t rows, int64_t cols, in
   P.scale = (float)scale;
   P.c = (float)((double)P.scale * 1.4426950408889634074);
   return P;
+}
+
+// The resident kernel's shape for rows of this size, or false for rows beyond
+// a cluster's shared memory.  The cluster is the smallest whose slices leave
+// three in a CTA's ring; a call whose rows leave more than half of the SMs idle
+// spreads each over a larger one while slices keep 2048 elements (a row of
+// 32000 on one CTA is bound by that SM's copy and exponentials).  Teams
+// take about 32 to 128 elements a thread: short rows are bound by their
+// barriers and scalar sections, which more teams overlap.
+static bool resident_plan(ResParams& P, int32_t lt, int64_t rows, int64_t cols) {
+  const int64_t g = lt == PSK_BF16 ? 8 : 4, groups = cols / g, sms = device_sm_count();
+  int64_t k = 1;
+  auto slice = [&](int64_t k) { return (groups + k - 1) / k; };
+  while (k < RES_MAX_CLUSTER && slice(k) * 16 > RES_SLICE) k *= 2;
+  if (slice(k) * 16 > RES_SLICE) return false;
+  while (k < RES_MAX_CLUSTER && rows * k * 2 <= sms && slice(2 * k) * g >= 2048) k *= 2;
+  P.cluster = (int32_t)k;
+  P.slice_groups = (int32_t)(slice(k) > 0 ? slice(k) : 1);
+  P.slot_bytes = (P.slice_groups * 16 + 127) / 128 * 128;
+  const int fits = RES_SMEM / P.slot_bytes < RES_MAX_SLOTS ? RES_SMEM / P.slot_bytes : RES_MAX_SLOTS;
+  const int64_t elements = P.slice_groups * g;
+  P.team_threads = 32;
+  while (P.team_threads < 256 && elements > 32 * P.team_threads) P.team_threads *= 2;
+  P.teams = 512 / P.team_threads;
+  if (rows * k <= sms && elements > 8192) P.team_threads = 512, P.teams = 1;
+  else if (fits == 3) P.team_threads = 192, P.teams = 3;
+  P.slots = fits / P.teams * P.teams;
+  return true;
+}
+
+// Clusters of `k` CTAs that run at once, asked once per device, kernel and size.
+template <int LT, int MODE>
+static int resident_clusters(int k) {
+  static int cache[PSK_MAX_DEVICES][4] = {};
+  static bool limit[PSK_MAX_DEVICES] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= PSK_MAX_DEVICES) dev = 0;
+  const void* kernel = (const void*)loss_resident_kernel<LT, MODE>;
+  smem_limit_once(kernel, RES_SMEM, limit);
+  const int i = k == 1 ? 0 : k == 2 ? 1 : k == 4 ? 2 : 3;
+  if (cache[dev][i] == 0) {
+    int n = 0;
+    if (k == 1) {
+      n = device_sm_count();
+    } else {
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = k, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(k);
+      cfg.blockDim = dim3(RES_THREADS);
+      cfg.dynamicSmemBytes = RES_SMEM;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, loss_resident_kernel<LT, MODE>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 1;
+      }
+      if (n < 1) n = 1;
+    }
+    cache[dev][i] = n;
+  }
+  return cache[dev][i];
+}
+
+// Launch the resident kernel; *parts: the partial sums it leaves.
+template <int LT, int MODE>
+static int resident_launch(ResParams P, const LossParams& L, int* parts, cudaStream_t s) {
+  P.L = L;
+  int64_t n = resident_clusters<LT, MODE>(P.cluster);
+  if (n > L.rows) n = L.rows;
+  if (n * P.teams > LOSS_MAX_CTAS) n = LOSS_MAX_CTAS / P.teams;
+  *parts = (int)n * P.teams;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = P.cluster, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(n * P.cluster));
+  cfg.blockDim = dim3((unsigned)(P.teams * P.team_threads + 32));
+  cfg.dynamicSmemBytes = RES_SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, loss_resident_kernel<LT, MODE>, P);
+  return check_launch("resident loss kernel");
+}
+
+int loss_status(unsigned int* v, bool reset) {
+  if (cudaMemcpyFromSymbol(v, g_pipe_status, sizeof(*v)) != cudaSuccess) return check_launch("device status read");
+  if (reset) {
+    const unsigned int z = 0;
+    if (cudaMemcpyToSymbol(g_pipe_status, &z, sizeof(z)) != cudaSuccess) return check_launch("device status reset");
+  }
+  return PSK_OK;
+}
+
+int loss_set_drop_row(long long row) {
+  if (cudaMemcpyToSymbol(g_pipe_drop_row, &row, sizeof(row)) != cudaSuccess) return check_launch("test hook write");
+  return PSK_OK;
 }
 
 static unsigned loss_grid(int64_t rows) {
@@ -293,6 +842,13 @@ extern "C" int psk_token_logp(const void* logits, int32_t lt, int64_t rows, int6
     return fail(PSK_E_ALIAS, "logp overlaps the logits or the targets");
   LossParams P = loss_params(logits, rows, cols, ldl, scale, targets, tt);
   P.logp = logp;
+  ResParams Q{};
+  if (resident_plan(Q, lt, rows, cols)) {
+    int parts = 0;
+    return with_dtype(lt, [&](auto LT) {
+      return resident_launch<LT.value, LOSS_LOGP>(Q, P, &parts, (cudaStream_t)stream);
+    });
+  }
   const bool vec = rows_vec8(logits, lt, ldl, rows);
   with_dtype(lt, [&](auto LT) {
     return with_bool(vec, [&](auto VEC) {
@@ -308,7 +864,7 @@ extern "C" int psk_policy_loss_workspace(int64_t rows, int64_t cols, uint64_t* b
   clear_error();
   if (!bytes) return fail(PSK_E_NULL, "bytes is NULL");
   if (rows < 0 || cols < 0) return fail(PSK_E_SHAPE, "rows %lld, cols %lld", (long long)rows, (long long)cols);
-  *bytes = 16ull * (uint64_t)(rows < LOSS_MAX_CTAS ? rows : LOSS_MAX_CTAS);
+  *bytes = rows ? 16ull * LOSS_MAX_CTAS : 0;
   return PSK_OK;
 }
 
@@ -331,8 +887,7 @@ extern "C" int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int
     return fail(PSK_E_ARG, "a vector of floats is not 4-byte aligned");
   cudaStream_t s = (cudaStream_t)stream;
   if (rows == 0) {
-    loss_finish_kernel<<<1, 64, 0, s>>>(nullptr, 0, loss);
-    return check_launch("policy loss finishing kernel");
+    return loss_finish(nullptr, 0, loss, s);
   }
   if (!old_logp || !advantage) return fail(PSK_E_NULL, "old_logp or advantage is NULL");
   uint64_t need = 0;
@@ -345,6 +900,7 @@ extern "C" int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int
   const uint64_t xb = rows_bytes(rows, cols, ldl, lt), vb = (uint64_t)rows * 4;
   uint64_t gb = 0;
   if (dlogits) {
+    if ((uintptr_t)dlogits % dtype_size(gt) != 0) return fail(PSK_E_ARG, "dlogits is not aligned to its type");
     if (ldg < cols) return fail(PSK_E_SHAPE, "gradient leading dimension below cols");
     if (!rows_addressable(rows, ldg)) return fail(PSK_E_SHAPE, "rows x leading dimension too large");
     gb = rows_bytes(rows, cols, ldg, gt);
@@ -374,6 +930,18 @@ extern "C" int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int
   P.beta = (float)kl_coef;
   P.loss = loss, P.logp = logp, P.grad = dlogits, P.ldg = ldg;
   P.part = (double*)workspace;
+  ResParams Q{};
+  // Gradient rows must begin as far from a 16-byte boundary as their logits.
+  const bool alike = !dlogits || (lt == gt && ((uintptr_t)logits - (uintptr_t)dlogits) % 16 == 0 &&
+                                  (rows == 1 || ((ldl - ldg) * dtype_size(lt)) % 16 == 0));
+  if (alike && resident_plan(Q, lt, rows, cols)) {
+    int parts = 0;
+    rc = with_dtype(lt, [&](auto LT) {
+      return dlogits ? resident_launch<LT.value, LOSS_GRAD>(Q, P, &parts, s)
+                     : resident_launch<LT.value, LOSS_VALUE>(Q, P, &parts, s);
+    });
+    return rc ? rc : loss_finish(P.part, parts, loss, s);
+  }
   const unsigned grid = loss_grid(rows);
   const bool vec = rows_vec8(logits, lt, ldl, rows) && (!dlogits || rows_vec8(dlogits, gt, ldg, rows));
   with_dtype(lt, [&](auto LT) {
@@ -389,7 +957,5 @@ extern "C" int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int
     });
   });
   rc = check_launch("policy loss kernel");
-  if (rc) return rc;
-  loss_finish_kernel<<<1, 64, 0, s>>>(P.part, (int)grid, loss);
-  return check_launch("policy loss finishing kernel");
+  return rc ? rc : loss_finish(P.part, (int)grid, loss, s);
 }

@@ -253,6 +253,10 @@ extern "C" int psk_norm_backward(const void* x, int32_t xt, const void* ct, int3
     return check_launch("norm backward zero kernel");
   }
   if (!x || !ct || !dx) return fail(PSK_E_NULL, "x, ct or dx is NULL");
+  if ((uintptr_t)x % dtype_size(xt) || (uintptr_t)ct % dtype_size(ct_t) || (uintptr_t)dx % dtype_size(dxt) ||
+      (gamma && (uintptr_t)gamma % dtype_size(param_dtype)) ||
+      (dgamma && (uintptr_t)dgamma % dtype_size(grad_dtype)) || (dbeta && (uintptr_t)dbeta % dtype_size(grad_dtype)))
+    return fail(PSK_E_ARG, "a tensor is not aligned to its type");
   if (ldx < cols || ldc < cols || ldd < cols) return fail(PSK_E_SHAPE, "leading dimension below cols");
   if (!rows_addressable(rows, ldx) || !rows_addressable(rows, ldc) || !rows_addressable(rows, ldd))
     return fail(PSK_E_SHAPE, "rows x leading dimension too large");

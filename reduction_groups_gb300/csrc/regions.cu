@@ -34,6 +34,7 @@
 #include "pipe.cuh"
 #include "pair.cuh"
 #include "rowmath.cuh"
+#include "trainops.h"
 
 namespace psk {
 
@@ -1457,7 +1458,8 @@ extern "C" int psk_test_drop_row(int64_t row) {
   if (row < -1) return fail(PSK_E_ARG, "row %lld (-1 or a local row index)", (long long)row);
   const long long v = row;
   if (cudaMemcpyToSymbol(g_pipe_drop_row, &v, sizeof(v)) != cudaSuccess) return check_launch("test hook write");
-  return lanes_set_drop_row(v);
+  const int rc = lanes_set_drop_row(v);
+  return rc ? rc : loss_set_drop_row(v);
 }
 
 namespace psk {
@@ -1491,7 +1493,10 @@ extern "C" int psk_device_status(uint32_t* status, int32_t reset) {
   unsigned int lv = 0;
   const int lrc = lanes_status(&lv, reset != 0);
   if (lrc) return lrc;
-  *status = v | lv;
+  unsigned int tv = 0;
+  const int trc = loss_status(&tv, reset != 0);
+  if (trc) return trc;
+  *status = v | lv | tv;
   return PSK_OK;
 }
 

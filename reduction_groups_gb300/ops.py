@@ -329,64 +329,83 @@ def psk_adamw_tree_static(leaves, hp, kind="constant", warmup=0, total=1, grad_c
 
 # ------------------------------------------- the training step's two ends
 
+# A call's checks run on the host before every launch: tuples and integers are
+# fetched once, torch's lookups are bound on the first call.
 _CODES = {}
+_IDS = {}
+_F32 = None
+_current_device = _current_stream = None
 
 
-def _code(t, what: str, ids: bool = False) -> int:
-    """The psk_dtype of a value tensor (f32, bf16) or, with ids, of an id tensor (int32, int64)."""
-    if not _CODES:
-        import torch
-
-        _CODES.update({torch.float32: N.PSK_F32, torch.bfloat16: N.PSK_BF16, torch.int32: N.PSK_I32,
-                       torch.int64: N.PSK_I64})
-    c = _CODES.get(t.dtype, -1)
-    if (c in (N.PSK_I32, N.PSK_I64)) if ids else (c in (N.PSK_F32, N.PSK_BF16)):
-        return c
-    raise TypeError(f"{what}: storage type {t.dtype} is not {'int32 or int64' if ids else 'f32 or bf16'}")
-
-
-def _same_device(stream, *ts) -> int:
-    """The stream's handle, the tensors checked to live on the device it runs on (the current one)."""
+def _bind_torch() -> None:
+    global _F32, _current_device, _current_stream
     import torch
 
-    dev = ts[0].device
-    for t in ts:
-        if t is not None and t.device != dev:
+    _CODES.update({torch.float32: N.PSK_F32, torch.bfloat16: N.PSK_BF16})
+    _IDS.update({torch.int32: N.PSK_I32, torch.int64: N.PSK_I64})
+    _F32 = torch.float32
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_stream = raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
+    _current_device = torch.cuda.current_device
+
+
+def _code(t, what: str) -> int:
+    c = _CODES.get(t.dtype)
+    if c is None:
+        raise TypeError(f"{what}: storage type {t.dtype} is not f32 or bf16")
+    return c
+
+
+def _id_code(t, what: str) -> int:
+    c = _IDS.get(t.dtype)
+    if c is None:
+        raise TypeError(f"{what}: storage type {t.dtype} is not int32 or int64")
+    return c
+
+
+def _same_device(stream, first, *rest) -> int:
+    """The stream's handle, the tensors checked to live on the device it runs on (the current one)."""
+    if _F32 is None:
+        _bind_torch()
+    index = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != index:
             raise ValueError("the tensors must live on one device")
-    if dev.type != "cuda":
+    if index < 0:
+        if any(t is not None and t.device != first.device for t in rest):
+            raise ValueError("the tensors must live on one device")
         raise ValueError("the tensors must live on a CUDA device")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors live on {dev}, which is not the current device")
+    if index != _current_device():
+        raise ValueError(f"the tensors live on cuda:{index}, which is not the current device")
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    if stream.device != dev:
-        raise ValueError(f"the stream runs on {stream.device}, the tensors live on {dev}")
+        return _current_stream(index)
+    if stream.device.index != index:
+        raise ValueError(f"the stream runs on {stream.device}, the tensors live on cuda:{index}")
     return stream.cuda_stream
 
 
 def _matrix(t, what: str, shape=None) -> int:
     """The leading dimension of a 2-D tensor of contiguous rows."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    size, stride = t.shape, t.stride()
+    if len(size) != 2 or (stride[1] != 1 and size[1] > 1):
         raise ValueError(f"{what} must be a 2-D tensor with contiguous rows")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    rows, cols = t.shape
-    if rows > 1 and t.stride(0) < cols:
+    if shape is not None and size != shape:
+        raise ValueError(f"{what} has shape {tuple(size)}, not {tuple(shape)}")
+    if stride[0] >= size[1]:
+        return stride[0]
+    if size[0] > 1:
         raise ValueError(f"{what} has rows that overlap")
-    return max(t.stride(0), cols)
+    return size[1]
 
 
 def _vector(t, what: str, n: int, f32: bool = False):
     """The address of a contiguous 1-D tensor of n elements (None: NULL)."""
     if t is None:
         return None
-    if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what} must be a contiguous vector of {n} elements")
-    if f32:
-        import torch
-
-        if t.dtype != torch.float32:
-            raise TypeError(f"{what} must be f32")
+    if f32 and t.dtype is not _F32:
+        raise TypeError(f"{what} must be f32")
     return t.data_ptr()
 
 
@@ -410,7 +429,7 @@ def psk_embed(ids, table, y, scale: float = 1.0, stream=None) -> None:
     s = _same_device(stream, table, ids, y)
     n, (vocab, cols) = ids.numel(), table.shape
     ldt, ldy = _matrix(table, "table"), _matrix(y, "y", (n, cols))
-    N.check(N.lib().psk_embed(_vector(ids, "ids", n), _code(ids, "ids", True), n, table.data_ptr(),
+    N.check(N.lib().psk_embed(_vector(ids, "ids", n), _id_code(ids, "ids"), n, table.data_ptr(),
                               _code(table, "table"), vocab, cols, ldt, scale, y.data_ptr(), _code(y, "y"), ldy, s))
 
 
@@ -429,7 +448,7 @@ def psk_embed_backward(ids, ct, dtable, scale: float = 1.0, accumulate: bool = F
     n, (vocab, cols) = ids.numel(), dtable.shape
     ldd, ldc = _matrix(dtable, "dtable"), _matrix(ct, "ct", (n, cols))
     ws, wb = _scratch(workspace)
-    N.check(N.lib().psk_embed_backward(_vector(ids, "ids", n), _code(ids, "ids", True), n, ct.data_ptr(),
+    N.check(N.lib().psk_embed_backward(_vector(ids, "ids", n), _id_code(ids, "ids"), n, ct.data_ptr(),
                                        _code(ct, "ct"), ldc, scale, dtable.data_ptr(), _code(dtable, "dtable"), vocab,
                                        cols, ldd, 1 if accumulate else 0, ws, wb, s))
 
@@ -440,8 +459,6 @@ def psk_dropout(x, y, p: float, seed: int, offset: int = 0, residual=None, count
     backward is psk_dropout(ct, dx, p, seed, offset).  counter: a one-element
     int64 device tensor added to offset when the kernel runs (for captured
     graphs)."""
-    import torch
-
     s = _same_device(stream, x, y, residual, counter)
     if x.dim() == 1:
         if y.dim() != 1 or (residual is not None and residual.dim() != 1):
@@ -450,7 +467,7 @@ def psk_dropout(x, y, p: float, seed: int, offset: int = 0, residual=None, count
         residual = None if residual is None else residual[None]
     ldx, ldy = _matrix(x, "x"), _matrix(y, "y", x.shape)
     ldr = 0 if residual is None else _matrix(residual, "residual", x.shape)
-    if counter is not None and (counter.dtype != torch.int64 or counter.numel() != 1):
+    if counter is not None and (_IDS.get(counter.dtype) != N.PSK_I64 or counter.numel() != 1):
         raise TypeError("counter must be a one-element int64 tensor")
     for v, what in ((seed, "seed"), (offset, "offset")):
         if not 0 <= v < 1 << 64:
@@ -497,7 +514,7 @@ def psk_token_logp(logits, targets, logp, scale: float = 1.0, stream=None) -> No
     rows, cols = logits.shape
     ldl = _matrix(logits, "logits")
     N.check(N.lib().psk_token_logp(logits.data_ptr(), _code(logits, "logits"), rows, cols, ldl, scale,
-                                   _vector(targets, "targets", rows), _code(targets, "targets", True),
+                                   _vector(targets, "targets", rows), _id_code(targets, "targets"),
                                    _vector(logp, "logp", rows, True), s))
 
 
@@ -520,7 +537,7 @@ def psk_policy_loss(logits, targets, old_logp, advantage, weight, loss, logp=Non
     ldg = 0 if dlogits is None else _matrix(dlogits, "dlogits", logits.shape)
     ws, wb = _scratch(workspace)
     N.check(N.lib().psk_policy_loss(logits.data_ptr(), _code(logits, "logits"), rows, cols, ldl, scale,
-                                    _vector(targets, "targets", rows), _code(targets, "targets", True),
+                                    _vector(targets, "targets", rows), _id_code(targets, "targets"),
                                     _vector(old_logp, "old_logp", rows, True),
                                     _vector(ref_logp, "ref_logp", rows, True),
                                     _vector(advantage, "advantage", rows, True),

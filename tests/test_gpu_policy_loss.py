@@ -208,3 +208,37 @@ def test_repeats_bit_for_bit_on_a_side_stream_and_in_a_graph(R, cols):
     for o in (second, third):
         assert all(torch.equal(a, b) for a, b in zip(first[:3], o[:3]))
     assert R.psk_device_status() == 0
+
+
+@pytest.mark.parametrize("rows,cols,lt", [(700, 32000, "bf16"), (500, 20001, "bf16"), (2000, 3000, "bf16"),
+                                          (400, 33000, "f32"), (900, 9000, "f32")])
+def test_many_rows_a_cta(R, rows, cols, lt):
+    _check(R, rows, cols, lt, lt, 0.1, 1.0)
+
+
+@pytest.mark.parametrize("rows,cols,lt", [(200, 131072, "bf16"), (90, 100003, "f32"), (130, 50000, "bf16")])
+def test_many_rows_a_cluster(R, rows, cols, lt):
+    _check(R, rows, cols, lt, lt, 0.1, 1.0)
+    rng = np.random.default_rng(1)
+    x, xv, t, targets, *_ = _inputs(rng, rows, cols, lt, 1.0)
+    logp = torch.empty(rows, device="cuda")
+    R.psk_token_logp(x, targets, logp)
+    want, bound, _, _ = OT.token_logp(xv, t, 1.0)
+    close(logp, want, bound, "f32")
+
+
+@pytest.mark.parametrize("rows,cols", [(400, 32000), (100, 131072)])
+def test_a_lost_copy_ends_in_a_status_not_a_hang(R, rows, cols):
+    x = torch.randn(rows, cols, device="cuda", dtype=torch.bfloat16)
+    t, logp = torch.zeros(rows, dtype=torch.int64, device="cuda"), torch.empty(rows, device="cuda")
+    assert R.psk_device_status(reset=True) == 0
+    try:
+        R.psk_test_drop_row(1)
+        R.psk_token_logp(x, t, logp)
+        torch.cuda.synchronize()
+        assert R.psk_device_status(reset=True) == 1
+    finally:
+        R.psk_test_drop_row(-1)
+    R.psk_token_logp(x, t, logp)
+    torch.cuda.synchronize()
+    assert R.psk_device_status() == 0 and bool(logp.isfinite().all())
