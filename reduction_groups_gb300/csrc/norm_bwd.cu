@@ -154,6 +154,204 @@ __global__ void __launch_bounds__(NB_THREADS) norm_bwd_apply_kernel(const __grid
   }
 }
 
+// ---------------------------------------------------------- the fused kernel
+//
+// One pass over rows of up to 8192 columns of one storage type: a team of T
+// threads holds a row's x and ct in registers (NV groups of eight columns a
+// thread) from the reductions to dx, while its next row's loads are in
+// flight, and keeps its columns' dgamma and dbeta sums in registers over all
+// of its rows.  The floor is one read of x and ct and one write of dx; a
+// CTA's column sums go to the workspace once.
+constexpr int NB_FUSED_COLS = 8192;
+constexpr int NB_ROWS_PER_TEAM = 4;        // at least, where there are as many
+
+// Eight of a thread's columns as loaded.
+template <int TY, bool VEC>
+struct Octet {
+  static constexpr int W = VEC && TY == PSK_BF16 ? 4 : 8;
+  uint32_t w[W];
+  __device__ __forceinline__ float get(int k) const {
+    if constexpr (VEC && TY == PSK_BF16) return __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+    else return __uint_as_float(w[k]);
+  }
+};
+
+// The columns of thread t: group j is columns (j T + t) 8 + k with 16-byte
+// accesses, else j 8 T + k T + t (a warp's accesses then coalesce).
+template <int TY, bool VEC>
+struct TeamCols {
+  int T, t, cols;
+  __device__ __forceinline__ int col(int j, int k) const { return VEC ? (j * T + t) * 8 + k : (j * 8 + k) * T + t; }
+  __device__ __forceinline__ bool has(int j, int k) const { return col(j, VEC ? 0 : k) < cols; }
+  __device__ __forceinline__ void load(const void* p, int64_t row, int j, Octet<TY, VEC>& o) const {
+    if constexpr (VEC) {
+      const bool in = has(j, 0);
+      if constexpr (TY == PSK_BF16) {
+        const uint4 u = in ? __ldcs((const uint4*)((const uint16_t*)p + row + col(j, 0))) : make_uint4(0, 0, 0, 0);
+        o.w[0] = u.x, o.w[1] = u.y, o.w[2] = u.z, o.w[3] = u.w;
+      } else {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        const uint4* q = (const uint4*)((const float*)p + row + col(j, 0));
+        const uint4 a = in ? __ldcs(q) : z, b = in ? __ldcs(q + 1) : z;
+        o.w[0] = a.x, o.w[1] = a.y, o.w[2] = a.z, o.w[3] = a.w, o.w[4] = b.x, o.w[5] = b.y, o.w[6] = b.z, o.w[7] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        o.w[k] = 0;
+        if (has(j, k)) {
+          if constexpr (TY == PSK_BF16) o.w[k] = (uint32_t)((const uint16_t*)p)[row + col(j, k)] << 16;
+          else o.w[k] = ((const uint32_t*)p)[row + col(j, k)];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(void* p, int64_t row, int j, const float* v) const {
+    if constexpr (VEC) {
+      if (has(j, 0)) store8<TY, true>(p, row + col(j, 0), 8, v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (has(j, k)) {
+          if constexpr (TY == PSK_BF16) ((uint16_t*)p)[row + col(j, k)] = f32_to_bf16_bits(v[k]);
+          else ((float*)p)[row + col(j, k)] = v[k];
+        }
+    }
+  }
+};
+
+struct NormFusedParams {
+  NormBwdParams B;
+  int32_t team, teams;       // threads of a team, teams of a CTA
+};
+
+template <int TY, int KIND, bool VEC, int NV, int CTA>
+__global__ void __launch_bounds__(CTA, 512 / CTA) norm_bwd_fused_kernel(const __grid_constant__ NormFusedParams Q) {
+  extern __shared__ float colsum[];                       // [cols] of the CTA, added team by team
+  __shared__ float2 red[2][CTA / 32];
+  const NormBwdParams& P = Q.B;
+  const int T = Q.team, team = threadIdx.x / T, t = threadIdx.x - team * T, nw = T / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const TeamCols<TY, VEC> tc{T, t, (int)P.cols};
+  const int64_t step = (int64_t)gridDim.x * Q.teams;
+  int flip = 0;
+  // Sum two values over the team; one barrier (the buffers alternate).
+  auto team_sum = [&](float a, float b) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+      b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    if (nw == 1) return make_float2(a, b);
+    flip ^= 1;
+    if (lane == 0) red[flip][warp] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(T) : "memory");
+    float2 s = red[flip][team * nw];
+    for (int w = 1; w < nw; ++w) {
+      const float2 u = red[flip][team * nw + w];
+      s.x += u.x, s.y += u.y;
+    }
+    return s;
+  };
+
+  float gamma[NV][8], dg[NV][8], db[KIND == PSK_NORM_LAYER ? NV : 1][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = tc.col(j, k);
+      gamma[j][k] = 1.0f;
+      if (P.gamma && c < P.cols)
+        gamma[j][k] = P.param_dtype == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)P.gamma)[c])
+                                                : ((const float*)P.gamma)[c];
+      dg[j][k] = 0.0f;
+      if (KIND == PSK_NORM_LAYER) db[j][k] = 0.0f;
+    }
+
+  int64_t r = (int64_t)blockIdx.x * Q.teams + team;
+  Octet<TY, VEC> x[NV], c[NV];
+  if (r < P.rows) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) tc.load(P.x, r * P.ldx, j, x[j]), tc.load(P.ct, r * P.ldc, j, c[j]);
+  }
+  for (; r < P.rows; r += step) {
+    float xv[NV][8], cv[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) xv[j][k] = x[j].get(k), cv[j][k] = c[j].get(k);
+    if (r + step < P.rows) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        tc.load(P.x, (r + step) * P.ldx, j, x[j]), tc.load(P.ct, (r + step) * P.ldc, j, c[j]);
+    }
+    float mg = 0.0f;
+    if (KIND == PSK_NORM_LAYER) {
+      float s = 0.0f, u = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += xv[j][k], u = fmaf(cv[j][k], gamma[j][k], u);
+      const float2 v = team_sum(s, u);
+      const float mu = v.x * P.inv_cols;
+      mg = v.y * P.inv_cols;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) xv[j][k] = tc.has(j, k) ? xv[j][k] - mu : 0.0f;
+    }
+    float s = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s = fmaf(xv[j][k], xv[j][k], s);
+        u = fmaf(xv[j][k], cv[j][k] * gamma[j][k], u);
+      }
+    const float2 v = team_sum(s, u);
+    const float rd = 1.0f / sqrtf(v.x * P.inv_cols + P.eps);
+    const float m2 = v.y * rd * P.inv_cols;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float xh = xv[j][k] * rd;
+        const float g = cv[j][k] * gamma[j][k];
+        o[k] = fmaf(-xh, m2, KIND == PSK_NORM_LAYER ? g - mg : g) * rd;
+        dg[j][k] = fmaf(cv[j][k], xh, dg[j][k]);
+        if (KIND == PSK_NORM_LAYER) db[j][k] += cv[j][k];
+      }
+      tc.store(P.dx, r * P.ldd, j, o);
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!P.dgamma && !P.dbeta) return;
+  // The CTA's column sums: its teams' in turn, through shared memory.
+#pragma unroll
+  for (int which = 0; which < (KIND == PSK_NORM_LAYER ? 2 : 1); ++which) {
+    float* part = P.part + ((int64_t)which * P.blocks + blockIdx.x) * P.pcols;
+    for (int q = 0; q < Q.teams; ++q) {
+      if (q > 0) __syncthreads();
+      if (team == q) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int col = tc.col(j, k);
+            if (col < P.cols) {
+              float a = which == 0 ? dg[j][k] : db[KIND == PSK_NORM_LAYER ? j : 0][k];
+              if (q > 0) a += colsum[col];
+              if (q + 1 == Q.teams) part[col] = a;
+              else colsum[col] = a;
+            }
+          }
+      }
+    }
+    if (Q.teams > 1) __syncthreads();
+  }
+}
+
 // The row blocks' sums joined: 32 columns a CTA, warps over blocks in turn.
 __global__ void __launch_bounds__(NB_THREADS) norm_bwd_join_kernel(const __grid_constant__ NormBwdParams P) {
   __shared__ float sums[NB_WARPS][32];
@@ -161,6 +359,7 @@ __global__ void __launch_bounds__(NB_THREADS) norm_bwd_join_kernel(const __grid_
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   const int which = blockIdx.y;
   void* out = which ? P.dbeta : P.dgamma;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!out) return;
   float s = 0.0f;
   if (col < P.cols) {
@@ -186,8 +385,8 @@ __global__ void __launch_bounds__(NB_THREADS) norm_bwd_zero_kernel(const __grid_
   else ((float*)out)[col] = 0.0f;
 }
 
-// Row blocks of the column sums: enough CTAs to fill the GPU, at least 16
-// rows each.
+// Row blocks of the two-pass kernels' column sums: enough CTAs to fill the
+// GPU, at least 16 rows each.
 static int norm_bwd_blocks(int64_t rows, int64_t cols) {
   const int64_t slices = (cols + 255) / 256;
   int64_t b = (152 * 8 + slices - 1) / slices;
@@ -195,11 +394,58 @@ static int norm_bwd_blocks(int64_t rows, int64_t cols) {
   return (int)(b < 1 ? 1 : b > NB_MAX_BLOCKS ? NB_MAX_BLOCKS : b);
 }
 
+// The fused kernel's shape: teams of the fewest threads that hold a row in
+// one or two groups of eight columns each.
+struct FusedShape {
+  int team, teams, nv, cta;
+};
+static FusedShape fused_shape(int64_t cols) {
+  FusedShape f{32, 1, 1, 256};
+  const int64_t groups = (cols + 7) / 8;
+  while (f.team < 256 && f.team < groups) f.team *= 2;
+  if (groups > 256) f.nv = 2;
+  if (groups > 512) f.team = f.cta = 512;
+  f.teams = f.cta / f.team;
+  return f;
+}
+
+// Most CTAs of the fused kernel (two of 256 threads an SM, or one of 512, on
+// 160 SMs), at least NB_ROWS_PER_TEAM rows for each team.
+static int fused_blocks(int64_t rows, int64_t cols) {
+  const FusedShape f = fused_shape(cols);
+  const int64_t most = 160 * (512 / f.cta), want = (rows + f.teams * NB_ROWS_PER_TEAM - 1) / (f.teams * NB_ROWS_PER_TEAM);
+  return (int)(want < most ? want : most);
+}
+
 static uint64_t norm_bwd_layout(int64_t rows, int64_t cols, uint64_t* part) {
   const uint64_t stats = ((uint64_t)rows * 16 + 255) / 256 * 256;
   const uint64_t pcols = (uint64_t)(cols + 7) / 8 * 8;
   *part = stats;
-  return stats + 2ull * norm_bwd_blocks(rows, cols) * pcols * 4;
+  int blocks = norm_bwd_blocks(rows, cols);
+  if (cols <= NB_FUSED_COLS && fused_blocks(rows, cols) > blocks) blocks = fused_blocks(rows, cols);
+  return stats + 2ull * blocks * pcols * 4;
+}
+
+template <int TY, int KIND, bool VEC, int NV, int CTA>
+static void fused_launch(const NormFusedParams& Q, cudaStream_t s) {
+  norm_bwd_fused_kernel<TY, KIND, VEC, NV, CTA>
+      <<<(unsigned)Q.B.blocks, CTA, Q.teams > 1 ? (size_t)Q.B.cols * 4 : 0, s>>>(Q);
+}
+
+// The column sums' join, launched so that its set-up overlaps the kernel
+// before it.
+static int norm_bwd_join(const NormBwdParams& P, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((P.cols + 31) / 32), P.dbeta ? 2 : 1);
+  cfg.blockDim = dim3(NB_THREADS);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, norm_bwd_join_kernel, P);
+  return check_launch("norm backward join kernel");
 }
 
 static int norm_bwd_check_sizes(int64_t rows, int64_t cols) {
@@ -290,6 +536,26 @@ extern "C" int psk_norm_backward(const void* x, int32_t xt, const void* ct, int3
   P.blocks = norm_bwd_blocks(rows, cols);
   const bool vec = rows_vec8(x, xt, ldx, rows) && rows_vec8(ct, ct_t, ldc, rows) && rows_vec8(dx, dxt, ldd, rows) &&
                    (!gamma || rows_vec8(gamma, param_dtype, cols, 1));
+  if (cols <= NB_FUSED_COLS && xt == ct_t && xt == dxt) {
+    const FusedShape f = fused_shape(cols);
+    NormFusedParams Q{P, f.team, f.teams};
+    const int64_t resident = (int64_t)device_sm_count() * (512 / f.cta);
+    Q.B.blocks = fused_blocks(rows, cols);
+    if (Q.B.blocks > resident) Q.B.blocks = (int)resident;
+    with_dtype(xt, [&](auto TY) {
+      return with_bool(kind == PSK_NORM_LAYER, [&](auto LAYER) {
+        constexpr int KIND = LAYER.value ? PSK_NORM_LAYER : PSK_NORM_RMS;
+        return with_bool(vec && cols % 8 == 0, [&](auto VEC) {
+          if (f.cta == 512) fused_launch<TY.value, KIND, VEC.value, 2, 512>(Q, s);
+          else if (f.nv == 2) fused_launch<TY.value, KIND, VEC.value, 2, 256>(Q, s);
+          else fused_launch<TY.value, KIND, VEC.value, 1, 256>(Q, s);
+          return 0;
+        });
+      });
+    });
+    rc = check_launch("norm backward fused kernel");
+    return rc || (!dgamma && !dbeta) ? rc : norm_bwd_join(Q.B, s);
+  }
   const int64_t most = (int64_t)device_sm_count() * 8;
   const unsigned rgrid = (unsigned)(rows < most ? rows : most);
   const dim3 agrid((unsigned)((cols + 255) / 256), (unsigned)P.blocks);
@@ -309,6 +575,5 @@ extern "C" int psk_norm_backward(const void* x, int32_t xt, const void* ct, int3
   });
   rc = check_launch("norm backward kernels");
   if (rc || (!dgamma && !dbeta)) return rc;
-  norm_bwd_join_kernel<<<dim3((unsigned)((cols + 31) / 32), 2), NB_THREADS, 0, s>>>(P);
-  return check_launch("norm backward join kernel");
+  return norm_bwd_join(P, s);
 }
