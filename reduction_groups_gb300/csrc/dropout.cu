@@ -45,34 +45,34 @@ __device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, u
   return make_uint4(c0, c1, c2, c3);
 }
 
-// One group of eight columns a thread; RT < 0: no residual.  x and the
-// residual are loaded before the generator's ~160 integer instructions, which
-// hide their latency.
+// One group of eight columns a thread; RT < 0: no residual.  VEC: rows of
+// whole groups, moved by 16-byte accesses, all loads issued before the
+// generator's instructions, which hide their latency.
 template <int XT, int RT, int YT, bool VEC>
 __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const __grid_constant__ DropoutParams P) {
   const uint64_t t = (uint64_t)blockIdx.x * DROP_THREADS + threadIdx.x;
   if (t >= P.items) return;
   const uint32_t r = P.per_row.div((uint32_t)t);
   const uint32_t g = (uint32_t)t - r * P.per_row.d;
-  const int64_t c = (int64_t)g * 8;
-  const int64_t left = P.cols - c;
-  const int n = left < 8 ? (int)left : 8;
   const uint32_t row = P.row0 + r;
-  float x[8], res[8];
-  load8<XT, VEC>(P.x, (int64_t)row * P.ldx + c, n, x);
-  if (RT >= 0) load8<(RT >= 0 ? RT : 0), VEC>(P.res, (int64_t)row * P.ldr + c, n, res);
-  uint32_t w[8];
+  constexpr int RES = RT >= 0 ? RT : 0;
+  const int64_t c = (int64_t)g * 8;
+  const Columns<VEC, 8> cols(c, 1, 0, P.cols);
+  Piece<XT, VEC, 8> x;
+  Piece<RES, VEC, 8> res;
+  cols.load(P.x, (int64_t)row * P.ldx, x);
+  if (RT >= 0) cols.load(P.res, (int64_t)row * P.ldr, res);
   const uint64_t off = P.offset + (P.counter ? *P.counter : 0);
   const uint4 w0 = philox(2 * g, row, (uint32_t)off, (uint32_t)(off >> 32), P.key);
   const uint4 w1 = philox(2 * g + 1, row, (uint32_t)off, (uint32_t)(off >> 32), P.key);
-  w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w, w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
+  const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+  float y[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    float v = (w[k] > P.last_dropped || P.keep_all) ? __fmul_rn(x[k], P.scale) : 0.0f;
-    if (RT >= 0) v = __fadd_rn(res[k], v);
-    x[k] = v;
+    y[k] = (w[k] > P.last_dropped || P.keep_all) ? __fmul_rn(x.get(k), P.scale) : 0.0f;
+    if (RT >= 0) y[k] = __fadd_rn(res.get(k), y[k]);
   }
-  store8<YT, VEC>(P.y, (int64_t)row * P.ldy + c, n, x);
+  cols.template store<YT>(P.y, (int64_t)row * P.ldy, y);
 }
 
 }  // namespace psk
@@ -118,7 +118,7 @@ extern "C" int psk_dropout(const void* x, int32_t xt, const void* residual, int3
   P.keep_all = dropped == 0;
   P.last_dropped = (uint32_t)(dropped - 1);
   P.scale = (float)(1.0 / (1.0 - p));
-  const bool vec = rows_vec8(x, xt, ldx, rows) && rows_vec8(y, yt, ldy, rows) &&
+  const bool vec = cols % 8 == 0 && rows_vec8(x, xt, ldx, rows) && rows_vec8(y, yt, ldy, rows) &&
                    (!residual || rows_vec8(residual, rt, ldr, rows));
   cudaStream_t s = (cudaStream_t)stream;
   // Slices of rows whose groups are counted in 32 bits (one slice up to

@@ -2,28 +2,18 @@
 //
 // Forward: a gather of table rows, scaled.  Backward: the leaf's gradient
 //   dtable[v, :] = scale * sum of ct[i, :] over the positions i with id v,
-// without atomics: positions are sorted by id (a stable radix sort, so each
+// without atomics on it: positions are sorted by id (a stable sort, so each
 // id's positions stay in increasing order), the sorted list is cut into runs
 // of EMB_RUN entries, each run is summed left to right by its own warps, and
 // an id whose entries span several runs has its run sums joined left to
 // right.  The order of every sum is fixed by the ids alone.
 #include "vec8.cuh"
-
-#include <cooperative_groups.h>
-
-namespace cg = cooperative_groups;
+#include "pair.cuh"
 
 namespace psk {
 
 constexpr int EMB_THREADS = 256;
 constexpr int EMB_RUN = 32;               // sorted entries a warp sums (one id per lane)
-constexpr int SORT_CTAS = 8;              // one cluster
-constexpr int SORT_THREADS = 512;
-constexpr int SORT_WARPS = SORT_THREADS / 32;
-constexpr int SORT_BITS = 8;              // digit of a pass
-constexpr int SORT_BINS = 1 << SORT_BITS;
-constexpr int SORT_PER_LANE = 8;          // entries a lane ranks in one tile
-constexpr int SORT_TILE = SORT_THREADS * SORT_PER_LANE;
 
 // ------------------------------------------------------------------ forward
 
@@ -43,26 +33,46 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int64_t i) {
   return I64 ? ((const int64_t*)ids)[i] : (int64_t)((const int32_t*)ids)[i];
 }
 
-template <int TT, int YT, bool I64, bool VEC>
+// One group of eight columns a thread, of ROWS rows `stride` items apart (all
+// of their loads in flight at once).
+template <int TT, int YT, bool I64, bool VEC, int ROWS>
 __global__ void __launch_bounds__(EMB_THREADS) embed_kernel(const __grid_constant__ EmbedParams P) {
-  const uint64_t t = (uint64_t)blockIdx.x * EMB_THREADS + threadIdx.x;
-  if (t >= P.items) return;
-  const uint32_t r = P.per_row.div((uint32_t)t);
-  const int64_t c = (int64_t)((uint32_t)t - r * P.per_row.d) * 8;
-  const int64_t left = P.cols - c;
-  const int n = left < 8 ? (int)left : 8;
-  const int64_t row = P.row0 + r;
-  const int64_t id = load_id<I64>(P.ids, row);
-  float v[8] = {};
-  if (id >= 0 && id < P.vocab) {
-    load8<TT, VEC>(P.table, id * P.ldt + c, n, v);
+  const uint64_t t0 = (uint64_t)blockIdx.x * EMB_THREADS + threadIdx.x;
+  const uint64_t stride = (uint64_t)gridDim.x * EMB_THREADS;
+  Piece<TT, VEC, 8> v[ROWS];
+  int64_t id[ROWS], row[ROWS];
+  uint32_t g[ROWS];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(v[k], P.scale);
+  for (int q = 0; q < ROWS; ++q) {
+    const uint64_t t = t0 + q * stride;
+    const uint32_t r = P.per_row.div((uint32_t)t);
+    g[q] = (uint32_t)t - r * P.per_row.d;
+    row[q] = t < P.items ? P.row0 + r : -1;
+    id[q] = row[q] >= 0 ? load_id<I64>(P.ids, row[q]) : -1;
   }
-  store8<YT, VEC>(P.y, row * P.ldy + c, n, v);
+#pragma unroll
+  for (int q = 0; q < ROWS; ++q)
+    if (id[q] >= 0 && id[q] < P.vocab)
+      Columns<VEC, 8>((int64_t)g[q] * 8, 1, 0, P.cols).load(P.table, id[q] * P.ldt, v[q]);
+#pragma unroll
+  for (int q = 0; q < ROWS; ++q) {
+    if (row[q] < 0) continue;
+    const bool in = id[q] >= 0 && id[q] < P.vocab;
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = in ? __fmul_rn(v[q].get(k), P.scale) : 0.0f;
+    Columns<VEC, 8>((int64_t)g[q] * 8, 1, 0, P.cols).template store<YT>(P.y, row[q] * P.ldy, y);
+  }
 }
 
 // ----------------------------------------------------------------- backward
+
+constexpr int SORT_THREADS = 512;
+constexpr int SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_PER_LANE = 16;
+constexpr int SORT_TILE = SORT_THREADS * SORT_PER_LANE;   // ids scanned at a time
+constexpr int SORT_BINS = 2048;                           // most ids of a slice
+constexpr int SORT_LIST = SORT_TILE;                      // entries ranked at a time
 
 struct EmbedGradParams {
   const void* ids;
@@ -70,207 +80,276 @@ struct EmbedGradParams {
   void* d;
   int64_t vocab, cols, ldc, ldd;
   int64_t tokens;
-  uint32_t* key[2];      // sort buffers: ids (vocab for a position without one) ...
-  uint32_t* pos[2];      // ... and their positions
+  uint32_t* key;         // the sorted ids of the positions that have one ...
+  uint32_t* pos;         // ... and the positions
+  uint8_t* seen;         // per id: does it occur
+  uint32_t* entries;     // length of the sorted list
   float* head;           // per run: the sum of its leading entries whose id the run before ends with
   float* tail;           // per run: the sum of its trailing entries whose id the next run goes on with
   int64_t pcols;         // row length of head and tail
-  int32_t passes, out;   // radix passes and the buffer the last one writes
-  int32_t bits;          // digit bits of each pass
+  int32_t slice_ids;     // ids of a sorting CTA's slice of the vocabulary
   int32_t accumulate;
-  int32_t slices;        // column slices of 256 of a row
+  int32_t slices;        // column slices of a row in the run sums
+  int32_t run_ctas;      // CTAs of the run sums; the others zero the rows that do not occur
   float scale;
 };
 
-// Zero the rows of the gradient (8 columns a step).
-template <int DT, bool VEC>
-__device__ void zero_rows(const EmbedGradParams& P, int64_t first, int64_t step) {
-  const float z[8] = {};
-  const uint32_t per_row = (uint32_t)((P.cols + 7) / 8);
-  const int64_t total = P.vocab * per_row;
-  for (int64_t t = first; t < total; t += step) {
-    const int64_t r = t / per_row;
-    const int64_t c = (t - r * per_row) * 8;
-    store8<DT, VEC>(P.d, r * P.ldd + c, (int)(P.cols - c < 8 ? P.cols - c : 8), z);
-  }
-}
+// The stable sort, without exchange between CTAs: each takes a slice of the
+// vocabulary, reads all ids (from L2: 8 bytes a token), counts those below
+// its slice -- its entries' first place in the list -- and collects its own
+// positions in order; the few collected entries are then counting-sorted by
+// id, warp by warp in order.  More entries than the collecting list holds
+// (a slice with very frequent ids in a long batch) are collected and ranked
+// a list at a time in a second scan.
+struct SortShared {
+  uint32_t pos[SORT_LIST];
+  uint16_t key[SORT_LIST];
+  uint32_t place[SORT_BINS];                 // counts, then each id's next place
+  uint16_t before[SORT_WARPS][SORT_BINS];    // a warp's entries of an id; then those of the warps before, growing
+  uint32_t warp_total[SORT_WARPS];
+  uint32_t below, total;
+};
 
-// Cluster 0 sorts the positions by id; the other clusters meanwhile zero the
-// gradient (when it is not accumulated into), so the sort's latency hides
-// behind the store of the rows that no position has.
-//
-// One radix pass: every CTA counts the digits of its own range of entries;
-// the counts of all CTAs, read through distributed shared memory, give each
-// digit's first place for this CTA's entries; then tile by tile each warp
-// ranks its entries among equal digits in order (match_any), and the entries
-// move to their places.  Entries live in global memory (L2); the cluster
-// barrier orders the passes.
-template <bool I64, int DT, bool VEC>
-__global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_THREADS)
-    embed_sort_kernel(const __grid_constant__ EmbedGradParams P) {
-  if (blockIdx.x >= SORT_CTAS) {
-    zero_rows<DT, VEC>(P, (int64_t)(blockIdx.x - SORT_CTAS) * SORT_THREADS + threadIdx.x,
-                       (int64_t)(gridDim.x - SORT_CTAS) * SORT_THREADS);
+template <bool I64>
+__global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_constant__ EmbedGradParams P) {
+  extern __shared__ __align__(16) unsigned char sort_smem[];
+  SortShared& S = *reinterpret_cast<SortShared*>(sort_smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t lt = (1u << lane) - 1;
+  const int64_t first = (int64_t)blockIdx.x * P.slice_ids;
+  const int bins = (int)(P.vocab - first < P.slice_ids ? P.vocab - first : P.slice_ids);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int b = tid; b < bins; b += SORT_THREADS) S.place[b] = 0;
+  if (tid == 0) S.below = 0, S.total = 0;
+  __syncthreads();
+
+  // Scan the ids of one tile: the slice's entries go to the list from `at` on,
+  // in order, where it has room; their number is returned.
+  uint32_t below = 0;
+  auto scan_tile = [&](int64_t t0, uint32_t at, bool count) -> uint32_t {
+    uint32_t key[SORT_PER_LANE];
+    uint32_t mine = 0;
+    const int64_t w0 = t0 + (int64_t)warp * 32 * SORT_PER_LANE + lane;
+#pragma unroll
+    for (int k = 0; k < SORT_PER_LANE; ++k) {
+      const int64_t i = w0 + 32 * k;
+      const int64_t id = i < P.tokens ? load_id<I64>(P.ids, i) : -1;
+      if (count) below += id >= 0 && id < first;
+      const int64_t local = id - first;
+      key[k] = local >= 0 && local < bins ? (uint32_t)local : 0xFFFFFFFFu;
+    }
+#pragma unroll
+    for (int k = 0; k < SORT_PER_LANE; ++k) mine += __popc(__ballot_sync(0xFFFFFFFFu, key[k] != 0xFFFFFFFFu));
+    __syncthreads();                         // the list's and warp_total's last readers are done
+    if (lane == 0) S.warp_total[warp] = mine;
+    __syncthreads();
+    uint32_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < SORT_WARPS; ++w) {
+      const uint32_t n = S.warp_total[w];
+      if (w < warp) at += n;
+      sum += n;
+    }
+#pragma unroll
+    for (int k = 0; k < SORT_PER_LANE; ++k) {
+      const bool in = key[k] != 0xFFFFFFFFu;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, in);
+      if (in) {
+        if (count) atomicAdd(&S.place[key[k]], 1u);
+        const uint32_t q = at + __popc(m & lt);
+        if (q < SORT_LIST) {
+          S.key[q] = (uint16_t)key[k];
+          S.pos[q] = (uint32_t)(w0 + 32 * k);
+        }
+      }
+      at += __popc(m);
+    }
+    return sum;
+  };
+
+  // Write the list's n entries to their places.
+  auto rank_list = [&](uint32_t n) {
+    const uint32_t per = ((n + SORT_WARPS - 1) / SORT_WARPS + 31) / 32 * 32;
+    const uint32_t a = warp * per, e = a + per < n ? a + per : n;
+    for (int b = lane; b < bins; b += 32) S.before[warp][b] = 0;
+    __syncthreads();
+    for (uint32_t i = a; i < e; i += 32) {
+      const bool in = i + lane < e;
+      const uint32_t key = in ? S.key[i + lane] : 0xFFFFu;
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key);
+      if (in && (peers & lt) == 0) S.before[warp][key] += (uint16_t)__popc(peers);
+      __syncwarp();
+    }
+    __syncthreads();
+    for (int b = tid; b < bins; b += SORT_THREADS) {
+      uint32_t sum = 0;
+#pragma unroll
+      for (int w = 0; w < SORT_WARPS; ++w) {
+        const uint32_t c = S.before[w][b];
+        S.before[w][b] = (uint16_t)sum;
+        sum += c;
+      }
+    }
+    __syncthreads();
+    for (uint32_t i = a; i < e; i += 32) {
+      const bool in = i + lane < e;
+      const uint32_t key = in ? S.key[i + lane] : 0xFFFFu;
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, key);
+      const uint32_t under = __popc(peers & lt);
+      uint32_t at = 0;
+      if (in) at = S.before[warp][key] + under;
+      __syncwarp();
+      if (in && under == 0) S.before[warp][key] += (uint16_t)__popc(peers);
+      __syncwarp();
+      if (in) {
+        const uint32_t q = S.place[key] + at;
+        P.key[q] = (uint32_t)first + key;
+        P.pos[q] = S.pos[i + lane];
+      }
+    }
+    __syncthreads();
+    // The last warp's counters have grown to the list's counts.
+    for (int b = tid; b < bins; b += SORT_THREADS) S.place[b] += S.before[SORT_WARPS - 1][b];
+    __syncthreads();
+  };
+
+  uint32_t n = 0;
+  for (int64_t t0 = 0; t0 < P.tokens; t0 += SORT_TILE) n += scan_tile(t0, n, true);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xFFFFFFFFu, below, o);
+  if (lane == 0) atomicAdd(&S.below, below);
+  __syncthreads();
+  for (int b = tid; b < bins; b += SORT_THREADS) P.seen[first + b] = S.place[b] != 0;
+  if (tid == 0 && blockIdx.x + 1 == gridDim.x) *P.entries = S.below + n;
+  // Counts to first places: four neighbouring ids a thread.
+  static_assert(SORT_BINS == 4 * SORT_THREADS, "four ids a thread");
+  uint32_t c[4], sum = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    c[k] = 4 * tid + k < bins ? S.place[4 * tid + k] : 0;
+    sum += c[k];
+  }
+  uint32_t scan = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    if (lane >= o) scan += u;
+  }
+  if (lane == 31) S.warp_total[warp] = scan;
+  __syncthreads();
+  uint32_t at = S.below + scan - sum;
+#pragma unroll
+  for (int w = 0; w < SORT_WARPS; ++w)
+    if (w < warp) at += S.warp_total[w];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (4 * tid + k < bins) S.place[4 * tid + k] = at;
+    at += c[k];
+  }
+  __syncthreads();
+  if (n <= SORT_LIST) {
+    rank_list(n);
     return;
   }
-  __shared__ uint32_t count[SORT_BINS];               // this CTA's digit counts (read by the cluster)
-  __shared__ uint32_t place[SORT_BINS];               // next place of each digit
-  __shared__ uint32_t warp_count[SORT_WARPS][SORT_BINS];
-  __shared__ uint32_t scan[SORT_BINS];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)blockIdx.x;
-  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t per = (((P.tokens + SORT_CTAS - 1) / SORT_CTAS) + 31) / 32 * 32;
-  const int64_t begin = rank * per < P.tokens ? rank * per : P.tokens;
-  const int64_t end = begin + per < P.tokens ? begin + per : P.tokens;
-
-  auto read_key = [&](int pass, int64_t i) -> uint32_t {
-    if (pass > 0) return __ldcg(P.key[(pass - 1) & 1] + i);
-    const int64_t id = load_id<I64>(P.ids, i);
-    return id >= 0 && id < P.vocab ? (uint32_t)id : (uint32_t)P.vocab;
-  };
-  const uint32_t mask = (1u << P.bits) - 1;
-  for (int pass = 0; pass < P.passes; ++pass) {
-    const int shift = pass * P.bits;
-    for (int b = tid; b < SORT_BINS; b += SORT_THREADS) count[b] = 0;
-    __syncthreads();
-    for (int64_t i = begin + tid; i < end; i += SORT_THREADS)
-      atomicAdd(&count[(read_key(pass, i) >> shift) & mask], 1u);
-    cluster.sync();
-    // place[b] = entries with a smaller digit anywhere + with digit b in the CTAs before.
-    uint32_t before = 0, total = 0;
-    if (tid < SORT_BINS) {
-      for (int q = 0; q < SORT_CTAS; ++q) {
-        const uint32_t n = *cluster.map_shared_rank(&count[tid], q);
-        if (q < rank) before += n;
-        total += n;
-      }
-      scan[tid] = total;
+  uint32_t held = 0;
+  for (int64_t t0 = 0; t0 < P.tokens; t0 += SORT_TILE) {
+    uint32_t more = scan_tile(t0, held, false);
+    if (held + more > SORT_LIST) {           // the tile's entries do not fit behind the held ones:
+      __syncthreads();
+      rank_list(held);                       // rank those, and collect the tile again
+      more = scan_tile(t0, 0, false);
+      held = 0;
     }
+    held += more;
     __syncthreads();
-    for (int step = 1; step < SORT_BINS; step <<= 1) {
-      uint32_t v = 0;
-      if (tid < SORT_BINS && tid >= step) v = scan[tid - step];
-      __syncthreads();
-      if (tid < SORT_BINS) scan[tid] += v;
-      __syncthreads();
-    }
-    if (tid < SORT_BINS) place[tid] = scan[tid] - total + before;
-    __syncthreads();
-    for (int64_t t0 = begin; t0 < end; t0 += SORT_TILE) {
-      for (int b = tid; b < SORT_WARPS * SORT_BINS; b += SORT_THREADS) (&warp_count[0][0])[b] = 0;
-      __syncthreads();
-      uint32_t key[SORT_PER_LANE], p[SORT_PER_LANE], rnk[SORT_PER_LANE];
-      const int64_t w0 = t0 + (int64_t)warp * (32 * SORT_PER_LANE) + lane;
-#pragma unroll
-      for (int k = 0; k < SORT_PER_LANE; ++k) {
-        const int64_t i = w0 + 32 * k;
-        key[k] = i < end ? read_key(pass, i) : 0u;
-        p[k] = i < end ? (pass > 0 ? __ldcg(P.pos[(pass - 1) & 1] + i) : (uint32_t)i) : 0u;
-      }
-#pragma unroll
-      for (int k = 0; k < SORT_PER_LANE; ++k) {
-        const bool in = w0 + 32 * k < end;
-        const uint32_t digit = in ? (key[k] >> shift) & mask : SORT_BINS;
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, digit);
-        const uint32_t below = __popc(peers & ((1u << lane) - 1));
-        rnk[k] = 0;
-        if (in) rnk[k] = warp_count[warp][digit] + below;
-        __syncwarp();
-        if (in && below == 0) warp_count[warp][digit] += __popc(peers);
-        __syncwarp();
-      }
-      __syncthreads();
-      // The warps' counts of each digit become their first places.
-      if (tid < SORT_BINS) {
-        uint32_t at = place[tid];
-        for (int w = 0; w < SORT_WARPS; ++w) {
-          const uint32_t n = warp_count[w][tid];
-          warp_count[w][tid] = at;
-          at += n;
-        }
-        place[tid] = at;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < SORT_PER_LANE; ++k) {
-        if (w0 + 32 * k < end) {
-          const uint32_t at = warp_count[warp][(key[k] >> shift) & mask] + rnk[k];
-          __stcg(P.key[pass & 1] + at, key[k]);
-          __stcg(P.pos[pass & 1] + at, p[k]);
-        }
-      }
-      __syncthreads();
-    }
-    __threadfence();
-    cluster.sync();
   }
+  rank_list(held);
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void write_row(const EmbedGradParams& P, const SliceCols<VEC>& sc, uint32_t id, const float* sum) {
-  float o[8];
+template <int DT, bool VEC, int NC>
+__device__ __forceinline__ void write_row(const EmbedGradParams& P, const Columns<VEC, NC>& cols, uint32_t id, const f2* sum) {
+  float o[NC];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) o[k] = __fmul_rn(sum[k], P.scale);
+  for (int k = 0; k < NC / 2; ++k) {
+    const f2 v = f2_mul(sum[k], f2_splat(P.scale));
+    o[2 * k] = v.x, o[2 * k + 1] = v.y;
+  }
   const int64_t row = (int64_t)id * P.ldd;
   if (P.accumulate) {
-    float old[8];
-    sc.template load<DT>(P.d, row, old);
+    Piece<DT, VEC, NC> old;
+    cols.load(P.d, row, old);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = __fadd_rn(old[k], o[k]);
+    for (int k = 0; k < NC; ++k) o[k] = __fadd_rn(old.get(k), o[k]);
   }
-  sc.template store<DT>(P.d, row, o);
+  cols.template store<DT>(P.d, row, o);
 }
 
-// One run and one slice of 256 columns a warp.
-template <int CT, int DT, bool VEC>
+// A span of zeros: the columns of a row, by one warp.
+template <int DT, bool VEC>
+__device__ __forceinline__ void zero_row(const EmbedGradParams& P, int64_t row, int lane) {
+  const float z[8] = {};
+  for (int64_t c = 0; c < P.cols; c += 256) Columns<VEC, 8>(c, 32, lane, P.cols).template store<DT>(P.d, row * P.ldd, z);
+}
+
+// The first run_ctas CTAs: one run and one slice of 32 NC columns a warp.  The
+// others zero the rows of ids that do not occur.
+template <int CT, int DT, bool VEC, int NC>
 __global__ void __launch_bounds__(EMB_THREADS) embed_runs_kernel(const __grid_constant__ EmbedGradParams P) {
-  const int64_t w = ((int64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x >= P.run_ctas) {
+    const int64_t warps = (int64_t)(gridDim.x - P.run_ctas) * (EMB_THREADS / 32);
+    for (int64_t v = ((int64_t)(blockIdx.x - P.run_ctas) * EMB_THREADS + threadIdx.x) >> 5; v < P.vocab; v += warps)
+      if (!P.seen[v]) zero_row<DT, VEC>(P, v, lane);
+    return;
+  }
+  const int64_t w = ((int64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5;
   const int64_t run = w / P.slices;
   const int64_t i0 = run * EMB_RUN;
-  if (i0 >= P.tokens) return;
-  const SliceCols<VEC> sc((int)(w - run * P.slices), lane, P.cols);
-  const uint32_t* key = P.key[P.out];
-  const uint32_t none = (uint32_t)P.vocab;
-  const int n = P.tokens - i0 < EMB_RUN ? (int)(P.tokens - i0) : EMB_RUN;
-  const uint32_t my_key = lane < n ? key[i0 + lane] : none;
-  const uint32_t my_pos = lane < n ? P.pos[P.out][i0 + lane] : 0;
+  const int64_t entries = *P.entries;
+  if (i0 >= entries) return;
+  const Columns<VEC, NC> cols((w - run * P.slices) * (32 * NC), 32, lane, P.cols);
+  const int n = entries - i0 < EMB_RUN ? (int)(entries - i0) : EMB_RUN;
+  const uint32_t my_key = lane < n ? P.key[i0 + lane] : 0xFFFFFFFFu;
+  const uint32_t my_pos = lane < n ? P.pos[i0 + lane] : 0;
+  const uint32_t after = i0 + n < entries ? P.key[i0 + n] : 0xFFFFFFFFu;
+  const uint32_t prior = i0 > 0 ? P.key[i0 - 1] : 0xFFFFFFFFu;
   const uint32_t next_key = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
-  const uint32_t after = i0 + n < P.tokens ? key[i0 + n] : none;
-  const bool first_continues = i0 > 0 && key[i0 - 1] == __shfl_sync(0xFFFFFFFFu, my_key, 0);
-  const int valid = __popc(__ballot_sync(0xFFFFFFFFu, my_key != none));   // ids come before the positions without one
   // Entries after which the sum ends: the id's last of this run.
-  const uint32_t ends = __ballot_sync(0xFFFFFFFFu, lane < valid && (lane == valid - 1 || next_key != my_key));
-  float acc[8] = {};
-  bool head = first_continues;
-  constexpr int GROUP = 8;
-  for (int e0 = 0; e0 < valid; e0 += GROUP) {
-    float v[GROUP][8];
+  const uint32_t ends = __ballot_sync(0xFFFFFFFFu, lane < n && (lane == n - 1 || next_key != my_key));
+  bool head = prior == __shfl_sync(0xFFFFFFFFu, my_key, 0);
+  f2 acc[NC / 2];
+#pragma unroll
+  for (int k = 0; k < NC / 2; ++k) acc[k] = f2{0.0f, 0.0f};
+  // Rows in flight: 32 registers' worth (a whole load of 16 bytes each where VEC).
+  constexpr int GROUP = 64 / Piece<CT, VEC, NC>::W < 16 ? 64 / Piece<CT, VEC, NC>::W : 16;
+  for (int e0 = 0; e0 < n; e0 += GROUP) {
+    Piece<CT, VEC, NC> v[GROUP];
 #pragma unroll
     for (int j = 0; j < GROUP; ++j) {
       const uint32_t p = __shfl_sync(0xFFFFFFFFu, my_pos, (e0 + j) & 31);
-      if (e0 + j < valid) sc.template load<CT>(P.ct, (int64_t)p * P.ldc, v[j]);
+      if (e0 + j < n) cols.load(P.ct, (int64_t)p * P.ldc, v[j]);
     }
 #pragma unroll
     for (int j = 0; j < GROUP; ++j) {
       const int e = e0 + j;
-      if (e < valid) {
+      if (e < n) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = __fadd_rn(acc[k], v[j][k]);
+        for (int k = 0; k < NC / 2; ++k) acc[k] = f2_add(acc[k], f2{v[j].get(2 * k), v[j].get(2 * k + 1)});
         if ((ends >> e) & 1) {
           const uint32_t id = __shfl_sync(0xFFFFFFFFu, my_key, e);
-          const bool goes_on = e == n - 1 && after == id;
-          if (head) {
-            sc.template store<PSK_F32>(P.head, run * P.pcols, acc);
-          } else if (goes_on) {
-            sc.template store<PSK_F32>(P.tail, run * P.pcols, acc);
+          if (head || (e == n - 1 && after == id)) {
+            float o[NC];
+#pragma unroll
+            for (int k = 0; k < NC; ++k) o[k] = k & 1 ? acc[k / 2].y : acc[k / 2].x;
+            cols.template store<PSK_F32>(head ? P.head : P.tail, run * P.pcols, o);
           } else {
-            write_row<DT, VEC>(P, sc, id, acc);
+            write_row<DT, VEC, NC>(P, cols, id, acc);
           }
           head = false;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+          for (int k = 0; k < NC / 2; ++k) acc[k] = f2{0.0f, 0.0f};
         }
       }
     }
@@ -279,53 +358,94 @@ __global__ void __launch_bounds__(EMB_THREADS) embed_runs_kernel(const __grid_co
 
 // Join the run sums of each id whose entries span several runs: the warps of
 // the run it begins in.
-template <int DT, bool VEC>
+template <int DT, bool VEC, int NC>
 __global__ void __launch_bounds__(EMB_THREADS) embed_join_kernel(const __grid_constant__ EmbedGradParams P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t w = ((int64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const int64_t run = w / P.slices;
   const int64_t i0 = run * EMB_RUN, i1 = i0 + EMB_RUN;
-  if (i1 >= P.tokens) return;                       // the last run goes on nowhere
-  const uint32_t* key = P.key[P.out];
-  const uint32_t id = key[i1 - 1];
-  if (id == (uint32_t)P.vocab || key[i1] != id) return;
-  if (key[i0] == id && i0 > 0 && key[i0 - 1] == id) return;   // begun in an earlier run
-  // The first entry past the id's own (entries are sorted).
-  int64_t lo = i1, hi = P.tokens;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (key[mid] > id) hi = mid;
-    else lo = mid + 1;
+  const int64_t entries = *P.entries;
+  if (i1 >= entries) return;                        // the last run goes on nowhere
+  const uint32_t id = P.key[i1 - 1], begin = P.key[i0], prior = i0 > 0 ? P.key[i0 - 1] : 0xFFFFFFFFu;
+  if (P.key[i1] != id || (begin == id && prior == id)) return;   // ends here, or begun in an earlier run
+  // Its last run: 32 run beginnings at a time.
+  int64_t last = run + 1;
+  for (;;) {
+    const int64_t q = last + 1 + lane;
+    const bool goes_on = q * EMB_RUN < entries && P.key[q * EMB_RUN] == id;
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, goes_on);
+    if (m != 0xFFFFFFFFu) {
+      last += __ffs(~m) - 1;
+      break;
+    }
+    last += 32;
   }
-  const int64_t last = (lo - 1) / EMB_RUN;
-  const SliceCols<VEC> sc((int)(w - run * P.slices), lane, P.cols);
-  float acc[8];
-  sc.template load<PSK_F32>(P.tail, run * P.pcols, acc);
-  constexpr int GROUP = 8;
+  const Columns<VEC, NC> cols((w - run * P.slices) * (32 * NC), 32, lane, P.cols);
+  f2 acc[NC / 2];
+  Piece<PSK_F32, VEC, NC> t;
+  cols.load(P.tail, run * P.pcols, t);
+#pragma unroll
+  for (int k = 0; k < NC / 2; ++k) acc[k] = f2{t.get(2 * k), t.get(2 * k + 1)};
+  constexpr int GROUP = 64 / NC;
   for (int64_t r = run + 1; r <= last; r += GROUP) {
-    float v[GROUP][8];
+    Piece<PSK_F32, VEC, NC> v[GROUP];
 #pragma unroll
     for (int j = 0; j < GROUP; ++j)
-      if (r + j <= last) sc.template load<PSK_F32>(P.head, (r + j) * P.pcols, v[j]);
+      if (r + j <= last) cols.load(P.head, (r + j) * P.pcols, v[j]);
 #pragma unroll
     for (int j = 0; j < GROUP; ++j)
       if (r + j <= last) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = __fadd_rn(acc[k], v[j][k]);
+        for (int k = 0; k < NC / 2; ++k) acc[k] = f2_add(acc[k], f2{v[j].get(2 * k), v[j].get(2 * k + 1)});
       }
   }
-  write_row<DT, VEC>(P, sc, id, acc);
+  write_row<DT, VEC, NC>(P, cols, id, acc);
+}
+
+// The gradient of no tokens.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(EMB_THREADS) embed_zero_kernel(const __grid_constant__ EmbedGradParams P) {
+  const int64_t warps = (int64_t)gridDim.x * (EMB_THREADS / 32);
+  for (int64_t v = ((int64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5; v < P.vocab; v += warps)
+    zero_row<DT, VEC>(P, v, threadIdx.x & 31);
+}
+
+// Launch a kernel whose set-up may overlap the one before it (it waits for
+// that one's results itself).
+template <typename K>
+static void launch_after(K kernel, unsigned grid, int threads, cudaStream_t s, const EmbedGradParams& P) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, P);
 }
 
 static uint64_t align256(uint64_t n) { return (n + 255) / 256 * 256; }
 
-// Workspace layout: key and pos buffers, then the head and tail run sums.
-static uint64_t embed_ws_layout(int64_t tokens, int64_t cols, uint64_t* list, uint64_t* part) {
+// Workspace layout: the sorted list, what occurs, the list's length, the head
+// and tail run sums.
+struct EmbedWorkspace {
+  uint64_t key, pos, seen, entries, head, tail, bytes;
+};
+static EmbedWorkspace embed_ws_layout(int64_t tokens, int64_t vocab, int64_t cols) {
   const uint64_t runs = (uint64_t)(tokens + EMB_RUN - 1) / EMB_RUN;
   const uint64_t pcols = (uint64_t)(cols + 7) / 8 * 8;
-  *list = align256((uint64_t)tokens * 4);
-  *part = align256(runs * pcols * 4);
-  return 4 * *list + 2 * *part;
+  EmbedWorkspace w;
+  w.key = 0;
+  w.pos = align256((uint64_t)tokens * 4);
+  w.seen = 2 * w.pos;
+  w.entries = w.seen + align256((uint64_t)vocab);
+  w.head = w.entries + 256;
+  w.tail = w.head + align256(runs * pcols * 4);
+  w.bytes = w.tail + align256(runs * pcols * 4);
+  return w;
 }
 
 static int embed_check_sizes(int64_t tokens, int64_t vocab, int64_t cols) {
@@ -366,19 +486,24 @@ extern "C" int psk_embed(const void* ids, int32_t idt, int64_t tokens, const voi
     return fail(PSK_E_ALIAS, "y overlaps the table");
   if (ranges_overlap(ids, (uint64_t)tokens * isz, y, yb)) return fail(PSK_E_ALIAS, "y overlaps the ids");
   EmbedParams P{ids, table, y, vocab, cols, ldt, ldy, 0, 0, FastDiv((uint32_t)((cols + 7) / 8)), (float)scale};
-  const bool vec = rows_vec8(table, tt, ldt, vocab) && rows_vec8(y, yt, ldy, tokens);
+  const bool vec = cols % 8 == 0 && rows_vec8(table, tt, ldt, vocab) && rows_vec8(y, yt, ldy, tokens);
   const uint64_t slice = 0xFFFFFFFFull / P.per_row.d;
   cudaStream_t s = (cudaStream_t)stream;
   for (uint64_t r0 = 0; r0 < (uint64_t)tokens; r0 += slice) {
     const uint64_t nr = (uint64_t)tokens - r0 < slice ? (uint64_t)tokens - r0 : slice;
     P.row0 = (int64_t)r0;
     P.items = (uint32_t)(nr * P.per_row.d);
-    const unsigned grid = (unsigned)(((uint64_t)P.items + EMB_THREADS - 1) / EMB_THREADS);
+    // Four rows a thread where that still leaves every SM full (16384 rows of
+    // 2048 bf16: see the kernel's figures); one where latency counts.
+    const bool four = (uint64_t)P.items >= 4ull * 2048 * (uint64_t)device_sm_count();
+    const uint64_t per_cta = (uint64_t)EMB_THREADS * (four ? 4 : 1);
+    const unsigned grid = (unsigned)(((uint64_t)P.items + per_cta - 1) / per_cta);
     with_dtype(tt, [&](auto TT) {
       return with_dtype(yt, [&](auto YT) {
         return with_bool(idt == PSK_I64, [&](auto I64) {
           return with_bool(vec, [&](auto VEC) {
-            embed_kernel<TT.value, YT.value, I64.value, VEC.value><<<grid, EMB_THREADS, 0, s>>>(P);
+            if (four) embed_kernel<TT.value, YT.value, I64.value, VEC.value, 4><<<grid, EMB_THREADS, 0, s>>>(P);
+            else embed_kernel<TT.value, YT.value, I64.value, VEC.value, 1><<<grid, EMB_THREADS, 0, s>>>(P);
             return 0;
           });
         });
@@ -395,8 +520,7 @@ extern "C" int psk_embed_workspace(int64_t tokens, int64_t vocab, int64_t cols, 
   if (!bytes) return fail(PSK_E_NULL, "bytes is NULL");
   const int rc = embed_check_sizes(tokens, vocab, cols);
   if (rc) return rc;
-  uint64_t list, part;
-  *bytes = tokens && vocab && cols ? embed_ws_layout(tokens, cols, &list, &part) : 0;
+  *bytes = tokens && vocab && cols ? embed_ws_layout(tokens, vocab, cols).bytes : 0;
   return PSK_OK;
 }
 
@@ -418,12 +542,13 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
   if (!rows_addressable(tokens, ldc) || !rows_addressable(vocab, ldd))
     return fail(PSK_E_SHAPE, "rows x leading dimension too large");
   EmbedGradParams P{};
-  uint64_t list = 0, part = 0;
+  EmbedWorkspace at{};
   const uint64_t db = rows_bytes(vocab, cols, ldd, dt);
   if (tokens > 0) {
     const uint64_t isz = idt == PSK_I64 ? 8 : 4;
     if ((uintptr_t)ids % isz != 0) return fail(PSK_E_ARG, "ids are not aligned to their type");
-    const uint64_t need = embed_ws_layout(tokens, cols, &list, &part);
+    at = embed_ws_layout(tokens, vocab, cols);
+    const uint64_t need = at.bytes;
     if (!workspace) return fail(PSK_E_NULL, "workspace is NULL");
     if ((uintptr_t)workspace % 16 != 0) return fail(PSK_E_ARG, "workspace is not 16-byte aligned");
     if (workspace_bytes < need)
@@ -439,55 +564,65 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
   }
   P.ids = ids, P.ct = ct, P.d = dtable;
   P.vocab = vocab, P.cols = cols, P.ldc = ldc, P.ldd = ldd, P.tokens = tokens;
-  char* w = (char*)workspace;
-  for (int k = 0; k < 2; ++k) {
-    P.key[k] = (uint32_t*)(w + (uint64_t)k * list);
-    P.pos[k] = (uint32_t*)(w + (uint64_t)(2 + k) * list);
-  }
-  P.head = (float*)(w + 4 * list);
-  P.tail = (float*)(w + 4 * list + part);
   P.pcols = (cols + 7) / 8 * 8;
-  int bits = 0;                                     // bits of the largest key, vocab
-  while (bits < 32 && ((uint64_t)vocab >> bits) != 0) ++bits;
-  P.passes = (bits + SORT_BITS - 1) / SORT_BITS;
-  P.bits = (bits + P.passes - 1) / P.passes;
-  P.out = (P.passes - 1) & 1;
   P.accumulate = accumulate != 0;
-  P.slices = (int32_t)((cols + 255) / 256);
   P.scale = (float)scale;
-  const int64_t runs = (tokens + EMB_RUN - 1) / EMB_RUN;
-  const uint64_t ctas = ((uint64_t)runs * P.slices + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32);
-  if (ctas > 0x7FFFFFFFull) return fail(PSK_E_SHAPE, "tokens x cols too large");
-  const bool vec = (tokens == 0 || rows_vec8(ct, ct_t, ldc, tokens)) && rows_vec8(dtable, dt, ldd, vocab);
+  const bool vec = cols % 8 == 0 && (tokens == 0 || rows_vec8(ct, ct_t, ldc, tokens)) && rows_vec8(dtable, dt, ldd, vocab);
   cudaStream_t s = (cudaStream_t)stream;
-  const int64_t zero_groups = accumulate ? 0 : vocab * ((cols + 7) / 8);
-  int64_t zero_ctas = (zero_groups + SORT_THREADS * 4 - 1) / (SORT_THREADS * 4);
-  const int64_t most = (int64_t)device_sm_count() * 4;
-  if (zero_ctas > most) zero_ctas = most;
-  const unsigned grid = (unsigned)((zero_ctas + SORT_CTAS - 1) / SORT_CTAS + 1) * SORT_CTAS;
-  with_dtype(dt, [&](auto DT) {
-    return with_bool(idt == PSK_I64, [&](auto I64) {
+  const int sms = device_sm_count();
+  // Zeroing CTAs: two an SM beside the run sums, a row a warp at least.
+  int64_t zero_ctas = accumulate ? 0 : (vocab + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32);
+  if (zero_ctas > 2 * sms) zero_ctas = 2 * sms;
+  if (tokens == 0) {
+    with_dtype(dt, [&](auto DT) {
       return with_bool(vec, [&](auto VEC) {
-        embed_sort_kernel<I64.value, DT.value, VEC.value><<<grid, SORT_THREADS, 0, s>>>(P);
+        embed_zero_kernel<DT.value, VEC.value><<<(unsigned)zero_ctas * 4, EMB_THREADS, 0, s>>>(P);
         return 0;
       });
     });
-  });
+    return check_launch("embedding gradient kernel");
+  }
+  char* w = (char*)workspace;
+  P.key = (uint32_t*)(w + at.key), P.pos = (uint32_t*)(w + at.pos);
+  P.seen = (uint8_t*)(w + at.seen), P.entries = (uint32_t*)(w + at.entries);
+  P.head = (float*)(w + at.head), P.tail = (float*)(w + at.tail);
+  // A sorting CTA an SM, or more where a slice would pass SORT_BINS ids.
+  int64_t slice = (vocab + sms - 1) / sms;
+  if (slice > SORT_BINS) slice = SORT_BINS;
+  P.slice_ids = (int32_t)slice;
+  const unsigned sort_ctas = (unsigned)((vocab + slice - 1) / slice);
+  // Eight columns a lane, or four where eight leave fewer than 16 warps an SM
+  // (latency then counts more than the instructions for each row).
+  const int64_t runs = (tokens + EMB_RUN - 1) / EMB_RUN;
+  const bool wide = runs * ((cols + 255) / 256) >= 16 * sms;
+  P.slices = (int32_t)((cols + (wide ? 255 : 127)) / (wide ? 256 : 128));
+  const uint64_t ctas = ((uint64_t)runs * P.slices + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32);
+  if (ctas + 2 * sms > 0x7FFFFFFFull) return fail(PSK_E_SHAPE, "tokens x cols too large");
+  P.run_ctas = (int32_t)ctas;
+  static bool limit[2][PSK_MAX_DEVICES] = {};
+  const bool i64 = idt == PSK_I64;
+  smem_limit_once(i64 ? (const void*)embed_sort_kernel<true> : (const void*)embed_sort_kernel<false>,
+                  (int)sizeof(SortShared), limit[i64]);
+  if (i64) embed_sort_kernel<true><<<sort_ctas, SORT_THREADS, sizeof(SortShared), s>>>(P);
+  else embed_sort_kernel<false><<<sort_ctas, SORT_THREADS, sizeof(SortShared), s>>>(P);
   rc = check_launch("embedding sort kernel");
-  if (rc || tokens == 0) return rc;
+  if (rc) return rc;
   with_dtype(ct_t, [&](auto CT) {
     return with_dtype(dt, [&](auto DT) {
       return with_bool(vec, [&](auto VEC) {
-        embed_runs_kernel<CT.value, DT.value, VEC.value><<<(unsigned)ctas, EMB_THREADS, 0, s>>>(P);
+        const unsigned grid = (unsigned)(ctas + zero_ctas);
+        if (wide) launch_after(embed_runs_kernel<CT.value, DT.value, VEC.value, 8>, grid, EMB_THREADS, s, P);
+        else launch_after(embed_runs_kernel<CT.value, DT.value, VEC.value, 4>, grid, EMB_THREADS, s, P);
         return 0;
       });
     });
   });
   rc = check_launch("embedding run sums kernel");
-  if (rc) return rc;
+  if (rc || runs == 1) return rc;
   with_dtype(dt, [&](auto DT) {
     return with_bool(vec, [&](auto VEC) {
-      embed_join_kernel<DT.value, VEC.value><<<(unsigned)ctas, EMB_THREADS, 0, s>>>(P);
+      if (wide) launch_after(embed_join_kernel<DT.value, VEC.value, 8>, (unsigned)ctas, EMB_THREADS, s, P);
+      else launch_after(embed_join_kernel<DT.value, VEC.value, 4>, (unsigned)ctas, EMB_THREADS, s, P);
       return 0;
     });
   });

@@ -4,6 +4,7 @@
 //   dgamma = sum over rows of ct * xh,   dbeta = sum over rows of ct.
 // Sums are held in f32 over trees fixed by the sizes: no atomics.
 #include "vec8.cuh"
+#include "pair.cuh"
 
 namespace psk {
 
@@ -105,13 +106,16 @@ template <int XT, int CT, int DT, int KIND, bool VEC>
 __global__ void __launch_bounds__(NB_THREADS) norm_bwd_apply_kernel(const __grid_constant__ NormBwdParams P) {
   __shared__ float sums[2][NB_WARPS][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const SliceCols<VEC> sc((int)blockIdx.x, lane, P.cols);
+  const Columns<VEC, 8> sc((int64_t)blockIdx.x * 256, 32, lane, P.cols);
   float gamma[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) gamma[k] = 1.0f;
   if (P.gamma) {
-    if (P.param_dtype == PSK_BF16) sc.template load<PSK_BF16>(P.gamma, 0, gamma);
-    else sc.template load<PSK_F32>(P.gamma, 0, gamma);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (sc.has(k))
+        gamma[k] = P.param_dtype == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)P.gamma)[sc.col(k)])
+                                             : ((const float*)P.gamma)[sc.col(k)];
   }
   float dg[8] = {}, db[8] = {};
   const int64_t per = (P.rows + P.blocks - 1) / P.blocks;
@@ -119,11 +123,14 @@ __global__ void __launch_bounds__(NB_THREADS) norm_bwd_apply_kernel(const __grid
   const int64_t r1 = r0 + per < P.rows ? r0 + per : P.rows;
   for (int64_t r = r0 + warp; r < r1; r += NB_WARPS) {
     const float4 st = P.stats[r];
+    Piece<XT, VEC, 8> xp;
+    Piece<CT, VEC, 8> cp;
+    sc.load(P.x, r * P.ldx, xp);
+    sc.load(P.ct, r * P.ldc, cp);
     float x[8], c[8];
-    sc.template load<XT>(P.x, r * P.ldx, x);
-    sc.template load<CT>(P.ct, r * P.ldc, c);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
+      x[k] = xp.get(k), c[k] = cp.get(k);
       const float xh = (x[k] - st.x) * st.y;
       const float g = c[k] * gamma[k];
       float t = KIND == PSK_NORM_LAYER ? g - st.z : g;
@@ -165,61 +172,6 @@ __global__ void __launch_bounds__(NB_THREADS) norm_bwd_apply_kernel(const __grid
 constexpr int NB_FUSED_COLS = 8192;
 constexpr int NB_ROWS_PER_TEAM = 4;        // at least, where there are as many
 
-// Eight of a thread's columns as loaded.
-template <int TY, bool VEC>
-struct Octet {
-  static constexpr int W = VEC && TY == PSK_BF16 ? 4 : 8;
-  uint32_t w[W];
-  __device__ __forceinline__ float get(int k) const {
-    if constexpr (VEC && TY == PSK_BF16) return __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
-    else return __uint_as_float(w[k]);
-  }
-};
-
-// The columns of thread t: group j is columns (j T + t) 8 + k with 16-byte
-// accesses, else j 8 T + k T + t (a warp's accesses then coalesce).
-template <int TY, bool VEC>
-struct TeamCols {
-  int T, t, cols;
-  __device__ __forceinline__ int col(int j, int k) const { return VEC ? (j * T + t) * 8 + k : (j * 8 + k) * T + t; }
-  __device__ __forceinline__ bool has(int j, int k) const { return col(j, VEC ? 0 : k) < cols; }
-  __device__ __forceinline__ void load(const void* p, int64_t row, int j, Octet<TY, VEC>& o) const {
-    if constexpr (VEC) {
-      const bool in = has(j, 0);
-      if constexpr (TY == PSK_BF16) {
-        const uint4 u = in ? __ldcs((const uint4*)((const uint16_t*)p + row + col(j, 0))) : make_uint4(0, 0, 0, 0);
-        o.w[0] = u.x, o.w[1] = u.y, o.w[2] = u.z, o.w[3] = u.w;
-      } else {
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        const uint4* q = (const uint4*)((const float*)p + row + col(j, 0));
-        const uint4 a = in ? __ldcs(q) : z, b = in ? __ldcs(q + 1) : z;
-        o.w[0] = a.x, o.w[1] = a.y, o.w[2] = a.z, o.w[3] = a.w, o.w[4] = b.x, o.w[5] = b.y, o.w[6] = b.z, o.w[7] = b.w;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        o.w[k] = 0;
-        if (has(j, k)) {
-          if constexpr (TY == PSK_BF16) o.w[k] = (uint32_t)((const uint16_t*)p)[row + col(j, k)] << 16;
-          else o.w[k] = ((const uint32_t*)p)[row + col(j, k)];
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ void store(void* p, int64_t row, int j, const float* v) const {
-    if constexpr (VEC) {
-      if (has(j, 0)) store8<TY, true>(p, row + col(j, 0), 8, v);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (has(j, k)) {
-          if constexpr (TY == PSK_BF16) ((uint16_t*)p)[row + col(j, k)] = f32_to_bf16_bits(v[k]);
-          else ((float*)p)[row + col(j, k)] = v[k];
-        }
-    }
-  }
-};
-
 struct NormFusedParams {
   NormBwdParams B;
   int32_t team, teams;       // threads of a team, teams of a CTA
@@ -227,109 +179,133 @@ struct NormFusedParams {
 
 template <int TY, int KIND, bool VEC, int NV, int CTA>
 __global__ void __launch_bounds__(CTA, 512 / CTA) norm_bwd_fused_kernel(const __grid_constant__ NormFusedParams Q) {
-  extern __shared__ float colsum[];                       // [cols] of the CTA, added team by team
+  // gamma in f32, laid out as the threads read it; then the CTA's column sums.
+  extern __shared__ __align__(16) float smem[];
   __shared__ float2 red[2][CTA / 32];
   const NormBwdParams& P = Q.B;
+  constexpr bool LAYER = KIND == PSK_NORM_LAYER;
   const int T = Q.team, team = threadIdx.x / T, t = threadIdx.x - team * T, nw = T / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const TeamCols<TY, VEC> tc{T, t, (int)P.cols};
   const int64_t step = (int64_t)gridDim.x * Q.teams;
+  auto group = [&](int j) { return Columns<VEC, 8>((int64_t)j * T * 8, T, t, P.cols); };
   int flip = 0;
   // Sum two values over the team; one barrier (the buffers alternate).
-  auto team_sum = [&](float a, float b) {
+  auto team_sum = [&](f2 a, f2 b) {
+    float s = a.x + a.y, u = b.x + b.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-      b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+      s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
     }
-    if (nw == 1) return make_float2(a, b);
+    if (nw == 1) return make_float2(s, u);
     flip ^= 1;
-    if (lane == 0) red[flip][warp] = make_float2(a, b);
+    if (lane == 0) red[flip][warp] = make_float2(s, u);
     asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(T) : "memory");
-    float2 s = red[flip][team * nw];
+    float2 v = red[flip][team * nw];
     for (int w = 1; w < nw; ++w) {
-      const float2 u = red[flip][team * nw + w];
-      s.x += u.x, s.y += u.y;
+      const float2 q = red[flip][team * nw + w];
+      v.x += q.x, v.y += q.y;
     }
-    return s;
+    return v;
   };
 
-  float gamma[NV][8], dg[NV][8], db[KIND == PSK_NORM_LAYER ? NV : 1][8];
+  // gamma of group j, columns k..k+3: float4 number (2 j + k / 4) T + t.
+  for (int i = threadIdx.x; i < NV * 8 * T; i += CTA) {
+    const int at = i >> 2, who = at % T, piece = at / T, k = (piece & 1) * 4 + (i & 3);
+    const int64_t c = Columns<VEC, 8>((int64_t)(piece >> 1) * T * 8, T, who, P.cols).col(k);
+    float g = 1.0f;
+    if (P.gamma && c < P.cols)
+      g = P.param_dtype == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)P.gamma)[c]) : ((const float*)P.gamma)[c];
+    smem[i] = g;
+  }
+  __syncthreads();
+  const float4* gamma = (const float4*)smem;
+
+  f2 dg[NV][4], db[LAYER ? NV : 1][4];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = tc.col(j, k);
-      gamma[j][k] = 1.0f;
-      if (P.gamma && c < P.cols)
-        gamma[j][k] = P.param_dtype == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)P.gamma)[c])
-                                                : ((const float*)P.gamma)[c];
-      dg[j][k] = 0.0f;
-      if (KIND == PSK_NORM_LAYER) db[j][k] = 0.0f;
+    for (int k = 0; k < 4; ++k) {
+      dg[j][k] = f2{0.0f, 0.0f};
+      if (LAYER) db[j][k] = f2{0.0f, 0.0f};
     }
-
   int64_t r = (int64_t)blockIdx.x * Q.teams + team;
-  Octet<TY, VEC> x[NV], c[NV];
-  if (r < P.rows) {
+  Piece<TY, VEC, 8> x[NV], c[NV];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) tc.load(P.x, r * P.ldx, j, x[j]), tc.load(P.ct, r * P.ldc, j, c[j]);
-  }
+    for (int j = 0; j < NV; ++j) group(j).load(P.x, row * P.ldx, x[j]), group(j).load(P.ct, row * P.ldc, c[j]);
+  };
+  if (r < P.rows) fetch(r);
   for (; r < P.rows; r += step) {
-    float xv[NV][8], cv[NV][8];
+    f2 xv[NV][4], cv[NV][4];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) xv[j][k] = x[j].get(k), cv[j][k] = c[j].get(k);
-    if (r + step < P.rows) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        tc.load(P.x, (r + step) * P.ldx, j, x[j]), tc.load(P.ct, (r + step) * P.ldc, j, c[j]);
-    }
+      for (int k = 0; k < 4; ++k) {
+        xv[j][k] = f2{x[j].get(2 * k), x[j].get(2 * k + 1)};
+        cv[j][k] = f2{c[j].get(2 * k), c[j].get(2 * k + 1)};
+      }
+    if (r + step < P.rows) fetch(r + step);
+    auto gated = [&](int j, f2* g) {       // ct gamma
+      const float4 a = gamma[(2 * j) * T + t], b = gamma[(2 * j + 1) * T + t];
+      g[0] = f2_mul(cv[j][0], f2{a.x, a.y}), g[1] = f2_mul(cv[j][1], f2{a.z, a.w});
+      g[2] = f2_mul(cv[j][2], f2{b.x, b.y}), g[3] = f2_mul(cv[j][3], f2{b.z, b.w});
+    };
     float mg = 0.0f;
-    if (KIND == PSK_NORM_LAYER) {
-      float s = 0.0f, u = 0.0f;
+    if (LAYER) {
+      f2 s{0.0f, 0.0f}, u{0.0f, 0.0f};
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        f2 g[4];
+        gated(j, g);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s += xv[j][k], u = fmaf(cv[j][k], gamma[j][k], u);
+        for (int k = 0; k < 4; ++k) s = f2_add(s, xv[j][k]), u = f2_add(u, g[k]);
+      }
       const float2 v = team_sum(s, u);
-      const float mu = v.x * P.inv_cols;
+      const f2 mu = f2_splat(-v.x * P.inv_cols);
       mg = v.y * P.inv_cols;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) xv[j][k] = tc.has(j, k) ? xv[j][k] - mu : 0.0f;
+        for (int k = 0; k < 4; ++k) {
+          xv[j][k] = f2_add(xv[j][k], mu);
+          if (!group(j).has(2 * k)) xv[j][k].x = 0.0f;
+          if (!group(j).has(2 * k + 1)) xv[j][k].y = 0.0f;
+        }
     }
-    float s = 0.0f, u = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        s = fmaf(xv[j][k], xv[j][k], s);
-        u = fmaf(xv[j][k], cv[j][k] * gamma[j][k], u);
-      }
-    const float2 v = team_sum(s, u);
-    const float rd = 1.0f / sqrtf(v.x * P.inv_cols + P.eps);
-    const float m2 = v.y * rd * P.inv_cols;
+    f2 s{0.0f, 0.0f}, u{0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      f2 g[4];
+      gated(j, g);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s = f2_fma(xv[j][k], xv[j][k], s), u = f2_fma(xv[j][k], g[k], u);
+    }
+    const float2 v = team_sum(s, u);
+    const float rd = 1.0f / sqrtf(v.x * P.inv_cols + P.eps);
+    const f2 rd2 = f2_splat(rd), m2 = f2_splat(-(v.y * rd * P.inv_cols)), nmg = f2_splat(-mg);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      f2 g[4];
+      gated(j, g);
       float o[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float xh = xv[j][k] * rd;
-        const float g = cv[j][k] * gamma[j][k];
-        o[k] = fmaf(-xh, m2, KIND == PSK_NORM_LAYER ? g - mg : g) * rd;
-        dg[j][k] = fmaf(cv[j][k], xh, dg[j][k]);
-        if (KIND == PSK_NORM_LAYER) db[j][k] += cv[j][k];
+      for (int k = 0; k < 4; ++k) {
+        const f2 xh = f2_mul(xv[j][k], rd2);
+        dg[j][k] = f2_fma(cv[j][k], xh, dg[j][k]);
+        if (LAYER) db[j][k] = f2_add(db[j][k], cv[j][k]);
+        const f2 y = f2_mul(f2_fma(xh, m2, LAYER ? f2_add(g[k], nmg) : g[k]), rd2);
+        o[2 * k] = y.x, o[2 * k + 1] = y.y;
       }
-      tc.store(P.dx, r * P.ldd, j, o);
+      group(j).template store<TY>(P.dx, r * P.ldd, o);
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!P.dgamma && !P.dbeta) return;
   // The CTA's column sums: its teams' in turn, through shared memory.
+  float* colsum = smem + NV * 8 * T;
 #pragma unroll
-  for (int which = 0; which < (KIND == PSK_NORM_LAYER ? 2 : 1); ++which) {
+  for (int which = 0; which < (LAYER ? 2 : 1); ++which) {
     float* part = P.part + ((int64_t)which * P.blocks + blockIdx.x) * P.pcols;
     for (int q = 0; q < Q.teams; ++q) {
       if (q > 0) __syncthreads();
@@ -338,13 +314,13 @@ __global__ void __launch_bounds__(CTA, 512 / CTA) norm_bwd_fused_kernel(const __
         for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int col = tc.col(j, k);
-            if (col < P.cols) {
-              float a = which == 0 ? dg[j][k] : db[KIND == PSK_NORM_LAYER ? j : 0][k];
-              if (q > 0) a += colsum[col];
-              if (q + 1 == Q.teams) part[col] = a;
-              else colsum[col] = a;
-            }
+            if (!group(j).has(k)) continue;
+            const int64_t col = group(j).col(k);
+            const f2 d = which == 0 ? dg[j][k / 2] : db[LAYER ? j : 0][k / 2];
+            float a = k & 1 ? d.y : d.x;
+            if (q > 0) a += colsum[col];
+            if (q + 1 == Q.teams) part[col] = a;
+            else colsum[col] = a;
           }
       }
     }
@@ -352,9 +328,11 @@ __global__ void __launch_bounds__(CTA, 512 / CTA) norm_bwd_fused_kernel(const __
   }
 }
 
-// The row blocks' sums joined: 32 columns a CTA, warps over blocks in turn.
-__global__ void __launch_bounds__(NB_THREADS) norm_bwd_join_kernel(const __grid_constant__ NormBwdParams P) {
-  __shared__ float sums[NB_WARPS][32];
+// The row blocks' sums joined: 32 columns a CTA, 32 warps over the blocks in
+// turn (the few sums a warp adds are all in flight at once).
+constexpr int NB_JOIN_THREADS = 1024;
+__global__ void __launch_bounds__(NB_JOIN_THREADS) norm_bwd_join_kernel(const __grid_constant__ NormBwdParams P) {
+  __shared__ float sums[NB_JOIN_THREADS / 32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   const int which = blockIdx.y;
@@ -364,15 +342,27 @@ __global__ void __launch_bounds__(NB_THREADS) norm_bwd_join_kernel(const __grid_
   float s = 0.0f;
   if (col < P.cols) {
     const float* p = P.part + (int64_t)which * P.blocks * P.pcols + col;
-    for (int b = warp; b < P.blocks; b += NB_WARPS) s += p[(int64_t)b * P.pcols];
+    for (int b0 = warp; b0 < P.blocks; b0 += 16 * (NB_JOIN_THREADS / 32)) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int b = b0 + i * (NB_JOIN_THREADS / 32);
+        v[i] = b < P.blocks ? p[(int64_t)b * P.pcols] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s += v[i];
+    }
   }
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && col < P.cols) {
+  // Column `warp`'s 32 sums, one a lane.
+  s = sums[lane][warp];
 #pragma unroll
-    for (int w = 1; w < NB_WARPS; ++w) s += sums[w][lane];
-    if (P.grad_dtype == PSK_BF16) ((uint16_t*)out)[col] = f32_to_bf16_bits(s);
-    else ((float*)out)[col] = s;
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  const int64_t c = (int64_t)blockIdx.x * 32 + warp;
+  if (lane == 0 && c < P.cols) {
+    if (P.grad_dtype == PSK_BF16) ((uint16_t*)out)[c] = f32_to_bf16_bits(s);
+    else ((float*)out)[c] = s;
   }
 }
 
@@ -429,7 +419,7 @@ static uint64_t norm_bwd_layout(int64_t rows, int64_t cols, uint64_t* part) {
 template <int TY, int KIND, bool VEC, int NV, int CTA>
 static void fused_launch(const NormFusedParams& Q, cudaStream_t s) {
   norm_bwd_fused_kernel<TY, KIND, VEC, NV, CTA>
-      <<<(unsigned)Q.B.blocks, CTA, Q.teams > 1 ? (size_t)Q.B.cols * 4 : 0, s>>>(Q);
+      <<<(unsigned)Q.B.blocks, CTA, (size_t)(NV * 8 * Q.team + (Q.teams > 1 ? Q.B.cols : 0)) * 4, s>>>(Q);
 }
 
 // The column sums' join, launched so that its set-up overlaps the kernel
@@ -440,7 +430,7 @@ static int norm_bwd_join(const NormBwdParams& P, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((P.cols + 31) / 32), P.dbeta ? 2 : 1);
-  cfg.blockDim = dim3(NB_THREADS);
+  cfg.blockDim = dim3(NB_JOIN_THREADS);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -534,7 +524,7 @@ extern "C" int psk_norm_backward(const void* x, int32_t xt, const void* ct, int3
   P.part = (float*)((char*)workspace + part);
   P.pcols = (cols + 7) / 8 * 8;
   P.blocks = norm_bwd_blocks(rows, cols);
-  const bool vec = rows_vec8(x, xt, ldx, rows) && rows_vec8(ct, ct_t, ldc, rows) && rows_vec8(dx, dxt, ldd, rows) &&
+  const bool vec = cols % 8 == 0 && rows_vec8(x, xt, ldx, rows) && rows_vec8(ct, ct_t, ldc, rows) && rows_vec8(dx, dxt, ldd, rows) &&
                    (!gamma || rows_vec8(gamma, param_dtype, cols, 1));
   if (cols <= NB_FUSED_COLS && xt == ct_t && xt == dxt) {
     const FusedShape f = fused_shape(cols);
@@ -545,7 +535,7 @@ extern "C" int psk_norm_backward(const void* x, int32_t xt, const void* ct, int3
     with_dtype(xt, [&](auto TY) {
       return with_bool(kind == PSK_NORM_LAYER, [&](auto LAYER) {
         constexpr int KIND = LAYER.value ? PSK_NORM_LAYER : PSK_NORM_RMS;
-        return with_bool(vec && cols % 8 == 0, [&](auto VEC) {
+        return with_bool(vec, [&](auto VEC) {
           if (f.cta == 512) fused_launch<TY.value, KIND, VEC.value, 2, 512>(Q, s);
           else if (f.nv == 2) fused_launch<TY.value, KIND, VEC.value, 2, 256>(Q, s);
           else fused_launch<TY.value, KIND, VEC.value, 1, 256>(Q, s);

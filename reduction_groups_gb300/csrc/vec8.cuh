@@ -65,50 +65,84 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int n, const float* v
   }
 }
 
-// A lane's eight columns of slice s: neighbouring ones when rows move by
-// 16-byte accesses, else every 32nd (so that a warp's loads coalesce).
-template <bool VEC>
-struct SliceCols {
-  int64_t c0;
-  int n;
-  __device__ __forceinline__ SliceCols(int slice, int lane, int64_t cols) {
-    if (VEC) {
-      c0 = (int64_t)slice * 256 + lane * 8;
-      const int64_t left = cols - c0;
-      n = left < 0 ? 0 : left < 8 ? (int)left : 8;
-    } else {
-      c0 = (int64_t)slice * 256 + lane;
-      const int64_t left = cols - c0;
-      n = left <= 0 ? 0 : left > 224 ? 8 : (int)((left + 31) / 32);
-    }
+// NC of a thread's columns as loaded, so that a batch of loads can be in
+// flight before the first is widened.
+template <int TY, bool VEC, int NC>
+struct Piece {
+  static constexpr int W = VEC && TY == PSK_BF16 ? NC / 2 : NC;
+  uint32_t w[W];
+  __device__ __forceinline__ float get(int k) const {
+    if constexpr (VEC && TY == PSK_BF16)
+      return __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+    else
+      return __uint_as_float(w[k]);
   }
-  template <int DT>
-  __device__ __forceinline__ void load(const void* p, int64_t row, float* v) const {
-    if (VEC) {
-      load8<DT, true>(p, row + c0, n, v);
+};
+
+// A thread's NC columns of the (T NC)-wide span that begins at column `base`,
+// for thread t of T: neighbouring ones when rows move by 16-byte accesses
+// (cols is then a multiple of 8), else every T-th, so that a warp's accesses
+// coalesce.  Columns from cols on are read as zeros and not written.
+template <bool VEC, int NC>
+struct Columns {
+  int64_t first, cols;
+  int stride;
+  __device__ __forceinline__ Columns(int64_t base, int T, int t, int64_t cols_)
+      : first(base + (VEC ? (int64_t)t * NC : t)), cols(cols_), stride(VEC ? 1 : T) {}
+  __device__ __forceinline__ int64_t col(int k) const { return first + (int64_t)k * stride; }
+  __device__ __forceinline__ bool has(int k) const { return VEC ? first < cols : col(k) < cols; }
+  template <int TY>
+  __device__ __forceinline__ void load(const void* p, int64_t row, Piece<TY, VEC, NC>& o) const {
+    if constexpr (VEC) {
+      constexpr int W = Piece<TY, VEC, NC>::W;
+      const char* q = (const char*)p + (row + first) * (TY == PSK_BF16 ? 2 : 4);
+#pragma unroll
+      for (int i = 0; i < W; ++i) o.w[i] = 0;
+      if (has(0)) {
+        if constexpr (W == 2) {
+          const uint2 u = *(const uint2*)q;
+          o.w[0] = u.x, o.w[1] = u.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; i += 4) {
+            const uint4 u = *(const uint4*)(q + 4 * i);
+            o.w[i] = u.x, o.w[i + 1] = u.y, o.w[i + 2] = u.z, o.w[i + 3] = u.w;
+          }
+        }
+      }
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[k] = 0.0f;
-        if (k < n) {
-          if (DT == PSK_BF16) v[k] = bf16_bits_to_f32(((const uint16_t*)p)[row + c0 + 32 * k]);
-          else v[k] = ((const float*)p)[row + c0 + 32 * k];
+      for (int k = 0; k < NC; ++k) {
+        o.w[k] = 0;
+        if (has(k)) {
+          if constexpr (TY == PSK_BF16) o.w[k] = (uint32_t)((const uint16_t*)p)[row + col(k)] << 16;
+          else o.w[k] = ((const uint32_t*)p)[row + col(k)];
         }
       }
     }
   }
-  template <int DT>
+  template <int TY>
   __device__ __forceinline__ void store(void* p, int64_t row, const float* v) const {
-    if (VEC) {
-      store8<DT, true>(p, row + c0, n, v);
-    } else {
+    if constexpr (VEC) {
+      if (has(0)) {
+        char* q = (char*)p + (row + first) * (TY == PSK_BF16 ? 2 : 4);
+        if constexpr (TY == PSK_BF16) {
+          if constexpr (NC == 4) *(uint2*)q = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
+          else
+            *(uint4*)q = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
+                                    f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
+        } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (k < n) {
-          if (DT == PSK_BF16) ((uint16_t*)p)[row + c0 + 32 * k] = f32_to_bf16_bits(v[k]);
-          else ((float*)p)[row + c0 + 32 * k] = v[k];
+          for (int i = 0; i < NC; i += 4) *(float4*)(q + 4 * i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NC; ++k)
+        if (has(k)) {
+          if constexpr (TY == PSK_BF16) ((uint16_t*)p)[row + col(k)] = f32_to_bf16_bits(v[k]);
+          else ((float*)p)[row + col(k)] = v[k];
+        }
     }
   }
 };
