@@ -5,6 +5,8 @@
 // Sums are held in f32 over trees fixed by the sizes: no atomics.
 #include "vec8.cuh"
 #include "pair.cuh"
+#include "pipe.cuh"
+#include "trainops.h"
 
 namespace psk {
 
@@ -328,6 +330,271 @@ __global__ void __launch_bounds__(CTA, 512 / CTA) norm_bwd_fused_kernel(const __
   }
 }
 
+// ----------------------------------------------------------- the ring kernel
+//
+// The same pass for rows of one storage type of 256 to 16384 columns that are
+// 16-byte aligned: x and ct rows are copied by TMA into a ring of shared
+// memory, several rows ahead (what keeps HBM busy: registers alone hold too
+// few bytes in flight), and read from there for each reduction and for dx; a
+// team's threads keep only their columns' dgamma and dbeta sums in registers.
+// A team's first thread refills its own slots as soon as the team's warps have
+// left them (a separate producer warp would leave 96 registers a thread):
+// LayerNorm past a row's first barrier, which comes early in it; RMSNorm, whose
+// only barrier comes halfway, as its warps report.
+constexpr int RING_THREADS = 512;          // sixteen warps: 128 registers a thread
+constexpr int RING_MAX_COLS = 16384;
+constexpr int RING_MAX_SLOTS = 32;
+constexpr int RING_MAX_BLOCKS = 160;
+constexpr int RING_SMEM = 220 * 1024;
+
+struct NormRingParams {
+  NormBwdParams B;
+  int32_t team, teams;       // threads of a team (the kernel's T), teams of a CTA
+  int32_t slots;             // a multiple of teams: a slot's phases are one team's, in order
+  int32_t row_bytes;         // of x and of ct; a slot holds one of each
+};
+
+// 1 / sqrt(v) by the unit's approximation and one Newton step (about one ulp;
+// v = 0 gives +inf, NaN and negative v NaN, as the division would).
+__device__ __forceinline__ float rsqrt_newton(float v) {
+  const float y = rsqrtf(v);
+  const float h = 0.5f * v * y;
+  const float z = fmaf(y, fmaf(-h, y, 0.5f), y);
+  return v > 0.0f && v < INFINITY ? z : y;
+}
+
+template <int TY, int KIND, int NV, int T>
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __grid_constant__ NormRingParams Q) {
+  // gamma in f32 as the threads read it (later the column sums), then the ring.
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ uint64_t full[RING_MAX_SLOTS], empty[RING_MAX_SLOTS];
+  __shared__ __align__(16) float red[2][3][RING_THREADS / 32];
+  __shared__ volatile int abort_flag;
+  constexpr bool LAYER = KIND == PSK_NORM_LAYER;
+  constexpr int E = TY == PSK_BF16 ? 8 : 4;              // elements of a 16-byte group
+  constexpr int NG = NV * 8 / E;                         // groups of a thread
+  const NormBwdParams& P = Q.B;
+  constexpr int TEAMS = RING_THREADS / T, nw = T / 32;
+  const int tid = threadIdx.x, slots = Q.slots;
+  const int groups = (int)P.cols / E;
+  float* gamma = (float*)ring_smem;
+  unsigned char* ring = ring_smem + (size_t)(NG * E * T) * 4;
+  const int slot_bytes = 2 * Q.row_bytes;
+  const int n_local = blockIdx.x < P.rows ? (int)((P.rows - 1 - blockIdx.x) / gridDim.x + 1) : 0;
+  if (tid == 0) {
+    for (int i = 0; i < slots; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], T / 32);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  // gamma of group j of thread t: float4 number (j E / 4 + i) T + t, i < E / 4.
+  for (int i = tid; i < NG * E * T; i += RING_THREADS) {
+    const int at = i >> 2, who = at % T, piece = at / T;
+    const int64_t c = ((int64_t)(piece * 4 / E) * T + who) * E + (piece * 4) % E + (i & 3);
+    float g = 1.0f;
+    if (P.gamma && c < P.cols)
+      g = P.param_dtype == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)P.gamma)[c]) : ((const float*)P.gamma)[c];
+    gamma[i] = g;
+  }
+  __syncthreads();
+
+  // After a timeout (`dead`) a thread skips waits and work but keeps meeting
+  // its team's barriers.
+  const int team = tid / T, t = tid - team * T, lane = tid & 31, warp = tid >> 5;
+  bool dead = false;
+  int flip = 0, issued = -1;
+  const long long drop = g_pipe_drop_row;
+  // The team's first thread copies local row i into its slot s.
+  auto fetch = [&](int i, int s) {
+    if (t != 0 || i >= n_local || dead || (drop >= 0 && i >= drop)) return;
+    const int64_t r = blockIdx.x + (int64_t)i * gridDim.x;
+    unsigned char* at = ring + (size_t)s * slot_bytes;
+    mbar_arrive_expect_tx(&full[s], (uint32_t)slot_bytes);
+    bulk_copy_g2s(at, (const unsigned char*)P.x + r * P.ldx * (16 / E), (uint32_t)Q.row_bytes, &full[s]);
+    bulk_copy_g2s(at + Q.row_bytes, (const unsigned char*)P.ct + r * P.ldc * (16 / E), (uint32_t)Q.row_bytes, &full[s]);
+    issued = i;
+  };
+  // Sums over the team, one barrier (the buffers alternate).
+  auto team_sum = [&](float* v, int n) {
+    flip ^= 1;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      if (q >= n) break;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v[q] += __shfl_xor_sync(0xFFFFFFFFu, v[q], o);
+      if (lane == 0) red[flip][q][warp] = v[q];
+    }
+    if (nw == 1) return;
+    named_barrier(1 + team, T);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      if (q >= n) break;
+      const float2* p = (const float2*)&red[flip][q][team * nw];     // nw: 2, 4, 8 or 16
+      float2 s = p[0];
+      #pragma unroll
+      for (int w = 1; w < nw / 2; ++w) {
+        const float2 u = p[w];
+        s.x += u.x, s.y += u.y;
+      }
+      v[q] = s.x + s.y;
+    }
+  };
+  for (int i = team; i < slots; i += TEAMS) fetch(i, i);
+  const f2 zero{0.0f, 0.0f};
+  f2 dg[NG][E / 2], db[LAYER ? NG : 1][E / 2];
+#pragma unroll
+  for (int j = 0; j < NG; ++j)
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) {
+      dg[j][k] = zero;
+      if (LAYER) db[j][k] = zero;
+    }
+  int s = team, before = 0;                  // the row's slot, the last row's
+  uint32_t parity = 0, parity_before = 0;    // of their phases
+  for (int i = team; i < n_local; i += TEAMS) {
+    const int64_t r = blockIdx.x + (int64_t)i * gridDim.x;
+    dead = dead || abort_flag;
+    if (!LAYER && i != team && t == 0 && !dead) {
+      if (mbar_wait(&empty[before], parity_before)) fetch(i - TEAMS + slots, before);
+      else abort_flag = 1, dead = true;
+    }
+    if (!dead && !mbar_wait(&full[s], parity)) { abort_flag = 1; dead = true; }
+    const unsigned char* xs = ring + (size_t)s * slot_bytes;
+    const unsigned char* cs = xs + Q.row_bytes;
+    auto values = [&](const unsigned char* p, int j, f2* v) {
+      const uint4 u = *(const uint4*)(p + (size_t)(j * T + t) * 16);
+      if constexpr (TY == PSK_BF16) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = f2{__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)};
+      } else {
+        v[0] = f2{__uint_as_float(u.x), __uint_as_float(u.y)}, v[1] = f2{__uint_as_float(u.z), __uint_as_float(u.w)};
+      }
+    };
+    auto gate = [&](int j, f2* g) {
+#pragma unroll
+      for (int q = 0; q < E / 4; ++q) {
+        const float4 a = ((const float4*)gamma)[(j * (E / 4) + q) * T + t];
+        g[2 * q] = f2_mul(g[2 * q], f2{a.x, a.y}), g[2 * q + 1] = f2_mul(g[2 * q + 1], f2{a.z, a.w});
+      }
+    };
+    float sums[3];
+    float mu = 0.0f;
+    if (LAYER) {
+      f2 a = zero;
+      if (!dead) {
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+          if (j * T + t >= groups) continue;
+          f2 x[E / 2];
+          values(xs, j, x);
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) a = f2_add(a, x[k]);
+        }
+      }
+      sums[0] = a.x + a.y;
+      team_sum(sums, 1);
+      if (nw == 1) __syncwarp();
+      if (i != team) fetch(i - TEAMS + slots, before);
+      mu = sums[0] * P.inv_cols;
+    }
+    const f2 nmu = f2_splat(-mu);
+    constexpr bool KEEP = !LAYER;            // widened values stay in registers for dx
+    f2 kx[KEEP ? NG : 1][E / 2], kc[KEEP ? NG : 1][E / 2];
+    f2 a = zero, b = zero, d = zero;
+    if (!dead) {
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        if (j * T + t >= groups) continue;
+        f2 x[E / 2], g[E / 2];
+        values(xs, j, x);
+        values(cs, j, g);
+        if (KEEP) {
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) kx[KEEP ? j : 0][k] = x[k], kc[KEEP ? j : 0][k] = g[k];
+        }
+        gate(j, g);
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) {
+          if (LAYER) x[k] = f2_add(x[k], nmu), d = f2_add(d, g[k]);
+          a = f2_fma(x[k], x[k], a), b = f2_fma(x[k], g[k], b);
+        }
+      }
+    }
+    sums[0] = a.x + a.y, sums[1] = b.x + b.y, sums[2] = d.x + d.y;
+    team_sum(sums, LAYER ? 3 : 2);
+    const float mg = sums[2] * P.inv_cols;
+    const float rd = rsqrt_newton(sums[0] * P.inv_cols + P.eps);
+    const f2 rd2 = f2_splat(rd), m2 = f2_splat(-(sums[1] * rd * P.inv_cols)), nmg = f2_splat(-mg);
+    if (!dead) {
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        if (j * T + t >= groups) continue;
+        f2 x[E / 2], c[E / 2], g[E / 2], y[E / 2];
+        if (KEEP) {
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) x[k] = kx[KEEP ? j : 0][k], c[k] = kc[KEEP ? j : 0][k];
+        } else {
+          values(xs, j, x);
+          values(cs, j, c);
+        }
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) g[k] = c[k];
+        gate(j, g);
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) {
+          const f2 xh = f2_mul(LAYER ? f2_add(x[k], nmu) : x[k], rd2);
+          dg[j][k] = f2_fma(c[k], xh, dg[j][k]);
+          if (LAYER) db[j][k] = f2_add(db[j][k], c[k]);
+          y[k] = f2_mul(f2_fma(xh, m2, LAYER ? f2_add(g[k], nmg) : g[k]), rd2);
+        }
+        unsigned char* o = (unsigned char*)P.dx + r * P.ldd * (16 / E) + (size_t)(j * T + t) * 16;
+        if constexpr (TY == PSK_BF16)
+          *(uint4*)o = make_uint4(f32x2_to_bf16x2(y[0].x, y[0].y), f32x2_to_bf16x2(y[1].x, y[1].y),
+                                  f32x2_to_bf16x2(y[2].x, y[2].y), f32x2_to_bf16x2(y[3].x, y[3].y));
+        else
+          *(float4*)o = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+      }
+    }
+    __syncwarp();
+    if (!LAYER && !dead && lane == 0) mbar_arrive(&empty[s]);
+    before = s, parity_before = parity;
+    s += TEAMS;
+    if (s >= slots) s -= slots, parity ^= 1;
+  }
+  // After a timeout, copies still in flight land before the CTA retires.
+  if (dead)
+    for (int i = issued; i >= 0 && i > issued - slots; i -= TEAMS)
+      mbar_wait(&full[i % slots], (uint32_t)(i / slots) & 1u);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!P.dgamma && !P.dbeta) return;
+  // The CTA's column sums, its teams' in turn, in gamma's place.
+#pragma unroll
+  for (int which = 0; which < (LAYER ? 2 : 1); ++which) {
+    float* part = P.part + ((int64_t)which * P.blocks + blockIdx.x) * P.pcols;
+    for (int q = 0; q < TEAMS; ++q) {
+      if (TEAMS > 1) named_barrier(15, RING_THREADS);
+      if (team != q) continue;
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        if (j * T + t >= groups) continue;
+#pragma unroll
+        for (int h = 0; h < E / 4; ++h) {
+          const f2 a = which == 0 ? dg[j][2 * h] : db[LAYER ? j : 0][2 * h];
+          const f2 b = which == 0 ? dg[j][2 * h + 1] : db[LAYER ? j : 0][2 * h + 1];
+          float4 sum = make_float4(a.x, a.y, b.x, b.y);
+          float4* held = (float4*)gamma + (j * (E / 4) + h) * T + t;
+          if (q > 0) {
+            const float4 u = *held;
+            sum.x += u.x, sum.y += u.y, sum.z += u.z, sum.w += u.w;
+          }
+          if (q + 1 == TEAMS) *(float4*)(part + (j * T + t) * E + 4 * h) = sum;
+          else *held = sum;
+        }
+      }
+    }
+  }
+}
+
 // The row blocks' sums joined: 32 columns a CTA, 32 warps over the blocks in
 // turn (the few sums a warp adds are all in flight at once).
 constexpr int NB_JOIN_THREADS = 1024;
@@ -407,12 +674,31 @@ static int fused_blocks(int64_t rows, int64_t cols) {
   return (int)(want < most ? want : most);
 }
 
+// The ring kernel's shape for rows of this size, or false: teams of the fewest
+// threads that hold a row's column sums in two (up to 512 columns) or four
+// groups of eight a thread -- wide threads share a row's shuffles and barrier
+// among more columns, and small teams overlap more rows -- and as many slots
+// as fit, two rows a team at least.
+static bool ring_shape(NormRingParams& Q, int* nv, int32_t dt, int64_t cols) {
+  if (cols < 256 || cols > RING_MAX_COLS || cols % 8 != 0) return false;
+  *nv = cols <= 512 ? 2 : 4;
+  Q.team = 32;
+  while (Q.team * *nv * 8 < cols) Q.team *= 2;
+  Q.teams = RING_THREADS / Q.team;
+  Q.row_bytes = (int32_t)cols * dtype_size(dt);
+  const int fits = (RING_SMEM - *nv * 8 * Q.team * 4) / (2 * Q.row_bytes);
+  Q.slots = (fits < RING_MAX_SLOTS ? fits : RING_MAX_SLOTS) / Q.teams * Q.teams;
+  return Q.slots >= 2 * Q.teams;
+}
+
 static uint64_t norm_bwd_layout(int64_t rows, int64_t cols, uint64_t* part) {
   const uint64_t stats = ((uint64_t)rows * 16 + 255) / 256 * 256;
   const uint64_t pcols = (uint64_t)(cols + 7) / 8 * 8;
   *part = stats;
   int blocks = norm_bwd_blocks(rows, cols);
   if (cols <= NB_FUSED_COLS && fused_blocks(rows, cols) > blocks) blocks = fused_blocks(rows, cols);
+  const int64_t ring = rows < RING_MAX_BLOCKS ? rows : RING_MAX_BLOCKS;
+  if (ring > blocks) blocks = (int)ring;
   return stats + 2ull * blocks * pcols * 4;
 }
 
@@ -420,6 +706,41 @@ template <int TY, int KIND, bool VEC, int NV, int CTA>
 static void fused_launch(const NormFusedParams& Q, cudaStream_t s) {
   norm_bwd_fused_kernel<TY, KIND, VEC, NV, CTA>
       <<<(unsigned)Q.B.blocks, CTA, (size_t)(NV * 8 * Q.team + (Q.teams > 1 ? Q.B.cols : 0)) * 4, s>>>(Q);
+}
+
+template <int TY, int KIND, int NV, int T>
+static int ring_launch_team(const NormRingParams& Q, cudaStream_t s) {
+  static bool limit[PSK_MAX_DEVICES] = {};
+  smem_limit_once((const void*)norm_bwd_ring_kernel<TY, KIND, NV, T>, RING_SMEM, limit);
+  const size_t smem = (size_t)NV * 8 * T * 4 + (size_t)Q.slots * 2 * Q.row_bytes;
+  norm_bwd_ring_kernel<TY, KIND, NV, T><<<(unsigned)Q.B.blocks, RING_THREADS, smem, s>>>(Q);
+  return check_launch("norm backward ring kernel");
+}
+
+template <int TY, int KIND>
+static int ring_launch(const NormRingParams& Q, int nv, cudaStream_t s) {
+  if (nv == 2) return ring_launch_team<TY, KIND, 2, 32>(Q, s);
+  switch (Q.team) {
+    case 32: return ring_launch_team<TY, KIND, 4, 32>(Q, s);
+    case 64: return ring_launch_team<TY, KIND, 4, 64>(Q, s);
+    case 128: return ring_launch_team<TY, KIND, 4, 128>(Q, s);
+    case 256: return ring_launch_team<TY, KIND, 4, 256>(Q, s);
+    default: return ring_launch_team<TY, KIND, 4, 512>(Q, s);
+  }
+}
+
+int norm_bwd_status(unsigned int* v, bool reset) {
+  if (cudaMemcpyFromSymbol(v, g_pipe_status, sizeof(*v)) != cudaSuccess) return check_launch("device status read");
+  if (reset) {
+    const unsigned int z = 0;
+    if (cudaMemcpyToSymbol(g_pipe_status, &z, sizeof(z)) != cudaSuccess) return check_launch("device status reset");
+  }
+  return PSK_OK;
+}
+
+int norm_bwd_set_drop_row(long long row) {
+  if (cudaMemcpyToSymbol(g_pipe_drop_row, &row, sizeof(row)) != cudaSuccess) return check_launch("test hook write");
+  return PSK_OK;
 }
 
 // The column sums' join, launched so that its set-up overlaps the kernel
@@ -526,6 +847,21 @@ extern "C" int psk_norm_backward(const void* x, int32_t xt, const void* ct, int3
   P.blocks = norm_bwd_blocks(rows, cols);
   const bool vec = cols % 8 == 0 && rows_vec8(x, xt, ldx, rows) && rows_vec8(ct, ct_t, ldc, rows) && rows_vec8(dx, dxt, ldd, rows) &&
                    (!gamma || rows_vec8(gamma, param_dtype, cols, 1));
+  NormRingParams G{};
+  int nv = 0;
+  if (vec && xt == ct_t && xt == dxt && ring_shape(G, &nv, xt, cols)) {
+    G.B = P;
+    int64_t blocks = (rows + G.teams - 1) / G.teams;
+    const int64_t sms = device_sm_count() < RING_MAX_BLOCKS ? device_sm_count() : RING_MAX_BLOCKS;
+    G.B.blocks = (int)(blocks < sms ? blocks : sms);
+    rc = with_dtype(xt, [&](auto TY) {
+      return with_bool(kind == PSK_NORM_LAYER, [&](auto LAYER) {
+        constexpr int KIND = LAYER.value ? PSK_NORM_LAYER : PSK_NORM_RMS;
+        return ring_launch<TY.value, KIND>(G, nv, s);
+      });
+    });
+    return rc || (!dgamma && !dbeta) ? rc : norm_bwd_join(G.B, s);
+  }
   if (cols <= NB_FUSED_COLS && xt == ct_t && xt == dxt) {
     const FusedShape f = fused_shape(cols);
     NormFusedParams Q{P, f.team, f.teams};

@@ -1458,8 +1458,9 @@ extern "C" int psk_test_drop_row(int64_t row) {
   if (row < -1) return fail(PSK_E_ARG, "row %lld (-1 or a local row index)", (long long)row);
   const long long v = row;
   if (cudaMemcpyToSymbol(g_pipe_drop_row, &v, sizeof(v)) != cudaSuccess) return check_launch("test hook write");
-  const int rc = lanes_set_drop_row(v);
-  return rc ? rc : loss_set_drop_row(v);
+  int rc = lanes_set_drop_row(v);
+  if (!rc) rc = loss_set_drop_row(v);
+  return rc ? rc : norm_bwd_set_drop_row(v);
 }
 
 namespace psk {
@@ -1496,7 +1497,10 @@ extern "C" int psk_device_status(uint32_t* status, int32_t reset) {
   unsigned int tv = 0;
   const int trc = loss_status(&tv, reset != 0);
   if (trc) return trc;
-  *status = v | lv | tv;
+  unsigned int nv = 0;
+  const int nrc = norm_bwd_status(&nv, reset != 0);
+  if (nrc) return nrc;
+  *status = v | lv | tv | nv;
   return PSK_OK;
 }
 

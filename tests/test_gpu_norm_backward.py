@@ -136,3 +136,28 @@ def test_repeats_bit_for_bit_on_a_side_stream_and_in_a_graph(R):
     torch.cuda.synchronize()
     for o in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(outs[0][:3], o[:3]))
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("rows,cols,dtype", [(2000, 4096, "bf16"), (3000, 2048, "f32"), (1500, 1032, "bf16"),
+                                             (700, 16384, "bf16"), (900, 12288, "f32"), (1100, 8192, "bf16"),
+                                             (4000, 320, "bf16"), (2500, 1001, "f32")])
+def test_many_rows(R, kind, rows, cols, dtype):
+    _check(R, kind, rows, cols, dtype, dtype, dtype, dtype, "f32")
+
+
+def test_a_lost_copy_ends_in_a_status_not_a_hang(R):
+    x = torch.randn(900, 4096, device="cuda", dtype=torch.bfloat16)
+    dx, dg = torch.empty_like(x), torch.empty(4096, device="cuda")
+    ws = scratch(R.psk_norm_backward_workspace(900, 4096))
+    assert R.psk_device_status(reset=True) == 0
+    try:
+        R.psk_test_drop_row(3)
+        R.psk_norm_backward(x, x, dx, "rms", 1e-6, None, dg, workspace=ws)
+        torch.cuda.synchronize()
+        assert R.psk_device_status(reset=True) == 1
+    finally:
+        R.psk_test_drop_row(-1)
+    R.psk_norm_backward(x, x, dx, "rms", 1e-6, None, dg, workspace=ws)
+    torch.cuda.synchronize()
+    assert R.psk_device_status() == 0 and bool(dx.isfinite().all()) and bool(dg.isfinite().all())
