@@ -163,177 +163,111 @@ __global__ void __launch_bounds__(NB_THREADS) norm_bwd_apply_kernel(const __grid
   }
 }
 
-// ---------------------------------------------------------- the fused kernel
+// 1 / sqrt(v) by the unit's approximation and one Newton step (about one ulp;
+// v = 0 gives +inf, NaN and negative v NaN, as the division would).
+__device__ __forceinline__ float rsqrt_newton(float v) {
+  const float y = rsqrtf(v);
+  const float h = 0.5f * v * y;
+  const float z = fmaf(y, fmaf(-h, y, 0.5f), y);
+  return v > 0.0f && v < INFINITY ? z : y;
+}
+
+// ------------------------------------------------------- the warp-a-row kernel
 //
-// One pass over rows of up to 8192 columns of one storage type: a team of T
-// threads holds a row's x and ct in registers (NV groups of eight columns a
-// thread) from the reductions to dx, while its next row's loads are in
-// flight, and keeps its columns' dgamma and dbeta sums in registers over all
-// of its rows.  The floor is one read of x and ct and one write of dx; a
-// CTA's column sums go to the workspace once.
-constexpr int NB_FUSED_COLS = 8192;
-constexpr int NB_ROWS_PER_TEAM = 4;        // at least, where there are as many
+// One pass over rows of up to 255 columns of one storage type: a warp holds a
+// row's x and ct in registers (eight columns a thread) from the reductions to
+// dx, while its next row's loads are in flight, and keeps its columns' dgamma
+// and dbeta sums in registers over all of its rows.  The floor is one read of
+// x and ct and one write of dx; a CTA's column sums go to the workspace once.
+constexpr int NB_FUSED_COLS = 255;
+constexpr int NB_ROWS_PER_WARP = 4;        // at least, where there are as many
 
-struct NormFusedParams {
-  NormBwdParams B;
-  int32_t team, teams;       // threads of a team, teams of a CTA
-};
-
-template <int TY, int KIND, bool VEC, int NV, int CTA>
-__global__ void __launch_bounds__(CTA, 512 / CTA) norm_bwd_fused_kernel(const __grid_constant__ NormFusedParams Q) {
-  // gamma in f32, laid out as the threads read it; then the CTA's column sums.
-  extern __shared__ __align__(16) float smem[];
-  __shared__ float2 red[2][CTA / 32];
-  const NormBwdParams& P = Q.B;
+template <int TY, int KIND, bool VEC>
+__global__ void __launch_bounds__(NB_THREADS) norm_bwd_warps_kernel(const __grid_constant__ NormBwdParams P) {
+  __shared__ float colsum[2][NB_WARPS][256];
   constexpr bool LAYER = KIND == PSK_NORM_LAYER;
-  const int T = Q.team, team = threadIdx.x / T, t = threadIdx.x - team * T, nw = T / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t step = (int64_t)gridDim.x * Q.teams;
-  auto group = [&](int j) { return Columns<VEC, 8>((int64_t)j * T * 8, T, t, P.cols); };
-  int flip = 0;
-  // Sum two values over the team; one barrier (the buffers alternate).
-  auto team_sum = [&](f2 a, f2 b) {
-    float s = a.x + a.y, u = b.x + b.y;
+  const int64_t step = (int64_t)gridDim.x * NB_WARPS;
+  const Columns<VEC, 8> cols(0, 32, lane, P.cols);
+  auto warp_sum = [&](f2 a) {
+    float s = a.x + a.y;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
-    }
-    if (nw == 1) return make_float2(s, u);
-    flip ^= 1;
-    if (lane == 0) red[flip][warp] = make_float2(s, u);
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(T) : "memory");
-    float2 v = red[flip][team * nw];
-    for (int w = 1; w < nw; ++w) {
-      const float2 q = red[flip][team * nw + w];
-      v.x += q.x, v.y += q.y;
-    }
-    return v;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    return s;
   };
-
-  // gamma of group j, columns k..k+3: float4 number (2 j + k / 4) T + t.
-  for (int i = threadIdx.x; i < NV * 8 * T; i += CTA) {
-    const int at = i >> 2, who = at % T, piece = at / T, k = (piece & 1) * 4 + (i & 3);
-    const int64_t c = Columns<VEC, 8>((int64_t)(piece >> 1) * T * 8, T, who, P.cols).col(k);
-    float g = 1.0f;
-    if (P.gamma && c < P.cols)
-      g = P.param_dtype == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)P.gamma)[c]) : ((const float*)P.gamma)[c];
-    smem[i] = g;
-  }
-  __syncthreads();
-  const float4* gamma = (const float4*)smem;
-
-  f2 dg[NV][4], db[LAYER ? NV : 1][4];
+  const f2 zero{0.0f, 0.0f};
+  f2 gamma[4], dg[4], db[4];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int k = 0; k < 8; ++k) {
+    float g = 1.0f;
+    if (P.gamma && cols.has(k))
+      g = P.param_dtype == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)P.gamma)[cols.col(k)])
+                                    : ((const float*)P.gamma)[cols.col(k)];
+    if (k & 1) gamma[k / 2].y = g;
+    else gamma[k / 2].x = g;
+    dg[k / 2] = zero, db[k / 2] = zero;
+  }
+  int64_t r = (int64_t)blockIdx.x * NB_WARPS + warp;
+  Piece<TY, VEC, 8> x, c;
+  if (r < P.rows) cols.load(P.x, r * P.ldx, x), cols.load(P.ct, r * P.ldc, c);
+  for (; r < P.rows; r += step) {
+    f2 xv[4], cv[4], g[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      dg[j][k] = f2{0.0f, 0.0f};
-      if (LAYER) db[j][k] = f2{0.0f, 0.0f};
+      xv[k] = f2{x.get(2 * k), x.get(2 * k + 1)}, cv[k] = f2{c.get(2 * k), c.get(2 * k + 1)};
+      g[k] = f2_mul(cv[k], gamma[k]);
     }
-  int64_t r = (int64_t)blockIdx.x * Q.teams + team;
-  Piece<TY, VEC, 8> x[NV], c[NV];
-  auto fetch = [&](int64_t row) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) group(j).load(P.x, row * P.ldx, x[j]), group(j).load(P.ct, row * P.ldc, c[j]);
-  };
-  if (r < P.rows) fetch(r);
-  for (; r < P.rows; r += step) {
-    f2 xv[NV][4], cv[NV][4];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        xv[j][k] = f2{x[j].get(2 * k), x[j].get(2 * k + 1)};
-        cv[j][k] = f2{c[j].get(2 * k), c[j].get(2 * k + 1)};
-      }
-    if (r + step < P.rows) fetch(r + step);
-    auto gated = [&](int j, f2* g) {       // ct gamma
-      const float4 a = gamma[(2 * j) * T + t], b = gamma[(2 * j + 1) * T + t];
-      g[0] = f2_mul(cv[j][0], f2{a.x, a.y}), g[1] = f2_mul(cv[j][1], f2{a.z, a.w});
-      g[2] = f2_mul(cv[j][2], f2{b.x, b.y}), g[3] = f2_mul(cv[j][3], f2{b.z, b.w});
-    };
+    if (r + step < P.rows) cols.load(P.x, (r + step) * P.ldx, x), cols.load(P.ct, (r + step) * P.ldc, c);
     float mg = 0.0f;
     if (LAYER) {
-      f2 s{0.0f, 0.0f}, u{0.0f, 0.0f};
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        f2 g[4];
-        gated(j, g);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s = f2_add(s, xv[j][k]), u = f2_add(u, g[k]);
-      }
-      const float2 v = team_sum(s, u);
-      const f2 mu = f2_splat(-v.x * P.inv_cols);
-      mg = v.y * P.inv_cols;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          xv[j][k] = f2_add(xv[j][k], mu);
-          if (!group(j).has(2 * k)) xv[j][k].x = 0.0f;
-          if (!group(j).has(2 * k + 1)) xv[j][k].y = 0.0f;
-        }
-    }
-    f2 s{0.0f, 0.0f}, u{0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      f2 g[4];
-      gated(j, g);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s = f2_fma(xv[j][k], xv[j][k], s), u = f2_fma(xv[j][k], g[k], u);
-    }
-    const float2 v = team_sum(s, u);
-    const float rd = 1.0f / sqrtf(v.x * P.inv_cols + P.eps);
-    const f2 rd2 = f2_splat(rd), m2 = f2_splat(-(v.y * rd * P.inv_cols)), nmg = f2_splat(-mg);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      f2 g[4];
-      gated(j, g);
-      float o[8];
+      const float mu = warp_sum(f2_add(f2_add(xv[0], xv[1]), f2_add(xv[2], xv[3]))) * P.inv_cols;
+      mg = warp_sum(f2_add(f2_add(g[0], g[1]), f2_add(g[2], g[3]))) * P.inv_cols;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const f2 xh = f2_mul(xv[j][k], rd2);
-        dg[j][k] = f2_fma(cv[j][k], xh, dg[j][k]);
-        if (LAYER) db[j][k] = f2_add(db[j][k], cv[j][k]);
-        const f2 y = f2_mul(f2_fma(xh, m2, LAYER ? f2_add(g[k], nmg) : g[k]), rd2);
-        o[2 * k] = y.x, o[2 * k + 1] = y.y;
+        xv[k] = f2_add(xv[k], f2_splat(-mu));
+        if (!cols.has(2 * k)) xv[k].x = 0.0f;
+        if (!cols.has(2 * k + 1)) xv[k].y = 0.0f;
       }
-      group(j).template store<TY>(P.dx, r * P.ldd, o);
     }
+    f2 a = zero, b = zero;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a = f2_fma(xv[k], xv[k], a), b = f2_fma(xv[k], g[k], b);
+    const float rd = rsqrt_newton(warp_sum(a) * P.inv_cols + P.eps);
+    const f2 rd2 = f2_splat(rd), m2 = f2_splat(-(warp_sum(b) * rd * P.inv_cols)), nmg = f2_splat(-mg);
+    float o[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const f2 xh = f2_mul(xv[k], rd2);
+      dg[k] = f2_fma(cv[k], xh, dg[k]);
+      if (LAYER) db[k] = f2_add(db[k], cv[k]);
+      const f2 y = f2_mul(f2_fma(xh, m2, LAYER ? f2_add(g[k], nmg) : g[k]), rd2);
+      o[2 * k] = y.x, o[2 * k + 1] = y.y;
+    }
+    cols.template store<TY>(P.dx, r * P.ldd, o);
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!P.dgamma && !P.dbeta) return;
-  // The CTA's column sums: its teams' in turn, through shared memory.
-  float* colsum = smem + NV * 8 * T;
 #pragma unroll
-  for (int which = 0; which < (LAYER ? 2 : 1); ++which) {
-    float* part = P.part + ((int64_t)which * P.blocks + blockIdx.x) * P.pcols;
-    for (int q = 0; q < Q.teams; ++q) {
-      if (q > 0) __syncthreads();
-      if (team == q) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (!group(j).has(k)) continue;
-            const int64_t col = group(j).col(k);
-            const f2 d = which == 0 ? dg[j][k / 2] : db[LAYER ? j : 0][k / 2];
-            float a = k & 1 ? d.y : d.x;
-            if (q > 0) a += colsum[col];
-            if (q + 1 == Q.teams) part[col] = a;
-            else colsum[col] = a;
-          }
-      }
+  for (int k = 0; k < 8; ++k)
+    if (cols.has(k)) {
+      colsum[0][warp][cols.col(k)] = k & 1 ? dg[k / 2].y : dg[k / 2].x;
+      if (LAYER) colsum[1][warp][cols.col(k)] = k & 1 ? db[k / 2].y : db[k / 2].x;
     }
-    if (Q.teams > 1) __syncthreads();
+  __syncthreads();
+  if (threadIdx.x < P.cols) {
+#pragma unroll
+    for (int which = 0; which < (LAYER ? 2 : 1); ++which) {
+      float s = colsum[which][0][threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < NB_WARPS; ++w) s += colsum[which][w][threadIdx.x];
+      P.part[((int64_t)which * P.blocks + blockIdx.x) * P.pcols + threadIdx.x] = s;
+    }
   }
 }
 
 // ----------------------------------------------------------- the ring kernel
 //
-// The same pass for rows of one storage type of 256 to 16384 columns that are
-// 16-byte aligned: x and ct rows are copied by TMA into a ring of shared
+// The same pass for rows of one storage type of 256 to 16384 columns: x and ct rows are copied by TMA into a ring of shared
 // memory, several rows ahead (what keeps HBM busy: registers alone hold too
 // few bytes in flight), and read from there for each reduction and for dx; a
 // team's threads keep only their columns' dgamma and dbeta sums in registers.
@@ -354,29 +288,27 @@ struct NormRingParams {
   int32_t row_bytes;         // of x and of ct; a slot holds one of each
 };
 
-// 1 / sqrt(v) by the unit's approximation and one Newton step (about one ulp;
-// v = 0 gives +inf, NaN and negative v NaN, as the division would).
-__device__ __forceinline__ float rsqrt_newton(float v) {
-  const float y = rsqrtf(v);
-  const float h = 0.5f * v * y;
-  const float z = fmaf(y, fmaf(-h, y, 0.5f), y);
-  return v > 0.0f && v < INFINITY ? z : y;
-}
-
-template <int TY, int KIND, int NV, int T>
+// VEC: 16-byte aligned rows of whole 16-byte groups; group j of thread t begins
+// at element (j T + t) E.  Else any rows: TMA copies a row's part between its
+// first and last 16-byte boundary, the few elements outside come from global
+// memory, and element k of group j is column (j 8 + k) T + t (the threads'
+// columns must not move with a row's alignment, and neighbouring threads then
+// read neighbouring elements).
+template <int TY, int KIND, int NV, int T, bool VEC>
 __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __grid_constant__ NormRingParams Q) {
-  // gamma in f32 as the threads read it (later the column sums), then the ring.
+  // gamma in f32 as the threads read it, then the ring.
   extern __shared__ __align__(128) unsigned char ring_smem[];
   __shared__ uint64_t full[RING_MAX_SLOTS], empty[RING_MAX_SLOTS];
   __shared__ __align__(16) float red[2][3][RING_THREADS / 32];
   __shared__ volatile int abort_flag;
   constexpr bool LAYER = KIND == PSK_NORM_LAYER;
-  constexpr int E = TY == PSK_BF16 ? 8 : 4;              // elements of a 16-byte group
+  constexpr int ESZ = TY == PSK_BF16 ? 2 : 4;
+  constexpr int E = VEC ? 16 / ESZ : 8;                  // elements of a group
   constexpr int NG = NV * 8 / E;                         // groups of a thread
-  const NormBwdParams& P = Q.B;
   constexpr int TEAMS = RING_THREADS / T, nw = T / 32;
+  const NormBwdParams& P = Q.B;
   const int tid = threadIdx.x, slots = Q.slots;
-  const int groups = (int)P.cols / E;
+  const int cols = (int)P.cols, groups = VEC ? cols / E : 0;
   float* gamma = (float*)ring_smem;
   unsigned char* ring = ring_smem + (size_t)(NG * E * T) * 4;
   const int slot_bytes = 2 * Q.row_bytes;
@@ -386,12 +318,12 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
     abort_flag = 0;
     fence_barrier_init();
   }
-  // gamma of group j of thread t: float4 number (j E / 4 + i) T + t, i < E / 4.
+  // VEC: gamma of group j of thread t is float4 number (j E / 4 + i) T + t, i < E / 4.
   for (int i = tid; i < NG * E * T; i += RING_THREADS) {
     const int at = i >> 2, who = at % T, piece = at / T;
-    const int64_t c = ((int64_t)(piece * 4 / E) * T + who) * E + (piece * 4) % E + (i & 3);
+    const int c = VEC ? ((piece * 4 / E) * T + who) * E + (piece * 4) % E + (i & 3) : i;
     float g = 1.0f;
-    if (P.gamma && c < P.cols)
+    if (P.gamma && c < cols)
       g = P.param_dtype == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)P.gamma)[c]) : ((const float*)P.gamma)[c];
     gamma[i] = g;
   }
@@ -403,14 +335,29 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
   bool dead = false;
   int flip = 0, issued = -1;
   const long long drop = g_pipe_drop_row;
+  // The elements of a row before its first 16-byte boundary and before its last.
+  struct Span {
+    int head, lim;
+  };
+  auto span_of = [&](const unsigned char* row) {
+    if constexpr (VEC) return Span{0, cols};
+    const int off = (int)((uintptr_t)row & 15u) / ESZ, per = 16 / ESZ;
+    int head = off ? per - off : 0;
+    if (head > cols) head = cols;
+    return Span{head, head + (cols - head) / per * per};
+  };
+  auto x_row = [&](int i) { return (const unsigned char*)P.x + (blockIdx.x + (int64_t)i * gridDim.x) * P.ldx * ESZ; };
+  auto c_row = [&](int i) { return (const unsigned char*)P.ct + (blockIdx.x + (int64_t)i * gridDim.x) * P.ldc * ESZ; };
   // The team's first thread copies local row i into its slot s.
   auto fetch = [&](int i, int s) {
     if (t != 0 || i >= n_local || dead || (drop >= 0 && i >= drop)) return;
-    const int64_t r = blockIdx.x + (int64_t)i * gridDim.x;
     unsigned char* at = ring + (size_t)s * slot_bytes;
-    mbar_arrive_expect_tx(&full[s], (uint32_t)slot_bytes);
-    bulk_copy_g2s(at, (const unsigned char*)P.x + r * P.ldx * (16 / E), (uint32_t)Q.row_bytes, &full[s]);
-    bulk_copy_g2s(at + Q.row_bytes, (const unsigned char*)P.ct + r * P.ldc * (16 / E), (uint32_t)Q.row_bytes, &full[s]);
+    const unsigned char *x = x_row(i), *c = c_row(i);
+    const Span sx = span_of(x), sc = span_of(c);
+    const uint32_t nx = (uint32_t)(sx.lim - sx.head) * ESZ, nc = (uint32_t)(sc.lim - sc.head) * ESZ;
+    mbar_arrive_expect_tx(&full[s], nx + nc);
+    if (VEC || nx > 0) bulk_copy_g2s(at, x + sx.head * ESZ, nx, &full[s]);
+    if (VEC || nc > 0) bulk_copy_g2s(at + Q.row_bytes, c + sc.head * ESZ, nc, &full[s]);
     issued = i;
   };
   // Sums over the team, one barrier (the buffers alternate).
@@ -421,7 +368,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
       if (q >= n) break;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v[q] += __shfl_xor_sync(0xFFFFFFFFu, v[q], o);
-      if (lane == 0) red[flip][q][warp] = v[q];
+      if (nw > 1 && lane == 0) red[flip][q][warp] = v[q];
     }
     if (nw == 1) return;
     named_barrier(1 + team, T);
@@ -430,7 +377,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
       if (q >= n) break;
       const float2* p = (const float2*)&red[flip][q][team * nw];     // nw: 2, 4, 8 or 16
       float2 s = p[0];
-      #pragma unroll
+#pragma unroll
       for (int w = 1; w < nw / 2; ++w) {
         const float2 u = p[w];
         s.x += u.x, s.y += u.y;
@@ -448,6 +395,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
       dg[j][k] = zero;
       if (LAYER) db[j][k] = zero;
     }
+  // Whether the thread has a group (VEC), or the team a column of the group's element k.
+  auto no_group = [&](int j) { return VEC ? j * T + t >= groups : j * 8 * T >= cols; };
+  auto absent = [&](int j, int k) { return !VEC && (j * 8 + k + 1) * T > cols && (j * 8 + k) * T + t >= cols; };
   int s = team, before = 0;                  // the row's slot, the last row's
   uint32_t parity = 0, parity_before = 0;    // of their phases
   for (int i = team; i < n_local; i += TEAMS) {
@@ -460,21 +410,51 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
     if (!dead && !mbar_wait(&full[s], parity)) { abort_flag = 1; dead = true; }
     const unsigned char* xs = ring + (size_t)s * slot_bytes;
     const unsigned char* cs = xs + Q.row_bytes;
-    auto values = [&](const unsigned char* p, int j, f2* v) {
-      const uint4 u = *(const uint4*)(p + (size_t)(j * T + t) * 16);
-      if constexpr (TY == PSK_BF16) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const unsigned char *xg = VEC ? nullptr : x_row(i), *cg = VEC ? nullptr : c_row(i);
+    const Span xspan = VEC ? Span{0, cols} : span_of(xg), cspan = VEC ? Span{0, cols} : span_of(cg);
+    auto element = [&](const unsigned char* p) {
+      return ESZ == 2 ? bf16_bits_to_f32(*(const uint16_t*)p) : *(const float*)p;
+    };
+    // Group j of x or ct, widened; columns past the row's end are 0.
+    auto values = [&](const unsigned char* p, const unsigned char* row, const Span& at, int j, f2* v) {
+      if constexpr (VEC) {
+        const uint4 u = *(const uint4*)(p + (size_t)(j * T + t) * 16);
+        if constexpr (TY == PSK_BF16) {
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = f2{__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)};
+          for (int k = 0; k < 4; ++k) v[k] = f2{__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)};
+        } else {
+          v[0] = f2{__uint_as_float(u.x), __uint_as_float(u.y)}, v[1] = f2{__uint_as_float(u.z), __uint_as_float(u.w)};
+        }
       } else {
-        v[0] = f2{__uint_as_float(u.x), __uint_as_float(u.y)}, v[1] = f2{__uint_as_float(u.z), __uint_as_float(u.w)};
+        const int c0 = j * 8 * T;
+        if (c0 >= at.head && c0 + 8 * T <= at.lim) {      // all from shared memory
+          const unsigned char* q = p + (c0 + t - at.head) * ESZ;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = f2{element(q + 2 * k * T * ESZ), element(q + (2 * k + 1) * T * ESZ)};
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int c = c0 + k * T + t;
+            float e = 0.0f;
+            if (c < cols) e = c < at.head || c >= at.lim ? element(row + (int64_t)c * ESZ) : element(p + (c - at.head) * ESZ);
+            if (k & 1) v[k / 2].y = e;
+            else v[k / 2].x = e;
+          }
+        }
       }
     };
     auto gate = [&](int j, f2* g) {
+      if constexpr (VEC) {
 #pragma unroll
-      for (int q = 0; q < E / 4; ++q) {
-        const float4 a = ((const float4*)gamma)[(j * (E / 4) + q) * T + t];
-        g[2 * q] = f2_mul(g[2 * q], f2{a.x, a.y}), g[2 * q + 1] = f2_mul(g[2 * q + 1], f2{a.z, a.w});
+        for (int q = 0; q < E / 4; ++q) {
+          const float4 a = ((const float4*)gamma)[(j * (E / 4) + q) * T + t];
+          g[2 * q] = f2_mul(g[2 * q], f2{a.x, a.y}), g[2 * q + 1] = f2_mul(g[2 * q + 1], f2{a.z, a.w});
+        }
+      } else {
+        const float* q = gamma + j * 8 * T + t;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) g[k] = f2_mul(g[k], f2{q[2 * k * T], q[(2 * k + 1) * T]});
       }
     };
     float sums[3];
@@ -484,9 +464,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
       if (!dead) {
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-          if (j * T + t >= groups) continue;
+          if (no_group(j)) continue;
           f2 x[E / 2];
-          values(xs, j, x);
+          values(xs, xg, xspan, j, x);
 #pragma unroll
           for (int k = 0; k < E / 2; ++k) a = f2_add(a, x[k]);
         }
@@ -498,24 +478,34 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
       mu = sums[0] * P.inv_cols;
     }
     const f2 nmu = f2_splat(-mu);
+    // x - mu, 0 past the row's end.
+    auto centre = [&](int j, f2* x) {
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        x[k] = f2_add(x[k], nmu);
+        if (absent(j, 2 * k)) x[k].x = 0.0f;
+        if (absent(j, 2 * k + 1)) x[k].y = 0.0f;
+      }
+    };
     constexpr bool KEEP = !LAYER;            // widened values stay in registers for dx
     f2 kx[KEEP ? NG : 1][E / 2], kc[KEEP ? NG : 1][E / 2];
     f2 a = zero, b = zero, d = zero;
     if (!dead) {
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
-        if (j * T + t >= groups) continue;
+        if (no_group(j)) continue;
         f2 x[E / 2], g[E / 2];
-        values(xs, j, x);
-        values(cs, j, g);
+        values(xs, xg, xspan, j, x);
+        values(cs, cg, cspan, j, g);
         if (KEEP) {
 #pragma unroll
           for (int k = 0; k < E / 2; ++k) kx[KEEP ? j : 0][k] = x[k], kc[KEEP ? j : 0][k] = g[k];
         }
         gate(j, g);
+        if (LAYER) centre(j, x);
 #pragma unroll
         for (int k = 0; k < E / 2; ++k) {
-          if (LAYER) x[k] = f2_add(x[k], nmu), d = f2_add(d, g[k]);
+          if (LAYER) d = f2_add(d, g[k]);
           a = f2_fma(x[k], x[k], a), b = f2_fma(x[k], g[k], b);
         }
       }
@@ -528,31 +518,43 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
     if (!dead) {
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
-        if (j * T + t >= groups) continue;
+        if (no_group(j)) continue;
         f2 x[E / 2], c[E / 2], g[E / 2], y[E / 2];
         if (KEEP) {
 #pragma unroll
           for (int k = 0; k < E / 2; ++k) x[k] = kx[KEEP ? j : 0][k], c[k] = kc[KEEP ? j : 0][k];
         } else {
-          values(xs, j, x);
-          values(cs, j, c);
+          values(xs, xg, xspan, j, x);
+          values(cs, cg, cspan, j, c);
+          centre(j, x);
         }
 #pragma unroll
         for (int k = 0; k < E / 2; ++k) g[k] = c[k];
         gate(j, g);
 #pragma unroll
         for (int k = 0; k < E / 2; ++k) {
-          const f2 xh = f2_mul(LAYER ? f2_add(x[k], nmu) : x[k], rd2);
+          const f2 xh = f2_mul(x[k], rd2);
           dg[j][k] = f2_fma(c[k], xh, dg[j][k]);
           if (LAYER) db[j][k] = f2_add(db[j][k], c[k]);
           y[k] = f2_mul(f2_fma(xh, m2, LAYER ? f2_add(g[k], nmg) : g[k]), rd2);
         }
-        unsigned char* o = (unsigned char*)P.dx + r * P.ldd * (16 / E) + (size_t)(j * T + t) * 16;
-        if constexpr (TY == PSK_BF16)
-          *(uint4*)o = make_uint4(f32x2_to_bf16x2(y[0].x, y[0].y), f32x2_to_bf16x2(y[1].x, y[1].y),
-                                  f32x2_to_bf16x2(y[2].x, y[2].y), f32x2_to_bf16x2(y[3].x, y[3].y));
-        else
-          *(float4*)o = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+        if constexpr (VEC) {
+          unsigned char* o = (unsigned char*)P.dx + r * P.ldd * ESZ + (size_t)(j * T + t) * 16;
+          if constexpr (TY == PSK_BF16)
+            *(uint4*)o = make_uint4(f32x2_to_bf16x2(y[0].x, y[0].y), f32x2_to_bf16x2(y[1].x, y[1].y),
+                                    f32x2_to_bf16x2(y[2].x, y[2].y), f32x2_to_bf16x2(y[3].x, y[3].y));
+          else
+            *(float4*)o = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float e = k & 1 ? y[k / 2].y : y[k / 2].x;
+            const int64_t at = r * P.ldd + (j * 8 + k) * T + t;
+            if (absent(j, k)) continue;
+            if constexpr (TY == PSK_BF16) ((uint16_t*)P.dx)[at] = f32_to_bf16_bits(e);
+            else ((float*)P.dx)[at] = e;
+          }
+        }
       }
     }
     __syncwarp();
@@ -567,29 +569,51 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
       mbar_wait(&full[i % slots], (uint32_t)(i / slots) & 1u);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!P.dgamma && !P.dbeta) return;
-  // The CTA's column sums, its teams' in turn, in gamma's place.
+  // The CTA's column sums: the teams' side by side in the ring, now free (its two
+  // rows a team are at least as large), then
+  // added in order, four (VEC) neighbouring columns or one a thread.
+  constexpr int WIDE = NG * E * T;
+  float* side = (float*)ring;
 #pragma unroll
   for (int which = 0; which < (LAYER ? 2 : 1); ++which) {
     float* part = P.part + ((int64_t)which * P.blocks + blockIdx.x) * P.pcols;
-    for (int q = 0; q < TEAMS; ++q) {
-      if (TEAMS > 1) named_barrier(15, RING_THREADS);
-      if (team != q) continue;
+    named_barrier(15, RING_THREADS);
 #pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        if (j * T + t >= groups) continue;
+    for (int j = 0; j < NG; ++j)
 #pragma unroll
-        for (int h = 0; h < E / 4; ++h) {
-          const f2 a = which == 0 ? dg[j][2 * h] : db[LAYER ? j : 0][2 * h];
-          const f2 b = which == 0 ? dg[j][2 * h + 1] : db[LAYER ? j : 0][2 * h + 1];
-          float4 sum = make_float4(a.x, a.y, b.x, b.y);
-          float4* held = (float4*)gamma + (j * (E / 4) + h) * T + t;
-          if (q > 0) {
-            const float4 u = *held;
-            sum.x += u.x, sum.y += u.y, sum.z += u.z, sum.w += u.w;
-          }
-          if (q + 1 == TEAMS) *(float4*)(part + (j * T + t) * E + 4 * h) = sum;
-          else *held = sum;
+      for (int k = 0; k < E / 2; k += 2) {
+        const f2 a = which == 0 ? dg[j][k] : db[LAYER ? j : 0][k];
+        const f2 b = which == 0 ? dg[j][k + 1] : db[LAYER ? j : 0][k + 1];
+        if constexpr (VEC) {
+          ((float4*)side)[(team * WIDE) / 4 + (j * (E / 4) + k / 2) * T + t] = make_float4(a.x, a.y, b.x, b.y);
+        } else {
+          const int c = (j * 8 + 2 * k) * T + t;
+          float* at = side + team * cols + c;
+          if (c < cols) at[0] = a.x;
+          if (c + T < cols) at[T] = a.y;
+          if (c + 2 * T < cols) at[2 * T] = b.x;
+          if (c + 3 * T < cols) at[3 * T] = b.y;
         }
+      }
+    named_barrier(15, RING_THREADS);
+    if constexpr (VEC) {
+      for (int q = tid; q < WIDE / 4; q += RING_THREADS) {
+        const int c = ((q / T * 4 / E) * T + q % T) * E + (q / T * 4) % E;
+        if (c >= cols) continue;
+        float4 s = ((const float4*)side)[q];
+#pragma unroll
+        for (int m = 1; m < TEAMS; ++m) {
+          const float4 u = ((const float4*)side)[m * (WIDE / 4) + q];
+          s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
+        }
+        *(float4*)(part + c) = s;
+      }
+    } else {
+      for (int c = tid; c < cols; c += RING_THREADS) {
+        float s = side[c];
+#pragma unroll
+        for (int m = 1; m < TEAMS; ++m) s += side[m * cols + c];
+        part[c] = s;
       }
     }
   }
@@ -651,44 +675,40 @@ static int norm_bwd_blocks(int64_t rows, int64_t cols) {
   return (int)(b < 1 ? 1 : b > NB_MAX_BLOCKS ? NB_MAX_BLOCKS : b);
 }
 
-// The fused kernel's shape: teams of the fewest threads that hold a row in
-// one or two groups of eight columns each.
-struct FusedShape {
-  int team, teams, nv, cta;
-};
-static FusedShape fused_shape(int64_t cols) {
-  FusedShape f{32, 1, 1, 256};
-  const int64_t groups = (cols + 7) / 8;
-  while (f.team < 256 && f.team < groups) f.team *= 2;
-  if (groups > 256) f.nv = 2;
-  if (groups > 512) f.team = f.cta = 512;
-  f.teams = f.cta / f.team;
-  return f;
-}
-
-// Most CTAs of the fused kernel (two of 256 threads an SM, or one of 512, on
-// 160 SMs), at least NB_ROWS_PER_TEAM rows for each team.
-static int fused_blocks(int64_t rows, int64_t cols) {
-  const FusedShape f = fused_shape(cols);
-  const int64_t most = 160 * (512 / f.cta), want = (rows + f.teams * NB_ROWS_PER_TEAM - 1) / (f.teams * NB_ROWS_PER_TEAM);
-  return (int)(want < most ? want : most);
+// CTAs of the warp-a-row kernel: four an SM on 160 SMs at most, at least
+// NB_ROWS_PER_WARP rows a warp.
+static int warps_blocks(int64_t rows) {
+  const int64_t want = (rows + NB_WARPS * NB_ROWS_PER_WARP - 1) / (NB_WARPS * NB_ROWS_PER_WARP);
+  return (int)(want < 640 ? want : 640);
 }
 
 // The ring kernel's shape for rows of this size, or false: teams of the fewest
-// threads that hold a row's column sums in two (up to 512 columns) or four
-// groups of eight a thread -- wide threads share a row's shuffles and barrier
-// among more columns, and small teams overlap more rows -- and as many slots
-// as fit, two rows a team at least.
-static bool ring_shape(NormRingParams& Q, int* nv, int32_t dt, int64_t cols) {
-  if (cols < 256 || cols > RING_MAX_COLS || cols % 8 != 0) return false;
-  *nv = cols <= 512 ? 2 : 4;
-  Q.team = 32;
-  while (Q.team * *nv * 8 < cols) Q.team *= 2;
-  Q.teams = RING_THREADS / Q.team;
-  Q.row_bytes = (int32_t)cols * dtype_size(dt);
-  const int fits = (RING_SMEM - *nv * 8 * Q.team * 4) / (2 * Q.row_bytes);
-  Q.slots = (fits < RING_MAX_SLOTS ? fits : RING_MAX_SLOTS) / Q.teams * Q.teams;
-  return Q.slots >= 2 * Q.teams;
+// threads that hold a row's column sums in four groups of eight (two for rows
+// of up to 512 columns, and where four leave no two rows a team: f32 rows) --
+// wide threads share a row's shuffles and barrier among more columns, and
+// small teams overlap more rows.
+static bool ring_shape(NormRingParams& Q, int* nv, int32_t dt, int32_t kind, bool vec, int64_t cols) {
+  if (cols <= NB_FUSED_COLS || cols > RING_MAX_COLS) return false;
+  Q.row_bytes = (int32_t)((cols * dtype_size(dt) + 15) / 16 * 16);
+  for (*nv = vec && cols > 512 ? 4 : vec ? 2 : 4; *nv >= 2; *nv -= 2) {
+    Q.team = 32;
+    while (Q.team * *nv * 8 < cols) Q.team *= 2;
+    if (Q.team > RING_THREADS) return false;
+    Q.teams = RING_THREADS / Q.team;
+    int fits = (RING_SMEM - *nv * 8 * Q.team * 4) / (2 * Q.row_bytes);
+    if (fits > RING_MAX_SLOTS) fits = RING_MAX_SLOTS;
+    // RMSNorm is held to about 128 KB in flight: more reads ahead cost it DRAM
+    // time ([32768, 4096] bf16: 133 us with 128 KB, 146 with 192); LayerNorm's
+    // two barriers want all there is (134 us with 192 KB, 141 with 128).
+    if (kind == PSK_NORM_RMS) {
+      const int enough = (128 * 1024) / (2 * Q.row_bytes), least = (Q.teams <= 2 ? 3 : 2) * Q.teams;
+      if (fits > enough && fits > least) fits = enough > least ? enough : least;
+    }
+    Q.slots = fits / Q.teams * Q.teams;
+    if (Q.slots >= 2 * Q.teams) return true;
+    if (!vec) return false;
+  }
+  return false;
 }
 
 static uint64_t norm_bwd_layout(int64_t rows, int64_t cols, uint64_t* part) {
@@ -696,37 +716,38 @@ static uint64_t norm_bwd_layout(int64_t rows, int64_t cols, uint64_t* part) {
   const uint64_t pcols = (uint64_t)(cols + 7) / 8 * 8;
   *part = stats;
   int blocks = norm_bwd_blocks(rows, cols);
-  if (cols <= NB_FUSED_COLS && fused_blocks(rows, cols) > blocks) blocks = fused_blocks(rows, cols);
+  if (cols <= NB_FUSED_COLS && warps_blocks(rows) > blocks) blocks = warps_blocks(rows);
   const int64_t ring = rows < RING_MAX_BLOCKS ? rows : RING_MAX_BLOCKS;
-  if (ring > blocks) blocks = (int)ring;
+  if (cols > NB_FUSED_COLS && ring > blocks) blocks = (int)ring;
   return stats + 2ull * blocks * pcols * 4;
 }
 
-template <int TY, int KIND, bool VEC, int NV, int CTA>
-static void fused_launch(const NormFusedParams& Q, cudaStream_t s) {
-  norm_bwd_fused_kernel<TY, KIND, VEC, NV, CTA>
-      <<<(unsigned)Q.B.blocks, CTA, (size_t)(NV * 8 * Q.team + (Q.teams > 1 ? Q.B.cols : 0)) * 4, s>>>(Q);
-}
-
-template <int TY, int KIND, int NV, int T>
+template <int TY, int KIND, int NV, int T, bool VEC>
 static int ring_launch_team(const NormRingParams& Q, cudaStream_t s) {
   static bool limit[PSK_MAX_DEVICES] = {};
-  smem_limit_once((const void*)norm_bwd_ring_kernel<TY, KIND, NV, T>, RING_SMEM, limit);
+  smem_limit_once((const void*)norm_bwd_ring_kernel<TY, KIND, NV, T, VEC>, RING_SMEM, limit);
   const size_t smem = (size_t)NV * 8 * T * 4 + (size_t)Q.slots * 2 * Q.row_bytes;
-  norm_bwd_ring_kernel<TY, KIND, NV, T><<<(unsigned)Q.B.blocks, RING_THREADS, smem, s>>>(Q);
+  norm_bwd_ring_kernel<TY, KIND, NV, T, VEC><<<(unsigned)Q.B.blocks, RING_THREADS, smem, s>>>(Q);
   return check_launch("norm backward ring kernel");
 }
 
-template <int TY, int KIND>
-static int ring_launch(const NormRingParams& Q, int nv, cudaStream_t s) {
-  if (nv == 2) return ring_launch_team<TY, KIND, 2, 32>(Q, s);
+template <int TY, int KIND, int NV, bool VEC>
+static int ring_launch_shape(const NormRingParams& Q, cudaStream_t s) {
   switch (Q.team) {
-    case 32: return ring_launch_team<TY, KIND, 4, 32>(Q, s);
-    case 64: return ring_launch_team<TY, KIND, 4, 64>(Q, s);
-    case 128: return ring_launch_team<TY, KIND, 4, 128>(Q, s);
-    case 256: return ring_launch_team<TY, KIND, 4, 256>(Q, s);
-    default: return ring_launch_team<TY, KIND, 4, 512>(Q, s);
+    case 32: return ring_launch_team<TY, KIND, NV, 32, VEC>(Q, s);
+    case 64: return ring_launch_team<TY, KIND, NV, 64, VEC>(Q, s);
+    case 128: return ring_launch_team<TY, KIND, NV, 128, VEC>(Q, s);
+    case 256: return ring_launch_team<TY, KIND, NV, 256, VEC>(Q, s);
+    default: return ring_launch_team<TY, KIND, NV, 512, VEC>(Q, s);
   }
+}
+
+template <int TY, int KIND>
+static int ring_launch(const NormRingParams& Q, int nv, bool vec, cudaStream_t s) {
+  if (!vec) return ring_launch_shape<TY, KIND, 4, false>(Q, s);
+  if (nv == 4) return ring_launch_shape<TY, KIND, 4, true>(Q, s);
+  if constexpr (TY == PSK_F32) return ring_launch_shape<TY, KIND, 2, true>(Q, s);
+  else return ring_launch_team<TY, KIND, 2, 32, true>(Q, s);
 }
 
 int norm_bwd_status(unsigned int* v, bool reset) {
@@ -849,38 +870,33 @@ extern "C" int psk_norm_backward(const void* x, int32_t xt, const void* ct, int3
                    (!gamma || rows_vec8(gamma, param_dtype, cols, 1));
   NormRingParams G{};
   int nv = 0;
-  if (vec && xt == ct_t && xt == dxt && ring_shape(G, &nv, xt, cols)) {
+  const bool one_type = xt == ct_t && xt == dxt;
+  if (one_type && ring_shape(G, &nv, xt, kind, vec, cols)) {
     G.B = P;
-    int64_t blocks = (rows + G.teams - 1) / G.teams;
+    const int64_t blocks = (rows + G.teams - 1) / G.teams;
     const int64_t sms = device_sm_count() < RING_MAX_BLOCKS ? device_sm_count() : RING_MAX_BLOCKS;
     G.B.blocks = (int)(blocks < sms ? blocks : sms);
     rc = with_dtype(xt, [&](auto TY) {
       return with_bool(kind == PSK_NORM_LAYER, [&](auto LAYER) {
-        constexpr int KIND = LAYER.value ? PSK_NORM_LAYER : PSK_NORM_RMS;
-        return ring_launch<TY.value, KIND>(G, nv, s);
+        return ring_launch<TY.value, LAYER.value ? PSK_NORM_LAYER : PSK_NORM_RMS>(G, nv, vec, s);
       });
     });
     return rc || (!dgamma && !dbeta) ? rc : norm_bwd_join(G.B, s);
   }
-  if (cols <= NB_FUSED_COLS && xt == ct_t && xt == dxt) {
-    const FusedShape f = fused_shape(cols);
-    NormFusedParams Q{P, f.team, f.teams};
-    const int64_t resident = (int64_t)device_sm_count() * (512 / f.cta);
-    Q.B.blocks = fused_blocks(rows, cols);
-    if (Q.B.blocks > resident) Q.B.blocks = (int)resident;
+  if (one_type && cols <= NB_FUSED_COLS) {
+    P.blocks = warps_blocks(rows);
+    if (P.blocks > 4 * device_sm_count()) P.blocks = 4 * device_sm_count();
     with_dtype(xt, [&](auto TY) {
       return with_bool(kind == PSK_NORM_LAYER, [&](auto LAYER) {
-        constexpr int KIND = LAYER.value ? PSK_NORM_LAYER : PSK_NORM_RMS;
         return with_bool(vec, [&](auto VEC) {
-          if (f.cta == 512) fused_launch<TY.value, KIND, VEC.value, 2, 512>(Q, s);
-          else if (f.nv == 2) fused_launch<TY.value, KIND, VEC.value, 2, 256>(Q, s);
-          else fused_launch<TY.value, KIND, VEC.value, 1, 256>(Q, s);
+          norm_bwd_warps_kernel<TY.value, LAYER.value ? PSK_NORM_LAYER : PSK_NORM_RMS, VEC.value>
+              <<<(unsigned)P.blocks, NB_THREADS, 0, s>>>(P);
           return 0;
         });
       });
     });
-    rc = check_launch("norm backward fused kernel");
-    return rc || (!dgamma && !dbeta) ? rc : norm_bwd_join(Q.B, s);
+    rc = check_launch("norm backward warp-a-row kernel");
+    return rc || (!dgamma && !dbeta) ? rc : norm_bwd_join(P, s);
   }
   const int64_t most = (int64_t)device_sm_count() * 8;
   const unsigned rgrid = (unsigned)(rows < most ? rows : most);
