@@ -272,16 +272,20 @@ __global__ void __launch_bounds__(LOSS_THREADS) loss_rows_kernel(const __grid_co
 // eight for rows of up to 8 x 72 KB or to spread a call of few rows), and
 // stays there for the sums and for the gradient, which goes straight to
 // memory: the floor of one read and one write per logit.  A producer warp
-// keeps the ring of slices full (rows ahead of the consumers), and hands each
-// row's scalars along with it.  Teams of consumer warps take rows in turn, so
+// keeps the ring of slices full, and hands each row's scalars along with it.
+// Teams of consumer warps take rows in turn, each with slots of its own, so
 // that one team's barriers and scalar section (logarithm, ratio, KL term)
-// overlap another's exponentials; the CTAs of a cluster exchange their
-// slices' maxima and sums through distributed shared memory.
+// overlap another's exponentials.  A slot is filled and freed in up to four
+// chunks: the sums begin with the first chunk, and the next row's copy with
+// the first chunk whose gradient is written.  The CTAs of a cluster exchange
+// their slices' maxima and sums through distributed shared memory.
 
-constexpr int RES_CONSUMERS = 576;             // at most (teams of 32 to 512 threads)
+constexpr int RES_CONSUMERS = 768;             // teams of 32 to 512 threads
 constexpr int RES_THREADS = RES_CONSUMERS + 32;
-constexpr int RES_MAX_TEAMS = 16;
+constexpr int RES_MAX_TEAMS = 24;
 constexpr int RES_MAX_SLOTS = 32;
+constexpr int RES_MAX_CHUNKS = 4;
+constexpr int RES_MAX_BARS = 32;               // slots x chunks
 constexpr int RES_MAX_CLUSTER = 8;
 constexpr int RES_SMEM = 216 * 1024;          // ring
 constexpr int RES_SLICE = 72 * 1024;          // largest slice: three in the ring
@@ -290,6 +294,7 @@ struct ResParams {
   LossParams L;
   int32_t slice_groups;     // 16-byte groups of a CTA's slice (the last may be short)
   int32_t slots, slot_bytes;
+  int32_t chunks, chunk_groups;  // of a slot
   int32_t team_threads, teams;   // slots is a multiple of teams: a slot's phases are all one team's, which
                                  // visits them in order (a parity wait must never run ahead of its barrier)
   int32_t cluster;
@@ -302,7 +307,7 @@ struct RowInfo {
 };
 
 struct ResShared {
-  uint64_t full[RES_MAX_SLOTS], empty[RES_MAX_SLOTS];
+  uint64_t full[RES_MAX_BARS], empty[RES_MAX_BARS];      // slot x chunks + chunk
   uint64_t xbar[RES_MAX_TEAMS][2];
   RowInfo info[RES_MAX_SLOTS];
   RowSum red[2][RES_CONSUMERS / 32];            // per warp
@@ -401,12 +406,12 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
   const uint32_t rank = K > 1 ? cluster_rank() : 0;
   const int64_t cid = blockIdx.x / K, ncl = gridDim.x / K;
   const int n_local = cid < L.rows ? (int)((L.rows - 1 - cid) / ncl + 1) : 0;
-  const int slots = P.slots;
+  const int slots = P.slots, chunks = P.chunks, CG = P.chunk_groups;
   const int64_t cols = L.cols;
   const uintptr_t base = (uintptr_t)L.x;
 
   if (tid == 0) {
-    for (int i = 0; i < slots; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], P.team_threads / 32);
+    for (int i = 0; i < slots * chunks; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], P.team_threads / 32);
     for (int t = 0; t < P.teams; ++t) mbar_init(&S.xbar[t][0], K), mbar_init(&S.xbar[t][1], K);
     S.abort_flag = 0;
     fence_barrier_init();
@@ -446,25 +451,28 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
       for (int k = 0; k < 32 && j0 + k < n_local; ++k) {
         const int j = j0 + k, s = j % slots;
         if (lane == k) {
+          const int head = head_of(mine);
+          const int64_t first = (int64_t)rank * P.slice_groups;
+          int64_t n = (cols - head) / G - first;
+          n = n < 0 || !info.live ? 0 : n < P.slice_groups ? n : P.slice_groups;
+          const unsigned char* src = (const unsigned char*)L.x + (mine * L.ldx + head) * ESZ + first * 16;
           bool ok = j != drop && !S.abort_flag;
-          if (ok && j >= slots && !mbar_wait(&S.empty[s], (uint32_t)((j / slots) - 1) & 1u)) {
-            S.abort_flag = 1;
-            ok = false;
+          for (int h = 0; h < chunks && ok; ++h) {
+            const int bar = s * chunks + h;
+            if (j >= slots && !mbar_wait(&S.empty[bar], (uint32_t)((j / slots) - 1) & 1u)) {
+              S.abort_flag = 1;
+              ok = false;
+              break;
+            }
+            if (h == 0) S.info[s] = info;
+            int64_t m = n - (int64_t)h * CG;
+            m = m < 0 ? 0 : m < CG ? m : CG;
+            mbar_arrive_expect_tx(&S.full[bar], (uint32_t)m * 16u);
+            if (m > 0)
+              bulk_copy_g2s(ring + (size_t)s * P.slot_bytes + (size_t)h * CG * 16, src + (size_t)h * CG * 16,
+                            (uint32_t)m * 16u, &S.full[bar]);
           }
-          if (ok) {
-            S.info[s] = info;
-            const int head = head_of(mine);
-            const int64_t body = (cols - head) / G;
-            const int64_t first = (int64_t)rank * P.slice_groups;
-            int64_t n = body - first;
-            n = n < 0 || !info.live ? 0 : n < P.slice_groups ? n : P.slice_groups;
-            mbar_arrive_expect_tx(&S.full[s], (uint32_t)n * 16u);
-            if (n > 0)
-              bulk_copy_g2s(ring + (size_t)s * P.slot_bytes,
-                            (const unsigned char*)L.x + (mine * L.ldx + head) * ESZ + first * 16, (uint32_t)n * 16u,
-                            &S.full[s]);
-            ++issued;
-          }
+          if (ok) ++issued;
           stop = !ok;
         }
         stop = __shfl_sync(0xFFFFFFFFu, stop, k);
@@ -475,7 +483,7 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
     for (int o = 16; o > 0; o >>= 1) issued += __shfl_xor_sync(0xFFFFFFFFu, issued, o);
     if (stop && lane == 0)
       for (int j = issued > slots ? issued - slots : 0; j < issued; ++j)
-        mbar_wait(&S.full[j % slots], (uint32_t)(j / slots) & 1u);
+        for (int h = 0; h < chunks; ++h) mbar_wait(&S.full[j % slots * chunks + h], (uint32_t)(j / slots) & 1u);
   } else {
     // ---------------- teams.  After a timeout (`dead`) a thread skips waits
     // and work but keeps meeting its team's barriers.
@@ -488,8 +496,9 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
       if (TT == 32) __syncwarp();
       else named_barrier(1 + team, TT);
     };
+    int s = team;                                  // the row's slot
+    uint32_t parity = 0;                           // of its phases
     for (int j = team; j < n_local; j += P.teams, ++rows_done) {
-      const int s = j % slots;
       const int64_t r = cid + (int64_t)j * ncl;
       const unsigned char* x = ring + (size_t)s * P.slot_bytes;
       const int head = head_of(r);
@@ -502,34 +511,47 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
                            : tt < 8 ? (tt < head ? tt : -1)
                                     : (tt - 8 < tail ? cols - tail + (tt - 8) : -1);
       dead = dead || S.abort_flag;
-      if (!dead && !mbar_wait(&S.full[s], (uint32_t)(j / slots) & 1u)) { S.abort_flag = 1; dead = true; }
+      uint64_t* full = &S.full[s * chunks];
+      uint64_t* empty = &S.empty[s * chunks];
+      if (!dead && !mbar_wait(full, parity)) { S.abort_flag = 1; dead = true; }
       RowInfo info{};
       if (!dead) info = S.info[s];
       const bool live = !dead && info.live;
       const float xe = live && edge >= 0 ? load1<LT>(L.x, r * L.ldx + edge) : -INFINITY;
 
       RowSum v{-INFINITY, 0.0f, 0.0f};
-      if (live) {
-        f2 sum{0.0f, 0.0f};
-        constexpr int STEP = GroupOf<LT>::PER_STEP;
-        for (int i = tt; i < n; i += STEP * TT) {
-          f2 e[8];
-          float m;
-          load_step<LT>(x, i, n, TT, e, m);
-          if (!(m <= v.m)) {                       // grows, or NaN
-            m = max_nan2(m, v.m);
-            const float f = ex2_approx((v.m - m) * c);
-            sum.x *= f, sum.y *= f;
-            v.m = m;
+      f2 sum{0.0f, 0.0f};
+      for (int h = 0; h < chunks; ++h) {
+        if (h > 0 && !dead && !mbar_wait(full + h, parity)) { S.abort_flag = 1; dead = true; }
+        if (live) {
+          constexpr int STEP = GroupOf<LT>::PER_STEP;
+          const int hi = n < (h + 1) * CG ? n : (h + 1) * CG;
+          for (int i = h * CG + tt; i < hi; i += STEP * TT) {
+            f2 e[8];
+            float m;
+            load_step<LT>(x, i, hi, TT, e, m);
+            if (!(m <= v.m)) {                       // grows, or NaN
+              m = max_nan2(m, v.m);
+              const float f = ex2_approx((v.m - m) * c);
+              sum.x *= f, sum.y *= f;
+              v.m = m;
+            }
+            const f2 nm = f2_splat(v.m == -INFINITY ? 0.0f : -v.m);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) e[q] = f2_mul(f2_add(e[q], nm), f2_splat(c));
+#pragma unroll
+            for (int q = 0; q < 8; ++q) e[q].x = ex2_approx(e[q].x), e[q].y = ex2_approx(e[q].y);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) e[q] = f2_add(e[q], e[q + 4]);
+            sum = f2_add(sum, f2_add(f2_add(e[0], e[1]), f2_add(e[2], e[3])));
           }
-          const f2 nm = f2_splat(v.m == -INFINITY ? 0.0f : -v.m);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) e[q] = f2_mul(f2_add(e[q], nm), f2_splat(c));
-#pragma unroll
-          for (int q = 0; q < 8; ++q) e[q].x = ex2_approx(e[q].x), e[q].y = ex2_approx(e[q].y);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) sum = f2_add(sum, e[q]);
         }
+        if (MODE != LOSS_GRAD) {
+          __syncwarp();
+          if (!dead && lane == 0) mbar_arrive(empty + h);
+        }
+      }
+      if (live) {
         v.s = __fadd_rn(sum.x, sum.y);
         if (edge >= 0) {
           if (!(xe <= v.m)) {
@@ -550,7 +572,6 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
         if (lane == 0) S.red[rows_done & 1][tid >> 5] = v;
       }
       __syncwarp();
-      if (MODE != LOSS_GRAD && !dead && lane == 0) mbar_arrive(&S.empty[s]);
       team_barrier();
       if (tw == 0 && live) {
         v = lane < nw ? S.red[rows_done & 1][team * nw + lane] : RowSum{-INFINITY, 0.0f, 0.0f};
@@ -609,44 +630,49 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
       if (MODE == LOSS_GRAD) {
         team_barrier();
         unsigned char* g = (unsigned char*)L.grad + (r * L.ldg + head) * ESZ + first * 16;
-        if (live) {
-          const float4 k = S.coef[team];
-          const f2 f{k.x, k.x}, nm = f2_splat(-k.z);
-          for (int i = tt; i < n; i += TT) {
-            if constexpr (LT == PSK_BF16) {
-              const uint4 u = *(const uint4*)(x + (size_t)i * 16);
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-              uint32_t o[4];
+        const float4 k = S.coef[team];
+        const f2 f = f2_splat(k.x), nm = f2_splat(-k.z);
+        for (int h = 0; h < chunks; ++h) {
+          const int hi = dead ? 0 : n < (h + 1) * CG ? n : (h + 1) * CG;
+          if (live) {
+            for (int i = h * CG + tt; i < hi; i += TT) {
+              if constexpr (LT == PSK_BF16) {
+                const uint4 u = *(const uint4*)(x + (size_t)i * 16);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                uint32_t o[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                f2 e = f2_mul(f2_add(unpack_bf16(w[q]), nm), f2_splat(c));
-                e = f2_mul(f2{ex2_approx(e.x), ex2_approx(e.y)}, f);
-                o[q] = f32x2_to_bf16x2(e.x, e.y);
+                for (int q = 0; q < 4; ++q) {
+                  f2 e = f2_mul(f2_add(unpack_bf16(w[q]), nm), f2_splat(c));
+                  e = f2_mul(f2{ex2_approx(e.x), ex2_approx(e.y)}, f);
+                  o[q] = f32x2_to_bf16x2(e.x, e.y);
+                }
+                *(uint4*)(g + (size_t)i * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+              } else {
+                const float4 u = *(const float4*)(x + (size_t)i * 16);
+                f2 a = f2_mul(f2_add(f2{u.x, u.y}, nm), f2_splat(c)), b = f2_mul(f2_add(f2{u.z, u.w}, nm), f2_splat(c));
+                a = f2_mul(f2{ex2_approx(a.x), ex2_approx(a.y)}, f);
+                b = f2_mul(f2{ex2_approx(b.x), ex2_approx(b.y)}, f);
+                *(float4*)(g + (size_t)i * 16) = make_float4(a.x, a.y, b.x, b.y);
               }
-              *(uint4*)(g + (size_t)i * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-            } else {
-              const float4 u = *(const float4*)(x + (size_t)i * 16);
-              f2 a = f2_mul(f2_add(f2{u.x, u.y}, nm), f2_splat(c)), b = f2_mul(f2_add(f2{u.z, u.w}, nm), f2_splat(c));
-              a = f2_mul(f2{ex2_approx(a.x), ex2_approx(a.y)}, f);
-              b = f2_mul(f2{ex2_approx(b.x), ex2_approx(b.y)}, f);
-              *(float4*)(g + (size_t)i * 16) = make_float4(a.x, a.y, b.x, b.y);
             }
+          } else {
+            for (int i = h * CG + tt; i < hi; i += TT) *(uint4*)(g + (size_t)i * 16) = make_uint4(0, 0, 0, 0);
           }
-          if (edge >= 0) {
-            const float e = edge == info.target ? k.y : ex2_approx((xe - k.z) * c) * k.x;
-            store1<LT>(L.grad, r * L.ldg + edge, e);
-          }
+          __syncwarp();
+          if (!dead && lane == 0) mbar_arrive(empty + h);
+        }
+        if (edge >= 0 && !dead) {
+          const float e = !live ? 0.0f : edge == info.target ? k.y : ex2_approx((xe - k.z) * c) * k.x;
+          store1<LT>(L.grad, r * L.ldg + edge, e);
+        }
+        if (live && info.target >= head) {
           // The target's own element, over what its thread has just stored.
           const int64_t at = ((int64_t)info.target - head) / G - first;
-          if (info.target >= head && at >= 0 && at < n && (int)at % TT == tt)
-            store1<LT>(L.grad, r * L.ldg + info.target, k.y);
-        } else if (!dead) {
-          for (int i = tt; i < n; i += TT) *(uint4*)(g + (size_t)i * 16) = make_uint4(0, 0, 0, 0);
-          if (edge >= 0) store1<LT>(L.grad, r * L.ldg + edge, 0.0f);
+          if (at >= 0 && at < n && (int)at % CG % TT == tt) store1<LT>(L.grad, r * L.ldg + info.target, k.y);
         }
-        __syncwarp();
-        if (!dead && lane == 0) mbar_arrive(&S.empty[s]);
       }
+      s += P.teams;
+      if (s >= slots) s -= slots, parity ^= 1;
     }
     if (MODE != LOSS_LOGP && tt == 0 && rank == 0) {
       L.part[2 * (cid * P.teams + team)] = loss_sum;
@@ -741,10 +767,16 @@ static bool resident_plan(ResParams& P, int32_t lt, int64_t rows, int64_t cols) 
   const int64_t elements = P.slice_groups * g;
   P.team_threads = 32;
   while (P.team_threads < 256 && elements > 32 * P.team_threads) P.team_threads *= 2;
-  P.teams = 512 / P.team_threads;
+  P.teams = RES_CONSUMERS / P.team_threads;
+  if (P.teams > fits) P.teams = fits;
   if (rows * k <= sms && elements > 8192) P.team_threads = 512, P.teams = 1;
-  else if (fits == 3) P.team_threads = 192, P.teams = 3;
   P.slots = fits / P.teams * P.teams;
+  // Chunks of whole steps (sixteen elements a thread).
+  const int step = (int)(16 / g) * P.team_threads, steps = (P.slice_groups + step - 1) / step;
+  int most = RES_MAX_BARS / P.slots < RES_MAX_CHUNKS ? RES_MAX_BARS / P.slots : RES_MAX_CHUNKS;
+  if (most > steps) most = steps;
+  P.chunk_groups = (steps + most - 1) / most * step;
+  P.chunks = (P.slice_groups + P.chunk_groups - 1) / P.chunk_groups;
   return true;
 }
 
