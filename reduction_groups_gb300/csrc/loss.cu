@@ -177,6 +177,40 @@ __device__ __forceinline__ RowLoss row_loss(const LossParams& P, double logp, fl
   return o;
 }
 
+// A row's logp as hi + lo (|lo| below half a step of hi), by error-free
+// transforms; tab: the log table (or its copy in shared memory).
+__device__ __forceinline__ void row_logp_pair(float xt, const RowSum& v, float scale, const float* tab, float& hi,
+                                              float& lo) {
+  lo = 0.0f;
+  hi = v.s + (v.m - v.m);                               // NaN unless the sums are finite
+  if (!(v.s < INFINITY) || !(fabsf(v.m) < INFINITY)) return;
+  hi = xt;
+  if (xt == -INFINITY) return;
+  float R, d, th, tl, ph, pl;
+  log_tier1_core(v.s, 0, tab, R, d);                    // s >= 1: the maximum's own term
+  two_sum(xt, -v.m, th, tl);
+  two_prod(scale, th, ph, pl);
+  pl = fmaf(scale, tl, pl);
+  two_sum(ph, -R, hi, lo);
+  lo += pl - (d + v.e / v.s);
+  fast_two_sum(hi, lo, hi, lo);
+}
+
+// a - b for a pair a = hi + lo.
+__device__ __forceinline__ float pair_minus(float hi, float lo, float b) {
+  float s, e;
+  two_sum(hi, -b, s, e);
+  return fabsf(s) < INFINITY ? s + (e + lo) : s;
+}
+
+// d(term + beta k) / dlogp in f32 from the ratio and e^q - 1.
+__device__ __forceinline__ float row_slope(const LossParams& P, float ratio, float em1, float adv) {
+  const float bound = fminf(fmaxf(ratio, P.low), P.high);
+  const float free_term = adv == 0.0f && ratio == ratio ? 0.0f : ratio * adv;
+  const float d = bound * adv < free_term ? 0.0f : -free_term;
+  return P.ref_logp && P.beta != 0.0f ? fmaf(-P.beta, em1, d) : d;
+}
+
 __device__ __forceinline__ int64_t row_target(const LossParams& P, int64_t r) {
   return P.targets64 ? ((const int64_t*)P.targets)[r] : (int64_t)((const int32_t*)P.targets)[r];
 }
@@ -287,8 +321,8 @@ constexpr int RES_MAX_SLOTS = 32;
 constexpr int RES_MAX_CHUNKS = 4;
 constexpr int RES_MAX_BARS = 32;               // slots x chunks
 constexpr int RES_MAX_CLUSTER = 8;
-constexpr int RES_SMEM = 216 * 1024;          // ring
-constexpr int RES_SLICE = 72 * 1024;          // largest slice: three in the ring
+constexpr int RES_SMEM = 210 * 1024;          // ring
+constexpr int RES_SLICE = 70 * 1024;          // largest slice: three in the ring
 
 struct ResParams {
   LossParams L;
@@ -313,6 +347,7 @@ struct ResShared {
   RowSum red[2][RES_CONSUMERS / 32];            // per warp
   RowSum xchg[RES_MAX_TEAMS][2][RES_MAX_CLUSTER];
   float4 coef[RES_MAX_TEAMS];
+  float4 log_tab[512];                          // psk_log_tab: a lookup from L2 would stall every row
   volatile int abort_flag;
 };
 
@@ -416,6 +451,8 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
     S.abort_flag = 0;
     fence_barrier_init();
   }
+  static_assert(sizeof(psk_log_tab) == sizeof(S.log_tab), "log table size");
+  for (int i = tid; i < 512; i += blockDim.x) S.log_tab[i] = ((const float4*)psk_log_tab)[i];
   __syncthreads();
   if (K > 1) cluster_barrier();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the finishing kernel may be set up
@@ -490,7 +527,21 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
     const int TT = P.team_threads, team = tid / TT, tt = tid - team * TT, tw = tt >> 5, nw = TT / 32;
     const float c = L.c;
     bool dead = false;
+    // The first warp's lane q holds the team's q-th row of 32 until their loss
+    // terms are taken together: 64-bit arithmetic costs a warp's instruction
+    // slots however few lanes need it.
     double loss_sum = 0.0, kl_sum = 0.0;
+    float held_hi = 0.0f, held_lo = 0.0f;
+    RowInfo held{};
+    int n_held = 0;
+    auto take_held = [&]() {
+      if (lane < n_held) {
+        const RowLoss o = row_loss(L, (double)held_hi + (double)held_lo, held.old, held.ref, held.adv);
+        loss_sum += (double)held.w * (o.term + (L.beta != 0.0f ? (double)L.beta * o.k : 0.0));
+        kl_sum += (double)held.w * o.k;
+      }
+      n_held = 0;
+    };
     uint32_t rows_done = 0, exchanges = 0;
     auto team_barrier = [&]() {
       if (TT == 32) __syncwarp();
@@ -610,18 +661,24 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
             v = join(v, u, c);
           }
         }
-        if (lane == 0 && !dead) {
-          const double logp = row_logp(info.xt, v, L.scale);
-          if (L.logp && rank == 0) L.logp[r] = (float)logp;
-          if (MODE != LOSS_LOGP) {
-            const RowLoss o = row_loss(L, logp, info.old, info.ref, info.adv);
-            if (MODE == LOSS_GRAD) {
-              const float a = info.w * o.d * L.scale;
-              S.coef[team] = make_float4(-a / v.s, a * -expm1f((float)logp), v.m, 0.0f);
-            }
-            loss_sum += (double)info.w * (o.term + (L.beta != 0.0f ? (double)L.beta * o.k : 0.0));
-            kl_sum += (double)info.w * o.k;
-          }
+        v.m = __shfl_sync(0xFFFFFFFFu, v.m, 0);
+        v.s = __shfl_sync(0xFFFFFFFFu, v.s, 0);
+        v.e = __shfl_sync(0xFFFFFFFFu, v.e, 0);
+        float hi, lo;
+        row_logp_pair(info.xt, v, L.scale, (const float*)S.log_tab, hi, lo);
+        if (lane == 0 && !dead && L.logp && rank == 0) L.logp[r] = hi;
+        if (MODE == LOSS_GRAD) {
+          // Two of the exponentials side by side: lane 1's for the KL term.
+          const float q = pair_minus(-hi, -lo, -info.ref);
+          const float em = expm1f(lane == 1 ? q : hi);
+          const float em_q = __shfl_sync(0xFFFFFFFFu, em, 1);
+          const float ratio = expf(pair_minus(hi, lo, info.old));
+          const float a = info.w * row_slope(L, ratio, em_q, info.adv) * L.scale;
+          if (lane == 0) S.coef[team] = make_float4(-a / v.s, a * -em, v.m, 0.0f);
+        }
+        if (MODE != LOSS_LOGP && !dead) {
+          if (lane == n_held) held_hi = hi, held_lo = lo, held = info;
+          if (++n_held == 32) take_held();
         }
         __syncwarp();
       } else if (tt == 0 && !dead && rank == 0 && L.logp) {
@@ -674,9 +731,18 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
       s += P.teams;
       if (s >= slots) s -= slots, parity ^= 1;
     }
-    if (MODE != LOSS_LOGP && tt == 0 && rank == 0) {
-      L.part[2 * (cid * P.teams + team)] = loss_sum;
-      L.part[2 * (cid * P.teams + team) + 1] = kl_sum;
+    if (MODE != LOSS_LOGP && tw == 0) {
+      take_held();
+      __syncwarp();
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        loss_sum += __shfl_xor_sync(0xFFFFFFFFu, loss_sum, o);
+        kl_sum += __shfl_xor_sync(0xFFFFFFFFu, kl_sum, o);
+      }
+      if (lane == 0 && rank == 0) {
+        L.part[2 * (cid * P.teams + team)] = loss_sum;
+        L.part[2 * (cid * P.teams + team) + 1] = kl_sum;
+      }
     }
   }
   __syncwarp();
