@@ -80,15 +80,23 @@ __device__ __forceinline__ RowSum join(const RowSum& a, const RowSum& b, float c
   return r;
 }
 
-__device__ __forceinline__ RowSum block_join(RowSum v, float c, RowSum* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    RowSum u;
-    u.m = __shfl_xor_sync(0xFFFFFFFFu, v.m, o);
-    u.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
-    u.e = __shfl_xor_sync(0xFFFFFFFFu, v.e, o);
-    v = join(v, u, c);
+// Join the sums of aligned groups of `lanes` lanes (a power of two): the
+// maximum first, one rescaling, then the sums with their rounding errors.
+__device__ __forceinline__ RowSum lanes_join(RowSum v, float c, int lanes) {
+  float m = v.m;
+  for (int o = lanes >> 1; o > 0; o >>= 1) m = max_nan2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const float f = v.m == m ? 1.0f : ex2_approx((v.m - m) * c);   // a NaN maximum gives NaN
+  float s = v.s * f, e = v.e * f;
+  for (int o = lanes >> 1; o > 0; o >>= 1) {
+    float err;
+    two_sum(s, __shfl_xor_sync(0xFFFFFFFFu, s, o), s, err);
+    e = (e + __shfl_xor_sync(0xFFFFFFFFu, e, o)) + err;
   }
+  return RowSum{m, s, e};
+}
+
+__device__ __forceinline__ RowSum block_join(RowSum v, float c, RowSum* red) {
+  v = lanes_join(v, c, 32);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   RowSum r = red[0];
@@ -399,15 +407,17 @@ __device__ __forceinline__ f2 unpack_bf16(uint32_t u) {
   return f2{__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)};
 }
 
-// A step's sixteen elements and their maximum (groups past the end: -inf).
-template <int LT>
+// A step's sixteen elements and their maximum; ALL: every group is there, else
+// groups from n on are -inf.
+template <int LT, bool ALL>
 __device__ __forceinline__ void load_step(const unsigned char* s, int i, int n, int stride, f2* x, float& m) {
   if constexpr (LT == PSK_BF16) {
     uint4 u[2];
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      u[q] = i + q * stride < n ? *(const uint4*)(s + (size_t)(i + q * stride) * 16)
-                                : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+    for (int q = 0; q < 2; ++q) {
+      if (!ALL) u[q] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+      if (ALL || i + q * stride < n) u[q] = *(const uint4*)(s + (size_t)(i + q * stride) * 16);
+    }
     uint32_t h = bf16x2_max(bf16x2_max(bf16x2_max(u[0].x, u[0].y), bf16x2_max(u[0].z, u[0].w)),
                             bf16x2_max(bf16x2_max(u[1].x, u[1].y), bf16x2_max(u[1].z, u[1].w)));
     const f2 e = unpack_bf16(h);
@@ -421,12 +431,34 @@ __device__ __forceinline__ void load_step(const unsigned char* s, int i, int n, 
     m = -INFINITY;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float4 v = i + q * stride < n ? *(const float4*)(s + (size_t)(i + q * stride) * 16)
-                                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (ALL || i + q * stride < n) v = *(const float4*)(s + (size_t)(i + q * stride) * 16);
       x[2 * q] = f2{v.x, v.y}, x[2 * q + 1] = f2{v.z, v.w};
       m = max_nan2(m, max_nan2(max_nan2(v.x, v.y), max_nan2(v.z, v.w)));
     }
   }
+}
+
+// A step into the running maximum and sum.
+template <int LT, bool ALL>
+__device__ __forceinline__ void add_step(const unsigned char* s, int i, int n, int stride, float c, float& max, f2& sum) {
+  f2 e[8];
+  float m;
+  load_step<LT, ALL>(s, i, n, stride, e, m);
+  if (!(m <= max)) {                       // grows, or NaN
+    m = max_nan2(m, max);
+    const float f = ex2_approx((max - m) * c);
+    sum.x *= f, sum.y *= f;
+    max = m;
+  }
+  const f2 nm = f2_splat(max == -INFINITY ? 0.0f : -max);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) e[q] = f2_mul(f2_add(e[q], nm), f2_splat(c));
+#pragma unroll
+  for (int q = 0; q < 8; ++q) e[q].x = ex2_approx(e[q].x), e[q].y = ex2_approx(e[q].y);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) e[q] = f2_add(e[q], e[q + 4]);
+  sum = f2_add(sum, f2_add(f2_add(e[0], e[1]), f2_add(e[2], e[3])));
 }
 
 template <int LT, int MODE>
@@ -577,25 +609,9 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
         if (live) {
           constexpr int STEP = GroupOf<LT>::PER_STEP;
           const int hi = n < (h + 1) * CG ? n : (h + 1) * CG;
-          for (int i = h * CG + tt; i < hi; i += STEP * TT) {
-            f2 e[8];
-            float m;
-            load_step<LT>(x, i, hi, TT, e, m);
-            if (!(m <= v.m)) {                       // grows, or NaN
-              m = max_nan2(m, v.m);
-              const float f = ex2_approx((v.m - m) * c);
-              sum.x *= f, sum.y *= f;
-              v.m = m;
-            }
-            const f2 nm = f2_splat(v.m == -INFINITY ? 0.0f : -v.m);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) e[q] = f2_mul(f2_add(e[q], nm), f2_splat(c));
-#pragma unroll
-            for (int q = 0; q < 8; ++q) e[q].x = ex2_approx(e[q].x), e[q].y = ex2_approx(e[q].y);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) e[q] = f2_add(e[q], e[q + 4]);
-            sum = f2_add(sum, f2_add(f2_add(e[0], e[1]), f2_add(e[2], e[3])));
-          }
+          int i = h * CG + tt;
+          for (; i + (STEP - 1) * TT < hi; i += STEP * TT) add_step<LT, true>(x, i, hi, TT, c, v.m, sum);
+          if (i < hi) add_step<LT, false>(x, i, hi, TT, c, v.m, sum);
         }
         if (MODE != LOSS_GRAD) {
           __syncwarp();
@@ -612,27 +628,14 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
           }
           v.s += v.m == -INFINITY ? 0.0f : ex2_approx((xe - v.m) * c);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          RowSum u;
-          u.m = __shfl_xor_sync(0xFFFFFFFFu, v.m, o);
-          u.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
-          u.e = __shfl_xor_sync(0xFFFFFFFFu, v.e, o);
-          v = join(v, u, c);
-        }
+        v = lanes_join(v, c, 32);
         if (lane == 0) S.red[rows_done & 1][tid >> 5] = v;
       }
       __syncwarp();
       team_barrier();
       if (tw == 0 && live) {
         v = lane < nw ? S.red[rows_done & 1][team * nw + lane] : RowSum{-INFINITY, 0.0f, 0.0f};
-        for (int o = 1; o < nw; o <<= 1) {
-          RowSum u;
-          u.m = __shfl_xor_sync(0xFFFFFFFFu, v.m, o);
-          u.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
-          u.e = __shfl_xor_sync(0xFFFFFFFFu, v.e, o);
-          v = join(v, u, c);
-        }
+        if (nw > 1) v = lanes_join(v, c, nw);
         if (K > 1) {
           v.m = __shfl_sync(0xFFFFFFFFu, v.m, 0);
           v.s = __shfl_sync(0xFFFFFFFFu, v.s, 0);
@@ -653,13 +656,7 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
           // every lane acquires what the peers wrote
           if (ok && lane != 0) mbar_wait_cluster(&S.xbar[team][p], ((exchanges - 1) >> 1) & 1u);
           v = ok && (uint32_t)lane < K ? S.xchg[team][p][lane] : RowSum{-INFINITY, 0.0f, 0.0f};
-          for (uint32_t o = 1; o < K; o <<= 1) {
-            RowSum u;
-            u.m = __shfl_xor_sync(0xFFFFFFFFu, v.m, o);
-            u.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
-            u.e = __shfl_xor_sync(0xFFFFFFFFu, v.e, o);
-            v = join(v, u, c);
-          }
+          v = lanes_join(v, c, (int)K);
         }
         v.m = __shfl_sync(0xFFFFFFFFu, v.m, 0);
         v.s = __shfl_sync(0xFFFFFFFFu, v.s, 0);
