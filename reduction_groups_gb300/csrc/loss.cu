@@ -313,16 +313,17 @@ __global__ void __launch_bounds__(LOSS_THREADS) loss_rows_kernel(const __grid_co
 // memory, a row slice per CTA of a cluster (one CTA where the row fits, up to
 // eight for rows of up to 8 x 72 KB or to spread a call of few rows), and
 // stays there for the sums and for the gradient, which goes straight to
-// memory: the floor of one read and one write per logit.  A producer warp
-// keeps the ring of slices full, and hands each row's scalars along with it.
-// Teams of consumer warps take rows in turn, each with slots of its own, so
-// that one team's barriers and scalar section (logarithm, ratio, KL term)
-// overlap another's exponentials.  A slot is filled and freed in up to four
-// chunks: the sums begin with the first chunk, and the next row's copy with
-// the first chunk whose gradient is written.  The CTAs of a cluster exchange
-// their slices' maxima and sums through distributed shared memory.
+// memory: the floor of one read and one write per logit.  Teams of warps take
+// rows in turn, each with slots of its own, so that one team's barriers and
+// scalar section (logarithm, ratio, KL term) overlap another's exponentials.
+// A slot is filled and freed in up to four chunks: the sums begin with the
+// first chunk, and the next row's copy with the first chunk whose gradient is
+// written.  A team's warps fetch the scalars of its next 32 rows at once.  A
+// producer warp, a lane for each chunk of each slot, refills them as they fall
+// free.  The CTAs of a cluster exchange their slices' maxima and sums through
+// distributed shared memory.
 
-constexpr int RES_CONSUMERS = 768;             // teams of 32 to 512 threads
+constexpr int RES_CONSUMERS = 768;             // at most: teams of 32 to 512 threads
 constexpr int RES_THREADS = RES_CONSUMERS + 32;
 constexpr int RES_MAX_TEAMS = 24;
 constexpr int RES_MAX_SLOTS = 32;
@@ -342,19 +343,19 @@ struct ResParams {
   int32_t cluster;
 };
 
-// A row's scalars, from the producer to the teams.
+// A row's scalars.
 struct RowInfo {
-  int32_t live, target;
+  int32_t target;
   float w, xt, old, ref, adv;
 };
 
 struct ResShared {
   uint64_t full[RES_MAX_BARS], empty[RES_MAX_BARS];      // slot x chunks + chunk
   uint64_t xbar[RES_MAX_TEAMS][2];
-  RowInfo info[RES_MAX_SLOTS];
   RowSum red[2][RES_CONSUMERS / 32];            // per warp
+  uint32_t live[RES_MAX_TEAMS][2];              // which of a team's 32 rows are live, two batches in turn
   RowSum xchg[RES_MAX_TEAMS][2][RES_MAX_CLUSTER];
-  float4 coef[RES_MAX_TEAMS];
+  float4 coef[RES_MAX_TEAMS];                   // -a / s (times 2^residue), a (1 - p_t), c m or m, the target
   float4 log_tab[512];                          // psk_log_tab: a lookup from L2 would stall every row
   volatile int abort_flag;
 };
@@ -394,6 +395,19 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   } while (clock64() - t0 < PIPE_WAIT_CYCLES);
   atomicOr(&g_pipe_status, PIPE_TIMEOUT);
   return false;
+}
+
+// Whether the phase with this parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Elements of a 16-byte group.
@@ -473,273 +487,317 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
   const uint32_t rank = K > 1 ? cluster_rank() : 0;
   const int64_t cid = blockIdx.x / K, ncl = gridDim.x / K;
   const int n_local = cid < L.rows ? (int)((L.rows - 1 - cid) / ncl + 1) : 0;
-  const int slots = P.slots, chunks = P.chunks, CG = P.chunk_groups;
+  const int slots = P.slots, chunks = P.chunks, CG = P.chunk_groups, teams = P.teams;
   const int64_t cols = L.cols;
   const uintptr_t base = (uintptr_t)L.x;
 
   if (tid == 0) {
     for (int i = 0; i < slots * chunks; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], P.team_threads / 32);
-    for (int t = 0; t < P.teams; ++t) mbar_init(&S.xbar[t][0], K), mbar_init(&S.xbar[t][1], K);
+    for (int t = 0; t < teams; ++t) mbar_init(&S.xbar[t][0], K), mbar_init(&S.xbar[t][1], K);
     S.abort_flag = 0;
     fence_barrier_init();
   }
   static_assert(sizeof(psk_log_tab) == sizeof(S.log_tab), "log table size");
   for (int i = tid; i < 512; i += blockDim.x) S.log_tab[i] = ((const float4*)psk_log_tab)[i];
-  __syncthreads();
-  if (K > 1) cluster_barrier();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the finishing kernel may be set up
 
+  const int TT = P.team_threads, depth = slots / teams;
+  const bool producer = tid >= teams * TT;
+  // The producer's lane l fills chunk l % chunks of slot l / chunks.
+  const int team = producer ? lane / chunks % teams : tid / TT;
+  const int64_t first = (int64_t)rank * P.slice_groups;
+  // The team's q-th row.
+  auto row_of = [&](int q) { return cid + (int64_t)(team + q * teams) * ncl; };
   // Row r: elements before its first 16-byte boundary, full groups after.
   auto head_of = [&](int64_t r) {
     const int a = (int)(((base + (uintptr_t)(r * L.ldx) * ESZ) & 15u) / ESZ);
     const int64_t h = a ? G - a : 0;
     return (int)(h < cols ? h : cols);
   };
-
-  if (tid >= P.teams * P.team_threads) {
-    // ---------------- producer: lanes fetch 32 rows' scalars at once, lane 0 issues
-    const long long drop = g_pipe_drop_row;
-    int issued = 0;
-    bool stop = false;
-    for (int j0 = 0; j0 < n_local && !stop; j0 += 32) {
-      RowInfo info{};
-      const int64_t mine = cid + (int64_t)(j0 + lane) * ncl;
-      if (j0 + lane < n_local) {
-        const int64_t t = row_target(L, mine);
-        info.w = MODE == LOSS_LOGP ? 1.0f : L.weight ? L.weight[mine] : L.uniform;
-        info.live = t >= 0 && t < cols && !(info.w == 0.0f);
-        if (info.live) {
-          info.target = (int32_t)t;
-          info.xt = load1<LT>(L.x, mine * L.ldx + t);
-          if (MODE != LOSS_LOGP) {
-            info.old = L.old_logp[mine], info.adv = L.adv[mine];
-            info.ref = L.ref_logp ? L.ref_logp[mine] : 0.0f;
-          }
+  auto groups_of = [&](int head) {                 // of the CTA's slice
+    const int64_t n = (cols - head) / G - first;
+    return (int)(n < 0 ? 0 : n < P.slice_groups ? n : P.slice_groups);
+  };
+  // Which of the team's rows q, .., q + 31 are live (the same in every warp, in
+  // every CTA of a cluster); their scalars in the first warp's lanes.
+  RowInfo batch{};
+  auto live_rows = [&](int q, bool scalars) {
+    bool live = false;
+    if (team + (q + lane) * teams < n_local) {
+      const int64_t r = row_of(q + lane), t = row_target(L, r);
+      const float w = MODE == LOSS_LOGP ? 1.0f : L.weight ? L.weight[r] : L.uniform;
+      live = t >= 0 && t < cols && !(w == 0.0f);
+      if (scalars && live) {
+        batch.target = (int32_t)t;
+        batch.w = w;
+        batch.xt = load1<LT>(L.x, r * L.ldx + t);
+        if (MODE != LOSS_LOGP) {
+          batch.old = L.old_logp[r], batch.adv = L.adv[r];
+          batch.ref = L.ref_logp ? L.ref_logp[r] : 0.0f;
         }
-      }
-      for (int k = 0; k < 32 && j0 + k < n_local; ++k) {
-        const int j = j0 + k, s = j % slots;
-        if (lane == k) {
-          const int head = head_of(mine);
-          const int64_t first = (int64_t)rank * P.slice_groups;
-          int64_t n = (cols - head) / G - first;
-          n = n < 0 || !info.live ? 0 : n < P.slice_groups ? n : P.slice_groups;
-          const unsigned char* src = (const unsigned char*)L.x + (mine * L.ldx + head) * ESZ + first * 16;
-          bool ok = j != drop && !S.abort_flag;
-          for (int h = 0; h < chunks && ok; ++h) {
-            const int bar = s * chunks + h;
-            if (j >= slots && !mbar_wait(&S.empty[bar], (uint32_t)((j / slots) - 1) & 1u)) {
-              S.abort_flag = 1;
-              ok = false;
-              break;
-            }
-            if (h == 0) S.info[s] = info;
-            int64_t m = n - (int64_t)h * CG;
-            m = m < 0 ? 0 : m < CG ? m : CG;
-            mbar_arrive_expect_tx(&S.full[bar], (uint32_t)m * 16u);
-            if (m > 0)
-              bulk_copy_g2s(ring + (size_t)s * P.slot_bytes + (size_t)h * CG * 16, src + (size_t)h * CG * 16,
-                            (uint32_t)m * 16u, &S.full[bar]);
-          }
-          if (ok) ++issued;
-          stop = !ok;
-        }
-        stop = __shfl_sync(0xFFFFFFFFu, stop, k);
-        if (stop) break;
       }
     }
-    // Wind-down after a timeout: copies still in flight land before the CTA retires.
-    for (int o = 16; o > 0; o >>= 1) issued += __shfl_xor_sync(0xFFFFFFFFu, issued, o);
-    if (stop && lane == 0)
-      for (int j = issued > slots ? issued - slots : 0; j < issued; ++j)
-        for (int h = 0; h < chunks; ++h) mbar_wait(&S.full[j % slots * chunks + h], (uint32_t)(j / slots) & 1u);
-  } else {
-    // ---------------- teams.  After a timeout (`dead`) a thread skips waits
-    // and work but keeps meeting its team's barriers.
-    const int TT = P.team_threads, team = tid / TT, tt = tid - team * TT, tw = tt >> 5, nw = TT / 32;
-    const float c = L.c;
-    bool dead = false;
-    // The first warp's lane q holds the team's q-th row of 32 until their loss
-    // terms are taken together: 64-bit arithmetic costs a warp's instruction
-    // slots however few lanes need it.
-    double loss_sum = 0.0, kl_sum = 0.0;
-    float held_hi = 0.0f, held_lo = 0.0f;
-    RowInfo held{};
-    int n_held = 0;
-    auto take_held = [&]() {
-      if (lane < n_held) {
-        const RowLoss o = row_loss(L, (double)held_hi + (double)held_lo, held.old, held.ref, held.adv);
-        loss_sum += (double)held.w * (o.term + (L.beta != 0.0f ? (double)L.beta * o.k : 0.0));
-        kl_sum += (double)held.w * o.k;
-      }
-      n_held = 0;
-    };
-    uint32_t rows_done = 0, exchanges = 0;
-    auto team_barrier = [&]() {
-      if (TT == 32) __syncwarp();
-      else named_barrier(1 + team, TT);
-    };
-    int s = team;                                  // the row's slot
-    uint32_t parity = 0;                           // of its phases
-    for (int j = team; j < n_local; j += P.teams, ++rows_done) {
-      const int64_t r = cid + (int64_t)j * ncl;
-      const unsigned char* x = ring + (size_t)s * P.slot_bytes;
-      const int head = head_of(r);
-      const int64_t body = (cols - head) / G;
-      const int tail = (int)(cols - head - body * G);
-      const int64_t first = (int64_t)rank * P.slice_groups;
-      const int n = body <= first ? 0 : body - first < P.slice_groups ? (int)(body - first) : P.slice_groups;
-      // The head's and tail's elements: one each for the first threads of the first CTA's team.
-      const int64_t edge = rank != 0 || tt >= 16 ? -1
-                           : tt < 8 ? (tt < head ? tt : -1)
-                                    : (tt - 8 < tail ? cols - tail + (tt - 8) : -1);
-      dead = dead || S.abort_flag;
-      uint64_t* full = &S.full[s * chunks];
-      uint64_t* empty = &S.empty[s * chunks];
-      if (!dead && !mbar_wait(full, parity)) { S.abort_flag = 1; dead = true; }
-      RowInfo info{};
-      if (!dead) info = S.info[s];
-      const bool live = !dead && info.live;
-      const float xe = live && edge >= 0 ? load1<LT>(L.x, r * L.ldx + edge) : -INFINITY;
+    return __ballot_sync(0xFFFFFFFFu, live);
+  };
+  const int tt = tid - team * TT, tw = tt >> 5, nw = TT / 32;
+  uint32_t live_now = 0;
+  // The live rows of the batch that begins at row q, and of the next one for
+  // the producer, which issues rows up to `depth` ahead.
+  auto next_batch = [&](int q) {
+    live_now = live_rows(q, tw == 0);
+    if (tw == 0) {
+      const uint32_t next = live_rows(q + 32, false);
+      if (lane == 0) S.live[team][(q / 32) & 1] = live_now, S.live[team][(q / 32 + 1) & 1] = next;
+    }
+  };
+  if (!producer) next_batch(0);
+  __syncthreads();
+  if (K > 1) cluster_barrier();
 
-      RowSum v{-INFINITY, 0.0f, 0.0f};
-      f2 sum{0.0f, 0.0f};
-      for (int h = 0; h < chunks; ++h) {
-        if (h > 0 && !dead && !mbar_wait(full + h, parity)) { S.abort_flag = 1; dead = true; }
-        if (live) {
-          constexpr int STEP = GroupOf<LT>::PER_STEP;
-          const int hi = n < (h + 1) * CG ? n : (h + 1) * CG;
-          int i = h * CG + tt;
-          for (; i + (STEP - 1) * TT < hi; i += STEP * TT) add_step<LT, true>(x, i, hi, TT, c, v.m, sum);
-          if (i < hi) add_step<LT, false>(x, i, hi, TT, c, v.m, sum);
-        }
-        if (MODE != LOSS_GRAD) {
-          __syncwarp();
-          if (!dead && lane == 0) mbar_arrive(empty + h);
-        }
+  if (producer) {
+    const long long drop = g_pipe_drop_row;
+    const int slot = lane / chunks, h = lane % chunks;
+    const bool mine = lane < slots * chunks;
+    int q = slot / teams, issued = -1;             // the lane's next and last row
+    uint32_t parity = 1;                           // of the slot's last phase; a fresh barrier passes 1
+    long long t0 = clock64();
+    while (true) {
+      const bool pending = mine && team + q * teams < n_local && !(drop >= 0 && team + q * teams >= drop);
+      if (!__any_sync(0xFFFFFFFFu, pending) || S.abort_flag) break;
+      const bool ready = pending && mbar_test(&S.empty[lane], parity);
+      if (ready) {
+        const int64_t r = row_of(q);
+        const int head = head_of(r);
+        const bool live = (S.live[team][(q / 32) & 1] >> (q & 31)) & 1;
+        int m = groups_of(head) - h * CG;
+        m = !live || m < 0 ? 0 : m < CG ? m : CG;
+        mbar_arrive_expect_tx(&S.full[lane], (uint32_t)m * 16u);
+        if (m > 0)
+          bulk_copy_g2s(ring + (size_t)slot * P.slot_bytes + (size_t)h * CG * 16,
+                        (const unsigned char*)L.x + (r * L.ldx + head) * ESZ + (first + (int64_t)h * CG) * 16,
+                        (uint32_t)m * 16u, &S.full[lane]);
+        issued = q;
+        q += depth;
+        parity ^= 1;
       }
-      if (live) {
-        v.s = __fadd_rn(sum.x, sum.y);
-        if (edge >= 0) {
-          if (!(xe <= v.m)) {
-            const float m = max_nan2(xe, v.m);
-            v.s *= ex2_approx((v.m - m) * c);
-            v.m = m;
-          }
-          v.s += v.m == -INFINITY ? 0.0f : ex2_approx((xe - v.m) * c);
+      if (__any_sync(0xFFFFFFFFu, ready)) {
+        t0 = clock64();
+      } else if (clock64() - t0 > PIPE_WAIT_CYCLES) {
+        if (lane == 0) atomicOr(&g_pipe_status, PIPE_TIMEOUT);
+        S.abort_flag = 1;
+      } else {
+        __nanosleep(20);
+      }
+    }
+    __syncwarp();
+    // After a timeout, copies still in flight land before the CTA retires.
+    if (S.abort_flag && issued >= 0) mbar_wait(&S.full[lane], (uint32_t)(issued / depth) & 1u);
+    __syncwarp();
+    if (K > 1) cluster_barrier();
+    return;
+  }
+
+  // ---------------- teams.  After a timeout (`dead`) a thread skips waits and
+  // work but keeps meeting its team's barriers.
+  const float c = L.c;
+  bool dead = false;
+  // The first warp's lane q holds the team's q-th row of 32 until their loss
+  // terms are taken together: 64-bit arithmetic costs a warp's instruction
+  // slots however few lanes need it.
+  double loss_sum = 0.0, kl_sum = 0.0;
+  float held_hi = 0.0f, held_lo = 0.0f;
+  RowInfo held{};
+  int n_held = 0;
+  auto take_held = [&]() {
+    if (lane < n_held) {
+      const RowLoss o = row_loss(L, (double)held_hi + (double)held_lo, held.old, held.ref, held.adv);
+      loss_sum += (double)held.w * (o.term + (L.beta != 0.0f ? (double)L.beta * o.k : 0.0));
+      kl_sum += (double)held.w * o.k;
+    }
+    n_held = 0;
+  };
+  uint32_t exchanges = 0;
+  auto team_barrier = [&]() {
+    if (TT == 32) __syncwarp();
+    else named_barrier(1 + team, TT);
+  };
+  int s = team;                                    // the row's slot
+  uint32_t parity = 0;                             // of its phases
+  for (int q = 0; team + q * teams < n_local; ++q) {
+    if (q > 0 && (q & 31) == 0) next_batch(q);
+    const int64_t r = row_of(q);
+    const unsigned char* x = ring + (size_t)s * P.slot_bytes;
+    const int head = head_of(r);
+    const int tail = (int)((cols - head) % G);
+    const int n = groups_of(head);
+    // The head's and tail's elements: one each for the first threads of the first CTA's team.
+    const int64_t edge = rank != 0 || tt >= 16 ? -1
+                         : tt < 8 ? (tt < head ? tt : -1)
+                                  : (tt - 8 < tail ? cols - tail + (tt - 8) : -1);
+    const bool live = (live_now >> (q & 31)) & 1;
+    dead = dead || S.abort_flag;
+    uint64_t* full = &S.full[s * chunks];
+    uint64_t* empty = &S.empty[s * chunks];
+    const float xe = live && edge >= 0 ? load1<LT>(L.x, r * L.ldx + edge) : -INFINITY;
+    auto leave = [&](int h) {                       // the warp is past a chunk
+      __syncwarp();
+      if (!dead && lane == 0) mbar_arrive(empty + h);
+    };
+
+    RowSum v{-INFINITY, 0.0f, 0.0f};
+    f2 sum{0.0f, 0.0f};
+    for (int h = 0; h < chunks; ++h) {
+      if (!dead && !mbar_wait(full + h, parity)) { S.abort_flag = 1; dead = true; }
+      if (live && !dead) {
+        constexpr int STEP = GroupOf<LT>::PER_STEP;
+        const int hi = n < (h + 1) * CG ? n : (h + 1) * CG;
+        int i = h * CG + tt;
+        for (; i + (STEP - 1) * TT < hi; i += STEP * TT) add_step<LT, true>(x, i, hi, TT, c, v.m, sum);
+        if (i < hi) add_step<LT, false>(x, i, hi, TT, c, v.m, sum);
+      }
+      if (MODE != LOSS_GRAD) leave(h);
+    }
+    if (live) {
+      v.s = __fadd_rn(sum.x, sum.y);
+      if (edge >= 0) {
+        if (!(xe <= v.m)) {
+          const float m = max_nan2(xe, v.m);
+          v.s *= ex2_approx((v.m - m) * c);
+          v.m = m;
         }
-        v = lanes_join(v, c, 32);
-        if (lane == 0) S.red[rows_done & 1][tid >> 5] = v;
+        v.s += v.m == -INFINITY ? 0.0f : ex2_approx((xe - v.m) * c);
       }
       __syncwarp();
-      team_barrier();
-      if (tw == 0 && live) {
-        v = lane < nw ? S.red[rows_done & 1][team * nw + lane] : RowSum{-INFINITY, 0.0f, 0.0f};
-        if (nw > 1) v = lanes_join(v, c, nw);
-        if (K > 1) {
-          v.m = __shfl_sync(0xFFFFFFFFu, v.m, 0);
-          v.s = __shfl_sync(0xFFFFFFFFu, v.s, 0);
-          v.e = __shfl_sync(0xFFFFFFFFu, v.e, 0);
-          const uint32_t p = exchanges & 1;
-          if ((uint32_t)lane < K) {
-            const uint32_t to = peer_addr(&S.xchg[team][p][rank], lane);
-            peer_store(to, v.m);
-            peer_store(to + 4, v.s);
-            peer_store(to + 8, v.e);
-            peer_arrive(peer_addr(&S.xbar[team][p], lane));
-          }
-          bool ok = true;
-          if (lane == 0) ok = mbar_wait_cluster(&S.xbar[team][p], (exchanges >> 1) & 1u);
-          ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-          ++exchanges;
-          if (!ok) { S.abort_flag = 1; dead = true; }
-          // every lane acquires what the peers wrote
-          if (ok && lane != 0) mbar_wait_cluster(&S.xbar[team][p], ((exchanges - 1) >> 1) & 1u);
-          v = ok && (uint32_t)lane < K ? S.xchg[team][p][lane] : RowSum{-INFINITY, 0.0f, 0.0f};
-          v = lanes_join(v, c, (int)K);
+      v = lanes_join(v, c, 32);
+      if (lane == 0) S.red[q & 1][tid >> 5] = v;
+    }
+    __syncwarp();
+    team_barrier();
+    if (tw == 0 && live) {
+      __syncwarp();
+      v = lane < nw ? S.red[q & 1][team * nw + lane] : RowSum{-INFINITY, 0.0f, 0.0f};
+      if (nw > 1) v = lanes_join(v, c, nw);
+      v.m = __shfl_sync(0xFFFFFFFFu, v.m, 0);
+      v.s = __shfl_sync(0xFFFFFFFFu, v.s, 0);
+      v.e = __shfl_sync(0xFFFFFFFFu, v.e, 0);
+      if (K > 1) {
+        const uint32_t p = exchanges & 1;
+        if ((uint32_t)lane < K) {
+          const uint32_t to = peer_addr(&S.xchg[team][p][rank], lane);
+          peer_store(to, v.m);
+          peer_store(to + 4, v.s);
+          peer_store(to + 8, v.e);
+          peer_arrive(peer_addr(&S.xbar[team][p], lane));
         }
+        // every lane acquires what the peers wrote
+        bool ok = dead || mbar_wait_cluster(&S.xbar[team][p], (exchanges >> 1) & 1u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        ++exchanges;
+        if (!ok) { S.abort_flag = 1; dead = true; }
+        v = (uint32_t)lane < K ? S.xchg[team][p][lane] : RowSum{-INFINITY, 0.0f, 0.0f};
+        v = lanes_join(v, c, (int)K);
         v.m = __shfl_sync(0xFFFFFFFFu, v.m, 0);
         v.s = __shfl_sync(0xFFFFFFFFu, v.s, 0);
         v.e = __shfl_sync(0xFFFFFFFFu, v.e, 0);
-        float hi, lo;
-        row_logp_pair(info.xt, v, L.scale, (const float*)S.log_tab, hi, lo);
-        if (lane == 0 && !dead && L.logp && rank == 0) L.logp[r] = hi;
-        if (MODE == LOSS_GRAD) {
-          // Two of the exponentials side by side: lane 1's for the KL term.
-          const float q = pair_minus(-hi, -lo, -info.ref);
-          const float em = expm1f(lane == 1 ? q : hi);
-          const float em_q = __shfl_sync(0xFFFFFFFFu, em, 1);
-          const float ratio = expf(pair_minus(hi, lo, info.old));
-          const float a = info.w * row_slope(L, ratio, em_q, info.adv) * L.scale;
-          if (lane == 0) S.coef[team] = make_float4(-a / v.s, a * -em, v.m, 0.0f);
-        }
-        if (MODE != LOSS_LOGP && !dead) {
-          if (lane == n_held) held_hi = hi, held_lo = lo, held = info;
-          if (++n_held == 32) take_held();
-        }
-        __syncwarp();
-      } else if (tt == 0 && !dead && rank == 0 && L.logp) {
-        L.logp[r] = 0.0f;                        // a row left out
       }
+      RowInfo info;
+      const int from = q & 31;
+      info.target = __shfl_sync(0xFFFFFFFFu, batch.target, from);
+      info.xt = __shfl_sync(0xFFFFFFFFu, batch.xt, from);
+      info.w = __shfl_sync(0xFFFFFFFFu, batch.w, from);
+      info.old = __shfl_sync(0xFFFFFFFFu, batch.old, from);
+      info.ref = __shfl_sync(0xFFFFFFFFu, batch.ref, from);
+      info.adv = __shfl_sync(0xFFFFFFFFu, batch.adv, from);
+      float hi, lo;
+      row_logp_pair(info.xt, v, L.scale, (const float*)S.log_tab, hi, lo);
+      if (lane == 0 && !dead && L.logp && rank == 0) L.logp[r] = hi;
       if (MODE == LOSS_GRAD) {
-        team_barrier();
-        unsigned char* g = (unsigned char*)L.grad + (r * L.ldg + head) * ESZ + first * 16;
-        const float4 k = S.coef[team];
-        const f2 f = f2_splat(k.x), nm = f2_splat(-k.z);
-        for (int h = 0; h < chunks; ++h) {
-          const int hi = dead ? 0 : n < (h + 1) * CG ? n : (h + 1) * CG;
-          if (live) {
-            for (int i = h * CG + tt; i < hi; i += TT) {
-              if constexpr (LT == PSK_BF16) {
-                const uint4 u = *(const uint4*)(x + (size_t)i * 16);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                uint32_t o[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  f2 e = f2_mul(f2_add(unpack_bf16(w[q]), nm), f2_splat(c));
-                  e = f2_mul(f2{ex2_approx(e.x), ex2_approx(e.y)}, f);
-                  o[q] = f32x2_to_bf16x2(e.x, e.y);
-                }
-                *(uint4*)(g + (size_t)i * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-              } else {
-                const float4 u = *(const float4*)(x + (size_t)i * 16);
-                f2 a = f2_mul(f2_add(f2{u.x, u.y}, nm), f2_splat(c)), b = f2_mul(f2_add(f2{u.z, u.w}, nm), f2_splat(c));
-                a = f2_mul(f2{ex2_approx(a.x), ex2_approx(a.y)}, f);
-                b = f2_mul(f2{ex2_approx(b.x), ex2_approx(b.y)}, f);
-                *(float4*)(g + (size_t)i * 16) = make_float4(a.x, a.y, b.x, b.y);
-              }
-            }
-          } else {
-            for (int i = h * CG + tt; i < hi; i += TT) *(uint4*)(g + (size_t)i * 16) = make_uint4(0, 0, 0, 0);
-          }
-          __syncwarp();
-          if (!dead && lane == 0) mbar_arrive(empty + h);
-        }
-        if (edge >= 0 && !dead) {
-          const float e = !live ? 0.0f : edge == info.target ? k.y : ex2_approx((xe - k.z) * c) * k.x;
-          store1<LT>(L.grad, r * L.ldg + edge, e);
-        }
-        if (live && info.target >= head) {
-          // The target's own element, over what its thread has just stored.
-          const int64_t at = ((int64_t)info.target - head) / G - first;
-          if (at >= 0 && at < n && (int)at % CG % TT == tt) store1<LT>(L.grad, r * L.ldg + info.target, k.y);
-        }
+        // Two of the exponentials side by side: lane 1's for the KL term.
+        const float d = pair_minus(-hi, -lo, -info.ref);
+        const float em = expm1f(lane == 1 ? d : hi);
+        const float em_q = __shfl_sync(0xFFFFFFFFu, em, 1);
+        const float ratio = expf(pair_minus(hi, lo, info.old));
+        const float a = info.w * row_slope(L, ratio, em_q, info.adv) * L.scale;
+        // softmax_j = 2^(c x_j - RN(c m)) 2^(RN(c m) - c m) / s in one fma a
+        // logit, but for values whose product might leave f32.
+        const float mc = v.m * c;
+        const bool near = fabsf(mc) < 0x1p100f;
+        const float f = -a / v.s;
+        if (lane == 0)
+          S.coef[team] = make_float4(near ? f * ex2_approx(fmaf(-v.m, c, mc)) : f, a * -em, near ? mc : v.m,
+                                     __int_as_float(near ? info.target : ~info.target));
       }
-      s += P.teams;
-      if (s >= slots) s -= slots, parity ^= 1;
-    }
-    if (MODE != LOSS_LOGP && tw == 0) {
-      take_held();
+      if (MODE != LOSS_LOGP && !dead) {
+        if (lane == n_held) held_hi = hi, held_lo = lo, held = info;
+        if (++n_held == 32) take_held();
+      }
       __syncwarp();
+    } else if (tt == 0 && !dead && rank == 0 && L.logp) {
+      L.logp[r] = 0.0f;                          // a row left out
+    }
+    if (MODE == LOSS_GRAD) {
+      __syncwarp();
+      team_barrier();
+      unsigned char* g = (unsigned char*)L.grad + (r * L.ldg + head) * ESZ + first * 16;
+      const float4 k = S.coef[team];
+      const bool near = __float_as_int(k.w) >= 0;
+      const int target = near ? __float_as_int(k.w) : ~__float_as_int(k.w);
+      const f2 f = f2_splat(k.x), nm = f2_splat(-k.z), cc = f2_splat(c);
+      auto grad = [&](auto NEAR, f2 e) {
+        e = NEAR.value ? f2_fma(e, cc, nm) : f2_mul(f2_add(e, nm), cc);
+        return f2_mul(f2{ex2_approx(e.x), ex2_approx(e.y)}, f);
+      };
+      auto chunk = [&](auto NEAR, int lo, int hi) {
+        for (int i = lo + tt; i < hi; i += TT) {
+          const uint4 u = *(const uint4*)(x + (size_t)i * 16);
+          if constexpr (LT == PSK_BF16) {
+            const f2 a = grad(NEAR, unpack_bf16(u.x)), b = grad(NEAR, unpack_bf16(u.y)),
+                     d = grad(NEAR, unpack_bf16(u.z)), e = grad(NEAR, unpack_bf16(u.w));
+            *(uint4*)(g + (size_t)i * 16) = make_uint4(f32x2_to_bf16x2(a.x, a.y), f32x2_to_bf16x2(b.x, b.y),
+                                                       f32x2_to_bf16x2(d.x, d.y), f32x2_to_bf16x2(e.x, e.y));
+          } else {
+            const f2 a = grad(NEAR, f2{__uint_as_float(u.x), __uint_as_float(u.y)}),
+                     b = grad(NEAR, f2{__uint_as_float(u.z), __uint_as_float(u.w)});
+            *(float4*)(g + (size_t)i * 16) = make_float4(a.x, a.y, b.x, b.y);
+          }
+        }
+      };
+      for (int h = 0; h < chunks; ++h) {
+        const int hi = dead ? 0 : n < (h + 1) * CG ? n : (h + 1) * CG;
+        if (!live) {
+          for (int i = h * CG + tt; i < hi; i += TT) *(uint4*)(g + (size_t)i * 16) = make_uint4(0, 0, 0, 0);
+        } else if (near) {
+          chunk(std::true_type{}, h * CG, hi);
+        } else {
+          chunk(std::false_type{}, h * CG, hi);
+        }
+        leave(h);
+      }
+      if (edge >= 0 && !dead) {
+        const f2 e = near ? grad(std::true_type{}, f2{xe, xe}) : grad(std::false_type{}, f2{xe, xe});
+        store1<LT>(L.grad, r * L.ldg + edge, !live ? 0.0f : edge == target ? k.y : e.x);
+      }
+      if (live && !dead && target >= head) {
+        // The target's own element, over what its thread has just stored.
+        const int64_t at = ((int64_t)target - head) / G - first;
+        if (at >= 0 && at < n && (int)at % CG % TT == tt) store1<LT>(L.grad, r * L.ldg + target, k.y);
+      }
+    }
+    s += teams;
+    if (s >= slots) s -= slots, parity ^= 1;
+  }
+  __syncwarp();
+  if (MODE != LOSS_LOGP && tw == 0) {
+    take_held();
+    __syncwarp();
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        loss_sum += __shfl_xor_sync(0xFFFFFFFFu, loss_sum, o);
-        kl_sum += __shfl_xor_sync(0xFFFFFFFFu, kl_sum, o);
-      }
-      if (lane == 0 && rank == 0) {
-        L.part[2 * (cid * P.teams + team)] = loss_sum;
-        L.part[2 * (cid * P.teams + team) + 1] = kl_sum;
-      }
+    for (int o = 16; o > 0; o >>= 1) {
+      loss_sum += __shfl_xor_sync(0xFFFFFFFFu, loss_sum, o);
+      kl_sum += __shfl_xor_sync(0xFFFFFFFFu, kl_sum, o);
+    }
+    if (lane == 0 && rank == 0) {
+      L.part[2 * (cid * teams + team)] = loss_sum;
+      L.part[2 * (cid * teams + team) + 1] = kl_sum;
     }
   }
   __syncwarp();
@@ -813,9 +871,9 @@ static LossParams loss_params(const void* logits, int64_t rows, int64_t cols, in
 // a cluster's shared memory.  The cluster is the smallest whose slices leave
 // three in a CTA's ring; a call whose rows leave more than half of the SMs idle
 // spreads each over a larger one while slices keep 2048 elements (a row of
-// 32000 on one CTA is bound by that SM's copy and exponentials).  Teams
-// take about 32 to 128 elements a thread: short rows are bound by their
-// barriers and scalar sections, which more teams overlap.
+// 32000 on one CTA is bound by that SM's copy and exponentials).  Teams take
+// up to 128 elements a thread: a row's joins, barriers and scalar section cost
+// every warp of its team, and more teams overlap them.
 static bool resident_plan(ResParams& P, int32_t lt, int64_t rows, int64_t cols) {
   const int64_t g = lt == PSK_BF16 ? 8 : 4, groups = cols / g, sms = device_sm_count();
   int64_t k = 1;
@@ -827,12 +885,15 @@ static bool resident_plan(ResParams& P, int32_t lt, int64_t rows, int64_t cols) 
   P.slice_groups = (int32_t)(slice(k) > 0 ? slice(k) : 1);
   P.slot_bytes = (P.slice_groups * 16 + 127) / 128 * 128;
   const int fits = RES_SMEM / P.slot_bytes < RES_MAX_SLOTS ? RES_SMEM / P.slot_bytes : RES_MAX_SLOTS;
-  const int64_t elements = P.slice_groups * g;
+  const int64_t elements = P.slice_groups * g, each = (rows * k + sms - 1) / sms;
   P.team_threads = 32;
-  while (P.team_threads < 256 && elements > 32 * P.team_threads) P.team_threads *= 2;
+  while (P.team_threads < 256 && elements > 128 * P.team_threads) P.team_threads *= 2;
+  // Fewer rows a cluster than teams: larger teams, down to 16 elements a thread.
+  while (P.team_threads < 256 && RES_CONSUMERS / P.team_threads > each && elements > 16 * P.team_threads)
+    P.team_threads *= 2;
+  if (each == 1 && elements > 8192) P.team_threads = 512;
   P.teams = RES_CONSUMERS / P.team_threads;
   if (P.teams > fits) P.teams = fits;
-  if (rows * k <= sms && elements > 8192) P.team_threads = 512, P.teams = 1;
   P.slots = fits / P.teams * P.teams;
   // Chunks of whole steps (sixteen elements a thread).
   const int step = (int)(16 / g) * P.team_threads, steps = (P.slice_groups + step - 1) / step;
