@@ -200,7 +200,7 @@ __device__ __forceinline__ void row_logp_pair(float xt, const RowSum& v, float s
   two_prod(scale, th, ph, pl);
   pl = fmaf(scale, tl, pl);
   two_sum(ph, -R, hi, lo);
-  lo += pl - (d + v.e / v.s);
+  lo += pl - (d + __fdividef(v.e, v.s));
   fast_two_sum(hi, lo, hi, lo);
 }
 
@@ -328,6 +328,7 @@ constexpr int RES_THREADS = RES_CONSUMERS + 32;
 constexpr int RES_MAX_TEAMS = 24;
 constexpr int RES_MAX_SLOTS = 32;
 constexpr int RES_MAX_CHUNKS = 4;
+constexpr int RES_ROWS_AHEAD = 3;              // slots of a team at most: rows a warp may be ahead of another
 constexpr int RES_MAX_BARS = 32;               // slots x chunks
 constexpr int RES_MAX_CLUSTER = 8;
 constexpr int RES_SMEM = 210 * 1024;          // ring
@@ -352,11 +353,13 @@ struct RowInfo {
 struct ResShared {
   uint64_t full[RES_MAX_BARS], empty[RES_MAX_BARS];      // slot x chunks + chunk
   uint64_t xbar[RES_MAX_TEAMS][2];
-  RowSum red[2][RES_CONSUMERS / 32];            // per warp
+  uint64_t rbar[RES_MAX_TEAMS][RES_ROWS_AHEAD + 1];      // a row's warp sums are in
+  RowSum red[RES_ROWS_AHEAD + 1][RES_CONSUMERS / 32];    // per warp
   uint32_t live[RES_MAX_TEAMS][2];              // which of a team's 32 rows are live, two batches in turn
   RowSum xchg[RES_MAX_TEAMS][2][RES_MAX_CLUSTER];
   float4 coef[RES_MAX_TEAMS];                   // -a / s (times 2^residue), a (1 - p_t), c m or m, the target
   float4 log_tab[512];                          // psk_log_tab: a lookup from L2 would stall every row
+  double sums[RES_CONSUMERS / 32][2];           // per warp: its rows' loss and KL sums
   volatile int abort_flag;
 };
 
@@ -493,7 +496,10 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
 
   if (tid == 0) {
     for (int i = 0; i < slots * chunks; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], P.team_threads / 32);
-    for (int t = 0; t < teams; ++t) mbar_init(&S.xbar[t][0], K), mbar_init(&S.xbar[t][1], K);
+    for (int t = 0; t < teams; ++t) {
+      mbar_init(&S.xbar[t][0], K), mbar_init(&S.xbar[t][1], K);
+      for (int b = 0; b <= RES_ROWS_AHEAD; ++b) mbar_init(&S.rbar[t][b], P.team_threads / 32);
+    }
     S.abort_flag = 0;
     fence_barrier_init();
   }
@@ -543,8 +549,9 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
   uint32_t live_now = 0;
   // The live rows of the batch that begins at row q, and of the next one for
   // the producer, which issues rows up to `depth` ahead.
+  const bool any_warp = MODE != LOSS_GRAD && K == 1;   // takes scalar sections
   auto next_batch = [&](int q) {
-    live_now = live_rows(q, tw == 0);
+    live_now = live_rows(q, any_warp || tw == 0);
     if (tw == 0) {
       const uint32_t next = live_rows(q + 32, false);
       if (lane == 0) S.live[team][(q / 32) & 1] = live_now, S.live[team][(q / 32 + 1) & 1] = next;
@@ -586,7 +593,7 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
         if (lane == 0) atomicOr(&g_pipe_status, PIPE_TIMEOUT);
         S.abort_flag = 1;
       } else {
-        __nanosleep(20);
+        __nanosleep(64);
       }
     }
     __syncwarp();
@@ -623,17 +630,25 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
   };
   int s = team;                                    // the row's slot
   uint32_t parity = 0;                             // of its phases
-  for (int q = 0; team + q * teams < n_local; ++q) {
+  int64_t r = row_of(0);
+  const int64_t r_step = (int64_t)teams * ncl;
+  // Where a row begins among 16-byte boundaries: the same for all rows of an
+  // aligned leading dimension.
+  const bool vary = (L.ldx * ESZ) % 16 != 0;
+  int head = 0, n = 0;
+  int64_t edge = -1;                               // the thread's element of the row's head or tail
+  for (int q = 0; team + q * teams < n_local; ++q, r += r_step) {
     if (q > 0 && (q & 31) == 0) next_batch(q);
-    const int64_t r = row_of(q);
     const unsigned char* x = ring + (size_t)s * P.slot_bytes;
-    const int head = head_of(r);
-    const int tail = (int)((cols - head) % G);
-    const int n = groups_of(head);
-    // The head's and tail's elements: one each for the first threads of the first CTA's team.
-    const int64_t edge = rank != 0 || tt >= 16 ? -1
-                         : tt < 8 ? (tt < head ? tt : -1)
-                                  : (tt - 8 < tail ? cols - tail + (tt - 8) : -1);
+    if (vary || q == 0) {
+      head = head_of(r);
+      n = groups_of(head);
+      // One each for the first threads of the first CTA's team.
+      const int tail = (int)((cols - head) % G);
+      edge = rank != 0 || tt >= 16 ? -1
+             : tt < 8 ? (tt < head ? tt : -1)
+                      : (tt - 8 < tail ? cols - tail + (tt - 8) : -1);
+    }
     const bool live = (live_now >> (q & 31)) & 1;
     dead = dead || S.abort_flag;
     uint64_t* full = &S.full[s * chunks];
@@ -669,13 +684,29 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
       }
       __syncwarp();
       v = lanes_join(v, c, 32);
-      if (lane == 0) S.red[q & 1][tid >> 5] = v;
+      if (lane == 0) S.red[q & RES_ROWS_AHEAD][tid >> 5] = v;
     }
     __syncwarp();
-    team_barrier();
-    if (tw == 0 && live) {
+    // Without a gradient no warp needs the row's result: each reports its sum
+    // and goes on, and the warps take the rows' scalar sections in turn (a warp
+    // is at most RES_ROWS_AHEAD rows ahead of the one that reads its sums, since
+    // a slot's refill waits for every warp).  In a cluster the first warp
+    // keeps them all: the exchange's two buffers rest on its order.
+    const bool turns = MODE != LOSS_GRAD && K == 1 && nw > 1;
+    const int scalar_warp = turns ? q % nw : 0;
+    if (turns) {
+      uint64_t* rbar = &S.rbar[team][q & RES_ROWS_AHEAD];
+      if (lane == 0) mbar_arrive(rbar);
+      if (tw == scalar_warp && !dead && !mbar_wait(rbar, (uint32_t)(q / (RES_ROWS_AHEAD + 1)) & 1u)) {
+        S.abort_flag = 1;
+        dead = true;
+      }
+    } else {
+      team_barrier();
+    }
+    if (tw == scalar_warp && live) {
       __syncwarp();
-      v = lane < nw ? S.red[q & 1][team * nw + lane] : RowSum{-INFINITY, 0.0f, 0.0f};
+      v = lane < nw ? S.red[q & RES_ROWS_AHEAD][team * nw + lane] : RowSum{-INFINITY, 0.0f, 0.0f};
       if (nw > 1) v = lanes_join(v, c, nw);
       v.m = __shfl_sync(0xFFFFFFFFu, v.m, 0);
       v.s = __shfl_sync(0xFFFFFFFFu, v.s, 0);
@@ -722,7 +753,7 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
         // logit, but for values whose product might leave f32.
         const float mc = v.m * c;
         const bool near = fabsf(mc) < 0x1p100f;
-        const float f = -a / v.s;
+        const float f = __fdividef(-a, v.s);
         if (lane == 0)
           S.coef[team] = make_float4(near ? f * ex2_approx(fmaf(-v.m, c, mc)) : f, a * -em, near ? mc : v.m,
                                      __int_as_float(near ? info.target : ~info.target));
@@ -732,7 +763,7 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
         if (++n_held == 32) take_held();
       }
       __syncwarp();
-    } else if (tt == 0 && !dead && rank == 0 && L.logp) {
+    } else if (!live && tt == 0 && !dead && rank == 0 && L.logp) {
       L.logp[r] = 0.0f;                          // a row left out
     }
     if (MODE == LOSS_GRAD) {
@@ -780,14 +811,14 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
       if (live && !dead && target >= head) {
         // The target's own element, over what its thread has just stored.
         const int64_t at = ((int64_t)target - head) / G - first;
-        if (at >= 0 && at < n && (int)at % CG % TT == tt) store1<LT>(L.grad, r * L.ldg + target, k.y);
+        if (at >= 0 && at < n && ((int)at & (TT - 1)) == tt) store1<LT>(L.grad, r * L.ldg + target, k.y);
       }
     }
     s += teams;
     if (s >= slots) s -= slots, parity ^= 1;
   }
   __syncwarp();
-  if (MODE != LOSS_LOGP && tw == 0) {
+  if (MODE != LOSS_LOGP && (any_warp || tw == 0)) {
     take_held();
     __syncwarp();
 #pragma unroll
@@ -795,7 +826,12 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
       loss_sum += __shfl_xor_sync(0xFFFFFFFFu, loss_sum, o);
       kl_sum += __shfl_xor_sync(0xFFFFFFFFu, kl_sum, o);
     }
-    if (lane == 0 && rank == 0) {
+    if (any_warp) {                                // the warps' sums in order, by the team's first
+      if (lane == 0) S.sums[tid >> 5][0] = loss_sum, S.sums[tid >> 5][1] = kl_sum;
+      team_barrier();
+      for (int w = 1; tt == 0 && w < nw; ++w) loss_sum += S.sums[team * nw + w][0], kl_sum += S.sums[team * nw + w][1];
+    }
+    if (tt == 0 && rank == 0) {
       L.part[2 * (cid * teams + team)] = loss_sum;
       L.part[2 * (cid * teams + team) + 1] = kl_sum;
     }
@@ -894,7 +930,8 @@ static bool resident_plan(ResParams& P, int32_t lt, int64_t rows, int64_t cols) 
   if (each == 1 && elements > 8192) P.team_threads = 512;
   P.teams = RES_CONSUMERS / P.team_threads;
   if (P.teams > fits) P.teams = fits;
-  P.slots = fits / P.teams * P.teams;
+  const int depth = fits / P.teams < RES_ROWS_AHEAD ? fits / P.teams : RES_ROWS_AHEAD;
+  P.slots = depth * P.teams;
   // Chunks of whole steps (sixteen elements a thread).
   const int step = (int)(16 / g) * P.team_threads, steps = (P.slice_groups + step - 1) / step;
   int most = RES_MAX_BARS / P.slots < RES_MAX_CHUNKS ? RES_MAX_BARS / P.slots : RES_MAX_CHUNKS;

@@ -242,3 +242,15 @@ def test_a_lost_copy_ends_in_a_status_not_a_hang(R, rows, cols):
     R.psk_token_logp(x, t, logp)
     torch.cuda.synchronize()
     assert R.psk_device_status() == 0 and bool(logp.isfinite().all())
+
+
+@pytest.mark.parametrize("rows,cols,lt", [(1200, 20000, "bf16"), (4000, 3001, "bf16"), (1000, 9000, "f32"),
+                                          (6000, 500, "f32"), (3000, 6000, "bf16")])
+def test_many_rows_without_a_gradient(R, rows, cols, lt):
+    _check(R, rows, cols, lt, lt, 0.1, 1.0, grad=False)
+    rng = np.random.default_rng(2)
+    x, xv, t, targets, *_ = _inputs(rng, rows, cols, lt, 0.8)
+    logp = torch.empty(rows, device="cuda")
+    R.psk_token_logp(x, targets, logp, scale=0.8)
+    want, bound, _, _ = OT.token_logp(xv, t, 0.8)
+    close(logp, want, bound, "f32")
