@@ -33,8 +33,9 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int64_t i) {
   return I64 ? ((const int64_t*)ids)[i] : (int64_t)((const int32_t*)ids)[i];
 }
 
-// One group of eight columns a thread, of ROWS rows `stride` items apart (all
-// of their loads in flight at once).
+// Eight columns a thread of ROWS rows, all of their loads in flight at once.
+// VEC: an item is a group of eight neighbouring columns of a row; else an item
+// is a lane of a 256-column slice, whose columns are 32 apart.
 template <int TT, int YT, bool I64, bool VEC, int ROWS>
 __global__ void __launch_bounds__(EMB_THREADS) embed_kernel(const __grid_constant__ EmbedParams P) {
   const uint64_t t0 = (uint64_t)blockIdx.x * EMB_THREADS + threadIdx.x;
@@ -50,10 +51,13 @@ __global__ void __launch_bounds__(EMB_THREADS) embed_kernel(const __grid_constan
     row[q] = t < P.items ? P.row0 + r : -1;
     id[q] = row[q] >= 0 ? load_id<I64>(P.ids, row[q]) : -1;
   }
+  auto columns = [&](int q) {
+    return VEC ? Columns<VEC, 8>((int64_t)g[q] * 8, 1, 0, P.cols)
+               : Columns<VEC, 8>((int64_t)(g[q] / 32) * 256, 32, g[q] % 32, P.cols);
+  };
 #pragma unroll
   for (int q = 0; q < ROWS; ++q)
-    if (id[q] >= 0 && id[q] < P.vocab)
-      Columns<VEC, 8>((int64_t)g[q] * 8, 1, 0, P.cols).load(P.table, id[q] * P.ldt, v[q]);
+    if (id[q] >= 0 && id[q] < P.vocab) columns(q).load(P.table, id[q] * P.ldt, v[q]);
 #pragma unroll
   for (int q = 0; q < ROWS; ++q) {
     if (row[q] < 0) continue;
@@ -61,13 +65,14 @@ __global__ void __launch_bounds__(EMB_THREADS) embed_kernel(const __grid_constan
     float y[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] = in ? __fmul_rn(v[q].get(k), P.scale) : 0.0f;
-    Columns<VEC, 8>((int64_t)g[q] * 8, 1, 0, P.cols).template store<YT>(P.y, row[q] * P.ldy, y);
+    columns(q).template store<YT>(P.y, row[q] * P.ldy, y);
   }
 }
 
 // ----------------------------------------------------------------- backward
 
-constexpr int SORT_THREADS = 512;
+constexpr int SORT_THREADS = 512;                         // of the sort; as many again zero rows beside it
+constexpr int SORT_FILL_BYTES = 384 * 1024;               // of a slice's rows zeroed beside the sort
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_PER_LANE = 16;
 constexpr int SORT_TILE = SORT_THREADS * SORT_PER_LANE;   // ids scanned at a time
@@ -88,8 +93,11 @@ struct EmbedGradParams {
   float* tail;           // per run: the sum of its trailing entries whose id the next run goes on with
   int64_t pcols;         // row length of head and tail
   int32_t slice_ids;     // ids of a sorting CTA's slice of the vocabulary
+  int32_t fill_ids;      // of them, first, whose rows the sort kernel zeroes unasked
+  FastDiv per_slice;     // by slice_ids
   int32_t accumulate;
   int32_t slices;        // column slices of a row in the run sums
+  int32_t join_slices;   // and in their join
   int32_t run_ctas;      // CTAs of the run sums; the others zero the rows that do not occur
   float scale;
 };
@@ -107,11 +115,25 @@ struct SortShared {
   uint32_t place[SORT_BINS];                 // counts, then each id's next place
   uint16_t before[SORT_WARPS][SORT_BINS];    // a warp's entries of an id; then those of the warps before, growing
   uint32_t warp_total[SORT_WARPS];
-  uint32_t below, total;
+  uint32_t below;
 };
 
-template <bool I64>
-__global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_constant__ EmbedGradParams P) {
+// A span of zeros: the columns of a row, by one warp.
+template <int DT, bool VEC>
+__device__ __forceinline__ void zero_row(const EmbedGradParams& P, int64_t row, int lane) {
+  const float z[8] = {};
+  for (int64_t c = 0; c < P.cols; c += 256) Columns<VEC, 8>(c, 32, lane, P.cols).template store<DT>(P.d, row * P.ldd, z);
+}
+
+// Barrier of the sorting threads.
+__device__ __forceinline__ void sort_sync() { asm volatile("bar.sync 1, %0;" ::"n"(SORT_THREADS) : "memory"); }
+
+// The sort's few microseconds of latency leave memory idle, so the other
+// half of the CTA's threads zero the first rows of the slice meanwhile (all of
+// them in a small table), whether they occur or not; the run sums' kernel,
+// which knows, zeroes the rest.
+template <bool I64, int DT, bool VEC>
+__global__ void __launch_bounds__(2 * SORT_THREADS) embed_sort_kernel(const __grid_constant__ EmbedGradParams P) {
   extern __shared__ __align__(16) unsigned char sort_smem[];
   SortShared& S = *reinterpret_cast<SortShared*>(sort_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -119,9 +141,13 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
   const int64_t first = (int64_t)blockIdx.x * P.slice_ids;
   const int bins = (int)(P.vocab - first < P.slice_ids ? P.vocab - first : P.slice_ids);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid >= SORT_THREADS) {
+    for (int v = warp - SORT_WARPS; v < P.fill_ids && v < bins; v += SORT_WARPS) zero_row<DT, VEC>(P, first + v, lane);
+    return;
+  }
   for (int b = tid; b < bins; b += SORT_THREADS) S.place[b] = 0;
-  if (tid == 0) S.below = 0, S.total = 0;
-  __syncthreads();
+  if (tid == 0) S.below = 0;
+  sort_sync();
 
   // Scan the ids of one tile: the slice's entries go to the list from `at` on,
   // in order, where it has room; their number is returned.
@@ -134,15 +160,19 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
     for (int k = 0; k < SORT_PER_LANE; ++k) {
       const int64_t i = w0 + 32 * k;
       const int64_t id = i < P.tokens ? load_id<I64>(P.ids, i) : -1;
-      if (count) below += id >= 0 && id < first;
-      const int64_t local = id - first;
-      key[k] = local >= 0 && local < bins ? (uint32_t)local : 0xFFFFFFFFu;
+      key[k] = id >= 0 && id < P.vocab ? (uint32_t)id : 0xFFFFFFFFu;
+    }
+#pragma unroll
+    for (int k = 0; k < SORT_PER_LANE; ++k) {
+      if (count) below += key[k] < (uint32_t)first;
+      const uint32_t local = key[k] - (uint32_t)first;     // an id below the slice, or none, wraps past it
+      key[k] = local < (uint32_t)bins ? local : 0xFFFFFFFFu;
     }
 #pragma unroll
     for (int k = 0; k < SORT_PER_LANE; ++k) mine += __popc(__ballot_sync(0xFFFFFFFFu, key[k] != 0xFFFFFFFFu));
-    __syncthreads();                         // the list's and warp_total's last readers are done
+    sort_sync();                         // the list's and warp_total's last readers are done
     if (lane == 0) S.warp_total[warp] = mine;
-    __syncthreads();
+    sort_sync();
     uint32_t sum = 0;
 #pragma unroll
     for (int w = 0; w < SORT_WARPS; ++w) {
@@ -172,7 +202,7 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
     const uint32_t per = ((n + SORT_WARPS - 1) / SORT_WARPS + 31) / 32 * 32;
     const uint32_t a = warp * per, e = a + per < n ? a + per : n;
     for (int b = lane; b < bins; b += 32) S.before[warp][b] = 0;
-    __syncthreads();
+    sort_sync();
     for (uint32_t i = a; i < e; i += 32) {
       const bool in = i + lane < e;
       const uint32_t key = in ? S.key[i + lane] : 0xFFFFu;
@@ -180,7 +210,7 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
       if (in && (peers & lt) == 0) S.before[warp][key] += (uint16_t)__popc(peers);
       __syncwarp();
     }
-    __syncthreads();
+    sort_sync();
     for (int b = tid; b < bins; b += SORT_THREADS) {
       uint32_t sum = 0;
 #pragma unroll
@@ -190,7 +220,7 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
         sum += c;
       }
     }
-    __syncthreads();
+    sort_sync();
     for (uint32_t i = a; i < e; i += 32) {
       const bool in = i + lane < e;
       const uint32_t key = in ? S.key[i + lane] : 0xFFFFu;
@@ -207,10 +237,10 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
         P.pos[q] = S.pos[i + lane];
       }
     }
-    __syncthreads();
+    sort_sync();
     // The last warp's counters have grown to the list's counts.
     for (int b = tid; b < bins; b += SORT_THREADS) S.place[b] += S.before[SORT_WARPS - 1][b];
-    __syncthreads();
+    sort_sync();
   };
 
   uint32_t n = 0;
@@ -218,7 +248,7 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xFFFFFFFFu, below, o);
   if (lane == 0) atomicAdd(&S.below, below);
-  __syncthreads();
+  sort_sync();
   for (int b = tid; b < bins; b += SORT_THREADS) P.seen[first + b] = S.place[b] != 0;
   if (tid == 0 && blockIdx.x + 1 == gridDim.x) *P.entries = S.below + n;
   // Counts to first places: four neighbouring ids a thread.
@@ -236,7 +266,7 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
     if (lane >= o) scan += u;
   }
   if (lane == 31) S.warp_total[warp] = scan;
-  __syncthreads();
+  sort_sync();
   uint32_t at = S.below + scan - sum;
 #pragma unroll
   for (int w = 0; w < SORT_WARPS; ++w)
@@ -246,7 +276,7 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
     if (4 * tid + k < bins) S.place[4 * tid + k] = at;
     at += c[k];
   }
-  __syncthreads();
+  sort_sync();
   if (n <= SORT_LIST) {
     rank_list(n);
     return;
@@ -255,13 +285,13 @@ __global__ void __launch_bounds__(SORT_THREADS) embed_sort_kernel(const __grid_c
   for (int64_t t0 = 0; t0 < P.tokens; t0 += SORT_TILE) {
     uint32_t more = scan_tile(t0, held, false);
     if (held + more > SORT_LIST) {           // the tile's entries do not fit behind the held ones:
-      __syncthreads();
+      sort_sync();
       rank_list(held);                       // rank those, and collect the tile again
       more = scan_tile(t0, 0, false);
       held = 0;
     }
     held += more;
-    __syncthreads();
+    sort_sync();
   }
   rank_list(held);
 }
@@ -284,13 +314,6 @@ __device__ __forceinline__ void write_row(const EmbedGradParams& P, const Column
   cols.template store<DT>(P.d, row, o);
 }
 
-// A span of zeros: the columns of a row, by one warp.
-template <int DT, bool VEC>
-__device__ __forceinline__ void zero_row(const EmbedGradParams& P, int64_t row, int lane) {
-  const float z[8] = {};
-  for (int64_t c = 0; c < P.cols; c += 256) Columns<VEC, 8>(c, 32, lane, P.cols).template store<DT>(P.d, row * P.ldd, z);
-}
-
 // The first run_ctas CTAs: one run and one slice of 32 NC columns a warp.  The
 // others zero the rows of ids that do not occur.
 template <int CT, int DT, bool VEC, int NC>
@@ -301,7 +324,8 @@ __global__ void __launch_bounds__(EMB_THREADS) embed_runs_kernel(const __grid_co
   if ((int)blockIdx.x >= P.run_ctas) {
     const int64_t warps = (int64_t)(gridDim.x - P.run_ctas) * (EMB_THREADS / 32);
     for (int64_t v = ((int64_t)(blockIdx.x - P.run_ctas) * EMB_THREADS + threadIdx.x) >> 5; v < P.vocab; v += warps)
-      if (!P.seen[v]) zero_row<DT, VEC>(P, v, lane);
+      if (!P.seen[v] && (int)((uint32_t)v - P.per_slice.div((uint32_t)v) * P.slice_ids) >= P.fill_ids)
+        zero_row<DT, VEC>(P, v, lane);
     return;
   }
   const int64_t w = ((int64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5;
@@ -357,13 +381,15 @@ __global__ void __launch_bounds__(EMB_THREADS) embed_runs_kernel(const __grid_co
 }
 
 // Join the run sums of each id whose entries span several runs: the warps of
-// the run it begins in.
-template <int DT, bool VEC, int NC>
+// the run it begins in, four columns a lane and sixteen run sums in flight (a
+// frequent id's join is a chain of such batches).
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(EMB_THREADS) embed_join_kernel(const __grid_constant__ EmbedGradParams P) {
+  constexpr int NC = 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t w = ((int64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  const int64_t run = w / P.slices;
+  const int64_t run = w / P.join_slices;
   const int64_t i0 = run * EMB_RUN, i1 = i0 + EMB_RUN;
   const int64_t entries = *P.entries;
   if (i1 >= entries) return;                        // the last run goes on nowhere
@@ -381,7 +407,7 @@ __global__ void __launch_bounds__(EMB_THREADS) embed_join_kernel(const __grid_co
     }
     last += 32;
   }
-  const Columns<VEC, NC> cols((w - run * P.slices) * (32 * NC), 32, lane, P.cols);
+  const Columns<VEC, NC> cols((w - run * P.join_slices) * (32 * NC), 32, lane, P.cols);
   f2 acc[NC / 2];
   Piece<PSK_F32, VEC, NC> t;
   cols.load(P.tail, run * P.pcols, t);
@@ -485,8 +511,9 @@ extern "C" int psk_embed(const void* ids, int32_t idt, int64_t tokens, const voi
   if (vocab > 0 && ranges_overlap(table, rows_bytes(vocab, cols, ldt, tt), y, yb))
     return fail(PSK_E_ALIAS, "y overlaps the table");
   if (ranges_overlap(ids, (uint64_t)tokens * isz, y, yb)) return fail(PSK_E_ALIAS, "y overlaps the ids");
-  EmbedParams P{ids, table, y, vocab, cols, ldt, ldy, 0, 0, FastDiv((uint32_t)((cols + 7) / 8)), (float)scale};
   const bool vec = cols % 8 == 0 && rows_vec8(table, tt, ldt, vocab) && rows_vec8(y, yt, ldy, tokens);
+  EmbedParams P{ids, table, y, vocab, cols, ldt, ldy, 0, 0,
+                FastDiv((uint32_t)(vec ? cols / 8 : (cols + 255) / 256 * 32)), (float)scale};
   const uint64_t slice = 0xFFFFFFFFull / P.per_row.d;
   cudaStream_t s = (cudaStream_t)stream;
   for (uint64_t r0 = 0; r0 < (uint64_t)tokens; r0 += slice) {
@@ -590,6 +617,10 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
   int64_t slice = (vocab + sms - 1) / sms;
   if (slice > SORT_BINS) slice = SORT_BINS;
   P.slice_ids = (int32_t)slice;
+  P.per_slice = FastDiv((uint32_t)slice);
+  const int64_t row_bytes = cols * dtype_size(dt), fill = SORT_FILL_BYTES / row_bytes;
+  P.fill_ids = accumulate ? 0 : (int32_t)(fill < slice ? fill : slice);
+  if (P.fill_ids == slice) zero_ctas = 0;
   const unsigned sort_ctas = (unsigned)((vocab + slice - 1) / slice);
   // Eight columns a lane, or four where eight leave fewer than 16 warps an SM
   // (latency then counts more than the instructions for each row).
@@ -597,14 +628,21 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
   const bool wide = runs * ((cols + 255) / 256) >= 16 * sms;
   P.slices = (int32_t)((cols + (wide ? 255 : 127)) / (wide ? 256 : 128));
   const uint64_t ctas = ((uint64_t)runs * P.slices + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32);
-  if (ctas + 2 * sms > 0x7FFFFFFFull) return fail(PSK_E_SHAPE, "tokens x cols too large");
+  P.join_slices = (int32_t)((cols + 127) / 128);
+  const uint64_t join_ctas = ((uint64_t)runs * P.join_slices + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32);
+  if (join_ctas + 2 * sms > 0x7FFFFFFFull) return fail(PSK_E_SHAPE, "tokens x cols too large");
   P.run_ctas = (int32_t)ctas;
-  static bool limit[2][PSK_MAX_DEVICES] = {};
-  const bool i64 = idt == PSK_I64;
-  smem_limit_once(i64 ? (const void*)embed_sort_kernel<true> : (const void*)embed_sort_kernel<false>,
-                  (int)sizeof(SortShared), limit[i64]);
-  if (i64) embed_sort_kernel<true><<<sort_ctas, SORT_THREADS, sizeof(SortShared), s>>>(P);
-  else embed_sort_kernel<false><<<sort_ctas, SORT_THREADS, sizeof(SortShared), s>>>(P);
+  with_bool(idt == PSK_I64, [&](auto I64) {
+    return with_dtype(dt, [&](auto DT) {
+      return with_bool(vec, [&](auto VEC) {
+        static bool limit[PSK_MAX_DEVICES] = {};
+        smem_limit_once((const void*)embed_sort_kernel<I64.value, DT.value, VEC.value>, (int)sizeof(SortShared), limit);
+        embed_sort_kernel<I64.value, DT.value, VEC.value>
+            <<<sort_ctas, 2 * SORT_THREADS, sizeof(SortShared), s>>>(P);
+        return 0;
+      });
+    });
+  });
   rc = check_launch("embedding sort kernel");
   if (rc) return rc;
   with_dtype(ct_t, [&](auto CT) {
@@ -621,8 +659,7 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
   if (rc || runs == 1) return rc;
   with_dtype(dt, [&](auto DT) {
     return with_bool(vec, [&](auto VEC) {
-      if (wide) launch_after(embed_join_kernel<DT.value, VEC.value, 8>, (unsigned)ctas, EMB_THREADS, s, P);
-      else launch_after(embed_join_kernel<DT.value, VEC.value, 4>, (unsigned)ctas, EMB_THREADS, s, P);
+      launch_after(embed_join_kernel<DT.value, VEC.value>, (unsigned)join_ctas, EMB_THREADS, s, P);
       return 0;
     });
   });

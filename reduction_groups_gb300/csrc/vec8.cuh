@@ -75,7 +75,7 @@ struct Piece {
     if constexpr (VEC && TY == PSK_BF16)
       return __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
     else
-      return __uint_as_float(w[k]);
+      return __uint_as_float(TY == PSK_BF16 ? w[k] << 16 : w[k]);
   }
 };
 
@@ -115,7 +115,7 @@ struct Columns {
       for (int k = 0; k < NC; ++k) {
         o.w[k] = 0;
         if (has(k)) {
-          if constexpr (TY == PSK_BF16) o.w[k] = (uint32_t)((const uint16_t*)p)[row + col(k)] << 16;
+          if constexpr (TY == PSK_BF16) o.w[k] = ((const uint16_t*)p)[row + col(k)];
           else o.w[k] = ((const uint32_t*)p)[row + col(k)];
         }
       }
