@@ -75,6 +75,70 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const __grid_cons
   cols.template store<YT>(P.y, (int64_t)row * P.ldy, y);
 }
 
+// Rows that begin anywhere, x, y and the residual of one type and alike: a
+// thread's eight elements begin at a 16-byte boundary of the row, `shift`
+// columns past a multiple of four, and take their words from three groups of
+// four columns.  A row's first and last elements go one by one.
+template <int TY, bool RES>
+__global__ void __launch_bounds__(DROP_THREADS) dropout_shifted_kernel(const __grid_constant__ DropoutParams P) {
+  constexpr int ESZ = TY == PSK_BF16 ? 2 : 4;
+  const uint64_t t = (uint64_t)blockIdx.x * DROP_THREADS + threadIdx.x;
+  if (t >= P.items) return;
+  const uint32_t r = P.per_row.div((uint32_t)t);
+  const uint32_t g = (uint32_t)t - r * P.per_row.d;
+  const uint32_t row = P.row0 + r;
+  const int64_t xo = (int64_t)row * P.ldx, ro = (int64_t)row * P.ldr, yo = (int64_t)row * P.ldy;
+  const int before = (int)(((uintptr_t)P.x + (uintptr_t)xo * ESZ) & 15u) / ESZ;   // elements from the boundary to column 0
+  const int64_t c = (int64_t)g * 8 - before;
+  if (c >= P.cols) return;
+  const bool whole = c >= 0 && c + 8 <= P.cols;
+  const Columns<true, 8> cols(c, 1, 0, P.cols);
+  Piece<TY, true, 8> x, res;
+  float xv[8], rv[8];
+  if (whole) {
+    cols.load(P.x, xo, x);
+    if (RES) cols.load(P.res, ro, res);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = c + k >= 0 && c + k < P.cols;
+      auto at = [&](const void* p, int64_t i) {
+        return TY == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)p)[i]) : ((const float*)p)[i];
+      };
+      xv[k] = in ? at(P.x, xo + c + k) : 0.0f;
+      rv[k] = RES && in ? at(P.res, ro + c + k) : 0.0f;
+    }
+  }
+  const uint64_t off = P.offset + (P.counter ? *P.counter : 0);
+  const uint32_t lo = (uint32_t)off, hi = (uint32_t)(off >> 32);
+  const int shift = (int)(c & 3);
+  const uint32_t quad = (uint32_t)(c >> 2);        // of columns before the row's first: words that nothing takes
+  const uint4 w0 = philox(quad, row, lo, hi, P.key), w1 = philox(quad + 1, row, lo, hi, P.key);
+  uint4 w2 = w1;
+  if (shift) w2 = philox(quad + 2, row, lo, hi, P.key);
+  uint32_t w[12] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w, w2.x, w2.y, w2.z, w2.w};
+#pragma unroll
+  for (int k = 0; k < 11; ++k) w[k] = shift & 1 ? w[k + 1] : w[k];
+#pragma unroll
+  for (int k = 0; k < 9; ++k) w[k] = shift & 2 ? w[k + 2] : w[k];
+  float y[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    y[k] = (w[k] > P.last_dropped || P.keep_all) ? __fmul_rn(whole ? x.get(k) : xv[k], P.scale) : 0.0f;
+    if (RES) y[k] = __fadd_rn(whole ? res.get(k) : rv[k], y[k]);
+  }
+  if (whole) {
+    cols.template store<TY>(P.y, yo, y);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k >= 0 && c + k < P.cols) {
+        if constexpr (TY == PSK_BF16) ((uint16_t*)P.y)[yo + c + k] = f32_to_bf16_bits(y[k]);
+        else ((float*)P.y)[yo + c + k] = y[k];
+      }
+  }
+}
+
 }  // namespace psk
 
 using namespace psk;
@@ -109,8 +173,6 @@ extern "C" int psk_dropout(const void* x, int32_t xt, const void* residual, int3
   DropoutParams P{};
   P.x = x, P.res = residual, P.y = y;
   P.ldx = ldx, P.ldr = ldr, P.ldy = ldy, P.cols = cols;
-  const uint64_t per_row = (uint64_t)(cols + 7) / 8;
-  P.per_row = FastDiv((uint32_t)per_row);
   uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
   for (int r = 0; r < 10; ++r, k0 += PHILOX_W0, k1 += PHILOX_W1) P.key[2 * r] = k0, P.key[2 * r + 1] = k1;
   P.offset = offset, P.counter = counter;
@@ -120,6 +182,15 @@ extern "C" int psk_dropout(const void* x, int32_t xt, const void* residual, int3
   P.scale = (float)(1.0 / (1.0 - p));
   const bool vec = cols % 8 == 0 && rows_vec8(x, xt, ldx, rows) && rows_vec8(y, yt, ldy, rows) &&
                    (!residual || rows_vec8(residual, rt, ldr, rows));
+  // Unaligned rows that begin equally far from a 16-byte boundary: shifted
+  // groups (16384 x 3001 bf16 with residual: see the kernel's figures); others
+  // element by element.
+  auto alike = [&](const void* p, int32_t dt, int64_t ld) {
+    return dt == xt && ((uintptr_t)p - (uintptr_t)x) % 16 == 0 && (rows == 1 || ((ld - ldx) * dtype_size(xt)) % 16 == 0);
+  };
+  const bool shifted = !vec && alike(y, yt, ldy) && (!residual || alike(residual, rt, ldr));
+  const uint64_t per_row = shifted ? (uint64_t)(cols + 7 + 7) / 8 : (uint64_t)(cols + 7) / 8;
+  P.per_row = FastDiv((uint32_t)per_row);
   cudaStream_t s = (cudaStream_t)stream;
   // Slices of rows whose groups are counted in 32 bits (one slice up to
   // 2^35 elements).
@@ -130,6 +201,12 @@ extern "C" int psk_dropout(const void* x, int32_t xt, const void* residual, int3
     P.items = (uint32_t)(nr * per_row);
     const unsigned grid = (unsigned)(((uint64_t)P.items + DROP_THREADS - 1) / DROP_THREADS);
     with_dtype(xt, [&](auto XT) {
+      if (shifted) {
+        return with_bool(residual != nullptr, [&](auto RES) {
+          dropout_shifted_kernel<XT.value, RES.value><<<grid, DROP_THREADS, 0, s>>>(P);
+          return 0;
+        });
+      }
       return with_dtype(yt, [&](auto YT) {
         return with_bool(vec, [&](auto VEC) {
           if (!residual)

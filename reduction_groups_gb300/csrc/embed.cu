@@ -6,7 +6,8 @@
 // id's positions stay in increasing order), the sorted list is cut into runs
 // of EMB_RUN entries, each run is summed left to right by its own warps, and
 // an id whose entries span several runs has its run sums joined left to
-// right.  The order of every sum is fixed by the ids alone.
+// right, by whichever of the runs' warps finishes last.  The order of every sum
+// is fixed by the ids alone.
 #include "vec8.cuh"
 #include "pair.cuh"
 
@@ -79,16 +80,19 @@ constexpr int SORT_TILE = SORT_THREADS * SORT_PER_LANE;   // ids scanned at a ti
 constexpr int SORT_BINS = 2048;                           // most ids of a slice
 constexpr int SORT_LIST = SORT_TILE;                      // entries ranked at a time
 
+constexpr uint32_t NO_ID = 0xFFFFFFFFu;
+constexpr int SMALL_TOKENS = 128;                         // longest list that needs no sort
+
 struct EmbedGradParams {
   const void* ids;
   const void* ct;
   void* d;
   int64_t vocab, cols, ldc, ldd;
   int64_t tokens;
-  uint32_t* key;         // the sorted ids of the positions that have one ...
+  uint32_t* key;         // the sorted ids of the positions that have one, NO_ID after them ...
   uint32_t* pos;         // ... and the positions
-  uint8_t* seen;         // per id: does it occur
-  uint32_t* entries;     // length of the sorted list
+  uint2* places;         // per id: its first place in the sorted list, its number of places
+  uint32_t* arrived;     // per run and column slice: run sums in of the id that begins there and goes on
   float* head;           // per run: the sum of its leading entries whose id the run before ends with
   float* tail;           // per run: the sum of its trailing entries whose id the next run goes on with
   int64_t pcols;         // row length of head and tail
@@ -97,7 +101,6 @@ struct EmbedGradParams {
   FastDiv per_slice;     // by slice_ids
   int32_t accumulate;
   int32_t slices;        // column slices of a row in the run sums
-  int32_t join_slices;   // and in their join
   int32_t run_ctas;      // CTAs of the run sums; the others zero the rows that do not occur
   float scale;
 };
@@ -249,8 +252,11 @@ __global__ void __launch_bounds__(2 * SORT_THREADS) embed_sort_kernel(const __gr
   for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xFFFFFFFFu, below, o);
   if (lane == 0) atomicAdd(&S.below, below);
   sort_sync();
-  for (int b = tid; b < bins; b += SORT_THREADS) P.seen[first + b] = S.place[b] != 0;
-  if (tid == 0 && blockIdx.x + 1 == gridDim.x) *P.entries = S.below + n;
+  const int64_t runs = (P.tokens + EMB_RUN - 1) / EMB_RUN;
+  for (int64_t i = (int64_t)blockIdx.x * SORT_THREADS + tid; i < runs * P.slices; i += (int64_t)gridDim.x * SORT_THREADS)
+    P.arrived[i] = 0;
+  if (blockIdx.x + 1 == gridDim.x)
+    for (int64_t i = (int64_t)S.below + n + tid; i < P.tokens; i += SORT_THREADS) P.key[i] = NO_ID;
   // Counts to first places: four neighbouring ids a thread.
   static_assert(SORT_BINS == 4 * SORT_THREADS, "four ids a thread");
   uint32_t c[4], sum = 0;
@@ -273,7 +279,10 @@ __global__ void __launch_bounds__(2 * SORT_THREADS) embed_sort_kernel(const __gr
     if (w < warp) at += S.warp_total[w];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    if (4 * tid + k < bins) S.place[4 * tid + k] = at;
+    if (4 * tid + k < bins) {
+      S.place[4 * tid + k] = at;
+      P.places[first + 4 * tid + k] = make_uint2(at, c[k]);
+    }
     at += c[k];
   }
   sort_sync();
@@ -296,7 +305,7 @@ __global__ void __launch_bounds__(2 * SORT_THREADS) embed_sort_kernel(const __gr
   rank_list(held);
 }
 
-template <int DT, bool VEC, int NC>
+template <int DT, bool VEC, int NC, bool ACC>
 __device__ __forceinline__ void write_row(const EmbedGradParams& P, const Columns<VEC, NC>& cols, uint32_t id, const f2* sum) {
   float o[NC];
 #pragma unroll
@@ -305,7 +314,7 @@ __device__ __forceinline__ void write_row(const EmbedGradParams& P, const Column
     o[2 * k] = v.x, o[2 * k + 1] = v.y;
   }
   const int64_t row = (int64_t)id * P.ldd;
-  if (P.accumulate) {
+  if (ACC) {
     Piece<DT, VEC, NC> old;
     cols.load(P.d, row, old);
 #pragma unroll
@@ -314,38 +323,84 @@ __device__ __forceinline__ void write_row(const EmbedGradParams& P, const Column
   cols.template store<DT>(P.d, row, o);
 }
 
+// A run sum of an id whose entries span several runs: kept, and by the warp
+// that brings the last of them all joined in order and written.
+template <int DT, bool VEC, int NC, bool ACC>
+__device__ __forceinline__ void join_runs(const EmbedGradParams& P, const Columns<VEC, NC>& cols, int64_t run, int slice,
+                                          uint32_t id, bool head, const f2* sum) {
+  float o[NC];
+#pragma unroll
+  for (int k = 0; k < NC; ++k) o[k] = k & 1 ? sum[k / 2].y : sum[k / 2].x;
+  cols.template store<PSK_F32>(head ? P.head : P.tail, run * P.pcols, o);
+  const uint2 place = P.places[id];
+  const int64_t begin = place.x / EMB_RUN, last = (place.x + place.y - 1) / EMB_RUN;
+  __threadfence();
+  __syncwarp();
+  uint32_t before = 0;
+  if ((threadIdx.x & 31) == 0) before = atomicAdd(&P.arrived[begin * P.slices + slice], 1u);
+  before = __shfl_sync(0xFFFFFFFFu, before, 0);
+  if (before != (uint32_t)(last - begin)) return;
+  __threadfence();
+  f2 acc[NC / 2];
+  Piece<PSK_F32, VEC, NC> t;
+  cols.load_l2(P.tail, begin * P.pcols, t);
+#pragma unroll
+  for (int k = 0; k < NC / 2; ++k) acc[k] = f2{t.get(2 * k), t.get(2 * k + 1)};
+  constexpr int GROUP = 64 / NC;
+  for (int64_t r = begin + 1; r <= last; r += GROUP) {
+    Piece<PSK_F32, VEC, NC> v[GROUP];
+#pragma unroll
+    for (int j = 0; j < GROUP; ++j)
+      if (r + j <= last) cols.load_l2(P.head, (r + j) * P.pcols, v[j]);
+#pragma unroll
+    for (int j = 0; j < GROUP; ++j)
+      if (r + j <= last) {
+#pragma unroll
+        for (int k = 0; k < NC / 2; ++k) acc[k] = f2_add(acc[k], f2{v[j].get(2 * k), v[j].get(2 * k + 1)});
+      }
+  }
+  write_row<DT, VEC, NC, ACC>(P, cols, id, acc);
+}
+
 // The first run_ctas CTAs: one run and one slice of 32 NC columns a warp.  The
 // others zero the rows of ids that do not occur.
-template <int CT, int DT, bool VEC, int NC>
-__global__ void __launch_bounds__(EMB_THREADS) embed_runs_kernel(const __grid_constant__ EmbedGradParams P) {
+template <int CT, int DT, bool VEC, int NC, bool ACC>
+__global__ void __launch_bounds__(EMB_THREADS, 2) embed_runs_kernel(const __grid_constant__ EmbedGradParams P) {
   const int lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if ((int)blockIdx.x >= P.run_ctas) {
+    // A warp's rows are a grid's warps apart; it looks 32 of them up at once.
     const int64_t warps = (int64_t)(gridDim.x - P.run_ctas) * (EMB_THREADS / 32);
-    for (int64_t v = ((int64_t)(blockIdx.x - P.run_ctas) * EMB_THREADS + threadIdx.x) >> 5; v < P.vocab; v += warps)
-      if (!P.seen[v] && (int)((uint32_t)v - P.per_slice.div((uint32_t)v) * P.slice_ids) >= P.fill_ids)
-        zero_row<DT, VEC>(P, v, lane);
+    for (int64_t v0 = ((int64_t)(blockIdx.x - P.run_ctas) * EMB_THREADS + threadIdx.x) >> 5; v0 < P.vocab; v0 += 32 * warps) {
+      const int64_t v = v0 + lane * warps;
+      const bool zero = v < P.vocab && P.places[v].y == 0 &&
+                        (int)((uint32_t)v - P.per_slice.div((uint32_t)v) * P.slice_ids) >= P.fill_ids;
+      for (uint32_t m = __ballot_sync(0xFFFFFFFFu, zero); m; m &= m - 1)
+        zero_row<DT, VEC>(P, v0 + (__ffs(m) - 1) * warps, lane);
+    }
     return;
   }
   const int64_t w = ((int64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5;
   const int64_t run = w / P.slices;
   const int64_t i0 = run * EMB_RUN;
-  const int64_t entries = *P.entries;
-  if (i0 >= entries) return;
+  if (i0 >= P.tokens) return;
   const Columns<VEC, NC> cols((w - run * P.slices) * (32 * NC), 32, lane, P.cols);
-  const int n = entries - i0 < EMB_RUN ? (int)(entries - i0) : EMB_RUN;
-  const uint32_t my_key = lane < n ? P.key[i0 + lane] : 0xFFFFFFFFu;
-  const uint32_t my_pos = lane < n ? P.pos[i0 + lane] : 0;
-  const uint32_t after = i0 + n < entries ? P.key[i0 + n] : 0xFFFFFFFFu;
-  const uint32_t prior = i0 > 0 ? P.key[i0 - 1] : 0xFFFFFFFFu;
+  const uint32_t my_key = i0 + lane < P.tokens ? P.key[i0 + lane] : NO_ID;
+  const uint32_t my_pos = i0 + lane < P.tokens ? P.pos[i0 + lane] : 0;
+  const uint32_t after = i0 + EMB_RUN < P.tokens ? P.key[i0 + EMB_RUN] : NO_ID;
+  const uint32_t prior = i0 > 0 ? P.key[i0 - 1] : NO_ID;
+  const int n = __popc(__ballot_sync(0xFFFFFFFFu, my_key != NO_ID));
   const uint32_t next_key = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
   // Entries after which the sum ends: the id's last of this run.
   const uint32_t ends = __ballot_sync(0xFFFFFFFFu, lane < n && (lane == n - 1 || next_key != my_key));
   bool head = prior == __shfl_sync(0xFFFFFFFFu, my_key, 0);
-  f2 acc[NC / 2];
+  // Sums of this run alone are written as they end; the first, of an id begun
+  // before, and the last, of an id that goes on, are kept for after.
+  f2 acc[NC / 2], lead[NC / 2];
 #pragma unroll
-  for (int k = 0; k < NC / 2; ++k) acc[k] = f2{0.0f, 0.0f};
+  for (int k = 0; k < NC / 2; ++k) acc[k] = lead[k] = f2{0.0f, 0.0f};
+  const bool leads = head;
+  const bool goes_on = n == EMB_RUN && after == __shfl_sync(0xFFFFFFFFu, my_key, EMB_RUN - 1);
   // Rows in flight: 32 registers' worth (a whole load of 16 bytes each where VEC).
   constexpr int GROUP = 64 / Piece<CT, VEC, NC>::W < 16 ? 64 / Piece<CT, VEC, NC>::W : 16;
   for (int e0 = 0; e0 < n; e0 += GROUP) {
@@ -363,70 +418,119 @@ __global__ void __launch_bounds__(EMB_THREADS) embed_runs_kernel(const __grid_co
         for (int k = 0; k < NC / 2; ++k) acc[k] = f2_add(acc[k], f2{v[j].get(2 * k), v[j].get(2 * k + 1)});
         if ((ends >> e) & 1) {
           const uint32_t id = __shfl_sync(0xFFFFFFFFu, my_key, e);
-          if (head || (e == n - 1 && after == id)) {
-            float o[NC];
+          if (head) {
 #pragma unroll
-            for (int k = 0; k < NC; ++k) o[k] = k & 1 ? acc[k / 2].y : acc[k / 2].x;
-            cols.template store<PSK_F32>(head ? P.head : P.tail, run * P.pcols, o);
+            for (int k = 0; k < NC / 2; ++k) lead[k] = acc[k];
+            head = false;
+          } else if (e == EMB_RUN - 1 && goes_on) {
+            break;
           } else {
-            write_row<DT, VEC, NC>(P, cols, id, acc);
+            write_row<DT, VEC, NC, ACC>(P, cols, id, acc);
           }
-          head = false;
 #pragma unroll
           for (int k = 0; k < NC / 2; ++k) acc[k] = f2{0.0f, 0.0f};
         }
       }
     }
   }
+  const int slice = (int)(w - run * P.slices);
+  const uint32_t first_id = __shfl_sync(0xFFFFFFFFu, my_key, 0), last_id = __shfl_sync(0xFFFFFFFFu, my_key, EMB_RUN - 1);
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    // A run all of one id that began before is a leading sum only.
+    if (which == 0 ? !leads || n == 0 : !goes_on || (leads && first_id == last_id)) continue;
+    f2 v[NC / 2];
+#pragma unroll
+    for (int k = 0; k < NC / 2; ++k) v[k] = which == 0 ? lead[k] : acc[k];
+    join_runs<DT, VEC, NC, ACC>(P, cols, run, slice, which == 0 ? first_id : last_id, which == 0, v);
+  }
 }
 
-// Join the run sums of each id whose entries span several runs: the warps of
-// the run it begins in, four columns a lane and sixteen run sums in flight (a
-// frequent id's join is a chain of such batches).
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(EMB_THREADS) embed_join_kernel(const __grid_constant__ EmbedGradParams P) {
-  constexpr int NC = 4;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t w = ((int64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5;
+// The gradient of up to SMALL_TOKENS tokens in one launch, with the same order
+// of every sum: the warps of an id's first position find its others by
+// comparing all ids (four a lane), and where the sorted list's runs would cut
+// its entries by counting the smaller ids; other CTAs zero the rows of ids that
+// do not occur.
+template <int CT, int DT, bool I64, bool VEC>
+__global__ void __launch_bounds__(EMB_THREADS) embed_small_kernel(const __grid_constant__ EmbedGradParams P) {
+  constexpr int PER = SMALL_TOKENS / 32, NC = 8, GROUP = 8;
   const int lane = threadIdx.x & 31;
-  const int64_t run = w / P.join_slices;
-  const int64_t i0 = run * EMB_RUN, i1 = i0 + EMB_RUN;
-  const int64_t entries = *P.entries;
-  if (i1 >= entries) return;                        // the last run goes on nowhere
-  const uint32_t id = P.key[i1 - 1], begin = P.key[i0], prior = i0 > 0 ? P.key[i0 - 1] : 0xFFFFFFFFu;
-  if (P.key[i1] != id || (begin == id && prior == id)) return;   // ends here, or begun in an earlier run
-  // Its last run: 32 run beginnings at a time.
-  int64_t last = run + 1;
-  for (;;) {
-    const int64_t q = last + 1 + lane;
-    const bool goes_on = q * EMB_RUN < entries && P.key[q * EMB_RUN] == id;
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, goes_on);
-    if (m != 0xFFFFFFFFu) {
-      last += __ffs(~m) - 1;
-      break;
+  uint32_t ids[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int64_t id = lane + 32 * k < P.tokens ? load_id<I64>(P.ids, lane + 32 * k) : -1;
+    ids[k] = id >= 0 && id < P.vocab ? (uint32_t)id : NO_ID;
+  }
+  if ((int)blockIdx.x >= P.run_ctas) {
+    const int64_t warps = (int64_t)(gridDim.x - P.run_ctas) * (EMB_THREADS / 32);
+    for (int64_t v = ((int64_t)(blockIdx.x - P.run_ctas) * EMB_THREADS + threadIdx.x) >> 5; v < P.vocab; v += warps) {
+      bool mine = false;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) mine = mine || ids[k] == (uint32_t)v;
+      if (!__any_sync(0xFFFFFFFFu, mine)) zero_row<DT, VEC>(P, v, lane);
     }
-    last += 32;
+    return;
   }
-  const Columns<VEC, NC> cols((w - run * P.join_slices) * (32 * NC), 32, lane, P.cols);
-  f2 acc[NC / 2];
-  Piece<PSK_F32, VEC, NC> t;
-  cols.load(P.tail, run * P.pcols, t);
+  const int w = (int)(((int64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5);
+  const int p = w / P.slices;
+  if (p >= P.tokens) return;
+  const Columns<VEC, NC> cols((int64_t)(w - p * P.slices) * (32 * NC), 32, lane, P.cols);
+  uint32_t id = NO_ID;
 #pragma unroll
-  for (int k = 0; k < NC / 2; ++k) acc[k] = f2{t.get(2 * k), t.get(2 * k + 1)};
-  constexpr int GROUP = 64 / NC;
-  for (int64_t r = run + 1; r <= last; r += GROUP) {
-    Piece<PSK_F32, VEC, NC> v[GROUP];
-#pragma unroll
-    for (int j = 0; j < GROUP; ++j)
-      if (r + j <= last) cols.load(P.head, (r + j) * P.pcols, v[j]);
-#pragma unroll
-    for (int j = 0; j < GROUP; ++j)
-      if (r + j <= last) {
-#pragma unroll
-        for (int k = 0; k < NC / 2; ++k) acc[k] = f2_add(acc[k], f2{v[j].get(2 * k), v[j].get(2 * k + 1)});
-      }
+  for (int k = 0; k < PER; ++k) {
+    const uint32_t u = __shfl_sync(0xFFFFFFFFu, ids[k], p & 31);
+    if (k == p >> 5) id = u;
   }
-  write_row<DT, VEC, NC>(P, cols, id, acc);
+  uint32_t at[PER];
+  int place = 0;                                  // of the id's next entry in the sorted list
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    at[k] = __ballot_sync(0xFFFFFFFFu, ids[k] == id);
+    place += __popc(__ballot_sync(0xFFFFFFFFu, ids[k] < id));
+  }
+  if (id == NO_ID) return;
+#pragma unroll
+  for (int k = 0; k < PER; ++k)
+    if ((k < p >> 5 && at[k]) || (k == p >> 5 && (at[k] & ((1u << (p & 31)) - 1)))) return;   // not the first
+  f2 acc[NC / 2], total[NC / 2];
+#pragma unroll
+  for (int k = 0; k < NC / 2; ++k) acc[k] = f2{0.0f, 0.0f};
+  bool first_run = true;
+  auto end_run = [&]() {
+#pragma unroll
+    for (int k = 0; k < NC / 2; ++k) {
+      total[k] = first_run ? acc[k] : f2_add(total[k], acc[k]);
+      acc[k] = f2{0.0f, 0.0f};
+    }
+    first_run = false;
+  };
+  bool any = false;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    for (uint32_t m = at[k]; m;) {
+      Piece<CT, VEC, NC> v[GROUP];
+      int got = 0;
+#pragma unroll
+      for (int j = 0; j < GROUP; ++j)
+        if (m) {
+          cols.load(P.ct, (int64_t)(32 * k + __ffs(m) - 1) * P.ldc, v[j]);
+          m &= m - 1;
+          ++got;
+        }
+#pragma unroll
+      for (int j = 0; j < GROUP; ++j)
+        if (j < got) {
+          if (any && place % EMB_RUN == 0) end_run();
+          any = true;
+          ++place;
+#pragma unroll
+          for (int q = 0; q < NC / 2; ++q) acc[q] = f2_add(acc[q], f2{v[j].get(2 * q), v[j].get(2 * q + 1)});
+        }
+    }
+  }
+  end_run();
+  if (P.accumulate) write_row<DT, VEC, NC, true>(P, cols, id, total);
+  else write_row<DT, VEC, NC, false>(P, cols, id, total);
 }
 
 // The gradient of no tokens.
@@ -455,10 +559,17 @@ static void launch_after(K kernel, unsigned grid, int threads, cudaStream_t s, c
 
 static uint64_t align256(uint64_t n) { return (n + 255) / 256 * 256; }
 
-// Workspace layout: the sorted list, what occurs, the list's length, the head
-// and tail run sums.
+// Column slices of the run sums: eight columns a lane, or four where eight
+// leave fewer than 16 warps an SM of 152 (latency then counts more than the
+// instructions for each row), or into a gradient that is added to.
+static bool embed_wide(int64_t tokens, int64_t cols, bool accumulate) {
+  return !accumulate && (tokens + EMB_RUN - 1) / EMB_RUN * ((cols + 255) / 256) >= 16 * 152;
+}
+
+// Workspace layout: the sorted list, each id's places in it, the head and tail
+// run sums, their arrivals.
 struct EmbedWorkspace {
-  uint64_t key, pos, seen, entries, head, tail, bytes;
+  uint64_t key, pos, places, head, tail, arrived, bytes;
 };
 static EmbedWorkspace embed_ws_layout(int64_t tokens, int64_t vocab, int64_t cols) {
   const uint64_t runs = (uint64_t)(tokens + EMB_RUN - 1) / EMB_RUN;
@@ -466,11 +577,11 @@ static EmbedWorkspace embed_ws_layout(int64_t tokens, int64_t vocab, int64_t col
   EmbedWorkspace w;
   w.key = 0;
   w.pos = align256((uint64_t)tokens * 4);
-  w.seen = 2 * w.pos;
-  w.entries = w.seen + align256((uint64_t)vocab);
-  w.head = w.entries + 256;
+  w.places = 2 * w.pos;
+  w.head = w.places + align256((uint64_t)vocab * 8);
   w.tail = w.head + align256(runs * pcols * 4);
-  w.bytes = w.tail + align256(runs * pcols * 4);
+  w.arrived = w.tail + align256(runs * pcols * 4);
+  w.bytes = w.arrived + align256(runs * (uint64_t)((cols + 127) / 128) * 4);
   return w;
 }
 
@@ -520,17 +631,24 @@ extern "C" int psk_embed(const void* ids, int32_t idt, int64_t tokens, const voi
     const uint64_t nr = (uint64_t)tokens - r0 < slice ? (uint64_t)tokens - r0 : slice;
     P.row0 = (int64_t)r0;
     P.items = (uint32_t)(nr * P.per_row.d);
-    // Four rows a thread where that still leaves every SM full (16384 rows of
-    // 2048 bf16: see the kernel's figures); one where latency counts.
-    const bool four = (uint64_t)P.items >= 4ull * 2048 * (uint64_t)device_sm_count();
-    const uint64_t per_cta = (uint64_t)EMB_THREADS * (four ? 4 : 1);
+    // Two 16-byte loads a thread in flight: two rows of bf16 (16384 x 2048: 20.8
+    // us, one row 24.7, four 21.1), one of f32 (8000 x 4096: 33 us, two 37) or of
+    // unaligned rows, whose eight loads are enough (4000 x 7999: 29 us, four 35);
+    // one too where latency counts.
+    const bool two = vec && tt == PSK_BF16 && (uint64_t)P.items >= 2ull * 2048 * (uint64_t)device_sm_count();
+    const uint64_t per_cta = (uint64_t)EMB_THREADS * (two ? 2 : 1);
     const unsigned grid = (unsigned)(((uint64_t)P.items + per_cta - 1) / per_cta);
     with_dtype(tt, [&](auto TT) {
       return with_dtype(yt, [&](auto YT) {
         return with_bool(idt == PSK_I64, [&](auto I64) {
           return with_bool(vec, [&](auto VEC) {
-            if (four) embed_kernel<TT.value, YT.value, I64.value, VEC.value, 4><<<grid, EMB_THREADS, 0, s>>>(P);
-            else embed_kernel<TT.value, YT.value, I64.value, VEC.value, 1><<<grid, EMB_THREADS, 0, s>>>(P);
+            if constexpr (TT.value == PSK_BF16 && VEC.value) {
+              if (two) {
+                embed_kernel<TT.value, YT.value, I64.value, VEC.value, 2><<<grid, EMB_THREADS, 0, s>>>(P);
+                return 0;
+              }
+            }
+            embed_kernel<TT.value, YT.value, I64.value, VEC.value, 1><<<grid, EMB_THREADS, 0, s>>>(P);
             return 0;
           });
         });
@@ -597,40 +715,53 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
   const bool vec = cols % 8 == 0 && (tokens == 0 || rows_vec8(ct, ct_t, ldc, tokens)) && rows_vec8(dtable, dt, ldd, vocab);
   cudaStream_t s = (cudaStream_t)stream;
   const int sms = device_sm_count();
-  // Zeroing CTAs: two an SM beside the run sums, a row a warp at least.
+  // Zeroing CTAs: four an SM beside the run sums, a row a warp at least.
   int64_t zero_ctas = accumulate ? 0 : (vocab + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32);
-  if (zero_ctas > 2 * sms) zero_ctas = 2 * sms;
+  if (zero_ctas > 4 * sms) zero_ctas = 4 * sms;
   if (tokens == 0) {
     with_dtype(dt, [&](auto DT) {
       return with_bool(vec, [&](auto VEC) {
-        embed_zero_kernel<DT.value, VEC.value><<<(unsigned)zero_ctas * 4, EMB_THREADS, 0, s>>>(P);
+        embed_zero_kernel<DT.value, VEC.value><<<(unsigned)zero_ctas, EMB_THREADS, 0, s>>>(P);
         return 0;
+      });
+    });
+    return check_launch("embedding gradient kernel");
+  }
+  if (tokens <= SMALL_TOKENS) {
+    P.slices = (int32_t)((cols + 255) / 256);
+    P.run_ctas = (int32_t)((tokens * P.slices + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32));
+    with_dtype(ct_t, [&](auto CT) {
+      return with_dtype(dt, [&](auto DT) {
+        return with_bool(idt == PSK_I64, [&](auto I64) {
+          return with_bool(vec, [&](auto VEC) {
+            embed_small_kernel<CT.value, DT.value, I64.value, VEC.value>
+                <<<(unsigned)(P.run_ctas + zero_ctas), EMB_THREADS, 0, s>>>(P);
+            return 0;
+          });
+        });
       });
     });
     return check_launch("embedding gradient kernel");
   }
   char* w = (char*)workspace;
   P.key = (uint32_t*)(w + at.key), P.pos = (uint32_t*)(w + at.pos);
-  P.seen = (uint8_t*)(w + at.seen), P.entries = (uint32_t*)(w + at.entries);
+  P.places = (uint2*)(w + at.places), P.arrived = (uint32_t*)(w + at.arrived);
   P.head = (float*)(w + at.head), P.tail = (float*)(w + at.tail);
   // A sorting CTA an SM, or more where a slice would pass SORT_BINS ids.
   int64_t slice = (vocab + sms - 1) / sms;
   if (slice > SORT_BINS) slice = SORT_BINS;
   P.slice_ids = (int32_t)slice;
   P.per_slice = FastDiv((uint32_t)slice);
+  // Unaligned rows' zeros, stored one by one, would outlast the sort.
   const int64_t row_bytes = cols * dtype_size(dt), fill = SORT_FILL_BYTES / row_bytes;
-  P.fill_ids = accumulate ? 0 : (int32_t)(fill < slice ? fill : slice);
+  P.fill_ids = accumulate || !vec ? 0 : (int32_t)(fill < slice ? fill : slice);
   if (P.fill_ids == slice) zero_ctas = 0;
   const unsigned sort_ctas = (unsigned)((vocab + slice - 1) / slice);
-  // Eight columns a lane, or four where eight leave fewer than 16 warps an SM
-  // (latency then counts more than the instructions for each row).
   const int64_t runs = (tokens + EMB_RUN - 1) / EMB_RUN;
-  const bool wide = runs * ((cols + 255) / 256) >= 16 * sms;
+  const bool wide = embed_wide(tokens, cols, accumulate);
   P.slices = (int32_t)((cols + (wide ? 255 : 127)) / (wide ? 256 : 128));
   const uint64_t ctas = ((uint64_t)runs * P.slices + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32);
-  P.join_slices = (int32_t)((cols + 127) / 128);
-  const uint64_t join_ctas = ((uint64_t)runs * P.join_slices + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32);
-  if (join_ctas + 2 * sms > 0x7FFFFFFFull) return fail(PSK_E_SHAPE, "tokens x cols too large");
+  if (ctas + 4 * sms > 0x7FFFFFFFull) return fail(PSK_E_SHAPE, "tokens x cols too large");
   P.run_ctas = (int32_t)ctas;
   with_bool(idt == PSK_I64, [&](auto I64) {
     return with_dtype(dt, [&](auto DT) {
@@ -649,19 +780,12 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
     return with_dtype(dt, [&](auto DT) {
       return with_bool(vec, [&](auto VEC) {
         const unsigned grid = (unsigned)(ctas + zero_ctas);
-        if (wide) launch_after(embed_runs_kernel<CT.value, DT.value, VEC.value, 8>, grid, EMB_THREADS, s, P);
-        else launch_after(embed_runs_kernel<CT.value, DT.value, VEC.value, 4>, grid, EMB_THREADS, s, P);
+        if (accumulate) launch_after(embed_runs_kernel<CT.value, DT.value, VEC.value, 4, true>, grid, EMB_THREADS, s, P);
+        else if (wide) launch_after(embed_runs_kernel<CT.value, DT.value, VEC.value, 8, false>, grid, EMB_THREADS, s, P);
+        else launch_after(embed_runs_kernel<CT.value, DT.value, VEC.value, 4, false>, grid, EMB_THREADS, s, P);
         return 0;
       });
     });
   });
-  rc = check_launch("embedding run sums kernel");
-  if (rc || runs == 1) return rc;
-  with_dtype(dt, [&](auto DT) {
-    return with_bool(vec, [&](auto VEC) {
-      launch_after(embed_join_kernel<DT.value, VEC.value>, (unsigned)join_ctas, EMB_THREADS, s, P);
-      return 0;
-    });
-  });
-  return check_launch("embedding join kernel");
+  return check_launch("embedding run sums kernel");
 }

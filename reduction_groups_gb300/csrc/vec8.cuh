@@ -121,6 +121,19 @@ struct Columns {
       }
     }
   }
+  // The same of f32 that other SMs have just written (from L2).
+  __device__ __forceinline__ void load_l2(const float* p, int64_t row, Piece<PSK_F32, VEC, NC>& o) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < NC; i += 4) {
+        const uint4 u = has(0) ? __ldcg((const uint4*)(p + row + first + i)) : make_uint4(0, 0, 0, 0);
+        o.w[i] = u.x, o.w[i + 1] = u.y, o.w[i + 2] = u.z, o.w[i + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NC; ++k) o.w[k] = has(k) ? __ldcg((const uint32_t*)p + row + col(k)) : 0u;
+    }
+  }
   template <int TY>
   __device__ __forceinline__ void store(void* p, int64_t row, const float* v) const {
     if constexpr (VEC) {

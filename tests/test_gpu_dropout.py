@@ -105,3 +105,27 @@ def test_counter_gives_captured_replays_new_masks(R):
     R.psk_dropout(x, y, 0.4, 21, 3, stream=side)
     side.synchronize()
     same_bits(y, OT.dropout(xv, None, 0.4, 21, 3), "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [1, 3, 9, 65, 1001, 1002, 1004])
+@pytest.mark.parametrize("start,pad", [(0, 0), (1, 0), (3, 5), (5, 2), (7, 1)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rows_beginning_anywhere(R, dtype, cols, start, pad, residual):
+    """x, y and the residual alike, at every distance from a 16-byte boundary, neighbours untouched."""
+    rng = np.random.default_rng(cols + start)
+    rows, ld = 11, cols + pad
+
+    def make():
+        t, v = stored(rng.normal(size=(rows, cols)), dtype)
+        buf = torch.full((start + rows * ld + 16,), 7.0, dtype=DT[dtype], device="cuda")
+        view = buf[start:start + rows * ld].view(rows, ld)[:, :cols]
+        view.copy_(t)
+        return buf, view, v
+
+    (_, x, xv), (_, r, rv), (buf, y, _) = make(), make(), make()
+    y.fill_(float("nan"))
+    R.psk_dropout(x, y, 0.4, 99, 3, residual=r if residual else None)
+    same_bits(y.contiguous(), OT.dropout(xv, rv if residual else None, 0.4, 99, 3), dtype)
+    y.fill_(7.0)
+    assert bool((buf == 7.0).all())

@@ -146,3 +146,27 @@ def test_side_stream_and_captured_replays(R):
         torch.cuda.synchronize()
         same_bits(y, OT.embed(a, tv, 1.0), "bf16")
         same_bits(d, OT.embed_backward_f32(a, cv, vocab, 1.0)[0], "f32")
+
+
+@pytest.mark.parametrize("tokens,vocab,cols,kind", [(128, 5, 264, "one"), (128, 3, 40, "mixed"), (127, 200, 33, "mixed"),
+                                                    (100, 2, 512, "mixed"), (129, 4, 24, "mixed"), (128, 9, 8, "none")])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_short_lists(R, tokens, vocab, cols, kind, accumulate):
+    rng = np.random.default_rng(tokens * 5 + vocab)
+    a, ids = _ids(rng, tokens, vocab, "i64", kind)
+    ct, cv = stored(rng.normal(size=(tokens, cols)), "bf16")
+    d, dv = stored(rng.normal(size=(vocab, cols)), "f32")
+    R.psk_embed_backward(ids, ct, d, scale=0.7, accumulate=accumulate,
+                         workspace=scratch(R.psk_embed_workspace(tokens, vocab, cols)))
+    g, seen = OT.embed_backward_f32(a, cv, vocab, 0.7)
+    same_bits(d, np.where(seen[:, None], dv + g, dv) if accumulate else g, "f32")
+
+
+def test_a_large_table_of_few_tokens(R):
+    rng = np.random.default_rng(12)
+    for tokens in (3, 300):
+        a, ids = _ids(rng, tokens, 400000, "i32")
+        ct, cv = stored(rng.normal(size=(tokens, 24)), "f32")
+        d = torch.full((400000, 24), float("nan"), device="cuda")
+        R.psk_embed_backward(ids, ct, d, workspace=scratch(R.psk_embed_workspace(tokens, 400000, 24)))
+        same_bits(d, OT.embed_backward_f32(a, cv, 400000, 1.0)[0], "f32")
