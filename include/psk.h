@@ -432,9 +432,10 @@ int psk_embed(const void* ids, int32_t idt, int64_t tokens, const void* table, i
  * are added left to right in f32, and an id's run sums left to right; the
  * bits depend on the ids and ct alone.  ct: tokens rows (f32 or bf16, ldc >=
  * cols); dtable: vocab rows (f32 or bf16, ldd >= cols), overlapping nothing
- * else.  workspace: 16-byte aligned DEVICE scratch of at least
- * psk_embed_workspace bytes, no initialisation, one per concurrent call
- * (calls and captured graphs that may overlap in time must not share it). */
+ * else; ldc, ldd <= 2^29 where there is a second row.  workspace: 16-byte
+ * aligned DEVICE scratch of at least psk_embed_workspace bytes, no
+ * initialisation, one per concurrent call (calls and captured graphs that may
+ * overlap in time must not share it). */
 int psk_embed_workspace(int64_t tokens, int64_t vocab, int64_t cols, uint64_t* bytes);
 int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, const void* ct, int32_t ct_t, int64_t ldc,
                        double scale, void* dtable, int32_t dt, int64_t vocab, int64_t cols, int64_t ldd,

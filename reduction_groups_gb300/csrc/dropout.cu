@@ -19,19 +19,20 @@ struct DropoutParams {
   void* y;
   int64_t ldx, ldr, ldy, cols;
   uint32_t row0;               // first row of this launch
-  uint32_t items;              // groups of eight columns in this launch
-  FastDiv per_row;             // groups per row
+  uint32_t items;              // threads' worth of work in this launch
+  FastDiv per_row;             // and in a row
   uint32_t key[20];            // the ten round keys
   uint64_t offset;
   const uint64_t* counter;     // added to offset when the kernel runs; NULL for none
-  uint32_t last_dropped;       // words <= this drop their element
-  int32_t keep_all;
+  uint32_t least_kept;         // words below this drop their element
+  int32_t drop_all;
   float scale;
 };
 
 constexpr uint32_t PHILOX_M0 = 0xD2511F53u, PHILOX_M1 = 0xCD9E8D57u;
 constexpr uint32_t PHILOX_W0 = 0x9E3779B9u, PHILOX_W1 = 0xBB67AE85u;
-constexpr int DROP_THREADS = 256;
+constexpr int SHIFT_THREADS = 256;         // of the shifted kernel
+constexpr int DROP_THREADS = 128;          // 121 us for [32768, 4096] bf16 with residual; 256: 126
 
 __device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, const uint32_t* key) {
 #pragma unroll
@@ -45,10 +46,21 @@ __device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, u
   return make_uint4(c0, c1, c2, c3);
 }
 
-// One group of eight columns a thread; RT < 0: no residual.  VEC: rows of
-// whole groups, moved by 16-byte accesses, all loads issued before the
-// generator's instructions, which hide their latency.
-template <int XT, int RT, int YT, bool VEC>
+// The words' test costs every element; p = 1, which no 32-bit threshold
+// expresses, has zero words and the threshold 1 instead.
+__device__ __forceinline__ float dropped(float x, uint32_t w, const DropoutParams& P) {
+  return w >= P.least_kept ? __fmul_rn(x, P.scale) : 0.0f;
+}
+
+// Integer instructions bind as hard as HBM (wide products run at a quarter of
+// the lanes' rate, logic at half: the generator alone needs about 75 us for
+// [32768, 4096]; bf16 with residual, 805 MB: 121 us, 6.6 TB/s, without, 537 MB:
+// 107 us), so a thread takes NO groups of eight columns of one row, 256 columns
+// apart, and shares among them its row's addresses and what the first two
+// rounds know of row and offset.
+// RT < 0: no residual.  VEC: rows of whole groups, moved by 16-byte accesses;
+// all loads are issued before the generator's instructions.
+template <int XT, int RT, int YT, bool VEC, int NO>
 __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const __grid_constant__ DropoutParams P) {
   const uint64_t t = (uint64_t)blockIdx.x * DROP_THREADS + threadIdx.x;
   if (t >= P.items) return;
@@ -56,49 +68,65 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const __grid_cons
   const uint32_t g = (uint32_t)t - r * P.per_row.d;
   const uint32_t row = P.row0 + r;
   constexpr int RES = RT >= 0 ? RT : 0;
-  const int64_t c = (int64_t)g * 8;
-  const Columns<VEC, 8> cols(c, 1, 0, P.cols);
-  Piece<XT, VEC, 8> x;
-  Piece<RES, VEC, 8> res;
-  cols.load(P.x, (int64_t)row * P.ldx, x);
-  if (RT >= 0) cols.load(P.res, (int64_t)row * P.ldr, res);
-  const uint64_t off = P.offset + (P.counter ? *P.counter : 0);
-  const uint4 w0 = philox(2 * g, row, (uint32_t)off, (uint32_t)(off >> 32), P.key);
-  const uint4 w1 = philox(2 * g + 1, row, (uint32_t)off, (uint32_t)(off >> 32), P.key);
-  const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-  float y[8];
+  // NO > 1: g is a lane of a slice of 256 NO columns.
+  const int64_t c = NO > 1 ? (int64_t)(g >> 5) * (256 * NO) + (g & 31) * 8 : (int64_t)g * 8;
+  Piece<XT, VEC, 8> x[NO];
+  Piece<RES, VEC, 8> res[NO];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    y[k] = (w[k] > P.last_dropped || P.keep_all) ? __fmul_rn(x.get(k), P.scale) : 0.0f;
-    if (RT >= 0) y[k] = __fadd_rn(res.get(k), y[k]);
+  for (int j = 0; j < NO; ++j) {
+    const Columns<VEC, 8> cols(c + 256 * j, 1, 0, P.cols);
+    cols.load(P.x, (int64_t)row * P.ldx, x[j]);
+    if (RT >= 0) cols.load(P.res, (int64_t)row * P.ldr, res[j]);
   }
-  cols.template store<YT>(P.y, (int64_t)row * P.ldy, y);
+  const uint64_t off = P.offset + (P.counter ? *P.counter : 0);
+#pragma unroll
+  for (int j = 0; j < NO; ++j) {
+    const uint32_t q = (uint32_t)(c >> 2) + 64 * j;
+    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+    if (!P.drop_all) {
+      w0 = philox(q, row, (uint32_t)off, (uint32_t)(off >> 32), P.key);
+      w1 = philox(q + 1, row, (uint32_t)off, (uint32_t)(off >> 32), P.key);
+    }
+    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      y[k] = dropped(x[j].get(k), w[k], P);
+      if (RT >= 0) y[k] = __fadd_rn(res[j].get(k), y[k]);
+    }
+    Columns<VEC, 8>(c + 256 * j, 1, 0, P.cols).template store<YT>(P.y, (int64_t)row * P.ldy, y);
+  }
 }
 
 // Rows that begin anywhere, x, y and the residual of one type and alike: a
 // thread's eight elements begin at a 16-byte boundary of the row, `shift`
 // columns past a multiple of four, and take their words from three groups of
-// four columns.  A row's first and last elements go one by one.
+// four columns.  The third group is the first of the lane above: a warp has 31
+// lanes with elements, and a row a last group of no elements, for their words
+// ([16384, 3001] bf16 with residual: 72 us; each lane drawing three 87).  A
+// row's first and last elements go one by one.
 template <int TY, bool RES>
-__global__ void __launch_bounds__(DROP_THREADS) dropout_shifted_kernel(const __grid_constant__ DropoutParams P) {
+__global__ void __launch_bounds__(SHIFT_THREADS) dropout_shifted_kernel(const __grid_constant__ DropoutParams P) {
   constexpr int ESZ = TY == PSK_BF16 ? 2 : 4;
-  const uint64_t t = (uint64_t)blockIdx.x * DROP_THREADS + threadIdx.x;
-  if (t >= P.items) return;
+  const int lane = threadIdx.x & 31;
+  const uint64_t w = ((uint64_t)blockIdx.x * SHIFT_THREADS + threadIdx.x) >> 5;
+  if (w * 31 >= P.items) return;
+  const uint64_t t = min(w * 31 + lane, (uint64_t)P.items - 1);   // past the end: the last row's words again
   const uint32_t r = P.per_row.div((uint32_t)t);
   const uint32_t g = (uint32_t)t - r * P.per_row.d;
   const uint32_t row = P.row0 + r;
   const int64_t xo = (int64_t)row * P.ldx, ro = (int64_t)row * P.ldr, yo = (int64_t)row * P.ldy;
   const int before = (int)(((uintptr_t)P.x + (uintptr_t)xo * ESZ) & 15u) / ESZ;   // elements from the boundary to column 0
   const int64_t c = (int64_t)g * 8 - before;
-  if (c >= P.cols) return;
-  const bool whole = c >= 0 && c + 8 <= P.cols;
+  const bool mine = lane < 31 && c < P.cols;
+  const bool whole = mine && c >= 0 && c + 8 <= P.cols;
   const Columns<true, 8> cols(c, 1, 0, P.cols);
   Piece<TY, true, 8> x, res;
   float xv[8], rv[8];
   if (whole) {
     cols.load(P.x, xo, x);
     if (RES) cols.load(P.res, ro, res);
-  } else {
+  } else if (mine) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const bool in = c + k >= 0 && c + k < P.cols;
@@ -114,17 +142,18 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_shifted_kernel(const __g
   const int shift = (int)(c & 3);
   const uint32_t quad = (uint32_t)(c >> 2);        // of columns before the row's first: words that nothing takes
   const uint4 w0 = philox(quad, row, lo, hi, P.key), w1 = philox(quad + 1, row, lo, hi, P.key);
-  uint4 w2 = w1;
-  if (shift) w2 = philox(quad + 2, row, lo, hi, P.key);
-  uint32_t w[12] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w, w2.x, w2.y, w2.z, w2.w};
+  const uint4 w2 = make_uint4(__shfl_down_sync(0xFFFFFFFFu, w0.x, 1), __shfl_down_sync(0xFFFFFFFFu, w0.y, 1),
+                              __shfl_down_sync(0xFFFFFFFFu, w0.z, 1), __shfl_down_sync(0xFFFFFFFFu, w0.w, 1));
+  if (!mine) return;
+  uint32_t word[12] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w, w2.x, w2.y, w2.z, w2.w};
 #pragma unroll
-  for (int k = 0; k < 11; ++k) w[k] = shift & 1 ? w[k + 1] : w[k];
+  for (int k = 0; k < 11; ++k) word[k] = shift & 1 ? word[k + 1] : word[k];
 #pragma unroll
-  for (int k = 0; k < 9; ++k) w[k] = shift & 2 ? w[k + 2] : w[k];
+  for (int k = 0; k < 9; ++k) word[k] = shift & 2 ? word[k + 2] : word[k];
   float y[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    y[k] = (w[k] > P.last_dropped || P.keep_all) ? __fmul_rn(whole ? x.get(k) : xv[k], P.scale) : 0.0f;
+    y[k] = dropped(whole ? x.get(k) : xv[k], word[k], P);
     if (RES) y[k] = __fadd_rn(whole ? res.get(k) : rv[k], y[k]);
   }
   if (whole) {
@@ -177,19 +206,28 @@ extern "C" int psk_dropout(const void* x, int32_t xt, const void* residual, int3
   for (int r = 0; r < 10; ++r, k0 += PHILOX_W0, k1 += PHILOX_W1) P.key[2 * r] = k0, P.key[2 * r + 1] = k1;
   P.offset = offset, P.counter = counter;
   const uint64_t dropped = (uint64_t)__builtin_llrint(p * 4294967296.0);   // words below this drop
-  P.keep_all = dropped == 0;
-  P.last_dropped = (uint32_t)(dropped - 1);
+  P.drop_all = dropped >> 32 != 0;
+  P.least_kept = P.drop_all ? 1u : (uint32_t)dropped;
   P.scale = (float)(1.0 / (1.0 - p));
   const bool vec = cols % 8 == 0 && rows_vec8(x, xt, ldx, rows) && rows_vec8(y, yt, ldy, rows) &&
                    (!residual || rows_vec8(residual, rt, ldr, rows));
   // Unaligned rows that begin equally far from a 16-byte boundary: shifted
-  // groups (16384 x 3001 bf16 with residual: see the kernel's figures); others
-  // element by element.
+  // groups (16384 x 3001 bf16 with residual: 72 us, element by element 114);
+  // others element by element.
   auto alike = [&](const void* p, int32_t dt, int64_t ld) {
     return dt == xt && ((uintptr_t)p - (uintptr_t)x) % 16 == 0 && (rows == 1 || ((ld - ldx) * dtype_size(xt)) % 16 == 0);
   };
-  const bool shifted = !vec && alike(y, yt, ldy) && (!residual || alike(residual, rt, ldr));
-  const uint64_t per_row = shifted ? (uint64_t)(cols + 7 + 7) / 8 : (uint64_t)(cols + 7) / 8;
+  const bool shifted = !vec && !P.drop_all && alike(y, yt, ldy) && (!residual || alike(residual, rt, ldr));
+  // Four groups a thread, or two, where no more than an eighth of the lanes
+  // stays idle past the row's end and every SM still has its threads.
+  int groups = 1;
+  for (int n = 4; n > 1 && groups == 1; n /= 2) {
+    const int64_t span = 256 * n, padded = (cols + span - 1) / span * span;
+    if (vec && padded - cols <= padded / 8 && rows * (padded / (8 * n)) >= 2048 * (int64_t)device_sm_count()) groups = n;
+  }
+  const uint64_t per_row = shifted      ? (uint64_t)(cols + 7 + 7) / 8 + 1
+                           : groups > 1 ? (uint64_t)(cols + 256 * groups - 1) / (256 * groups) * 32
+                                        : (uint64_t)(cols + 7) / 8;
   P.per_row = FastDiv((uint32_t)per_row);
   cudaStream_t s = (cudaStream_t)stream;
   // Slices of rows whose groups are counted in 32 bits (one slice up to
@@ -199,24 +237,29 @@ extern "C" int psk_dropout(const void* x, int32_t xt, const void* residual, int3
     const uint64_t nr = (uint64_t)rows - r0 < slice ? (uint64_t)rows - r0 : slice;
     P.row0 = (uint32_t)r0;
     P.items = (uint32_t)(nr * per_row);
-    const unsigned grid = (unsigned)(((uint64_t)P.items + DROP_THREADS - 1) / DROP_THREADS);
+    const int threads = shifted ? SHIFT_THREADS : DROP_THREADS;
+    const uint64_t lanes = shifted ? ((uint64_t)P.items + 30) / 31 * 32 : P.items;
+    const unsigned grid = (unsigned)((lanes + threads - 1) / threads);
     with_dtype(xt, [&](auto XT) {
       if (shifted) {
         return with_bool(residual != nullptr, [&](auto RES) {
-          dropout_shifted_kernel<XT.value, RES.value><<<grid, DROP_THREADS, 0, s>>>(P);
+          dropout_shifted_kernel<XT.value, RES.value><<<grid, threads, 0, s>>>(P);
           return 0;
         });
       }
       return with_dtype(yt, [&](auto YT) {
-        return with_bool(vec, [&](auto VEC) {
+        auto launch = [&](auto VEC, auto NO) {
           if (!residual)
-            dropout_kernel<XT.value, -1, YT.value, VEC.value><<<grid, DROP_THREADS, 0, s>>>(P);
+            dropout_kernel<XT.value, -1, YT.value, VEC.value, NO.value><<<grid, threads, 0, s>>>(P);
           else if (rt == PSK_BF16)
-            dropout_kernel<XT.value, PSK_BF16, YT.value, VEC.value><<<grid, DROP_THREADS, 0, s>>>(P);
+            dropout_kernel<XT.value, PSK_BF16, YT.value, VEC.value, NO.value><<<grid, threads, 0, s>>>(P);
           else
-            dropout_kernel<XT.value, PSK_F32, YT.value, VEC.value><<<grid, DROP_THREADS, 0, s>>>(P);
+            dropout_kernel<XT.value, PSK_F32, YT.value, VEC.value, NO.value><<<grid, threads, 0, s>>>(P);
           return 0;
-        });
+        };
+        if (groups == 4) return launch(std::true_type{}, std::integral_constant<int, 4>{});
+        if (groups == 2) return launch(std::true_type{}, std::integral_constant<int, 2>{});
+        return with_bool(vec, [&](auto VEC) { return launch(VEC, std::integral_constant<int, 1>{}); });
       });
     });
     const int rc = check_launch("dropout kernel");

@@ -24,8 +24,8 @@ struct EmbedParams {
   void* y;
   int64_t vocab, cols, ldt, ldy;
   int64_t row0;
-  uint32_t items;
-  FastDiv per_row;
+  uint32_t warps;        // of this launch: one for each slice of 256 NO columns of each row
+  FastDiv slices;        // of a row
   float scale;
 };
 
@@ -34,39 +34,33 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int64_t i) {
   return I64 ? ((const int64_t*)ids)[i] : (int64_t)((const int32_t*)ids)[i];
 }
 
-// Eight columns a thread of ROWS rows, all of their loads in flight at once.
-// VEC: an item is a group of eight neighbouring columns of a row; else an item
-// is a lane of a 256-column slice, whose columns are 32 apart.
-template <int TT, int YT, bool I64, bool VEC, int ROWS>
+// A warp's slice of a row: NO groups of eight columns a lane, 256 columns apart,
+// all of their loads in flight.  (A thread for each group spent more integer
+// instructions, at half of the lanes' rate, on its row's addresses than the
+// 33 million values of a 16384 x 2048 lookup could hide.)
+template <int TT, int YT, bool I64, bool VEC, int NO>
 __global__ void __launch_bounds__(EMB_THREADS) embed_kernel(const __grid_constant__ EmbedParams P) {
-  const uint64_t t0 = (uint64_t)blockIdx.x * EMB_THREADS + threadIdx.x;
-  const uint64_t stride = (uint64_t)gridDim.x * EMB_THREADS;
-  Piece<TT, VEC, 8> v[ROWS];
-  int64_t id[ROWS], row[ROWS];
-  uint32_t g[ROWS];
+  const uint32_t w = (uint32_t)(((uint64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5);
+  if (w >= P.warps) return;
+  const uint32_t r = P.slices.div(w);
+  const int64_t c = (int64_t)(w - r * P.slices.d) * (256 * NO);
+  const int lane = threadIdx.x & 31;
+  const int64_t row = P.row0 + r, id = load_id<I64>(P.ids, row);
+  if (id >= 0 && id < P.vocab) {
+    Piece<TT, VEC, 8> v[NO];
 #pragma unroll
-  for (int q = 0; q < ROWS; ++q) {
-    const uint64_t t = t0 + q * stride;
-    const uint32_t r = P.per_row.div((uint32_t)t);
-    g[q] = (uint32_t)t - r * P.per_row.d;
-    row[q] = t < P.items ? P.row0 + r : -1;
-    id[q] = row[q] >= 0 ? load_id<I64>(P.ids, row[q]) : -1;
-  }
-  auto columns = [&](int q) {
-    return VEC ? Columns<VEC, 8>((int64_t)g[q] * 8, 1, 0, P.cols)
-               : Columns<VEC, 8>((int64_t)(g[q] / 32) * 256, 32, g[q] % 32, P.cols);
-  };
+    for (int j = 0; j < NO; ++j) Columns<VEC, 8>(c + 256 * j, 32, lane, P.cols).load(P.table, id * P.ldt, v[j]);
 #pragma unroll
-  for (int q = 0; q < ROWS; ++q)
-    if (id[q] >= 0 && id[q] < P.vocab) columns(q).load(P.table, id[q] * P.ldt, v[q]);
+    for (int j = 0; j < NO; ++j) {
+      float y[8];
 #pragma unroll
-  for (int q = 0; q < ROWS; ++q) {
-    if (row[q] < 0) continue;
-    const bool in = id[q] >= 0 && id[q] < P.vocab;
-    float y[8];
+      for (int k = 0; k < 8; ++k) y[k] = __fmul_rn(v[j].get(k), P.scale);
+      Columns<VEC, 8>(c + 256 * j, 32, lane, P.cols).template store<YT>(P.y, row * P.ldy, y);
+    }
+  } else {
+    const float z[8] = {};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = in ? __fmul_rn(v[q].get(k), P.scale) : 0.0f;
-    columns(q).template store<YT>(P.y, row[q] * P.ldy, y);
+    for (int j = 0; j < NO; ++j) Columns<VEC, 8>(c + 256 * j, 32, lane, P.cols).template store<YT>(P.y, row * P.ldy, z);
   }
 }
 
@@ -87,8 +81,9 @@ struct EmbedGradParams {
   const void* ids;
   const void* ct;
   void* d;
-  int64_t vocab, cols, ldc, ldd;
+  int64_t vocab, cols;
   int64_t tokens;
+  uint32_t ct_row, d_row;   // bytes from a row to the next: an address is one wide multiply-add
   uint32_t* key;         // the sorted ids of the positions that have one, NO_ID after them ...
   uint32_t* pos;         // ... and the positions
   uint2* places;         // per id: its first place in the sorted list, its number of places
@@ -121,11 +116,22 @@ struct SortShared {
   uint32_t below;
 };
 
-// A span of zeros: the columns of a row, by one warp.
+// A row of zeros, by one warp.
 template <int DT, bool VEC>
 __device__ __forceinline__ void zero_row(const EmbedGradParams& P, int64_t row, int lane) {
-  const float z[8] = {};
-  for (int64_t c = 0; c < P.cols; c += 256) Columns<VEC, 8>(c, 32, lane, P.cols).template store<DT>(P.d, row * P.ldd, z);
+  char* q = (char*)P.d + (uint64_t)row * P.d_row;
+  constexpr int ESZ = DT == PSK_BF16 ? 2 : 4;
+  const int64_t bytes = P.cols * ESZ;
+  if constexpr (VEC) {
+#pragma unroll 1
+    for (int64_t c = lane * 16; c < bytes; c += 512) *(uint4*)(q + c) = make_uint4(0, 0, 0, 0);
+  } else {
+#pragma unroll 4
+    for (int64_t c = lane * ESZ; c < bytes; c += 32 * ESZ) {
+      if constexpr (DT == PSK_BF16) *(uint16_t*)(q + c) = 0;
+      else *(uint32_t*)(q + c) = 0;
+    }
+  }
 }
 
 // Barrier of the sorting threads.
@@ -313,14 +319,14 @@ __device__ __forceinline__ void write_row(const EmbedGradParams& P, const Column
     const f2 v = f2_mul(sum[k], f2_splat(P.scale));
     o[2 * k] = v.x, o[2 * k + 1] = v.y;
   }
-  const int64_t row = (int64_t)id * P.ldd;
+  char* q = (char*)cols.template at<DT>(P.d) + (uint64_t)id * P.d_row;
   if (ACC) {
     Piece<DT, VEC, NC> old;
-    cols.load(P.d, row, old);
+    cols.load_at(q, old);
 #pragma unroll
     for (int k = 0; k < NC; ++k) o[k] = __fadd_rn(old.get(k), o[k]);
   }
-  cols.template store<DT>(P.d, row, o);
+  cols.template store_at<DT>(q, o);
 }
 
 // A run sum of an id whose entries span several runs: kept, and by the warp
@@ -382,50 +388,51 @@ __global__ void __launch_bounds__(EMB_THREADS, 2) embed_runs_kernel(const __grid
   }
   const int64_t w = ((int64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5;
   const int64_t run = w / P.slices;
+  const int slice = (int)(w - run * P.slices);
   const int64_t i0 = run * EMB_RUN;
   if (i0 >= P.tokens) return;
-  const Columns<VEC, NC> cols((w - run * P.slices) * (32 * NC), 32, lane, P.cols);
+  const Columns<VEC, NC> cols((int64_t)slice * (32 * NC), 32, lane, P.cols);
   const uint32_t my_key = i0 + lane < P.tokens ? P.key[i0 + lane] : NO_ID;
   const uint32_t my_pos = i0 + lane < P.tokens ? P.pos[i0 + lane] : 0;
   const uint32_t after = i0 + EMB_RUN < P.tokens ? P.key[i0 + EMB_RUN] : NO_ID;
   const uint32_t prior = i0 > 0 ? P.key[i0 - 1] : NO_ID;
   const int n = __popc(__ballot_sync(0xFFFFFFFFu, my_key != NO_ID));
+  if (n == 0) return;
   const uint32_t next_key = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
-  // Entries after which the sum ends: the id's last of this run.
-  const uint32_t ends = __ballot_sync(0xFFFFFFFFu, lane < n && (lane == n - 1 || next_key != my_key));
-  bool head = prior == __shfl_sync(0xFFFFFFFFu, my_key, 0);
-  // Sums of this run alone are written as they end; the first, of an id begun
-  // before, and the last, of an id that goes on, are kept for after.
+  // The first id of the run may have begun in an earlier one, the last may go
+  // on in the next: their sums are joined, the others written as they end.
+  const bool leads = prior == __shfl_sync(0xFFFFFFFFu, my_key, 0);
+  const bool goes_on = n == EMB_RUN && after == __shfl_sync(0xFFFFFFFFu, my_key, EMB_RUN - 1);
+  // Entries after which a sum ends.
+  const uint32_t ends = __ballot_sync(0xFFFFFFFFu, lane < n && (lane == n - 1 ? !goes_on : next_key != my_key));
   f2 acc[NC / 2], lead[NC / 2];
 #pragma unroll
   for (int k = 0; k < NC / 2; ++k) acc[k] = lead[k] = f2{0.0f, 0.0f};
-  const bool leads = head;
-  const bool goes_on = n == EMB_RUN && after == __shfl_sync(0xFFFFFFFFu, my_key, EMB_RUN - 1);
-  // Rows in flight: 32 registers' worth (a whole load of 16 bytes each where VEC).
-  constexpr int GROUP = 64 / Piece<CT, VEC, NC>::W < 16 ? 64 / Piece<CT, VEC, NC>::W : 16;
+  bool head = leads;
+  const char* ct = cols.template at<CT>(P.ct);
+  // Rows in flight: eight of eight columns (sixteen of bf16 took the gradient of
+  // 16384 x 2048 from 48 to 52 us, in registers that then spill), sixteen of four.
+  constexpr int GROUP = 64 / NC;
   for (int e0 = 0; e0 < n; e0 += GROUP) {
     Piece<CT, VEC, NC> v[GROUP];
+    const uint32_t now = ends >> e0;
 #pragma unroll
     for (int j = 0; j < GROUP; ++j) {
-      const uint32_t p = __shfl_sync(0xFFFFFFFFu, my_pos, (e0 + j) & 31);
-      if (e0 + j < n) cols.load(P.ct, (int64_t)p * P.ldc, v[j]);
+      const uint32_t p = __shfl_sync(0xFFFFFFFFu, my_pos, e0 + j);
+      if (e0 + j < n) cols.load_at(ct + (uint64_t)p * P.ct_row, v[j]);
     }
 #pragma unroll
     for (int j = 0; j < GROUP; ++j) {
-      const int e = e0 + j;
-      if (e < n) {
+      if (e0 + j < n) {
 #pragma unroll
         for (int k = 0; k < NC / 2; ++k) acc[k] = f2_add(acc[k], f2{v[j].get(2 * k), v[j].get(2 * k + 1)});
-        if ((ends >> e) & 1) {
-          const uint32_t id = __shfl_sync(0xFFFFFFFFu, my_key, e);
+        if ((now >> j) & 1) {
           if (head) {
 #pragma unroll
             for (int k = 0; k < NC / 2; ++k) lead[k] = acc[k];
             head = false;
-          } else if (e == EMB_RUN - 1 && goes_on) {
-            break;
           } else {
-            write_row<DT, VEC, NC, ACC>(P, cols, id, acc);
+            write_row<DT, VEC, NC, ACC>(P, cols, __shfl_sync(0xFFFFFFFFu, my_key, e0 + j), acc);
           }
 #pragma unroll
           for (int k = 0; k < NC / 2; ++k) acc[k] = f2{0.0f, 0.0f};
@@ -433,12 +440,15 @@ __global__ void __launch_bounds__(EMB_THREADS, 2) embed_runs_kernel(const __grid
       }
     }
   }
-  const int slice = (int)(w - run * P.slices);
+  // A run all of one id that began before is one leading sum.
   const uint32_t first_id = __shfl_sync(0xFFFFFFFFu, my_key, 0), last_id = __shfl_sync(0xFFFFFFFFu, my_key, EMB_RUN - 1);
+  if (head && goes_on) {
+#pragma unroll
+    for (int k = 0; k < NC / 2; ++k) lead[k] = acc[k];
+  }
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
-    // A run all of one id that began before is a leading sum only.
-    if (which == 0 ? !leads || n == 0 : !goes_on || (leads && first_id == last_id)) continue;
+    if (which == 0 ? !leads : !goes_on || head) continue;
     f2 v[NC / 2];
 #pragma unroll
     for (int k = 0; k < NC / 2; ++k) v[k] = which == 0 ? lead[k] : acc[k];
@@ -513,7 +523,7 @@ __global__ void __launch_bounds__(EMB_THREADS) embed_small_kernel(const __grid_c
 #pragma unroll
       for (int j = 0; j < GROUP; ++j)
         if (m) {
-          cols.load(P.ct, (int64_t)(32 * k + __ffs(m) - 1) * P.ldc, v[j]);
+          cols.load_at(cols.template at<CT>(P.ct) + (uint64_t)(32 * k + __ffs(m) - 1) * P.ct_row, v[j]);
           m &= m - 1;
           ++got;
         }
@@ -623,28 +633,27 @@ extern "C" int psk_embed(const void* ids, int32_t idt, int64_t tokens, const voi
     return fail(PSK_E_ALIAS, "y overlaps the table");
   if (ranges_overlap(ids, (uint64_t)tokens * isz, y, yb)) return fail(PSK_E_ALIAS, "y overlaps the ids");
   const bool vec = cols % 8 == 0 && rows_vec8(table, tt, ldt, vocab) && rows_vec8(y, yt, ldy, tokens);
-  EmbedParams P{ids, table, y, vocab, cols, ldt, ldy, 0, 0,
-                FastDiv((uint32_t)(vec ? cols / 8 : (cols + 255) / 256 * 32)), (float)scale};
-  const uint64_t slice = 0xFFFFFFFFull / P.per_row.d;
+  // Four groups a lane (bf16 rows of 1024 columns and more: 16384 x 2048 18.8
+  // us, one 24.7) where that leaves every SM its warps, else one (f32, whose
+  // groups are two loads: 8000 x 4096 33 us, four 37; and decoding, where more
+  // warps mean less latency).
+  const int64_t wide = (cols + 1023) / 1024, narrow = (cols + 255) / 256;
+  const bool four = tt == PSK_BF16 && cols >= 1024 && tokens * wide >= 32 * (int64_t)device_sm_count();
+  EmbedParams P{ids, table, y, vocab, cols, ldt, ldy, 0, 0, FastDiv((uint32_t)(four ? wide : narrow)), (float)scale};
+  const uint64_t slice = 0xFFFFFFFFull / P.slices.d;
   cudaStream_t s = (cudaStream_t)stream;
   for (uint64_t r0 = 0; r0 < (uint64_t)tokens; r0 += slice) {
     const uint64_t nr = (uint64_t)tokens - r0 < slice ? (uint64_t)tokens - r0 : slice;
     P.row0 = (int64_t)r0;
-    P.items = (uint32_t)(nr * P.per_row.d);
-    // Two 16-byte loads a thread in flight: two rows of bf16 (16384 x 2048: 20.8
-    // us, one row 24.7, four 21.1), one of f32 (8000 x 4096: 33 us, two 37) or of
-    // unaligned rows, whose eight loads are enough (4000 x 7999: 29 us, four 35);
-    // one too where latency counts.
-    const bool two = vec && tt == PSK_BF16 && (uint64_t)P.items >= 2ull * 2048 * (uint64_t)device_sm_count();
-    const uint64_t per_cta = (uint64_t)EMB_THREADS * (two ? 2 : 1);
-    const unsigned grid = (unsigned)(((uint64_t)P.items + per_cta - 1) / per_cta);
+    P.warps = (uint32_t)(nr * P.slices.d);
+    const unsigned grid = (unsigned)(((uint64_t)P.warps + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32));
     with_dtype(tt, [&](auto TT) {
       return with_dtype(yt, [&](auto YT) {
         return with_bool(idt == PSK_I64, [&](auto I64) {
           return with_bool(vec, [&](auto VEC) {
-            if constexpr (TT.value == PSK_BF16 && VEC.value) {
-              if (two) {
-                embed_kernel<TT.value, YT.value, I64.value, VEC.value, 2><<<grid, EMB_THREADS, 0, s>>>(P);
+            if constexpr (TT.value == PSK_BF16) {
+              if (four) {
+                embed_kernel<TT.value, YT.value, I64.value, VEC.value, 4><<<grid, EMB_THREADS, 0, s>>>(P);
                 return 0;
               }
             }
@@ -686,6 +695,7 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
   if (ldd < cols || (tokens > 0 && ldc < cols)) return fail(PSK_E_SHAPE, "leading dimension below cols");
   if (!rows_addressable(tokens, ldc) || !rows_addressable(vocab, ldd))
     return fail(PSK_E_SHAPE, "rows x leading dimension too large");
+  if ((vocab > 1 && ldd > (1LL << 29)) || (tokens > 1 && ldc > (1LL << 29))) return fail(PSK_E_SHAPE, "leading dimension above 2^29");
   EmbedGradParams P{};
   EmbedWorkspace at{};
   const uint64_t db = rows_bytes(vocab, cols, ldd, dt);
@@ -708,7 +718,8 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
       return fail(PSK_E_ALIAS, "the workspace overlaps ct or the ids");
   }
   P.ids = ids, P.ct = ct, P.d = dtable;
-  P.vocab = vocab, P.cols = cols, P.ldc = ldc, P.ldd = ldd, P.tokens = tokens;
+  P.vocab = vocab, P.cols = cols, P.tokens = tokens;
+  P.ct_row = (uint32_t)(ldc * dtype_size(ct_t)), P.d_row = (uint32_t)(ldd * dtype_size(dt));
   P.pcols = (cols + 7) / 8 * 8;
   P.accumulate = accumulate != 0;
   P.scale = (float)scale;

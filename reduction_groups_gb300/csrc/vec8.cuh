@@ -85,17 +85,28 @@ struct Piece {
 // coalesce.  Columns from cols on are read as zeros and not written.
 template <bool VEC, int NC>
 struct Columns {
-  int64_t first, cols;
-  int stride;
-  __device__ __forceinline__ Columns(int64_t base, int T, int t, int64_t cols_)
-      : first(base + (VEC ? (int64_t)t * NC : t)), cols(cols_), stride(VEC ? 1 : T) {}
+  int64_t first;
+  int stride, present;       // of the thread's columns, those below cols
+  __device__ __forceinline__ Columns(int64_t base, int T, int t, int64_t cols)
+      : first(base + (VEC ? (int64_t)t * NC : t)), stride(VEC ? 1 : T) {
+    const int64_t left = cols - first;
+    present = VEC ? (left > 0 ? NC : 0) : left <= 0 ? 0 : left > (int64_t)(NC - 1) * T ? NC : (int)((left + T - 1) / T);
+  }
   __device__ __forceinline__ int64_t col(int k) const { return first + (int64_t)k * stride; }
-  __device__ __forceinline__ bool has(int k) const { return VEC ? first < cols : col(k) < cols; }
+  __device__ __forceinline__ bool has(int k) const { return k < present; }
+  // Where the thread's columns of the row at element `row` begin.
+  template <int TY>
+  __device__ __forceinline__ const char* at(const void* p, int64_t row = 0) const {
+    return (const char*)p + (row + first) * (TY == PSK_BF16 ? 2 : 4);
+  }
   template <int TY>
   __device__ __forceinline__ void load(const void* p, int64_t row, Piece<TY, VEC, NC>& o) const {
+    load_at(at<TY>(p, row), o);
+  }
+  template <int TY>
+  __device__ __forceinline__ void load_at(const char* q, Piece<TY, VEC, NC>& o) const {
     if constexpr (VEC) {
       constexpr int W = Piece<TY, VEC, NC>::W;
-      const char* q = (const char*)p + (row + first) * (TY == PSK_BF16 ? 2 : 4);
 #pragma unroll
       for (int i = 0; i < W; ++i) o.w[i] = 0;
       if (has(0)) {
@@ -115,8 +126,8 @@ struct Columns {
       for (int k = 0; k < NC; ++k) {
         o.w[k] = 0;
         if (has(k)) {
-          if constexpr (TY == PSK_BF16) o.w[k] = ((const uint16_t*)p)[row + col(k)];
-          else o.w[k] = ((const uint32_t*)p)[row + col(k)];
+          if constexpr (TY == PSK_BF16) o.w[k] = ((const uint16_t*)q)[k * stride];
+          else o.w[k] = ((const uint32_t*)q)[k * stride];
         }
       }
     }
@@ -136,9 +147,12 @@ struct Columns {
   }
   template <int TY>
   __device__ __forceinline__ void store(void* p, int64_t row, const float* v) const {
+    store_at<TY>((char*)at<TY>(p, row), v);
+  }
+  template <int TY>
+  __device__ __forceinline__ void store_at(char* q, const float* v) const {
     if constexpr (VEC) {
       if (has(0)) {
-        char* q = (char*)p + (row + first) * (TY == PSK_BF16 ? 2 : 4);
         if constexpr (TY == PSK_BF16) {
           if constexpr (NC == 4) *(uint2*)q = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
           else
@@ -153,8 +167,8 @@ struct Columns {
 #pragma unroll
       for (int k = 0; k < NC; ++k)
         if (has(k)) {
-          if constexpr (TY == PSK_BF16) ((uint16_t*)p)[row + col(k)] = f32_to_bf16_bits(v[k]);
-          else ((float*)p)[row + col(k)] = v[k];
+          if constexpr (TY == PSK_BF16) ((uint16_t*)q)[k * stride] = f32_to_bf16_bits(v[k]);
+          else ((float*)q)[k * stride] = v[k];
         }
     }
   }

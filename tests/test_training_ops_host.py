@@ -140,6 +140,14 @@ def test_policy_loss_refusals(native, change, name):
     _refused(native, native.lib().psk_policy_loss(*{**ok, **change}.values()), name)
 
 
+def test_embed_backward_refuses_rows_too_far_apart(native):
+    L, far = native.lib(), (1 << 29) + 8
+    ok = dict(ids=A, idt=I64, tokens=4, ct=B, ct_t=F32, ldc=8, scale=1.0, d=C, dt=F32, vocab=10, cols=8, ldd=8,
+              accumulate=0, ws=W, wb=_embed_ws(native), s=0)
+    for change in (dict(ldc=far), dict(ldd=far)):
+        _refused(native, L.psk_embed_backward(*{**ok, **change}.values()), "PSK_E_SHAPE")
+
+
 def test_workspace_sizes(native):
     L, v = native.lib(), ctypes.c_uint64(0)
     assert _embed_ws(native, 0, 10, 8) == 0 and _embed_ws(native, 1, 1, 1) > 0
