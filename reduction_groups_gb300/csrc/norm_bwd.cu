@@ -179,6 +179,9 @@ __device__ __forceinline__ float rsqrt_newton(float v) {
 // dx, while its next row's loads are in flight, and keeps its columns' dgamma
 // and dbeta sums in registers over all of its rows.  The floor is one read of
 // x and ct and one write of dx; a CTA's column sums go to the workspace once.
+// Rows this short are bound by their chains of shuffles (65536 x 200 bf16, 79
+// MB: RMSNorm 27 us, 2.9 TB/s; f32 LayerNorm, 157 MB, 39 us, 4.0 TB/s); a
+// second row in flight costs registers that more warps use better.
 constexpr int NB_FUSED_COLS = 255;
 constexpr int NB_ROWS_PER_WARP = 4;        // at least, where there are as many
 
@@ -275,9 +278,16 @@ __global__ void __launch_bounds__(NB_THREADS) norm_bwd_warps_kernel(const __grid
 // left them (a separate producer warp would leave 96 registers a thread):
 // LayerNorm past a row's first barrier, which comes early in it; RMSNorm, whose
 // only barrier comes halfway, as its warps report.
+//
+// [32768, 4096] bf16, 805 MB: 133 us (RMSNorm) and 134 us (LayerNorm), 6.0 TB/s,
+// bound by HBM with two reads to a write; [32768, 2048] 71 and 72 us; [16384, 4096] f32
+// 139 and 150 us; [512, 2048] 13 us, launches; [4096, 16384] 83 and 104 us, one
+// team whose two rows are all that fits beside gamma.  Rows beginning anywhere
+// are bound by their 2-byte accesses to shared memory: [32768, 1001] bf16 51 us,
+// [16384, 3001] bf16 LayerNorm 117 us; f32 [8192, 3001] 60 us, 4.9 TB/s.
 constexpr int RING_THREADS = 512;          // sixteen warps: 128 registers a thread
 constexpr int RING_MAX_COLS = 16384;
-constexpr int RING_MAX_SLOTS = 32;
+constexpr int RING_MAX_SLOTS = 64;
 constexpr int RING_MAX_BLOCKS = 160;
 constexpr int RING_SMEM = 220 * 1024;
 
@@ -289,11 +299,12 @@ struct NormRingParams {
 };
 
 // VEC: 16-byte aligned rows of whole 16-byte groups; group j of thread t begins
-// at element (j T + t) E.  Else any rows: TMA copies a row's part between its
-// first and last 16-byte boundary, the few elements outside come from global
-// memory, and element k of group j is column (j 8 + k) T + t (the threads'
-// columns must not move with a row's alignment, and neighbouring threads then
-// read neighbouring elements).
+// at element (j T + t) E.  Else any rows: TMA copies the 16-byte blocks that a
+// row lies in (what they hold of its neighbours is not used; the blocks in
+// which the tensor begins and ends are left out, their few elements stored by
+// the copying thread), so the row stands whole in its slot, and element k of
+// group j is column (j 8 + k) T + t (the threads' columns must not move with a
+// row's alignment, and neighbouring threads then read neighbouring elements).
 template <int TY, int KIND, int NV, int T, bool VEC>
 __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __grid_constant__ NormRingParams Q) {
   // gamma in f32 as the threads read it, then the ring.
@@ -335,29 +346,43 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
   bool dead = false;
   int flip = 0, issued = -1;
   const long long drop = g_pipe_drop_row;
-  // The elements of a row before its first 16-byte boundary and before its last.
-  struct Span {
-    int head, lim;
-  };
-  auto span_of = [&](const unsigned char* row) {
-    if constexpr (VEC) return Span{0, cols};
-    const int off = (int)((uintptr_t)row & 15u) / ESZ, per = 16 / ESZ;
-    int head = off ? per - off : 0;
-    if (head > cols) head = cols;
-    return Span{head, head + (cols - head) / per * per};
-  };
   auto x_row = [&](int i) { return (const unsigned char*)P.x + (blockIdx.x + (int64_t)i * gridDim.x) * P.ldx * ESZ; };
   auto c_row = [&](int i) { return (const unsigned char*)P.ct + (blockIdx.x + (int64_t)i * gridDim.x) * P.ldc * ESZ; };
+  // A row's bytes past the last 16-byte boundary before it.
+  auto skew = [](const unsigned char* row) { return VEC ? 0 : (int)((uintptr_t)row & 15u); };
   // The team's first thread copies local row i into its slot s.
   auto fetch = [&](int i, int s) {
     if (t != 0 || i >= n_local || dead || (drop >= 0 && i >= drop)) return;
     unsigned char* at = ring + (size_t)s * slot_bytes;
-    const unsigned char *x = x_row(i), *c = c_row(i);
-    const Span sx = span_of(x), sc = span_of(c);
-    const uint32_t nx = (uint32_t)(sx.lim - sx.head) * ESZ, nc = (uint32_t)(sc.lim - sc.head) * ESZ;
-    mbar_arrive_expect_tx(&full[s], nx + nc);
-    if (VEC || nx > 0) bulk_copy_g2s(at, x + sx.head * ESZ, nx, &full[s]);
-    if (VEC || nc > 0) bulk_copy_g2s(at + Q.row_bytes, c + sc.head * ESZ, nc, &full[s]);
+    const unsigned char* from[2] = {x_row(i), c_row(i)};
+    uint32_t lo[2] = {0, 0}, hi[2];                  // of the blocks' bytes, those copied
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int64_t r = blockIdx.x + (int64_t)i * gridDim.x;
+      const int off = skew(from[q]), end = off + cols * ESZ;
+      hi[q] = (uint32_t)(end + 15) & ~15u;
+      if constexpr (!VEC) {
+        unsigned char* o = at + q * Q.row_bytes;
+        const unsigned char* base = from[q] - off;
+        auto keep = [&](int b) {
+          if (ESZ == 2) *(uint16_t*)(o + b) = *(const uint16_t*)(base + b);
+          else *(uint32_t*)(o + b) = *(const uint32_t*)(base + b);
+        };
+        if (r == 0 && off != 0) {
+          lo[q] = 16;
+          for (int b = off; b < 16; b += ESZ) keep(b);
+        }
+        if (r == P.rows - 1 && (end & 15) != 0) {
+          hi[q] = (uint32_t)end & ~15u;
+          for (int b = (int)hi[q]; b < end; b += ESZ) keep(b);
+        }
+        from[q] = base;
+      }
+    }
+    mbar_arrive_expect_tx(&full[s], hi[0] - lo[0] + hi[1] - lo[1]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      bulk_copy_g2s(at + q * Q.row_bytes + lo[q], from[q] + lo[q], hi[q] - lo[q], &full[s]);
     issued = i;
   };
   // Sums over the team, one barrier (the buffers alternate).
@@ -408,15 +433,13 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
       else abort_flag = 1, dead = true;
     }
     if (!dead && !mbar_wait(&full[s], parity)) { abort_flag = 1; dead = true; }
-    const unsigned char* xs = ring + (size_t)s * slot_bytes;
-    const unsigned char* cs = xs + Q.row_bytes;
-    const unsigned char *xg = VEC ? nullptr : x_row(i), *cg = VEC ? nullptr : c_row(i);
-    const Span xspan = VEC ? Span{0, cols} : span_of(xg), cspan = VEC ? Span{0, cols} : span_of(cg);
+    const unsigned char* slot = ring + (size_t)s * slot_bytes;
+    const unsigned char *xs = slot + skew(x_row(i)), *cs = slot + Q.row_bytes + skew(c_row(i));
     auto element = [&](const unsigned char* p) {
       return ESZ == 2 ? bf16_bits_to_f32(*(const uint16_t*)p) : *(const float*)p;
     };
     // Group j of x or ct, widened; columns past the row's end are 0.
-    auto values = [&](const unsigned char* p, const unsigned char* row, const Span& at, int j, f2* v) {
+    auto values = [&](const unsigned char* p, int j, f2* v) {
       if constexpr (VEC) {
         const uint4 u = *(const uint4*)(p + (size_t)(j * T + t) * 16);
         if constexpr (TY == PSK_BF16) {
@@ -427,19 +450,15 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
           v[0] = f2{__uint_as_float(u.x), __uint_as_float(u.y)}, v[1] = f2{__uint_as_float(u.z), __uint_as_float(u.w)};
         }
       } else {
-        const int c0 = j * 8 * T;
-        if (c0 >= at.head && c0 + 8 * T <= at.lim) {      // all from shared memory
-          const unsigned char* q = p + (c0 + t - at.head) * ESZ;
+        const unsigned char* q = p + (j * 8 * T + t) * ESZ;
+        if ((j + 1) * 8 * T <= cols) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[k] = f2{element(q + 2 * k * T * ESZ), element(q + (2 * k + 1) * T * ESZ)};
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int c = c0 + k * T + t;
-            float e = 0.0f;
-            if (c < cols) e = c < at.head || c >= at.lim ? element(row + (int64_t)c * ESZ) : element(p + (c - at.head) * ESZ);
-            if (k & 1) v[k / 2].y = e;
-            else v[k / 2].x = e;
+          for (int k = 0; k < 4; ++k) {
+            v[k].x = absent(j, 2 * k) ? 0.0f : element(q + 2 * k * T * ESZ);
+            v[k].y = absent(j, 2 * k + 1) ? 0.0f : element(q + (2 * k + 1) * T * ESZ);
           }
         }
       }
@@ -466,7 +485,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
         for (int j = 0; j < NG; ++j) {
           if (no_group(j)) continue;
           f2 x[E / 2];
-          values(xs, xg, xspan, j, x);
+          values(xs, j, x);
 #pragma unroll
           for (int k = 0; k < E / 2; ++k) a = f2_add(a, x[k]);
         }
@@ -495,8 +514,8 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
       for (int j = 0; j < NG; ++j) {
         if (no_group(j)) continue;
         f2 x[E / 2], g[E / 2];
-        values(xs, xg, xspan, j, x);
-        values(cs, cg, cspan, j, g);
+        values(xs, j, x);
+        values(cs, j, g);
         if (KEEP) {
 #pragma unroll
           for (int k = 0; k < E / 2; ++k) kx[KEEP ? j : 0][k] = x[k], kc[KEEP ? j : 0][k] = g[k];
@@ -524,8 +543,8 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
 #pragma unroll
           for (int k = 0; k < E / 2; ++k) x[k] = kx[KEEP ? j : 0][k], c[k] = kc[KEEP ? j : 0][k];
         } else {
-          values(xs, xg, xspan, j, x);
-          values(cs, cg, cspan, j, c);
+          values(xs, j, x);
+          values(cs, j, c);
           centre(j, x);
         }
 #pragma unroll
@@ -675,11 +694,11 @@ static int norm_bwd_blocks(int64_t rows, int64_t cols) {
   return (int)(b < 1 ? 1 : b > NB_MAX_BLOCKS ? NB_MAX_BLOCKS : b);
 }
 
-// CTAs of the warp-a-row kernel: four an SM on 160 SMs at most, at least
+// CTAs of the warp-a-row kernel: three an SM on 160 SMs at most, at least
 // NB_ROWS_PER_WARP rows a warp.
 static int warps_blocks(int64_t rows) {
   const int64_t want = (rows + NB_WARPS * NB_ROWS_PER_WARP - 1) / (NB_WARPS * NB_ROWS_PER_WARP);
-  return (int)(want < 640 ? want : 640);
+  return (int)(want < 480 ? want : 480);
 }
 
 // The ring kernel's shape for rows of this size, or false: teams of the fewest
@@ -689,7 +708,8 @@ static int warps_blocks(int64_t rows) {
 // small teams overlap more rows.
 static bool ring_shape(NormRingParams& Q, int* nv, int32_t dt, int32_t kind, bool vec, int64_t cols) {
   if (cols <= NB_FUSED_COLS || cols > RING_MAX_COLS) return false;
-  Q.row_bytes = (int32_t)((cols * dtype_size(dt) + 15) / 16 * 16);
+  const int64_t bytes = cols * dtype_size(dt);      // of a row, not vec: up to 14 before it in its first block
+  Q.row_bytes = (int32_t)((bytes + (vec ? 0 : 14) + 15) / 16 * 16);
   for (*nv = vec && cols > 512 ? 4 : vec ? 2 : 4; *nv >= 2; *nv -= 2) {
     Q.team = 32;
     while (Q.team * *nv * 8 < cols) Q.team *= 2;
@@ -885,7 +905,11 @@ extern "C" int psk_norm_backward(const void* x, int32_t xt, const void* ct, int3
   }
   if (one_type && cols <= NB_FUSED_COLS) {
     P.blocks = warps_blocks(rows);
-    if (P.blocks > 4 * device_sm_count()) P.blocks = 4 * device_sm_count();
+    // As many CTAs as an SM holds at once by their registers: three of RMSNorm in
+    // bf16 (65536 x 200: 27 us, four 34), else two (LayerNorm 65536 x 199 bf16: 34
+    // us, four 40; three 38 with registers for them).
+    const int per_sm = kind == PSK_NORM_RMS && xt == PSK_BF16 ? 3 : 2;
+    if (P.blocks > per_sm * device_sm_count()) P.blocks = per_sm * device_sm_count();
     with_dtype(xt, [&](auto TY) {
       return with_bool(kind == PSK_NORM_LAYER, [&](auto LAYER) {
         return with_bool(vec, [&](auto VEC) {
