@@ -346,7 +346,7 @@ def _bind_torch() -> None:
     _F32 = torch.float32
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _current_stream = raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
-    _current_device = torch.cuda.current_device
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # of tensors on a CUDA device
 
 
 def _code(t, what: str) -> int:
@@ -386,11 +386,16 @@ def _same_device(stream, first, *rest) -> int:
 
 def _matrix(t, what: str, shape=None) -> int:
     """The leading dimension of a 2-D tensor of contiguous rows."""
-    size, stride = t.shape, t.stride()
-    if len(size) != 2 or (stride[1] != 1 and size[1] > 1):
+    size = t.shape
+    if len(size) != 2:
         raise ValueError(f"{what} must be a 2-D tensor with contiguous rows")
     if shape is not None and size != shape:
         raise ValueError(f"{what} has shape {tuple(size)}, not {tuple(shape)}")
+    if t.is_contiguous():
+        return size[1]
+    stride = t.stride()
+    if stride[1] != 1 and size[1] > 1:
+        raise ValueError(f"{what} must be a 2-D tensor with contiguous rows")
     if stride[0] >= size[1]:
         return stride[0]
     if size[0] > 1:
@@ -402,7 +407,7 @@ def _vector(t, what: str, n: int, f32: bool = False):
     """The address of a contiguous 1-D tensor of n elements (None: NULL)."""
     if t is None:
         return None
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous vector of {n} elements")
     if f32 and t.dtype is not _F32:
         raise TypeError(f"{what} must be f32")
