@@ -379,7 +379,7 @@ __device__ __forceinline__ void join_runs(const EmbedGradParams& P, const Column
 //
 // 16384 tokens x 2048 bf16 into 32000 rows (198 MB): 48 us with the sort, 4.1
 // TB/s; 30000 x 1000 f32 into 60000: 73 us, 4.9 TB/s; rows beginning anywhere,
-// 4000 x 8001 bf16 into 8000: 51 us, 3.8 TB/s.  What is left is latency: a
+// 4000 x 8001 bf16 into 8000: 50 us, 3.9 TB/s.  What is left is latency: a
 // warp's chain of sorted list, four groups of rows, stores.  More rows in
 // flight (copied asynchronously into shared memory), more warps, smaller or
 // rolled loops all took as long or longer, as did zeroing elsewhere.

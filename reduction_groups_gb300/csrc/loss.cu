@@ -234,14 +234,21 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
 }
 
 // Any row: a CTA per row, CTAs over rows in turn, the row read from global
-// memory for its sums and (from L2) again for its gradient.  Rows that the
-// resident kernel below cannot take: longer than a cluster's shared memory,
-// gradients of another type or alignment than the logits.
+// memory for its sums and (from L2) again for its gradient, four groups of
+// eight columns a thread in flight (a lane's columns are 32 apart in unaligned
+// rows).  Rows that the resident kernel below cannot take: longer than a
+// cluster's shared memory, gradients of another type or alignment than the
+// logits.  Bound by its loads' latency: [512, 300000] bf16 167 us, 3.7 TB/s (one
+// group in flight for the gradient: 466); [4096, 32000] bf16 to f32 173 us, 4.5
+// TB/s; unaligned, [4096, 32001], 367 us; 512 threads were slower.
 template <int LT, int GT, int MODE, bool VEC>
 __global__ void __launch_bounds__(LOSS_THREADS) loss_rows_kernel(const __grid_constant__ LossParams P) {
   __shared__ RowSum red[LOSS_WARPS];
-  __shared__ float coef[3];
-  const int64_t groups = (P.cols + 7) / 8;
+  __shared__ float coef[2];
+  const int64_t groups = VEC ? P.cols / 8 : (P.cols + 255) / 256 * 32;
+  auto columns = [&](int64_t q) {
+    return VEC ? Columns<VEC, 8>(q * 8, 1, 0, P.cols) : Columns<VEC, 8>(q / 32 * 256, 32, (int)(q % 32), P.cols);
+  };
   double loss_sum = 0.0, kl_sum = 0.0;
   for (int64_t r = blockIdx.x; r < P.rows; r += gridDim.x) {
     const int64_t t = row_target(P, r);
@@ -251,23 +258,31 @@ __global__ void __launch_bounds__(LOSS_THREADS) loss_rows_kernel(const __grid_co
       if (threadIdx.x == 0 && P.logp) P.logp[r] = 0.0f;
       if (MODE == LOSS_GRAD) {
         const float z[8] = {};
-        for (int64_t q = threadIdx.x; q < groups; q += LOSS_THREADS)
-          store8<GT, VEC>(P.grad, r * P.ldg + q * 8, (int)(P.cols - q * 8 < 8 ? P.cols - q * 8 : 8), z);
+        for (int64_t q = threadIdx.x; q < groups; q += LOSS_THREADS) columns(q).template store<GT>(P.grad, r * P.ldg, z);
       }
       continue;
     }
     const int64_t xo = r * P.ldx;
     const float xt = load1<LT>(P.x, xo + t);       // read before the row may be overwritten in place
     RowSum v{-INFINITY, 0.0f, 0.0f};
+    // Four of the thread's groups, all of their loads in flight.
+    auto load4 = [&](int64_t q0, float (&x)[4][8], int (&n)[4]) {
+      Piece<LT, VEC, 8> raw[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const auto cols = columns(q0 + j * LOSS_THREADS);
+        n[j] = cols.present;
+        cols.load(P.x, xo, raw[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[j][k] = raw[j].get(k);
+    };
     for (int64_t q0 = threadIdx.x; q0 < groups; q0 += 4 * LOSS_THREADS) {
       float x[4][8];
       int n[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t left = P.cols - (q0 + j * LOSS_THREADS) * 8;
-        n[j] = left <= 0 ? 0 : left < 8 ? (int)left : 8;
-        if (n[j] > 0) load8<LT, VEC>(P.x, xo + (q0 + j * LOSS_THREADS) * 8, n[j], x[j]);
-      }
+      load4(q0, x, n);
 #pragma unroll
       for (int j = 0; j < 4; ++j) add8(v, x[j], n[j], P.c);
     }
@@ -289,14 +304,18 @@ __global__ void __launch_bounds__(LOSS_THREADS) loss_rows_kernel(const __grid_co
     __syncthreads();
     if (MODE == LOSS_GRAD) {
       const float f = coef[0], ft = coef[1];
-      for (int64_t q = threadIdx.x; q < groups; q += LOSS_THREADS) {
-        const int64_t c0 = q * 8;
-        const int n = P.cols - c0 < 8 ? (int)(P.cols - c0) : 8;
-        float x[8];
-        load8<LT, VEC>(P.x, xo + c0, n, x);
+      for (int64_t q0 = threadIdx.x; q0 < groups; q0 += 4 * LOSS_THREADS) {
+        float x[4][8];
+        int n[4];
+        load4(q0, x, n);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = c0 + k == t ? ft : ex2_approx((x[k] - v.m) * P.c) * f;
-        store8<GT, VEC>(P.grad, r * P.ldg + c0, n, x);
+        for (int j = 0; j < 4; ++j) {
+          const auto cols = columns(q0 + j * LOSS_THREADS);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            x[j][k] = (VEC ? cols.first + k : cols.col(k)) == t ? ft : ex2_approx((x[j][k] - v.m) * P.c) * f;
+          cols.template store<GT>(P.grad, r * P.ldg, x[j]);
+        }
       }
     }
   }
@@ -322,6 +341,15 @@ __global__ void __launch_bounds__(LOSS_THREADS) loss_rows_kernel(const __grid_co
 // producer warp, a lane for each chunk of each slot, refills them as they fall
 // free.  The CTAs of a cluster exchange their slices' maxima and sums through
 // distributed shared memory.
+//
+// With gradient: [8192, 32000] bf16, an eighth of the rows left out, 983 MB: 169
+// us, 5.8 TB/s; the same in f32, [4096, 32000]: 187 us, 5.6 TB/s; [2048, 131072]
+// bf16, clusters of four (36 of them fit: 144 SMs work): 197 us, 5.3 TB/s;
+// [8192, 9001] bf16, rows beginning anywhere: 74 us, 4.0 TB/s.  Without: [4096,
+// 32000] bf16 48 us, 5.4 TB/s; [2048, 131072] 121 us, 4.4 TB/s.  HBM is about
+// two thirds busy: the rest is the joins' and barriers' latency, which three
+// teams of 256 threads do not all hide (two ex2 a logit alone would take about
+// 50 of the 169 us).
 
 constexpr int RES_CONSUMERS = 768;             // at most: teams of 32 to 512 threads
 constexpr int RES_THREADS = RES_CONSUMERS + 32;
@@ -1042,7 +1070,7 @@ extern "C" int psk_token_logp(const void* logits, int32_t lt, int64_t rows, int6
       return resident_launch<LT.value, LOSS_LOGP>(Q, P, &parts, (cudaStream_t)stream);
     });
   }
-  const bool vec = rows_vec8(logits, lt, ldl, rows);
+  const bool vec = cols % 8 == 0 && rows_vec8(logits, lt, ldl, rows);
   with_dtype(lt, [&](auto LT) {
     return with_bool(vec, [&](auto VEC) {
       loss_rows_kernel<LT.value, PSK_F32, LOSS_LOGP, VEC.value>
@@ -1136,7 +1164,7 @@ extern "C" int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int
     return rc ? rc : loss_finish(P.part, parts, loss, s);
   }
   const unsigned grid = loss_grid(rows);
-  const bool vec = rows_vec8(logits, lt, ldl, rows) && (!dlogits || rows_vec8(dlogits, gt, ldg, rows));
+  const bool vec = cols % 8 == 0 && rows_vec8(logits, lt, ldl, rows) && (!dlogits || rows_vec8(dlogits, gt, ldg, rows));
   with_dtype(lt, [&](auto LT) {
     return with_bool(vec, [&](auto VEC) {
       if (!dlogits) {

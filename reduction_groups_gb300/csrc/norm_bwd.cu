@@ -48,7 +48,10 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float2* red) {
 
 // Row statistics, a CTA per row.  Rows are read once per reduction (two for
 // LayerNorm, whose variance is taken about the mean); the later reads hit L1
-// or L2.
+// or L2.  This kernel and the next serve what the kernels of one pass below do
+// not: tensors of several types, rows beyond 16384 columns.  They read x and ct
+// from HBM twice: [16384, 4096] f32 x, bf16 ct, f32 dx 184 us, 0.67 GB (0.4 GB of
+// it once more); [4096, 20000] bf16 204 us.
 template <int XT, int CT, int KIND, bool VEC>
 __global__ void __launch_bounds__(NB_THREADS) norm_bwd_stats_kernel(const __grid_constant__ NormBwdParams P) {
   __shared__ float2 red[NB_WARPS];

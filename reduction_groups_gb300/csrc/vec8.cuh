@@ -39,32 +39,6 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, int n, float* v)
   }
 }
 
-// v[0, n) rounded to DT into elements [i, i + n) of p.
-template <int DT, bool VEC>
-__device__ __forceinline__ void store8(void* p, int64_t i, int n, const float* v) {
-  if constexpr (DT == PSK_BF16) {
-    uint16_t* q = (uint16_t*)p + i;
-    if (VEC && n >= 8) {
-      *(uint4*)q = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
-                              f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n) q[k] = f32_to_bf16_bits(v[k]);
-    }
-  } else {
-    float* q = (float*)p + i;
-    if (VEC && n >= 8) {
-      *(float4*)q = make_float4(v[0], v[1], v[2], v[3]);
-      *(float4*)(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n) q[k] = v[k];
-    }
-  }
-}
-
 // NC of a thread's columns as loaded, so that a batch of loads can be in
 // flight before the first is widened.
 template <int TY, bool VEC, int NC>
