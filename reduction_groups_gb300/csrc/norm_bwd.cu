@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
   __shared__ volatile int abort_flag;
   constexpr bool LAYER = KIND == PSK_NORM_LAYER;
   constexpr int ESZ = TY == PSK_BF16 ? 2 : 4;
-  constexpr int E = VEC ? 16 / ESZ : 8;                  // elements of a group
+  constexpr int E = VEC ? 16 / ESZ : NV == 2 ? 4 : 8;    // elements of a group
   constexpr int NG = NV * 8 / E;                         // groups of a thread
   constexpr int TEAMS = RING_THREADS / T, nw = T / 32;
   const NormBwdParams& P = Q.B;
@@ -423,9 +423,12 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
       dg[j][k] = zero;
       if (LAYER) db[j][k] = zero;
     }
+  // The row's widened values stay in registers for dx where RMSNorm has one pass
+  // before it, and in narrow threads of unaligned rows.
+  constexpr bool KEEP = !LAYER || (!VEC && NV == 2);
   // Whether the thread has a group (VEC), or the team a column of the group's element k.
-  auto no_group = [&](int j) { return VEC ? j * T + t >= groups : j * 8 * T >= cols; };
-  auto absent = [&](int j, int k) { return !VEC && (j * 8 + k + 1) * T > cols && (j * 8 + k) * T + t >= cols; };
+  auto no_group = [&](int j) { return VEC ? j * T + t >= groups : j * E * T >= cols; };
+  auto absent = [&](int j, int k) { return !VEC && (j * E + k + 1) * T > cols && (j * E + k) * T + t >= cols; };
   int s = team, before = 0;                  // the row's slot, the last row's
   uint32_t parity = 0, parity_before = 0;    // of their phases
   for (int i = team; i < n_local; i += TEAMS) {
@@ -453,13 +456,13 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
           v[0] = f2{__uint_as_float(u.x), __uint_as_float(u.y)}, v[1] = f2{__uint_as_float(u.z), __uint_as_float(u.w)};
         }
       } else {
-        const unsigned char* q = p + (j * 8 * T + t) * ESZ;
-        if ((j + 1) * 8 * T <= cols) {
+        const unsigned char* q = p + (j * E * T + t) * ESZ;
+        if ((j + 1) * E * T <= cols) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = f2{element(q + 2 * k * T * ESZ), element(q + (2 * k + 1) * T * ESZ)};
+          for (int k = 0; k < E / 2; ++k) v[k] = f2{element(q + 2 * k * T * ESZ), element(q + (2 * k + 1) * T * ESZ)};
         } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < E / 2; ++k) {
             v[k].x = absent(j, 2 * k) ? 0.0f : element(q + 2 * k * T * ESZ);
             v[k].y = absent(j, 2 * k + 1) ? 0.0f : element(q + (2 * k + 1) * T * ESZ);
           }
@@ -474,11 +477,12 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
           g[2 * q] = f2_mul(g[2 * q], f2{a.x, a.y}), g[2 * q + 1] = f2_mul(g[2 * q + 1], f2{a.z, a.w});
         }
       } else {
-        const float* q = gamma + j * 8 * T + t;
+        const float* q = gamma + j * E * T + t;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) g[k] = f2_mul(g[k], f2{q[2 * k * T], q[(2 * k + 1) * T]});
+        for (int k = 0; k < E / 2; ++k) g[k] = f2_mul(g[k], f2{q[2 * k * T], q[(2 * k + 1) * T]});
       }
     };
+    f2 kx[KEEP ? NG : 1][E / 2], kc[KEEP ? NG : 1][E / 2];    // KEEP: the row's (centred) x and ct
     float sums[3];
     float mu = 0.0f;
     if (LAYER) {
@@ -490,7 +494,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
           f2 x[E / 2];
           values(xs, j, x);
 #pragma unroll
-          for (int k = 0; k < E / 2; ++k) a = f2_add(a, x[k]);
+          for (int k = 0; k < E / 2; ++k) {
+            a = f2_add(a, x[k]);
+            if (KEEP) kx[KEEP ? j : 0][k] = x[k];
+          }
         }
       }
       sums[0] = a.x + a.y;
@@ -509,22 +516,25 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
         if (absent(j, 2 * k + 1)) x[k].y = 0.0f;
       }
     };
-    constexpr bool KEEP = !LAYER;            // widened values stay in registers for dx
-    f2 kx[KEEP ? NG : 1][E / 2], kc[KEEP ? NG : 1][E / 2];
     f2 a = zero, b = zero, d = zero;
     if (!dead) {
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
         if (no_group(j)) continue;
         f2 x[E / 2], g[E / 2];
-        values(xs, j, x);
+        if (KEEP && LAYER) {
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) x[k] = kx[KEEP ? j : 0][k];
+        } else {
+          values(xs, j, x);
+        }
         values(cs, j, g);
+        if (LAYER) centre(j, x);
         if (KEEP) {
 #pragma unroll
           for (int k = 0; k < E / 2; ++k) kx[KEEP ? j : 0][k] = x[k], kc[KEEP ? j : 0][k] = g[k];
         }
         gate(j, g);
-        if (LAYER) centre(j, x);
 #pragma unroll
         for (int k = 0; k < E / 2; ++k) {
           if (LAYER) d = f2_add(d, g[k]);
@@ -548,7 +558,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
         } else {
           values(xs, j, x);
           values(cs, j, c);
-          centre(j, x);
+          if (LAYER) centre(j, x);
         }
 #pragma unroll
         for (int k = 0; k < E / 2; ++k) g[k] = c[k];
@@ -569,9 +579,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
             *(float4*)o = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < E; ++k) {
             const float e = k & 1 ? y[k / 2].y : y[k / 2].x;
-            const int64_t at = r * P.ldd + (j * 8 + k) * T + t;
+            const int64_t at = r * P.ldd + (j * E + k) * T + t;
             if (absent(j, k)) continue;
             if constexpr (TY == PSK_BF16) ((uint16_t*)P.dx)[at] = f32_to_bf16_bits(e);
             else ((float*)P.dx)[at] = e;
@@ -609,7 +619,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
         if constexpr (VEC) {
           ((float4*)side)[(team * WIDE) / 4 + (j * (E / 4) + k / 2) * T + t] = make_float4(a.x, a.y, b.x, b.y);
         } else {
-          const int c = (j * 8 + 2 * k) * T + t;
+          const int c = (j * E + 2 * k) * T + t;
           float* at = side + team * cols + c;
           if (c < cols) at[0] = a.x;
           if (c + T < cols) at[T] = a.y;
@@ -713,7 +723,7 @@ static bool ring_shape(NormRingParams& Q, int* nv, int32_t dt, int32_t kind, boo
   if (cols <= NB_FUSED_COLS || cols > RING_MAX_COLS) return false;
   const int64_t bytes = cols * dtype_size(dt);      // of a row, not vec: up to 14 before it in its first block
   Q.row_bytes = (int32_t)((bytes + (vec ? 0 : 14) + 15) / 16 * 16);
-  for (*nv = vec && cols > 512 ? 4 : vec ? 2 : 4; *nv >= 2; *nv -= 2) {
+  for (*nv = cols > 512 ? 4 : 2; *nv >= 2; *nv -= 2) {
     Q.team = 32;
     while (Q.team * *nv * 8 < cols) Q.team *= 2;
     if (Q.team > RING_THREADS) return false;
@@ -729,7 +739,6 @@ static bool ring_shape(NormRingParams& Q, int* nv, int32_t dt, int32_t kind, boo
     }
     Q.slots = fits / Q.teams * Q.teams;
     if (Q.slots >= 2 * Q.teams) return true;
-    if (!vec) return false;
   }
   return false;
 }
@@ -767,7 +776,7 @@ static int ring_launch_shape(const NormRingParams& Q, cudaStream_t s) {
 
 template <int TY, int KIND>
 static int ring_launch(const NormRingParams& Q, int nv, bool vec, cudaStream_t s) {
-  if (!vec) return ring_launch_shape<TY, KIND, 4, false>(Q, s);
+  if (!vec) return nv == 2 ? ring_launch_shape<TY, KIND, 2, false>(Q, s) : ring_launch_shape<TY, KIND, 4, false>(Q, s);
   if (nv == 4) return ring_launch_shape<TY, KIND, 4, true>(Q, s);
   if constexpr (TY == PSK_F32) return ring_launch_shape<TY, KIND, 2, true>(Q, s);
   else return ring_launch_team<TY, KIND, 2, 32, true>(Q, s);
