@@ -286,8 +286,9 @@ __global__ void __launch_bounds__(NB_THREADS) norm_bwd_warps_kernel(const __grid
 // bound by HBM with two reads to a write; [32768, 2048] 71 and 72 us; [16384, 4096] f32
 // 139 and 150 us; [512, 2048] 13 us, launches; [4096, 16384] 83 and 104 us, one
 // team whose two rows are all that fits beside gamma.  Rows beginning anywhere
-// are bound by their 2-byte accesses to shared memory: [32768, 1001] bf16 51 us,
-// [16384, 3001] bf16 LayerNorm 117 us; f32 [8192, 3001] 60 us, 4.9 TB/s.
+// are bound by the instructions of their element-wise accesses: [32768, 1001]
+// bf16 48 us, [16384, 3001] bf16 79 and 103 us (twice the warps at half the
+// registers took as long); f32 [8192, 3001] 59 us, 5.0 TB/s, [8192, 7999] 149 us.
 constexpr int RING_THREADS = 512;          // sixteen warps: 128 registers a thread
 constexpr int RING_MAX_COLS = 16384;
 constexpr int RING_MAX_SLOTS = 64;
@@ -306,7 +307,7 @@ struct NormRingParams {
 // row lies in (what they hold of its neighbours is not used; the blocks in
 // which the tensor begins and ends are left out, their few elements stored by
 // the copying thread), so the row stands whole in its slot, and element k of
-// group j is column (j 8 + k) T + t (the threads' columns must not move with a
+// group j is column (j E + k) T + t (the threads' columns must not move with a
 // row's alignment, and neighbouring threads then read neighbouring elements).
 template <int TY, int KIND, int NV, int T, bool VEC>
 __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __grid_constant__ NormRingParams Q) {
@@ -426,9 +427,11 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
   // The row's widened values stay in registers for dx where RMSNorm has one pass
   // before it, and in narrow threads of unaligned rows.
   constexpr bool KEEP = !LAYER || (!VEC && NV == 2);
-  // Whether the thread has a group (VEC), or the team a column of the group's element k.
+  // Whether the thread (VEC) or the team has nothing of a group; whether every
+  // thread has all of it; if not, whether the thread lacks its element k.
   auto no_group = [&](int j) { return VEC ? j * T + t >= groups : j * E * T >= cols; };
-  auto absent = [&](int j, int k) { return !VEC && (j * E + k + 1) * T > cols && (j * E + k) * T + t >= cols; };
+  auto whole = [&](int j) { return VEC || (j + 1) * E * T <= cols; };
+  auto absent = [&](int j, int k) { return !VEC && (j * E + k) * T + t >= cols; };
   int s = team, before = 0;                  // the row's slot, the last row's
   uint32_t parity = 0, parity_before = 0;    // of their phases
   for (int i = team; i < n_local; i += TEAMS) {
@@ -457,7 +460,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
         }
       } else {
         const unsigned char* q = p + (j * E * T + t) * ESZ;
-        if ((j + 1) * E * T <= cols) {
+        if (whole(j)) {
 #pragma unroll
           for (int k = 0; k < E / 2; ++k) v[k] = f2{element(q + 2 * k * T * ESZ), element(q + (2 * k + 1) * T * ESZ)};
         } else {
@@ -512,8 +515,13 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
 #pragma unroll
       for (int k = 0; k < E / 2; ++k) {
         x[k] = f2_add(x[k], nmu);
-        if (absent(j, 2 * k)) x[k].x = 0.0f;
-        if (absent(j, 2 * k + 1)) x[k].y = 0.0f;
+      }
+      if (!whole(j)) {
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) {
+          if (absent(j, 2 * k)) x[k].x = 0.0f;
+          if (absent(j, 2 * k + 1)) x[k].y = 0.0f;
+        }
       }
     };
     f2 a = zero, b = zero, d = zero;
@@ -578,13 +586,19 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_bwd_ring_kernel(const __
           else
             *(float4*)o = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
         } else {
-#pragma unroll
-          for (int k = 0; k < E; ++k) {
+          unsigned char* o = (unsigned char*)P.dx + (r * P.ldd + j * E * T + t) * ESZ;
+          auto put = [&](int k) {
             const float e = k & 1 ? y[k / 2].y : y[k / 2].x;
-            const int64_t at = r * P.ldd + (j * E + k) * T + t;
-            if (absent(j, k)) continue;
-            if constexpr (TY == PSK_BF16) ((uint16_t*)P.dx)[at] = f32_to_bf16_bits(e);
-            else ((float*)P.dx)[at] = e;
+            if constexpr (TY == PSK_BF16) *(uint16_t*)(o + k * T * ESZ) = f32_to_bf16_bits(e);
+            else *(float*)(o + k * T * ESZ) = e;
+          };
+          if (whole(j)) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) put(k);
+          } else {
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+              if (!absent(j, k)) put(k);
           }
         }
       }
