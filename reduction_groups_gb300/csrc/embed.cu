@@ -318,7 +318,8 @@ __global__ void __launch_bounds__(2 * SORT_THREADS) embed_sort_kernel(const __gr
 }
 
 template <int DT, bool VEC, int NC, bool ACC>
-__device__ __forceinline__ void write_row(const EmbedGradParams& P, const Columns<VEC, NC>& cols, uint32_t id, const f2* sum) {
+__device__ __forceinline__ void write_row(const EmbedGradParams& P, const Columns<VEC, NC>& cols, uint32_t id, const f2* sum,
+                                          const Piece<DT, VEC, NC>* before = nullptr) {
   float o[NC];
 #pragma unroll
   for (int k = 0; k < NC / 2; ++k) {
@@ -328,7 +329,8 @@ __device__ __forceinline__ void write_row(const EmbedGradParams& P, const Column
   char* q = (char*)cols.template at<DT>(P.d) + (uint64_t)id * P.d_row;
   if (ACC) {
     Piece<DT, VEC, NC> old;
-    cols.load_at(q, old);
+    if (before) old = *before;
+    else cols.load_at(q, old);
 #pragma unroll
     for (int k = 0; k < NC; ++k) o[k] = __fadd_rn(old.get(k), o[k]);
   }
@@ -374,8 +376,9 @@ __device__ __forceinline__ void join_runs(const EmbedGradParams& P, const Column
   write_row<DT, VEC, NC, ACC>(P, cols, id, acc);
 }
 
-// The first run_ctas CTAs: one run and one slice of 32 NC columns a warp.  The
-// others zero the rows of ids that do not occur.
+// The first run_ctas CTAs: one slice of 32 NC columns of one run a warp, or of
+// a quarter of it (PARTS = 4: the ids that begin there, each to its end in the
+// run).  The others zero the rows of ids that do not occur.
 //
 // 16384 tokens x 2048 bf16 into 32000 rows (198 MB): 48 us with the sort, 4.1
 // TB/s; 30000 x 1000 f32 into 60000: 73 us, 4.9 TB/s; rows beginning anywhere,
@@ -383,7 +386,7 @@ __device__ __forceinline__ void join_runs(const EmbedGradParams& P, const Column
 // warp's chain of sorted list, four groups of rows, stores.  More rows in
 // flight (copied asynchronously into shared memory), more warps, smaller or
 // rolled loops all took as long or longer, as did zeroing elsewhere.
-template <int CT, int DT, bool VEC, int NC, bool ACC>
+template <int CT, int DT, bool VEC, int NC, bool ACC, int PARTS>
 __global__ void __launch_bounds__(EMB_THREADS, 2) embed_runs_kernel(const __grid_constant__ EmbedGradParams P) {
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -400,8 +403,8 @@ __global__ void __launch_bounds__(EMB_THREADS, 2) embed_runs_kernel(const __grid
     return;
   }
   const int64_t w = ((int64_t)blockIdx.x * EMB_THREADS + threadIdx.x) >> 5;
-  const int64_t run = w / P.slices;
-  const int slice = (int)(w - run * P.slices);
+  const int64_t unit = w / P.slices, run = unit / PARTS;
+  const int slice = (int)(w - unit * P.slices), part = (int)(unit % PARTS);
   const int64_t i0 = run * EMB_RUN;
   if (i0 >= P.tokens) return;
   const Columns<VEC, NC> cols((int64_t)slice * (32 * NC), 32, lane, P.cols);
@@ -414,29 +417,48 @@ __global__ void __launch_bounds__(EMB_THREADS, 2) embed_runs_kernel(const __grid
   const uint32_t next_key = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
   // The first id of the run may have begun in an earlier one, the last may go
   // on in the next: their sums are joined, the others written as they end.
-  const bool leads = prior == __shfl_sync(0xFFFFFFFFu, my_key, 0);
-  const bool goes_on = n == EMB_RUN && after == __shfl_sync(0xFFFFFFFFu, my_key, EMB_RUN - 1);
+  bool leads = prior == __shfl_sync(0xFFFFFFFFu, my_key, 0);
+  bool goes_on = n == EMB_RUN && after == __shfl_sync(0xFFFFFFFFu, my_key, EMB_RUN - 1);
   // Entries after which a sum ends.
   const uint32_t ends = __ballot_sync(0xFFFFFFFFu, lane < n && (lane == n - 1 ? !goes_on : next_key != my_key));
+  // The warp's entries.
+  int begin = 0, stop = n;
+  if constexpr (PARTS > 1) {
+    const uint32_t last_key = __shfl_up_sync(0xFFFFFFFFu, my_key, 1);
+    const uint32_t starts = __ballot_sync(0xFFFFFFFFu, lane < n && (lane == 0 || last_key != my_key));
+    auto first_from = [&](int at) {          // the first entry from `at` on with which an id begins
+      const uint32_t m = at < 32 ? starts >> at : 0;
+      return m ? at + __ffs(m) - 1 : n;
+    };
+    begin = first_from(part * (EMB_RUN / PARTS)), stop = first_from((part + 1) * (EMB_RUN / PARTS));
+    if (begin >= stop) return;
+    leads = leads && begin == 0, goes_on = goes_on && stop == n;
+  }
   f2 acc[NC / 2], lead[NC / 2];
 #pragma unroll
   for (int k = 0; k < NC / 2; ++k) acc[k] = lead[k] = f2{0.0f, 0.0f};
   bool head = leads;
   const char* ct = cols.template at<CT>(P.ct);
   // Rows in flight: eight of eight columns (sixteen of bf16 took the gradient of
-  // 16384 x 2048 from 48 to 52 us, in registers that then spill), sixteen of four.
-  constexpr int GROUP = 64 / NC;
-  for (int e0 = 0; e0 < n; e0 += GROUP) {
+  // 16384 x 2048 from 48 to 52 us, in registers that then spill), sixteen of
+  // four, or eight with the rows that they are added to, or of a part.
+  constexpr int GROUP = ACC || PARTS > 1 ? 8 : 64 / NC;
+  for (int e0 = begin; e0 < stop; e0 += GROUP) {
     Piece<CT, VEC, NC> v[GROUP];
+    Piece<DT, VEC, NC> old[ACC ? GROUP : 1];
     const uint32_t now = ends >> e0;
 #pragma unroll
     for (int j = 0; j < GROUP; ++j) {
-      const uint32_t p = __shfl_sync(0xFFFFFFFFu, my_pos, e0 + j);
-      if (e0 + j < n) cols.load_at(ct + (uint64_t)p * P.ct_row, v[j]);
+      const uint32_t p = __shfl_sync(0xFFFFFFFFu, my_pos, (e0 + j) & 31);
+      if (e0 + j < stop) cols.load_at(ct + (uint64_t)p * P.ct_row, v[j]);
+      if constexpr (ACC) {
+        const uint32_t id = __shfl_sync(0xFFFFFFFFu, my_key, (e0 + j) & 31);
+        if (e0 + j < stop && ((now >> j) & 1)) cols.load_at(cols.template at<DT>(P.d) + (uint64_t)id * P.d_row, old[j]);
+      }
     }
 #pragma unroll
     for (int j = 0; j < GROUP; ++j) {
-      if (e0 + j < n) {
+      if (e0 + j < stop) {
 #pragma unroll
         for (int k = 0; k < NC / 2; ++k) acc[k] = f2_add(acc[k], f2{v[j].get(2 * k), v[j].get(2 * k + 1)});
         if ((now >> j) & 1) {
@@ -445,7 +467,7 @@ __global__ void __launch_bounds__(EMB_THREADS, 2) embed_runs_kernel(const __grid
             for (int k = 0; k < NC / 2; ++k) lead[k] = acc[k];
             head = false;
           } else {
-            write_row<DT, VEC, NC, ACC>(P, cols, __shfl_sync(0xFFFFFFFFu, my_key, e0 + j), acc);
+            write_row<DT, VEC, NC, ACC>(P, cols, __shfl_sync(0xFFFFFFFFu, my_key, e0 + j), acc, ACC ? &old[ACC ? j : 0] : nullptr);
           }
 #pragma unroll
           for (int k = 0; k < NC / 2; ++k) acc[k] = f2{0.0f, 0.0f};
@@ -582,11 +604,19 @@ static void launch_after(K kernel, unsigned grid, int threads, cudaStream_t s, c
 
 static uint64_t align256(uint64_t n) { return (n + 255) / 256 * 256; }
 
-// Column slices of the run sums: eight columns a lane, or four where eight
-// leave fewer than 16 warps an SM of 152 (latency then counts more than the
-// instructions for each row), or into a gradient that is added to.
-static bool embed_wide(int64_t tokens, int64_t cols, bool accumulate) {
-  return !accumulate && (tokens + EMB_RUN - 1) / EMB_RUN * ((cols + 255) / 256) >= 16 * 152;
+// How the run sums are cut: eight columns a lane where that leaves 16 warps an
+// SM of 152; four, into a gradient that is added to too (latency then counts
+// more than the instructions for each row); and quarters of a run where four
+// columns leave fewer than 4 warps an SM, each of which would pass its 32
+// entries alone on its scheduler (500 tokens x 1001 bf16: 14.9 us, whole runs
+// 17.9; 10000 x 501 f32, above the limit: 20.9 us whole, 23.1 in quarters).
+struct EmbedCut {
+  int columns, parts;
+};
+static EmbedCut embed_cut(int64_t tokens, int64_t cols, bool accumulate) {
+  const int64_t runs = (tokens + EMB_RUN - 1) / EMB_RUN;
+  if (!accumulate && runs * ((cols + 255) / 256) >= 16 * 152) return {8, 1};
+  return {4, runs * ((cols + 127) / 128) >= 4 * 152 ? 1 : 4};
 }
 
 // Workspace layout: the sorted list, each id's places in it, the head and tail
@@ -783,9 +813,9 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
   if (P.fill_ids == slice) zero_ctas = 0;
   const unsigned sort_ctas = (unsigned)((vocab + slice - 1) / slice);
   const int64_t runs = (tokens + EMB_RUN - 1) / EMB_RUN;
-  const bool wide = embed_wide(tokens, cols, accumulate);
-  P.slices = (int32_t)((cols + (wide ? 255 : 127)) / (wide ? 256 : 128));
-  const uint64_t ctas = ((uint64_t)runs * P.slices + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32);
+  const EmbedCut cut = embed_cut(tokens, cols, accumulate);
+  P.slices = (int32_t)((cols + 32 * cut.columns - 1) / (32 * cut.columns));
+  const uint64_t ctas = ((uint64_t)runs * cut.parts * P.slices + EMB_THREADS / 32 - 1) / (EMB_THREADS / 32);
   if (ctas + 4 * sms > 0x7FFFFFFFull) return fail(PSK_E_SHAPE, "tokens x cols too large");
   P.run_ctas = (int32_t)ctas;
   with_bool(idt == PSK_I64, [&](auto I64) {
@@ -805,9 +835,18 @@ extern "C" int psk_embed_backward(const void* ids, int32_t idt, int64_t tokens, 
     return with_dtype(dt, [&](auto DT) {
       return with_bool(vec, [&](auto VEC) {
         const unsigned grid = (unsigned)(ctas + zero_ctas);
-        if (accumulate) launch_after(embed_runs_kernel<CT.value, DT.value, VEC.value, 4, true>, grid, EMB_THREADS, s, P);
-        else if (wide) launch_after(embed_runs_kernel<CT.value, DT.value, VEC.value, 8, false>, grid, EMB_THREADS, s, P);
-        else launch_after(embed_runs_kernel<CT.value, DT.value, VEC.value, 4, false>, grid, EMB_THREADS, s, P);
+        auto launch = [&](auto NC, auto ACC, auto PARTS) {
+          launch_after(embed_runs_kernel<CT.value, DT.value, VEC.value, NC.value, ACC.value, PARTS.value>, grid, EMB_THREADS, s, P);
+        };
+        using std::integral_constant;
+        using Four = integral_constant<int, 4>;
+        using One = integral_constant<int, 1>;
+        if (cut.columns == 8) launch(integral_constant<int, 8>{}, std::false_type{}, One{});
+        else with_bool(accumulate != 0, [&](auto ACC) {
+          if (cut.parts == 4) launch(Four{}, ACC, Four{});
+          else launch(Four{}, ACC, One{});
+          return 0;
+        });
         return 0;
       });
     });

@@ -184,3 +184,28 @@ def test_calls_at_the_same_time(R):
     for _, o in sets:
         for k in ("loss", "g", "dx", "dg", "d"):
             assert torch.equal(o[k], want[k]), k
+
+
+@pytest.mark.parametrize("tokens", [300, 2000, 20000])
+@pytest.mark.parametrize("cols", [264, 771])
+@pytest.mark.parametrize("ids", ["few", "many", "one"])
+def test_adding_to_a_leaf_is_the_leaf_plus_the_gradient(R, tokens, cols, ids):
+    torch.manual_seed(tokens + cols)
+    vocab = {"few": 9, "many": 1500, "one": 40}[ids]
+    t = torch.full((tokens,), 17, device="cuda") if ids == "one" else torch.randint(-1, vocab, (tokens,), device="cuda")
+    ct = torch.randn(tokens, cols, device="cuda").to(torch.bfloat16)
+    ws = scratch(R.psk_embed_workspace(tokens, vocab, cols))
+    g = torch.empty(vocab, cols, device="cuda")
+    R.psk_embed_backward(t, ct, g, scale=0.75, workspace=ws)
+    seen = torch.zeros(vocab, dtype=torch.bool, device="cuda")
+    seen[t[t >= 0]] = True
+    assert not g[~seen].any()
+    for dt in (torch.float32, torch.bfloat16):
+        old = torch.randn(vocab, cols, device="cuda").to(dt)
+        old[~seen] = float("nan")                # left as they are
+        d = old.clone()
+        R.psk_embed_backward(t, ct, d, scale=0.75, accumulate=True, workspace=ws)
+        torch.cuda.synchronize()
+        # One f32 rounding of the sum, one to the leaf's type.
+        assert torch.equal(d[seen], (old.float() + g).to(dt)[seen])
+        assert bool(d[~seen].isnan().all())
