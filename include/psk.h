@@ -472,7 +472,9 @@ int psk_dropout(const void* x, int32_t xt, const void* residual, int32_t rt, voi
  * x, ct, dx: f32 or bf16 rows, leading dimensions ldx, ldc, ldd >= cols; dx
  * may be x or ct in place (same type and leading dimension), no other overlap.
  * cols up to 49152; rows == 0 writes zero dgamma and dbeta.  workspace: as for
- * psk_embed_backward, psk_norm_backward_workspace bytes. */
+ * psk_embed_backward, psk_norm_backward_workspace bytes.  Between
+ * the first and the last row, bytes beside a row that share a 16-byte block
+ * with it may be read (never used, never written). */
 int psk_norm_backward_workspace(int64_t rows, int64_t cols, uint64_t* bytes);
 int psk_norm_backward(const void* x, int32_t xt, const void* ct, int32_t ct_t, void* dx, int32_t dxt, int64_t rows,
                       int64_t cols, int64_t ldx, int64_t ldc, int64_t ldd, int32_t kind, double eps,
