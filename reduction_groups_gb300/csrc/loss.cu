@@ -198,6 +198,12 @@ __device__ __forceinline__ void row_logp_pair(float xt, const RowSum& v, float s
   log_tier1_core(v.s, 0, tab, R, d);                    // s >= 1: the maximum's own term
   two_sum(xt, -v.m, th, tl);
   two_prod(scale, th, ph, pl);
+  if (!(fabsf(ph) < INFINITY)) {                        // x_t - m or its product passes f32, whose error terms mean nothing then
+    const double z = (double)scale * ((double)xt - (double)v.m) - ((double)R + (double)d);
+    hi = (float)z;
+    lo = fabsf(hi) < INFINITY ? (float)(z - (double)hi) : 0.0f;
+    return;
+  }
   pl = fmaf(scale, tl, pl);
   two_sum(ph, -R, hi, lo);
   lo += pl - (d + __fdividef(v.e, v.s));
