@@ -784,9 +784,10 @@ __global__ void __launch_bounds__(RES_THREADS, 1) loss_resident_kernel(const __g
         const float ratio = expf(pair_minus(hi, lo, info.old));
         const float a = info.w * row_slope(L, ratio, em_q, info.adv) * L.scale;
         // softmax_j = 2^(c x_j - RN(c m)) 2^(RN(c m) - c m) / s in one fma a
-        // logit, but for values whose product might leave f32.
+        // logit, where the product's rounding error, an exponent here, is at most
+        // a half (from 2^31 on it can pass 127); else 2^(c (x_j - m)) / s.
         const float mc = v.m * c;
-        const bool near = fabsf(mc) < 0x1p100f;
+        const bool near = fabsf(mc) < 0x1p24f;
         const float f = __fdividef(-a, v.s);
         if (lane == 0)
           S.coef[team] = make_float4(near ? f * ex2_approx(fmaf(-v.m, c, mc)) : f, a * -em, near ? mc : v.m,

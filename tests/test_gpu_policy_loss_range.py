@@ -64,7 +64,12 @@ def _check(R, x, xv, t, scale, gt, kl=0.0, modes=("logp", "value", "gradient")):
         close(loss, *want["loss"], "f32")
         _close_or_infinite(out, *want["logp"])
         if d is not None:
-            close(d, *want["dlogits"], gt)
+            # An exponential below 2^-126 is taken as zero, in the fused form one of up to sqrt(2) times as much:
+            # with the row's coefficient |a| = |w dterm scale|, the ratio at most 1.25 here, an absolute error
+            # below 2^-125 |a| on top of the relative ones.
+            flushed = 2.0 ** -125 * 1.25 * np.abs(w * adv)[:, None].astype(np.float64) * scale
+            value, bound = want["dlogits"]
+            close(d, value, bound + flushed, gt)
     assert R.psk_device_status() == 0
 
 
@@ -100,3 +105,43 @@ def test_a_difference_beyond_the_range(R, cols, lt, scale):
     a[0, t[0]], a[1, t[1]], a[3, t[3]] = -3e38, -1e38, -2.5e38
     x, xv = stored(a, lt)
     _check(R, x, xv, t, scale, lt)
+
+
+def _far_rows(cols, top, step):
+    """Six rows whose maximum is `top`, with `step` the distance of neighbouring values there: all equal;
+    two levels, the token at the upper and at the lower one; all at -top; a ladder of neighbouring values; one
+    far above the others."""
+    rng = np.random.default_rng(cols)
+    a = np.full((6, cols), top)
+    lower = rng.random((2, cols)) < 0.5
+    a[1:3][lower] -= 2.0 ** 17 * step
+    t = rng.integers(0, cols, 6)
+    a[1, t[1]] = a[2, (t[2] + 1) % cols] = top
+    a[2, t[2]] = top - 2.0 ** 17 * step
+    a[3] = -top
+    a[4] -= step * rng.integers(0, 16, cols)
+    a[4, t[4]] = top
+    a[5] = rng.normal(size=cols) * top / 64
+    a[5, t[5]] = top
+    return a, t
+
+
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("lt", ["bf16", "f32"])
+@pytest.mark.parametrize("through", ["logits", "scale"])
+@pytest.mark.parametrize("power", [20, 23, 24, 27, 29, 31, 34, 60, 99])
+def test_scaled_logits_far_from_zero(R, cols, lt, through, power):
+    """scale * max from 2^20 to 2^99 (1.37 times it: no power of two, whose products would be exact)."""
+    far = 1.37 * 2.0 ** power
+    top, scale = (far, 1.0) if through == "logits" else (10.0, far / 10.0)
+    a, t = _far_rows(cols, top, 2.0 ** (np.floor(np.log2(top)) - 23))
+    x, xv = stored(a, lt)
+    _check(R, x, xv, t, scale, lt)
+
+
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("lt", ["bf16", "f32"])
+def test_tiny_logits_at_the_largest_scale(R, cols, lt):
+    a, t = _far_rows(cols, 5e-22, 2.0 ** -94)       # scale * max = 5e8; a gradient of 1e29
+    x, xv = stored(a, lt)
+    _check(R, x, xv, t, 1e30, lt)
