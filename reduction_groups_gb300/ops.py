@@ -343,10 +343,10 @@ def _bind_torch() -> None:
 
     _CODES.update({torch.float32: N.PSK_F32, torch.bfloat16: N.PSK_BF16})
     _IDS.update({torch.int32: N.PSK_I32, torch.int64: N.PSK_I64})
-    _F32 = torch.float32
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _current_stream = raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
     _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # of tensors on a CUDA device
+    _F32 = torch.float32     # last: calls on other threads bind for themselves until it is set
 
 
 def _code(t, what: str) -> int:

@@ -169,3 +169,32 @@ def test_binding_refuses_what_it_cannot_pass_on(native):
         R.psk_embed(torch.zeros(4, dtype=torch.int64), x, torch.zeros(4, 8))
     with pytest.raises(ValueError, match="one device"):
         R.psk_token_logp(x, torch.zeros(4, dtype=torch.int64, device="meta"), torch.zeros(4))
+
+
+def test_binding_torch_is_complete_before_it_shows(monkeypatch):
+    """A call on another thread binds for itself until every lookup is bound: whatever torch attribute the
+    binding reads, the flag that calls go by must not be set yet."""
+    import sys
+    import types
+
+    from reduction_groups_gb300 import ops
+
+    for name in ("_F32", "_current_device", "_current_stream"):
+        monkeypatch.setattr(ops, name, None)
+    read = []
+
+    class Watched(types.ModuleType):
+        def __init__(self, real):
+            super().__init__("torch")
+            self.__dict__["_real"] = real
+
+        def __getattr__(self, name):
+            read.append(name)
+            assert ops._F32 is None or None not in (ops._current_device, ops._current_stream), name
+            v = getattr(self._real, name)
+            return Watched(v) if name in ("_C", "cuda") else v
+
+    monkeypatch.setitem(sys.modules, "torch", Watched(torch))
+    ops._bind_torch()
+    assert "_C" in read and ops._F32 is torch.float32
+    assert ops._current_device is not None and ops._current_stream is not None
