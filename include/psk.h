@@ -498,8 +498,12 @@ int psk_norm_backward(const void* x, int32_t xt, const void* ct, int32_t ct_t, v
  * A row of weight 0 or of a padding target is left out: its logits are not
  * read, its logp is 0 and its gradient row zero.  A row holding a NaN or +inf
  * logit, or only -inf, gives NaN; -inf logits otherwise have probability 0.
- * A zero advantage gives zero terms whatever the (non-NaN) ratio.  Each row's
- * logp carries an absolute error of a few 1e-7.
+ * A zero advantage gives zero terms whatever the (non-NaN) ratio.  A logp
+ * below f32's range is -inf, its ratio 0.  Each row's logp carries an absolute
+ * error of a few 1e-7 (rows of several 100000 columns: 2^-24 for each 256 of
+ * them at most) and its own rounding (2^-24 |logp|); 1 - softmax at the target
+ * carries the first too.  Softmax values below 2^-125 may be taken as 0, ratios
+ * and exp(q) beyond f32's range as infinite.
  * logp may be NULL; ref_logp may be NULL if kl_coef is 0; dlogits NULL computes
  * the loss alone, else rows (type gt, ldg >= cols) written whole, in place of
  * the logits if wanted (same type and leading dimension).  No other overlap.

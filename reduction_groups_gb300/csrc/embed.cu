@@ -605,7 +605,7 @@ static void launch_after(K kernel, unsigned grid, int threads, cudaStream_t s, c
 static uint64_t align256(uint64_t n) { return (n + 255) / 256 * 256; }
 
 // How the run sums are cut: eight columns a lane where that leaves 16 warps an
-// SM of 152; four, into a gradient that is added to too (latency then counts
+// SM; four, into a gradient that is added to too (latency then counts
 // more than the instructions for each row); and quarters of a run where four
 // columns leave fewer than 4 warps an SM, each of which would pass its 32
 // entries alone on its scheduler (500 tokens x 1001 bf16: 14.9 us, whole runs
@@ -615,8 +615,8 @@ struct EmbedCut {
 };
 static EmbedCut embed_cut(int64_t tokens, int64_t cols, bool accumulate) {
   const int64_t runs = (tokens + EMB_RUN - 1) / EMB_RUN;
-  if (!accumulate && runs * ((cols + 255) / 256) >= 16 * 152) return {8, 1};
-  return {4, runs * ((cols + 127) / 128) >= 4 * 152 ? 1 : 4};
+  if (!accumulate && runs * ((cols + 255) / 256) >= 16 * NOMINAL_SMS) return {8, 1};
+  return {4, runs * ((cols + 127) / 128) >= 4 * NOMINAL_SMS ? 1 : 4};
 }
 
 // Workspace layout: the sorted list, each id's places in it, the head and tail

@@ -6,11 +6,17 @@
 //   loss  = sum w (term + beta k)
 //   dx_j  = scale w (dterm/dlogp - beta (e^q - 1)) ([j = t] - softmax_j)
 // Sums of 2^(c (x - m)) about a running maximum m (c = scale log2 e; the
-// maximum's own term is exactly 1), rescaled when the maximum grows, joined
-// across threads in pairs of floats (sum and rounding error), so that 1 - p of
-// a nearly certain token keeps its digits; logp is formed in 64 bits, and the
-// ratio and the KL term from it with an exp of extra digits (exp_tier1_core),
-// since their sum over rows cancels.
+// maximum's own term is exactly 1), rescaled when the maximum grows: plain f32
+// within a thread, joined across threads in pairs of floats (sum and rounding
+// error).  So logp, and 1 - p of a nearly certain token, carry an absolute error
+// of a few 2^-24; keeping more within a thread too would cost every step of
+// sixteen logits its issue slots for digits that only the target's own entry has.
+// logp is formed with its rounding error (a pair of floats, or 64 bits where
+// f32 overflows and for long rows), and the loss's ratio and KL term from it in
+// 64 bits with an exp of extra digits (exp_tier1_core), since their sum over
+// rows cancels.  The gradient, whose entries do not, takes both in f32 in the
+// resident kernel; within their rounding of a clip bound its case may differ
+// from the loss's.
 #include "vec8.cuh"
 #include "crmath.cuh"
 #include "pair.cuh"

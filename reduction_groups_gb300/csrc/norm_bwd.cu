@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(NB_THREADS) norm_bwd_zero_kernel(const __grid_
 // GPU, at least 16 rows each.
 static int norm_bwd_blocks(int64_t rows, int64_t cols) {
   const int64_t slices = (cols + 255) / 256;
-  int64_t b = (152 * 8 + slices - 1) / slices;
+  int64_t b = (NOMINAL_SMS * 8 + slices - 1) / slices;
   if (b > (rows + 15) / 16) b = (rows + 15) / 16;
   return (int)(b < 1 ? 1 : b > NB_MAX_BLOCKS ? NB_MAX_BLOCKS : b);
 }
@@ -745,8 +745,8 @@ static bool ring_shape(NormRingParams& Q, int* nv, int32_t dt, int32_t kind, boo
     int fits = (RING_SMEM - *nv * 8 * Q.team * 4) / (2 * Q.row_bytes);
     if (fits > RING_MAX_SLOTS) fits = RING_MAX_SLOTS;
     // RMSNorm is held to about 128 KB in flight: more reads ahead cost it DRAM
-    // time ([32768, 4096] bf16: 133 us with 128 KB, 146 with 192); LayerNorm's
-    // two barriers want all there is (134 us with 192 KB, 141 with 128).
+    // time (measured at [32768, 4096] bf16: 133 us with 128 KB, 146 with 192);
+    // LayerNorm's two barriers want all there is (134 us with 192 KB, 141 with 128).
     if (kind == PSK_NORM_RMS) {
       const int enough = (128 * 1024) / (2 * Q.row_bytes), least = (Q.teams <= 2 ? 3 : 2) * Q.teams;
       if (fits > enough && fits > least) fits = enough > least ? enough : least;

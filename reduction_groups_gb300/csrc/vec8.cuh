@@ -10,6 +10,10 @@
 
 namespace psk {
 
+// SMs that the rules of cutting work count on where the answer must not vary
+// with the device, or be known without one (workspace sizes): a GB300's.
+constexpr int NOMINAL_SMS = 152;
+
 // bf16 or f32 elements [i, i + n) of p as f32; lanes from n on are 0.
 template <int DT, bool VEC>
 __device__ __forceinline__ void load8(const void* p, int64_t i, int n, float* v) {

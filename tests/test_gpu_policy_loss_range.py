@@ -145,3 +145,18 @@ def test_tiny_logits_at_the_largest_scale(R, cols, lt):
     a, t = _far_rows(cols, 5e-22, 2.0 ** -94)       # scale * max = 5e8; a gradient of 1e29
     x, xv = stored(a, lt)
     _check(R, x, xv, t, 1e30, lt)
+
+
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("lt", ["bf16", "f32"])
+def test_nearly_certain_tokens(R, cols, lt):
+    """The target's probability within 2^-8 to 2^-30 of one, the runner-up beside it, in another 16-byte group
+    or half a row away: the other entries keep their digits, the target's carries the absolute error of logp."""
+    places = (1, 17, cols // 2)
+    a = np.full((12, cols), -104.0)
+    t = (np.arange(12) * 53) % cols
+    for r in range(12):
+        a[r, t[r]] = 0.0
+        a[r, (t[r] + places[r % 3]) % cols] = np.log(2.0) * -(8, 16, 25, 30)[r // 3]
+    x, xv = stored(a, lt)
+    _check(R, x, xv, t, 1.0, lt, kl=0.1)
