@@ -21,7 +21,10 @@
  * step begins and ends: psk_embed and psk_embed_backward (token embedding and
  * its leaf gradient), psk_dropout, psk_norm_backward (the norm regions'
  * backward), psk_token_logp and psk_policy_loss (log-probabilities and the
- * clipped policy loss over vocabulary rows, with its gradient).  Their f32
+ * clipped policy loss over vocabulary rows, with its gradient); and those of
+ * a layer's matrices: psk_linear and its backward, psk_qk_norm_rotary (the
+ * norm and rotation of query and key heads) and its backward, and
+ * psk_orthogonalize (the orthogonalised update of matrix leaves).  Their f32
  * sums run over fixed trees, not over a declared order: one call's bits
  * repeat on one device.
  *
@@ -517,6 +520,128 @@ int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int64_t cols, 
                     const float* advantage, const float* weight, double clip_low, double clip_high, double kl_coef,
                     float* loss, float* logp, void* dlogits, int32_t gt, int64_t ldg, void* workspace,
                     uint64_t workspace_bytes, void* stream);
+
+/* ============================================================ psk_linear
+ * The linear layer over rows of `in` elements:
+ *   z = x w + bias,   y = act(z) + residual
+ * x: rows x in (f32 or bf16, ldx >= in).  w: in x out (PSK_W_IN_OUT: in rows
+ * of out elements, as the parameter trees hold them; PSK_W_OUT_IN: out rows of
+ * in), leading dimension ldw of its memory rows.  bias: out elements or NULL;
+ * residual: rows x out or NULL.  z: NULL, or rows x out that receive z (what
+ * the backward reads).  Every tensor f32 or bf16, of its own type.
+ * The products of a sum are exact (an f32 operand enters as three bf16 parts,
+ * products of parts below 2^-24 of the largest left out) and added in f32 in
+ * an order fixed by the sizes and types; z, act and the residual's sum in f32;
+ * y and z are rounded once.  PSK_ACT_GELU is z Phi(z), its negative tail to
+ * f32's relative accuracy; at z = +-inf an activation is its limit.  A row of
+ * x or a column of w that holds an infinity or a NaN gives infinities or NaNs
+ * in its own row or column of z (NaN also where the exact sum is infinite, if
+ * an operand is f32).
+ * y may be the residual in place (same type and leading dimension); no other
+ * overlap of what is written with anything else.  rows, out < 2^31 - 1024, in
+ * <= 2^25; in == 0 leaves z = bias.  workspace: 16-byte aligned DEVICE scratch
+ * of at least psk_linear_workspace bytes (0 for bf16 operands with 16-byte
+ * aligned rows), no initialisation, one per concurrent call (calls and
+ * captured graphs that may overlap in time must not share it). */
+typedef enum { PSK_W_IN_OUT = 0, PSK_W_OUT_IN = 1 } psk_weight_layout;
+typedef enum { PSK_ACT_NONE = 0, PSK_ACT_RELU = 1, PSK_ACT_GELU = 2, PSK_ACT_SILU = 3 } psk_act;
+int psk_linear_workspace(const void* x, int32_t xt, int64_t ldx, const void* w, int32_t wt, int64_t ldw,
+                         int32_t layout, int64_t rows, int64_t in, int64_t out, uint64_t* bytes);
+int psk_linear(const void* x, int32_t xt, int64_t ldx, const void* w, int32_t wt, int64_t ldw, int32_t layout,
+               int64_t rows, int64_t in, int64_t out, const void* bias, int32_t bt, int32_t act, const void* residual,
+               int32_t rt, int64_t ldr, void* z, int32_t zt, int64_t ldz, void* y, int32_t yt, int64_t ldy,
+               void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* The linear layer's backward from y's cotangent ct (rows x out):
+ *   dz = ct act'(z),  dx = dz w^T,  dw = x^T dz,  dbias = the column sums of dz
+ * (the residual's gradient is ct).  z: as psk_linear stored it; not read for
+ * PSK_ACT_NONE.  dx (rows x in), dw (w's layout) and dbias (out elements) may
+ * each be NULL: not wanted; x is read for dw alone, w for dx alone.  With
+ * accumulate != 0, dw and dbias are added to (micro-batches that share a
+ * leaf): RN(dw + sum).  dz is formed in f32; a product of bf16 ct, bf16
+ * operand and bf16 result takes it rounded to bf16, any other to f32's
+ * accuracy.  act' of relu at 0 is 0.  rows == 0 gives dw = 0 and dbias = 0
+ * (accumulating: unchanged).  No overlap of what is written with anything
+ * else.  rows, out <= 2^25, in < 2^31 - 1024.  workspace as for psk_linear,
+ * psk_linear_backward_workspace bytes for the same arguments. */
+int psk_linear_backward_workspace(const void* ct, int32_t ct_t, int64_t ldc, const void* x, int32_t xt, int64_t ldx,
+                                  const void* w, int32_t wt, int64_t ldw, int32_t layout, int64_t rows, int64_t in,
+                                  int64_t out, int32_t act, const void* dx, int32_t dxt, const void* dw, int32_t dwt,
+                                  const void* dbias, int32_t dbt, uint64_t* bytes);
+int psk_linear_backward(const void* ct, int32_t ct_t, int64_t ldc, const void* x, int32_t xt, int64_t ldx,
+                        const void* w, int32_t wt, int64_t ldw, int32_t layout, int64_t rows, int64_t in, int64_t out,
+                        int32_t act, const void* z, int32_t zt, int64_t ldz, void* dx, int32_t dxt, int64_t lddx,
+                        void* dw, int32_t dwt, int64_t lddw, void* dbias, int32_t dbt, int32_t accumulate,
+                        void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* =================================================== psk_orthogonalize
+ * The orthogonalised update of matrix leaves (the Muon optimiser's): each of
+ * n_leaves matrices G of one shape goes through `steps` Newton-Schulz products,
+ *   X = G / (||G||_F + eps);  X <- a X + b (X X^T) X + c (X X^T)^2 X,
+ * with the step's (a, b, c) = coefficients[3 i .. 3 i + 2] (HOST, each in
+ * [-32, 32]), and y = scale X.  x, y: rows x cols, one storage type each, ldx,
+ * ldy >= cols; y may be any of the x (all are read before the first y is
+ * written), the results must not overlap one another.  X is held in two
+ * fp16 parts (times 2^10), sums are f32; for a y stored in bf16 the products
+ * take one part of each factor (an error of 1e-3 of ||y|| at most for matrices
+ * of some size, below the storage's), for f32 two.  Coefficients that drive a
+ * singular value beyond 2^5 overflow.  A zero
+ * matrix (with eps > 0) gives zeros; a matrix with a NaN or an infinity gives
+ * NaNs, alone.  steps in [1, 64]; rows, cols <= 2^20; n_leaves <=
+ * PSK_ORTHO_MAX_LEAVES; an empty list or shape launches nothing.  workspace as
+ * for psk_linear, psk_orthogonalize_workspace bytes. */
+#define PSK_ORTHO_MAX_LEAVES 512
+typedef struct {
+  const void* x;
+  int64_t ldx;
+  void* y;
+  int64_t ldy;
+} psk_ortho_leaf;
+int psk_orthogonalize_workspace(int32_t n_leaves, int64_t rows, int64_t cols, int32_t yt, uint64_t* bytes);
+int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves, int64_t rows, int64_t cols, int32_t xt,
+                      int32_t yt, const double* coefficients, int32_t steps, double eps, double scale, void* workspace,
+                      uint64_t workspace_bytes, void* stream);
+
+/* ================================================== psk_qk_norm_rotary
+ * The norm of each query and key head and its rotation by the token's
+ * position, in one pass.  q: tokens x hq x dim, k: tokens x hk x dim (xt), with
+ * element strides of a token and of a head (columns of the qkv product's rows,
+ * for instance, or head after head); yq, yk likewise (yt).
+ *   u = x / sqrt(mean(x^2) + eps) gamma      (PSK_HEAD_NORM_RMS; gamma NULL: 1)
+ *   u = x                                    (PSK_HEAD_NORM_NONE)
+ * then pair j < rot / 2 of the first rot columns turns by the angle
+ * positions[token] freqs[j]:
+ *   (u_a, u_b) -> (u_a cos - u_b sin, u_b cos + u_a sin),
+ * a = j, b = j + rot / 2 (PSK_PAIRS_HALVES) or a = 2 j, b = 2 j + 1
+ * (PSK_PAIRS_NEIGHBOURS); columns from rot on do not turn.  positions: DEVICE,
+ * PSK_I32 or PSK_I64, any sign; freqs: rot / 2 f32, radians a position.  The
+ * angle is the exact product reduced to a turn with an error of 2^-62 a
+ * position.  Arithmetic in f32, one rounding to yt.  yq may be q and yk k in
+ * place (same type and strides); no other overlap.  hq or hk may be 0.  dim
+ * in [1, 512], rot even, <= dim.
+ *
+ * The backward, from the cotangents cq, ck of yq, yk: with g the cotangent
+ * turned back, d = sqrt(mean(x^2) + eps), xh = x / d and t = g gamma,
+ *   dx = (t - xh mean(t xh)) / d,   dgamma = sum over tokens and heads of g xh
+ * (PSK_HEAD_NORM_NONE: dx = g; q and k are not read).  dgamma_q, dgamma_k may
+ * be NULL: not wanted.  dq may be cq or q in place, dk ck or k; no other
+ * overlap.  tokens == 0 writes zero dgamma.  workspace as for psk_linear,
+ * psk_qk_norm_rotary_backward_workspace bytes; none is read without a dgamma. */
+typedef enum { PSK_HEAD_NORM_NONE = 0, PSK_HEAD_NORM_RMS = 1 } psk_head_norm;
+typedef enum { PSK_PAIRS_HALVES = 0, PSK_PAIRS_NEIGHBOURS = 1 } psk_pairs;
+int psk_qk_norm_rotary(const void* q, const void* k, int32_t xt, int64_t q_token, int64_t q_head, int64_t k_token,
+                       int64_t k_head, void* yq, void* yk, int32_t yt, int64_t yq_token, int64_t yq_head,
+                       int64_t yk_token, int64_t yk_head, int64_t tokens, int64_t hq, int64_t hk, int64_t dim,
+                       int64_t rot, const void* positions, int32_t pt, const float* freqs, int32_t pairs, int32_t norm,
+                       double eps, const void* gamma_q, const void* gamma_k, int32_t gt, void* stream);
+int psk_qk_norm_rotary_backward_workspace(int64_t tokens, int64_t hq, int64_t hk, int64_t dim, uint64_t* bytes);
+int psk_qk_norm_rotary_backward(
+    const void* cq, const void* ck, int32_t ct, int64_t cq_token, int64_t cq_head, int64_t ck_token, int64_t ck_head,
+    const void* q, const void* k, int32_t xt, int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head,
+    void* dq, void* dk, int32_t dt, int64_t dq_token, int64_t dq_head, int64_t dk_token, int64_t dk_head,
+    int64_t tokens, int64_t hq, int64_t hk, int64_t dim, int64_t rot, const void* positions, int32_t pt,
+    const float* freqs, int32_t pairs, int32_t norm, double eps, const void* gamma_q, const void* gamma_k, int32_t gt,
+    void* dgamma_q, void* dgamma_k, int32_t dgt, void* workspace, uint64_t workspace_bytes, void* stream);
 
 /* Host-only, synchronous: the device status word of the pipelined kernels of
  * the current device (0 = no bounded wait ever timed out; bit 0 = a wait gave

@@ -2,7 +2,9 @@
 loop nest, the reduction-rooted softmax region, and the AdamW step over a
 parameter tree, each one CUDA launch through a C ABI (include/psk.h); and
 around them the operators a training step begins and ends with: the embedding
-and its gradient, dropout, the norms' backward and the clipped policy loss.
+and its gradient, dropout, the norms' backward and the clipped policy loss; and
+those of a layer's matrices: the linear layer and its gradient, the norm and
+rotation of query and key heads, and the orthogonalised update.
 
     from reduction_groups_gb300 import psk_group_run, psk_softmax_region, psk_adamw_tree
 """
@@ -26,11 +28,20 @@ from .ops import (  # noqa: F401
     psk_group_prepare,
     psk_group_run,
     psk_group_run_interp,
+    psk_linear,
+    psk_linear_backward,
+    psk_linear_backward_workspace,
+    psk_linear_workspace,
     psk_norm_backward,
     psk_norm_backward_workspace,
     psk_norm_region,
+    psk_orthogonalize,
+    psk_orthogonalize_workspace,
     psk_policy_loss,
     psk_policy_loss_workspace,
+    psk_qk_norm_rotary,
+    psk_qk_norm_rotary_backward,
+    psk_qk_norm_rotary_backward_workspace,
     psk_softmax_backward,
     psk_softmax_masked,
     psk_softmax_region,

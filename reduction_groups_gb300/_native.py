@@ -19,6 +19,11 @@ PSK_NORM_RMS, PSK_NORM_LAYER = 0, 1
 PSK_LR_CONSTANT, PSK_LR_LINEAR, PSK_LR_COSINE = 0, 1, 2
 PSK_MAX_RANK = 4
 PSK_ADAMW_MAX_LEAVES = 512
+PSK_W_IN_OUT, PSK_W_OUT_IN = 0, 1
+PSK_ACT_NONE, PSK_ACT_RELU, PSK_ACT_GELU, PSK_ACT_SILU = 0, 1, 2, 3
+PSK_ORTHO_MAX_LEAVES = 512
+PSK_HEAD_NORM_NONE, PSK_HEAD_NORM_RMS = 0, 1
+PSK_PAIRS_HALVES, PSK_PAIRS_NEIGHBOURS = 0, 1
 
 ERRORS = {
     -1: "PSK_E_PROGRAM", -2: "PSK_E_TOO_MANY_NODES", -3: "PSK_E_SHAPE", -4: "PSK_E_DTYPE",
@@ -32,6 +37,9 @@ EXPORTS = ("psk_group_run", "psk_group_run_ex", "psk_group_run_interp", "psk_gro
            "psk_embed", "psk_embed_workspace", "psk_embed_backward", "psk_dropout",
            "psk_norm_backward_workspace", "psk_norm_backward",
            "psk_token_logp", "psk_policy_loss_workspace", "psk_policy_loss",
+           "psk_linear_workspace", "psk_linear", "psk_linear_backward_workspace", "psk_linear_backward",
+           "psk_orthogonalize_workspace", "psk_orthogonalize",
+           "psk_qk_norm_rotary", "psk_qk_norm_rotary_backward_workspace", "psk_qk_norm_rotary_backward",
            "psk_device_status", "psk_test_drop_row", "psk_test_fast_exp", "psk_last_error")
 
 
@@ -67,6 +75,10 @@ class psk_adamw_hparams(ctypes.Structure):
 class psk_adamw_schedule(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("warmup", ctypes.c_int64), ("total", ctypes.c_int64),
                 ("grad_clip", ctypes.c_double)]
+
+
+class psk_ortho_leaf(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
 
 
 class PskError(RuntimeError):
@@ -136,6 +148,19 @@ def lib() -> ctypes.CDLL:
         L.psk_policy_loss_workspace.argtypes = [I64, I64, P(U64)]
         L.psk_policy_loss.argtypes = [V, I32, I64, I64, I64, F64, V, I32, V, V, V, V, F64, F64, F64, V, V, V, I32, I64,
                                       V, U64, V]
+        mat, head = [V, I32, I64], [I64, I64]
+        L.psk_linear_workspace.argtypes = mat + mat + [I32, I64, I64, I64, P(U64)]
+        L.psk_linear.argtypes = mat + mat + [I32, I64, I64, I64, V, I32, I32] + mat + mat + mat + [V, U64, V]
+        L.psk_linear_backward_workspace.argtypes = (mat + mat + mat + [I32, I64, I64, I64, I32, V, I32, V, I32, V, I32,
+                                                                       P(U64)])
+        L.psk_linear_backward.argtypes = (mat + mat + mat + [I32, I64, I64, I64, I32] + mat + mat + mat
+                                          + [V, I32, I32, V, U64, V])
+        L.psk_orthogonalize_workspace.argtypes = [I32, I64, I64, I32, P(U64)]
+        L.psk_orthogonalize.argtypes = [P(psk_ortho_leaf), I32, I64, I64, I32, I32, P(F64), I32, F64, F64, V, U64, V]
+        rot = [I64, I64, I64, I64, I64, V, I32, V, I32, I32, F64, V, V, I32]
+        L.psk_qk_norm_rotary.argtypes = [V, V, I32] + head * 2 + [V, V, I32] + head * 2 + rot + [V]
+        L.psk_qk_norm_rotary_backward_workspace.argtypes = [I64, I64, I64, I64, P(U64)]
+        L.psk_qk_norm_rotary_backward.argtypes = (([V, V, I32] + head * 2) * 3 + rot + [V, V, I32, V, U64, V])
         L.psk_last_error.restype = ctypes.c_char_p
         for f in ("psk_group_run", "psk_group_run_ex", "psk_group_run_interp", "psk_group_check", "psk_group_prepare", "psk_group_prepare_ex",
                   "psk_softmax_region", "psk_norm_region",
@@ -147,6 +172,9 @@ def lib() -> ctypes.CDLL:
                   "psk_embed", "psk_embed_workspace", "psk_embed_backward", "psk_dropout",
                   "psk_norm_backward_workspace", "psk_norm_backward",
                   "psk_token_logp", "psk_policy_loss_workspace", "psk_policy_loss",
+                  "psk_linear_workspace", "psk_linear", "psk_linear_backward_workspace", "psk_linear_backward",
+                  "psk_orthogonalize_workspace", "psk_orthogonalize",
+                  "psk_qk_norm_rotary", "psk_qk_norm_rotary_backward_workspace", "psk_qk_norm_rotary_backward",
                   "psk_device_status", "psk_test_drop_row", "psk_test_fast_exp"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L

@@ -1,0 +1,498 @@
+// psk_linear: y = act(x w + bias) + residual, and its backward.  The products
+// run in matmul.cu; here are what prepares their operands and the host side.
+//
+// An operand stored in bf16 with 16-byte aligned rows goes to the tensor
+// cores as it stands.  Any other is copied into the workspace first: rows
+// padded to 16 bytes, and an f32 operand split into three bf16 parts, h =
+// RN(x), m = RN(x - h), l = RN(x - h - m), whose sum is x to its last bit (24
+// = 3 x 8 significant bits).  Of the nine products of parts the six above
+// 2^-24 of the largest are added, from the smallest up; the three left out
+// are below 2^-24 |x w| together.
+#include "common.cuh"
+#include "vec8.cuh"
+#include "act.cuh"
+#include "mm.h"
+#include "views.h"
+
+namespace psk {
+
+constexpr int64_t LINEAR_MAX_SUM = 1LL << 25;      // of a product: a tile's time stays far below a wait's bound
+constexpr int64_t LINEAR_MAX_SIDE = (1LL << 31) - 1024;
+constexpr int PACK_THREADS = 256;
+
+// x as the sum of three bf16 parts; an infinity or a NaN is the first part alone.
+__device__ __forceinline__ void split3(float x, uint32_t& h, uint32_t& m, uint32_t& l) {
+  uint32_t b = f32_to_bf16_bits(x);
+  const bool finite = fabsf(x) <= 3.4028234663852886e38f;
+  if (finite && (b & 0x7FFF) == 0x7F80) b -= 1;              // rounded up to infinity: the largest bf16 instead
+  const float r = finite ? x - bf16_bits_to_f32(b) : 0.0f;
+  h = b;
+  m = f32_to_bf16_bits(r);
+  l = f32_to_bf16_bits(r - bf16_bits_to_f32(m));
+}
+
+__device__ __forceinline__ uint4 pack8(const uint32_t* h) {
+  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
+
+struct PackParams {
+  const void *x, *z;            // z: the value is x slope(z)
+  uint16_t* to;                 // planes of prows x pcols (NULL: column sums alone)
+  float* sums;                  // column sums of `blocks` blocks of rows (NULL: not wanted)
+  int64_t rows, cols, ldx, ldz, prows, pcols, plane_stride;
+  int32_t xt, zt, act, planes, vec_x, vec_z, blocks;
+};
+
+// Eight columns a thread, 256 a CTA, its warps the rows of a block in turn.
+__global__ void __launch_bounds__(PACK_THREADS) linear_pack_kernel(const __grid_constant__ PackParams P) {
+  __shared__ float part[8][256 + 8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t groups = (P.pcols + 255) / 256;
+  const int64_t cb = blockIdx.x % groups, rb = blockIdx.x / groups;
+  const int64_t c = cb * 256 + lane * 8;
+  const int64_t each = (P.prows + P.blocks - 1) / P.blocks;
+  const int64_t end = (rb + 1) * each < P.prows ? (rb + 1) * each : P.prows;
+  const int64_t left = P.cols - c;
+  const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
+  float s[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s[k] = 0.0f;
+  if (c < P.pcols)
+    for (int64_t r = rb * each + warp; r < end; r += 8) {
+      float v[8], z[8];
+      const int have = r < P.rows ? n : 0;
+      if (P.xt == PSK_BF16) {
+        if (P.vec_x) load8<PSK_BF16, true>(P.x, r * P.ldx + c, have, v);
+        else load8<PSK_BF16, false>(P.x, r * P.ldx + c, have, v);
+      } else {
+        if (P.vec_x) load8<PSK_F32, true>(P.x, r * P.ldx + c, have, v);
+        else load8<PSK_F32, false>(P.x, r * P.ldx + c, have, v);
+      }
+      if (P.act) {
+        if (P.zt == PSK_BF16) {
+          if (P.vec_z) load8<PSK_BF16, true>(P.z, r * P.ldz + c, have, z);
+          else load8<PSK_BF16, false>(P.z, r * P.ldz + c, have, z);
+        } else {
+          if (P.vec_z) load8<PSK_F32, true>(P.z, r * P.ldz + c, have, z);
+          else load8<PSK_F32, false>(P.z, r * P.ldz + c, have, z);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float g = P.act == ACT_RELU   ? act_slope<ACT_RELU>(z[k])
+                          : P.act == ACT_GELU ? act_slope<ACT_GELU>(z[k])
+                                              : act_slope<ACT_SILU>(z[k]);
+          v[k] *= g;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[k] += v[k];
+      if (P.to) {
+        uint32_t h[8], m[8], l[8];
+        uint16_t* q = P.to + r * P.pcols + c;
+        if (P.planes == 1) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[k] = f32_to_bf16_bits(v[k]);
+          *(uint4*)q = pack8(h);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) split3(v[k], h[k], m[k], l[k]);
+          *(uint4*)q = pack8(h);
+          *(uint4*)(q + P.plane_stride) = pack8(m);
+          *(uint4*)(q + 2 * P.plane_stride) = pack8(l);
+        }
+      }
+    }
+  if (!P.sums) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) part[warp][k * 33 + lane] = s[k];
+  __syncthreads();
+  const int col = threadIdx.x;
+  float t = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) t += part[w][(col & 7) * 33 + (col >> 3)];
+  if (cb * 256 + col < P.cols) P.sums[rb * P.cols + cb * 256 + col] = t;
+}
+
+// dbias from the row blocks' sums: 32 columns a CTA, 8 warps the blocks in turn.
+__global__ void __launch_bounds__(256) linear_bias_kernel(const float* sums, int blocks, int64_t cols, void* out,
+                                                          int32_t dt, int32_t add) {
+  __shared__ float part[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  float s = 0.0f;
+  if (c < cols)
+    for (int b = warp; b < blocks; b += 8) s += sums[(int64_t)b * cols + c];
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp || c >= cols) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) s += part[w][lane];
+  if (dt == PSK_BF16) {
+    uint16_t* q = (uint16_t*)out + c;
+    *q = f32_to_bf16_bits(add ? bf16_bits_to_f32(*q) + s : s);
+  } else {
+    float* q = (float*)out + c;
+    *q = add ? *q + s : s;
+  }
+}
+
+// ---------------------------------------------------------------------- host
+
+static int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+
+// A matrix of `rows` memory rows and where its tensor-core form stands.
+struct Matrix {
+  const void* p;
+  int32_t dt;
+  int64_t rows, cols, ld;
+  bool packed;
+  int planes;
+  int64_t prows, pcols;
+  uint64_t offset, bytes;       // in the workspace, when packed
+};
+
+static Matrix matrix(const void* p, int32_t dt, int64_t rows, int64_t cols, int64_t ld, uint64_t* used) {
+  Matrix m{p, dt, rows, cols, ld};
+  m.planes = dt == PSK_F32 ? 3 : 1;
+  m.packed = dt == PSK_F32 || rows == 0 || cols == 0 || !rows_vec8(p, dt, ld, rows);
+  m.prows = rows ? rows : 1, m.pcols = cols ? up8(cols) : 8;
+  m.offset = *used;
+  m.bytes = m.packed ? ((uint64_t)m.planes * m.prows * m.pcols * 2 + 255) / 256 * 256 : 0;
+  *used += m.bytes;
+  return m;
+}
+
+static MMOperand operand(const Matrix& m, void* workspace, bool k_inner) {
+  MMOperand o{};
+  o.planes = m.planes, o.k_inner = k_inner;
+  if (m.packed) {
+    o.p = (char*)workspace + m.offset;
+    o.inner = m.cols ? m.cols : 8, o.outer = m.prows, o.ld = m.pcols;
+  } else {
+    o.p = m.p, o.inner = m.cols, o.outer = m.rows, o.ld = m.rows > 1 ? m.ld : up8(m.cols);
+  }
+  o.plane_stride = o.ld * o.outer;
+  return o;
+}
+
+// Blocks of rows of the pack kernel: enough CTAs for eight an SM, 32 rows each at least.
+static int pack_blocks(int64_t rows, int64_t cols) {
+  const int64_t groups = (cols + 255) / 256;
+  int64_t b = (NOMINAL_SMS * 8 + groups - 1) / groups;
+  if (b > (rows + 31) / 32) b = (rows + 31) / 32;
+  return (int)(b < 1 ? 1 : b);
+}
+
+static int pack(const Matrix& m, void* workspace, const void* z, int32_t zt, int64_t ldz, int32_t act, bool store,
+                float* sums, cudaStream_t s) {
+  PackParams P{};
+  P.x = m.p, P.z = z;
+  P.to = store ? (uint16_t*)((char*)workspace + m.offset) : nullptr;
+  P.sums = sums;
+  P.rows = m.rows, P.cols = m.cols, P.ldx = m.ld, P.ldz = ldz;
+  P.prows = m.prows, P.pcols = m.pcols, P.plane_stride = m.prows * m.pcols;
+  P.xt = m.dt, P.zt = zt, P.act = act, P.planes = m.planes;
+  P.vec_x = rows_vec8(m.p, m.dt, m.ld, m.rows), P.vec_z = act && rows_vec8(z, zt, ldz, m.rows);
+  P.blocks = pack_blocks(m.prows, m.pcols);
+  const int64_t ctas = (m.pcols + 255) / 256 * P.blocks;
+  if (ctas > 0x7FFFFFFF) return fail(PSK_E_SHAPE, "too many blocks");
+  linear_pack_kernel<<<(unsigned)ctas, PACK_THREADS, 0, s>>>(P);
+  return check_launch("linear pack kernel");
+}
+
+// The products of the operands' planes, smallest first.
+static void plane_pairs(MMCall& C) {
+  C.pairs = 0;
+  for (int sum = 2; sum >= 0; --sum)
+    for (int a = 0; a <= sum; ++a)
+      if (a < C.a.planes && sum - a < C.b.planes) C.pa[C.pairs] = a, C.pb[C.pairs] = sum - a, ++C.pairs;
+}
+
+static int check_side(const char* what, int64_t v, int64_t most) {
+  if (v < 0 || v > most) return fail(PSK_E_SHAPE, "%s %lld is not in [0, %lld]", what, (long long)v, (long long)most);
+  return PSK_OK;
+}
+
+static int check_rows(const char* what, const void* p, int32_t dt, int64_t rows, int64_t cols, int64_t ld) {
+  if (!dtype_ok(dt)) return fail(PSK_E_DTYPE, "%s dtype %d", what, dt);
+  if (ld < cols) return fail(PSK_E_SHAPE, "%s: leading dimension %lld below %lld", what, (long long)ld, (long long)cols);
+  if (!rows_addressable(rows, ld)) return fail(PSK_E_SHAPE, "%s: rows x leading dimension too large", what);
+  if (rows && cols && !p) return fail(PSK_E_NULL, "%s is NULL", what);
+  if ((uintptr_t)p % dtype_size(dt)) return fail(PSK_E_ARG, "%s is not aligned to its type", what);
+  return PSK_OK;
+}
+
+struct Named {
+  const char* name;
+  View view;
+};
+
+static View mat_view(const void* p, int32_t dt, int64_t rows, int64_t cols, int64_t ld) {
+  if (!p) return View{0, 0, 0, 0};
+  return view_of(p, rows, cols, ld, dtype_size(dt));
+}
+
+static int check_apart(const Named& out, const Named* others, int n) {
+  for (int i = 0; i < n; ++i)
+    if (views_overlap(out.view, others[i].view)) return fail(PSK_E_ALIAS, "%s overlaps %s", out.name, others[i].name);
+  return PSK_OK;
+}
+
+static int check_workspace(const void* workspace, uint64_t bytes, uint64_t need) {
+  if (!need) return PSK_OK;
+  if (!workspace) return fail(PSK_E_NULL, "workspace is NULL, %llu bytes needed", (unsigned long long)need);
+  if ((uintptr_t)workspace % 16) return fail(PSK_E_ARG, "workspace is not 16-byte aligned");
+  if (bytes < need)
+    return fail(PSK_E_ARG, "workspace of %llu bytes, %llu needed", (unsigned long long)bytes, (unsigned long long)need);
+  return PSK_OK;
+}
+
+static int check_layout(int32_t layout) {
+  if (layout != PSK_W_IN_OUT && layout != PSK_W_OUT_IN) return fail(PSK_E_ARG, "weight layout %d", layout);
+  return PSK_OK;
+}
+
+static int check_act(int32_t act) {
+  if (act < PSK_ACT_NONE || act > PSK_ACT_SILU) return fail(PSK_E_ARG, "activation %d", act);
+  return PSK_OK;
+}
+
+// The checked operands of both directions.
+static int check_operands(const void* x, int32_t xt, int64_t ldx, const void* w, int32_t wt, int64_t ldw,
+                          int32_t layout, int64_t rows, int64_t in, int64_t out) {
+  int rc = check_side("rows", rows, LINEAR_MAX_SIDE);
+  if (!rc) rc = check_side("in", in, LINEAR_MAX_SUM);
+  if (!rc) rc = check_side("out", out, LINEAR_MAX_SIDE);
+  if (!rc) rc = check_layout(layout);
+  if (!rc) rc = check_rows("x", x, xt, rows, in, ldx);
+  if (!rc) rc = layout == PSK_W_IN_OUT ? check_rows("w", w, wt, in, out, ldw) : check_rows("w", w, wt, out, in, ldw);
+  return rc;
+}
+
+static Matrix weight(const void* w, int32_t wt, int64_t ldw, int32_t layout, int64_t in, int64_t out, uint64_t* used) {
+  return layout == PSK_W_IN_OUT ? matrix(w, wt, in, out, ldw, used) : matrix(w, wt, out, in, ldw, used);
+}
+
+}  // namespace psk
+
+using namespace psk;
+
+extern "C" int psk_linear_workspace(const void* x, int32_t xt, int64_t ldx, const void* w, int32_t wt, int64_t ldw,
+                                    int32_t layout, int64_t rows, int64_t in, int64_t out, uint64_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(PSK_E_NULL, "bytes is NULL");
+  const int rc = check_operands(x, xt, ldx, w, wt, ldw, layout, rows, in, out);
+  if (rc) return rc;
+  *bytes = 0;
+  if (!rows || !out) return PSK_OK;
+  matrix(x, xt, rows, in, ldx, bytes);
+  weight(w, wt, ldw, layout, in, out, bytes);
+  return PSK_OK;
+}
+
+extern "C" int psk_linear(const void* x, int32_t xt, int64_t ldx, const void* w, int32_t wt, int64_t ldw,
+                          int32_t layout, int64_t rows, int64_t in, int64_t out, const void* bias, int32_t bt,
+                          int32_t act, const void* residual, int32_t rt, int64_t ldr, void* z, int32_t zt, int64_t ldz,
+                          void* y, int32_t yt, int64_t ldy, void* workspace, uint64_t workspace_bytes, void* stream) {
+  clear_error();
+  int rc = check_operands(x, xt, ldx, w, wt, ldw, layout, rows, in, out);
+  if (!rc) rc = check_act(act);
+  if (!rc && bias) rc = check_rows("bias", bias, bt, 1, out, out);
+  if (!rc && residual) rc = check_rows("residual", residual, rt, rows, out, ldr);
+  if (!rc && z) rc = check_rows("z", z, zt, rows, out, ldz);
+  if (!rc) rc = check_rows("y", y, yt, rows, out, ldy);
+  if (rc || !rows || !out) return rc;
+  uint64_t need = 0;
+  const Matrix mx = matrix(x, xt, rows, in, ldx, &need), mw = weight(w, wt, ldw, layout, in, out, &need);
+  rc = check_workspace(workspace, workspace_bytes, need);
+  if (rc) return rc;
+  const View vy = mat_view(y, yt, rows, out, ldy), vz = mat_view(z, zt, rows, out, ldz),
+             vr = mat_view(residual, rt, rows, out, ldr);
+  const View vws{(uintptr_t)workspace, need ? 1 : 0, need, need};
+  const Named read[] = {{"x", mat_view(x, xt, mx.rows, mx.cols, ldx)},
+                        {"w", mat_view(w, wt, mw.rows, mw.cols, ldw)},
+                        {"the bias", mat_view(bias, bt, 1, out, out)},
+                        {"the workspace", vws},
+                        {"z", vz}};
+  rc = check_apart({"y", vy}, read, 5);
+  if (!rc && views_overlap(vy, vr) && !(same_view(vy, vr) && yt == rt))
+    rc = fail(PSK_E_ALIAS, "y overlaps the residual and is not the same buffer");
+  if (!rc && z) rc = check_apart({"z", vz}, read, 4);
+  if (!rc && z && views_overlap(vz, vr)) rc = fail(PSK_E_ALIAS, "z overlaps the residual");
+  if (!rc) rc = check_apart({"the workspace", vws}, read, 3);
+  if (!rc && views_overlap(vws, vr)) rc = fail(PSK_E_ALIAS, "the workspace overlaps the residual");
+  if (rc) return rc;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (mx.packed) rc = pack(mx, workspace, nullptr, 0, 0, 0, true, nullptr, s);
+  if (!rc && mw.packed) rc = pack(mw, workspace, nullptr, 0, 0, 0, true, nullptr, s);
+  if (rc) return rc;
+  MMCall C{};
+  C.m = rows, C.n = out, C.k = in ? in : 1, C.matrices = 1, C.kind = MM_LINEAR;
+  C.a = operand(mx, workspace, true);
+  C.b = operand(mw, workspace, layout == PSK_W_OUT_IN);
+  plane_pairs(C);
+  MMEpilogue& E = C.e;
+  E.bias = bias, E.bt = bt, E.act = act;
+  E.res = residual, E.rt = rt, E.ldr = ldr;
+  E.z = z, E.zt = zt, E.ldz = ldz;
+  E.y = y, E.yt = yt, E.ldy = ldy;
+  E.vec_bias = bias && rows_vec8(bias, bt, out, 1), E.vec_res = residual && rows_vec8(residual, rt, ldr, rows);
+  E.vec_z = z && rows_vec8(z, zt, ldz, rows), E.vec_y = rows_vec8(y, yt, ldy, rows);
+  return mm_launch(C, s);
+}
+
+namespace psk {
+
+// The backward's operands and where they stand in the workspace.  dz carries
+// three parts where a product stored in f32 reads it, or where it is f32.
+struct LinearBackward {
+  Matrix x, w, dz;
+  bool want_dx, want_dw, want_db, direct;    // direct: dz is ct as it stands
+  int dx_planes, dw_planes;                  // of dz, in each product
+  int blocks;
+  uint64_t sums, need;
+};
+
+static void plan_backward(LinearBackward& B, const void* ct, int32_t ct_t, int64_t ldc, const void* x, int32_t xt,
+                          int64_t ldx, const void* w, int32_t wt, int64_t ldw, int32_t layout, int64_t rows,
+                          int64_t in, int64_t out, int32_t act, const void* dx, int32_t dxt, const void* dw,
+                          int32_t dwt, const void* db) {
+  B.need = 0;
+  B.want_dx = dx && rows && in, B.want_dw = dw && in && out, B.want_db = db && out;
+  uint64_t none = 0;
+  B.x = matrix(x, xt, rows, in, ldx, B.want_dw ? &B.need : &none);
+  B.w = weight(w, wt, ldw, layout, in, out, B.want_dx ? &B.need : &none);
+  // With an activation dz is rounded: to bf16 where that is the product's own
+  // storage (a rounding beside ct's and the result's), else kept in three parts.
+  const bool act_on = act != PSK_ACT_NONE;
+  const auto planes = [&](int32_t result, int32_t other) {
+    return ct_t == PSK_F32 || (act_on && (result == PSK_F32 || other == PSK_F32)) ? 3 : 1;
+  };
+  B.dx_planes = planes(dxt, wt), B.dw_planes = planes(dwt, xt);
+  B.dz = Matrix{ct, ct_t, rows, out, ldc};
+  B.dz.planes = (B.want_dx && B.dx_planes == 3) || (B.want_dw && B.dw_planes == 3) ? 3 : 1;
+  B.direct = !act_on && ct_t == PSK_BF16 && rows && out && rows_vec8(ct, ct_t, ldc, rows);
+  B.dz.packed = !B.direct;
+  B.dz.prows = rows ? rows : 1, B.dz.pcols = out ? up8(out) : 8;
+  B.dz.offset = B.need;
+  if (!B.direct && (B.want_dx || B.want_dw))
+    B.need += ((uint64_t)B.dz.planes * B.dz.prows * B.dz.pcols * 2 + 255) / 256 * 256;
+  B.blocks = pack_blocks(B.dz.prows, B.dz.pcols);
+  B.sums = B.need;
+  if (B.want_db) B.need += ((uint64_t)B.blocks * out * 4 + 255) / 256 * 256;
+}
+
+static int check_backward(const void* ct, int32_t ct_t, int64_t ldc, const void* x, int32_t xt, int64_t ldx,
+                          const void* w, int32_t wt, int64_t ldw, int32_t layout, int64_t rows, int64_t in,
+                          int64_t out, int32_t act, const void* dx, int32_t dxt, const void* dw, int32_t dwt,
+                          const void* db, int32_t dbt) {
+  int rc = check_side("rows", rows, LINEAR_MAX_SUM);
+  if (!rc) rc = check_side("in", in, LINEAR_MAX_SIDE);
+  if (!rc) rc = check_side("out", out, LINEAR_MAX_SUM);
+  if (!rc) rc = check_layout(layout);
+  if (!rc) rc = check_act(act);
+  if (!rc) rc = check_rows("ct", ct, ct_t, rows, out, ldc);
+  if (!rc && dw) rc = check_rows("x", x, xt, rows, in, ldx);
+  if (!rc && dx)
+    rc = layout == PSK_W_IN_OUT ? check_rows("w", w, wt, in, out, ldw) : check_rows("w", w, wt, out, in, ldw);
+  if (!rc && dx && !dtype_ok(dxt)) rc = fail(PSK_E_DTYPE, "dx dtype %d", dxt);
+  if (!rc && dw && !dtype_ok(dwt)) rc = fail(PSK_E_DTYPE, "dw dtype %d", dwt);
+  if (!rc && db && !dtype_ok(dbt)) rc = fail(PSK_E_DTYPE, "dbias dtype %d", dbt);
+  return rc;
+}
+
+}  // namespace psk
+
+extern "C" int psk_linear_backward_workspace(const void* ct, int32_t ct_t, int64_t ldc, const void* x, int32_t xt,
+                                             int64_t ldx, const void* w, int32_t wt, int64_t ldw, int32_t layout,
+                                             int64_t rows, int64_t in, int64_t out, int32_t act, const void* dx,
+                                             int32_t dxt, const void* dw, int32_t dwt, const void* dbias, int32_t dbt,
+                                             uint64_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(PSK_E_NULL, "bytes is NULL");
+  const int rc = check_backward(ct, ct_t, ldc, x, xt, ldx, w, wt, ldw, layout, rows, in, out, act, dx, dxt, dw, dwt,
+                                dbias, dbt);
+  if (rc) return rc;
+  LinearBackward B{};
+  plan_backward(B, ct, ct_t, ldc, x, xt, ldx, w, wt, ldw, layout, rows, in, out, act, dx, dxt, dw, dwt, dbias);
+  *bytes = B.need;
+  return PSK_OK;
+}
+
+extern "C" int psk_linear_backward(const void* ct, int32_t ct_t, int64_t ldc, const void* x, int32_t xt, int64_t ldx,
+                                   const void* w, int32_t wt, int64_t ldw, int32_t layout, int64_t rows, int64_t in,
+                                   int64_t out, int32_t act, const void* z, int32_t zt, int64_t ldz, void* dx,
+                                   int32_t dxt, int64_t lddx, void* dw, int32_t dwt, int64_t lddw, void* dbias,
+                                   int32_t dbt, int32_t accumulate, void* workspace, uint64_t workspace_bytes,
+                                   void* stream) {
+  clear_error();
+  int rc = check_backward(ct, ct_t, ldc, x, xt, ldx, w, wt, ldw, layout, rows, in, out, act, dx, dxt, dw, dwt, dbias,
+                          dbt);
+  if (!rc && act != PSK_ACT_NONE) rc = check_rows("z", z, zt, rows, out, ldz);
+  if (!rc && dx) rc = check_rows("dx", dx, dxt, rows, in, lddx);
+  const int64_t wrows = layout == PSK_W_IN_OUT ? in : out, wcols = layout == PSK_W_IN_OUT ? out : in;
+  if (!rc && dw) rc = check_rows("dw", dw, dwt, wrows, wcols, lddw);
+  if (!rc && dbias) rc = check_rows("dbias", dbias, dbt, 1, out, out);
+  if (rc) return rc;
+  LinearBackward B{};
+  plan_backward(B, ct, ct_t, ldc, x, xt, ldx, w, wt, ldw, layout, rows, in, out, act, dx, dxt, dw, dwt, dbias);
+  rc = check_workspace(workspace, workspace_bytes, B.need);
+  if (rc) return rc;
+  const View vws{(uintptr_t)workspace, B.need ? 1 : 0, B.need, B.need};
+  const Named read[] = {{"ct", mat_view(ct, ct_t, rows, out, ldc)},
+                        {"z", act != PSK_ACT_NONE ? mat_view(z, zt, rows, out, ldz) : View{0, 0, 0, 0}},
+                        {"x", dw ? mat_view(x, xt, rows, in, ldx) : View{0, 0, 0, 0}},
+                        {"w", dx ? mat_view(w, wt, wrows, wcols, ldw) : View{0, 0, 0, 0}},
+                        {"the workspace", vws}};
+  const Named wrote[] = {{"dx", mat_view(dx, dxt, rows, in, lddx)},
+                         {"dw", mat_view(dw, dwt, wrows, wcols, lddw)},
+                         {"dbias", mat_view(dbias, dbt, 1, out, out)}};
+  for (int i = 0; !rc && i < 3; ++i) {
+    rc = check_apart(wrote[i], read, 5);
+    if (!rc) rc = check_apart(wrote[i], wrote + i + 1, 2 - i);
+  }
+  if (!rc) rc = check_apart({"the workspace", vws}, read, 4);
+  if (rc) return rc;
+  cudaStream_t s = (cudaStream_t)stream;
+  const bool products = B.want_dx || B.want_dw;
+  float* sums = B.want_db ? (float*)((char*)workspace + B.sums) : nullptr;
+  if (B.want_db || (products && !B.direct)) {
+    rc = pack(B.dz, workspace, z, zt, ldz, act, products && !B.direct, sums, s);
+    if (rc) return rc;
+  }
+  if (B.want_db) {
+    linear_bias_kernel<<<(unsigned)((out + 31) / 32), 256, 0, s>>>(sums, B.blocks, out, dbias, dbt, accumulate != 0);
+    rc = check_launch("linear bias kernel");
+    if (rc) return rc;
+  }
+  if (B.want_dx) {
+    if (B.w.packed) rc = pack(B.w, workspace, nullptr, 0, 0, 0, true, nullptr, s);
+    if (rc) return rc;
+    MMCall C{};
+    C.m = rows, C.n = in, C.k = out ? out : 1, C.matrices = 1, C.kind = MM_LINEAR;
+    C.a = operand(B.dz, workspace, true);
+    C.a.planes = B.dx_planes;
+    C.b = operand(B.w, workspace, layout == PSK_W_IN_OUT);
+    plane_pairs(C);
+    C.e.y = dx, C.e.yt = dxt, C.e.ldy = lddx;
+    C.e.vec_y = rows_vec8(dx, dxt, lddx, rows);
+    rc = mm_launch(C, s);
+    if (rc) return rc;
+  }
+  if (B.want_dw) {
+    if (B.x.packed) rc = pack(B.x, workspace, nullptr, 0, 0, 0, true, nullptr, s);
+    if (rc) return rc;
+    MMCall C{};
+    MMOperand ox = operand(B.x, workspace, false), oz = operand(B.dz, workspace, false);
+    oz.planes = B.dw_planes;
+    C.m = wrows, C.n = wcols, C.k = rows ? rows : 1, C.matrices = 1, C.kind = MM_LINEAR;
+    C.a = layout == PSK_W_IN_OUT ? ox : oz;
+    C.b = layout == PSK_W_IN_OUT ? oz : ox;
+    plane_pairs(C);
+    C.e.y = dw, C.e.yt = dwt, C.e.ldy = lddw;
+    C.e.vec_y = rows_vec8(dw, dwt, lddw, wrows);
+    if (accumulate) C.e.res = dw, C.e.rt = dwt, C.e.ldr = lddw, C.e.vec_res = C.e.vec_y;
+    rc = mm_launch(C, s);
+  }
+  return rc;
+}

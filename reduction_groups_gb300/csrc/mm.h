@@ -1,0 +1,62 @@
+// The matrix product behind the linear layer and the orthogonalised update:
+// the host's description of one launch (matmul.cu runs it).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace psk {
+
+// A 16-bit operand in device memory: `outer` rows of `inner` contiguous
+// elements, ld elements apart (16-byte aligned rows), in `planes` parts whose
+// sum is the operand (plane after plane), one set of planes for each of the
+// call's matrices.  k_inner: the contiguous direction is the summed one.
+struct MMOperand {
+  const void* p;
+  int64_t inner, outer, ld, plane_stride;
+  int planes;
+  bool k_inner;
+};
+
+// Where a matrix of the orthogonalised update goes.
+struct MMLeaf {
+  void* y;
+  int64_t ld, vec;
+};
+
+enum MMEpilogueKind { MM_LINEAR = 0, MM_ORTHO = 1 };
+
+// What becomes of the accumulated product p(r, c).
+struct MMEpilogue {
+  // MM_LINEAR: z = p + bias, y = act(z) + residual.  NULL: not there.
+  const void *bias, *res;
+  void *y, *z;
+  int64_t ldr, ldy, ldz;
+  int32_t bt, rt, yt, zt, act;
+  int32_t vec_bias, vec_res, vec_y, vec_z;      // 16-byte accesses allowed
+  // MM_ORTHO: v = alpha p + beta r, r and v matrices of fp16 planes (`ld`,
+  // `plane_stride`, matrix after matrix), or v stored into leaves[matrix] (DEVICE, type yt).
+  float alpha, beta;
+  const uint16_t* from;
+  uint16_t* to;
+  int64_t ld, plane_stride;
+  int32_t planes;
+  const MMLeaf* leaves;
+  int32_t transposed;                           // the leaves hold v's transpose
+};
+
+struct MMCall {
+  int64_t m, n, k;
+  MMOperand a, b;               // a: m x k, b: k x n
+  bool f16;                     // operands fp16, else bf16
+  int pairs;                    // products of planes, in the order they are added
+  uint8_t pa[8], pb[8];
+  int64_t matrices;
+  bool symmetric;               // m == n, the result its own transpose: one triangle is computed
+  MMEpilogueKind kind;
+  MMEpilogue e;
+};
+
+int mm_launch(const MMCall& call, cudaStream_t stream);
+
+}  // namespace psk

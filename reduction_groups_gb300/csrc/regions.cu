@@ -1460,7 +1460,8 @@ extern "C" int psk_test_drop_row(int64_t row) {
   if (cudaMemcpyToSymbol(g_pipe_drop_row, &v, sizeof(v)) != cudaSuccess) return check_launch("test hook write");
   int rc = lanes_set_drop_row(v);
   if (!rc) rc = loss_set_drop_row(v);
-  return rc ? rc : norm_bwd_set_drop_row(v);
+  if (!rc) rc = norm_bwd_set_drop_row(v);
+  return rc ? rc : mm_set_drop_row(v);
 }
 
 namespace psk {
@@ -1500,7 +1501,10 @@ extern "C" int psk_device_status(uint32_t* status, int32_t reset) {
   unsigned int nv = 0;
   const int nrc = norm_bwd_status(&nv, reset != 0);
   if (nrc) return nrc;
-  *status = v | lv | tv | nv;
+  unsigned int mv = 0;
+  const int mrc = mm_status(&mv, reset != 0);
+  if (mrc) return mrc;
+  *status = v | lv | tv | nv | mv;
   return PSK_OK;
 }
 

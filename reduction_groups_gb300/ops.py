@@ -550,3 +550,251 @@ def psk_policy_loss(logits, targets, old_logp, advantage, weight, loss, logp=Non
                                     _vector(loss, "loss", 2, True), _vector(logp, "logp", rows, True),
                                     None if dlogits is None else dlogits.data_ptr(),
                                     0 if dlogits is None else _code(dlogits, "dlogits"), ldg, ws, wb, s))
+
+
+# --------------------------------------------------- a layer's matrices
+
+_ACT = {"none": N.PSK_ACT_NONE, "relu": N.PSK_ACT_RELU, "gelu": N.PSK_ACT_GELU, "silu": N.PSK_ACT_SILU}
+_HEAD_NORM = {"none": N.PSK_HEAD_NORM_NONE, "rms": N.PSK_HEAD_NORM_RMS}
+_PAIRS = {"halves": N.PSK_PAIRS_HALVES, "neighbours": N.PSK_PAIRS_NEIGHBOURS}
+
+
+def _choice(table, v, what: str) -> int:
+    c = table.get(v)
+    if c is None:
+        raise ValueError(f"{what} must be one of {', '.join(table)}, not {v!r}")
+    return c
+
+
+def _weight(w, what: str, shape=None):
+    """(leading dimension, layout) of a weight [in, out] whose rows or columns are contiguous."""
+    if len(w.shape) != 2:
+        raise ValueError(f"{what} must be a 2-D tensor")
+    if shape is not None and w.shape != shape:
+        raise ValueError(f"{what} has shape {tuple(w.shape)}, not {tuple(shape)}")
+    if w.is_contiguous() or w.stride(1) == 1 or w.stride(0) != 1:
+        return _matrix(w, what), N.PSK_W_IN_OUT
+    return _matrix(w.t(), what), N.PSK_W_OUT_IN
+
+
+def _mat(t, what: str, shape):
+    """(address, dtype, leading dimension) of an optional matrix."""
+    if t is None:
+        return None, 0, 0
+    ld = _matrix(t, what, shape)
+    return t.data_ptr(), _code(t, what), ld
+
+
+def psk_linear_workspace(x, w) -> int:
+    """Device workspace bytes psk_linear needs for these operands (0 for bf16
+    tensors with 16-byte aligned rows)."""
+    if _F32 is None:
+        _bind_torch()
+    (rows, cin), cout = x.shape, w.shape[1]
+    ldw, layout = _weight(w, "w", (cin, cout))
+    return _bytes_of(N.lib().psk_linear_workspace, x.data_ptr(), _code(x, "x"), _matrix(x, "x"), w.data_ptr(),
+                     _code(w, "w"), ldw, layout, rows, cin, cout)
+
+
+def _bytes_of(f, *args) -> int:
+    out = ctypes.c_uint64(0)
+    N.check(f(*args, ctypes.byref(out)))
+    return int(out.value)
+
+
+def psk_linear(x, w, y, bias=None, act: str = "none", residual=None, z=None, workspace=None, stream=None) -> None:
+    """y = act(x @ w + bias) + residual.  x: [rows, in]; w: [in, out], its rows
+    or its columns contiguous (an [out, in] weight goes in as weight.t());
+    bias: [out]; residual, y, z: [rows, out].  z, unless None, receives
+    x @ w + bias (what psk_linear_backward reads).  act: "none", "relu", "gelu"
+    or "silu".  y may be the residual.  workspace: a device tensor of at least
+    psk_linear_workspace(x, w) bytes (None where that is 0)."""
+    s = _same_device(stream, x, w, y, bias, residual, z, workspace)
+    (rows, cin), cout = x.shape, w.shape[1]
+    ldw, layout = _weight(w, "w", (cin, cout))
+    shape = (rows, cout)
+    ws, wb = _scratch(workspace)
+    N.check(N.lib().psk_linear(x.data_ptr(), _code(x, "x"), _matrix(x, "x"), w.data_ptr(), _code(w, "w"), ldw, layout,
+                               rows, cin, cout, _vector(bias, "bias", cout), 0 if bias is None else _code(bias, "bias"),
+                               _choice(_ACT, act, "act"), *_mat(residual, "residual", shape), *_mat(z, "z", shape),
+                               *_mat(y, "y", shape), ws, wb, s))
+
+
+def _backward_operands(ct, x, w, dx, dw, dbias):
+    (rows, cin), cout = x.shape, w.shape[1]
+    ldw, layout = _weight(w, "w", (cin, cout))
+    head = (ct.data_ptr(), _code(ct, "ct"), _matrix(ct, "ct", (rows, cout)), x.data_ptr(), _code(x, "x"),
+            _matrix(x, "x"), w.data_ptr(), _code(w, "w"), ldw, layout, rows, cin, cout)
+    return head, layout, (rows, cin, cout)
+
+
+def psk_linear_backward_workspace(ct, x, w, dx=None, dw=None, dbias=None, act: str = "none") -> int:
+    """Device workspace bytes psk_linear_backward needs for these tensors."""
+    if _F32 is None:
+        _bind_torch()
+    head, _, _ = _backward_operands(ct, x, w, dx, dw, dbias)
+    outs = []
+    for t, what in ((dx, "dx"), (dw, "dw"), (dbias, "dbias")):
+        outs += [None, 0] if t is None else [t.data_ptr(), _code(t, what)]
+    return _bytes_of(N.lib().psk_linear_backward_workspace, *head, _choice(_ACT, act, "act"), *outs)
+
+
+def psk_linear_backward(ct, x, w, dx=None, dw=None, dbias=None, act: str = "none", z=None, accumulate: bool = False,
+                        workspace=None, stream=None) -> None:
+    """The backward of psk_linear(x, w, y, bias, act, residual, z) from the
+    cotangent ct of y: dx = dz @ w.T, dw = x.T @ dz (laid out as w), dbias =
+    dz.sum(0), dz = ct * act'(z); each of dx, dw, dbias None: not wanted.  z:
+    what psk_linear stored (act "none" takes none).  accumulate: dw and dbias
+    are added to.  The residual's gradient is ct.  workspace: a device tensor
+    of at least psk_linear_backward_workspace bytes."""
+    s = _same_device(stream, ct, x, w, dx, dw, dbias, z, workspace)
+    head, layout, (rows, cin, cout) = _backward_operands(ct, x, w, dx, dw, dbias)
+    a = _choice(_ACT, act, "act")
+    if a != N.PSK_ACT_NONE and z is None:
+        raise ValueError(f"z is needed for act {act!r}")
+    if dw is None:
+        dw_args = (None, 0, 0)
+    else:
+        lddw, dw_layout = (_matrix(dw, "dw", (cin, cout)), layout) if layout == N.PSK_W_IN_OUT else (
+            _matrix(dw.t(), "dw transposed", (cout, cin)), layout)
+        dw_args = (dw.data_ptr(), _code(dw, "dw"), lddw)
+    ws, wb = _scratch(workspace)
+    N.check(N.lib().psk_linear_backward(*head, a, *_mat(z if a else None, "z", (rows, cout)),
+                                        *_mat(dx, "dx", (rows, cin)), *dw_args, _vector(dbias, "dbias", cout),
+                                        0 if dbias is None else _code(dbias, "dbias"), 1 if accumulate else 0, ws, wb,
+                                        s))
+
+
+def psk_orthogonalize_workspace(n: int, rows: int, cols: int, dtype) -> int:
+    """Device workspace bytes psk_orthogonalize needs for n matrices of this
+    shape with results of this torch dtype."""
+    if _F32 is None:
+        _bind_torch()
+    c = _CODES.get(dtype)
+    if c is None:
+        raise TypeError(f"storage type {dtype} is not f32 or bf16")
+    return _bytes(N.lib().psk_orthogonalize_workspace, n, rows, cols, c)
+
+
+def psk_orthogonalize(xs, ys, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                      scale: float = 1.0, workspace=None, stream=None) -> None:
+    """ys[i] = scale * X after `steps` of X <- a X + b (X X.T) X + c (X X.T)^2 X
+    from X = xs[i] / (norm(xs[i]) + eps): lists of matrices of one shape, each
+    list of one dtype.  coefficients: (a, b, c), or one such triple a step.
+    ys[i] may be any of the xs.  workspace: a device tensor of at least
+    psk_orthogonalize_workspace bytes."""
+    if len(xs) != len(ys):
+        raise ValueError(f"{len(xs)} matrices, {len(ys)} results")
+    flat = [float(v) for t in coefficients for v in (t if hasattr(t, "__len__") else (t,))]
+    if len(flat) == 3:
+        flat = flat * steps
+    if len(flat) != 3 * steps:
+        raise ValueError("coefficients must be one triple, or one a step")
+    if not xs:
+        return
+    s = _same_device(stream, *xs, *ys, workspace)
+    rows, cols = xs[0].shape
+    leaves = (N.psk_ortho_leaf * len(xs))()
+    for f, x, y in zip(leaves, xs, ys):
+        f.ldx, f.ldy = _matrix(x, "x", (rows, cols)), _matrix(y, "y", (rows, cols))
+        f.x, f.y = x.data_ptr(), y.data_ptr()
+        if x.dtype != xs[0].dtype or y.dtype != ys[0].dtype:
+            raise TypeError("the matrices, and the results, must share one storage type each")
+    ws, wb = _scratch(workspace)
+    N.check(N.lib().psk_orthogonalize(leaves, len(xs), rows, cols, _code(xs[0], "x"), _code(ys[0], "y"),
+                                      (ctypes.c_double * len(flat))(*flat), steps, eps, scale, ws, wb, s))
+
+
+def _heads(t, what: str, shape=None):
+    """(tokens, heads, dim, token stride, head stride) of a [tokens, heads, dim] tensor (None: no heads)."""
+    if t is None:
+        return None
+    if len(t.shape) != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{what} must be a [tokens, heads, dim] tensor" + (f" of shape {tuple(shape)}" if shape else ""))
+    ts, hs, es = t.stride()
+    if es != 1 and t.shape[2] > 1:
+        raise ValueError(f"{what}: a head's columns must be contiguous")
+    return t.data_ptr(), ts, hs
+
+
+def _qk(a, b, what: str, shape_a=None, shape_b=None):
+    """The C arguments of a pair of head tensors, either of them None."""
+    ha, hb = _heads(a, what + " of q", shape_a), _heads(b, what + " of k", shape_b)
+    if a is not None and b is not None and a.dtype != b.dtype:
+        raise TypeError(f"{what}: q's and k's must share one storage type")
+    t = a if a is not None else b
+    pa, ta, sa = ha or (None, 0, 0)
+    pb, tb, sb = hb or (None, 0, 0)
+    return pa, pb, 0 if t is None else _code(t, what), ta, sa, tb, sb
+
+
+def _rotary_rest(q, k, positions, freqs, gamma_q, gamma_k, norm, eps, pairs):
+    t = q if q is not None else k
+    if t is None:
+        raise ValueError("q and k are both None")
+    if len(t.shape) != 3:
+        raise ValueError("q and k must be [tokens, heads, dim] tensors")
+    tokens, _, dim = t.shape
+    if q is not None and k is not None and (len(k.shape) != 3 or k.shape[0] != tokens or k.shape[2] != dim):
+        raise ValueError("q and k must have the same tokens and head size")
+    if gamma_q is not None and gamma_k is not None and gamma_q.dtype != gamma_k.dtype:
+        raise TypeError("gamma_q and gamma_k must share one storage type")
+    g = gamma_q if gamma_q is not None else gamma_k
+    hq, hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    nf = freqs.numel()
+    return (tokens, hq, hk, dim, 2 * nf, _vector(positions, "positions", tokens), _id_code(positions, "positions"),
+            _vector(freqs, "freqs", nf, True), _choice(_PAIRS, pairs, "pairs"), _choice(_HEAD_NORM, norm, "norm"), eps,
+            _vector(gamma_q, "gamma_q", dim), _vector(gamma_k, "gamma_k", dim), 0 if g is None else _code(g, "gamma"))
+
+
+def _shape(t):
+    return None if t is None else t.shape
+
+
+def psk_qk_norm_rotary(q, k, yq, yk, positions, freqs, gamma_q=None, gamma_k=None, norm: str = "rms",
+                       eps: float = 1e-6, pairs: str = "halves", stream=None) -> None:
+    """yq, yk = the heads of q and k, [tokens, heads, dim] (views into the qkv
+    product's rows, for instance), each normalised (norm "rms", with its scale;
+    "none") and turned by its token's position in the same pass.  positions:
+    [tokens], int32 or int64; freqs: f32, radians a position for each of the
+    turning pairs (2 * len(freqs) <= dim columns turn); pairs: "halves" (column
+    j with j + len(freqs)) or "neighbours" (2 j with 2 j + 1).  q and yq, or k
+    and yk, may be None, and each result may be its input in place."""
+    s = _same_device(stream, positions, q, k, yq, yk, freqs, gamma_q, gamma_k)
+    if (q is None) != (yq is None) or (k is None) != (yk is None):
+        raise ValueError("q and yq, k and yk go together")
+    rest = _rotary_rest(q, k, positions, freqs, gamma_q, gamma_k, norm, eps, pairs)
+    N.check(N.lib().psk_qk_norm_rotary(*_qk(q, k, "x"), *_qk(yq, yk, "y", _shape(q), _shape(k)), *rest, s))
+
+
+def psk_qk_norm_rotary_backward_workspace(tokens: int, hq: int, hk: int, dim: int) -> int:
+    """Device workspace bytes psk_qk_norm_rotary_backward needs (none without
+    a scale's gradient)."""
+    return _bytes(N.lib().psk_qk_norm_rotary_backward_workspace, tokens, hq, hk, dim)
+
+
+def psk_qk_norm_rotary_backward(cq, ck, q, k, dq, dk, positions, freqs, gamma_q=None, gamma_k=None, dgamma_q=None,
+                                dgamma_k=None, norm: str = "rms", eps: float = 1e-6, pairs: str = "halves",
+                                workspace=None, stream=None) -> None:
+    """The backward of psk_qk_norm_rotary: dq, dk from the cotangents cq, ck of
+    yq, yk, and the scales' gradients (None: not wanted).  q and k are read for
+    norm "rms" alone.  dq may be cq or q in place, dk ck or k.  workspace: a
+    device tensor of at least psk_qk_norm_rotary_backward_workspace bytes where
+    a scale's gradient is wanted."""
+    s = _same_device(stream, positions, cq, ck, q, k, dq, dk, freqs, gamma_q, gamma_k, dgamma_q, dgamma_k, workspace)
+    if (cq is None) != (dq is None) or (ck is None) != (dk is None):
+        raise ValueError("cq and dq, ck and dk go together")
+    if norm == "rms" and ((q is None) != (cq is None) or (k is None) != (ck is None)):
+        raise ValueError("cq and q, ck and k go together")
+    if dgamma_q is not None and dgamma_k is not None and dgamma_q.dtype != dgamma_k.dtype:
+        raise TypeError("dgamma_q and dgamma_k must share one storage type")
+    rest = _rotary_rest(cq, ck, positions, freqs, gamma_q, gamma_k, norm, eps, pairs)
+    dim = rest[3]
+    if norm == "none":
+        q = k = None
+    g = dgamma_q if dgamma_q is not None else dgamma_k
+    ws, wb = _scratch(workspace)
+    N.check(N.lib().psk_qk_norm_rotary_backward(
+        *_qk(cq, ck, "ct"), *_qk(q, k, "x", _shape(cq), _shape(ck)), *_qk(dq, dk, "dx", _shape(cq), _shape(ck)), *rest,
+        _vector(dgamma_q, "dgamma_q", dim), _vector(dgamma_k, "dgamma_k", dim), 0 if g is None else _code(g, "dgamma"),
+        ws, wb, s))
