@@ -20,97 +20,96 @@ constexpr int64_t LINEAR_MAX_SUM = 1LL << 25;      // of a product: a tile's tim
 constexpr int64_t LINEAR_MAX_SIDE = (1LL << 31) - 1024;
 constexpr int PACK_THREADS = 256;
 
-// x as the sum of three bf16 parts; an infinity or a NaN is the first part alone.
-__device__ __forceinline__ void split3(float x, uint32_t& h, uint32_t& m, uint32_t& l) {
-  uint32_t b = f32_to_bf16_bits(x);
-  const bool finite = fabsf(x) <= 3.4028234663852886e38f;
-  if (finite && (b & 0x7FFF) == 0x7F80) b -= 1;              // rounded up to infinity: the largest bf16 instead
-  const float r = finite ? x - bf16_bits_to_f32(b) : 0.0f;
-  h = b;
-  m = f32_to_bf16_bits(r);
-  l = f32_to_bf16_bits(r - bf16_bits_to_f32(m));
-}
-
-__device__ __forceinline__ uint4 pack8(const uint32_t* h) {
-  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-}
-
 struct PackParams {
   const void *x, *z;            // z: the value is x slope(z)
   uint16_t* to;                 // planes of prows x pcols (NULL: column sums alone)
   float* sums;                  // column sums of `blocks` blocks of rows (NULL: not wanted)
   int64_t rows, cols, ldx, ldz, prows, pcols, plane_stride;
-  int32_t xt, zt, act, planes, vec_x, vec_z, blocks;
+  int32_t planes, blocks;
 };
 
-// Eight columns a thread, 256 a CTA, its warps the rows of a block in turn.
-__global__ void __launch_bounds__(PACK_THREADS) linear_pack_kernel(const __grid_constant__ PackParams P) {
-  __shared__ float part[8][256 + 8];
+// Eight columns a thread, 256 a CTA, its warps the rows of a block in turn,
+// two rows on their way at once.  VEC: 16-byte accesses, the columns
+// neighbours; else every 32nd, so that lanes read neighbours.
+template <int XT, int ZT, int ACT, bool VEC>
+__global__ void __launch_bounds__(PACK_THREADS, 3) linear_pack_kernel(const __grid_constant__ PackParams P) {
+  __shared__ float part[8][256];
+  constexpr int R = 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t groups = (P.pcols + 255) / 256;
   const int64_t cb = blockIdx.x % groups, rb = blockIdx.x / groups;
-  const int64_t c = cb * 256 + lane * 8;
+  // The span that is written, padding among it, and the part of it that is read.
+  const Columns<VEC, 8> wide(cb * 256, 32, lane, P.pcols), cols(cb * 256, 32, lane, P.cols);
   const int64_t each = (P.prows + P.blocks - 1) / P.blocks;
   const int64_t end = (rb + 1) * each < P.prows ? (rb + 1) * each : P.prows;
-  const int64_t left = P.cols - c;
-  const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
   float s[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) s[k] = 0.0f;
-  if (c < P.pcols)
-    for (int64_t r = rb * each + warp; r < end; r += 8) {
-      float v[8], z[8];
-      const int have = r < P.rows ? n : 0;
-      if (P.xt == PSK_BF16) {
-        if (P.vec_x) load8<PSK_BF16, true>(P.x, r * P.ldx + c, have, v);
-        else load8<PSK_BF16, false>(P.x, r * P.ldx + c, have, v);
+  for (int64_t r0 = rb * each + warp; r0 < end; r0 += 8 * R) {
+    Piece<XT, VEC, 8> x[R];
+    Piece<ZT, VEC, 8> z[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t r = r0 + 8 * j;
+      const bool there = r < end && r < P.rows;
+      if (there) {
+        cols.template load<XT>(P.x, r * P.ldx, x[j]);
       } else {
-        if (P.vec_x) load8<PSK_F32, true>(P.x, r * P.ldx + c, have, v);
-        else load8<PSK_F32, false>(P.x, r * P.ldx + c, have, v);
+#pragma unroll
+        for (int i = 0; i < Piece<XT, VEC, 8>::W; ++i) x[j].w[i] = 0;
       }
-      if (P.act) {
-        if (P.zt == PSK_BF16) {
-          if (P.vec_z) load8<PSK_BF16, true>(P.z, r * P.ldz + c, have, z);
-          else load8<PSK_BF16, false>(P.z, r * P.ldz + c, have, z);
-        } else {
-          if (P.vec_z) load8<PSK_F32, true>(P.z, r * P.ldz + c, have, z);
-          else load8<PSK_F32, false>(P.z, r * P.ldz + c, have, z);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float g = P.act == ACT_RELU   ? act_slope<ACT_RELU>(z[k])
-                          : P.act == ACT_GELU ? act_slope<ACT_GELU>(z[k])
-                                              : act_slope<ACT_SILU>(z[k]);
-          v[k] *= g;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s[k] += v[k];
-      if (P.to) {
-        uint32_t h[8], m[8], l[8];
-        uint16_t* q = P.to + r * P.pcols + c;
-        if (P.planes == 1) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) h[k] = f32_to_bf16_bits(v[k]);
-          *(uint4*)q = pack8(h);
+      if constexpr (ACT != ACT_NONE) {
+        if (there) {
+          cols.template load<ZT>(P.z, r * P.ldz, z[j]);
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) split3(v[k], h[k], m[k], l[k]);
-          *(uint4*)q = pack8(h);
-          *(uint4*)(q + P.plane_stride) = pack8(m);
-          *(uint4*)(q + 2 * P.plane_stride) = pack8(l);
+          for (int i = 0; i < Piece<ZT, VEC, 8>::W; ++i) z[j].w[i] = 0;
         }
       }
     }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t r = r0 + 8 * j;
+      if (r >= end) break;
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        float2 t = make_float2(x[j].get(k), x[j].get(k + 1));
+        if constexpr (ACT != ACT_NONE) t = __fmul2_rn(t, act_slope<ACT>(make_float2(z[j].get(k), z[j].get(k + 1))));
+        v[k] = t.x, v[k + 1] = t.y;
+        s[k] += t.x, s[k + 1] += t.y;
+      }
+      if (!P.to) continue;
+      if (P.planes == 1) {
+        wide.template store<PSK_BF16>(P.to, r * P.pcols, v);
+      } else {
+        // each part is what bf16 leaves of the value; an infinity or a NaN is the first part alone
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          float h[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t b = f32_to_bf16_bits(v[k]);
+            const bool finite = fabsf(v[k]) <= 3.4028234663852886e38f;
+            if (finite && (b & 0x7FFF) == 0x7F80) b -= 1;      // rounded up to infinity: the largest bf16 instead
+            h[k] = bf16_bits_to_f32(b);
+            v[k] = finite ? v[k] - h[k] : 0.0f;
+          }
+          wide.template store<PSK_BF16>(P.to + p * P.plane_stride, r * P.pcols, h);
+        }
+      }
+    }
+  }
   if (!P.sums) return;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) part[warp][k * 33 + lane] = s[k];
+  for (int k = 0; k < 8; ++k) part[warp][k * 32 + lane] = s[k];
   __syncthreads();
-  const int col = threadIdx.x;
-  float t = 0.0f;
+  const int t = threadIdx.x;
+  float sum = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) t += part[w][(col & 7) * 33 + (col >> 3)];
-  if (cb * 256 + col < P.cols) P.sums[rb * P.cols + cb * 256 + col] = t;
+  for (int w = 0; w < 8; ++w) sum += part[w][t];
+  const int64_t c = cb * 256 + (VEC ? (t & 31) * 8 + (t >> 5) : t);
+  if (c < P.cols) P.sums[rb * P.cols + c] = sum;
 }
 
 // dbias from the row blocks' sums: 32 columns a CTA, 8 warps the blocks in turn.
@@ -175,10 +174,10 @@ static MMOperand operand(const Matrix& m, void* workspace, bool k_inner) {
   return o;
 }
 
-// Blocks of rows of the pack kernel: enough CTAs for eight an SM, 32 rows each at least.
+// Blocks of rows of the pack kernel: six CTAs an SM (twice what it holds), 32 rows each at least.
 static int pack_blocks(int64_t rows, int64_t cols) {
   const int64_t groups = (cols + 255) / 256;
-  int64_t b = (NOMINAL_SMS * 8 + groups - 1) / groups;
+  int64_t b = NOMINAL_SMS * 6 / groups;
   if (b > (rows + 31) / 32) b = (rows + 31) / 32;
   return (int)(b < 1 ? 1 : b);
 }
@@ -191,12 +190,26 @@ static int pack(const Matrix& m, void* workspace, const void* z, int32_t zt, int
   P.sums = sums;
   P.rows = m.rows, P.cols = m.cols, P.ldx = m.ld, P.ldz = ldz;
   P.prows = m.prows, P.pcols = m.pcols, P.plane_stride = m.prows * m.pcols;
-  P.xt = m.dt, P.zt = zt, P.act = act, P.planes = m.planes;
-  P.vec_x = rows_vec8(m.p, m.dt, m.ld, m.rows), P.vec_z = act && rows_vec8(z, zt, ldz, m.rows);
+  P.planes = m.planes;
+  const bool vec = m.cols % 8 == 0 && rows_vec8(m.p, m.dt, m.ld, m.rows) && (!act || rows_vec8(z, zt, ldz, m.rows));
   P.blocks = pack_blocks(m.prows, m.pcols);
   const int64_t ctas = (m.pcols + 255) / 256 * P.blocks;
   if (ctas > 0x7FFFFFFF) return fail(PSK_E_SHAPE, "too many blocks");
-  linear_pack_kernel<<<(unsigned)ctas, PACK_THREADS, 0, s>>>(P);
+  const unsigned grid = (unsigned)ctas;
+  with_dtype(m.dt, [&](auto XT) {
+    return with_bool(vec, [&](auto VEC) {
+      if (act == ACT_NONE) {
+        linear_pack_kernel<XT.value, PSK_BF16, ACT_NONE, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
+        return 0;
+      }
+      return with_dtype(zt, [&](auto ZT) {
+        if (act == ACT_RELU) linear_pack_kernel<XT.value, ZT.value, ACT_RELU, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
+        else if (act == ACT_GELU) linear_pack_kernel<XT.value, ZT.value, ACT_GELU, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
+        else linear_pack_kernel<XT.value, ZT.value, ACT_SILU, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
+        return 0;
+      });
+    });
+  });
   return check_launch("linear pack kernel");
 }
 
@@ -327,7 +340,7 @@ extern "C" int psk_linear(const void* x, int32_t xt, int64_t ldx, const void* w,
   if (!rc && mw.packed) rc = pack(mw, workspace, nullptr, 0, 0, 0, true, nullptr, s);
   if (rc) return rc;
   MMCall C{};
-  C.m = rows, C.n = out, C.k = in ? in : 1, C.matrices = 1, C.kind = MM_LINEAR;
+  C.m = rows, C.n = out, C.k = in ? in : 1, C.matrices = 1;
   C.a = operand(mx, workspace, true);
   C.b = operand(mw, workspace, layout == PSK_W_OUT_IN);
   plane_pairs(C);
@@ -336,8 +349,6 @@ extern "C" int psk_linear(const void* x, int32_t xt, int64_t ldx, const void* w,
   E.res = residual, E.rt = rt, E.ldr = ldr;
   E.z = z, E.zt = zt, E.ldz = ldz;
   E.y = y, E.yt = yt, E.ldy = ldy;
-  E.vec_bias = bias && rows_vec8(bias, bt, out, 1), E.vec_res = residual && rows_vec8(residual, rt, ldr, rows);
-  E.vec_z = z && rows_vec8(z, zt, ldz, rows), E.vec_y = rows_vec8(y, yt, ldy, rows);
   return mm_launch(C, s);
 }
 
@@ -469,13 +480,12 @@ extern "C" int psk_linear_backward(const void* ct, int32_t ct_t, int64_t ldc, co
     if (B.w.packed) rc = pack(B.w, workspace, nullptr, 0, 0, 0, true, nullptr, s);
     if (rc) return rc;
     MMCall C{};
-    C.m = rows, C.n = in, C.k = out ? out : 1, C.matrices = 1, C.kind = MM_LINEAR;
+    C.m = rows, C.n = in, C.k = out ? out : 1, C.matrices = 1;
     C.a = operand(B.dz, workspace, true);
     C.a.planes = B.dx_planes;
     C.b = operand(B.w, workspace, layout == PSK_W_IN_OUT);
     plane_pairs(C);
     C.e.y = dx, C.e.yt = dxt, C.e.ldy = lddx;
-    C.e.vec_y = rows_vec8(dx, dxt, lddx, rows);
     rc = mm_launch(C, s);
     if (rc) return rc;
   }
@@ -485,13 +495,12 @@ extern "C" int psk_linear_backward(const void* ct, int32_t ct_t, int64_t ldc, co
     MMCall C{};
     MMOperand ox = operand(B.x, workspace, false), oz = operand(B.dz, workspace, false);
     oz.planes = B.dw_planes;
-    C.m = wrows, C.n = wcols, C.k = rows ? rows : 1, C.matrices = 1, C.kind = MM_LINEAR;
+    C.m = wrows, C.n = wcols, C.k = rows ? rows : 1, C.matrices = 1;
     C.a = layout == PSK_W_IN_OUT ? ox : oz;
     C.b = layout == PSK_W_IN_OUT ? oz : ox;
     plane_pairs(C);
     C.e.y = dw, C.e.yt = dwt, C.e.ldy = lddw;
-    C.e.vec_y = rows_vec8(dw, dwt, lddw, wrows);
-    if (accumulate) C.e.res = dw, C.e.rt = dwt, C.e.ldr = lddw, C.e.vec_res = C.e.vec_y;
+    if (accumulate) C.e.res = dw, C.e.rt = dwt, C.e.ldr = lddw;
     rc = mm_launch(C, s);
   }
   return rc;

@@ -5,7 +5,7 @@
 // One persistent CTA (or pair of CTAs, CG = 2) an SM takes output tiles in
 // turn.  Warp 0 fills a ring of shared-memory stages by TMA (64 summed
 // elements of both operands, 128-byte swizzled), warp 1 issues tcgen05.mma
-// from one thread into one of two accumulators in TMEM, warps 4 to 11 take
+// from one thread into one of two accumulators in TMEM, the warps from 4 on take
 // finished accumulators out of TMEM and run the epilogue on them while the
 // next tile's products are running.  A pair shares one tile of 256 rows: each
 // CTA brings half of A's rows and half of B's columns, the first issues the
@@ -16,8 +16,9 @@
 // instruction descriptor say which, so no operand is transposed in memory.
 //
 // f32 operands come as planes of 16-bit parts; the launch lists the products
-// of planes to be added, the smallest first, and each is a pass over the
-// summed axis into the same accumulator.
+// of planes to be added, the smallest first: a stage holds every plane of its
+// part of the summed axis, each product of planes goes into the same
+// accumulator.
 //
 // Every wait is bounded: a role that gives up records it in the device status
 // and leaves its loop, all meet at the end of the kernel.
@@ -32,8 +33,11 @@
 
 namespace psk {
 
-constexpr int MM_THREADS = 384;
-constexpr int MM_EPI_WARPS = 8;
+// Warps of the epilogue: sixteen, or eight where each keeps its sums in registers.
+template <bool SUM>
+struct MMWarps {
+  static constexpr int EPI = SUM ? 8 : 16, THREADS = 128 + 32 * EPI;
+};
 constexpr int MM_BK = 64;                  // summed elements a stage: one 128-byte swizzled row
 constexpr int MM_A_BYTES = 128 * MM_BK * 2;
 
@@ -46,6 +50,7 @@ struct MMParams {
   int32_t a_k, b_k, f16;
   int32_t tiles_m, tiles_n, tiles, symmetric;
   int32_t chunk;                           // blocks of the summed axis that one accumulator takes
+  int32_t na, nb, stages;                  // planes of A and B in a stage (one each but with SUM), stages of the ring
   uint8_t pa[8], pb[8];
 };
 
@@ -133,20 +138,17 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lbo) {
          (1ull << 46) | (2ull << 61);
 }
 
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
-  uint32_t r[32];
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float* v) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -198,16 +200,6 @@ __device__ __forceinline__ Tile tile_at(const MMParams& P, int32_t t) {
 
 // ----------------------------------------------------------------- epilogue
 
-__device__ __forceinline__ void load8_rt(const void* p, int32_t dt, int64_t i, int n, bool vec, float* v) {
-  if (dt == PSK_BF16) {
-    if (vec) load8<PSK_BF16, true>(p, i, n, v);
-    else load8<PSK_BF16, false>(p, i, n, v);
-  } else {
-    if (vec) load8<PSK_F32, true>(p, i, n, v);
-    else load8<PSK_F32, false>(p, i, n, v);
-  }
-}
-
 __device__ __forceinline__ void store8_rt(void* p, int32_t dt, int64_t i, int n, bool vec, const float* v) {
   if (dt == PSK_BF16) {
     uint16_t* q = (uint16_t*)p + i;
@@ -237,34 +229,117 @@ __device__ __forceinline__ void store1_rt(void* p, int32_t dt, int64_t i, float 
   else ((float*)p)[i] = v;
 }
 
-__device__ __forceinline__ float act_rt(float z, int32_t act) {
-  switch (act) {
-    case ACT_RELU: return act_value<ACT_RELU>(z);
-    case ACT_GELU: return act_value<ACT_GELU>(z);
-    case ACT_SILU: return act_value<ACT_SILU>(z);
-    default: return z;
+// Sixteen bf16 of a 32-byte aligned row: one sector an access, so that lanes
+// on different rows fetch and write whole sectors.
+__device__ __forceinline__ void load16_bf16(const void* p, int64_t i, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"((const uint16_t*)p + i));
+}
+__device__ __forceinline__ void store16(void* p, int64_t i, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"((uint16_t*)p + i), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void store16_bf16(void* p, int64_t i, const float* v) {
+  uint32_t w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = f32x2_to_bf16x2(v[2 * k], v[2 * k + 1]);
+  store16(p, i, w);
+}
+
+template <int ACT, bool FINE, int N>
+__device__ __forceinline__ void act_all(float* v) {
+  if constexpr (ACT != ACT_NONE) {
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+      const float2 a = act_value<ACT, FINE>(make_float2(v[k], v[k + 1]));
+      v[k] = a.x, v[k + 1] = a.y;
+    }
   }
 }
 
-// Eight neighbouring columns of one row.
-__device__ __forceinline__ void linear_row8(const MMEpilogue& E, int64_t r, int64_t c, int n, float* v) {
-  float t[8];
-  if (E.bias) {
-    load8_rt(E.bias, E.bt, c, n, E.vec_bias, t);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += t[k];
+__device__ __forceinline__ float load1_rt(const void* p, int32_t dt, int64_t i) {
+  return dt == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)p)[i]) : ((const float*)p)[i];
+}
+
+template <int N>
+__device__ __forceinline__ void act_rt(float* v, int32_t act) {
+  switch (act) {
+    case ACT_RELU: act_all<ACT_RELU, true, N>(v); break;
+    case ACT_GELU: act_all<ACT_GELU, true, N>(v); break;
+    case ACT_SILU: act_all<ACT_SILU, true, N>(v); break;
+    default: break;
   }
-  if (E.z) store8_rt(E.z, E.zt, r * E.ldz + c, n, E.vec_z, v);
-  if (E.act) {
+}
+
+// Sixteen columns of a warp's 32 rows, of any types and strides: turned
+// through shared memory, so that lanes hold neighbouring columns (two rows at
+// a time) and what they load and store is coalesced wherever rows begin.  Kept
+// short and rolled up: a small call runs it once, and code that is not in the
+// instruction cache costs more than it computes (unrolled throughout, a tile
+// of [1003, 771] x [771, 1501] f32 spent 10 us in here, of 27).
+__device__ __forceinline__ void linear_any16(const MMParams& P, int64_t row0, int64_t c0, int lane, float* stage,
+                                             const float* v) {
+  const MMEpilogue& E = P.e;
+  __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = act_rt(v[k], E.act);
-  }
-  if (E.res) {
-    load8_rt(E.res, E.rt, r * E.ldr + c, n, E.vec_res, t);
+  for (int k = 0; k < 16; ++k) stage[lane * 17 + k] = v[k];
+  __syncwarp();
+  const int64_t c = c0 + (lane & 15);
+  if (c >= P.n) return;
+  const float bias = E.bias ? load1_rt(E.bias, E.bt, c) : 0.0f;
+#pragma unroll 1
+  for (int i = lane >> 4; i < 32; i += 16) {           // eight rows: i, i + 2, ...
+    const int64_t r = row0 + i;
+    const int n = P.m - r >= 16 ? 8 : P.m > r ? (int)((P.m - r + 1) / 2) : 0;
+    float t[8], res[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += t[k];
+    for (int k = 0; k < 8; ++k) {
+      t[k] = stage[(i + 2 * k) * 17 + (lane & 15)] + bias;
+      res[k] = E.res && k < n ? load1_rt(E.res, E.rt, (r + 2 * k) * E.ldr + c) : 0.0f;
+    }
+    if (E.z) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < n) store1_rt(E.z, E.zt, (r + 2 * k) * E.ldz + c, t[k]);
+    }
+    act_rt<8>(t, E.act);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) store1_rt(E.y, E.yt, (r + 2 * k) * E.ldy + c, E.res ? t[k] + res[k] : t[k]);
   }
-  store8_rt(E.y, E.yt, r * E.ldy + c, n, E.vec_y, v);
+}
+
+// What the epilogue of 16 columns reads from memory, fetched while the
+// columns before them are worked on: the residual and the bias (both bf16,
+// on 32-byte boundaries), or the two parts of the update's own term.
+struct Fetched {
+  uint32_t a[8], b[8];
+};
+
+__device__ __forceinline__ void unpack16(const uint32_t (&w)[8], float* t) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) t[2 * k] = __uint_as_float(w[k] << 16), t[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void add16(const uint32_t (&w)[8], float* v) {
+  float t[16];
+  unpack16(w, t);
+#pragma unroll
+  for (int k = 0; k < 16; k += 2) {
+    const float2 s = __fadd2_rn(make_float2(v[k], v[k + 1]), make_float2(t[k], t[k + 1]));
+    v[k] = s.x, v[k + 1] = s.y;
+  }
+}
+
+// Sixteen columns of one row, every matrix in bf16 with 32-byte aligned rows.
+template <int ACT>
+__device__ __forceinline__ void linear_row16(const MMEpilogue& E, int64_t r, int64_t c, const Fetched& F, float* v) {
+  if (E.bias) add16(F.b, v);
+  if (E.z) store16_bf16(E.z, r * E.ldz + c, v);
+  act_all<ACT, false, 16>(v);
+  if (E.res) add16(F.a, v);
+  store16_bf16(E.y, r * E.ldy + c, v);
 }
 
 __device__ __forceinline__ float f16_to_f32(uint32_t h) {
@@ -272,91 +347,113 @@ __device__ __forceinline__ float f16_to_f32(uint32_t h) {
   asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"((uint16_t)h));
   return f;
 }
-__device__ __forceinline__ uint32_t f32_to_f16(float f) {
-  uint16_t h;
-  asm("cvt.rn.f16.f32 %0, %1;" : "=h"(h) : "f"(f));
-  return h;
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t w) {
+  return make_float2(f16_to_f32(w & 0xFFFF), f16_to_f32(w >> 16));
+}
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
-// Eight columns of one row of an fp16 matrix in planes: v = alpha v + beta from.
-__device__ __forceinline__ void ortho_mix8(const MMEpilogue& E, const uint16_t* from, float* v) {
+// Sixteen columns of one row of the orthogonalised update: v = alpha v + beta
+// from, stored in fp16 planes (and mirrored) or into a leaf.  The planes' rows
+// are padded to 32 bytes; their padding may be written.
+__device__ __forceinline__ void ortho_row16(const MMParams& P, int32_t matrix, int64_t r, int64_t c, bool mirrored,
+                                            const Fetched& F, float* v) {
+  const MMEpilogue& E = P.e;
+  const int64_t at = (int64_t)matrix * E.planes * E.plane_stride;
+  const int64_t left = P.n - c;
+  const float2 alpha = pair_of(E.alpha), beta = pair_of(E.beta);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] *= E.alpha;
-  if (!from) return;
-  for (int p = E.planes - 1; p >= 0; --p) {
-    const uint4 u = *(const uint4*)(from + p * E.plane_stride);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = fmaf(E.beta, f16_to_f32(w[k] & 0xFFFF), v[2 * k]);
-      v[2 * k + 1] = fmaf(E.beta, f16_to_f32(w[k] >> 16), v[2 * k + 1]);
+  for (int k = 0; k < 8; ++k) {
+    float2 x = __fmul2_rn(make_float2(v[2 * k], v[2 * k + 1]), alpha);
+    if (E.from) {
+      if (E.planes == 2) x = __ffma2_rn(beta, f16x2_to_f32(F.b[k]), x);
+      x = __ffma2_rn(beta, f16x2_to_f32(F.a[k]), x);
     }
+    v[2 * k] = x.x, v[2 * k + 1] = x.y;
+  }
+  if (E.to) {
+    for (int p = 0; p < E.planes; ++p) {
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        w[k] = f32x2_to_f16x2(v[2 * k], v[2 * k + 1]);
+        const float2 h = f16x2_to_f32(w[k]);
+        v[2 * k] -= h.x, v[2 * k + 1] -= h.y;
+      }
+      uint16_t* to = E.to + at + p * E.plane_stride;
+      store16(to, r * E.ld + c, w);
+      if (mirrored) {
+        uint16_t* o = to + c * E.ld + r;
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (k < left) o[(int64_t)k * E.ld] = (uint16_t)(k & 1 ? w[k >> 1] >> 16 : w[k >> 1]);
+      }
+    }
+    return;
+  }
+  const MMLeaf L = E.leaves[matrix];
+  if (E.transposed) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (k < left) store1_rt(L.y, E.yt, (c + k) * L.ld + r, v[k]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 16; h += 8)
+      if (h < left) store8_rt(L.y, E.yt, r * L.ld + c + h, left - h < 8 ? (int)(left - h) : 8, L.vec != 0, v + h);
   }
 }
 
-// The epilogue of 32 neighbouring accumulators of row r, from column col on.
 template <int KIND>
-__device__ __forceinline__ void finish32(const MMParams& P, int32_t matrix, int64_t r, int64_t col, bool mirrored,
-                                         float* v) {
+__device__ __forceinline__ void fetch16(const MMParams& P, int32_t matrix, int64_t r, int64_t c, Fetched& F) {
   const MMEpilogue& E = P.e;
-  if (r >= P.m) return;
-  const int64_t at = (int64_t)matrix * E.planes * E.plane_stride;
-#pragma unroll
-  for (int g = 0; g < 32; g += 8) {
-    const int64_t left = P.n - (col + g);
-    if (left <= 0) break;
-    const int have = left < 8 ? (int)left : 8;
-    if constexpr (KIND == MM_LINEAR) {
-      linear_row8(E, r, col + g, have, v + g);
-    } else {
-      ortho_mix8(E, E.from ? E.from + at + r * E.ld + col + g : nullptr, v + g);
-      if (E.to) {
-        uint16_t* q = E.to + at + r * E.ld + col + g;
-        for (int p = 0; p < E.planes; ++p) {
-          uint32_t h[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            h[k] = f32_to_f16(v[g + k]);
-            v[g + k] -= f16_to_f32(h[k]);
-          }
-          *(uint4*)(q + p * E.plane_stride) = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
-                                                         h[6] | h[7] << 16);
-          if (mirrored) {
-            uint16_t* o = E.to + at + p * E.plane_stride + (col + g) * E.ld + r;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k < have) o[(int64_t)k * E.ld] = (uint16_t)h[k];
-          }
-        }
-      } else {
-        const MMLeaf L = E.leaves[matrix];
-        if (E.transposed) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < have) store1_rt(L.y, E.yt, (col + g + k) * L.ld + r, v[g + k]);
-        } else {
-          store8_rt(L.y, E.yt, r * L.ld + col + g, have, L.vec != 0, v + g);
-        }
-      }
-    }
+  if (KIND == MM_ANY || r >= P.m || c >= P.n) return;
+  if constexpr (KIND == MM_ORTHO) {
+    if (!E.from) return;
+    const uint16_t* from = E.from + (int64_t)matrix * E.planes * E.plane_stride + r * E.ld + c;
+    load16_bf16(from, 0, F.a);
+    if (E.planes == 2) load16_bf16(from, E.plane_stride, F.b);
+  } else {
+    if (E.res) load16_bf16(E.res, r * E.ldr + c, F.a);
+    if (E.bias) load16_bf16(E.bias, c, F.b);
+  }
+}
+
+// The epilogue of 16 neighbouring accumulators, from column c on, of row0 + lane.
+template <int KIND>
+__device__ __forceinline__ void finish16(const MMParams& P, int32_t matrix, int64_t row0, int lane, int64_t c,
+                                         bool mirrored, const Fetched& F, float* stage, float* v) {
+  if (c >= P.n) return;
+  if constexpr (KIND == MM_ANY) {
+    linear_any16(P, row0, c, lane, stage, v);
+  } else if (row0 + lane < P.m) {
+    if constexpr (KIND == MM_ORTHO) ortho_row16(P, matrix, row0 + lane, c, mirrored, F, v);
+    else linear_row16<KIND>(P.e, row0 + lane, c, F, v);
   }
 }
 
 // ------------------------------------------------------------------- kernel
 
-template <int CG, int BN>
+// KIND: an activation with every matrix in bf16, 32-byte aligned rows and n a
+// multiple of 16; MM_ANY: the linear layer with any types; MM_ORTHO.
+template <int CG, int BN, int KIND, bool SUM>
 struct MMShape {
   static constexpr int BM = 128 * CG;
   static constexpr int B_ROWS = BN / CG;                        // of B's tile in one CTA
-  static constexpr int STAGE = MM_A_BYTES + B_ROWS * MM_BK * 2;
-  static constexpr int STAGES = (200 * 1024) / STAGE < 8 ? (200 * 1024) / STAGE : 8;
-  static constexpr int SMEM = STAGES * STAGE + 1024;            // and what aligns the ring to 1024 bytes
+  static constexpr int B_BYTES = B_ROWS * MM_BK * 2;
+  static constexpr int STAGE = MM_A_BYTES + B_BYTES;            // of one plane each
+  static constexpr int TURN = KIND == MM_ANY ? MMWarps<SUM>::EPI * 32 * 17 * 4 : 0;     // of the epilogue
+  static constexpr int STAGES = (225 * 1024 - TURN) / STAGE < 8 ? (225 * 1024 - TURN) / STAGE : 8;
+  static constexpr int RING = SUM ? (225 * 1024 - TURN) / 1024 * 1024 : STAGES * STAGE;
+  static constexpr int SMEM = RING + TURN + 1024;               // and what aligns the ring to 1024 bytes
   static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
 };
 
 template <int CG, int BN, int KIND, bool SUM>
-__global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant__ MMParams P) {
-  using S = MMShape<CG, BN>;
+__global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __grid_constant__ MMParams P) {
+  using S = MMShape<CG, BN, KIND, SUM>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[S::STAGES], empty[S::STAGES], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
@@ -365,6 +462,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int32_t first = blockIdx.x / CG, step = gridDim.x / CG;
   const int32_t total = P.tiles * P.matrices;
+  const int na = SUM ? P.na : 1, nb = SUM ? P.nb : 1, stages = SUM ? P.stages : S::STAGES;
+  const uint32_t stage_bytes = na * MM_A_BYTES + nb * S::B_BYTES;
 
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < S::STAGES; ++i) {
@@ -373,7 +472,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], MM_EPI_WARPS * CG);
+      mbar_init(&acc_empty[i], MMWarps<SUM>::EPI * CG);
     }
     mbar_init(&drain, 1);
     fence_barrier_init();
@@ -384,60 +483,63 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
   if constexpr (CG == 2) cluster_sync_all();
   fence_after();
   const uint32_t tmem = tmem_slot;
+  // set up beside the kernel before it; its results, and the memory it reads, from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0 && lane == 0) {
     // ---- producer
     const long long drop = g_pipe_drop_row;
     long long issued = 0;
+    int slot = 0;
+    uint32_t round = 0;
     bool ok = true;
     for (int32_t t = first; ok && t < total; t += step) {
       const Tile tile = tile_at<S::BM / BN>(P, t);
       const int32_t am = tile.tm * S::BM + (int32_t)rank * 128;
       const int32_t bn = tile.tn * BN + (int32_t)rank * S::B_ROWS;
-      for (int32_t k = 0; ok && k < P.kblocks; k += P.chunk)
-      for (int p = 0; ok && p < P.pairs; ++p) {
-        const int32_t za = tile.matrix * P.planes_a + P.pa[p], zb = tile.matrix * P.planes_b + P.pb[p];
-        const int32_t end = P.kblocks - k < P.chunk ? P.kblocks : k + P.chunk;
-        for (int32_t kb = k; kb < end; ++kb) {
-          const int s = (int)(issued % S::STAGES);
-          const uint32_t round = (uint32_t)(issued / S::STAGES);
-          if (!mbar_wait(&empty[s], (round & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          if (drop >= 0 && issued >= drop) {      // the lost copies of the test hook
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], S::STAGE * CG);
-          const uint32_t a = ring + s * S::STAGE, b = a + MM_A_BYTES, bar = smem_addr(&full[s]);
-          const int32_t k0 = kb * MM_BK;
+      for (int32_t kb = 0; kb < P.kblocks; ++kb) {
+        if (!mbar_wait(&empty[slot], (round & 1) ^ 1) || (drop >= 0 && issued >= drop)) {      // the test hook's lost copies
+          ok = false;
+          break;
+        }
+        if (rank == 0) mbar_arrive_expect_tx(&full[slot], stage_bytes * CG);
+        uint32_t at = ring + slot * stage_bytes;
+        const uint32_t bar = smem_addr(&full[slot]);
+        const int32_t k0 = kb * MM_BK;
+        for (int p = 0; p < na; ++p, at += MM_A_BYTES) {
+          const int32_t z = tile.matrix * P.planes_a + p;
           if (P.a_k) {
-            tma_box<CG>(a, &P.ta, k0, am, za, bar);
+            tma_box<CG>(at, &P.ta, k0, am, z, bar);
           } else {
-            tma_box<CG>(a, &P.ta, am, k0, za, bar);
-            tma_box<CG>(a + MM_A_BYTES / 2, &P.ta, am + 64, k0, za, bar);
+            tma_box<CG>(at, &P.ta, am, k0, z, bar);
+            tma_box<CG>(at + MM_A_BYTES / 2, &P.ta, am + 64, k0, z, bar);
           }
+        }
+        for (int p = 0; p < nb; ++p, at += S::B_BYTES) {
+          const int32_t z = tile.matrix * P.planes_b + p;
           if (P.b_k) {
-            tma_box<CG>(b, &P.tb, k0, bn, zb, bar);
+            tma_box<CG>(at, &P.tb, k0, bn, z, bar);
           } else {
 #pragma unroll
             for (int j = 0; j < S::B_ROWS / 64; ++j)
-              tma_box<CG>(b + j * (64 * MM_BK * 2), &P.tb, bn + j * 64, k0, zb, bar);
+              tma_box<CG>(at + j * (64 * MM_BK * 2), &P.tb, bn + j * 64, k0, z, bar);
           }
-          ++issued;
         }
+        ++issued;
+        if (++slot == stages) slot = 0, ++round;
       }
     }
     if (!ok && rank == 0)        // copies in flight land before the kernel's memory is given up
-      for (long long i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
-        mbar_wait(&full[i % S::STAGES], (uint32_t)(i / S::STAGES) & 1);
+      for (long long i = issued > stages ? issued - stages : 0; i < issued; ++i)
+        mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---- products
     const uint32_t idesc = (1u << 4) | (P.f16 ? 0u : (1u << 7) | (1u << 10)) | (P.a_k ? 0u : 1u << 15) |
                            (P.b_k ? 0u : 1u << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(S::BM >> 4) << 24);
     const uint32_t a_step = (P.a_k ? 32u : 2048u) >> 4, b_step = (P.b_k ? 32u : 2048u) >> 4;
-    uint32_t n = 0, it = 0;
+    uint32_t n = 0, round = 0;
+    int slot = 0;
     bool ok = true;
     for (int32_t t = first; ok && t < total; t += step)
       for (int32_t k = 0; ok && k < P.kblocks; k += P.chunk, ++n) {
@@ -448,20 +550,23 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         }
         fence_after();
         const uint32_t d = tmem + buf * BN;
-        const int32_t blocks = (P.kblocks - k < P.chunk ? P.kblocks - k : P.chunk) * P.pairs;
-        for (int32_t i = 0; i < blocks; ++i, ++it) {
-          const int s = it % S::STAGES;
-          if (!mbar_wait(&full[s], (it / S::STAGES) & 1)) {
+        const int32_t blocks = P.kblocks - k < P.chunk ? P.kblocks - k : P.chunk;
+        for (int32_t i = 0; i < blocks; ++i) {
+          if (!mbar_wait(&full[slot], round & 1)) {
             ok = false;
             break;
           }
           fence_after();
-          const uint32_t a = ring + s * S::STAGE, b = a + MM_A_BYTES;
-          const uint64_t da = operand_desc(a, MM_A_BYTES / 2), db = operand_desc(b, 64 * MM_BK * 2);
+          const uint32_t at = ring + slot * stage_bytes;
+          for (int p = 0; p < (SUM ? P.pairs : 1); ++p) {
+            const uint32_t a = at + (SUM ? P.pa[p] : 0) * MM_A_BYTES, b = at + na * MM_A_BYTES + (SUM ? P.pb[p] : 0) * S::B_BYTES;
+            const uint64_t da = operand_desc(a, MM_A_BYTES / 2), db = operand_desc(b, 64 * MM_BK * 2);
 #pragma unroll
-          for (int j = 0; j < MM_BK / 16; ++j)
-            mma_16<CG>(d, da + (uint64_t)(j * a_step), db + (uint64_t)(j * b_step), idesc, (i | j) != 0);
-          mma_commit<CG>(&empty[s]);
+            for (int j = 0; j < MM_BK / 16; ++j)
+              mma_16<CG>(d, da + (uint64_t)(j * a_step), db + (uint64_t)(j * b_step), idesc, (i | j | p) != 0);
+          }
+          mma_commit<CG>(&empty[slot]);
+          if (++slot == stages) slot = 0, ++round;
         }
         if (ok) mma_commit<CG>(&acc_full[buf]);
       }
@@ -470,15 +575,16 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
       mbar_wait(&drain, 0);
     }
   } else if (warp >= 4) {
-    // ---- epilogue: a warp's 32 accumulator rows (set by its number), half the columns
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * (BN / 2);
-    constexpr int COLS = BN / 2;
+    // ---- epilogue: a warp's 32 accumulator rows (set by its number), a share of the columns
+    constexpr int COLS = BN * 4 / MMWarps<SUM>::EPI;
+    const int rows = (warp & 3) * 32, share = (warp - 4) >> 2;
+    float* stage = (float*)(smem_raw + (ring - smem_addr(smem_raw)) + S::RING) + (warp - 4) * (32 * 17);
+    const uint32_t mine = tmem + ((uint32_t)rows << 16) + share * COLS;
     uint32_t n = 0;
     for (int32_t t = first; t < total; t += step) {
       const Tile tile = tile_at<S::BM / BN>(P, t);
-      const int64_t r = (int64_t)tile.tm * S::BM + rank * 128 + quarter * 32 + lane;
-      const int64_t col = (int64_t)tile.tn * BN + half * COLS;
+      const int64_t row0 = (int64_t)tile.tm * S::BM + rank * 128 + rows, r = row0 + lane;
+      const int64_t col = (int64_t)tile.tn * BN + share * COLS;
       const bool mirrored = P.symmetric && (tile.tn + 1) * BN <= tile.tm * S::BM;
       bool ok = true;
       if constexpr (SUM) {
@@ -489,36 +595,51 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
           if (!ok) break;
           fence_after();
 #pragma unroll
-          for (int c = 0; c < COLS; c += 32) {
-            float v[32];
-            tmem_load32(mine + buf * BN + c, v);
+          for (int c = 0; c < COLS; c += 16) {
+            float v[16];
+            tmem_load16(mine + buf * BN + c, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[c + i] = k ? sum[c + i] + v[i] : v[i];
+            for (int i = 0; i < 16; ++i) sum[c + i] = k ? sum[c + i] + v[i] : v[i];
           }
           fence_before();
           __syncwarp();
           if (lane == 0) arrive_first<CG>(&acc_empty[buf]);
         }
         if (!ok) break;
+#pragma unroll 1
+        for (int c = 0; c < COLS; c += 16) {
+          Fetched F;
+          fetch16<KIND>(P, tile.matrix, r, col + c, F);
+          float v[16];
 #pragma unroll
-        for (int c = 0; c < COLS; c += 32) finish32<KIND>(P, tile.matrix, r, col + c, mirrored, sum + c);
+          for (int i = 0; i < 16; ++i) {
+            v[i] = sum[i];
+#pragma unroll
+            for (int q = 16; q < COLS; q += 16) v[i] = c == q ? sum[q + i] : v[i];
+          }
+          finish16<KIND>(P, tile.matrix, row0, lane, col + c, mirrored, F, stage, v);
+        }
       } else {
         const int buf = n & 1;
+        Fetched F;
+        fetch16<KIND>(P, tile.matrix, r, col, F);
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[buf], (n >> 1) & 1));
         if (!ok) break;
         ++n;
         fence_after();
 #pragma unroll 1
-        for (int c = 0; c < COLS; c += 32) {
-          float v[32];
+        for (int c = 0; c < COLS; c += 16) {
+          float v[16];
           __syncwarp();
-          tmem_load32(mine + buf * BN + c, v);
-          if (c + 32 >= COLS) {      // the accumulator is read: the next tile but one may have it
+          tmem_load16(mine + buf * BN + c, v);
+          if (c + 16 >= COLS) {      // the accumulator is read: the next tile but one may have it
             fence_before();
             __syncwarp();
             if (lane == 0) arrive_first<CG>(&acc_empty[buf]);
           }
-          finish32<KIND>(P, tile.matrix, r, col + c, mirrored, v);
+          const Fetched now = F;
+          if (c + 16 < COLS) fetch16<KIND>(P, tile.matrix, r, col + c + 16, F);
+          finish16<KIND>(P, tile.matrix, row0, lane, col + c, mirrored, now, stage, v);
         }
       }
     }
@@ -529,6 +650,145 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
   if constexpr (CG == 2) cluster_sync_all();
   fence_after();
   if (warp == 2) tmem_free<CG>(tmem, S::TMEM_COLS);
+}
+
+// -------------------------------------------------------------- few rows
+//
+// For up to 64 rows of x the weights' bytes are the time: the product is taken
+// the other way round, 128 columns of w as the tensor core's rows and the rows
+// of x as its N, and the CTAs of a cluster share the summed axis, so that
+// every SM has its part of w on the way at once.  Their accumulators meet in
+// shared memory and are added in the cluster's order; a CTA finishes its share
+// of the elements, lanes on neighbouring columns of y.
+template <int BN>
+struct ThinShape {
+  static constexpr int STAGE = MM_A_BYTES + BN * MM_BK * 2;
+  static constexpr int STAGES = 8;
+  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
+};
+constexpr int THIN_THREADS = 192;
+
+__device__ __forceinline__ float load_cluster(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v)
+               : "r"(addr), "r"(rank)
+               : "memory");
+  return v;
+}
+
+template <int BN>
+__global__ void __launch_bounds__(THIN_THREADS, 1) mm_thin_kernel(const __grid_constant__ MMParams P, int split) {
+  using S = ThinShape<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[S::STAGES], empty[S::STAGES], acc_full, drain;
+  __shared__ uint32_t tmem_slot;
+  const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int32_t tile = blockIdx.x / split;
+  const int32_t k0 = (int32_t)((int64_t)P.kblocks * rank / split), k1 = (int32_t)((int64_t)P.kblocks * (rank + 1) / split);
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < S::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&acc_full, 1);
+    mbar_init(&drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc<1>(&tmem_slot, S::TMEM_COLS);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == 0 && lane == 0) {
+    const long long drop = g_pipe_drop_row;
+    int issued = 0;
+    bool ok = true;
+    for (int32_t kb = k0; kb < k1; ++kb, ++issued) {
+      const int s = issued % S::STAGES;
+      if (!mbar_wait(&empty[s], ((issued / S::STAGES) & 1) ^ 1) || (drop >= 0 && issued >= drop)) {
+        ok = false;
+        break;
+      }
+      mbar_arrive_expect_tx(&full[s], S::STAGE);
+      const uint32_t a = ring + s * S::STAGE, bar = smem_addr(&full[s]);
+      if (P.a_k) {
+        tma_box<1>(a, &P.ta, kb * MM_BK, tile * 128, 0, bar);
+      } else {
+        tma_box<1>(a, &P.ta, tile * 128, kb * MM_BK, 0, bar);
+        tma_box<1>(a + MM_A_BYTES / 2, &P.ta, tile * 128 + 64, kb * MM_BK, 0, bar);
+      }
+      tma_box<1>(a + MM_A_BYTES, &P.tb, kb * MM_BK, 0, 0, bar);
+    }
+    if (!ok)
+      for (int i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
+        mbar_wait(&full[i % S::STAGES], (i / S::STAGES) & 1);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (P.a_k ? 0u : 1u << 15) | ((uint32_t)(BN >> 3) << 17) |
+                           ((uint32_t)(128 >> 4) << 24);
+    const uint32_t a_step = (P.a_k ? 32u : 2048u) >> 4;
+    bool ok = true;
+    for (int32_t i = 0; i < k1 - k0; ++i) {
+      const int s = i % S::STAGES;
+      if (!mbar_wait(&full[s], (i / S::STAGES) & 1)) {
+        ok = false;
+        break;
+      }
+      fence_after();
+      const uint32_t a = ring + s * S::STAGE;
+      const uint64_t da = operand_desc(a, MM_A_BYTES / 2), db = operand_desc(a + MM_A_BYTES, 64 * MM_BK * 2);
+#pragma unroll
+      for (int j = 0; j < MM_BK / 16; ++j)
+        mma_16<1>(tmem, da + (uint64_t)(j * a_step), db + (uint64_t)(j * 2), idesc, (i | j) != 0);
+      mma_commit<1>(&empty[s]);
+    }
+    if (ok) {
+      mma_commit<1>(&acc_full);
+    } else {
+      mma_commit<1>(&drain);
+      mbar_wait(&drain, 0);
+    }
+  }
+  __syncwarp();
+  // Every part of the ring has been used up once the accumulator is there: it takes the sums, column after column.
+  float* part = (float*)(smem_raw + (ring - smem_addr(smem_raw)));
+  if (warp >= 2 && __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full, 0))) {
+    fence_after();
+    const int row = (warp & 3) * 32;
+#pragma unroll
+    for (int c = 0; c < BN; c += 16) {
+      float v[16];
+      tmem_load16(tmem + ((uint32_t)row << 16) + c, v);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) part[(c + k) * 128 + row + lane] = v[k];
+    }
+    fence_before();
+  }
+  __syncwarp();
+  cluster_sync_all();
+  fence_after();
+  if (warp == 1) tmem_free<1>(tmem, S::TMEM_COLS);
+  const MMEpilogue& E = P.e;
+  const int rows = (int)P.n, total = 128 * rows;                       // P.m: columns of y
+  const int from = (int)((int64_t)total * rank / split), to = (int)((int64_t)total * (rank + 1) / split);
+  for (int i = from + threadIdx.x; i < to; i += THIN_THREADS) {
+    const int64_t c = (int64_t)tile * 128 + (i & 127), r = i >> 7;
+    if (c >= P.m) continue;
+    float v = load_cluster(smem_addr(part + i), 0);
+    for (int q = 1; q < split; ++q) v += load_cluster(smem_addr(part + i), q);
+    if (E.bias) v += load1_rt(E.bias, E.bt, c);
+    if (E.z) store1_rt(E.z, E.zt, r * E.ldz + c, v);
+    float t[2] = {v, v};
+    act_rt<2>(t, E.act);
+    store1_rt(E.y, E.yt, r * E.ldy + c, E.res ? t[0] + load1_rt(E.res, E.rt, r * E.ldr + c) : t[0]);
+  }
+  cluster_sync_all();
 }
 
 // --------------------------------------------------------------------- host
@@ -571,9 +831,14 @@ static int encode_operand(CUtensorMap* map, const MMOperand& o, int64_t matrices
 // accumulator is added to a register with one rounding instead.
 constexpr int MM_SUM_BLOCKS = 4;
 
+// Absent, or bf16 rows that begin on 32-byte boundaries.
+static bool rows_32(const void* p, int32_t dt, int64_t ld) {
+  return !p || (dt == PSK_BF16 && (uintptr_t)p % 32 == 0 && ld % 16 == 0);
+}
+
 template <int CG, int BN, int KIND, bool SUM>
 static int launch_shape(const MMCall& C, cudaStream_t stream) {
-  using S = MMShape<CG, BN>;
+  using S = MMShape<CG, BN, KIND, SUM>;
   MMParams P{};
   int rc = encode_operand(&P.ta, C.a, C.matrices, C.f16, C.a.k_inner ? 128 : 64);
   if (!rc) rc = encode_operand(&P.tb, C.b, C.matrices, C.f16, C.b.k_inner ? S::B_ROWS : 64);
@@ -582,6 +847,12 @@ static int launch_shape(const MMCall& C, cudaStream_t stream) {
   P.m = C.m, P.n = C.n;
   P.kblocks = (int32_t)((C.k + MM_BK - 1) / MM_BK), P.pairs = C.pairs, P.matrices = (int32_t)C.matrices;
   P.chunk = SUM ? MM_SUM_BLOCKS : P.kblocks;
+  for (int i = 0; i < C.pairs; ++i) {
+    P.na = C.pa[i] + 1 > P.na ? C.pa[i] + 1 : P.na;
+    P.nb = C.pb[i] + 1 > P.nb ? C.pb[i] + 1 : P.nb;
+  }
+  P.stages = S::RING / (P.na * MM_A_BYTES + P.nb * S::B_BYTES);
+  if (P.stages > S::STAGES) P.stages = S::STAGES;
   P.planes_a = C.a.planes, P.planes_b = C.b.planes;
   P.a_k = C.a.k_inner, P.b_k = C.b.k_inner, P.f16 = C.f16;
   const int64_t tm = (C.m + S::BM - 1) / S::BM, tn = (C.n + BN - 1) / BN;
@@ -596,27 +867,89 @@ static int launch_shape(const MMCall& C, cudaStream_t stream) {
   static bool limit[PSK_MAX_DEVICES] = {};
   smem_limit_once((const void*)mm_kernel<CG, BN, KIND, SUM>, S::SMEM, limit);
   const int64_t most = device_sm_count() / CG, want = tiles * C.matrices;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((want < most ? want : most) * CG));
-  cfg.blockDim = dim3(MM_THREADS);
+  cfg.blockDim = dim3(MMWarps<SUM>::THREADS);
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
+  cfg.numAttrs = CG > 1 ? 2 : 1;
   cudaLaunchKernelEx(&cfg, mm_kernel<CG, BN, KIND, SUM>, P);
   return check_launch("matrix product kernel");
 }
 
-template <int KIND>
+template <int BN>
+static int launch_thin(const MMCall& C, cudaStream_t stream) {
+  using S = ThinShape<BN>;
+  MMParams P{};
+  int rc = encode_operand(&P.ta, C.b, 1, false, C.b.k_inner ? 128 : 64);
+  if (!rc) rc = encode_operand(&P.tb, C.a, 1, false, BN);
+  if (rc) return rc;
+  P.e = C.e;
+  P.m = C.n, P.n = C.m;
+  P.kblocks = (int32_t)((C.k + MM_BK - 1) / MM_BK);
+  P.a_k = C.b.k_inner;
+  const int64_t tiles = (C.n + 127) / 128;
+  // CTAs of a tile: what fills the SMs once, two blocks of the summed axis each at least
+  int64_t split = device_sm_count() / tiles;
+  split = split < 1 ? 1 : split > 8 ? 8 : split;
+  while (split > 1 && P.kblocks < 2 * split) --split;
+  static bool limit[PSK_MAX_DEVICES] = {};
+  smem_limit_once((const void*)mm_thin_kernel<BN>, S::SMEM, limit);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(THIN_THREADS);
+  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaLaunchKernelEx(&cfg, mm_thin_kernel<BN>, P, (int)split);
+  return check_launch("matrix product kernel of few rows");
+}
+
+// Pairs of CTAs on tiles of 256 x 256, or single ones on 128 x 128: by the
+// time of the tiles that one SM takes in turn.  64 summed elements of a tile
+// take about 0.34 us of a pair and 0.30 us of one CTA, whose 128 columns are
+// bound by shared memory (operands read and filled in: 2048^3 16.8 and 24.3 us,
+// 512 x 2048 x 5632 15.9 and 23.8, 1024^3 11.4 and 9.0, 128 x 2048 x 5632 15.6
+// and 13.4).
+template <int KIND, bool SUM>
 static int launch_kind(const MMCall& C, cudaStream_t stream) {
-  return C.pairs > 1 ? launch_shape<1, 128, KIND, true>(C, stream) : launch_shape<1, 128, KIND, false>(C, stream);
+  const int64_t sms = device_sm_count(), pairs = sms / 2;
+  const auto waves = [&](int64_t side, int64_t units) {
+    const int64_t tm = (C.m + side - 1) / side, tn = (C.n + side - 1) / side;
+    return ((C.symmetric ? tm * (tm + 1) / 2 : tm * tn) * C.matrices + units - 1) / units;
+  };
+  if (pairs > 0 && waves(256, pairs) * 34 < waves(128, sms) * 30) return launch_shape<2, 256, KIND, SUM>(C, stream);
+  return launch_shape<1, 128, KIND, SUM>(C, stream);
 }
 
 int mm_launch(const MMCall& C, cudaStream_t stream) {
-  return C.kind == MM_LINEAR ? launch_kind<MM_LINEAR>(C, stream) : launch_kind<MM_ORTHO>(C, stream);
+  const MMEpilogue& E = C.e;
+  const bool sum = C.pairs > 1;
+  if (C.ortho) return sum ? launch_kind<MM_ORTHO, true>(C, stream) : launch_kind<MM_ORTHO, false>(C, stream);
+  const bool wide = C.n % 16 == 0 && rows_32(E.y, E.yt, E.ldy) && rows_32(E.z, E.zt, E.ldz) &&
+                    rows_32(E.res, E.rt, E.ldr) && rows_32(E.bias, E.bt, 0);
+  if (!sum && C.m <= 64 && C.a.k_inner)
+    return C.m <= 16 ? launch_thin<16>(C, stream) : C.m <= 32 ? launch_thin<32>(C, stream) : launch_thin<64>(C, stream);
+  if (sum) return launch_kind<MM_ANY, true>(C, stream);
+  if (!wide) return launch_kind<MM_ANY, false>(C, stream);
+  switch (E.act) {
+    case ACT_RELU: return launch_kind<ACT_RELU, false>(C, stream);
+    case ACT_GELU: return launch_kind<ACT_GELU, false>(C, stream);
+    case ACT_SILU: return launch_kind<ACT_SILU, false>(C, stream);
+    default: return launch_kind<ACT_NONE, false>(C, stream);
+  }
 }
 
 int mm_status(unsigned int* v, bool reset) {

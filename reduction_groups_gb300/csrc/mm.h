@@ -24,18 +24,19 @@ struct MMLeaf {
   int64_t ld, vec;
 };
 
-enum MMEpilogueKind { MM_LINEAR = 0, MM_ORTHO = 1 };
+// An epilogue's kind: the orthogonalised update, the linear layer of any
+// types, or of bf16 with an activation.
+constexpr int MM_ORTHO = 16, MM_ANY = 17;
 
 // What becomes of the accumulated product p(r, c).
 struct MMEpilogue {
-  // MM_LINEAR: z = p + bias, y = act(z) + residual.  NULL: not there.
+  // The linear layer: z = p + bias, y = act(z) + residual.  NULL: not there.
   const void *bias, *res;
   void *y, *z;
   int64_t ldr, ldy, ldz;
   int32_t bt, rt, yt, zt, act;
-  int32_t vec_bias, vec_res, vec_y, vec_z;      // 16-byte accesses allowed
-  // MM_ORTHO: v = alpha p + beta r, r and v matrices of fp16 planes (`ld`,
-  // `plane_stride`, matrix after matrix), or v stored into leaves[matrix] (DEVICE, type yt).
+  // The orthogonalised update: v = alpha p + beta r, r and v matrices of fp16 planes (`ld`, a
+  // multiple of 16, `plane_stride`, matrix after matrix), or v stored into leaves[matrix] (DEVICE, type yt).
   float alpha, beta;
   const uint16_t* from;
   uint16_t* to;
@@ -53,7 +54,7 @@ struct MMCall {
   uint8_t pa[8], pb[8];
   int64_t matrices;
   bool symmetric;               // m == n, the result its own transpose: one triangle is computed
-  MMEpilogueKind kind;
+  bool ortho;
   MMEpilogue e;
 };
 

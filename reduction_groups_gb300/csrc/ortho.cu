@@ -49,17 +49,38 @@ struct OrthoShape {
   int32_t xt, tall, blocks, leaves;
   double eps;
   double* sums;                 // [leaf][block]
+  float* factors;               // [leaf]
   MMLeaf* table;
   uint16_t* x;                  // [leaf][part][m][ldn]
 };
 
-// Where the results go, for the last product's epilogue.
-__global__ void ortho_targets_kernel(const __grid_constant__ OrthoTargets T, MMLeaf* table, int leaves) {
-  for (int i = threadIdx.x; i < leaves; i += blockDim.x) table[i] = MMLeaf{T.y[i], T.ldy[i], T.vec[i]};
+// A block of rows' sum of squares: f32 within a thread's share of a row, 64
+// bits beyond.  A warp a row, up to 1024 columns of it on their way at once.
+// A share whose squares leave f32 (elements above 2^60 or so) is taken again
+// times 2^-64.
+template <int XT, bool VEC>
+__device__ __forceinline__ float ortho_share(const void* x, int64_t row, int64_t cols, int lane, float scale) {
+  float2 s = make_float2(0.0f, 0.0f);
+  for (int64_t c = 0; c < cols; c += 1024) {
+    Piece<XT, VEC, 8> p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const Columns<VEC, 8> C(c + j * 256, 32, lane, cols);
+      C.template load<XT>(x, row, p[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        float2 v = make_float2(p[j].get(k), p[j].get(k + 1));
+        if (scale != 1.0f) v.x *= scale, v.y *= scale;
+        s = __ffma2_rn(v, v, s);
+      }
+  }
+  return s.x + s.y;
 }
 
-// A block of rows' sum of squares: f32 within a thread's row, 64 bits beyond.
-// Elements above 2^50, whose squares would leave f32, are taken times 2^-64.
+template <int XT, bool VEC>
 __global__ void __launch_bounds__(256) ortho_sum_kernel(const __grid_constant__ OrthoTable T, OrthoShape S) {
   __shared__ double part[8];
   const int leaf = blockIdx.x / S.blocks, block = blockIdx.x % S.blocks;
@@ -68,18 +89,10 @@ __global__ void __launch_bounds__(256) ortho_sum_kernel(const __grid_constant__ 
   const int64_t ld = T.ldx[leaf];
   double total = 0.0;
   for (int64_t r = (int64_t)block * 8 + warp; r < S.rows; r += (int64_t)S.blocks * 8) {
-    float s = 0.0f, big = 0.0f;
-    for (int64_t c = lane; c < S.cols; c += 32) {
-      const int64_t i = r * ld + c;
-      const float v = S.xt == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)x)[i]) : ((const float*)x)[i];
-      if (fabsf(v) > 1.1e15f) {
-        const float u = v * 5.421010862427522e-20f;
-        big = fmaf(u, u, big);
-      } else {
-        s = fmaf(v, v, s);
-      }
-    }
-    total += (double)s + (double)big * 3.402823669209385e38;
+    const float s = ortho_share<XT, VEC>(x, r * ld, S.cols, lane, 1.0f);
+    if (s > 3.4028234663852886e38f)
+      total += (double)ortho_share<XT, VEC>(x, r * ld, S.cols, lane, 5.421010862427522e-20f) * 3.402823669209385e38;
+    else total += (double)s;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
@@ -88,6 +101,21 @@ __global__ void __launch_bounds__(256) ortho_sum_kernel(const __grid_constant__ 
   if (threadIdx.x == 0) {
     for (int w = 1; w < 8; ++w) total += part[w];
     S.sums[blockIdx.x] = total;
+  }
+}
+
+// A warp a leaf: the blocks' sums, the factor S / (norm + eps), and where the
+// result goes, for the last product's epilogue.
+__global__ void __launch_bounds__(256) ortho_factor_kernel(const __grid_constant__ OrthoTargets T, OrthoShape S) {
+  const int leaf = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (leaf >= S.leaves) return;
+  double s = 0.0;
+  for (int i = lane; i < S.blocks; i += 32) s += S.sums[leaf * S.blocks + i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (lane == 0) {
+    S.factors[leaf] = (float)((double)ORTHO_SCALE / (sqrt(s) + S.eps));
+    S.table[leaf] = MMLeaf{T.y[leaf], T.ldy[leaf], T.vec[leaf]};
   }
 }
 
@@ -102,68 +130,73 @@ __device__ __forceinline__ float from_f16(uint32_t h) {
   return f;
 }
 
-// The first iterate: 64 x 64 of it a CTA, through shared memory, so that the
-// leaf's rows and the iterate's are both walked along.
+// Eight columns of the iterate in its two parts.
+__device__ __forceinline__ void ortho_store8(const OrthoShape& S, int64_t leaf, int64_t r, int64_t c, float* v) {
+  uint16_t* q = S.x + leaf * ORTHO_PARTS * S.m * S.ldn + r * S.ldn + c;
+#pragma unroll
+  for (int p = 0; p < ORTHO_PARTS; ++p) {
+    uint32_t h[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      h[k] = to_f16(v[k]);
+      v[k] -= from_f16(h[k]);
+    }
+    *(uint4*)(q + p * S.m * S.ldn) = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
+                                                h[6] | h[7] << 16);
+  }
+}
+
+// The first iterate.  64 x 64 of it a CTA: of a leaf whose rows are the
+// iterate's, straight from rows to rows; of a tall one through shared memory,
+// so that the leaf's rows and the iterate's are both walked along.
+template <int XT, bool VEC, bool TALL>
 __global__ void __launch_bounds__(256) ortho_begin_kernel(const __grid_constant__ OrthoTable T, OrthoShape S) {
-  __shared__ float tile[64][65];
-  __shared__ float factor;
+  __shared__ float tile[TALL ? 64 : 1][65];
   const int64_t tn = (S.ldn + 63) / 64, tm = (S.m + 63) / 64;
   const int64_t leaf = blockIdx.x / (tn * tm), at = blockIdx.x % (tn * tm);
   const int64_t r0 = at / tn * 64, c0 = at % tn * 64;
   const void* x = T.x[leaf];
   const int64_t ld = T.ldx[leaf];
-  if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int i = 0; i < S.blocks; ++i) s += S.sums[leaf * S.blocks + i];
-    factor = (float)((double)ORTHO_SCALE / (sqrt(s) + S.eps));
+  const int i = threadIdx.x >> 3, g = (threadIdx.x & 7) * 8;           // a tile row, and 8 of its columns
+  float v[2][8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t r = (TALL ? c0 : r0) + i + 32 * h, c = (TALL ? r0 : c0) + g;
+    const int64_t left = S.cols - c;
+    load8<XT, VEC>(x, r * ld + c, r < S.rows && left > 0 ? (left < 8 ? (int)left : 8) : 0, v[h]);
   }
-  __syncthreads();
-  const float f = factor;
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int a = i >> 6, b = i & 63;                      // b along the leaf's rows
-    const int64_t r = r0 + (S.tall ? b : a), c = c0 + (S.tall ? a : b);
-    float v = 0.0f;
-    if (r < S.m && c < S.n) {
-      const int64_t e = S.tall ? c * ld + r : r * ld + c;
-      v = (S.xt == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)x)[e]) : ((const float*)x)[e]) * f;
+  const float f = S.factors[leaf];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[h][k] *= f;
+      if constexpr (TALL) tile[g + k][i + 32 * h] = v[h][k];
     }
-    if (S.tall) tile[b][a] = v;
-    else tile[a][b] = v;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-    const int a = i >> 3, g = (i & 7) * 8;
-    if (r0 + a >= S.m || c0 + g >= S.ldn) continue;
-    uint16_t* q = S.x + leaf * ORTHO_PARTS * S.m * S.ldn + (r0 + a) * S.ldn + c0 + g;
-    float v[8];
+  if constexpr (TALL) __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = tile[a][g + k];
+  for (int h = 0; h < 2; ++h) {
+    const int a = i + 32 * h;
+    if constexpr (TALL) {
 #pragma unroll
-    for (int p = 0; p < ORTHO_PARTS; ++p) {
-      uint32_t h[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        h[k] = to_f16(v[k]);
-        v[k] -= from_f16(h[k]);
-      }
-      *(uint4*)(q + p * S.m * S.ldn) = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
-                                                  h[6] | h[7] << 16);
+      for (int k = 0; k < 8; ++k) v[h][k] = tile[a][g + k];
     }
+    if (r0 + a < S.m && c0 + g < S.ldn) ortho_store8(S, leaf, r0 + a, c0 + g, v[h]);
   }
 }
 
 struct OrthoLayout {
-  uint64_t sums, table, x0, x1, a, b, bytes;
+  uint64_t sums, factors, table, x0, x1, a, b, bytes;
   int64_t xsize, asize;         // elements of one plane
 };
 
-static int64_t ortho_up8(int64_t v) { return (v + 7) / 8 * 8; }
+static int64_t ortho_up16(int64_t v) { return (v + 15) / 16 * 16; }      // rows of whole 32-byte sectors
 
 static OrthoLayout ortho_layout(int32_t leaves, int64_t rows, int64_t cols, int32_t yt) {
   OrthoLayout L{};
   const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
   const int planes = yt == PSK_F32 ? 2 : 1;
-  L.xsize = m * ortho_up8(n), L.asize = m * ortho_up8(m);
+  L.xsize = m * ortho_up16(n), L.asize = m * ortho_up16(m);
   uint64_t at = 0;
   const auto take = [&](uint64_t bytes) {
     const uint64_t o = at;
@@ -171,6 +204,7 @@ static OrthoLayout ortho_layout(int32_t leaves, int64_t rows, int64_t cols, int3
     return o;
   };
   L.sums = take((uint64_t)leaves * ORTHO_SUM_BLOCKS * 8);
+  L.factors = take((uint64_t)leaves * 4);
   L.table = take((uint64_t)leaves * sizeof(MMLeaf));
   L.x0 = take((uint64_t)leaves * ORTHO_PARTS * L.xsize * 2);
   L.x1 = take((uint64_t)leaves * ORTHO_PARTS * L.xsize * 2);
@@ -258,18 +292,27 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
   S.rows = rows, S.cols = cols;
   S.tall = rows > cols;
   S.m = S.tall ? cols : rows, S.n = S.tall ? rows : cols;
-  S.ldn = ortho_up8(S.n), S.ldm = ortho_up8(S.m);
+  S.ldn = ortho_up16(S.n), S.ldm = ortho_up16(S.m);
   S.xt = xt, S.leaves = n_leaves;
   const int planes = yt == PSK_F32 ? 2 : 1;
   int64_t blocks = (rows + 31) / 32;
   S.blocks = (int32_t)(blocks < ORTHO_SUM_BLOCKS ? blocks : ORTHO_SUM_BLOCKS);
   S.eps = eps;
-  S.sums = (double*)(ws + L.sums), S.table = (MMLeaf*)(ws + L.table), S.x = (uint16_t*)(ws + L.x0);
-  ortho_targets_kernel<<<1, 256, 0, s>>>(Y, S.table, n_leaves);
-  ortho_sum_kernel<<<(unsigned)(n_leaves * S.blocks), 256, 0, s>>>(T, S);
+  S.sums = (double*)(ws + L.sums), S.factors = (float*)(ws + L.factors);
+  S.table = (MMLeaf*)(ws + L.table), S.x = (uint16_t*)(ws + L.x0);
+  bool vec = cols % 8 == 0;
+  for (int i = 0; i < n_leaves; ++i) vec = vec && rows_vec8(leaves[i].x, xt, leaves[i].ldx, rows);
   const int64_t tiles = (S.ldn + 63) / 64 * ((S.m + 63) / 64) * n_leaves;
   if (tiles > 0x7FFFFFFF) return fail(PSK_E_SHAPE, "too many tiles");
-  ortho_begin_kernel<<<(unsigned)tiles, 256, 0, s>>>(T, S);
+  with_dtype(xt, [&](auto XT) {
+    return with_bool(vec, [&](auto VEC) {
+      ortho_sum_kernel<XT.value, VEC.value><<<(unsigned)(n_leaves * S.blocks), 256, 0, s>>>(T, S);
+      ortho_factor_kernel<<<(unsigned)((n_leaves + 7) / 8), 256, 0, s>>>(Y, S);
+      if (S.tall) ortho_begin_kernel<XT.value, VEC.value, true><<<(unsigned)tiles, 256, 0, s>>>(T, S);
+      else ortho_begin_kernel<XT.value, VEC.value, false><<<(unsigned)tiles, 256, 0, s>>>(T, S);
+      return 0;
+    });
+  });
   rc = check_launch("orthogonalisation's first kernels");
   uint16_t *x = S.x, *x2 = (uint16_t*)(ws + L.x1), *A = (uint16_t*)(ws + L.a), *B = (uint16_t*)(ws + L.b);
   const auto wide = [&](const uint16_t* p, bool k_inner) {
@@ -277,7 +320,7 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
   };
   const auto square = [&](const uint16_t* p) { return MMOperand{p, S.m, S.m, S.ldm, L.asize, planes, true}; };
   MMCall C{};
-  C.f16 = true, C.matrices = n_leaves, C.kind = MM_ORTHO;
+  C.f16 = true, C.matrices = n_leaves, C.ortho = true;
   if (planes == 1) {
     C.pairs = 1;
   } else {

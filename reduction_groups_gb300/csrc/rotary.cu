@@ -10,8 +10,8 @@
 // warp forms its token's cosines and sines once for all heads.
 //
 // Memory-bound: x is read once and y written once.  Heads are taken by teams
-// of lanes, a lane holding groups of V pairs (V = 8: 16-byte accesses), several
-// heads of a token in flight in a warp.
+// of lanes, several heads of a token by a warp at once, and the loads of the
+// steps to come are in flight while one is worked on.
 #include "common.cuh"
 #include "vec8.cuh"
 #include "views.h"
@@ -21,7 +21,12 @@ namespace psk {
 constexpr int ROT_THREADS = 256;
 constexpr int ROT_WARPS = ROT_THREADS / 32;
 constexpr int ROT_MAX_DIM = 512;
-constexpr int ROT_MAX_BLOCKS = 304;
+#ifndef RFC
+#define RFC 3
+#define RBC 2
+#endif
+constexpr int ROT_FWD_CTAS = RFC, ROT_BWD_CTAS = RBC;    // an SM
+constexpr int ROT_MAX_BLOCKS = 4 * NOMINAL_SMS;      // CTAs of the backward, at most
 
 struct RotSide {
   const void *x, *ct, *gamma;
@@ -78,83 +83,47 @@ __device__ __forceinline__ void rot_angles(float2* cs, const RotTable& T, const 
   __syncwarp();
 }
 
-// A lane's group g of V pairs of a head: its columns, in two runs of V (pairs
-// of halves) or as 2 V neighbours.
-template <int V, bool NEIGH>
-struct RotGroup {
-  int first[2];                            // of each run
-  int pair;                                // its first pair
+// ------------------------------------------------- heads of any size and type
+//
+// A lane holds NG pairs of a head, `team` lanes apart, loaded and stored
+// element by element.
+
+struct RotPair {
+  int col[2], pair;
   bool turns, has[2];
-  __device__ __forceinline__ RotGroup(int g, const RotParams& P) {
-    pair = g * V;
-    turns = pair < P.rot / 2;
-    if constexpr (NEIGH) {
-      first[0] = 2 * pair, first[1] = 2 * pair + V;
-    } else if (turns) {
-      first[0] = pair, first[1] = pair + P.rot / 2;
+  __device__ __forceinline__ void place(int p, bool neighbours, const RotParams& P) {
+    pair = p;
+    turns = p < P.rot / 2;
+    const int rest = (P.dim - P.rot + 1) / 2;          // pairs of columns that do not turn
+    if (turns) {
+      col[0] = neighbours ? 2 * p : p, col[1] = neighbours ? 2 * p + 1 : p + P.rot / 2;
     } else {
-      const int i = pair - P.rot / 2;
-      first[0] = P.rot + i, first[1] = P.rot + (P.dim - P.rot + 1) / 2 + i;
+      col[0] = P.rot + p - P.rot / 2, col[1] = col[0] + rest;
     }
-    const int pairs = P.rot / 2 + (P.dim - P.rot + 1) / 2;
-    has[0] = pair < pairs;
-    has[1] = has[0] && first[1] < P.dim;
+    has[0] = p < P.rot / 2 + rest;
+    has[1] = has[0] && col[1] < P.dim;
   }
-  // Element index of the members of pair i in the 2 V values.
-  static __device__ __forceinline__ constexpr int a(int i) { return NEIGH ? 2 * i : i; }
-  static __device__ __forceinline__ constexpr int b(int i) { return NEIGH ? 2 * i + 1 : i + V; }
-  __device__ __forceinline__ void load(const void* p, int32_t dt, int64_t at, float* v) const {
+  __device__ __forceinline__ void load(const void* p, int32_t dt, int64_t at, bool live, float (&v)[2]) const {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if constexpr (V == 8) {
-        const int n = has[k] ? 8 : 0;
-        if (dt == PSK_BF16) {
-          if (n) load8<PSK_BF16, true>(p, at + first[k], 8, v + 8 * k);
-        } else {
-          if (n) load8<PSK_F32, true>(p, at + first[k], 8, v + 8 * k);
-        }
-        if (!n) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[8 * k + i] = 0.0f;
-        }
-      } else {
-        v[k] = !has[k] ? 0.0f
-               : dt == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)p)[at + first[k]])
-                                : ((const float*)p)[at + first[k]];
-      }
-    }
+    for (int k = 0; k < 2; ++k)
+      v[k] = !live || !has[k] ? 0.0f
+             : dt == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)p)[at + col[k]])
+                              : ((const float*)p)[at + col[k]];
   }
-  __device__ __forceinline__ void store(void* p, int32_t dt, int64_t at, const float* v) const {
+  __device__ __forceinline__ void store(void* p, int32_t dt, int64_t at, const float (&v)[2]) const {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!has[k]) continue;
-      if constexpr (V == 8) {
-        const float* w = v + 8 * k;
-        if (dt == PSK_BF16) {
-          *(uint4*)((uint16_t*)p + at + first[k]) = make_uint4(f32x2_to_bf16x2(w[0], w[1]), f32x2_to_bf16x2(w[2], w[3]),
-                                                               f32x2_to_bf16x2(w[4], w[5]), f32x2_to_bf16x2(w[6], w[7]));
-        } else {
-          float4* q = (float4*)((float*)p + at + first[k]);
-          q[0] = make_float4(w[0], w[1], w[2], w[3]);
-          q[1] = make_float4(w[4], w[5], w[6], w[7]);
-        }
-      } else if (dt == PSK_BF16) {
-        ((uint16_t*)p)[at + first[k]] = f32_to_bf16_bits(v[k]);
-      } else {
-        ((float*)p)[at + first[k]] = v[k];
-      }
+      if (dt == PSK_BF16) ((uint16_t*)p)[at + col[k]] = f32_to_bf16_bits(v[k]);
+      else ((float*)p)[at + col[k]] = v[k];
     }
   }
-  // Turn the pairs by sign times their angle.
-  __device__ __forceinline__ void turn(const float2* cs, float sign, float* v) const {
-    if (!turns || !has[0]) return;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float2 t = cs[pair + i];
-      const float x = v[a(i)], y = v[b(i)], s = sign * t.y;
-      v[a(i)] = fmaf(x, t.x, -(y * s));
-      v[b(i)] = fmaf(y, t.x, x * s);
-    }
+  __device__ __forceinline__ float2 angle(const float2* cs) const { return turns ? cs[pair] : make_float2(1.0f, 0.0f); }
+  __device__ __forceinline__ void turn(float2 t, float (&v)[2]) const {
+    if (!turns) return;
+    const float x = v[0], y = v[1];
+    v[0] = fmaf(x, t.x, -(y * t.y));
+    v[1] = fmaf(y, t.x, x * t.y);
   }
 };
 
@@ -163,74 +132,77 @@ __device__ __forceinline__ float team_sum(float s, int team) {
   return s;
 }
 
-// Lanes of a team (a power of two): one for each group of V pairs, a warp at most.
-template <int V>
-static int rot_team(const RotParams& P) {
-  const int pairs = P.rot / 2 + (P.dim - P.rot + 1) / 2, groups = (pairs + V - 1) / V;
-  int t = 1;
-  while (t < 32 && t < groups) t *= 2;
-  return t;
-}
-
-template <int V, int NG, bool NEIGH, int XT, int YT>
-__global__ void __launch_bounds__(ROT_THREADS) rotary_kernel(const __grid_constant__ RotParams P, int team) {
-  __shared__ RotTable T;
-  __shared__ float2 angles[ROT_WARPS][ROT_MAX_DIM / 2];
-  __shared__ float gammas[2][ROT_MAX_DIM];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int xt = XT < 0 ? P.x_type : XT, yt = YT < 0 ? P.y_type : YT;
-  rot_table(T, P);
+__device__ __forceinline__ void rot_scales(float (&gammas)[2][ROT_MAX_DIM], const RotParams& P) {
   for (int i = threadIdx.x; i < 2 * P.dim; i += ROT_THREADS) {
     const int s = i >= P.dim, c = i - s * P.dim;
     const void* g = P.side[s].gamma;
     gammas[s][c] = !g ? 1.0f : P.gamma_type == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)g)[c]) : ((const float*)g)[c];
   }
   __syncthreads();
+}
+
+// A CTA's sums of one side: its warps' joined.
+__device__ __forceinline__ void rot_part(const float (&sums)[ROT_WARPS][ROT_MAX_DIM], int sd, const RotParams& P) {
+  __syncthreads();
+  for (int c = threadIdx.x; c < P.dim; c += ROT_THREADS) {
+    float s = sums[0][c];
+#pragma unroll
+    for (int w = 1; w < ROT_WARPS; ++w) s += sums[w][c];
+    P.part[((int64_t)blockIdx.x * 2 + sd) * P.dim + c] = s;
+  }
+}
+
+template <int NG>
+__global__ void __launch_bounds__(ROT_THREADS, 3) rotary_any_kernel(const __grid_constant__ RotParams P, int team) {
+  __shared__ RotTable T;
+  __shared__ float2 angles[ROT_WARPS][ROT_MAX_DIM / 2];
+  __shared__ float gammas[2][ROT_MAX_DIM];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  rot_table(T, P);
+  rot_scales(gammas, P);
   const int slots = 32 / team, slot = lane / team, in = lane % team;
-  const int heads = P.side[0].heads + P.side[1].heads;
-  float2* cs = angles[warp];
+  const int qsteps = (P.side[0].heads + slots - 1) / slots, steps = qsteps + (P.side[1].heads + slots - 1) / slots;
+  RotPair G[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) G[g].place(in + g * team, P.neighbours, P);
+  constexpr int U = NG <= 2 ? 4 : NG == 4 ? 2 : 1;             // steps in flight together
   const int64_t units = P.tokens * P.chunks;
   for (int64_t u = (int64_t)blockIdx.x * ROT_WARPS + warp; u < units; u += (int64_t)gridDim.x * ROT_WARPS) {
     const int64_t token = u / P.chunks;
-    const int h0 = (int)(u - token * P.chunks) * P.per * slots;
-    rot_angles(cs, T, P, token, lane);
-    for (int i = 0; i < P.per; ++i) {
-      const int head = h0 + i * slots + slot;
-      const bool live = head < heads;
-      const int sd = head >= P.side[0].heads;
-      const RotSide& S = P.side[sd];
-      const int h = head - (sd ? P.side[0].heads : 0);
-      float v[NG][2 * V];
-      float sum = 0.0f;
+    const int s0 = (int)(u - token * P.chunks) * P.per, s1 = s0 + P.per < steps ? s0 + P.per : steps;
+    for (int i = s0; i < s1; i += U) {
+      float v[U][NG][2];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        RotGroup<V, NEIGH> G(in + g * team, P);
-        if (live) G.load(S.x, xt, token * S.xt + h * S.xh, v[g]);
+      for (int j = 0; j < U; ++j) {
+        const int sd = i + j >= qsteps, h = (i + j - sd * qsteps) * slots + slot;
+        const RotSide& S = P.side[sd];
 #pragma unroll
-        for (int k = 0; k < 2 * V; ++k) {
-          if (!live) v[g][k] = 0.0f;
-          sum = fmaf(v[g][k], v[g][k], sum);
-        }
+        for (int g = 0; g < NG; ++g)
+          G[g].load(S.x, P.x_type, token * S.xt + h * S.xh, i + j < s1 && h < S.heads, v[j][g]);
       }
-      if (P.rms) {
-        sum = team_sum(sum, team);
-        const float r = __frsqrt_rn(fmaf(sum, P.inv_dim, P.eps));
+      if (i == s0) rot_angles(angles[warp], T, P, token, lane);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if (i + j >= s1) break;
+        const int sd = i + j >= qsteps, h = (i + j - sd * qsteps) * slots + slot;
+        const RotSide& S = P.side[sd];
+        float r = 1.0f;
+        if (P.rms) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) sum = fmaf(v[j][g][0], v[j][g][0], fmaf(v[j][g][1], v[j][g][1], sum));
+          r = __frsqrt_rn(fmaf(team_sum(sum, team), P.inv_dim, P.eps));
+        }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          RotGroup<V, NEIGH> G(in + g * team, P);
+          if (P.rms) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (G.has[k]) {
-#pragma unroll
-              for (int j = 0; j < V; ++j) v[g][k * V + j] = v[g][k * V + j] * r * gammas[sd][G.first[k] + j];
-            }
+            for (int k = 0; k < 2; ++k)
+              if (G[g].has[k]) v[j][g][k] = v[j][g][k] * r * gammas[sd][G[g].col[k]];
+          }
+          G[g].turn(G[g].angle(angles[warp]), v[j][g]);
+          if (h < S.heads) G[g].store(S.y, P.y_type, token * S.yt + h * S.yh, v[j][g]);
         }
-      }
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        RotGroup<V, NEIGH> G(in + g * team, P);
-        G.turn(cs, 1.0f, v[g]);
-        if (live) G.store(S.y, yt, token * S.yt + h * S.yh, v[g]);
       }
     }
   }
@@ -238,93 +210,79 @@ __global__ void __launch_bounds__(ROT_THREADS) rotary_kernel(const __grid_consta
 
 // The backward: the cotangent turned back, then the norm's.  A CTA's dgamma
 // sums stay in registers over all its tokens, side after side.
-template <int V, int NG, bool NEIGH, int XT, int CT, int YT>
-__global__ void __launch_bounds__(ROT_THREADS) rotary_backward_kernel(const __grid_constant__ RotParams P, int team) {
+template <int NG>
+__global__ void __launch_bounds__(ROT_THREADS, 2) rotary_any_backward_kernel(const __grid_constant__ RotParams P, int team) {
   __shared__ RotTable T;
   __shared__ float2 angles[ROT_WARPS][ROT_MAX_DIM / 2];
   __shared__ float gammas[2][ROT_MAX_DIM];
   __shared__ float sums[ROT_WARPS][ROT_MAX_DIM];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int xt = XT < 0 ? P.x_type : XT, ct = CT < 0 ? P.ct_type : CT, yt = YT < 0 ? P.y_type : YT;
   rot_table(T, P);
-  for (int i = threadIdx.x; i < 2 * P.dim; i += ROT_THREADS) {
-    const int s = i >= P.dim, c = i - s * P.dim;
-    const void* g = P.side[s].gamma;
-    gammas[s][c] = !g ? 1.0f : P.gamma_type == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)g)[c]) : ((const float*)g)[c];
-  }
-  __syncthreads();
+  rot_scales(gammas, P);
   const int slots = 32 / team, slot = lane / team, in = lane % team;
-  float2* cs = angles[warp];
-  float dg[2][NG][2 * V];
+  RotPair G[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) G[g].place(in + g * team, P.neighbours, P);
+  constexpr int U = NG <= 2 ? 2 : 1;
+  float dg[2][NG][2];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int k = 0; k < 2 * V; ++k) dg[s][g][k] = 0.0f;
+    for (int g = 0; g < NG; ++g) dg[s][g][0] = dg[s][g][1] = 0.0f;
   for (int64_t token = (int64_t)blockIdx.x * ROT_WARPS + warp; token < P.tokens;
        token += (int64_t)gridDim.x * ROT_WARPS) {
-    rot_angles(cs, T, P, token, lane);
+    bool fresh = true;
 #pragma unroll
     for (int sd = 0; sd < 2; ++sd) {
       const RotSide& S = P.side[sd];
-      for (int h0 = 0; h0 < S.heads; h0 += slots) {
-        const int h = h0 + slot;
-        const bool live = h < S.heads;
-        float v[NG][2 * V], x[NG][2 * V];
+      for (int h0 = slot; h0 - slot < S.heads; h0 += slots * U) {
+        float v[U][NG][2], x[U][NG][2];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          RotGroup<V, NEIGH> G(in + g * team, P);
-          if (live) G.load(S.ct, ct, token * S.ct_t + h * S.ct_h, v[g]);
-          if (live && P.rms) G.load(S.x, xt, token * S.xt + h * S.xh, x[g]);
-          if (!live || !P.rms) {
+        for (int j = 0; j < U; ++j) {
+          const int h = h0 + j * slots;
 #pragma unroll
-            for (int k = 0; k < 2 * V; ++k) x[g][k] = 0.0f;
-          }
-          if (!live) {
-#pragma unroll
-            for (int k = 0; k < 2 * V; ++k) v[g][k] = 0.0f;
+          for (int g = 0; g < NG; ++g) {
+            G[g].load(S.ct, P.ct_type, token * S.ct_t + h * S.ct_h, h < S.heads, v[j][g]);
+            G[g].load(S.x, P.x_type, token * S.xt + h * S.xh, P.rms && h < S.heads, x[j][g]);
           }
         }
-        float r = 1.0f, m = 0.0f;
-        if (P.rms) {
-          float sum = 0.0f;
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int k = 0; k < 2 * V; ++k) sum = fmaf(x[g][k], x[g][k], sum);
-          r = __frsqrt_rn(fmaf(team_sum(sum, team), P.inv_dim, P.eps));
+        if (fresh) {
+          fresh = false;
+          rot_angles(angles[warp], T, P, token, lane);
         }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          RotGroup<V, NEIGH> G(in + g * team, P);
-          G.turn(cs, -1.0f, v[g]);
+        for (int j = 0; j < U; ++j) {
+          const int h = h0 + j * slots;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float2 t = G[g].angle(angles[warp]);
+            G[g].turn(make_float2(t.x, -t.y), v[j][g]);
+          }
           if (P.rms) {
+            float sum = 0.0f, m = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              if (G.has[k] && live) {
+            for (int g = 0; g < NG; ++g)
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                  const int e = k * V + j;
-                  x[g][e] *= r;
-                  dg[sd][g][e] = fmaf(v[g][e], x[g][e], dg[sd][g][e]);
-                  v[g][e] *= gammas[sd][G.first[k] + j];
-                  m = fmaf(v[g][e], x[g][e], m);
-                }
+              for (int k = 0; k < 2; ++k) {
+                const float w = G[g].has[k] ? gammas[sd][G[g].col[k]] : 0.0f;
+                sum = fmaf(x[j][g][k], x[j][g][k], sum);
+                m = fmaf(v[j][g][k] * w, x[j][g][k], m);
+              }
+            sum = team_sum(sum, team), m = team_sum(m, team);
+            const float r = __frsqrt_rn(fmaf(sum, P.inv_dim, P.eps));
+            m = m * r * P.inv_dim;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float w = G[g].has[k] ? gammas[sd][G[g].col[k]] : 0.0f, xh = x[j][g][k] * r;
+                if (h < S.heads) dg[sd][g][k] = fmaf(v[j][g][k], xh, dg[sd][g][k]);
+                v[j][g][k] = fmaf(-xh, m, v[j][g][k] * w) * r;
               }
           }
-        }
-        if (P.rms) {
-          m = team_sum(m, team) * P.inv_dim;
 #pragma unroll
           for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int k = 0; k < 2 * V; ++k) v[g][k] = fmaf(-x[g][k], m, v[g][k]) * r;
-        }
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          RotGroup<V, NEIGH> G(in + g * team, P);
-          if (live) G.store(S.y, yt, token * S.yt + h * S.yh, v[g]);
+            if (h < S.heads) G[g].store(S.y, P.y_type, token * S.yt + h * S.yh, v[j][g]);
         }
       }
     }
@@ -336,28 +294,376 @@ __global__ void __launch_bounds__(ROT_THREADS) rotary_backward_kernel(const __gr
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int k = 0; k < 2 * V; ++k)
+      for (int k = 0; k < 2; ++k)
         for (int o = team; o < 32; o <<= 1) dg[sd][g][k] += __shfl_xor_sync(0xFFFFFFFFu, dg[sd][g][k], o);
     __syncthreads();
     if (slot == 0) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        RotGroup<V, NEIGH> G(in + g * team, P);
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          if (G.has[k]) {
+          if (G[g].has[k]) sums[warp][G[g].col[k]] = dg[sd][g][k];
+    }
+    rot_part(sums, sd, P);
+  }
+}
+
+// ------------------------------------- heads of 16-column groups, one type
+//
+// A lane holds eight pairs of a head, its first members as four float2 and
+// its second members as four, for packed arithmetic; memory is accessed 16
+// bytes at a time and pairs that are neighbours come apart as they are widened.
+// Cosines, sines and scales stand in shared memory by pair.  Both kernels walk
+// a token's heads step after step (a step: one head a team) and have the next
+// step's loads under way while one is worked on, across tokens too.
+
+template <int TY>
+struct RotRaw {
+  static constexpr int W = TY == PSK_BF16 ? 8 : 16;
+  uint32_t w[W];
+};
+
+// The eight pairs' members.
+struct Rot8 {
+  float2 a[4], b[4];
+};
+
+struct RotTables {
+  uint64_t turn[ROT_MAX_DIM / 2];                              // as RotTable
+  float bad[ROT_MAX_DIM / 2];
+  float cosine[ROT_WARPS][ROT_MAX_DIM / 2], sine[ROT_WARPS][ROT_MAX_DIM / 2];
+  float gamma[2][2][ROT_MAX_DIM / 2];                          // [side][member][pair]
+};
+
+template <bool NEIGH>
+struct RotLane {
+  int first[2], pair;                      // the columns of the two runs of eight, the first pair
+  bool turns, there;
+  __device__ __forceinline__ RotLane(int g, const RotParams& P) {
+    pair = 8 * g;
+    turns = pair < P.rot / 2;
+    there = 2 * pair < P.dim;
+    if (NEIGH) first[0] = 2 * pair, first[1] = 2 * pair + 8;
+    else if (turns) first[0] = pair, first[1] = pair + P.rot / 2;
+    else first[0] = P.rot / 2 + pair, first[1] = first[0] + (P.dim - P.rot) / 2;
+  }
+  // The column of a member of pair `pair + i`.
+  __device__ __forceinline__ int column(int member, int i) const {
+    return NEIGH ? first[0] + 2 * i + member : first[member] + i;
+  }
+  template <int TY>
+  __device__ __forceinline__ void load(const char* p, bool live, RotRaw<TY>& o) const {
+    constexpr int N = RotRaw<TY>::W / 8;               // 16-byte accesses a run
 #pragma unroll
-            for (int j = 0; j < V; ++j) sums[warp][G.first[k] + j] = dg[sd][g][k * V + j];
-          }
+    for (int i = 0; i < RotRaw<TY>::W; ++i) o.w[i] = 0;
+    if (!live || !there) return;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint4 u = *(const uint4*)(p + (k ? (first[1] - first[0]) * (TY == PSK_BF16 ? 2 : 4) : 0) + 16 * i);
+        uint32_t* w = o.w + (k * N + i) * 4;
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+      }
+  }
+  template <int TY>
+  __device__ __forceinline__ void widen(const RotRaw<TY>& o, Rot8& v) const {
+    // element e of the lane's sixteen, in memory order
+    const auto at = [&](int e) {
+      if constexpr (TY == PSK_BF16) return __uint_as_float(e & 1 ? o.w[e >> 1] & 0xFFFF0000u : o.w[e >> 1] << 16);
+      else return __uint_as_float(o.w[e]);
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v.a[j] = NEIGH ? make_float2(at(4 * j), at(4 * j + 2)) : make_float2(at(2 * j), at(2 * j + 1));
+      v.b[j] = NEIGH ? make_float2(at(4 * j + 1), at(4 * j + 3)) : make_float2(at(8 + 2 * j), at(9 + 2 * j));
+    }
+  }
+  template <int TY>
+  __device__ __forceinline__ void store(char* p, const Rot8& v) const {
+    if (!there) return;
+    float e[16];                                       // in memory order
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      e[NEIGH ? 4 * j : 2 * j] = v.a[j].x, e[NEIGH ? 4 * j + 2 : 2 * j + 1] = v.a[j].y;
+      e[NEIGH ? 4 * j + 1 : 8 + 2 * j] = v.b[j].x, e[NEIGH ? 4 * j + 3 : 9 + 2 * j] = v.b[j].y;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      char* q = p + (k ? (first[1] - first[0]) * (TY == PSK_BF16 ? 2 : 4) : 0);
+      const float* w = e + 8 * k;
+      if constexpr (TY == PSK_BF16) {
+        *(uint4*)q = make_uint4(f32x2_to_bf16x2(w[0], w[1]), f32x2_to_bf16x2(w[2], w[3]), f32x2_to_bf16x2(w[4], w[5]),
+                                f32x2_to_bf16x2(w[6], w[7]));
+      } else {
+        *(float4*)q = make_float4(w[0], w[1], w[2], w[3]);
+        *(float4*)(q + 16) = make_float4(w[4], w[5], w[6], w[7]);
       }
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < P.dim; c += ROT_THREADS) {
-      float s = sums[0][c];
-#pragma unroll
-      for (int w = 1; w < ROT_WARPS; ++w) s += sums[w][c];
-      P.part[((int64_t)blockIdx.x * 2 + sd) * P.dim + c] = s;
+  }
+  // Four float2 of a table by pair.
+  __device__ __forceinline__ void of_pairs(const float* table, float2 (&o)[4]) const {
+    const float4 x = *(const float4*)(table + pair), y = *(const float4*)(table + pair + 4);
+    o[0] = make_float2(x.x, x.y), o[1] = make_float2(x.z, x.w), o[2] = make_float2(y.x, y.y), o[3] = make_float2(y.z, y.w);
+  }
+};
+
+template <bool NEIGH>
+__device__ __forceinline__ void rot_tables(RotTables& T, const RotParams& P) {
+  const int half = P.rot / 2, pairs = P.dim / 2;
+  for (int j = threadIdx.x; j < pairs; j += ROT_THREADS) {
+    if (j < half) {
+      const float f = P.tokens ? P.freqs[j] : 0.0f;
+      T.turn[j] = turn_fraction(f);
+      T.bad[j] = f * 0.0f;
     }
+    for (int w = 0; w < ROT_WARPS; ++w) T.cosine[w][j] = 1.0f, T.sine[w][j] = 0.0f;
+    for (int s = 0; s < 2; ++s)
+      for (int m = 0; m < 2; ++m) {
+        const void* g = P.side[s].gamma;
+        const int rest = j - half, c = j < half ? (NEIGH ? 2 * j + m : j + m * half)
+                                                : (NEIGH ? 2 * j + m : P.rot + rest + m * (pairs - half));
+        T.gamma[s][m][j] = !g ? 1.0f
+                           : P.gamma_type == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)g)[c])
+                                                      : ((const float*)g)[c];
+      }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void rot_angles8(RotTables& T, const RotParams& P, int64_t token, int warp, int lane) {
+  const int64_t pos = P.pos64 ? ((const int64_t*)P.pos)[token] : (int64_t)((const int32_t*)P.pos)[token];
+  __syncwarp();
+  for (int j = lane; j < P.rot / 2; j += 32) {
+    const int64_t frac = (int64_t)((uint64_t)pos * T.turn[j]);
+    float s, c;
+    sincospif(__ll2float_rn(frac) * 1.0842021724855044e-19f, &s, &c);     // 2 turns 2^-64
+    T.cosine[warp][j] = c + T.bad[j], T.sine[warp][j] = s + T.bad[j];
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+
+// A lane's way through one side's heads in one tensor: where its columns begin
+// in its first head of token 0, and the bytes to the next token and step.
+struct RotWalk {
+  const char* base;
+  int64_t token, step;
+  __device__ __forceinline__ RotWalk(const void* p, int64_t ts, int64_t hs, int slot, int slots, int column, int size)
+      : base((const char*)p + (slot * hs + column) * size), token(ts * size), step(slots * hs * size) {}
+  __device__ __forceinline__ const char* at(int64_t t, int i) const { return base + t * token + i * step; }
+};
+
+// 1 / sqrt to 2^-22.9.
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float y;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The scale is folded into a token's cosines and sines, once for all its
+// heads, so a head's pass is a sum of squares, y = r (x p + x' q) with x' the
+// pair's other member, and its loads and stores.
+template <bool NEIGH, int TY>
+__global__ void __launch_bounds__(ROT_THREADS, ROT_FWD_CTAS) rotary_kernel(const __grid_constant__ RotParams P, int team) {
+  __shared__ __align__(16) RotTables T;
+  constexpr int SIZE = TY == PSK_BF16 ? 2 : 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slots = 32 / team, slot = lane / team;
+  const RotLane<NEIGH> G(lane % team, P);
+  // steps of both sides, and those in which this lane's team has a head
+  const int nq = (P.side[0].heads + slots - 1) / slots, nk = (P.side[1].heads + slots - 1) / slots;
+  const int lq = (P.side[0].heads - slot + slots - 1) / slots, lk = (P.side[1].heads - slot + slots - 1) / slots;
+  const int64_t jump = (int64_t)gridDim.x * ROT_WARPS, units = P.tokens * P.chunks;
+  RotRaw<TY> raw;
+  const auto walk = [&](int sd, bool y) {
+    const RotSide& S = P.side[sd];
+    return y ? RotWalk(S.y, S.yt, S.yh, slot, slots, G.first[0], SIZE) : RotWalk(S.x, S.xt, S.xh, slot, slots, G.first[0], SIZE);
+  };
+  // The first step of a unit: a token's steps [s0, s0 + per) of both sides, queries first.
+  const auto first = [&](int64_t token, int s0) {
+    if (s0 < nq) G.load(walk(0, false).at(token, s0), s0 < lq, raw);
+    else G.load(walk(1, false).at(token, s0 - nq), s0 - nq < lk, raw);
+  };
+  int64_t u = (int64_t)blockIdx.x * ROT_WARPS + warp;
+  int64_t token = P.chunks == 1 ? u : u / P.chunks;
+  int s0 = (int)(u - token * P.chunks) * P.per;
+  if (u < units) first(token, s0);
+  rot_tables<NEIGH>(T, P);
+  while (u < units) {
+    const int s1 = s0 + P.per < nq + nk ? s0 + P.per : nq + nk;
+    const int64_t next = u + jump, next_token = P.chunks == 1 ? next : next / P.chunks;
+    const int next_s0 = (int)(next - next_token * P.chunks) * P.per;
+    rot_angles8(T, P, token, warp, lane);
+    const auto side = [&](auto SD) {
+      constexpr int sd = SD.value;
+      const int from = sd ? (s0 > nq ? s0 - nq : 0) : s0, to = sd ? s1 - nq : (s1 < nq ? s1 : nq);
+      if (from >= to) return;
+      float2 pa[4], qa[4], pb[4], qb[4];
+      {
+        float2 c[4], s[4], ga[4], gb[4];
+        G.of_pairs(T.cosine[warp], c), G.of_pairs(T.sine[warp], s);
+        G.of_pairs(T.gamma[sd][0], ga), G.of_pairs(T.gamma[sd][1], gb);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          pa[j] = __fmul2_rn(ga[j], c[j]), pb[j] = __fmul2_rn(gb[j], c[j]);
+          qa[j] = __fmul2_rn(gb[j], make_float2(-s[j].x, -s[j].y)), qb[j] = __fmul2_rn(ga[j], s[j]);
+        }
+      }
+      const RotWalk X = walk(sd, false), Y = walk(sd, true);
+      const char* px = X.at(token, from);
+      char* py = (char*)Y.at(token, from);
+      const int mine = sd ? lk : lq;
+      for (int i = from; i < to; ++i) {
+        Rot8 v;
+        G.widen(raw, v);
+        if (i + 1 < to) {
+          px += X.step;
+          G.load(px, i + 1 < mine, raw);
+        } else if (sd == 0 && s1 > nq) {
+          G.load(walk(1, false).at(token, 0), 0 < lk, raw);
+        } else if (next < units) {
+          first(next_token, next_s0);
+        }
+        float2 r = splat(1.0f);
+        if (P.rms) {
+          float2 sum = splat(0.0f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum = __ffma2_rn(v.a[j], v.a[j], __ffma2_rn(v.b[j], v.b[j], sum));
+          r = splat(rsqrt_approx(fmaf(team_sum(sum.x + sum.y, team), P.inv_dim, P.eps)));
+        }
+        Rot8 y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 a = __fmul2_rn(v.a[j], r), b = __fmul2_rn(v.b[j], r);
+          y.a[j] = __fmul2_rn(a, pa[j]), y.b[j] = __fmul2_rn(b, pb[j]);
+          if (G.turns) y.a[j] = __ffma2_rn(b, qa[j], y.a[j]), y.b[j] = __ffma2_rn(a, qb[j], y.b[j]);
+        }
+        if (i < mine) G.template store<TY>(py, y);
+        py += Y.step;
+      }
+    };
+    side(std::integral_constant<int, 0>{});
+    side(std::integral_constant<int, 1>{});
+    u = next, token = next_token, s0 = next_s0;
+  }
+}
+
+template <bool NEIGH, int TY>
+__global__ void __launch_bounds__(ROT_THREADS, ROT_BWD_CTAS) rotary_backward_kernel(const __grid_constant__ RotParams P, int team) {
+  __shared__ __align__(16) RotTables T;
+  __shared__ float sums[ROT_WARPS][ROT_MAX_DIM];
+  constexpr int SIZE = TY == PSK_BF16 ? 2 : 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slots = 32 / team, slot = lane / team;
+  const RotLane<NEIGH> G(lane % team, P);
+  const int nq = (P.side[0].heads + slots - 1) / slots, nk = (P.side[1].heads + slots - 1) / slots;
+  const int lq = (P.side[0].heads - slot + slots - 1) / slots, lk = (P.side[1].heads - slot + slots - 1) / slots;
+  const int64_t jump = (int64_t)gridDim.x * ROT_WARPS;
+  int64_t token = (int64_t)blockIdx.x * ROT_WARPS + warp;
+  Rot8 dg[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dg[0].a[j] = dg[0].b[j] = dg[1].a[j] = dg[1].b[j] = splat(0.0f);
+  RotRaw<TY> craw, xraw;
+  const auto walk = [&](int sd, int which) {
+    const RotSide& S = P.side[sd];
+    if (which == 0) return RotWalk(S.ct, S.ct_t, S.ct_h, slot, slots, G.first[0], SIZE);
+    if (which == 1) return RotWalk(S.x, S.xt, S.xh, slot, slots, G.first[0], SIZE);
+    return RotWalk(S.y, S.yt, S.yh, slot, slots, G.first[0], SIZE);
+  };
+  const auto first = [&](int sd, int64_t t) {
+    G.load(walk(sd, 0).at(t, 0), 0 < (sd ? lk : lq), craw);
+    G.load(walk(sd, 1).at(t, 0), P.rms && 0 < (sd ? lk : lq), xraw);
+  };
+  if (token < P.tokens) {
+    if (nq) first(0, token);
+    else first(1, token);
+  }
+  rot_tables<NEIGH>(T, P);
+  for (; token < P.tokens; token += jump) {
+    rot_angles8(T, P, token, warp, lane);
+    float2 c[4], s[4];
+    G.of_pairs(T.cosine[warp], c), G.of_pairs(T.sine[warp], s);
+    const auto side = [&](auto SD) {
+      constexpr int sd = SD.value;
+      const int n = sd ? nk : nq, mine = sd ? lk : lq;
+      if (!n) return;
+      const RotWalk C = walk(sd, 0), X = walk(sd, 1), Y = walk(sd, 2);
+      const char *pc = C.at(token, 0), *px = X.at(token, 0);
+      char* py = (char*)Y.at(token, 0);
+      for (int i = 0; i < n; ++i) {
+        Rot8 v, x;
+        G.widen(craw, v), G.widen(xraw, x);
+        // the next step's, the other side's first, or the next token's
+        if (i + 1 < n) {
+          pc += C.step, px += X.step;
+          G.load(pc, i + 1 < mine, craw);
+          G.load(px, P.rms && i + 1 < mine, xraw);
+        } else if (sd == 0 && nk) {
+          first(1, token);
+        } else if (token + jump < P.tokens) {
+          if (nq) first(0, token + jump);
+          else first(1, token + jump);
+        }
+        if (G.turns) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 a = v.a[j], b = v.b[j];
+            v.a[j] = __ffma2_rn(a, c[j], __fmul2_rn(b, s[j]));
+            v.b[j] = __ffma2_rn(b, c[j], __fmul2_rn(a, make_float2(-s[j].x, -s[j].y)));
+          }
+        }
+        if (P.rms) {
+          float2 ga[4], gb[4], sum = splat(0.0f), m = splat(0.0f);
+          G.of_pairs(T.gamma[sd][0], ga), G.of_pairs(T.gamma[sd][1], gb);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            ga[j] = __fmul2_rn(v.a[j], ga[j]), gb[j] = __fmul2_rn(v.b[j], gb[j]);
+            sum = __ffma2_rn(x.a[j], x.a[j], __ffma2_rn(x.b[j], x.b[j], sum));
+            m = __ffma2_rn(ga[j], x.a[j], __ffma2_rn(gb[j], x.b[j], m));
+          }
+          float s1 = sum.x + sum.y, s2 = m.x + m.y;
+          for (int o = team >> 1; o > 0; o >>= 1) {
+            s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+            s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
+          }
+          const float r = rsqrt_approx(fmaf(s1, P.inv_dim, P.eps));
+          const float2 r2 = splat(r), mean = splat(-(s2 * r * P.inv_dim));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 xa = __fmul2_rn(x.a[j], r2), xb = __fmul2_rn(x.b[j], r2);
+            if (i < mine) {
+              dg[sd].a[j] = __ffma2_rn(v.a[j], xa, dg[sd].a[j]);
+              dg[sd].b[j] = __ffma2_rn(v.b[j], xb, dg[sd].b[j]);
+            }
+            v.a[j] = __fmul2_rn(__ffma2_rn(xa, mean, ga[j]), r2);
+            v.b[j] = __fmul2_rn(__ffma2_rn(xb, mean, gb[j]), r2);
+          }
+        }
+        if (i < mine) G.template store<TY>(py, v);
+        py += Y.step;
+      }
+    };
+    side(std::integral_constant<int, 0>{});
+    side(std::integral_constant<int, 1>{});
+  }
+  if (!P.part) return;
+#pragma unroll
+  for (int sd = 0; sd < 2; ++sd) {
+    // teams of a warp joined by shuffles, warps through shared memory
+    const auto join = [&](float v) {
+      for (int o = team; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      return v;
+    };
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 da = dg[sd].a[i >> 1], db = dg[sd].b[i >> 1];
+      const float a = join(i & 1 ? da.y : da.x), b = join(i & 1 ? db.y : db.x);
+      if (slot == 0 && G.there) sums[warp][G.column(0, i)] = a, sums[warp][G.column(1, i)] = b;
+    }
+    rot_part(sums, sd, P);
   }
 }
 
@@ -462,18 +768,23 @@ static int rot_check_common(int64_t tokens, const void* pos, int32_t pt, const f
 
 static bool rot_vec(int64_t dim, int64_t rot) { return dim % 16 == 0 && rot % 16 == 0; }
 
+// Lanes of a team (a power of two): one for each group of V pairs, a warp at most.
+static int rot_team(const RotParams& P, int V) {
+  const int pairs = P.rot / 2 + (P.dim - P.rot + 1) / 2, groups = (pairs + V - 1) / V;
+  int t = 1;
+  while (t < 32 && t < groups) t *= 2;
+  return t;
+}
+
+// Pairs a lane of the general kernels.
 template <typename F>
-static int rot_shape(const RotParams& P, bool vec, F&& f) {
+static int rot_pairs(const RotParams& P, F&& f) {
   const int pairs = P.rot / 2 + (P.dim - P.rot + 1) / 2;
-  const auto with_pairs = [&](auto V, auto NG) {
-    return with_bool(P.neighbours != 0, [&](auto N) { return f(V, NG, N); });
-  };
   using std::integral_constant;
-  if (vec) return with_pairs(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-  if (pairs <= 32) return with_pairs(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  if (pairs <= 64) return with_pairs(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  if (pairs <= 128) return with_pairs(integral_constant<int, 1>{}, integral_constant<int, 4>{});
-  return with_pairs(integral_constant<int, 1>{}, integral_constant<int, 8>{});
+  if (pairs <= 32) return f(integral_constant<int, 1>{});
+  if (pairs <= 64) return f(integral_constant<int, 2>{});
+  if (pairs <= 128) return f(integral_constant<int, 4>{});
+  return f(integral_constant<int, 8>{});
 }
 
 }  // namespace psk
@@ -518,24 +829,30 @@ extern "C" int psk_qk_norm_rotary(const void* q, const void* k, int32_t xt, int6
   P.eps = (float)eps, P.inv_dim = 1.0f / (float)dim;
   const bool vec = rot_vec(dim, rot) && heads_vec(in[0]) && heads_vec(in[1]) && heads_vec(out[0]) && heads_vec(out[1]);
   cudaStream_t s = (cudaStream_t)stream;
-  return rot_shape(P, vec, [&](auto V, auto NG, auto N) {
-    const int team = rot_team<V.value>(P), slots = 32 / team;
-    const int64_t steps = (hq + hk + slots - 1) / slots, warps = (int64_t)device_sm_count() * 8 * ROT_WARPS;
-    // A token's heads go to one warp where tokens alone fill the GPU, else to several.
-    int64_t chunks = tokens >= warps ? 1 : (warps + tokens - 1) / tokens;
-    if (chunks > steps) chunks = steps;
-    P.per = (int32_t)((steps + chunks - 1) / chunks);
-    P.chunks = (int32_t)((steps + P.per - 1) / P.per);
-    const int64_t ctas = (tokens * P.chunks + ROT_WARPS - 1) / ROT_WARPS, most = (int64_t)device_sm_count() * 8;
-    const unsigned grid = (unsigned)(ctas < most ? ctas : most);
-    if (V.value == 8 && xt == yt)
-      with_dtype(xt, [&](auto TY) {
-        rotary_kernel<V.value, NG.value, N.value, TY.value, TY.value><<<grid, ROT_THREADS, 0, s>>>(P, team);
+  const bool fast = vec && xt == yt;
+  const int team = rot_team(P, fast ? 8 : 1), slots = 32 / team, per_sm = fast ? ROT_FWD_CTAS : 3;
+  const int64_t steps = (hq + slots - 1) / slots + (hk + slots - 1) / slots;
+  const int64_t most = (int64_t)device_sm_count() * per_sm, warps = most * ROT_WARPS;
+  // A token's heads go to one warp where tokens alone fill the GPU, else to several.
+  int64_t chunks = tokens >= warps ? 1 : (warps + tokens - 1) / tokens;
+  if (chunks > steps) chunks = steps;
+  P.per = (int32_t)((steps + chunks - 1) / chunks);
+  P.chunks = (int32_t)((steps + P.per - 1) / P.per);
+  const int64_t ctas = (tokens * P.chunks + ROT_WARPS - 1) / ROT_WARPS;
+  const unsigned grid = (unsigned)(ctas < most ? ctas : most);
+  if (fast)
+    with_dtype(xt, [&](auto TY) {
+      return with_bool(P.neighbours != 0, [&](auto N) {
+        rotary_kernel<N.value, TY.value><<<grid, ROT_THREADS, 0, s>>>(P, team);
         return 0;
       });
-    else rotary_kernel<V.value, NG.value, N.value, -1, -1><<<grid, ROT_THREADS, 0, s>>>(P, team);
-    return check_launch("rotary kernel");
-  });
+    });
+  else
+    rot_pairs(P, [&](auto NG) {
+      rotary_any_kernel<NG.value><<<grid, ROT_THREADS, 0, s>>>(P, team);
+      return 0;
+    });
+  return check_launch("rotary kernel");
 }
 
 extern "C" int psk_qk_norm_rotary_backward_workspace(int64_t tokens, int64_t hq, int64_t hk, int64_t dim,
@@ -621,18 +938,24 @@ extern "C" int psk_qk_norm_rotary_backward(
   const bool vec = rot_vec(dim, rot) && heads_vec(cts[0]) && heads_vec(cts[1]) && heads_vec(out[0]) &&
                    heads_vec(out[1]) && (!rms || (heads_vec(xs[0]) && heads_vec(xs[1])));
   cudaStream_t s = (cudaStream_t)stream;
-  rc = rot_shape(P, vec, [&](auto V, auto NG, auto N) {
-    const int team = rot_team<V.value>(P);
-    const unsigned grid = (unsigned)P.blocks;
-    if (V.value == 8 && ct == dt && (!rms || xt == ct))
-      with_dtype(ct, [&](auto TY) {
-        rotary_backward_kernel<V.value, NG.value, N.value, TY.value, TY.value, TY.value>
-            <<<grid, ROT_THREADS, 0, s>>>(P, team);
+  const bool fast = vec && ct == dt && (!rms || xt == ct);
+  const int team = rot_team(P, fast ? 8 : 1);
+  const int64_t most = (int64_t)device_sm_count() * (fast ? ROT_BWD_CTAS : 2);
+  if (P.blocks > most) P.blocks = (int32_t)most;
+  const unsigned grid = (unsigned)P.blocks;
+  if (fast)
+    with_dtype(ct, [&](auto TY) {
+      return with_bool(P.neighbours != 0, [&](auto N) {
+        rotary_backward_kernel<N.value, TY.value><<<grid, ROT_THREADS, 0, s>>>(P, team);
         return 0;
       });
-    else rotary_backward_kernel<V.value, NG.value, N.value, -1, -1, -1><<<grid, ROT_THREADS, 0, s>>>(P, team);
-    return check_launch("rotary backward kernel");
-  });
+    });
+  else
+    rot_pairs(P, [&](auto NG) {
+      rotary_any_backward_kernel<NG.value><<<grid, ROT_THREADS, 0, s>>>(P, team);
+      return 0;
+    });
+  rc = check_launch("rotary backward kernel");
   if (rc || !sums) return rc;
   rotary_join_kernel<<<dim3((unsigned)((dim + 31) / 32), 2), 1024, 0, s>>>(P);
   return check_launch("rotary join kernel");
