@@ -20,24 +20,29 @@ constexpr int64_t LINEAR_MAX_SUM = 1LL << 25;      // of a product: a tile's tim
 constexpr int64_t LINEAR_MAX_SIDE = (1LL << 31) - 1024;
 constexpr int PACK_THREADS = 256;
 
-struct PackParams {
+struct PackJob {
   const void *x, *z;            // z: the value is x slope(z)
   uint16_t* to;                 // planes of prows x pcols (NULL: column sums alone)
   float* sums;                  // column sums of `blocks` blocks of rows (NULL: not wanted)
   int64_t rows, cols, ldx, ldz, prows, pcols, plane_stride;
-  int32_t planes, blocks;
+  int32_t planes, blocks, xt, vec;
+};
+
+// Up to three operands in one launch; job j has the CTAs from first[j] on.
+struct PackParams {
+  PackJob job[3];
+  int32_t first[3], jobs;
 };
 
 // Eight columns a thread, 256 a CTA, its warps the rows of a block in turn,
 // two rows on their way at once.  VEC: 16-byte accesses, the columns
 // neighbours; else every 32nd, so that lanes read neighbours.
 template <int XT, int ZT, int ACT, bool VEC>
-__global__ void __launch_bounds__(PACK_THREADS, 3) linear_pack_kernel(const __grid_constant__ PackParams P) {
-  __shared__ float part[8][256];
+__device__ __forceinline__ void pack_job(const PackJob& P, int64_t cta, float (&part)[8][256]) {
   constexpr int R = 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t groups = (P.pcols + 255) / 256;
-  const int64_t cb = blockIdx.x % groups, rb = blockIdx.x / groups;
+  const int64_t cb = cta % groups, rb = cta / groups;
   // The span that is written, padding among it, and the part of it that is read.
   const Columns<VEC, 8> wide(cb * 256, 32, lane, P.pcols), cols(cb * 256, 32, lane, P.cols);
   const int64_t each = (P.prows + P.blocks - 1) / P.blocks;
@@ -112,7 +117,29 @@ __global__ void __launch_bounds__(PACK_THREADS, 3) linear_pack_kernel(const __gr
   if (c < P.cols) P.sums[rb * P.cols + c] = sum;
 }
 
-// dbias from the row blocks' sums: 32 columns a CTA, 8 warps the blocks in turn.
+// The first job's types are the kernel's; the others have no activation and
+// no sums.
+template <int XT, int ZT, int ACT, bool VEC>
+__global__ void __launch_bounds__(PACK_THREADS, 3) linear_pack_kernel(const __grid_constant__ PackParams P) {
+  __shared__ float part[8][256];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int cta = (int)blockIdx.x;
+  if (P.jobs == 1 || cta < P.first[1]) {
+    pack_job<XT, ZT, ACT, VEC>(P.job[0], cta, part);
+    return;
+  }
+  const int j = P.jobs == 3 && cta >= P.first[2] ? 2 : 1;
+  const PackJob& J = P.job[j];
+  if (J.xt == PSK_BF16) {
+    if (J.vec) pack_job<PSK_BF16, PSK_BF16, ACT_NONE, true>(J, cta - P.first[j], part);
+    else pack_job<PSK_BF16, PSK_BF16, ACT_NONE, false>(J, cta - P.first[j], part);
+  } else {
+    if (J.vec) pack_job<PSK_F32, PSK_BF16, ACT_NONE, true>(J, cta - P.first[j], part);
+    else pack_job<PSK_F32, PSK_BF16, ACT_NONE, false>(J, cta - P.first[j], part);
+  }
+}
+
+// dbias from the row blocks' sums where no product is launched: 32 columns a CTA, 8 warps the blocks in turn.
 __global__ void __launch_bounds__(256) linear_bias_kernel(const float* sums, int blocks, int64_t cols, void* out,
                                                           int32_t dt, int32_t add) {
   __shared__ float part[8][32];
@@ -182,36 +209,48 @@ static int pack_blocks(int64_t rows, int64_t cols) {
   return (int)(b < 1 ? 1 : b);
 }
 
-static int pack(const Matrix& m, void* workspace, const void* z, int32_t zt, int64_t ldz, int32_t act, bool store,
-                float* sums, cudaStream_t s) {
+// The operands to be packed, in one launch.
+struct Packing {
   PackParams P{};
-  P.x = m.p, P.z = z;
-  P.to = store ? (uint16_t*)((char*)workspace + m.offset) : nullptr;
-  P.sums = sums;
-  P.rows = m.rows, P.cols = m.cols, P.ldx = m.ld, P.ldz = ldz;
-  P.prows = m.prows, P.pcols = m.pcols, P.plane_stride = m.prows * m.pcols;
-  P.planes = m.planes;
-  const bool vec = m.cols % 8 == 0 && rows_vec8(m.p, m.dt, m.ld, m.rows) && (!act || rows_vec8(z, zt, ldz, m.rows));
-  P.blocks = pack_blocks(m.prows, m.pcols);
-  const int64_t ctas = (m.pcols + 255) / 256 * P.blocks;
-  if (ctas > 0x7FFFFFFF) return fail(PSK_E_SHAPE, "too many blocks");
-  const unsigned grid = (unsigned)ctas;
-  with_dtype(m.dt, [&](auto XT) {
-    return with_bool(vec, [&](auto VEC) {
-      if (act == ACT_NONE) {
-        linear_pack_kernel<XT.value, PSK_BF16, ACT_NONE, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
-        return 0;
-      }
-      return with_dtype(zt, [&](auto ZT) {
-        if (act == ACT_RELU) linear_pack_kernel<XT.value, ZT.value, ACT_RELU, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
-        else if (act == ACT_GELU) linear_pack_kernel<XT.value, ZT.value, ACT_GELU, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
-        else linear_pack_kernel<XT.value, ZT.value, ACT_SILU, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
-        return 0;
+  int64_t ctas = 0;
+  int32_t act = ACT_NONE, zt = PSK_BF16;
+  // The first one may have an activation's slope and column sums.
+  void add(const Matrix& m, void* workspace, bool store = true, const void* z = nullptr, int32_t z_type = PSK_BF16,
+           int64_t ldz = 0, int32_t slope = ACT_NONE, float* sums = nullptr) {
+    PackJob& J = P.job[P.jobs];
+    J.x = m.p, J.z = z;
+    J.to = store ? (uint16_t*)((char*)workspace + m.offset) : nullptr;
+    J.sums = sums;
+    J.rows = m.rows, J.cols = m.cols, J.ldx = m.ld, J.ldz = ldz;
+    J.prows = m.prows, J.pcols = m.pcols, J.plane_stride = m.prows * m.pcols;
+    J.planes = m.planes, J.xt = m.dt;
+    J.vec = m.cols % 8 == 0 && rows_vec8(m.p, m.dt, m.ld, m.rows) && (!slope || rows_vec8(z, z_type, ldz, m.rows));
+    J.blocks = pack_blocks(m.prows, m.pcols);
+    if (!P.jobs) act = slope, zt = z_type;
+    P.first[P.jobs++] = (int32_t)(ctas < 0x7FFFFFFF ? ctas : 0x7FFFFFFF);
+    ctas += (m.pcols + 255) / 256 * J.blocks;
+  }
+  int launch(cudaStream_t s) const {
+    if (!P.jobs) return PSK_OK;
+    if (ctas > 0x7FFFFFFF) return fail(PSK_E_SHAPE, "too many blocks");
+    const unsigned grid = (unsigned)ctas;
+    with_dtype(P.job[0].xt, [&](auto XT) {
+      return with_bool(P.job[0].vec != 0, [&](auto VEC) {
+        if (act == ACT_NONE) {
+          linear_pack_kernel<XT.value, PSK_BF16, ACT_NONE, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
+          return 0;
+        }
+        return with_dtype(zt, [&](auto ZT) {
+          if (act == ACT_RELU) linear_pack_kernel<XT.value, ZT.value, ACT_RELU, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
+          else if (act == ACT_GELU) linear_pack_kernel<XT.value, ZT.value, ACT_GELU, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
+          else linear_pack_kernel<XT.value, ZT.value, ACT_SILU, VEC.value><<<grid, PACK_THREADS, 0, s>>>(P);
+          return 0;
+        });
       });
     });
-  });
-  return check_launch("linear pack kernel");
-}
+    return check_launch("linear pack kernel");
+  }
+};
 
 // The products of the operands' planes, smallest first.
 static void plane_pairs(MMCall& C) {
@@ -336,8 +375,10 @@ extern "C" int psk_linear(const void* x, int32_t xt, int64_t ldx, const void* w,
   if (!rc && views_overlap(vws, vr)) rc = fail(PSK_E_ALIAS, "the workspace overlaps the residual");
   if (rc) return rc;
   cudaStream_t s = (cudaStream_t)stream;
-  if (mx.packed) rc = pack(mx, workspace, nullptr, 0, 0, 0, true, nullptr, s);
-  if (!rc && mw.packed) rc = pack(mw, workspace, nullptr, 0, 0, 0, true, nullptr, s);
+  Packing K;
+  if (mx.packed) K.add(mx, workspace);
+  if (mw.packed) K.add(mw, workspace);
+  rc = K.launch(s);
   if (rc) return rc;
   MMCall C{};
   C.m = rows, C.n = out, C.k = in ? in : 1, C.matrices = 1;
@@ -349,7 +390,7 @@ extern "C" int psk_linear(const void* x, int32_t xt, int64_t ldx, const void* w,
   E.res = residual, E.rt = rt, E.ldr = ldr;
   E.z = z, E.zt = zt, E.ldz = ldz;
   E.y = y, E.yt = yt, E.ldy = ldy;
-  return mm_launch(C, s);
+  return mm_launch(&C, 1, nullptr, s);
 }
 
 namespace psk {
@@ -467,41 +508,39 @@ extern "C" int psk_linear_backward(const void* ct, int32_t ct_t, int64_t ldc, co
   cudaStream_t s = (cudaStream_t)stream;
   const bool products = B.want_dx || B.want_dw;
   float* sums = B.want_db ? (float*)((char*)workspace + B.sums) : nullptr;
-  if (B.want_db || (products && !B.direct)) {
-    rc = pack(B.dz, workspace, z, zt, ldz, act, products && !B.direct, sums, s);
-    if (rc) return rc;
-  }
-  if (B.want_db) {
+  Packing K;
+  if (B.want_db || (products && !B.direct)) K.add(B.dz, workspace, products && !B.direct, z, zt, ldz, act, sums);
+  if (B.want_dx && B.w.packed) K.add(B.w, workspace);
+  if (B.want_dw && B.x.packed) K.add(B.x, workspace);
+  rc = K.launch(s);
+  if (rc) return rc;
+  if (B.want_db && !products) {
     linear_bias_kernel<<<(unsigned)((out + 31) / 32), 256, 0, s>>>(sums, B.blocks, out, dbias, dbt, accumulate != 0);
-    rc = check_launch("linear bias kernel");
-    if (rc) return rc;
+    return check_launch("linear bias kernel");
   }
+  if (!products) return PSK_OK;
+  MMCall C[2] = {};
+  int count = 0;
   if (B.want_dx) {
-    if (B.w.packed) rc = pack(B.w, workspace, nullptr, 0, 0, 0, true, nullptr, s);
-    if (rc) return rc;
-    MMCall C{};
-    C.m = rows, C.n = in, C.k = out ? out : 1, C.matrices = 1;
-    C.a = operand(B.dz, workspace, true);
-    C.a.planes = B.dx_planes;
-    C.b = operand(B.w, workspace, layout == PSK_W_IN_OUT);
-    plane_pairs(C);
-    C.e.y = dx, C.e.yt = dxt, C.e.ldy = lddx;
-    rc = mm_launch(C, s);
-    if (rc) return rc;
+    MMCall& D = C[count++];
+    D.m = rows, D.n = in, D.k = out ? out : 1, D.matrices = 1;
+    D.a = operand(B.dz, workspace, true);
+    D.a.planes = B.dx_planes;
+    D.b = operand(B.w, workspace, layout == PSK_W_IN_OUT);
+    plane_pairs(D);
+    D.e.y = dx, D.e.yt = dxt, D.e.ldy = lddx;
   }
   if (B.want_dw) {
-    if (B.x.packed) rc = pack(B.x, workspace, nullptr, 0, 0, 0, true, nullptr, s);
-    if (rc) return rc;
-    MMCall C{};
+    MMCall& D = C[count++];
     MMOperand ox = operand(B.x, workspace, false), oz = operand(B.dz, workspace, false);
     oz.planes = B.dw_planes;
-    C.m = wrows, C.n = wcols, C.k = rows ? rows : 1, C.matrices = 1;
-    C.a = layout == PSK_W_IN_OUT ? ox : oz;
-    C.b = layout == PSK_W_IN_OUT ? oz : ox;
-    plane_pairs(C);
-    C.e.y = dw, C.e.yt = dwt, C.e.ldy = lddw;
-    if (accumulate) C.e.res = dw, C.e.rt = dwt, C.e.ldr = lddw;
-    rc = mm_launch(C, s);
+    D.m = wrows, D.n = wcols, D.k = rows ? rows : 1, D.matrices = 1;
+    D.a = layout == PSK_W_IN_OUT ? ox : oz;
+    D.b = layout == PSK_W_IN_OUT ? oz : ox;
+    plane_pairs(D);
+    D.e.y = dw, D.e.yt = dwt, D.e.ldy = lddw;
+    if (accumulate) D.e.res = dw, D.e.rt = dwt, D.e.ldr = lddw;
   }
-  return rc;
+  const MMColumnSums J{sums, dbias, out, B.blocks, dbt, accumulate != 0};
+  return mm_launch(C, count, B.want_db ? &J : nullptr, s);
 }

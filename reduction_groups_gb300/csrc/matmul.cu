@@ -41,17 +41,23 @@ struct MMWarps {
 constexpr int MM_BK = 64;                  // summed elements a stage: one 128-byte swizzled row
 constexpr int MM_A_BYTES = 128 * MM_BK * 2;
 
-struct MMParams {
+struct MMProblem {
   CUtensorMap ta, tb;
   MMEpilogue e;
   int64_t m, n;
-  int32_t kblocks, pairs, matrices;
-  int32_t planes_a, planes_b;
-  int32_t a_k, b_k, f16;
-  int32_t tiles_m, tiles_n, tiles, symmetric;
+  int32_t kblocks, pairs, planes_a, planes_b;
   int32_t chunk;                           // blocks of the summed axis that one accumulator takes
-  int32_t na, nb, stages;                  // planes of A and B in a stage (one each but with SUM), stages of the ring
+  int32_t na, nb;                          // planes of A and B in a stage (one each but with SUM)
+  int32_t a_k, b_k, tiles_m, tiles_n, tiles, symmetric;      // tiles: of one matrix
   uint8_t pa[8], pb[8];
+};
+
+// One launch: one product or two, the second's tiles after the first's.
+struct MMParams {
+  MMProblem q[2];
+  int32_t split, total;                    // tiles of the first, of both
+  int32_t f16, stages, slot_bytes;         // of the ring
+  MMColumnSums sums;
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -177,7 +183,7 @@ struct Tile {
 // walk through the columns together, so that the tiles running at one time
 // share operand rows in L2.  Symmetric: the lower triangle, row after row.
 template <int Q>
-__device__ __forceinline__ Tile tile_at(const MMParams& P, int32_t t) {
+__device__ __forceinline__ Tile tile_at(const MMProblem& P, int32_t t) {
   Tile o;
   const int32_t per = P.tiles;
   o.matrix = t / per;
@@ -273,13 +279,36 @@ __device__ __forceinline__ void act_rt(float* v, int32_t act) {
   }
 }
 
+// Eight elements `step` bytes apart, those below n.
+template <int DT>
+__device__ __forceinline__ void gather8(const char* p, int64_t step, int n, float* v) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k, p += step) {
+    v[k] = 0.0f;
+    if (k < n) v[k] = DT == PSK_BF16 ? bf16_bits_to_f32(*(const uint16_t*)p) : *(const float*)p;
+  }
+}
+template <int DT>
+__device__ __forceinline__ void scatter8(char* p, int64_t step, int n, const float* v) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k, p += step)
+    if (k < n) {
+      if (DT == PSK_BF16) *(uint16_t*)p = f32_to_bf16_bits(v[k]);
+      else *(float*)p = v[k];
+    }
+}
+__device__ __forceinline__ void scatter8_rt(void* p, int32_t dt, int64_t i, int64_t ld, int n, const float* v) {
+  if (dt == PSK_BF16) scatter8<PSK_BF16>((char*)p + 2 * i, 4 * ld, n, v);
+  else scatter8<PSK_F32>((char*)p + 4 * i, 8 * ld, n, v);
+}
+
 // Sixteen columns of a warp's 32 rows, of any types and strides: turned
 // through shared memory, so that lanes hold neighbouring columns (two rows at
-// a time) and what they load and store is coalesced wherever rows begin.  Kept
-// short and rolled up: a small call runs it once, and code that is not in the
-// instruction cache costs more than it computes (unrolled throughout, a tile
-// of [1003, 771] x [771, 1501] f32 spent 10 us in here, of 27).
-__device__ __forceinline__ void linear_any16(const MMParams& P, int64_t row0, int64_t c0, int lane, float* stage,
+// a time) and what they load and store is coalesced wherever rows begin.  Few
+// instructions: in a small call a warp is alone on its scheduler, each costs
+// its latency (unrolled throughout and with types and bounds looked up for
+// every element, a tile of [1003, 771] x [771, 1501] f32 spent 10 us here).
+__device__ __forceinline__ void linear_any16(const MMProblem& P, int64_t row0, int64_t c0, int lane, float* stage,
                                              const float* v) {
   const MMEpilogue& E = P.e;
   __syncwarp();
@@ -289,25 +318,25 @@ __device__ __forceinline__ void linear_any16(const MMParams& P, int64_t row0, in
   const int64_t c = c0 + (lane & 15);
   if (c >= P.n) return;
   const float bias = E.bias ? load1_rt(E.bias, E.bt, c) : 0.0f;
+  const float* from = stage + (lane >> 4) * 17 + (lane & 15);
+  int64_t r = row0 + (lane >> 4);
 #pragma unroll 1
-  for (int i = lane >> 4; i < 32; i += 16) {           // eight rows: i, i + 2, ...
-    const int64_t r = row0 + i;
+  for (int half = 0; half < 2; ++half, r += 16, from += 16 * 17) {     // eight rows, two apart
     const int n = P.m - r >= 16 ? 8 : P.m > r ? (int)((P.m - r + 1) / 2) : 0;
     float t[8], res[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      t[k] = stage[(i + 2 * k) * 17 + (lane & 15)] + bias;
-      res[k] = E.res && k < n ? load1_rt(E.res, E.rt, (r + 2 * k) * E.ldr + c) : 0.0f;
+    if (E.res) {
+      if (E.rt == PSK_BF16) gather8<PSK_BF16>((const char*)E.res + 2 * (r * E.ldr + c), 4 * E.ldr, n, res);
+      else gather8<PSK_F32>((const char*)E.res + 4 * (r * E.ldr + c), 8 * E.ldr, n, res);
     }
-    if (E.z) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < n) store1_rt(E.z, E.zt, (r + 2 * k) * E.ldz + c, t[k]);
-    }
+    for (int k = 0; k < 8; ++k) t[k] = from[2 * k * 17] + bias;
+    if (E.z) scatter8_rt(E.z, E.zt, r * E.ldz + c, E.ldz, n, t);
     act_rt<8>(t, E.act);
+    if (E.res) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) store1_rt(E.y, E.yt, (r + 2 * k) * E.ldy + c, E.res ? t[k] + res[k] : t[k]);
+      for (int k = 0; k < 8; ++k) t[k] += res[k];
+    }
+    scatter8_rt(E.y, E.yt, r * E.ldy + c, E.ldy, n, t);
   }
 }
 
@@ -359,7 +388,7 @@ __device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
 // Sixteen columns of one row of the orthogonalised update: v = alpha v + beta
 // from, stored in fp16 planes (and mirrored) or into a leaf.  The planes' rows
 // are padded to 32 bytes; their padding may be written.
-__device__ __forceinline__ void ortho_row16(const MMParams& P, int32_t matrix, int64_t r, int64_t c, bool mirrored,
+__device__ __forceinline__ void ortho_row16(const MMProblem& P, int32_t matrix, int64_t r, int64_t c, bool mirrored,
                                             const Fetched& F, float* v) {
   const MMEpilogue& E = P.e;
   const int64_t at = (int64_t)matrix * E.planes * E.plane_stride;
@@ -407,7 +436,7 @@ __device__ __forceinline__ void ortho_row16(const MMParams& P, int32_t matrix, i
 }
 
 template <int KIND>
-__device__ __forceinline__ void fetch16(const MMParams& P, int32_t matrix, int64_t r, int64_t c, Fetched& F) {
+__device__ __forceinline__ void fetch16(const MMProblem& P, int32_t matrix, int64_t r, int64_t c, Fetched& F) {
   const MMEpilogue& E = P.e;
   if (KIND == MM_ANY || r >= P.m || c >= P.n) return;
   if constexpr (KIND == MM_ORTHO) {
@@ -423,7 +452,7 @@ __device__ __forceinline__ void fetch16(const MMParams& P, int32_t matrix, int64
 
 // The epilogue of 16 neighbouring accumulators, from column c on, of row0 + lane.
 template <int KIND>
-__device__ __forceinline__ void finish16(const MMParams& P, int32_t matrix, int64_t row0, int lane, int64_t c,
+__device__ __forceinline__ void finish16(const MMProblem& P, int32_t matrix, int64_t row0, int lane, int64_t c,
                                          bool mirrored, const Fetched& F, float* stage, float* v) {
   if (c >= P.n) return;
   if constexpr (KIND == MM_ANY) {
@@ -448,11 +477,13 @@ struct MMShape {
   static constexpr int STAGES = (225 * 1024 - TURN) / STAGE < 8 ? (225 * 1024 - TURN) / STAGE : 8;
   static constexpr int RING = SUM ? (225 * 1024 - TURN) / 1024 * 1024 : STAGES * STAGE;
   static constexpr int SMEM = RING + TURN + 1024;               // and what aligns the ring to 1024 bytes
-  static constexpr int TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
+  // Columns of one accumulator: with SUM the last product of planes has its own,
+  // beside that of the others.
+  static constexpr int ACC = SUM ? 2 * BN : BN;
 };
 
-template <int CG, int BN, int KIND, bool SUM>
-__global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __grid_constant__ MMParams P) {
+template <int CG, int BN, int KIND, bool SUM, int COUNT>
+__global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __grid_constant__ MMParams G) {
   using S = MMShape<CG, BN, KIND, SUM>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[S::STAGES], empty[S::STAGES], acc_full[2], acc_empty[2], drain;
@@ -461,9 +492,9 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int32_t first = blockIdx.x / CG, step = gridDim.x / CG;
-  const int32_t total = P.tiles * P.matrices;
-  const int na = SUM ? P.na : 1, nb = SUM ? P.nb : 1, stages = SUM ? P.stages : S::STAGES;
-  const uint32_t stage_bytes = na * MM_A_BYTES + nb * S::B_BYTES;
+  const int32_t total = G.total;
+  const int stages = SUM ? G.stages : S::STAGES;
+  const uint32_t slot_bytes = SUM ? G.slot_bytes : S::STAGE;
 
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < S::STAGES; ++i) {
@@ -477,7 +508,7 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
     mbar_init(&drain, 1);
     fence_barrier_init();
   }
-  if (warp == 2) tmem_alloc<CG>(&tmem_slot, S::TMEM_COLS);
+  if (warp == 2) tmem_alloc<CG>(&tmem_slot, 2 * S::ACC);
   fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync_all();
@@ -495,7 +526,10 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
     uint32_t round = 0;
     bool ok = true;
     for (int32_t t = first; ok && t < total; t += step) {
-      const Tile tile = tile_at<S::BM / BN>(P, t);
+      const int q = COUNT == 2 && t >= G.split;
+      const MMProblem& P = G.q[q];
+      const Tile tile = tile_at<S::BM / BN>(P, q ? t - G.split : t);
+      const int na = SUM ? P.na : 1, nb = SUM ? P.nb : 1;
       const int32_t am = tile.tm * S::BM + (int32_t)rank * 128;
       const int32_t bn = tile.tn * BN + (int32_t)rank * S::B_ROWS;
       for (int32_t kb = 0; kb < P.kblocks; ++kb) {
@@ -503,8 +537,8 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
           ok = false;
           break;
         }
-        if (rank == 0) mbar_arrive_expect_tx(&full[slot], stage_bytes * CG);
-        uint32_t at = ring + slot * stage_bytes;
+        if (rank == 0) mbar_arrive_expect_tx(&full[slot], (na * MM_A_BYTES + nb * S::B_BYTES) * CG);
+        uint32_t at = ring + slot * slot_bytes;
         const uint32_t bar = smem_addr(&full[slot]);
         const int32_t k0 = kb * MM_BK;
         for (int p = 0; p < na; ++p, at += MM_A_BYTES) {
@@ -535,13 +569,15 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
         mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---- products
-    const uint32_t idesc = (1u << 4) | (P.f16 ? 0u : (1u << 7) | (1u << 10)) | (P.a_k ? 0u : 1u << 15) |
-                           (P.b_k ? 0u : 1u << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(S::BM >> 4) << 24);
-    const uint32_t a_step = (P.a_k ? 32u : 2048u) >> 4, b_step = (P.b_k ? 32u : 2048u) >> 4;
     uint32_t n = 0, round = 0;
     int slot = 0;
     bool ok = true;
-    for (int32_t t = first; ok && t < total; t += step)
+    for (int32_t t = first; ok && t < total; t += step) {
+      const MMProblem& P = G.q[COUNT == 2 && t >= G.split];
+      const uint32_t idesc = (1u << 4) | (G.f16 ? 0u : (1u << 7) | (1u << 10)) | (P.a_k ? 0u : 1u << 15) |
+                             (P.b_k ? 0u : 1u << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(S::BM >> 4) << 24);
+      const uint32_t a_step = (P.a_k ? 32u : 2048u) >> 4, b_step = (P.b_k ? 32u : 2048u) >> 4;
+      const int32_t b_first = (SUM ? P.na : 1) * MM_A_BYTES;
       for (int32_t k = 0; ok && k < P.kblocks; k += P.chunk, ++n) {
         const int buf = n & 1;
         if (!mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1)) {
@@ -549,7 +585,7 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
           break;
         }
         fence_after();
-        const uint32_t d = tmem + buf * BN;
+        const uint32_t d = tmem + buf * S::ACC;
         const int32_t blocks = P.kblocks - k < P.chunk ? P.kblocks - k : P.chunk;
         for (int32_t i = 0; i < blocks; ++i) {
           if (!mbar_wait(&full[slot], round & 1)) {
@@ -557,22 +593,43 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
             break;
           }
           fence_after();
-          const uint32_t at = ring + slot * stage_bytes;
+          const uint32_t at = ring + slot * slot_bytes;
           for (int p = 0; p < (SUM ? P.pairs : 1); ++p) {
-            const uint32_t a = at + (SUM ? P.pa[p] : 0) * MM_A_BYTES, b = at + na * MM_A_BYTES + (SUM ? P.pb[p] : 0) * S::B_BYTES;
+            const uint32_t a = at + (SUM ? P.pa[p] : 0) * MM_A_BYTES, b = at + b_first + (SUM ? P.pb[p] : 0) * S::B_BYTES;
             const uint64_t da = operand_desc(a, MM_A_BYTES / 2), db = operand_desc(b, 64 * MM_BK * 2);
 #pragma unroll
             for (int j = 0; j < MM_BK / 16; ++j)
-              mma_16<CG>(d, da + (uint64_t)(j * a_step), db + (uint64_t)(j * b_step), idesc, (i | j | p) != 0);
+              mma_16<CG>(SUM && p + 1 < P.pairs ? d + BN : d, da + (uint64_t)(j * a_step), db + (uint64_t)(j * b_step), idesc,
+                         (i | j) != 0 || (SUM && p > 0 && p + 1 < P.pairs));
           }
           mma_commit<CG>(&empty[slot]);
           if (++slot == stages) slot = 0, ++round;
         }
         if (ok) mma_commit<CG>(&acc_full[buf]);
       }
+    }
     if (!ok) {                   // products in flight end before the memory is given up
       mma_commit<CG>(&drain);
       mbar_wait(&drain, 0);
+    }
+  } else if (warp == 3) {
+    // ---- columns' sums joined, beside the products
+    const MMColumnSums& J = G.sums;
+    for (int64_t c = (int64_t)blockIdx.x * 32 + lane; J.out && c < J.cols; c += (int64_t)gridDim.x * 32) {
+      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      int b = 0;
+      for (; b + 4 <= J.blocks; b += 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += J.parts[(int64_t)(b + i) * J.cols + c];
+      for (; b < J.blocks; ++b) s[0] += J.parts[(int64_t)b * J.cols + c];
+      const float v = (s[0] + s[1]) + (s[2] + s[3]);
+      if (J.dt == PSK_BF16) {
+        uint16_t* q = (uint16_t*)J.out + c;
+        *q = f32_to_bf16_bits(J.add ? bf16_bits_to_f32(*q) + v : v);
+      } else {
+        float* q = (float*)J.out + c;
+        *q = J.add ? *q + v : v;
+      }
     }
   } else if (warp >= 4) {
     // ---- epilogue: a warp's 32 accumulator rows (set by its number), a share of the columns
@@ -581,7 +638,8 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
     float* stage = (float*)(smem_raw + (ring - smem_addr(smem_raw)) + S::RING) + (warp - 4) * (32 * 17);
     const uint32_t mine = tmem + ((uint32_t)rows << 16) + share * COLS;
     uint32_t n = 0;
-    for (int32_t t = first; t < total; t += step) {
+    // One tile of a product; false if a wait gave up.
+    const auto finish = [&](const MMProblem& P, int32_t t) {
       const Tile tile = tile_at<S::BM / BN>(P, t);
       const int64_t row0 = (int64_t)tile.tm * S::BM + rank * 128 + rows, r = row0 + lane;
       const int64_t col = (int64_t)tile.tn * BN + share * COLS;
@@ -592,20 +650,20 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
         for (int32_t k = 0; k < P.kblocks; k += P.chunk, ++n) {
           const int buf = n & 1;
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[buf], (n >> 1) & 1));
-          if (!ok) break;
+          if (!ok) return false;
           fence_after();
 #pragma unroll
           for (int c = 0; c < COLS; c += 16) {
-            float v[16];
-            tmem_load16(mine + buf * BN + c, v);
+            float v[16], w[16];
+            tmem_load16(mine + buf * S::ACC + BN + c, w);
+            tmem_load16(mine + buf * S::ACC + c, v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[c + i] = k ? sum[c + i] + v[i] : v[i];
+            for (int i = 0; i < 16; ++i) sum[c + i] = k ? sum[c + i] + (v[i] + w[i]) : v[i] + w[i];
           }
           fence_before();
           __syncwarp();
           if (lane == 0) arrive_first<CG>(&acc_empty[buf]);
         }
-        if (!ok) break;
 #pragma unroll 1
         for (int c = 0; c < COLS; c += 16) {
           Fetched F;
@@ -624,14 +682,14 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
         Fetched F;
         fetch16<KIND>(P, tile.matrix, r, col, F);
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[buf], (n >> 1) & 1));
-        if (!ok) break;
+        if (!ok) return false;
         ++n;
         fence_after();
 #pragma unroll 1
         for (int c = 0; c < COLS; c += 16) {
           float v[16];
           __syncwarp();
-          tmem_load16(mine + buf * BN + c, v);
+          tmem_load16(mine + buf * S::ACC + c, v);
           if (c + 16 >= COLS) {      // the accumulator is read: the next tile but one may have it
             fence_before();
             __syncwarp();
@@ -642,6 +700,11 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
           finish16<KIND>(P, tile.matrix, row0, lane, col + c, mirrored, now, stage, v);
         }
       }
+      return true;
+    };
+    for (int32_t t = first; t < total; t += step) {
+      // (each product's parameters are read as constants)
+      if (!(COUNT == 2 && t >= G.split ? finish(G.q[COUNT - 1], t - G.split) : finish(G.q[0], t))) break;
     }
   }
   __syncwarp();
@@ -649,7 +712,7 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
   __syncthreads();
   if constexpr (CG == 2) cluster_sync_all();
   fence_after();
-  if (warp == 2) tmem_free<CG>(tmem, S::TMEM_COLS);
+  if (warp == 2) tmem_free<CG>(tmem, 2 * S::ACC);
 }
 
 // -------------------------------------------------------------- few rows
@@ -679,7 +742,7 @@ __device__ __forceinline__ float load_cluster(uint32_t addr, uint32_t rank) {
 }
 
 template <int BN>
-__global__ void __launch_bounds__(THIN_THREADS, 1) mm_thin_kernel(const __grid_constant__ MMParams P, int split) {
+__global__ void __launch_bounds__(THIN_THREADS, 1) mm_thin_kernel(const __grid_constant__ MMProblem P, int split) {
   using S = ThinShape<BN>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[S::STAGES], empty[S::STAGES], acc_full, drain;
@@ -828,7 +891,9 @@ static int encode_operand(CUtensorMap* map, const MMOperand& o, int64_t matrices
 // Blocks of the summed axis that one accumulator takes where the sum is an
 // f32 operand's: the tensor core's additions truncate (an f32 result of 2048
 // terms is off by 1e-5 of its size, of 65536 by 2e-4), so every 256 terms the
-// accumulator is added to a register with one rounding instead.
+// accumulator is added to a register with one rounding instead.  And the small
+// products of planes have an accumulator of their own: added into the large
+// one, each would truncate it again (1.5e-6 of the result's size, apart 1.5e-7).
 constexpr int MM_SUM_BLOCKS = 4;
 
 // Absent, or bf16 rows that begin on 32-byte boundaries.
@@ -836,57 +901,68 @@ static bool rows_32(const void* p, int32_t dt, int64_t ld) {
   return !p || (dt == PSK_BF16 && (uintptr_t)p % 32 == 0 && ld % 16 == 0);
 }
 
-template <int CG, int BN, int KIND, bool SUM>
-static int launch_shape(const MMCall& C, cudaStream_t stream) {
+template <int CG, int BN, int KIND, bool SUM, int COUNT>
+static int launch_shape(const MMCall* calls, const MMColumnSums* sums, cudaStream_t stream) {
   using S = MMShape<CG, BN, KIND, SUM>;
-  MMParams P{};
-  int rc = encode_operand(&P.ta, C.a, C.matrices, C.f16, C.a.k_inner ? 128 : 64);
-  if (!rc) rc = encode_operand(&P.tb, C.b, C.matrices, C.f16, C.b.k_inner ? S::B_ROWS : 64);
-  if (rc) return rc;
-  P.e = C.e;
-  P.m = C.m, P.n = C.n;
-  P.kblocks = (int32_t)((C.k + MM_BK - 1) / MM_BK), P.pairs = C.pairs, P.matrices = (int32_t)C.matrices;
-  P.chunk = SUM ? MM_SUM_BLOCKS : P.kblocks;
-  for (int i = 0; i < C.pairs; ++i) {
-    P.na = C.pa[i] + 1 > P.na ? C.pa[i] + 1 : P.na;
-    P.nb = C.pb[i] + 1 > P.nb ? C.pb[i] + 1 : P.nb;
+  MMParams G{};
+  int64_t all = 0;
+  for (int q = 0; q < COUNT; ++q) {
+    const MMCall& C = calls[q];
+    MMProblem& P = G.q[q];
+    int rc = encode_operand(&P.ta, C.a, C.matrices, C.f16, C.a.k_inner ? 128 : 64);
+    if (!rc) rc = encode_operand(&P.tb, C.b, C.matrices, C.f16, C.b.k_inner ? S::B_ROWS : 64);
+    if (rc) return rc;
+    P.e = C.e;
+    P.m = C.m, P.n = C.n;
+    P.kblocks = (int32_t)((C.k + MM_BK - 1) / MM_BK), P.pairs = C.pairs;
+    P.chunk = SUM ? MM_SUM_BLOCKS : P.kblocks;
+    P.planes_a = C.a.planes, P.planes_b = C.b.planes;
+    P.a_k = C.a.k_inner, P.b_k = C.b.k_inner;
+    for (int i = 0; i < C.pairs; ++i) {
+      P.pa[i] = C.pa[i], P.pb[i] = C.pb[i];
+      P.na = C.pa[i] + 1 > P.na ? C.pa[i] + 1 : P.na;
+      P.nb = C.pb[i] + 1 > P.nb ? C.pb[i] + 1 : P.nb;
+    }
+    const int32_t slot = P.na * MM_A_BYTES + P.nb * S::B_BYTES;
+    if (slot > G.slot_bytes) G.slot_bytes = slot;
+    const int64_t tm = (C.m + S::BM - 1) / S::BM, tn = (C.n + BN - 1) / BN;
+    int64_t tiles = tm * tn;
+    if (C.symmetric) {               // the last row of tiles may end before the diagonal block does
+      constexpr int Q = S::BM / BN;
+      tiles = Q * (tm * (tm - 1) / 2) + (Q * tm < tn ? Q * tm : tn);
+    }
+    all += tiles * C.matrices;
+    if (all > 0x7FFFFFFF) return fail(PSK_E_SHAPE, "too many output tiles");
+    P.tiles_m = (int32_t)tm, P.tiles_n = (int32_t)tn, P.tiles = (int32_t)tiles, P.symmetric = C.symmetric;
+    if (q == 0) G.split = (int32_t)all;
+    G.f16 = C.f16;
   }
-  P.stages = S::RING / (P.na * MM_A_BYTES + P.nb * S::B_BYTES);
-  if (P.stages > S::STAGES) P.stages = S::STAGES;
-  P.planes_a = C.a.planes, P.planes_b = C.b.planes;
-  P.a_k = C.a.k_inner, P.b_k = C.b.k_inner, P.f16 = C.f16;
-  const int64_t tm = (C.m + S::BM - 1) / S::BM, tn = (C.n + BN - 1) / BN;
-  int64_t tiles = tm * tn;
-  if (C.symmetric) {                 // the last row of tiles may end before the diagonal block does
-    constexpr int Q = S::BM / BN;
-    tiles = Q * (tm * (tm - 1) / 2) + (Q * tm < tn ? Q * tm : tn);
-  }
-  if (tiles * C.matrices > 0x7FFFFFFF) return fail(PSK_E_SHAPE, "too many output tiles");
-  P.tiles_m = (int32_t)tm, P.tiles_n = (int32_t)tn, P.tiles = (int32_t)tiles, P.symmetric = C.symmetric;
-  for (int i = 0; i < 8; ++i) P.pa[i] = C.pa[i], P.pb[i] = C.pb[i];
+  G.total = (int32_t)all;
+  G.stages = S::RING / G.slot_bytes < S::STAGES ? S::RING / G.slot_bytes : S::STAGES;
+  if (sums) G.sums = *sums;
   static bool limit[PSK_MAX_DEVICES] = {};
-  smem_limit_once((const void*)mm_kernel<CG, BN, KIND, SUM>, S::SMEM, limit);
-  const int64_t most = device_sm_count() / CG, want = tiles * C.matrices;
+  smem_limit_once((const void*)mm_kernel<CG, BN, KIND, SUM, COUNT>, S::SMEM, limit);
+  const int64_t most = device_sm_count() / CG;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = CG, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((want < most ? want : most) * CG));
+  cfg.gridDim = dim3((unsigned)((all < most ? all : most) * CG));
   cfg.blockDim = dim3(MMWarps<SUM>::THREADS);
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = CG > 1 ? 2 : 1;
-  cudaLaunchKernelEx(&cfg, mm_kernel<CG, BN, KIND, SUM>, P);
+  cudaLaunchKernelEx(&cfg, mm_kernel<CG, BN, KIND, SUM, COUNT>, G);
   return check_launch("matrix product kernel");
 }
 
 template <int BN>
 static int launch_thin(const MMCall& C, cudaStream_t stream) {
   using S = ThinShape<BN>;
-  MMParams P{};
+  MMProblem P{};
   int rc = encode_operand(&P.ta, C.b, 1, false, C.b.k_inner ? 128 : 64);
   if (!rc) rc = encode_operand(&P.tb, C.a, 1, false, BN);
   if (rc) return rc;
@@ -922,33 +998,64 @@ static int launch_thin(const MMCall& C, cudaStream_t stream) {
 // take about 0.34 us of a pair and 0.30 us of one CTA, whose 128 columns are
 // bound by shared memory (operands read and filled in: 2048^3 16.8 and 24.3 us,
 // 512 x 2048 x 5632 15.9 and 23.8, 1024^3 11.4 and 9.0, 128 x 2048 x 5632 15.6
-// and 13.4).
+// and 13.4).  With SUM always the latter: two accumulators of 256 columns would
+// leave no second pair of them, and pairs on 256 x 128 gain nothing (4096 x 2048
+// x 2048 f32 199 us, single ones 195).
 template <int KIND, bool SUM>
-static int launch_kind(const MMCall& C, cudaStream_t stream) {
+static int launch_kind(const MMCall* calls, const MMColumnSums* sums, cudaStream_t stream) {
+  const MMCall& C = calls[0];
   const int64_t sms = device_sm_count(), pairs = sms / 2;
   const auto waves = [&](int64_t side, int64_t units) {
     const int64_t tm = (C.m + side - 1) / side, tn = (C.n + side - 1) / side;
     return ((C.symmetric ? tm * (tm + 1) / 2 : tm * tn) * C.matrices + units - 1) / units;
   };
-  if (pairs > 0 && waves(256, pairs) * 34 < waves(128, sms) * 30) return launch_shape<2, 256, KIND, SUM>(C, stream);
-  return launch_shape<1, 128, KIND, SUM>(C, stream);
+  if constexpr (!SUM)
+    if (pairs > 0 && waves(256, pairs) * 34 < waves(128, sms) * 30)
+      return launch_shape<2, 256, KIND, false, 1>(calls, sums, stream);
+  return launch_shape<1, 128, KIND, SUM, 1>(calls, sums, stream);
 }
 
-int mm_launch(const MMCall& C, cudaStream_t stream) {
+static bool is_wide(const MMCall& C) {
   const MMEpilogue& E = C.e;
-  const bool sum = C.pairs > 1;
-  if (C.ortho) return sum ? launch_kind<MM_ORTHO, true>(C, stream) : launch_kind<MM_ORTHO, false>(C, stream);
-  const bool wide = C.n % 16 == 0 && rows_32(E.y, E.yt, E.ldy) && rows_32(E.z, E.zt, E.ldz) &&
-                    rows_32(E.res, E.rt, E.ldr) && rows_32(E.bias, E.bt, 0);
-  if (!sum && C.m <= 64 && C.a.k_inner)
+  return C.n % 16 == 0 && rows_32(E.y, E.yt, E.ldy) && rows_32(E.z, E.zt, E.ldz) && rows_32(E.res, E.rt, E.ldr) &&
+         rows_32(E.bias, E.bt, 0);
+}
+
+int mm_launch(const MMCall* calls, int count, const MMColumnSums* sums, cudaStream_t stream) {
+  const MMCall& C = calls[0];
+  const bool sum = C.pairs > 1, wide = !sum && is_wide(C);
+  if (count == 2) {
+    // One launch where one kernel serves both and their tiles together fill the
+    // SMs once at most ([509, 771] x [771, 1003] f32: 78 us as two, 40 as one);
+    // more tiles run better one product after the other (8192 x 2048 x 5632:
+    // 252 us, together 275).
+    int64_t tiles = 0;
+    for (int q = 0; q < 2; ++q) tiles += ((calls[q].m + 127) / 128) * ((calls[q].n + 127) / 128);
+    if (tiles > device_sm_count() || (calls[1].pairs > 1) != sum || (!sum && is_wide(calls[1]) != wide)) {
+      const int rc = mm_launch(calls, 1, sums, stream);
+      return rc ? rc : mm_launch(calls + 1, 1, nullptr, stream);
+    }
+    if (calls[1].k * calls[1].pairs > C.k * C.pairs) {      // the longer tiles first
+      const MMCall turned[2] = {calls[1], calls[0]};
+      return mm_launch(turned, 2, sums, stream);
+    }
+  }
+  if (count == 2) {
+    if (sum) return launch_shape<1, 128, MM_ANY, true, 2>(calls, sums, stream);
+    if (!wide) return launch_shape<1, 128, MM_ANY, false, 2>(calls, sums, stream);
+    return launch_shape<1, 128, ACT_NONE, false, 2>(calls, sums, stream);
+  }
+  if (C.ortho)
+    return sum ? launch_kind<MM_ORTHO, true>(calls, sums, stream) : launch_kind<MM_ORTHO, false>(calls, sums, stream);
+  if (!sums && !sum && C.m <= 64 && C.a.k_inner)
     return C.m <= 16 ? launch_thin<16>(C, stream) : C.m <= 32 ? launch_thin<32>(C, stream) : launch_thin<64>(C, stream);
-  if (sum) return launch_kind<MM_ANY, true>(C, stream);
-  if (!wide) return launch_kind<MM_ANY, false>(C, stream);
-  switch (E.act) {
-    case ACT_RELU: return launch_kind<ACT_RELU, false>(C, stream);
-    case ACT_GELU: return launch_kind<ACT_GELU, false>(C, stream);
-    case ACT_SILU: return launch_kind<ACT_SILU, false>(C, stream);
-    default: return launch_kind<ACT_NONE, false>(C, stream);
+  if (sum) return launch_kind<MM_ANY, true>(calls, sums, stream);
+  if (!wide) return launch_kind<MM_ANY, false>(calls, sums, stream);
+  switch (C.e.act) {
+    case ACT_RELU: return launch_kind<ACT_RELU, false>(calls, sums, stream);
+    case ACT_GELU: return launch_kind<ACT_GELU, false>(calls, sums, stream);
+    case ACT_SILU: return launch_kind<ACT_SILU, false>(calls, sums, stream);
+    default: return launch_kind<ACT_NONE, false>(calls, sums, stream);
   }
 }
 

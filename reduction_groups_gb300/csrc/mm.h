@@ -58,6 +58,17 @@ struct MMCall {
   MMEpilogue e;
 };
 
-int mm_launch(const MMCall& call, cudaStream_t stream);
+// Sums of columns from their parts, `blocks` rows of `cols`, taken beside the
+// products: out = [out +] the sum.
+struct MMColumnSums {
+  const float* parts;
+  void* out;
+  int64_t cols;
+  int32_t blocks, dt, add;
+};
+
+// One product, or two (of no activation) whose tiles are shared out together
+// (`count`), and column sums or NULL.
+int mm_launch(const MMCall* calls, int count, const MMColumnSums* sums, cudaStream_t stream);
 
 }  // namespace psk

@@ -336,13 +336,13 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
     C.a = wide(x, true), C.b = wide(x, true);
     C.e.alpha = 1.0f / ORTHO_SCALE, C.e.beta = 0.0f, C.e.from = nullptr, C.e.to = A;
     C.e.ld = S.ldm, C.e.plane_stride = L.asize, C.e.planes = planes;
-    rc = mm_launch(C, s);
+    rc = mm_launch(&C, 1, nullptr, s);
     if (rc) break;
     // B S = b (A S) + c (A S)(A S) / S
     C.k = S.m;
     C.a = square(A), C.b = square(A);
     C.e.alpha = (float)(c / ORTHO_SCALE), C.e.beta = (float)b, C.e.from = A, C.e.to = B;
-    rc = mm_launch(C, s);
+    rc = mm_launch(&C, 1, nullptr, s);
     if (rc) break;
     // X S <- a (X S) + (B S)(X S) / S
     C.n = S.n, C.symmetric = false, C.e.transposed = S.tall;
@@ -351,7 +351,7 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
     C.e.alpha = (float)(out_scale / ORTHO_SCALE), C.e.beta = (float)(a * out_scale);
     C.e.from = x, C.e.to = last ? nullptr : x2, C.e.leaves = S.table;
     C.e.ld = S.ldn, C.e.plane_stride = L.xsize, C.e.planes = ORTHO_PARTS;
-    rc = mm_launch(C, s);
+    rc = mm_launch(&C, 1, nullptr, s);
     std::swap(x, x2);
   }
   return rc;

@@ -22,10 +22,11 @@ constexpr int ROT_THREADS = 256;
 constexpr int ROT_WARPS = ROT_THREADS / 32;
 constexpr int ROT_MAX_DIM = 512;
 #ifndef RFC
-#define RFC 3
+#define RFC 4
+#define RFA 2
 #define RBC 2
 #endif
-constexpr int ROT_FWD_CTAS = RFC, ROT_BWD_CTAS = RBC;    // an SM
+constexpr int ROT_FWD_CTAS = RFC, ROT_BWD_CTAS = RBC, ROT_AHEAD = RFA;    // an SM
 constexpr int ROT_MAX_BLOCKS = 4 * NOMINAL_SMS;      // CTAs of the backward, at most
 
 struct RotSide {
@@ -308,24 +309,27 @@ __global__ void __launch_bounds__(ROT_THREADS, 2) rotary_any_backward_kernel(con
   }
 }
 
-// ------------------------------------- heads of 16-column groups, one type
+// --------------------------------------- heads of 8-column groups, one type
 //
-// A lane holds eight pairs of a head, its first members as four float2 and
-// its second members as four, for packed arithmetic; memory is accessed 16
-// bytes at a time and pairs that are neighbours come apart as they are widened.
-// Cosines, sines and scales stand in shared memory by pair.  Both kernels walk
-// a token's heads step after step (a step: one head a team) and have the next
-// step's loads under way while one is worked on, across tokens too.
+// A lane holds NP pairs of a head (four, or eight where four would need more
+// lanes than a warp has), first and second members apart, as float2 for packed
+// arithmetic; memory is accessed 8 or 16 bytes at a time and pairs that are
+// neighbours come apart as they are widened.  Cosines, sines and scales stand
+// in shared memory by pair.  Both kernels walk a token's heads step after step
+// (a step: one head a team) and have the next steps' loads under way while one
+// is worked on, across tokens too.  Four pairs a lane rather than eight halve
+// its registers, and twice the warps hide the latencies of a short pass.
 
-template <int TY>
+template <int TY, int NP>
 struct RotRaw {
-  static constexpr int W = TY == PSK_BF16 ? 8 : 16;
+  static constexpr int W = TY == PSK_BF16 ? NP : 2 * NP;       // words
   uint32_t w[W];
 };
 
-// The eight pairs' members.
-struct Rot8 {
-  float2 a[4], b[4];
+// The pairs' members.
+template <int NP>
+struct RotPairs {
+  float2 a[NP / 2], b[NP / 2];
 };
 
 struct RotTables {
@@ -335,15 +339,15 @@ struct RotTables {
   float gamma[2][2][ROT_MAX_DIM / 2];                          // [side][member][pair]
 };
 
-template <bool NEIGH>
+template <bool NEIGH, int NP>
 struct RotLane {
-  int first[2], pair;                      // the columns of the two runs of eight, the first pair
+  int first[2], pair;                      // the columns of the two runs of NP, the first pair
   bool turns, there;
   __device__ __forceinline__ RotLane(int g, const RotParams& P) {
-    pair = 8 * g;
+    pair = NP * g;
     turns = pair < P.rot / 2;
     there = 2 * pair < P.dim;
-    if (NEIGH) first[0] = 2 * pair, first[1] = 2 * pair + 8;
+    if (NEIGH) first[0] = 2 * pair, first[1] = 2 * pair + NP;
     else if (turns) first[0] = pair, first[1] = pair + P.rot / 2;
     else first[0] = P.rot / 2 + pair, first[1] = first[0] + (P.dim - P.rot) / 2;
   }
@@ -352,59 +356,71 @@ struct RotLane {
     return NEIGH ? first[0] + 2 * i + member : first[member] + i;
   }
   template <int TY>
-  __device__ __forceinline__ void load(const char* p, bool live, RotRaw<TY>& o) const {
-    constexpr int N = RotRaw<TY>::W / 8;               // 16-byte accesses a run
+  __device__ __forceinline__ void load(const char* p, bool live, RotRaw<TY, NP>& o) const {
+    constexpr int N = RotRaw<TY, NP>::W / 2;           // words of a run
 #pragma unroll
-    for (int i = 0; i < RotRaw<TY>::W; ++i) o.w[i] = 0;
+    for (int i = 0; i < 2 * N; ++i) o.w[i] = 0;
     if (!live || !there) return;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) {
+      const char* q = p + (k ? (first[1] - first[0]) * (TY == PSK_BF16 ? 2 : 4) : 0);
+      if constexpr (N == 2) {
+        const uint2 u = *(const uint2*)q;
+        o.w[2 * k] = u.x, o.w[2 * k + 1] = u.y;
+      } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const uint4 u = *(const uint4*)(p + (k ? (first[1] - first[0]) * (TY == PSK_BF16 ? 2 : 4) : 0) + 16 * i);
-        uint32_t* w = o.w + (k * N + i) * 4;
-        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        for (int i = 0; i < N; i += 4) {
+          const uint4 u = *(const uint4*)(q + 4 * i);
+          uint32_t* w = o.w + k * N + i;
+          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        }
       }
+    }
   }
   template <int TY>
-  __device__ __forceinline__ void widen(const RotRaw<TY>& o, Rot8& v) const {
-    // element e of the lane's sixteen, in memory order
+  __device__ __forceinline__ void widen(const RotRaw<TY, NP>& o, RotPairs<NP>& v) const {
+    // element e of the lane's 2 NP, in memory order
     const auto at = [&](int e) {
       if constexpr (TY == PSK_BF16) return __uint_as_float(e & 1 ? o.w[e >> 1] & 0xFFFF0000u : o.w[e >> 1] << 16);
       else return __uint_as_float(o.w[e]);
     };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NP / 2; ++j) {
       v.a[j] = NEIGH ? make_float2(at(4 * j), at(4 * j + 2)) : make_float2(at(2 * j), at(2 * j + 1));
-      v.b[j] = NEIGH ? make_float2(at(4 * j + 1), at(4 * j + 3)) : make_float2(at(8 + 2 * j), at(9 + 2 * j));
+      v.b[j] = NEIGH ? make_float2(at(4 * j + 1), at(4 * j + 3)) : make_float2(at(NP + 2 * j), at(NP + 1 + 2 * j));
     }
   }
   template <int TY>
-  __device__ __forceinline__ void store(char* p, const Rot8& v) const {
+  __device__ __forceinline__ void store(char* p, const RotPairs<NP>& v) const {
     if (!there) return;
-    float e[16];                                       // in memory order
+    float e[2 * NP];                                   // in memory order
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NP / 2; ++j) {
       e[NEIGH ? 4 * j : 2 * j] = v.a[j].x, e[NEIGH ? 4 * j + 2 : 2 * j + 1] = v.a[j].y;
-      e[NEIGH ? 4 * j + 1 : 8 + 2 * j] = v.b[j].x, e[NEIGH ? 4 * j + 3 : 9 + 2 * j] = v.b[j].y;
+      e[NEIGH ? 4 * j + 1 : NP + 2 * j] = v.b[j].x, e[NEIGH ? 4 * j + 3 : NP + 1 + 2 * j] = v.b[j].y;
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       char* q = p + (k ? (first[1] - first[0]) * (TY == PSK_BF16 ? 2 : 4) : 0);
-      const float* w = e + 8 * k;
-      if constexpr (TY == PSK_BF16) {
+      const float* w = e + NP * k;
+      if constexpr (TY == PSK_F32) {
+#pragma unroll
+        for (int i = 0; i < NP; i += 4) *(float4*)(q + 4 * i) = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+      } else if constexpr (NP == 4) {
+        *(uint2*)q = make_uint2(f32x2_to_bf16x2(w[0], w[1]), f32x2_to_bf16x2(w[2], w[3]));
+      } else {
         *(uint4*)q = make_uint4(f32x2_to_bf16x2(w[0], w[1]), f32x2_to_bf16x2(w[2], w[3]), f32x2_to_bf16x2(w[4], w[5]),
                                 f32x2_to_bf16x2(w[6], w[7]));
-      } else {
-        *(float4*)q = make_float4(w[0], w[1], w[2], w[3]);
-        *(float4*)(q + 16) = make_float4(w[4], w[5], w[6], w[7]);
       }
     }
   }
-  // Four float2 of a table by pair.
-  __device__ __forceinline__ void of_pairs(const float* table, float2 (&o)[4]) const {
-    const float4 x = *(const float4*)(table + pair), y = *(const float4*)(table + pair + 4);
-    o[0] = make_float2(x.x, x.y), o[1] = make_float2(x.z, x.w), o[2] = make_float2(y.x, y.y), o[3] = make_float2(y.z, y.w);
+  // NP values of a table by pair.
+  __device__ __forceinline__ void of_pairs(const float* table, float2 (&o)[NP / 2]) const {
+#pragma unroll
+    for (int i = 0; i < NP; i += 4) {
+      const float4 x = *(const float4*)(table + pair + i);
+      o[i / 2] = make_float2(x.x, x.y), o[i / 2 + 1] = make_float2(x.z, x.w);
+    }
   }
 };
 
@@ -431,8 +447,12 @@ __device__ __forceinline__ void rot_tables(RotTables& T, const RotParams& P) {
   __syncthreads();
 }
 
-__device__ __forceinline__ void rot_angles8(RotTables& T, const RotParams& P, int64_t token, int warp, int lane) {
-  const int64_t pos = P.pos64 ? ((const int64_t*)P.pos)[token] : (int64_t)((const int32_t*)P.pos)[token];
+__device__ __forceinline__ int64_t rot_position(const RotParams& P, int64_t token) {
+  if (!P.rot) return 0;
+  return P.pos64 ? ((const int64_t*)P.pos)[token] : (int64_t)((const int32_t*)P.pos)[token];
+}
+
+__device__ __forceinline__ void rot_angles_at(RotTables& T, const RotParams& P, int64_t pos, int warp, int lane) {
   __syncwarp();
   for (int j = lane; j < P.rot / 2; j += 32) {
     const int64_t frac = (int64_t)((uint64_t)pos * T.turn[j]);
@@ -445,14 +465,19 @@ __device__ __forceinline__ void rot_angles8(RotTables& T, const RotParams& P, in
 
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
-// A lane's way through one side's heads in one tensor: where its columns begin
-// in its first head of token 0, and the bytes to the next token and step.
+// A lane's way through one side's heads in one tensor, in bytes: from the
+// tensor's beginning to its columns in its first head, from step to step.  The
+// launch has seen to it that a token's stretch and the distance of tokens stay
+// below 2^31 bytes.
 struct RotWalk {
   const char* base;
-  int64_t token, step;
+  uint32_t offset, step, token;
   __device__ __forceinline__ RotWalk(const void* p, int64_t ts, int64_t hs, int slot, int slots, int column, int size)
-      : base((const char*)p + (slot * hs + column) * size), token(ts * size), step(slots * hs * size) {}
-  __device__ __forceinline__ const char* at(int64_t t, int i) const { return base + t * token + i * step; }
+      : base((const char*)p), offset(((uint32_t)hs * slot + column) * size), step((uint32_t)hs * slots * size),
+        token((uint32_t)ts * size) {}
+  __device__ __forceinline__ const char* at(uint32_t t, int i) const {
+    return base + (uint64_t)t * token + (offset + i * step);
+  }
 };
 
 // 1 / sqrt to 2^-22.9.
@@ -464,126 +489,140 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 
 // The scale is folded into a token's cosines and sines, once for all its
 // heads, so a head's pass is a sum of squares, y = r (x p + x' q) with x' the
-// pair's other member, and its loads and stores.
-template <bool NEIGH, int TY>
-__global__ void __launch_bounds__(ROT_THREADS, ROT_FWD_CTAS) rotary_kernel(const __grid_constant__ RotParams P, int team) {
+// pair's other member, and its loads and stores.  AHEAD steps are in flight.
+template <bool NEIGH, int TY, int NP>
+__global__ void __launch_bounds__(ROT_THREADS, NP == 4 ? ROT_FWD_CTAS : 2) rotary_kernel(const __grid_constant__ RotParams P, int team) {
   __shared__ __align__(16) RotTables T;
-  constexpr int SIZE = TY == PSK_BF16 ? 2 : 4;
+  constexpr int SIZE = TY == PSK_BF16 ? 2 : 4, AHEAD = NP == 8 && TY == PSK_F32 ? 1 : ROT_AHEAD;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slots = 32 / team, slot = lane / team;
-  const RotLane<NEIGH> G(lane % team, P);
+  const RotLane<NEIGH, NP> G(lane % team, P);
   // steps of both sides, and those in which this lane's team has a head
   const int nq = (P.side[0].heads + slots - 1) / slots, nk = (P.side[1].heads + slots - 1) / slots;
   const int lq = (P.side[0].heads - slot + slots - 1) / slots, lk = (P.side[1].heads - slot + slots - 1) / slots;
-  const int64_t jump = (int64_t)gridDim.x * ROT_WARPS, units = P.tokens * P.chunks;
-  RotRaw<TY> raw;
+  const uint32_t jump = gridDim.x * ROT_WARPS, units = (uint32_t)P.tokens * P.chunks;
   const auto walk = [&](int sd, bool y) {
     const RotSide& S = P.side[sd];
     return y ? RotWalk(S.y, S.yt, S.yh, slot, slots, G.first[0], SIZE) : RotWalk(S.x, S.xt, S.xh, slot, slots, G.first[0], SIZE);
   };
-  // The first step of a unit: a token's steps [s0, s0 + per) of both sides, queries first.
-  const auto first = [&](int64_t token, int s0) {
-    if (s0 < nq) G.load(walk(0, false).at(token, s0), s0 < lq, raw);
-    else G.load(walk(1, false).at(token, s0 - nq), s0 - nq < lk, raw);
+  const RotWalk Xq = walk(0, false), Xk = walk(1, false), Yq = walk(0, true), Yk = walk(1, true);
+  // What is fetched next: step `fi` of unit `fu` (token `ft`), a unit being a
+  // token's steps [s0, s0 + per) of both sides, queries first.
+  uint32_t fu = blockIdx.x * ROT_WARPS + warp, ft = 0;
+  int fi = 0, fend = 0;
+  const auto enter = [&]() {
+    if (fu >= units) return;
+    if (P.chunks == 1) {
+      ft = fu, fi = 0, fend = nq + nk;
+    } else {
+      ft = fu / (uint32_t)P.chunks, fi = (int)(fu - ft * P.chunks) * P.per;
+      fend = fi + P.per < nq + nk ? fi + P.per : nq + nk;
+    }
   };
-  int64_t u = (int64_t)blockIdx.x * ROT_WARPS + warp;
-  int64_t token = P.chunks == 1 ? u : u / P.chunks;
-  int s0 = (int)(u - token * P.chunks) * P.per;
-  if (u < units) first(token, s0);
+  RotRaw<TY, NP> raw[AHEAD];
+  const auto fetch = [&](RotRaw<TY, NP>& o) {
+    if (fu >= units) return;
+    if (fi < nq) G.load(Xq.at(ft, fi), fi < lq, o);
+    else G.load(Xk.at(ft, fi - nq), fi - nq < lk, o);
+    if (++fi == fend) fu += jump, enter();
+  };
+  enter();
+  int64_t pos = fu < units ? rot_position(P, ft) : 0;
+  uint32_t u = fu;
+#pragma unroll
+  for (int j = 0; j < AHEAD; ++j) fetch(raw[j]);
   rot_tables<NEIGH>(T, P);
+  uint32_t token = 0;
+  int i = 0, end = 0;
+  bool fresh = true, keys = false;
+  float2 pa[NP / 2], qa[NP / 2], pb[NP / 2], qb[NP / 2];
   while (u < units) {
-    const int s1 = s0 + P.per < nq + nk ? s0 + P.per : nq + nk;
-    const int64_t next = u + jump, next_token = P.chunks == 1 ? next : next / P.chunks;
-    const int next_s0 = (int)(next - next_token * P.chunks) * P.per;
-    rot_angles8(T, P, token, warp, lane);
-    const auto side = [&](auto SD) {
-      constexpr int sd = SD.value;
-      const int from = sd ? (s0 > nq ? s0 - nq : 0) : s0, to = sd ? s1 - nq : (s1 < nq ? s1 : nq);
-      if (from >= to) return;
-      float2 pa[4], qa[4], pb[4], qb[4];
-      {
-        float2 c[4], s[4], ga[4], gb[4];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (u >= units) break;
+      RotPairs<NP> v;
+      G.widen(raw[j], v);
+      fetch(raw[j]);
+      if (fresh) {
+        if (P.chunks == 1) token = u, i = 0, end = nq + nk;
+        else {
+          token = u / (uint32_t)P.chunks, i = (int)(u - token * P.chunks) * P.per;
+          end = i + P.per < nq + nk ? i + P.per : nq + nk;
+        }
+        rot_angles_at(T, P, pos, warp, lane);
+        if (u + jump < units) pos = rot_position(P, P.chunks == 1 ? u + jump : (u + jump) / (uint32_t)P.chunks);
+      }
+      if (fresh || (i >= nq) != keys) {
+        fresh = false, keys = i >= nq;
+        float2 c[NP / 2], s[NP / 2], ga[NP / 2], gb[NP / 2];
         G.of_pairs(T.cosine[warp], c), G.of_pairs(T.sine[warp], s);
-        G.of_pairs(T.gamma[sd][0], ga), G.of_pairs(T.gamma[sd][1], gb);
+        G.of_pairs(T.gamma[keys][0], ga), G.of_pairs(T.gamma[keys][1], gb);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          pa[j] = __fmul2_rn(ga[j], c[j]), pb[j] = __fmul2_rn(gb[j], c[j]);
-          qa[j] = __fmul2_rn(gb[j], make_float2(-s[j].x, -s[j].y)), qb[j] = __fmul2_rn(ga[j], s[j]);
+        for (int m = 0; m < NP / 2; ++m) {
+          pa[m] = __fmul2_rn(ga[m], c[m]), pb[m] = __fmul2_rn(gb[m], c[m]);
+          qa[m] = __fmul2_rn(gb[m], make_float2(-s[m].x, -s[m].y)), qb[m] = __fmul2_rn(ga[m], s[m]);
         }
       }
-      const RotWalk X = walk(sd, false), Y = walk(sd, true);
-      const char* px = X.at(token, from);
-      char* py = (char*)Y.at(token, from);
-      const int mine = sd ? lk : lq;
-      for (int i = from; i < to; ++i) {
-        Rot8 v;
-        G.widen(raw, v);
-        if (i + 1 < to) {
-          px += X.step;
-          G.load(px, i + 1 < mine, raw);
-        } else if (sd == 0 && s1 > nq) {
-          G.load(walk(1, false).at(token, 0), 0 < lk, raw);
-        } else if (next < units) {
-          first(next_token, next_s0);
-        }
-        float2 r = splat(1.0f);
-        if (P.rms) {
-          float2 sum = splat(0.0f);
+      float2 r = splat(1.0f);
+      if (P.rms) {
+        float2 sum = splat(0.0f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sum = __ffma2_rn(v.a[j], v.a[j], __ffma2_rn(v.b[j], v.b[j], sum));
-          r = splat(rsqrt_approx(fmaf(team_sum(sum.x + sum.y, team), P.inv_dim, P.eps)));
-        }
-        Rot8 y;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 a = __fmul2_rn(v.a[j], r), b = __fmul2_rn(v.b[j], r);
-          y.a[j] = __fmul2_rn(a, pa[j]), y.b[j] = __fmul2_rn(b, pb[j]);
-          if (G.turns) y.a[j] = __ffma2_rn(b, qa[j], y.a[j]), y.b[j] = __ffma2_rn(a, qb[j], y.b[j]);
-        }
-        if (i < mine) G.template store<TY>(py, y);
-        py += Y.step;
+        for (int m = 0; m < NP / 2; ++m) sum = __ffma2_rn(v.a[m], v.a[m], __ffma2_rn(v.b[m], v.b[m], sum));
+        r = splat(rsqrt_approx(fmaf(team_sum(sum.x + sum.y, team), P.inv_dim, P.eps)));
       }
-    };
-    side(std::integral_constant<int, 0>{});
-    side(std::integral_constant<int, 1>{});
-    u = next, token = next_token, s0 = next_s0;
+      RotPairs<NP> y;
+#pragma unroll
+      for (int m = 0; m < NP / 2; ++m) {
+        const float2 a = __fmul2_rn(v.a[m], r), b = __fmul2_rn(v.b[m], r);
+        y.a[m] = __fmul2_rn(a, pa[m]), y.b[m] = __fmul2_rn(b, pb[m]);
+        if (G.turns) y.a[m] = __ffma2_rn(b, qa[m], y.a[m]), y.b[m] = __ffma2_rn(a, qb[m], y.b[m]);
+      }
+      if (keys) {
+        if (i - nq < lk) G.template store<TY>((char*)Yk.at(token, i - nq), y);
+      } else if (i < lq) {
+        G.template store<TY>((char*)Yq.at(token, i), y);
+      }
+      if (++i == end) u += jump, fresh = true;
+    }
   }
 }
 
-template <bool NEIGH, int TY>
-__global__ void __launch_bounds__(ROT_THREADS, ROT_BWD_CTAS) rotary_backward_kernel(const __grid_constant__ RotParams P, int team) {
+template <bool NEIGH, int TY, int NP>
+__global__ void __launch_bounds__(ROT_THREADS, NP == 4 ? ROT_BWD_CTAS : 2) rotary_backward_kernel(const __grid_constant__ RotParams P, int team) {
   __shared__ __align__(16) RotTables T;
   __shared__ float sums[ROT_WARPS][ROT_MAX_DIM];
   constexpr int SIZE = TY == PSK_BF16 ? 2 : 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slots = 32 / team, slot = lane / team;
-  const RotLane<NEIGH> G(lane % team, P);
+  const RotLane<NEIGH, NP> G(lane % team, P);
   const int nq = (P.side[0].heads + slots - 1) / slots, nk = (P.side[1].heads + slots - 1) / slots;
   const int lq = (P.side[0].heads - slot + slots - 1) / slots, lk = (P.side[1].heads - slot + slots - 1) / slots;
-  const int64_t jump = (int64_t)gridDim.x * ROT_WARPS;
-  int64_t token = (int64_t)blockIdx.x * ROT_WARPS + warp;
-  Rot8 dg[2];
+  const uint32_t jump = gridDim.x * ROT_WARPS, tokens = (uint32_t)P.tokens;
+  uint32_t token = blockIdx.x * ROT_WARPS + warp;
+  RotPairs<NP> dg[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) dg[0].a[j] = dg[0].b[j] = dg[1].a[j] = dg[1].b[j] = splat(0.0f);
-  RotRaw<TY> craw, xraw;
+  for (int j = 0; j < NP / 2; ++j) dg[0].a[j] = dg[0].b[j] = dg[1].a[j] = dg[1].b[j] = splat(0.0f);
+  RotRaw<TY, NP> craw, xraw;
   const auto walk = [&](int sd, int which) {
     const RotSide& S = P.side[sd];
     if (which == 0) return RotWalk(S.ct, S.ct_t, S.ct_h, slot, slots, G.first[0], SIZE);
     if (which == 1) return RotWalk(S.x, S.xt, S.xh, slot, slots, G.first[0], SIZE);
     return RotWalk(S.y, S.yt, S.yh, slot, slots, G.first[0], SIZE);
   };
-  const auto first = [&](int sd, int64_t t) {
+  const auto first = [&](int sd, uint32_t t) {
     G.load(walk(sd, 0).at(t, 0), 0 < (sd ? lk : lq), craw);
     G.load(walk(sd, 1).at(t, 0), P.rms && 0 < (sd ? lk : lq), xraw);
   };
-  if (token < P.tokens) {
+  if (token < tokens) {
     if (nq) first(0, token);
     else first(1, token);
   }
   rot_tables<NEIGH>(T, P);
-  for (; token < P.tokens; token += jump) {
-    rot_angles8(T, P, token, warp, lane);
-    float2 c[4], s[4];
+  int64_t pos = token < tokens ? rot_position(P, token) : 0;
+  for (; token < tokens; token += jump) {
+    rot_angles_at(T, P, pos, warp, lane);
+    if (token + jump < tokens) pos = rot_position(P, token + jump);
+    float2 c[NP / 2], s[NP / 2];
     G.of_pairs(T.cosine[warp], c), G.of_pairs(T.sine[warp], s);
     const auto side = [&](auto SD) {
       constexpr int sd = SD.value;
@@ -593,7 +632,7 @@ __global__ void __launch_bounds__(ROT_THREADS, ROT_BWD_CTAS) rotary_backward_ker
       const char *pc = C.at(token, 0), *px = X.at(token, 0);
       char* py = (char*)Y.at(token, 0);
       for (int i = 0; i < n; ++i) {
-        Rot8 v, x;
+        RotPairs<NP> v, x;
         G.widen(craw, v), G.widen(xraw, x);
         // the next step's, the other side's first, or the next token's
         if (i + 1 < n) {
@@ -602,23 +641,23 @@ __global__ void __launch_bounds__(ROT_THREADS, ROT_BWD_CTAS) rotary_backward_ker
           G.load(px, P.rms && i + 1 < mine, xraw);
         } else if (sd == 0 && nk) {
           first(1, token);
-        } else if (token + jump < P.tokens) {
+        } else if (token + jump < tokens) {
           if (nq) first(0, token + jump);
           else first(1, token + jump);
         }
         if (G.turns) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < NP / 2; ++j) {
             const float2 a = v.a[j], b = v.b[j];
             v.a[j] = __ffma2_rn(a, c[j], __fmul2_rn(b, s[j]));
             v.b[j] = __ffma2_rn(b, c[j], __fmul2_rn(a, make_float2(-s[j].x, -s[j].y)));
           }
         }
         if (P.rms) {
-          float2 ga[4], gb[4], sum = splat(0.0f), m = splat(0.0f);
+          float2 ga[NP / 2], gb[NP / 2], sum = splat(0.0f), m = splat(0.0f);
           G.of_pairs(T.gamma[sd][0], ga), G.of_pairs(T.gamma[sd][1], gb);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < NP / 2; ++j) {
             ga[j] = __fmul2_rn(v.a[j], ga[j]), gb[j] = __fmul2_rn(v.b[j], gb[j]);
             sum = __ffma2_rn(x.a[j], x.a[j], __ffma2_rn(x.b[j], x.b[j], sum));
             m = __ffma2_rn(ga[j], x.a[j], __ffma2_rn(gb[j], x.b[j], m));
@@ -631,7 +670,7 @@ __global__ void __launch_bounds__(ROT_THREADS, ROT_BWD_CTAS) rotary_backward_ker
           const float r = rsqrt_approx(fmaf(s1, P.inv_dim, P.eps));
           const float2 r2 = splat(r), mean = splat(-(s2 * r * P.inv_dim));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < NP / 2; ++j) {
             const float2 xa = __fmul2_rn(x.a[j], r2), xb = __fmul2_rn(x.b[j], r2);
             if (i < mine) {
               dg[sd].a[j] = __ffma2_rn(v.a[j], xa, dg[sd].a[j]);
@@ -658,7 +697,7 @@ __global__ void __launch_bounds__(ROT_THREADS, ROT_BWD_CTAS) rotary_backward_ker
     };
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < NP; ++i) {
       const float2 da = dg[sd].a[i >> 1], db = dg[sd].b[i >> 1];
       const float a = join(i & 1 ? da.y : da.x), b = join(i & 1 ? db.y : db.x);
       if (slot == 0 && G.there) sums[warp][G.column(0, i)] = a, sums[warp][G.column(1, i)] = b;
@@ -746,6 +785,12 @@ static bool heads_vec(const Heads& h) {
   return !h.there() || ((uintptr_t)h.p % 16 == 0 && (h.tokens <= 1 || h.ts % e == 0) && (h.heads <= 1 || h.hs % e == 0));
 }
 
+// Whether a token's stretch and the distance of tokens stay below 2^31 bytes.
+static bool heads_near(const Heads& h) {
+  const int64_t most = (1LL << 31) / dtype_size(h.dt) - 1;
+  return !h.there() || ((h.tokens <= 1 || h.ts <= most) && h.of_token() <= most - 32 * (h.heads > 1 ? h.hs : 0));
+}
+
 static View span_view(const void* p, uint64_t bytes) { return View{(uintptr_t)p, p && bytes ? 1 : 0, bytes, bytes}; }
 
 static int rot_check_common(int64_t tokens, const void* pos, int32_t pt, const float* freqs, int64_t dim, int64_t rot,
@@ -766,7 +811,11 @@ static int rot_check_common(int64_t tokens, const void* pos, int32_t pt, const f
   return PSK_OK;
 }
 
-static bool rot_vec(int64_t dim, int64_t rot) { return dim % 16 == 0 && rot % 16 == 0; }
+// The fast kernels' groups of columns, of four pairs or eight.
+static int rot_group(int64_t dim, int64_t rot) {
+  if (dim <= 256) return dim % 8 == 0 && rot % 8 == 0 ? 4 : 0;
+  return dim % 16 == 0 && rot % 16 == 0 ? 8 : 0;
+}
 
 // Lanes of a team (a power of two): one for each group of V pairs, a warp at most.
 static int rot_team(const RotParams& P, int V) {
@@ -827,10 +876,12 @@ extern "C" int psk_qk_norm_rotary(const void* q, const void* k, int32_t xt, int6
   P.pos64 = pt == PSK_I64, P.rms = norm == PSK_HEAD_NORM_RMS, P.neighbours = pairs == PSK_PAIRS_NEIGHBOURS;
   P.x_type = xt, P.y_type = yt, P.gamma_type = gt;
   P.eps = (float)eps, P.inv_dim = 1.0f / (float)dim;
-  const bool vec = rot_vec(dim, rot) && heads_vec(in[0]) && heads_vec(in[1]) && heads_vec(out[0]) && heads_vec(out[1]);
+  const int np = rot_group(dim, rot);
+  const bool vec = np && tokens * (hq + hk) < 1LL << 31 && heads_near(in[0]) && heads_near(in[1]) &&
+                   heads_near(out[0]) && heads_near(out[1]) && heads_vec(in[0]) && heads_vec(in[1]) && heads_vec(out[0]) && heads_vec(out[1]);
   cudaStream_t s = (cudaStream_t)stream;
   const bool fast = vec && xt == yt;
-  const int team = rot_team(P, fast ? 8 : 1), slots = 32 / team, per_sm = fast ? ROT_FWD_CTAS : 3;
+  const int team = rot_team(P, fast ? np : 1), slots = 32 / team, per_sm = !fast ? 3 : np == 4 ? ROT_FWD_CTAS : 2;
   const int64_t steps = (hq + slots - 1) / slots + (hk + slots - 1) / slots;
   const int64_t most = (int64_t)device_sm_count() * per_sm, warps = most * ROT_WARPS;
   // A token's heads go to one warp where tokens alone fill the GPU, else to several.
@@ -843,7 +894,8 @@ extern "C" int psk_qk_norm_rotary(const void* q, const void* k, int32_t xt, int6
   if (fast)
     with_dtype(xt, [&](auto TY) {
       return with_bool(P.neighbours != 0, [&](auto N) {
-        rotary_kernel<N.value, TY.value><<<grid, ROT_THREADS, 0, s>>>(P, team);
+        if (np == 4) rotary_kernel<N.value, TY.value, 4><<<grid, ROT_THREADS, 0, s>>>(P, team);
+        else rotary_kernel<N.value, TY.value, 8><<<grid, ROT_THREADS, 0, s>>>(P, team);
         return 0;
       });
     });
@@ -935,18 +987,21 @@ extern "C" int psk_qk_norm_rotary_backward(
   P.eps = (float)eps, P.inv_dim = 1.0f / (float)dim;
   P.part = sums ? (float*)workspace : nullptr;
   P.blocks = (int32_t)rot_blocks(tokens);
-  const bool vec = rot_vec(dim, rot) && heads_vec(cts[0]) && heads_vec(cts[1]) && heads_vec(out[0]) &&
+  const int np = rot_group(dim, rot);
+  const bool vec = np && tokens * (hq + hk) < 1LL << 31 && heads_near(cts[0]) && heads_near(cts[1]) &&
+                   heads_near(out[0]) && heads_near(out[1]) && heads_near(xs[0]) && heads_near(xs[1]) && heads_vec(cts[0]) && heads_vec(cts[1]) && heads_vec(out[0]) &&
                    heads_vec(out[1]) && (!rms || (heads_vec(xs[0]) && heads_vec(xs[1])));
   cudaStream_t s = (cudaStream_t)stream;
   const bool fast = vec && ct == dt && (!rms || xt == ct);
-  const int team = rot_team(P, fast ? 8 : 1);
-  const int64_t most = (int64_t)device_sm_count() * (fast ? ROT_BWD_CTAS : 2);
+  const int team = rot_team(P, fast ? np : 1);
+  const int64_t most = (int64_t)device_sm_count() * (fast && np == 4 ? ROT_BWD_CTAS : 2);
   if (P.blocks > most) P.blocks = (int32_t)most;
   const unsigned grid = (unsigned)P.blocks;
   if (fast)
     with_dtype(ct, [&](auto TY) {
       return with_bool(P.neighbours != 0, [&](auto N) {
-        rotary_backward_kernel<N.value, TY.value><<<grid, ROT_THREADS, 0, s>>>(P, team);
+        if (np == 4) rotary_backward_kernel<N.value, TY.value, 4><<<grid, ROT_THREADS, 0, s>>>(P, team);
+        else rotary_backward_kernel<N.value, TY.value, 8><<<grid, ROT_THREADS, 0, s>>>(P, team);
         return 0;
       });
     });

@@ -568,11 +568,15 @@ def _choice(table, v, what: str) -> int:
 
 def _weight(w, what: str, shape=None):
     """(leading dimension, layout) of a weight [in, out] whose rows or columns are contiguous."""
-    if len(w.shape) != 2:
+    size = w.shape
+    if len(size) != 2:
         raise ValueError(f"{what} must be a 2-D tensor")
-    if shape is not None and w.shape != shape:
-        raise ValueError(f"{what} has shape {tuple(w.shape)}, not {tuple(shape)}")
-    if w.is_contiguous() or w.stride(1) == 1 or w.stride(0) != 1:
+    if shape is not None and size != shape:
+        raise ValueError(f"{what} has shape {tuple(size)}, not {tuple(shape)}")
+    if w.is_contiguous():
+        return size[1], N.PSK_W_IN_OUT
+    stride = w.stride()
+    if stride[1] == 1 or stride[0] != 1:
         return _matrix(w, what), N.PSK_W_IN_OUT
     return _matrix(w.t(), what), N.PSK_W_OUT_IN
 
@@ -705,50 +709,54 @@ def psk_orthogonalize(xs, ys, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0
                                       (ctypes.c_double * len(flat))(*flat), steps, eps, scale, ws, wb, s))
 
 
-def _heads(t, what: str, shape=None):
-    """(tokens, heads, dim, token stride, head stride) of a [tokens, heads, dim] tensor (None: no heads)."""
-    if t is None:
-        return None
-    if len(t.shape) != 3 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{what} must be a [tokens, heads, dim] tensor" + (f" of shape {tuple(shape)}" if shape else ""))
-    ts, hs, es = t.stride()
-    if es != 1 and t.shape[2] > 1:
+def _heads(t, what: str, tokens: int, dim: int):
+    """(address, token stride, head stride, heads) of a [tokens, heads, dim] tensor."""
+    size, stride = t.shape, t.stride()
+    if len(size) != 3 or size[0] != tokens or size[2] != dim:
+        raise ValueError(f"{what} must be a [tokens, heads, dim] tensor of {tokens} tokens and heads of {dim}")
+    if stride[2] != 1 and dim > 1:
         raise ValueError(f"{what}: a head's columns must be contiguous")
-    return t.data_ptr(), ts, hs
+    return t.data_ptr(), stride[0], stride[1], size[1]
 
 
-def _qk(a, b, what: str, shape_a=None, shape_b=None):
+_NO_HEADS = (None, 0, 0, 0)
+
+
+def _qk(a, b, what: str, tokens: int, dim: int, hq: int, hk: int):
     """The C arguments of a pair of head tensors, either of them None."""
-    ha, hb = _heads(a, what + " of q", shape_a), _heads(b, what + " of k", shape_b)
-    if a is not None and b is not None and a.dtype != b.dtype:
+    pa, ta, sa, na = _NO_HEADS if a is None else _heads(a, what + " of q", tokens, dim)
+    pb, tb, sb, nb = _NO_HEADS if b is None else _heads(b, what + " of k", tokens, dim)
+    if (a is not None and na != hq) or (b is not None and nb != hk):
+        raise ValueError(f"{what}: {na} and {nb} heads, not {hq} and {hk}")
+    if a is None:
+        return pa, pb, 0 if b is None else _code(b, what), ta, sa, tb, sb
+    if b is not None and a.dtype is not b.dtype:
         raise TypeError(f"{what}: q's and k's must share one storage type")
-    t = a if a is not None else b
-    pa, ta, sa = ha or (None, 0, 0)
-    pb, tb, sb = hb or (None, 0, 0)
-    return pa, pb, 0 if t is None else _code(t, what), ta, sa, tb, sb
+    return pa, pb, _code(a, what), ta, sa, tb, sb
 
 
-def _rotary_rest(q, k, positions, freqs, gamma_q, gamma_k, norm, eps, pairs):
-    t = q if q is not None else k
+def _qk_sizes(q, k):
+    """(tokens, heads of q, heads of k, dim)."""
+    t = k if q is None else q
     if t is None:
         raise ValueError("q and k are both None")
-    if len(t.shape) != 3:
+    size = t.shape
+    if len(size) != 3:
         raise ValueError("q and k must be [tokens, heads, dim] tensors")
-    tokens, _, dim = t.shape
-    if q is not None and k is not None and (len(k.shape) != 3 or k.shape[0] != tokens or k.shape[2] != dim):
-        raise ValueError("q and k must have the same tokens and head size")
-    if gamma_q is not None and gamma_k is not None and gamma_q.dtype != gamma_k.dtype:
+    if q is None:
+        return size[0], 0, size[1], size[2]
+    return size[0], size[1], 0 if k is None else k.shape[1], size[2]
+
+
+def _rotary_rest(sizes, positions, freqs, gamma_q, gamma_k, norm, eps, pairs):
+    tokens, hq, hk, dim = sizes
+    g = gamma_k if gamma_q is None else gamma_q
+    if gamma_q is not None and gamma_k is not None and gamma_q.dtype is not gamma_k.dtype:
         raise TypeError("gamma_q and gamma_k must share one storage type")
-    g = gamma_q if gamma_q is not None else gamma_k
-    hq, hk = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
     nf = freqs.numel()
     return (tokens, hq, hk, dim, 2 * nf, _vector(positions, "positions", tokens), _id_code(positions, "positions"),
             _vector(freqs, "freqs", nf, True), _choice(_PAIRS, pairs, "pairs"), _choice(_HEAD_NORM, norm, "norm"), eps,
             _vector(gamma_q, "gamma_q", dim), _vector(gamma_k, "gamma_k", dim), 0 if g is None else _code(g, "gamma"))
-
-
-def _shape(t):
-    return None if t is None else t.shape
 
 
 def psk_qk_norm_rotary(q, k, yq, yk, positions, freqs, gamma_q=None, gamma_k=None, norm: str = "rms",
@@ -763,8 +771,9 @@ def psk_qk_norm_rotary(q, k, yq, yk, positions, freqs, gamma_q=None, gamma_k=Non
     s = _same_device(stream, positions, q, k, yq, yk, freqs, gamma_q, gamma_k)
     if (q is None) != (yq is None) or (k is None) != (yk is None):
         raise ValueError("q and yq, k and yk go together")
-    rest = _rotary_rest(q, k, positions, freqs, gamma_q, gamma_k, norm, eps, pairs)
-    N.check(N.lib().psk_qk_norm_rotary(*_qk(q, k, "x"), *_qk(yq, yk, "y", _shape(q), _shape(k)), *rest, s))
+    sizes = tokens, hq, hk, dim = _qk_sizes(q, k)
+    N.check(N.lib().psk_qk_norm_rotary(*_qk(q, k, "x", tokens, dim, hq, hk), *_qk(yq, yk, "y", tokens, dim, hq, hk),
+                                       *_rotary_rest(sizes, positions, freqs, gamma_q, gamma_k, norm, eps, pairs), s))
 
 
 def psk_qk_norm_rotary_backward_workspace(tokens: int, hq: int, hk: int, dim: int) -> int:
@@ -788,13 +797,13 @@ def psk_qk_norm_rotary_backward(cq, ck, q, k, dq, dk, positions, freqs, gamma_q=
         raise ValueError("cq and q, ck and k go together")
     if dgamma_q is not None and dgamma_k is not None and dgamma_q.dtype != dgamma_k.dtype:
         raise TypeError("dgamma_q and dgamma_k must share one storage type")
-    rest = _rotary_rest(cq, ck, positions, freqs, gamma_q, gamma_k, norm, eps, pairs)
-    dim = rest[3]
+    sizes = tokens, hq, hk, dim = _qk_sizes(cq, ck)
+    rest = _rotary_rest(sizes, positions, freqs, gamma_q, gamma_k, norm, eps, pairs)
     if norm == "none":
         q = k = None
-    g = dgamma_q if dgamma_q is not None else dgamma_k
+    g = dgamma_k if dgamma_q is None else dgamma_q
     ws, wb = _scratch(workspace)
     N.check(N.lib().psk_qk_norm_rotary_backward(
-        *_qk(cq, ck, "ct"), *_qk(q, k, "x", _shape(cq), _shape(ck)), *_qk(dq, dk, "dx", _shape(cq), _shape(ck)), *rest,
-        _vector(dgamma_q, "dgamma_q", dim), _vector(dgamma_k, "dgamma_k", dim), 0 if g is None else _code(g, "dgamma"),
-        ws, wb, s))
+        *_qk(cq, ck, "ct", tokens, dim, hq, hk), *_qk(q, k, "x", tokens, dim, hq, hk),
+        *_qk(dq, dk, "dx", tokens, dim, hq, hk), *rest, _vector(dgamma_q, "dgamma_q", dim),
+        _vector(dgamma_k, "dgamma_k", dim), 0 if g is None else _code(g, "dgamma"), ws, wb, s))
