@@ -28,7 +28,7 @@ OUT = os.path.join(HERE, "_build")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 CU_SOURCES = ["group.cu", "regions.cu", "lanes.cu", "adamw.cu", "dropout.cu", "embed.cu", "norm_bwd.cu",
-              "loss.cu", "matmul.cu", "linear.cu", "ortho.cu", "rotary.cu"]
+              "loss.cu", "matmul.cu", "linear.cu", "ortho.cu", "ortho_small.cu", "rotary.cu"]
 CPP_SOURCES = ["api.cpp"]
 
 NVCC_FLAGS = [

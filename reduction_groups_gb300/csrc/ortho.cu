@@ -23,6 +23,7 @@
 #include "common.cuh"
 #include "vec8.cuh"
 #include "mm.h"
+#include "ortho.h"
 #include "views.h"
 
 namespace psk {
@@ -185,6 +186,18 @@ __global__ void __launch_bounds__(256) ortho_begin_kernel(const __grid_constant_
   }
 }
 
+// A leaf's rows, one behind the other.
+__global__ void __launch_bounds__(256) ortho_copy_kernel(const __grid_constant__ OrthoTable T, int rows, int cols, int32_t xt,
+                                                         char* to) {
+  const int leaf = blockIdx.x;
+  const int64_t ld = T.ldx[leaf], at = (int64_t)leaf * rows * cols;
+  for (int i = threadIdx.x; i < rows * cols; i += 256) {
+    const int64_t e = (int64_t)(i / cols) * ld + i % cols;
+    if (xt == PSK_BF16) ((uint16_t*)to)[at + i] = ((const uint16_t*)T.x[leaf])[e];
+    else ((uint32_t*)to)[at + i] = ((const uint32_t*)T.x[leaf])[e];
+  }
+}
+
 struct OrthoLayout {
   uint64_t sums, factors, table, x0, x1, a, b, bytes;
   int64_t xsize, asize;         // elements of one plane
@@ -212,6 +225,30 @@ static OrthoLayout ortho_layout(int32_t leaves, int64_t rows, int64_t cols, int3
   L.b = take((uint64_t)leaves * planes * L.asize * 2);
   L.bytes = at;
   return L;
+}
+
+// One CTA a matrix: fifteen dependent products of one
+// tile or two are launches' latency otherwise ([64, 192] x 2 f32: 116 us).
+static bool ortho_is_small(int64_t rows, int64_t cols) {
+  const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
+  return m <= ORTHO_SMALL_M && n <= ORTHO_SMALL_N;
+}
+
+// Whether a result lies on another matrix's x.
+static bool ortho_crossed(const std::vector<View>& in, const std::vector<View>& out) {
+  std::vector<std::pair<uintptr_t, int>> at;             // the x's by their beginnings
+  uint64_t longest = 0;
+  for (size_t i = 0; i < in.size(); ++i) {
+    at.push_back({in[i].p, (int)i});
+    longest = longest > in[i].bytes() ? longest : in[i].bytes();
+  }
+  std::sort(at.begin(), at.end());
+  for (size_t j = 0; j < out.size(); ++j) {
+    const uintptr_t from = out[j].p > longest ? out[j].p - longest : 0, to = out[j].p + out[j].bytes();
+    for (auto it = std::lower_bound(at.begin(), at.end(), std::make_pair(from, -1)); it != at.end() && it->first < to; ++it)
+      if (it->second != (int)j && views_overlap(in[it->second], out[j])) return true;
+  }
+  return false;
 }
 
 static int ortho_check_sizes(int32_t leaves, int64_t rows, int64_t cols) {
@@ -261,9 +298,10 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
   static thread_local OrthoTable T;
   static thread_local OrthoTargets Y;
   const View vws{(uintptr_t)workspace, 1, L.bytes, L.bytes};
-  std::vector<View> out;
+  std::vector<View> out, in;
   try {
     out.reserve(n_leaves);
+    in.reserve(n_leaves);
   } catch (...) {
     return fail(PSK_E_ARG, "out of host memory");
   }
@@ -278,15 +316,27 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
     const View vx = view_of(f.x, rows, cols, f.ldx, dtype_size(xt)), vy = view_of(f.y, rows, cols, f.ldy, dtype_size(yt));
     if (views_overlap(vx, vws) || views_overlap(vy, vws)) return fail(PSK_E_ALIAS, "matrix %d overlaps the workspace", i);
     out.push_back(vy);
+    in.push_back(vx);
     T.x[i] = f.x, T.ldx[i] = f.ldx;
     Y.y[i] = f.y, Y.ldy[i] = f.ldy, Y.vec[i] = rows_vec8(f.y, yt, f.ldy, rows);
   }
+  const bool crossed = ortho_is_small(rows, cols) && ortho_crossed(in, out);
   std::sort(out.begin(), out.end(), [](const View& a, const View& b) { return a.p < b.p; });
   for (size_t i = 0; i < out.size(); ++i)
     for (size_t j = i + 1; j < out.size() && out[j].p < out[i].p + out[i].bytes(); ++j)
       if (views_overlap(out[i], out[j])) return fail(PSK_E_ALIAS, "two results overlap");
 
   cudaStream_t s = (cudaStream_t)stream;
+  if (ortho_is_small(rows, cols)) {
+    const char* copies = nullptr;
+    if (crossed) {                       // every x is read before the first y is written
+      copies = (const char*)workspace + L.x0;
+      ortho_copy_kernel<<<n_leaves, 256, 0, s>>>(T, (int)rows, (int)cols, xt, (char*)workspace + L.x0);
+      rc = check_launch("orthogonalisation's copies");
+      if (rc) return rc;
+    }
+    return ortho_small_launch(leaves, copies, n_leaves, rows, cols, xt, yt, coefficients, steps, eps, scale, s);
+  }
   char* ws = (char*)workspace;
   OrthoShape S{};
   S.rows = rows, S.cols = cols;

@@ -1504,7 +1504,10 @@ extern "C" int psk_device_status(uint32_t* status, int32_t reset) {
   unsigned int mv = 0;
   const int mrc = mm_status(&mv, reset != 0);
   if (mrc) return mrc;
-  *status = v | lv | tv | nv | mv;
+  unsigned int ov = 0;
+  const int orc = ortho_small_status(&ov, reset != 0);
+  if (orc) return orc;
+  *status = v | lv | tv | nv | mv | ov;
   return PSK_OK;
 }
 
