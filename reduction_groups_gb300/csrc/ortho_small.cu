@@ -15,22 +15,22 @@
 
 namespace psk {
 
-constexpr int OS_THREADS = 256;
+constexpr int OS_THREADS = 512;            // four warps for each quarter of the rows
 constexpr int OS_BLOCK = 128 * 128;        // bytes of 128 rows of 64 elements
 
 struct OrthoSmallParams {
-  const void* x[PSK_ORTHO_MAX_LEAVES];
-  void* y[PSK_ORTHO_MAX_LEAVES];
-  int64_t ldx[PSK_ORTHO_MAX_LEAVES], ldy[PSK_ORTHO_MAX_LEAVES];
   int32_t rows, cols, m, n, tall, xt, yt, steps;
   double eps, scale;
   float a[64], b[64], c[64];
 };
-
-__device__ __forceinline__ float os_load(const OrthoSmallParams& P, const void* x, int64_t ld, int r, int c) {
-  const int64_t i = P.tall ? (int64_t)c * ld + r : (int64_t)r * ld + c;
-  return P.xt == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)x)[i]) : ((const float*)x)[i];
-}
+// The leaves, with room for CAP of them: the parameters of a launch are copied
+// for every one.
+template <int CAP>
+struct OrthoSmallLeaves {
+  const void* x[CAP];
+  void* y[CAP];
+  int64_t ldx[CAP], ldy[CAP];
+};
 
 // Where 16 bytes (elements c .. c + 7 of row r) of a block of 64 columns stand, swizzled.
 __device__ __forceinline__ uint32_t os_at(int r, int c) { return (uint32_t)(r * 128 + (((c & 63) * 2) ^ ((r & 7) << 4))); }
@@ -51,13 +51,43 @@ __device__ __forceinline__ void os_store8(char* p, uint32_t apart, float* v) {
   }
 }
 
+// Calls f(row, column, element or 0) for a leaf's elements: rows by warps,
+// columns by lanes, sixteen loads a thread on their way at once.  (The loops
+// stay rolled: code that runs once or twice costs what it takes to fetch it.)
+template <typename F>
+__device__ __forceinline__ void os_each(const OrthoSmallParams& P, const void* x, int64_t ld, F&& f) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int r0 = warp; r0 < P.rows; r0 += 4 * (OS_THREADS / 32))
+#pragma unroll 1
+    for (int c0 = lane; c0 < P.cols; c0 += 128) {
+      float v[4][4];
+      const char* p = (const char*)x + ((int64_t)r0 * ld + c0) * (P.xt == PSK_BF16 ? 2 : 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[i][j] = 0.0f;
+          if (r0 + i * (OS_THREADS / 32) < P.rows && c0 + 32 * j < P.cols) {
+            const int64_t e = (int64_t)i * (OS_THREADS / 32) * ld + 32 * j;
+            v[i][j] = P.xt == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)p)[e]) : ((const float*)p)[e];
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f(r0 + i * (OS_THREADS / 32), c0 + 32 * j, v[i][j]);
+    }
+}
+
 // PLANES: of each factor of a product.
-template <int PLANES>
-__global__ void __launch_bounds__(OS_THREADS, 1) ortho_small_kernel(const __grid_constant__ OrthoSmallParams P) {
+template <int PLANES, int CAP>
+__global__ void __launch_bounds__(OS_THREADS, 1)
+    ortho_small_kernel(const __grid_constant__ OrthoSmallParams P, const __grid_constant__ OrthoSmallLeaves<CAP> L) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t done;
   __shared__ uint32_t tmem_slot;
-  __shared__ double part[8];
+  __shared__ double part[OS_THREADS / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   char* base = (char*)smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
   const int blocks = (P.n + 63) / 64;                       // of X's columns
@@ -65,8 +95,8 @@ __global__ void __launch_bounds__(OS_THREADS, 1) ortho_small_kernel(const __grid
   char* xs = base;                                          // [part][block][128 rows]
   char* as = base + 2 * x_plane;
   const uint32_t xa = smem_addr(xs), aa = smem_addr(as);
-  const void* x = P.x[blockIdx.x];
-  const int64_t ldx = P.ldx[blockIdx.x];
+  const void* x = L.x[blockIdx.x];
+  const int64_t ldx = L.ldx[blockIdx.x];
   if (warp == 0 && lane == 0) {
     mbar_init(&done, 1);
     fence_barrier_init();
@@ -80,42 +110,42 @@ __global__ void __launch_bounds__(OS_THREADS, 1) ortho_small_kernel(const __grid
   // their smaller products.
   constexpr uint32_t SMALL = 256;
 
-  // ---- the norm, then X = G S / (norm + eps): rows by warps, lanes along the leaf's rows
+  // ---- X = G S / (norm + eps), zeros around it
+  for (uint32_t i = threadIdx.x; i < 2 * x_plane / 16; i += OS_THREADS) ((uint4*)xs)[i] = make_uint4(0, 0, 0, 0);
   float s = 0.0f, big = 0.0f;
-  for (int i = threadIdx.x; i < P.rows * P.cols; i += OS_THREADS) {
-    const int r = i / P.cols;
-    const int64_t e = (int64_t)r * ldx + (i - r * P.cols);
-    const float v = P.xt == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)x)[e]) : ((const float*)x)[e];
-    if (fabsf(v) > 1.1e15f) {
-      const float u = v * 5.421010862427522e-20f;           // squares that would leave f32
-      big = fmaf(u, u, big);
-    } else {
-      s = fmaf(v, v, s);
-    }
-  }
+  os_each(P, x, ldx, [&](int, int, float v) {
+    // squares that would leave f32 are taken times 2^-128
+    const bool over = fabsf(v) > 1.1e15f;
+    const float u = over ? v * 5.421010862427522e-20f : 0.0f, w = over ? 0.0f : v;
+    big = fmaf(u, u, big), s = fmaf(w, w, s);
+  });
   double total = (double)s + (double)big * 3.402823669209385e38;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
   if (lane == 0) part[warp] = total;
   __syncthreads();
   total = 0.0;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) total += part[w];
+  for (int w = 0; w < OS_THREADS / 32; ++w) total += part[w];
   const float f = (float)(1024.0 / (sqrt(total) + P.eps));
-  for (int i = threadIdx.x; i < 128 * blocks * 8; i += OS_THREADS) {
-    // a leaf's row runs along c, a tall one's along r
-    const int r = P.tall ? i & 127 : i / (blocks * 8), c = (P.tall ? i >> 7 : i % (blocks * 8)) * 8;
-    float v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = r < P.m && c + k < P.n ? os_load(P, x, ldx, r, c + k) * f : 0.0f;
-    os_store8<2>(xs + (c >> 6) * OS_BLOCK + os_at(r, c), x_plane, v);
-  }
+  // Where element (row, column) of the leaf stands in X.
+  const auto at = [&](int lr, int lc) {
+    const int r = P.tall ? lc : lr, c = P.tall ? lr : lc;
+    return xs + (c >> 6) * OS_BLOCK + os_at(r, c & ~7) + (c & 7) * 2;
+  };
+  os_each(P, x, ldx, [&](int lr, int lc, float v) {
+    if (lr >= P.rows || lc >= P.cols) return;
+    const float t = v * f;
+    const uint32_t w = f32x2_to_f16x2(t, 0.0f);
+    char* q = at(lr, lc);
+    *(uint16_t*)q = (uint16_t)w;
+    *(uint16_t*)(q + x_plane) = (uint16_t)f32x2_to_f16x2(t - f16x2_to_f32(w).x, 0.0f);
+  });
 
   const uint32_t idesc = (1u << 4) | ((uint32_t)(128 >> 4) << 24);                     // fp16, 128 rows, K-major
   const uint32_t square = idesc | ((uint32_t)(128 >> 3) << 17);
   const int wide_n = (P.n + 15) / 16 * 16;
   const uint32_t wide = idesc | (1u << 16) | ((uint32_t)(wide_n >> 3) << 17);          // B MN-major
-  const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+  const int row = (warp & 3) * 32 + lane, share = (warp >> 2) * 32;
   const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
   const float unit = 1.0f / 1024.0f;
   uint32_t phase = 0;
@@ -159,42 +189,40 @@ __global__ void __launch_bounds__(OS_THREADS, 1) ortho_small_kernel(const __grid
   };
 
   for (int step = 0; step < P.steps && ok; ++step) {
-    float af[64];                          // this thread's half row of A S
+    float af[32];                          // this thread's share of a row of A S
     multiply(xa, x_plane, xa, x_plane, (P.n + 15) / 16, square, false);
     if (!ok) break;
 #pragma unroll
-    for (int c = 0; c < 64; c += 16) {
-      take16(half * 64 + c, af + c);
+    for (int c = 0; c < 32; c += 16) {
+      take16(share + c, af + c);
 #pragma unroll
       for (int h = 0; h < 16; h += 8) {
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = af[c + h + k] *= unit;
-        os_store8<PLANES>(as + half * OS_BLOCK + os_at(row, c + h), a_plane, v);
+        os_store8<PLANES>(as + (share >> 6) * OS_BLOCK + os_at(row, share + c + h), a_plane, v);
       }
     }
     multiply(aa, a_plane, aa, a_plane, 8, square, false);
     if (!ok) break;
     const float b = P.b[step], cu = P.c[step] * unit;
 #pragma unroll
-    for (int c = 0; c < 64; c += 16) {
+    for (int c = 0; c < 32; c += 16) {
       float v[16];
-      take16(half * 64 + c, v);
+      take16(share + c, v);
 #pragma unroll
       for (int h = 0; h < 16; h += 8) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[h + k] = fmaf(b, af[c + h + k], v[h + k] * cu);
-        os_store8<PLANES>(as + half * OS_BLOCK + os_at(row, c + h), a_plane, v + h);
+        os_store8<PLANES>(as + (share >> 6) * OS_BLOCK + os_at(row, share + c + h), a_plane, v + h);
       }
     }
     multiply(aa, a_plane, xa, x_plane, 8, wide, true);
     if (!ok) break;
     const bool last = step + 1 == P.steps;
     const float out = last ? (float)(P.scale / 1024.0) : 1.0f, a = P.a[step] * out, u = unit * out;
-    void* y = P.y[blockIdx.x];
-    const int64_t ldy = P.ldy[blockIdx.x];
 #pragma unroll 1
-    for (int c = half * 16; c < wide_n; c += 32) {
+    for (int c = share / 2; c < wide_n; c += 64) {
       float v[16];
       take16(c, v);
 #pragma unroll
@@ -208,18 +236,34 @@ __global__ void __launch_bounds__(OS_THREADS, 1) ortho_small_kernel(const __grid
           v[h + 2 * k] = fmaf(a, e.x, fmaf(a, g.x, v[h + 2 * k] * u));
           v[h + 2 * k + 1] = fmaf(a, e.y, fmaf(a, g.y, v[h + 2 * k + 1] * u));
         }
-        if (!last) os_store8<2>(q, x_plane, v + h);
-      }
-      if (last && row < P.m) {
+        if (!last) {
+          os_store8<2>(q, x_plane, v + h);
+        } else {                           // f32 in two halves
+          uint32_t top[4], low[4];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (c + k < P.n) {
-            const int64_t i = P.tall ? (int64_t)(c + k) * ldy + row : (int64_t)row * ldy + c + k;
-            if (P.yt == PSK_BF16) ((uint16_t*)y)[i] = f32_to_bf16_bits(v[k]);
-            else ((float*)y)[i] = v[k];
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t e = __float_as_uint(v[h + 2 * k]), g = __float_as_uint(v[h + 2 * k + 1]);
+            top[k] = e >> 16 | (g & 0xFFFF0000u), low[k] = (e & 0xFFFFu) | g << 16;
           }
+          *(uint4*)q = make_uint4(top[0], top[1], top[2], top[3]);
+          *(uint4*)(q + x_plane) = make_uint4(low[0], low[1], low[2], low[3]);
+        }
       }
     }
+  }
+  // ---- the result: rows by warps, columns by lanes
+  __syncthreads();
+  if (ok) {
+    void* y = L.y[blockIdx.x];
+    const int64_t ldy = L.ldy[blockIdx.x];
+    for (int lr = warp; lr < P.rows; lr += OS_THREADS / 32)
+#pragma unroll 4
+      for (int lc = lane; lc < P.cols; lc += 32) {
+        const char* q = at(lr, lc);
+        const float v = __uint_as_float((uint32_t) * (const uint16_t*)q << 16 | *(const uint16_t*)(q + x_plane));
+        if (P.yt == PSK_BF16) ((uint16_t*)y)[lr * ldy + lc] = f32_to_bf16_bits(v);
+        else ((float*)y)[lr * ldy + lc] = v;
+      }
   }
   __syncwarp();
   fence_before();
@@ -228,12 +272,25 @@ __global__ void __launch_bounds__(OS_THREADS, 1) ortho_small_kernel(const __grid
   if (warp == 1) tmem_free<1>(tmem, 512);
 }
 
-int ortho_small_launch(const psk_ortho_leaf* leaves, const char* copies, int n_leaves, int64_t rows, int64_t cols, int32_t xt, int32_t yt,
-                       const double* coefficients, int32_t steps, double eps, double scale, cudaStream_t stream) {
-  static thread_local OrthoSmallParams P;
-  for (int i = 0; i < n_leaves; ++i)
-    P.x[i] = copies ? copies + i * rows * cols * dtype_size(xt) : leaves[i].x, P.ldx[i] = copies ? cols : leaves[i].ldx,
-    P.y[i] = leaves[i].y, P.ldy[i] = leaves[i].ldy;
+template <int PLANES, int CAP>
+static void launch_small(const OrthoSmallParams& P, const psk_ortho_leaf* leaves, const char* copies, int count, int smem,
+                         cudaStream_t stream) {
+  static thread_local OrthoSmallLeaves<CAP> L;
+  for (int i = 0; i < count; ++i) {
+    const psk_ortho_leaf& f = leaves[i];
+    L.x[i] = copies ? copies + (int64_t)i * P.rows * P.cols * dtype_size(P.xt) : f.x;
+    L.ldx[i] = copies ? P.cols : f.ldx;
+    L.y[i] = f.y, L.ldy[i] = f.ldy;
+  }
+  static bool limit[PSK_MAX_DEVICES] = {};
+  smem_limit_once((const void*)ortho_small_kernel<PLANES, CAP>, 12 * OS_BLOCK + 1024, limit);
+  ortho_small_kernel<PLANES, CAP><<<count, OS_THREADS, smem, stream>>>(P, L);
+}
+
+int ortho_small_launch(const psk_ortho_leaf* leaves, const char* copies, int n_leaves, int64_t rows, int64_t cols, int32_t xt,
+                       int32_t yt, const double* coefficients, int32_t steps, double eps, double scale,
+                       cudaStream_t stream) {
+  OrthoSmallParams P{};
   P.rows = (int32_t)rows, P.cols = (int32_t)cols;
   P.tall = rows > cols;
   P.m = P.tall ? (int32_t)cols : (int32_t)rows, P.n = P.tall ? (int32_t)rows : (int32_t)cols;
@@ -242,14 +299,13 @@ int ortho_small_launch(const psk_ortho_leaf* leaves, const char* copies, int n_l
     P.a[i] = (float)coefficients[3 * i], P.b[i] = (float)coefficients[3 * i + 1], P.c[i] = (float)coefficients[3 * i + 2];
   const int blocks = (P.n + 63) / 64, planes = yt == PSK_F32 ? 2 : 1;
   const int smem = 2 * blocks * OS_BLOCK + planes * 2 * OS_BLOCK + 1024;
-  static bool limit1[PSK_MAX_DEVICES] = {}, limit2[PSK_MAX_DEVICES] = {};
-  constexpr int MOST = 2 * 4 * OS_BLOCK + 4 * OS_BLOCK + 1024;
-  if (planes == 2) {
-    smem_limit_once((const void*)ortho_small_kernel<2>, MOST, limit2);
-    ortho_small_kernel<2><<<n_leaves, OS_THREADS, smem, stream>>>(P);
+  if (n_leaves <= 16) {
+    if (planes == 2) launch_small<2, 16>(P, leaves, copies, n_leaves, smem, stream);
+    else launch_small<1, 16>(P, leaves, copies, n_leaves, smem, stream);
+  } else if (planes == 2) {
+    launch_small<2, PSK_ORTHO_MAX_LEAVES>(P, leaves, copies, n_leaves, smem, stream);
   } else {
-    smem_limit_once((const void*)ortho_small_kernel<1>, MOST, limit1);
-    ortho_small_kernel<1><<<n_leaves, OS_THREADS, smem, stream>>>(P);
+    launch_small<1, PSK_ORTHO_MAX_LEAVES>(P, leaves, copies, n_leaves, smem, stream);
   }
   return check_launch("small orthogonalisation kernel");
 }
