@@ -336,6 +336,27 @@ __device__ __forceinline__ void finish16(const MMProblem& P, int32_t matrix, int
   }
 }
 
+// Columns first, first + step, ... of the sums.
+__device__ __forceinline__ void column_sums(const MMColumnSums& J, int64_t first, int64_t step) {
+  if (!J.out) return;
+  for (int64_t c = first; c < J.cols; c += step) {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int b = 0;
+    for (; b + 4 <= J.blocks; b += 4)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += J.parts[(int64_t)(b + i) * J.cols + c];
+    for (; b < J.blocks; ++b) s[0] += J.parts[(int64_t)b * J.cols + c];
+    const float v = (s[0] + s[1]) + (s[2] + s[3]);
+    if (J.dt == PSK_BF16) {
+      uint16_t* q = (uint16_t*)J.out + c;
+      *q = f32_to_bf16_bits(J.add ? bf16_bits_to_f32(*q) + v : v);
+    } else {
+      float* q = (float*)J.out + c;
+      *q = J.add ? *q + v : v;
+    }
+  }
+}
+
 // ------------------------------------------------------------------- kernel
 
 // KIND: an activation with every matrix in bf16, 32-byte aligned rows and n a
@@ -487,23 +508,7 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
     }
   } else if (warp == 3) {
     // ---- columns' sums joined, beside the products
-    const MMColumnSums& J = G.sums;
-    for (int64_t c = (int64_t)blockIdx.x * 32 + lane; J.out && c < J.cols; c += (int64_t)gridDim.x * 32) {
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      int b = 0;
-      for (; b + 4 <= J.blocks; b += 4)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] += J.parts[(int64_t)(b + i) * J.cols + c];
-      for (; b < J.blocks; ++b) s[0] += J.parts[(int64_t)b * J.cols + c];
-      const float v = (s[0] + s[1]) + (s[2] + s[3]);
-      if (J.dt == PSK_BF16) {
-        uint16_t* q = (uint16_t*)J.out + c;
-        *q = f32_to_bf16_bits(J.add ? bf16_bits_to_f32(*q) + v : v);
-      } else {
-        float* q = (float*)J.out + c;
-        *q = J.add ? *q + v : v;
-      }
-    }
+    column_sums(G.sums, (int64_t)blockIdx.x * 32 + lane, (int64_t)gridDim.x * 32);
   } else if (warp >= 4) {
     // ---- epilogue: a warp's 32 accumulator rows (set by its number), a share of the columns
     constexpr int COLS = BN * 4 / MMWarps<SUM>::EPI;
@@ -588,49 +593,93 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
   if (warp == 2) tmem_free<CG>(tmem, 2 * S::ACC);
 }
 
-// -------------------------------------------------------------- few rows
+// -------------------------------------------------------------- few tiles
 //
-// For up to 64 rows of x the weights' bytes are the time: the product is taken
-// the other way round, 128 columns of w as the tensor core's rows and the rows
-// of x as its N, and the CTAs of a cluster share the summed axis, so that
-// every SM has its part of w on the way at once.  Their accumulators meet in
-// shared memory and are added in the cluster's order; a CTA finishes its share
-// of the elements, lanes on neighbouring columns of y.
-template <int BN>
-struct ThinShape {
-  static constexpr int STAGE = MM_A_BYTES + BN * MM_BK * 2;
-  static constexpr int STAGES = 8;
-  static constexpr int SMEM = STAGES * STAGE + 1024;
-  static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
+// A CTA is fed at 64 bytes a clock, so a product of few tiles takes what one
+// tile's operands take, while most SMs idle.  Here the CTAs of a cluster share
+// a tile's summed axis, so that more SMs have a part of it on the way at once.
+// Their accumulators meet in shared memory and are added in the cluster's
+// order; a CTA finishes its share of the elements.  The product is taken the
+// other way round, 128 columns of the second operand as the tensor core's rows
+// and BN rows of the first as its N: for few rows of x the weights' bytes are
+// the time, and lanes hold neighbouring columns of y.
+template <int BN, bool SUM>
+struct SplitShape {
+  static constexpr int B_BYTES = BN * MM_BK * 2, STAGE = MM_A_BYTES + B_BYTES;
+  static constexpr int STAGES = BN < 128 ? 8 : 6;                // with SUM as many as the planes leave room for
+  static constexpr int RING = SUM ? 224 * 1024 : STAGES * STAGE;
+  static constexpr int SMEM = RING + 1024;
+  static constexpr int ACC = SUM ? 2 * BN : BN, BUFS = SUM ? 2 : 1;
+  static constexpr int TMEM_COLS = BUFS * ACC < 32 ? 32 : BUFS * ACC;
 };
-constexpr int THIN_THREADS = 192;
+constexpr int SPLIT_THREADS = 320;
+constexpr int SPLIT_ROW = 132;             // floats of a column of the accumulator in shared memory
 
-__device__ __forceinline__ float load_cluster(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-               : "=f"(v)
+struct SplitParams {
+  MMProblem q;                             // a: the columns' operand, b: the rows'
+  MMColumnSums sums;
+  int32_t split, row_tiles, stages, slot_bytes;
+};
+
+__device__ __forceinline__ float4 load_cluster(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(addr), "r"(rank)
                : "memory");
   return v;
 }
 
-template <int BN>
-__global__ void __launch_bounds__(THIN_THREADS, 1) mm_thin_kernel(const __grid_constant__ MMProblem P, int split) {
-  using S = ThinShape<BN>;
+__device__ __forceinline__ void load4_rt(const void* p, int32_t dt, int64_t i, int n, float* v) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = k < n ? load1_rt(p, dt, i + k) : 0.0f;
+}
+__device__ __forceinline__ void store4_rt(void* p, int32_t dt, int64_t i, int n, const float* v) {
+  if (dt == PSK_BF16) {
+    uint16_t* q = (uint16_t*)p + i;
+    if (n == 4 && (uintptr_t)q % 8 == 0) {
+      *(uint2*)q = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) q[k] = f32_to_bf16_bits(v[k]);
+  } else {
+    float* q = (float*)p + i;
+    if (n == 4 && (uintptr_t)q % 16 == 0) {
+      *(float4*)q = make_float4(v[0], v[1], v[2], v[3]);
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) q[k] = v[k];
+  }
+}
+
+template <int BN, bool SUM>
+__global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid_constant__ SplitParams G) {
+  using S = SplitShape<BN, SUM>;
+  const MMProblem& P = G.q;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[S::STAGES], empty[S::STAGES], acc_full, drain;
+  __shared__ uint64_t full[S::STAGES], empty[S::STAGES], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, split = G.split;
   const uint32_t rank = cluster_rank();
-  const int32_t tile = blockIdx.x / split;
+  const int32_t tile = blockIdx.x / split, tc = tile / G.row_tiles, tr = tile - tc * G.row_tiles;
   const int32_t k0 = (int32_t)((int64_t)P.kblocks * rank / split), k1 = (int32_t)((int64_t)P.kblocks * (rank + 1) / split);
+  const int stages = SUM ? G.stages : S::STAGES, na = SUM ? P.na : 1, nb = SUM ? P.nb : 1;
+  const uint32_t slot_bytes = SUM ? G.slot_bytes : S::STAGE;
+  const int32_t chunk = SUM ? P.chunk : P.kblocks;
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < S::STAGES; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(&acc_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], SPLIT_THREADS / 32 - 2);
+    }
     mbar_init(&drain, 1);
     fence_barrier_init();
   }
@@ -639,6 +688,7 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) mm_thin_kernel(const __grid_c
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_slot;
+  // set up beside the kernel before it; its results, and the memory it reads, from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -647,83 +697,165 @@ __global__ void __launch_bounds__(THIN_THREADS, 1) mm_thin_kernel(const __grid_c
     int issued = 0;
     bool ok = true;
     for (int32_t kb = k0; kb < k1; ++kb, ++issued) {
-      const int s = issued % S::STAGES;
-      if (!mbar_wait(&empty[s], ((issued / S::STAGES) & 1) ^ 1) || (drop >= 0 && issued >= drop)) {
+      const int s = issued % stages;
+      if (!mbar_wait(&empty[s], ((issued / stages) & 1) ^ 1) || (drop >= 0 && issued >= drop)) {
         ok = false;
         break;
       }
-      mbar_arrive_expect_tx(&full[s], S::STAGE);
-      const uint32_t a = ring + s * S::STAGE, bar = smem_addr(&full[s]);
-      if (P.a_k) {
-        tma_box<1>(a, &P.ta, kb * MM_BK, tile * 128, 0, bar);
-      } else {
-        tma_box<1>(a, &P.ta, tile * 128, kb * MM_BK, 0, bar);
-        tma_box<1>(a + MM_A_BYTES / 2, &P.ta, tile * 128 + 64, kb * MM_BK, 0, bar);
+      mbar_arrive_expect_tx(&full[s], na * MM_A_BYTES + nb * S::B_BYTES);
+      uint32_t at = ring + s * slot_bytes;
+      const uint32_t bar = smem_addr(&full[s]);
+      for (int p = 0; p < na; ++p, at += MM_A_BYTES) {
+        if (P.a_k) {
+          tma_box<1>(at, &P.ta, kb * MM_BK, tc * 128, p, bar);
+        } else {
+          tma_box<1>(at, &P.ta, tc * 128, kb * MM_BK, p, bar);
+          tma_box<1>(at + MM_A_BYTES / 2, &P.ta, tc * 128 + 64, kb * MM_BK, p, bar);
+        }
       }
-      tma_box<1>(a + MM_A_BYTES, &P.tb, kb * MM_BK, 0, 0, bar);
+      for (int p = 0; p < nb; ++p, at += S::B_BYTES) {
+        if (P.b_k) {
+          tma_box<1>(at, &P.tb, kb * MM_BK, tr * BN, p, bar);
+        } else {
+#pragma unroll
+          for (int j = 0; j < BN / 64; ++j)
+            tma_box<1>(at + j * (64 * MM_BK * 2), &P.tb, tr * BN + j * 64, kb * MM_BK, p, bar);
+        }
+      }
     }
     if (!ok)
-      for (int i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
-        mbar_wait(&full[i % S::STAGES], (i / S::STAGES) & 1);
+      for (int i = issued > stages ? issued - stages : 0; i < issued; ++i) mbar_wait(&full[i % stages], (i / stages) & 1);
   } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (P.a_k ? 0u : 1u << 15) | ((uint32_t)(BN >> 3) << 17) |
-                           ((uint32_t)(128 >> 4) << 24);
-    const uint32_t a_step = (P.a_k ? 32u : 2048u) >> 4;
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (P.a_k ? 0u : 1u << 15) | (P.b_k ? 0u : 1u << 16) |
+                           ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+    const uint32_t a_step = (P.a_k ? 32u : 2048u) >> 4, b_step = (P.b_k ? 32u : 2048u) >> 4;
     bool ok = true;
-    for (int32_t i = 0; i < k1 - k0; ++i) {
-      const int s = i % S::STAGES;
-      if (!mbar_wait(&full[s], (i / S::STAGES) & 1)) {
+    int i = 0;
+    for (int n = 0; ok && i < k1 - k0; ++n) {
+      const int buf = SUM ? n & 1 : 0;
+      if (SUM && !mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1)) {
         ok = false;
         break;
       }
       fence_after();
-      const uint32_t a = ring + s * S::STAGE;
-      const uint64_t da = operand_desc(a, MM_A_BYTES / 2), db = operand_desc(a + MM_A_BYTES, 64 * MM_BK * 2);
+      const uint32_t d = tmem + buf * S::ACC;
+      const int end = k1 - k0 - i < chunk ? k1 - k0 : i + chunk;
+      for (bool fresh = true; i < end; ++i, fresh = false) {
+        const int s = i % stages;
+        if (!mbar_wait(&full[s], (i / stages) & 1)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint32_t at = ring + s * slot_bytes;
+        for (int p = 0; p < (SUM ? P.pairs : 1); ++p) {
+          const bool small = SUM && p + 1 < P.pairs;
+          const uint64_t da = operand_desc(at + (SUM ? P.pa[p] : 0) * MM_A_BYTES, MM_A_BYTES / 2);
+          const uint64_t db = operand_desc(at + na * MM_A_BYTES + (SUM ? P.pb[p] : 0) * S::B_BYTES, 64 * MM_BK * 2);
 #pragma unroll
-      for (int j = 0; j < MM_BK / 16; ++j)
-        mma_16<1>(tmem, da + (uint64_t)(j * a_step), db + (uint64_t)(j * 2), idesc, (i | j) != 0);
-      mma_commit<1>(&empty[s]);
+          for (int j = 0; j < MM_BK / 16; ++j)
+            mma_16<1>(small ? d + BN : d, da + (uint64_t)(j * a_step), db + (uint64_t)(j * b_step), idesc,
+                      !fresh || j != 0 || (small && p > 0));
+        }
+        mma_commit<1>(&empty[s]);
+      }
+      if (ok) mma_commit<1>(&acc_full[buf]);
     }
-    if (ok) {
-      mma_commit<1>(&acc_full);
-    } else {
+    if (!ok) {
       mma_commit<1>(&drain);
       mbar_wait(&drain, 0);
     }
   }
   __syncwarp();
-  // Every part of the ring has been used up once the accumulator is there: it takes the sums, column after column.
+  // Every part of the ring has been used up once the last accumulator is there:
+  // it takes the sums, column after column.
   float* part = (float*)(smem_raw + (ring - smem_addr(smem_raw)));
-  if (warp >= 2 && __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full, 0))) {
-    fence_after();
-    const int row = (warp & 3) * 32;
+  if (warp >= 2) {
+    constexpr int MINE = BN < 32 ? 1 : BN / 32;          // sixteens of columns of this warp's
+    const int row = (warp & 3) * 32, share = (warp - 2) / 4;
+    const uint32_t mine = tmem + ((uint32_t)row << 16);
+    if constexpr (SUM) {
+      float sum[MINE * 16];
+      bool ok = true;
+      int n = 0;
+      for (int32_t k = k0; k < k1; k += chunk, ++n) {
+        const int buf = n & 1;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[buf], (n >> 1) & 1));
+        if (!ok) break;
+        fence_after();
 #pragma unroll
-    for (int c = 0; c < BN; c += 16) {
-      float v[16];
-      tmem_load16(tmem + ((uint32_t)row << 16) + c, v);
+        for (int c = 0; c < MINE; ++c) {
+          float v[16], w[16];
+          const int at = (share + 2 * c) * 16;
+          tmem_load16(mine + buf * S::ACC + BN + at, w);
+          tmem_load16(mine + buf * S::ACC + at, v);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) part[(c + k) * 128 + row + lane] = v[k];
+          for (int j = 0; j < 16; ++j) sum[16 * c + j] = n ? sum[16 * c + j] + (v[j] + w[j]) : v[j] + w[j];
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      }
+      // (all of them: the ring is another's until every warp has its last sums)
+      named_barrier(1, SPLIT_THREADS - 64);
+      if (ok) {
+#pragma unroll
+        for (int c = 0; c < MINE; ++c)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part[((share + 2 * c) * 16 + j) * SPLIT_ROW + row + lane] = sum[16 * c + j];
+      }
+    } else if (__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[0], 0))) {
+      fence_after();
+#pragma unroll 1
+      for (int c = share * 16; c < BN; c += 32) {
+        float v[16];
+        __syncwarp();
+        tmem_load16(mine + c, v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) part[(c + k) * SPLIT_ROW + row + lane] = v[k];
+      }
+      fence_before();
     }
-    fence_before();
   }
   __syncwarp();
   cluster_sync_all();
   fence_after();
   if (warp == 1) tmem_free<1>(tmem, S::TMEM_COLS);
   const MMEpilogue& E = P.e;
-  const int rows = (int)P.n, total = 128 * rows;                       // P.m: columns of y
-  const int from = (int)((int64_t)total * rank / split), to = (int)((int64_t)total * (rank + 1) / split);
-  for (int i = from + threadIdx.x; i < to; i += THIN_THREADS) {
-    const int64_t c = (int64_t)tile * 128 + (i & 127), r = i >> 7;
+  // P.m: columns of y, P.n: its rows; four columns a thread
+  const int rows = P.n - (int64_t)tr * BN < BN ? (int)(P.n - (int64_t)tr * BN) : BN, total = 32 * rows;
+  const int from = total * (int)rank / split, to = total * (int)(rank + 1) / split;
+#pragma unroll 1
+  for (int i = from + threadIdx.x; i < to; i += SPLIT_THREADS) {
+    const int64_t c = (int64_t)tc * 128 + (i & 31) * 4, r = (int64_t)tr * BN + (i >> 5);
     if (c >= P.m) continue;
-    float v = load_cluster(smem_addr(part + i), 0);
-    for (int q = 1; q < split; ++q) v += load_cluster(smem_addr(part + i), q);
-    if (E.bias) v += load1_rt(E.bias, E.bt, c);
-    if (E.z) store1_rt(E.z, E.zt, r * E.ldz + c, v);
-    float t[2] = {v, v};
-    act_rt<2>(t, E.act);
-    store1_rt(E.y, E.yt, r * E.ldy + c, E.res ? t[0] + load1_rt(E.res, E.rt, r * E.ldr + c) : t[0]);
+    const int n = P.m - c < 4 ? (int)(P.m - c) : 4;
+    const uint32_t at = smem_addr(part + (i >> 5) * SPLIT_ROW + (i & 31) * 4);
+    float4 parts[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < split) parts[q] = load_cluster(at, q);
+    float res[4], t[4];
+    if (E.res) load4_rt(E.res, E.rt, r * E.ldr + c, n, res);
+    t[0] = parts[0].x, t[1] = parts[0].y, t[2] = parts[0].z, t[3] = parts[0].w;
+#pragma unroll
+    for (int q = 1; q < 8; ++q)
+      if (q < split) t[0] += parts[q].x, t[1] += parts[q].y, t[2] += parts[q].z, t[3] += parts[q].w;
+    if (E.bias) {
+      float b[4];
+      load4_rt(E.bias, E.bt, c, n, b);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t[k] += b[k];
+    }
+    if (E.z) store4_rt(E.z, E.zt, r * E.ldz + c, n, t);
+    act_rt<4>(t, E.act);
+    if (E.res) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t[k] += res[k];
+    }
+    store4_rt(E.y, E.yt, r * E.ldy + c, n, t);
   }
+  column_sums(G.sums, (int64_t)blockIdx.x * SPLIT_THREADS + threadIdx.x, (int64_t)gridDim.x * SPLIT_THREADS);
   cluster_sync_all();
 }
 
@@ -832,38 +964,68 @@ static int launch_shape(const MMCall* calls, const MMColumnSums* sums, cudaStrea
   return check_launch("matrix product kernel");
 }
 
-template <int BN>
-static int launch_thin(const MMCall& C, cudaStream_t stream) {
-  using S = ThinShape<BN>;
-  MMProblem P{};
+// CTAs that share a tile of 128 columns and `rows` rows: what fills the SMs
+// once, two blocks of the summed axis each at least; four at most beyond eight
+// tiles, because few clusters of eight such CTAs find their place at one time
+// (512 x 2048 x 512, 16 tiles: 12.6 us by eight, 7.2 by four; the gradients of
+// 16384 x 128 x 128, 1 and 128: 32.5 and 42.2).
+static int split_of(const MMCall& C, int rows) {
+  const int64_t tiles = ((C.n + 127) / 128) * ((C.m + rows - 1) / rows), blocks = (C.k + MM_BK - 1) / MM_BK;
+  int64_t split = device_sm_count() / tiles;
+  const int64_t most = tiles <= 8 ? 8 : 4;
+  split = split < 1 ? 1 : split > most ? most : split;
+  while (split > 1 && blocks < 2 * split) --split;
+  return (int)split;
+}
+
+template <int BN, bool SUM>
+static int launch_split(const MMCall& C, const MMColumnSums* sums, cudaStream_t stream) {
+  using S = SplitShape<BN, SUM>;
+  SplitParams G{};
+  MMProblem& P = G.q;
   int rc = encode_operand(&P.ta, C.b, 1, false, C.b.k_inner ? 128 : 64);
-  if (!rc) rc = encode_operand(&P.tb, C.a, 1, false, BN);
+  if (!rc) rc = encode_operand(&P.tb, C.a, 1, false, C.a.k_inner ? BN : 64);
   if (rc) return rc;
   P.e = C.e;
   P.m = C.n, P.n = C.m;
-  P.kblocks = (int32_t)((C.k + MM_BK - 1) / MM_BK);
-  P.a_k = C.b.k_inner;
-  const int64_t tiles = (C.n + 127) / 128;
-  // CTAs of a tile: what fills the SMs once, two blocks of the summed axis each at least
-  int64_t split = device_sm_count() / tiles;
-  split = split < 1 ? 1 : split > 8 ? 8 : split;
-  while (split > 1 && P.kblocks < 2 * split) --split;
+  P.kblocks = (int32_t)((C.k + MM_BK - 1) / MM_BK), P.chunk = MM_SUM_BLOCKS, P.pairs = C.pairs;
+  P.a_k = C.b.k_inner, P.b_k = C.a.k_inner;
+  for (int i = 0; i < C.pairs; ++i) {
+    P.pa[i] = C.pb[i], P.pb[i] = C.pa[i];
+    P.na = C.pb[i] + 1 > P.na ? C.pb[i] + 1 : P.na;
+    P.nb = C.pa[i] + 1 > P.nb ? C.pa[i] + 1 : P.nb;
+  }
+  G.slot_bytes = P.na * MM_A_BYTES + P.nb * S::B_BYTES;
+  G.stages = S::RING / G.slot_bytes < S::STAGES ? S::RING / G.slot_bytes : S::STAGES;
+  if (sums) G.sums = *sums;
+  G.split = split_of(C, BN), G.row_tiles = (int32_t)((C.m + BN - 1) / BN);
+  const int64_t tiles = ((C.n + 127) / 128) * G.row_tiles;
+  if (tiles * G.split > 0x7FFFFFFF) return fail(PSK_E_SHAPE, "too many output tiles");
   static bool limit[PSK_MAX_DEVICES] = {};
-  smem_limit_once((const void*)mm_thin_kernel<BN>, S::SMEM, limit);
+  smem_limit_once((const void*)mm_split_kernel<BN, SUM>, S::SMEM, limit);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  attr[1].val.clusterDim.x = (unsigned)G.split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tiles * split));
-  cfg.blockDim = dim3(THIN_THREADS);
+  cfg.gridDim = dim3((unsigned)(tiles * G.split));
+  cfg.blockDim = dim3(SPLIT_THREADS);
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaLaunchKernelEx(&cfg, mm_thin_kernel<BN>, P, (int)split);
-  return check_launch("matrix product kernel of few rows");
+  cudaLaunchKernelEx(&cfg, mm_split_kernel<BN, SUM>, G);
+  return check_launch("matrix product kernel of few tiles");
+}
+
+// Rows of the split kernel's tile for a product (0: it gains nothing).
+static int split_rows(const MMCall& C) {
+  if (C.ortho) return 0;
+  if (C.pairs > 1) return split_of(C, 64) >= 2 ? 64 : 0;
+  // (the rows' operand is read along the summed axis, or in boxes of 64 rows)
+  if (C.m <= 64) return C.m > 32 || !C.a.k_inner ? 64 : C.m > 16 ? 32 : 16;
+  return split_of(C, 128) >= 2 ? 128 : 0;
 }
 
 // Pairs of CTAs on tiles of 256 x 256, or single ones on 128 x 128: by the
@@ -873,7 +1035,8 @@ static int launch_thin(const MMCall& C, cudaStream_t stream) {
 // 512 x 2048 x 5632 15.9 and 23.8, 1024^3 11.4 and 9.0, 128 x 2048 x 5632 15.6
 // and 13.4).  With SUM always the latter: two accumulators of 256 columns would
 // leave no second pair of them, and pairs on 256 x 128 gain nothing (4096 x 2048
-// x 2048 f32 199 us, single ones 195).
+// x 2048 f32 199 us, single ones 195).  The update's products take 128 x 64 where
+// those still fit the SMs once (512 x 512, five steps: 114 us, 95).
 template <int KIND, bool SUM>
 static int launch_kind(const MMCall* calls, const MMColumnSums* sums, cudaStream_t stream) {
   const MMCall& C = calls[0];
@@ -885,6 +1048,8 @@ static int launch_kind(const MMCall* calls, const MMColumnSums* sums, cudaStream
   if constexpr (!SUM)
     if (pairs > 0 && waves(256, pairs) * 34 < waves(128, sms) * 30)
       return launch_shape<2, 256, KIND, false, 1>(calls, sums, stream);
+  if constexpr (KIND == MM_ORTHO && !SUM)
+    if (waves(128, 1) * 2 <= sms) return launch_shape<1, 64, KIND, false, 1>(calls, sums, stream);
   return launch_shape<1, 128, KIND, SUM, 1>(calls, sums, stream);
 }
 
@@ -898,13 +1063,24 @@ int mm_launch(const MMCall* calls, int count, const MMColumnSums* sums, cudaStre
   const MMCall& C = calls[0];
   const bool sum = C.pairs > 1, wide = !sum && is_wide(C);
   if (count == 2) {
-    // One launch where one kernel serves both and their tiles together fill the
-    // SMs once at most ([509, 771] x [771, 1003] f32: 78 us as two, 40 as one);
-    // more tiles run better one product after the other (8192 x 2048 x 5632:
-    // 252 us, together 275).
-    int64_t tiles = 0;
-    for (int q = 0; q < 2; ++q) tiles += ((calls[q].m + 127) / 128) * ((calls[q].n + 127) / 128);
-    if (tiles > device_sm_count() || (calls[1].pairs > 1) != sum || (!sum && is_wide(calls[1]) != wide)) {
+    // One launch where one kernel serves both, their tiles together fill the SMs
+    // once at most, and the longer tile takes less than the two launches with
+    // their summed axes shared among CTAs ([509, 771] x [771, 1003] f32: 78 us as
+    // two unshared ones, 40 as one; 16384 x 128 x 128 bf16: 106 us as one).
+    // More tiles run better one product after the other (8192 x 2048 x 5632: 252
+    // us, together 275).
+    int64_t tiles = 0, longest = 0, apart = 0;
+    for (int q = 0; q < 2; ++q) {
+      const MMCall& D = calls[q];
+      tiles += ((D.m + 127) / 128) * ((D.n + 127) / 128);
+      const int64_t blocks = (D.k + MM_BK - 1) / MM_BK;
+      const int rows = split_rows(D);
+      longest = longest > blocks ? longest : blocks;
+      apart += blocks / (rows ? split_of(D, rows) : 1);
+    }
+    // a launch more costs what eight blocks take, with planes three
+    if (tiles > device_sm_count() || longest > apart + (sum ? 3 : 8) || (calls[1].pairs > 1) != sum ||
+        (!sum && is_wide(calls[1]) != wide)) {
       const int rc = mm_launch(calls, 1, sums, stream);
       return rc ? rc : mm_launch(calls + 1, 1, nullptr, stream);
     }
@@ -920,8 +1096,13 @@ int mm_launch(const MMCall* calls, int count, const MMColumnSums* sums, cudaStre
   }
   if (C.ortho)
     return sum ? launch_kind<MM_ORTHO, true>(calls, sums, stream) : launch_kind<MM_ORTHO, false>(calls, sums, stream);
-  if (!sums && !sum && C.m <= 64 && C.a.k_inner)
-    return C.m <= 16 ? launch_thin<16>(C, stream) : C.m <= 32 ? launch_thin<32>(C, stream) : launch_thin<64>(C, stream);
+  switch (split_rows(C)) {
+    case 16: return launch_split<16, false>(C, sums, stream);
+    case 32: return launch_split<32, false>(C, sums, stream);
+    case 64: return sum ? launch_split<64, true>(C, sums, stream) : launch_split<64, false>(C, sums, stream);
+    case 128: return launch_split<128, false>(C, sums, stream);
+    default: break;
+  }
   if (sum) return launch_kind<MM_ANY, true>(calls, sums, stream);
   if (!wide) return launch_kind<MM_ANY, false>(calls, sums, stream);
   switch (C.e.act) {

@@ -34,15 +34,20 @@ constexpr int ORTHO_PARTS = 2;                      // of X
 constexpr int ORTHO_SUM_BLOCKS = 64;                // of a matrix's square sum, at most
 constexpr int64_t ORTHO_MAX_SIDE = 1 << 20;
 
+// The leaves, with room for CAP of them: a launch's parameters are copied for
+// every one, so few leaves have a small table.
+template <int CAP>
 struct OrthoTable {
-  const void* x[ORTHO_MAX_LEAVES];
-  int64_t ldx[ORTHO_MAX_LEAVES];
+  const void* x[CAP];
+  int64_t ldx[CAP];
 };
+template <int CAP>
 struct OrthoTargets {
-  void* y[ORTHO_MAX_LEAVES];
-  int64_t ldy[ORTHO_MAX_LEAVES];
-  uint8_t vec[ORTHO_MAX_LEAVES];
+  void* y[CAP];
+  int64_t ldy[CAP];
+  uint8_t vec[CAP];
 };
+constexpr int ORTHO_FEW = 32;
 
 struct OrthoShape {
   int64_t rows, cols;           // of a leaf
@@ -81,8 +86,8 @@ __device__ __forceinline__ float ortho_share(const void* x, int64_t row, int64_t
   return s.x + s.y;
 }
 
-template <int XT, bool VEC>
-__global__ void __launch_bounds__(256) ortho_sum_kernel(const __grid_constant__ OrthoTable T, OrthoShape S) {
+template <int XT, bool VEC, int CAP>
+__global__ void __launch_bounds__(256) ortho_sum_kernel(const __grid_constant__ OrthoTable<CAP> T, OrthoShape S) {
   __shared__ double part[8];
   const int leaf = blockIdx.x / S.blocks, block = blockIdx.x % S.blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -107,7 +112,8 @@ __global__ void __launch_bounds__(256) ortho_sum_kernel(const __grid_constant__ 
 
 // A warp a leaf: the blocks' sums, the factor S / (norm + eps), and where the
 // result goes, for the last product's epilogue.
-__global__ void __launch_bounds__(256) ortho_factor_kernel(const __grid_constant__ OrthoTargets T, OrthoShape S) {
+template <int CAP>
+__global__ void __launch_bounds__(256) ortho_factor_kernel(const __grid_constant__ OrthoTargets<CAP> T, OrthoShape S) {
   const int leaf = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (leaf >= S.leaves) return;
   double s = 0.0;
@@ -150,8 +156,8 @@ __device__ __forceinline__ void ortho_store8(const OrthoShape& S, int64_t leaf, 
 // The first iterate.  64 x 64 of it a CTA: of a leaf whose rows are the
 // iterate's, straight from rows to rows; of a tall one through shared memory,
 // so that the leaf's rows and the iterate's are both walked along.
-template <int XT, bool VEC, bool TALL>
-__global__ void __launch_bounds__(256) ortho_begin_kernel(const __grid_constant__ OrthoTable T, OrthoShape S) {
+template <int XT, bool VEC, bool TALL, int CAP>
+__global__ void __launch_bounds__(256) ortho_begin_kernel(const __grid_constant__ OrthoTable<CAP> T, OrthoShape S) {
   __shared__ float tile[TALL ? 64 : 1][65];
   const int64_t tn = (S.ldn + 63) / 64, tm = (S.m + 63) / 64;
   const int64_t leaf = blockIdx.x / (tn * tm), at = blockIdx.x % (tn * tm);
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(256) ortho_begin_kernel(const __grid_constant_
 }
 
 // A leaf's rows, one behind the other.
-__global__ void __launch_bounds__(256) ortho_copy_kernel(const __grid_constant__ OrthoTable T, int rows, int cols, int32_t xt,
+__global__ void __launch_bounds__(256) ortho_copy_kernel(const __grid_constant__ OrthoTable<ORTHO_MAX_LEAVES> T, int rows, int cols, int32_t xt,
                                                          char* to) {
   const int leaf = blockIdx.x;
   const int64_t ld = T.ldx[leaf], at = (int64_t)leaf * rows * cols;
@@ -295,8 +301,8 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
   if (workspace_bytes < L.bytes)
     return fail(PSK_E_ARG, "workspace of %llu bytes, %llu needed", (unsigned long long)workspace_bytes,
                 (unsigned long long)L.bytes);
-  static thread_local OrthoTable T;
-  static thread_local OrthoTargets Y;
+  static thread_local OrthoTable<ORTHO_MAX_LEAVES> T;
+  static thread_local OrthoTargets<ORTHO_MAX_LEAVES> Y;
   const View vws{(uintptr_t)workspace, 1, L.bytes, L.bytes};
   std::vector<View> out, in;
   try {
@@ -354,15 +360,27 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
   for (int i = 0; i < n_leaves; ++i) vec = vec && rows_vec8(leaves[i].x, xt, leaves[i].ldx, rows);
   const int64_t tiles = (S.ldn + 63) / 64 * ((S.m + 63) / 64) * n_leaves;
   if (tiles > 0x7FFFFFFF) return fail(PSK_E_SHAPE, "too many tiles");
-  with_dtype(xt, [&](auto XT) {
-    return with_bool(vec, [&](auto VEC) {
-      ortho_sum_kernel<XT.value, VEC.value><<<(unsigned)(n_leaves * S.blocks), 256, 0, s>>>(T, S);
-      ortho_factor_kernel<<<(unsigned)((n_leaves + 7) / 8), 256, 0, s>>>(Y, S);
-      if (S.tall) ortho_begin_kernel<XT.value, VEC.value, true><<<(unsigned)tiles, 256, 0, s>>>(T, S);
-      else ortho_begin_kernel<XT.value, VEC.value, false><<<(unsigned)tiles, 256, 0, s>>>(T, S);
-      return 0;
+  const auto begin = [&](const auto& TT, const auto& YY) {
+    constexpr int CAP = sizeof(TT.x) / sizeof(TT.x[0]);
+    with_dtype(xt, [&](auto XT) {
+      return with_bool(vec, [&](auto VEC) {
+        ortho_sum_kernel<XT.value, VEC.value, CAP><<<(unsigned)(n_leaves * S.blocks), 256, 0, s>>>(TT, S);
+        ortho_factor_kernel<CAP><<<(unsigned)((n_leaves + 7) / 8), 256, 0, s>>>(YY, S);
+        if (S.tall) ortho_begin_kernel<XT.value, VEC.value, true, CAP><<<(unsigned)tiles, 256, 0, s>>>(TT, S);
+        else ortho_begin_kernel<XT.value, VEC.value, false, CAP><<<(unsigned)tiles, 256, 0, s>>>(TT, S);
+        return 0;
+      });
     });
-  });
+  };
+  if (n_leaves <= ORTHO_FEW) {
+    OrthoTable<ORTHO_FEW> t;
+    OrthoTargets<ORTHO_FEW> y;
+    for (int i = 0; i < n_leaves; ++i)
+      t.x[i] = T.x[i], t.ldx[i] = T.ldx[i], y.y[i] = Y.y[i], y.ldy[i] = Y.ldy[i], y.vec[i] = Y.vec[i];
+    begin(t, y);
+  } else {
+    begin(T, Y);
+  }
   rc = check_launch("orthogonalisation's first kernels");
   uint16_t *x = S.x, *x2 = (uint16_t*)(ws + L.x1), *A = (uint16_t*)(ws + L.a), *B = (uint16_t*)(ws + L.b);
   const auto wide = [&](const uint16_t* p, bool k_inner) {

@@ -21,12 +21,10 @@ namespace psk {
 constexpr int ROT_THREADS = 256;
 constexpr int ROT_WARPS = ROT_THREADS / 32;
 constexpr int ROT_MAX_DIM = 512;
-#ifndef RFC
-#define RFC 4
-#define RFA 2
-#define RBC 2
-#endif
-constexpr int ROT_FWD_CTAS = RFC, ROT_BWD_CTAS = RBC, ROT_AHEAD = RFA;    // an SM
+// CTAs an SM of the kernels with four pairs a lane (by their registers) and
+// steps in flight, the best of those tried at [16384, 32 + 4, 64] bf16: forward
+// 4 and 2 36.2 us (3 and 3 36.8, 4 and 3 38.2), backward 2 65.9 (3 74.8, spilled).
+constexpr int ROT_FWD_CTAS = 4, ROT_BWD_CTAS = 2, ROT_AHEAD = 2;
 constexpr int ROT_MAX_BLOCKS = 4 * NOMINAL_SMS;      // CTAs of the backward, at most
 
 struct RotSide {

@@ -320,19 +320,23 @@ def test_repeats_bit_for_bit_on_a_side_stream_and_in_a_graph(R):
             assert all(torch.equal(a, b) for a, b in zip(outs[0][:4], o[:4]))
 
 
-def test_a_lost_copy_ends_in_a_status_not_a_hang(R):
-    x = torch.randn(400, 512, device="cuda", dtype=torch.bfloat16)
-    w = torch.randn(512, 640, device="cuda", dtype=torch.bfloat16)
-    y, ref = (torch.empty(400, 640, device="cuda", dtype=torch.bfloat16) for _ in range(2))
-    R.psk_linear(x, w, ref)
+@pytest.mark.parametrize("rows,cin,cout,dtype,at", [(8, 1024, 640, "bf16", 1), (400, 512, 640, "bf16", 1), (3000, 512, 2048, "bf16", 3),
+                                                    (1500, 512, 1000, "bf16", 5), (300, 512, 600, "f32", 1), (1003, 512, 1501, "f32", 3)])
+def test_a_lost_copy_ends_in_a_status_not_a_hang(R, rows, cin, cout, dtype, at):
+    """In each of the product's kernels: few tiles, pairs of CTAs, single ones; parts of f32 shared and unshared."""
+    x = torch.randn(rows, cin, device="cuda").to(DT[dtype])
+    w = torch.randn(cin, cout, device="cuda").to(DT[dtype])
+    y, ref = (torch.empty(rows, cout, device="cuda", dtype=DT[dtype]) for _ in range(2))
+    ws = scratch(R.psk_linear_workspace(x, w))
+    R.psk_linear(x, w, ref, workspace=ws)
     assert R.psk_device_status(reset=True) == 0
     try:
-        R.psk_test_drop_row(3)
-        R.psk_linear(x, w, y)
+        R.psk_test_drop_row(at)
+        R.psk_linear(x, w, y, workspace=ws)
         torch.cuda.synchronize()
         assert R.psk_device_status(reset=True) == 1
     finally:
         R.psk_test_drop_row(-1)
-    R.psk_linear(x, w, y)
+    R.psk_linear(x, w, y, workspace=ws)
     torch.cuda.synchronize()
     assert R.psk_device_status() == 0 and torch.equal(y, ref)
