@@ -70,8 +70,14 @@ __device__ __forceinline__ void rot_table(RotTable& T, const RotParams& P) {
   __syncthreads();
 }
 
+// (Without turning columns there need be no positions.)
+__device__ __forceinline__ int64_t rot_position(const RotParams& P, int64_t token) {
+  if (!P.rot) return 0;
+  return P.pos64 ? ((const int64_t*)P.pos)[token] : (int64_t)((const int32_t*)P.pos)[token];
+}
+
 __device__ __forceinline__ void rot_angles(float2* cs, const RotTable& T, const RotParams& P, int64_t token, int lane) {
-  const int64_t pos = P.pos64 ? ((const int64_t*)P.pos)[token] : (int64_t)((const int32_t*)P.pos)[token];
+  const int64_t pos = rot_position(P, token);
   __syncwarp();
   for (int j = lane; j < P.rot / 2; j += 32) {
     const int64_t frac = (int64_t)((uint64_t)pos * T.turn[j]);
@@ -443,11 +449,6 @@ __device__ __forceinline__ void rot_tables(RotTables& T, const RotParams& P) {
       }
   }
   __syncthreads();
-}
-
-__device__ __forceinline__ int64_t rot_position(const RotParams& P, int64_t token) {
-  if (!P.rot) return 0;
-  return P.pos64 ? ((const int64_t*)P.pos)[token] : (int64_t)((const int32_t*)P.pos)[token];
 }
 
 __device__ __forceinline__ void rot_angles_at(RotTables& T, const RotParams& P, int64_t pos, int warp, int lane) {

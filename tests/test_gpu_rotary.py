@@ -199,3 +199,20 @@ def test_repeats_bit_for_bit_on_a_side_stream_and_in_a_graph(R):
     torch.cuda.synchronize()
     for o in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(outs[0][:3], o[:3]))
+
+
+@pytest.mark.parametrize("dim", [64, 50])
+def test_no_turning_columns_need_no_positions(R, dim):
+    import reduction_groups_gb300._native as N
+
+    x, y, dx = (torch.randn(9, 3, dim, device="cuda") for _ in range(3))
+    want, wdx = torch.empty_like(x), torch.empty_like(x)
+    p, f = torch.arange(9, device="cuda"), torch.empty(0, device="cuda")
+    R.psk_qk_norm_rotary(x, None, want, None, p, f)
+    R.psk_qk_norm_rotary_backward(x, None, x, None, wdx, None, p, f)
+    s = torch.cuda.current_stream().cuda_stream
+    head = lambda t: (t.data_ptr(), None, N.PSK_F32, 3 * dim, dim, 0, 0)  # noqa: E731
+    rest = (9, 3, 0, dim, 0, None, N.PSK_I64, None, N.PSK_PAIRS_HALVES, N.PSK_HEAD_NORM_RMS, 1e-6, None, None, 0)
+    N.check(N.lib().psk_qk_norm_rotary(*head(x), *head(y), *rest, s))
+    N.check(N.lib().psk_qk_norm_rotary_backward(*head(x), *head(x), *head(dx), *rest, None, None, 0, None, 0, s))
+    assert torch.equal(y, want) and torch.equal(dx, wdx)
