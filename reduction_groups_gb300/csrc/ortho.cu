@@ -240,10 +240,11 @@ static bool ortho_is_small(int64_t rows, int64_t cols) {
   return m <= ORTHO_SMALL_M && n <= ORTHO_SMALL_N;
 }
 
-// Whether a result lies on another matrix's x.
-static bool ortho_crossed(const std::vector<View>& in, const std::vector<View>& out) {
-  std::vector<std::pair<uintptr_t, int>> at;             // the x's by their beginnings
+// Whether a result lies on another matrix's x.  at: room for the x's, sorted by their beginnings.
+static bool ortho_crossed(const std::vector<View>& in, const std::vector<View>& out,
+                          std::vector<std::pair<uintptr_t, int>>& at) {
   uint64_t longest = 0;
+  at.clear();
   for (size_t i = 0; i < in.size(); ++i) {
     at.push_back({in[i].p, (int)i});
     longest = longest > in[i].bytes() ? longest : in[i].bytes();
@@ -305,9 +306,11 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
   static thread_local OrthoTargets<ORTHO_MAX_LEAVES> Y;
   const View vws{(uintptr_t)workspace, 1, L.bytes, L.bytes};
   std::vector<View> out, in;
-  try {
+  std::vector<std::pair<uintptr_t, int>> starts;
+  try {                                    // all that allocates: no exception leaves this entry
     out.reserve(n_leaves);
     in.reserve(n_leaves);
+    starts.reserve(n_leaves);
   } catch (...) {
     return fail(PSK_E_ARG, "out of host memory");
   }
@@ -326,7 +329,7 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
     T.x[i] = f.x, T.ldx[i] = f.ldx;
     Y.y[i] = f.y, Y.ldy[i] = f.ldy, Y.vec[i] = rows_vec8(f.y, yt, f.ldy, rows);
   }
-  const bool crossed = ortho_is_small(rows, cols) && ortho_crossed(in, out);
+  const bool crossed = ortho_is_small(rows, cols) && ortho_crossed(in, out, starts);
   std::sort(out.begin(), out.end(), [](const View& a, const View& b) { return a.p < b.p; });
   for (size_t i = 0; i < out.size(); ++i)
     for (size_t j = i + 1; j < out.size() && out[j].p < out[i].p + out[i].bytes(); ++j)
