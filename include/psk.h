@@ -43,6 +43,8 @@
  *   rounded once to f32 and only the root is rounded to its storage type; exp
  *   and erf nodes are correctly rounded.  bf16 is storage only: a shift on
  *   the way in, one round to nearest even on the way out.
+ *   (The operators of a layer's matrices fuse multiply-adds and multiply on the
+ *   tensor cores; each states its error.)
  */
 #ifndef PSK_H
 #define PSK_H
@@ -530,10 +532,14 @@ int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int64_t cols, 
  * residual: rows x out or NULL.  z: NULL, or rows x out that receive z (what
  * the backward reads).  Every tensor f32 or bf16, of its own type.
  * The products of a sum are exact (an f32 operand enters as three bf16 parts,
- * products of parts below 2^-24 of the largest left out) and added in f32 in
- * an order fixed by the sizes and types; z, act and the residual's sum in f32;
- * y and z are rounded once.  PSK_ACT_GELU is z Phi(z), its negative tail to
- * f32's relative accuracy; at z = +-inf an activation is its limit.  A row of
+ * products of parts below 2^-24 of the largest left out) and added in f32: by
+ * the tensor core, which truncates (at most 17 f32 steps of the sum so far for
+ * each 16 terms), and with an f32 operand every 256 terms by one rounded
+ * addition.  The order is fixed by the sizes, types, the rows' alignment and
+ * the device's SMs.  z, act and the residual's sum are f32; y and z are rounded
+ * once.  PSK_ACT_GELU is z Phi(z), its negative tail included to 2^-20 of its
+ * value, where x, w, y, z, bias and residual are all bf16 to 2^-16; at
+ * z = +-inf an activation is its limit.  A row of
  * x or a column of w that holds an infinity or a NaN gives infinities or NaNs
  * in its own row or column of z (NaN also where the exact sum is infinite, if
  * an operand is f32).
@@ -558,9 +564,9 @@ int psk_linear(const void* x, int32_t xt, int64_t ldx, const void* w, int32_t wt
  * PSK_ACT_NONE.  dx (rows x in), dw (w's layout) and dbias (out elements) may
  * each be NULL: not wanted; x is read for dw alone, w for dx alone.  With
  * accumulate != 0, dw and dbias are added to (micro-batches that share a
- * leaf): RN(dw + sum).  dz is formed in f32; a product of bf16 ct, bf16
- * operand and bf16 result takes it rounded to bf16, any other to f32's
- * accuracy.  act' of relu at 0 is 0.  rows == 0 gives dw = 0 and dbias = 0
+ * leaf): RN(dw + sum).  act'(z) is f32 to 2^-20 absolutely, dz is formed in
+ * f32; a product of bf16 ct, bf16 operand and bf16 result takes it rounded to
+ * bf16, any other to f32's accuracy.  act' of relu at 0 is 0.  rows == 0 gives dw = 0 and dbias = 0
  * (accumulating: unchanged).  No overlap of what is written with anything
  * else.  rows, out <= 2^25, in < 2^31 - 1024.  workspace as for psk_linear,
  * psk_linear_backward_workspace bytes for the same arguments. */
@@ -585,9 +591,10 @@ int psk_linear_backward(const void* ct, int32_t ct_t, int64_t ldc, const void* x
  * fp16 parts (times 2^10), sums are f32; for a y stored in bf16 the products
  * take one part of each factor (an error of 1e-3 of ||y|| at most for matrices
  * of some size, below the storage's), for f32 two.  Coefficients that drive a
- * singular value beyond 2^5 overflow.  A zero
- * matrix (with eps > 0) gives zeros; a matrix with a NaN or an infinity gives
- * NaNs, alone.  steps in [1, 64]; rows, cols <= 2^20; n_leaves <=
+ * singular value beyond 2^5 overflow.  The norm's squares are f32: elements
+ * below 2^-63 may count as 0 in it, and ||G||_F + eps of at least 2^-100 is
+ * expected.  A zero matrix (with eps > 0) gives zeros; a matrix with a NaN or
+ * an infinity gives NaNs, alone.  steps in [1, 64]; rows, cols <= 2^20; n_leaves <=
  * PSK_ORTHO_MAX_LEAVES; an empty list or shape launches nothing.  workspace as
  * for psk_linear, psk_orthogonalize_workspace bytes. */
 #define PSK_ORTHO_MAX_LEAVES 512
@@ -616,7 +623,9 @@ int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves, int64_t ro
  * (PSK_PAIRS_NEIGHBOURS); columns from rot on do not turn.  positions: DEVICE,
  * PSK_I32 or PSK_I64, any sign; freqs: rot / 2 f32, radians a position.  The
  * angle is the exact product reduced to a turn with an error of 2^-62 a
- * position.  Arithmetic in f32, one rounding to yt.  yq may be q and yk k in
+ * position.  Arithmetic in f32, one rounding to yt; the squares of a head are
+ * expected within f32's range (|x| below 2^59, and eps above 0 or |x| above
+ * 2^-60).  Without turning columns positions and freqs may be NULL.  yq may be q and yk k in
  * place (same type and strides); no other overlap.  hq or hk may be 0.  dim
  * in [1, 512], rot even, <= dim.
  *
@@ -653,7 +662,7 @@ int psk_device_status(uint32_t* status, int32_t reset);
 /* Test hook for the bounded waits (no counterpart on the pages): from the
  * next launch on, the pipelined row-region kernels of the current device stop
  * producing at local row `row` of every CTA, as if that row's copy had been
- * lost.  Every wait for it gives up after about two seconds of clock, the
+ * lost, and the matrix products at the copy of that number.  Every wait for it gives up after about two seconds of clock, the
  * kernel sets bit 0 of the status word and winds down (its output then
  * unspecified), and the device stays usable.  row = -1 (the default) turns
  * it off.  Host-only, synchronous; for tests, never for production use.
