@@ -141,6 +141,22 @@ __device__ __forceinline__ void store16_bf16(void* p, int64_t i, const float* v)
   store16(p, i, w);
 }
 
+// Sixteen columns of a half warp's sixteen rows turned: lane l of a half gets
+// column l of its rows.  Four exchanges, of lanes 8, 4, 2 and 1 apart.
+__device__ __forceinline__ void turn16(float* v, int lane) {
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (k & d) continue;
+      const float give = up ? v[k] : v[k + d], got = __shfl_xor_sync(0xFFFFFFFFu, give, d);
+      if (up) v[k] = got;
+      else v[k + d] = got;
+    }
+  }
+}
+
 template <int ACT, bool FINE, int N>
 __device__ __forceinline__ void act_all(float* v) {
   if constexpr (ACT != ACT_NONE) {
@@ -258,11 +274,13 @@ __device__ __forceinline__ void linear_row16(const MMEpilogue& E, int64_t r, int
   store16_bf16(E.y, r * E.ldy + c, v);
 }
 
-// Sixteen columns of one row of the orthogonalised update: v = alpha v + beta
-// from, stored in fp16 planes (and mirrored) or into a leaf.  The planes' rows
-// are padded to 32 bytes; their padding may be written.
-__device__ __forceinline__ void ortho_row16(const MMProblem& P, int32_t matrix, int64_t r, int64_t c, bool mirrored,
-                                            const Fetched& F, float* v) {
+// Sixteen columns of a warp's rows of the orthogonalised update: v = alpha v +
+// beta from, stored in fp16 planes (and mirrored) or into a leaf.  The planes'
+// rows are padded to 32 bytes; their padding may be written.
+__device__ __forceinline__ void ortho_row16(const MMProblem& P, int32_t matrix, int64_t row0, int lane, int64_t c,
+                                            bool mirrored, const Fetched& F, float* v) {
+  const int64_t r = row0 + lane;
+  const bool live = r < P.m;
   const MMEpilogue& E = P.e;
   const int64_t at = (int64_t)matrix * E.planes * E.plane_stride;
   const int64_t left = P.n - c;
@@ -277,6 +295,7 @@ __device__ __forceinline__ void ortho_row16(const MMProblem& P, int32_t matrix, 
     v[2 * k] = x.x, v[2 * k + 1] = x.y;
   }
   if (E.to) {
+    if (!live) return;
     for (int p = 0; p < E.planes; ++p) {
       uint32_t w[8];
 #pragma unroll
@@ -297,6 +316,15 @@ __device__ __forceinline__ void ortho_row16(const MMProblem& P, int32_t matrix, 
     return;
   }
   const MMLeaf L = E.leaves[matrix];
+  if (!E.transposed && !L.vec) {           // rows that begin anywhere: lanes along them
+    turn16(v, lane);
+    const int64_t col = c + (lane & 15), first = row0 + (lane & 16);
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (first + k < P.m && col < P.n) store1_rt(L.y, E.yt, (first + k) * L.ld + col, v[k]);
+    return;
+  }
+  if (!live) return;
   if (E.transposed) {
 #pragma unroll
     for (int k = 0; k < 16; ++k)
@@ -330,9 +358,10 @@ __device__ __forceinline__ void finish16(const MMProblem& P, int32_t matrix, int
   if (c >= P.n) return;
   if constexpr (KIND == MM_ANY) {
     linear_any16(P, row0, c, lane, stage, v);
+  } else if constexpr (KIND == MM_ORTHO) {
+    ortho_row16(P, matrix, row0, lane, c, mirrored, F, v);
   } else if (row0 + lane < P.m) {
-    if constexpr (KIND == MM_ORTHO) ortho_row16(P, matrix, row0 + lane, c, mirrored, F, v);
-    else linear_row16<KIND>(P.e, row0 + lane, c, F, v);
+    linear_row16<KIND>(P.e, row0 + lane, c, F, v);
   }
 }
 

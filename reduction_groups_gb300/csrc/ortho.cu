@@ -60,29 +60,30 @@ struct OrthoShape {
   uint16_t* x;                  // [leaf][part][m][ldn]
 };
 
-// A block of rows' sum of squares: f32 within a thread's share of a row, 64
-// bits beyond.  A warp a row, up to 1024 columns of it on their way at once.
+// A block's sum of squares: f32 within a thread's share of up to 1024 columns
+// of a row, which are on their way at once, 64 bits beyond.  Warps take such
+// pieces in turn (whole rows left few warps at work: 18 of [145, 4299] 58 us).
 // A share whose squares leave f32 (elements above 2^60 or so) is taken again
 // times 2^-64.
+constexpr int ORTHO_PIECE = 1024;
+
 template <int XT, bool VEC>
-__device__ __forceinline__ float ortho_share(const void* x, int64_t row, int64_t cols, int lane, float scale) {
+__device__ __forceinline__ float ortho_share(const void* x, int64_t row, int64_t c, int64_t cols, int lane, float scale) {
   float2 s = make_float2(0.0f, 0.0f);
-  for (int64_t c = 0; c < cols; c += 1024) {
-    Piece<XT, VEC, 8> p[4];
+  Piece<XT, VEC, 8> p[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const Columns<VEC, 8> C(c + j * 256, 32, lane, cols);
-      C.template load<XT>(x, row, p[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int k = 0; k < 8; k += 2) {
-        float2 v = make_float2(p[j].get(k), p[j].get(k + 1));
-        if (scale != 1.0f) v.x *= scale, v.y *= scale;
-        s = __ffma2_rn(v, v, s);
-      }
+  for (int j = 0; j < 4; ++j) {
+    const Columns<VEC, 8> C(c + j * 256, 32, lane, cols);
+    C.template load<XT>(x, row, p[j]);
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      float2 v = make_float2(p[j].get(k), p[j].get(k + 1));
+      if (scale != 1.0f) v.x *= scale, v.y *= scale;
+      s = __ffma2_rn(v, v, s);
+    }
   return s.x + s.y;
 }
 
@@ -94,10 +95,12 @@ __global__ void __launch_bounds__(256) ortho_sum_kernel(const __grid_constant__ 
   const void* x = T.x[leaf];
   const int64_t ld = T.ldx[leaf];
   double total = 0.0;
-  for (int64_t r = (int64_t)block * 8 + warp; r < S.rows; r += (int64_t)S.blocks * 8) {
-    const float s = ortho_share<XT, VEC>(x, r * ld, S.cols, lane, 1.0f);
+  const int64_t across = (S.cols + ORTHO_PIECE - 1) / ORTHO_PIECE, pieces = S.rows * across;
+  for (int64_t i = (int64_t)block * 8 + warp; i < pieces; i += (int64_t)S.blocks * 8) {
+    const int64_t r = i / across, c = (i - r * across) * ORTHO_PIECE;
+    const float s = ortho_share<XT, VEC>(x, r * ld, c, S.cols, lane, 1.0f);
     if (s > 3.4028234663852886e38f)
-      total += (double)ortho_share<XT, VEC>(x, r * ld, S.cols, lane, 5.421010862427522e-20f) * 3.402823669209385e38;
+      total += (double)ortho_share<XT, VEC>(x, r * ld, c, S.cols, lane, 5.421010862427522e-20f) * 3.402823669209385e38;
     else total += (double)s;
   }
 #pragma unroll
@@ -354,7 +357,7 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
   S.ldn = ortho_up16(S.n), S.ldm = ortho_up16(S.m);
   S.xt = xt, S.leaves = n_leaves;
   const int planes = yt == PSK_F32 ? 2 : 1;
-  int64_t blocks = (rows + 31) / 32;
+  const int64_t blocks = (rows * ((cols + ORTHO_PIECE - 1) / ORTHO_PIECE) + 15) / 16;     // two pieces a warp at least
   S.blocks = (int32_t)(blocks < ORTHO_SUM_BLOCKS ? blocks : ORTHO_SUM_BLOCKS);
   S.eps = eps;
   S.sums = (double*)(ws + L.sums), S.factors = (float*)(ws + L.factors);
