@@ -647,7 +647,7 @@ constexpr int SPLIT_ROW = 132;             // floats of a column of the accumula
 struct SplitParams {
   MMProblem q;                             // a: the columns' operand, b: the rows'
   MMColumnSums sums;
-  int32_t split, row_tiles, stages, slot_bytes;
+  int32_t split, row_tiles, tiles, stages, slot_bytes, f16;      // tiles: of one matrix
 };
 
 __device__ __forceinline__ float4 load_cluster(uint32_t addr, uint32_t rank) {
@@ -685,7 +685,28 @@ __device__ __forceinline__ void store4_rt(void* p, int32_t dt, int64_t i, int n,
   }
 }
 
-template <int BN, bool SUM>
+// Four columns of a row of the orthogonalised update, into fp16 planes.
+__device__ __forceinline__ void ortho_row4(const MMEpilogue& E, int32_t matrix, int64_t r, int64_t c, float* t) {
+  const int64_t at = (int64_t)matrix * E.planes * E.plane_stride + r * E.ld + c;
+  float v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = E.alpha * t[k];
+  if (E.from)
+    for (int p = E.planes - 1; p >= 0; --p) {
+      const uint2 w = *(const uint2*)(E.from + at + p * E.plane_stride);
+      const float2 x = f16x2_to_f32(w.x), y = f16x2_to_f32(w.y);
+      v[0] = fmaf(E.beta, x.x, v[0]), v[1] = fmaf(E.beta, x.y, v[1]);
+      v[2] = fmaf(E.beta, y.x, v[2]), v[3] = fmaf(E.beta, y.y, v[3]);
+    }
+  for (int p = 0; p < E.planes; ++p) {
+    const uint2 w = make_uint2(f32x2_to_f16x2(v[0], v[1]), f32x2_to_f16x2(v[2], v[3]));
+    const float2 x = f16x2_to_f32(w.x), y = f16x2_to_f32(w.y);
+    v[0] -= x.x, v[1] -= x.y, v[2] -= y.x, v[3] -= y.y;
+    *(uint2*)(E.to + at + p * E.plane_stride) = w;
+  }
+}
+
+template <int BN, bool SUM, bool ORTHO>
 __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid_constant__ SplitParams G) {
   using S = SplitShape<BN, SUM>;
   const MMProblem& P = G.q;
@@ -695,7 +716,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid
   const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, split = G.split;
   const uint32_t rank = cluster_rank();
-  const int32_t tile = blockIdx.x / split, tc = tile / G.row_tiles, tr = tile - tc * G.row_tiles;
+  const int32_t unit = blockIdx.x / split, matrix = ORTHO ? unit / G.tiles : 0, tile = unit - matrix * G.tiles;
+  const int32_t tc = tile / G.row_tiles, tr = tile - tc * G.row_tiles;
+  const int32_t za = matrix * P.planes_a, zb = matrix * P.planes_b;
   const int32_t k0 = (int32_t)((int64_t)P.kblocks * rank / split), k1 = (int32_t)((int64_t)P.kblocks * (rank + 1) / split);
   const int stages = SUM ? G.stages : S::STAGES, na = SUM ? P.na : 1, nb = SUM ? P.nb : 1;
   const uint32_t slot_bytes = SUM ? G.slot_bytes : S::STAGE;
@@ -736,26 +759,26 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid
       const uint32_t bar = smem_addr(&full[s]);
       for (int p = 0; p < na; ++p, at += MM_A_BYTES) {
         if (P.a_k) {
-          tma_box<1>(at, &P.ta, kb * MM_BK, tc * 128, p, bar);
+          tma_box<1>(at, &P.ta, kb * MM_BK, tc * 128, za + p, bar);
         } else {
-          tma_box<1>(at, &P.ta, tc * 128, kb * MM_BK, p, bar);
-          tma_box<1>(at + MM_A_BYTES / 2, &P.ta, tc * 128 + 64, kb * MM_BK, p, bar);
+          tma_box<1>(at, &P.ta, tc * 128, kb * MM_BK, za + p, bar);
+          tma_box<1>(at + MM_A_BYTES / 2, &P.ta, tc * 128 + 64, kb * MM_BK, za + p, bar);
         }
       }
       for (int p = 0; p < nb; ++p, at += S::B_BYTES) {
         if (P.b_k) {
-          tma_box<1>(at, &P.tb, kb * MM_BK, tr * BN, p, bar);
+          tma_box<1>(at, &P.tb, kb * MM_BK, tr * BN, zb + p, bar);
         } else {
 #pragma unroll
           for (int j = 0; j < BN / 64; ++j)
-            tma_box<1>(at + j * (64 * MM_BK * 2), &P.tb, tr * BN + j * 64, kb * MM_BK, p, bar);
+            tma_box<1>(at + j * (64 * MM_BK * 2), &P.tb, tr * BN + j * 64, kb * MM_BK, zb + p, bar);
         }
       }
     }
     if (!ok)
       for (int i = issued > stages ? issued - stages : 0; i < issued; ++i) mbar_wait(&full[i % stages], (i / stages) & 1);
   } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (P.a_k ? 0u : 1u << 15) | (P.b_k ? 0u : 1u << 16) |
+    const uint32_t idesc = (1u << 4) | (G.f16 ? 0u : (1u << 7) | (1u << 10)) | (P.a_k ? 0u : 1u << 15) | (P.b_k ? 0u : 1u << 16) |
                            ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
     const uint32_t a_step = (P.a_k ? 32u : 2048u) >> 4, b_step = (P.b_k ? 32u : 2048u) >> 4;
     bool ok = true;
@@ -865,11 +888,15 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid
     for (int q = 0; q < 8; ++q)
       if (q < split) parts[q] = load_cluster(at, q);
     float res[4], t[4];
-    if (E.res) load4_rt(E.res, E.rt, r * E.ldr + c, n, res);
+    if (!ORTHO && E.res) load4_rt(E.res, E.rt, r * E.ldr + c, n, res);
     t[0] = parts[0].x, t[1] = parts[0].y, t[2] = parts[0].z, t[3] = parts[0].w;
 #pragma unroll
     for (int q = 1; q < 8; ++q)
       if (q < split) t[0] += parts[q].x, t[1] += parts[q].y, t[2] += parts[q].z, t[3] += parts[q].w;
+    if constexpr (ORTHO) {
+      ortho_row4(E, matrix, r, c, t);
+      continue;
+    }
     if (E.bias) {
       float b[4];
       load4_rt(E.bias, E.bt, c, n, b);
@@ -999,7 +1026,7 @@ static int launch_shape(const MMCall* calls, const MMColumnSums* sums, cudaStrea
 // (512 x 2048 x 512, 16 tiles: 12.6 us by eight, 7.2 by four; the gradients of
 // 16384 x 128 x 128, 1 and 128: 32.5 and 42.2).
 static int split_of(const MMCall& C, int rows) {
-  const int64_t tiles = ((C.n + 127) / 128) * ((C.m + rows - 1) / rows), blocks = (C.k + MM_BK - 1) / MM_BK;
+  const int64_t tiles = ((C.n + 127) / 128) * ((C.m + rows - 1) / rows) * C.matrices, blocks = (C.k + MM_BK - 1) / MM_BK;
   int64_t split = device_sm_count() / tiles;
   const int64_t most = tiles <= 8 ? 8 : 4;
   split = split < 1 ? 1 : split > most ? most : split;
@@ -1007,18 +1034,18 @@ static int split_of(const MMCall& C, int rows) {
   return (int)split;
 }
 
-template <int BN, bool SUM>
+template <int BN, bool SUM, bool ORTHO = false>
 static int launch_split(const MMCall& C, const MMColumnSums* sums, cudaStream_t stream) {
   using S = SplitShape<BN, SUM>;
   SplitParams G{};
   MMProblem& P = G.q;
-  int rc = encode_operand(&P.ta, C.b, 1, false, C.b.k_inner ? 128 : 64);
-  if (!rc) rc = encode_operand(&P.tb, C.a, 1, false, C.a.k_inner ? BN : 64);
+  int rc = encode_operand(&P.ta, C.b, C.matrices, C.f16, C.b.k_inner ? 128 : 64);
+  if (!rc) rc = encode_operand(&P.tb, C.a, C.matrices, C.f16, C.a.k_inner ? BN : 64);
   if (rc) return rc;
   P.e = C.e;
   P.m = C.n, P.n = C.m;
   P.kblocks = (int32_t)((C.k + MM_BK - 1) / MM_BK), P.chunk = MM_SUM_BLOCKS, P.pairs = C.pairs;
-  P.a_k = C.b.k_inner, P.b_k = C.a.k_inner;
+  P.a_k = C.b.k_inner, P.b_k = C.a.k_inner, P.planes_a = C.b.planes, P.planes_b = C.a.planes;
   for (int i = 0; i < C.pairs; ++i) {
     P.pa[i] = C.pb[i], P.pb[i] = C.pa[i];
     P.na = C.pb[i] + 1 > P.na ? C.pb[i] + 1 : P.na;
@@ -1028,10 +1055,11 @@ static int launch_split(const MMCall& C, const MMColumnSums* sums, cudaStream_t 
   G.stages = S::RING / G.slot_bytes < S::STAGES ? S::RING / G.slot_bytes : S::STAGES;
   if (sums) G.sums = *sums;
   G.split = split_of(C, BN), G.row_tiles = (int32_t)((C.m + BN - 1) / BN);
-  const int64_t tiles = ((C.n + 127) / 128) * G.row_tiles;
+  const int64_t each = ((C.n + 127) / 128) * G.row_tiles, tiles = each * C.matrices;
   if (tiles * G.split > 0x7FFFFFFF) return fail(PSK_E_SHAPE, "too many output tiles");
+  G.tiles = (int32_t)each, G.f16 = C.f16;
   static bool limit[PSK_MAX_DEVICES] = {};
-  smem_limit_once((const void*)mm_split_kernel<BN, SUM>, S::SMEM, limit);
+  smem_limit_once((const void*)mm_split_kernel<BN, SUM, ORTHO>, S::SMEM, limit);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1044,13 +1072,21 @@ static int launch_split(const MMCall& C, const MMColumnSums* sums, cudaStream_t 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaLaunchKernelEx(&cfg, mm_split_kernel<BN, SUM>, G);
+  cudaLaunchKernelEx(&cfg, mm_split_kernel<BN, SUM, ORTHO>, G);
   return check_launch("matrix product kernel of few tiles");
 }
 
 // Rows of the split kernel's tile for a product (0: it gains nothing).
 static int split_rows(const MMCall& C) {
-  if (C.ortho) return 0;
+  if (C.ortho) {
+    // Of f32 results wherever they can (1 x 512 x 512, five steps: 201 us, 111);
+    // else, where both triangles are more tiles than one, if a tile's summed axis
+    // shrinks by 12 blocks at least (8 x 64 x 4096 162 us, 92; 1 x 512 x 1024 105,
+    // 97; by 8 or less 1 x 1024 x 1024 132, 150, and 1 x 512 x 512 95, 101).
+    const int rows = C.pairs > 1 || C.m <= 64 ? 64 : 128, split = split_of(C, rows);
+    const int64_t blocks = (C.k + MM_BK - 1) / MM_BK;
+    return C.e.to && split >= 2 && (C.pairs > 1 || blocks - blocks / split >= 12) ? rows : 0;
+  }
   if (C.pairs > 1) return split_of(C, 64) >= 2 ? 64 : 0;
   // (the rows' operand is read along the summed axis, or in boxes of 64 rows)
   if (C.m <= 64) return C.m > 32 || !C.a.k_inner ? 64 : C.m > 16 ? 32 : 16;
@@ -1123,8 +1159,14 @@ int mm_launch(const MMCall* calls, int count, const MMColumnSums* sums, cudaStre
     if (!wide) return launch_shape<1, 128, MM_ANY, false, 2>(calls, sums, stream);
     return launch_shape<1, 128, ACT_NONE, false, 2>(calls, sums, stream);
   }
-  if (C.ortho)
+  if (C.ortho) {
+    switch (split_rows(C)) {
+      case 64: return sum ? launch_split<64, true, true>(C, sums, stream) : launch_split<64, false, true>(C, sums, stream);
+      case 128: return launch_split<128, false, true>(C, sums, stream);
+      default: break;
+    }
     return sum ? launch_kind<MM_ORTHO, true>(calls, sums, stream) : launch_kind<MM_ORTHO, false>(calls, sums, stream);
+  }
   switch (split_rows(C)) {
     case 16: return launch_split<16, false>(C, sums, stream);
     case 32: return launch_split<32, false>(C, sums, stream);
