@@ -108,19 +108,21 @@ struct RotPair {
     has[0] = p < P.rot / 2 + rest;
     has[1] = has[0] && col[1] < P.dim;
   }
-  __device__ __forceinline__ void load(const void* p, int32_t dt, int64_t at, bool live, float (&v)[2]) const {
+  template <int DT>
+  __device__ __forceinline__ void load(const void* p, bool live, float (&v)[2]) const {
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      v[k] = !live || !has[k] ? 0.0f
-             : dt == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)p)[at + col[k]])
-                              : ((const float*)p)[at + col[k]];
+    for (int k = 0; k < 2; ++k) {
+      v[k] = 0.0f;
+      if (live && has[k]) v[k] = DT == PSK_BF16 ? bf16_bits_to_f32(((const uint16_t*)p)[col[k]]) : ((const float*)p)[col[k]];
+    }
   }
-  __device__ __forceinline__ void store(void* p, int32_t dt, int64_t at, const float (&v)[2]) const {
+  template <int DT>
+  __device__ __forceinline__ void store(void* p, const float (&v)[2]) const {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!has[k]) continue;
-      if (dt == PSK_BF16) ((uint16_t*)p)[at + col[k]] = f32_to_bf16_bits(v[k]);
-      else ((float*)p)[at + col[k]] = v[k];
+      if (DT == PSK_BF16) ((uint16_t*)p)[col[k]] = f32_to_bf16_bits(v[k]);
+      else ((float*)p)[col[k]] = v[k];
     }
   }
   __device__ __forceinline__ float2 angle(const float2* cs) const { return turns ? cs[pair] : make_float2(1.0f, 0.0f); }
@@ -131,6 +133,31 @@ struct RotPair {
     v[1] = fmaf(y, t.x, x * t.y);
   }
 };
+
+// A lane's pairs of one head (at: the head's first element); the type is looked
+// up once for all of them.
+template <int NG>
+__device__ __forceinline__ void load_pairs(const RotPair (&G)[NG], const void* p, int32_t dt, int64_t at, bool live,
+                                           float (&v)[NG][2]) {
+  if (dt == PSK_BF16) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) G[g].template load<PSK_BF16>((const uint16_t*)p + at, live, v[g]);
+  } else {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) G[g].template load<PSK_F32>((const float*)p + at, live, v[g]);
+  }
+}
+template <int NG>
+__device__ __forceinline__ void store_pairs(const RotPair (&G)[NG], void* p, int32_t dt, int64_t at,
+                                            const float (&v)[NG][2]) {
+  if (dt == PSK_BF16) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) G[g].template store<PSK_BF16>((uint16_t*)p + at, v[g]);
+  } else {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) G[g].template store<PSK_F32>((float*)p + at, v[g]);
+  }
+}
 
 __device__ __forceinline__ float team_sum(float s, int team) {
   for (int o = team >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
@@ -170,7 +197,7 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) rotary_any_kernel(const __grid
   RotPair G[NG];
 #pragma unroll
   for (int g = 0; g < NG; ++g) G[g].place(in + g * team, P.neighbours, P);
-  constexpr int U = NG <= 2 ? 4 : NG == 4 ? 2 : 1;             // steps in flight together
+  constexpr int U = NG == 2 ? 4 : NG == 4 ? 2 : 1;             // steps in flight together
   const int64_t units = P.tokens * P.chunks;
   for (int64_t u = (int64_t)blockIdx.x * ROT_WARPS + warp; u < units; u += (int64_t)gridDim.x * ROT_WARPS) {
     const int64_t token = u / P.chunks;
@@ -181,9 +208,7 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) rotary_any_kernel(const __grid
       for (int j = 0; j < U; ++j) {
         const int sd = i + j >= qsteps, h = (i + j - sd * qsteps) * slots + slot;
         const RotSide& S = P.side[sd];
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-          G[g].load(S.x, P.x_type, token * S.xt + h * S.xh, i + j < s1 && h < S.heads, v[j][g]);
+        load_pairs(G, S.x, P.x_type, token * S.xt + h * S.xh, i + j < s1 && h < S.heads, v[j]);
       }
       if (i == s0) rot_angles(angles[warp], T, P, token, lane);
 #pragma unroll
@@ -206,8 +231,8 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) rotary_any_kernel(const __grid
               if (G[g].has[k]) v[j][g][k] = v[j][g][k] * r * gammas[sd][G[g].col[k]];
           }
           G[g].turn(G[g].angle(angles[warp]), v[j][g]);
-          if (h < S.heads) G[g].store(S.y, P.y_type, token * S.yt + h * S.yh, v[j][g]);
         }
+        if (h < S.heads) store_pairs(G, S.y, P.y_type, token * S.yt + h * S.yh, v[j]);
       }
     }
   }
@@ -228,7 +253,6 @@ __global__ void __launch_bounds__(ROT_THREADS, 2) rotary_any_backward_kernel(con
   RotPair G[NG];
 #pragma unroll
   for (int g = 0; g < NG; ++g) G[g].place(in + g * team, P.neighbours, P);
-  constexpr int U = NG <= 2 ? 2 : 1;
   float dg[2][NG][2];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
@@ -240,55 +264,42 @@ __global__ void __launch_bounds__(ROT_THREADS, 2) rotary_any_backward_kernel(con
 #pragma unroll
     for (int sd = 0; sd < 2; ++sd) {
       const RotSide& S = P.side[sd];
-      for (int h0 = slot; h0 - slot < S.heads; h0 += slots * U) {
-        float v[U][NG][2], x[U][NG][2];
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-          const int h = h0 + j * slots;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            G[g].load(S.ct, P.ct_type, token * S.ct_t + h * S.ct_h, h < S.heads, v[j][g]);
-            G[g].load(S.x, P.x_type, token * S.xt + h * S.xh, P.rms && h < S.heads, x[j][g]);
-          }
-        }
+      for (int h = slot; h - slot < S.heads; h += slots) {
+        float v[NG][2], x[NG][2];
+        load_pairs(G, S.ct, P.ct_type, token * S.ct_t + h * S.ct_h, h < S.heads, v);
+        load_pairs(G, S.x, P.x_type, token * S.xt + h * S.xh, P.rms && h < S.heads, x);
         if (fresh) {
           fresh = false;
           rot_angles(angles[warp], T, P, token, lane);
         }
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          const int h = h0 + j * slots;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const float2 t = G[g].angle(angles[warp]);
-            G[g].turn(make_float2(t.x, -t.y), v[j][g]);
-          }
-          if (P.rms) {
-            float sum = 0.0f, m = 0.0f;
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float w = G[g].has[k] ? gammas[sd][G[g].col[k]] : 0.0f;
-                sum = fmaf(x[j][g][k], x[j][g][k], sum);
-                m = fmaf(v[j][g][k] * w, x[j][g][k], m);
-              }
-            sum = team_sum(sum, team), m = team_sum(m, team);
-            const float r = __frsqrt_rn(fmaf(sum, P.inv_dim, P.eps));
-            m = m * r * P.inv_dim;
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float w = G[g].has[k] ? gammas[sd][G[g].col[k]] : 0.0f, xh = x[j][g][k] * r;
-                if (h < S.heads) dg[sd][g][k] = fmaf(v[j][g][k], xh, dg[sd][g][k]);
-                v[j][g][k] = fmaf(-xh, m, v[j][g][k] * w) * r;
-              }
-          }
+        for (int g = 0; g < NG; ++g) {
+          const float2 t = G[g].angle(angles[warp]);
+          G[g].turn(make_float2(t.x, -t.y), v[g]);
+        }
+        if (P.rms) {
+          float sum = 0.0f, m = 0.0f;
 #pragma unroll
           for (int g = 0; g < NG; ++g)
-            if (h < S.heads) G[g].store(S.y, P.y_type, token * S.yt + h * S.yh, v[j][g]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float w = G[g].has[k] ? gammas[sd][G[g].col[k]] : 0.0f;
+              sum = fmaf(x[g][k], x[g][k], sum);
+              m = fmaf(v[g][k] * w, x[g][k], m);
+            }
+          sum = team_sum(sum, team), m = team_sum(m, team);
+          const float r = __frsqrt_rn(fmaf(sum, P.inv_dim, P.eps));
+          m = m * r * P.inv_dim;
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float w = G[g].has[k] ? gammas[sd][G[g].col[k]] : 0.0f, xh = x[g][k] * r;
+              if (h < S.heads) dg[sd][g][k] = fmaf(v[g][k], xh, dg[sd][g][k]);
+              v[g][k] = fmaf(-xh, m, v[g][k] * w) * r;
+            }
         }
+        if (h < S.heads) store_pairs(G, S.y, P.y_type, token * S.yt + h * S.yh, v);
       }
     }
   }
@@ -824,13 +835,17 @@ static int rot_team(const RotParams& P, int V) {
   return t;
 }
 
-// Pairs a lane of the general kernels.
-template <typename F>
+// Pairs a lane of the general kernels: as many as the head needs, two at least
+// in the forward and four in the backward (fewer lanes a head and more heads a
+// warp save instructions: [16384, 6 + 6, 50] bf16 with one, two and four pairs
+// 50, 39 and 42 us forward, 102, 88 and 77 backward; 33 and 68 since a head's
+// type is looked up once and not for every element).
+template <int LEAST, typename F>
 static int rot_pairs(const RotParams& P, F&& f) {
   const int pairs = P.rot / 2 + (P.dim - P.rot + 1) / 2;
   using std::integral_constant;
-  if (pairs <= 32) return f(integral_constant<int, 1>{});
-  if (pairs <= 64) return f(integral_constant<int, 2>{});
+  if constexpr (LEAST <= 2)
+    if (pairs <= 64) return f(integral_constant<int, 2>{});
   if (pairs <= 128) return f(integral_constant<int, 4>{});
   return f(integral_constant<int, 8>{});
 }
@@ -880,7 +895,7 @@ extern "C" int psk_qk_norm_rotary(const void* q, const void* k, int32_t xt, int6
                    heads_near(out[0]) && heads_near(out[1]) && heads_vec(in[0]) && heads_vec(in[1]) && heads_vec(out[0]) && heads_vec(out[1]);
   cudaStream_t s = (cudaStream_t)stream;
   const bool fast = vec && xt == yt;
-  const int team = rot_team(P, fast ? np : 1), slots = 32 / team, per_sm = !fast ? 3 : np == 4 ? ROT_FWD_CTAS : 2;
+  const int team = rot_team(P, fast ? np : rot_pairs<2>(P, [](auto NG) { return (int)NG.value; })), slots = 32 / team, per_sm = !fast ? 3 : np == 4 ? ROT_FWD_CTAS : 2;
   const int64_t steps = (hq + slots - 1) / slots + (hk + slots - 1) / slots;
   const int64_t most = (int64_t)device_sm_count() * per_sm, warps = most * ROT_WARPS;
   // A token's heads go to one warp where tokens alone fill the GPU, else to several.
@@ -899,7 +914,7 @@ extern "C" int psk_qk_norm_rotary(const void* q, const void* k, int32_t xt, int6
       });
     });
   else
-    rot_pairs(P, [&](auto NG) {
+    rot_pairs<2>(P, [&](auto NG) {
       rotary_any_kernel<NG.value><<<grid, ROT_THREADS, 0, s>>>(P, team);
       return 0;
     });
@@ -992,7 +1007,7 @@ extern "C" int psk_qk_norm_rotary_backward(
                    heads_vec(out[1]) && (!rms || (heads_vec(xs[0]) && heads_vec(xs[1])));
   cudaStream_t s = (cudaStream_t)stream;
   const bool fast = vec && ct == dt && (!rms || xt == ct);
-  const int team = rot_team(P, fast ? np : 1);
+  const int team = rot_team(P, fast ? np : rot_pairs<4>(P, [](auto NG) { return (int)NG.value; }));
   const int64_t most = (int64_t)device_sm_count() * (fast && np == 4 ? ROT_BWD_CTAS : 2);
   if (P.blocks > most) P.blocks = (int32_t)most;
   const unsigned grid = (unsigned)P.blocks;
@@ -1005,7 +1020,7 @@ extern "C" int psk_qk_norm_rotary_backward(
       });
     });
   else
-    rot_pairs(P, [&](auto NG) {
+    rot_pairs<4>(P, [&](auto NG) {
       rotary_any_backward_kernel<NG.value><<<grid, ROT_THREADS, 0, s>>>(P, team);
       return 0;
     });
