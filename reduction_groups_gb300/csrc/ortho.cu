@@ -236,8 +236,8 @@ static OrthoLayout ortho_layout(int32_t leaves, int64_t rows, int64_t cols, int3
   return L;
 }
 
-// One CTA a matrix: fifteen dependent products of one
-// tile or two are launches' latency otherwise ([64, 192] x 2 f32: 116 us).
+// One CTA a matrix: fifteen dependent products of one tile or two are launches'
+// latency otherwise ([64, 192] x 2 f32: 116 us, here 51).
 static bool ortho_is_small(int64_t rows, int64_t cols) {
   const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
   return m <= ORTHO_SMALL_M && n <= ORTHO_SMALL_N;
