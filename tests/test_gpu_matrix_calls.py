@@ -206,3 +206,31 @@ def test_one_side_long(R, rows, cin, cout, dtype):
     # a column's sum: rows of a warp, eight warps, a quarter of at most 912 blocks one after the other, four quarters
     adds = rows / 7296 + 1 + 8 + min(rows / 32 + 1, 912) / 4 + 1 + 3
     close(db, cv.astype(np.float64).sum(0), np.abs(cv.astype(np.float64)).sum(0) * adds * 2.0 ** -24, "f32")
+
+
+@pytest.mark.parametrize("n,rows,cols", [(2, 40, 2000), (1, 2100, 60), (3, 300, 3001), (1, 700, 5000), (9, 129, 1800)])
+@pytest.mark.parametrize("yt", ["bf16", "f32"])
+def test_thin_matrices(R, n, rows, cols, yt):
+    """Few tiles with a long summed axis: shared out among CTAs."""
+    from tests.test_gpu_orthogonalize import _run
+
+    _run(R, n, rows, cols, yt, yt)
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(128, 1000, "bf16"), (128, 1000, "f32"), (600, 700, "bf16")])
+def test_a_lost_copy_of_the_update_ends_in_a_status(R, rows, cols, dtype):
+    x = torch.randn(rows, cols, device="cuda").to(DT[dtype])
+    y, ref = torch.empty_like(x), torch.empty_like(x)
+    ws = scratch(R.psk_orthogonalize_workspace(1, rows, cols, DT[dtype]))
+    R.psk_orthogonalize([x], [ref], 1, workspace=ws)
+    assert R.psk_device_status(reset=True) == 0
+    try:
+        R.psk_test_drop_row(1)
+        R.psk_orthogonalize([x], [y], 1, workspace=ws)
+        torch.cuda.synchronize()
+        assert R.psk_device_status(reset=True) == 1
+    finally:
+        R.psk_test_drop_row(-1)
+    R.psk_orthogonalize([x], [y], 1, workspace=ws)
+    torch.cuda.synchronize()
+    assert R.psk_device_status() == 0 and torch.equal(y, ref)
