@@ -135,8 +135,8 @@ def test_offsets_past_32_bits(R, rows, step):
         assert torch.equal(heads(2048), q) and torch.equal(heads(2560), dq)
     u = torch.empty_like(x)
     R.psk_orthogonalize([x], [u], workspace=ws)
-    R.psk_orthogonalize([far(0, 320)], [far(3072, 320)], workspace=ws)
-    assert torch.equal(far(3072, 320), u)
+    R.psk_orthogonalize([far(0, 320)], [far(3200, 320)], workspace=ws)
+    assert torch.equal(far(3200, 320), u)
     del pool
     torch.cuda.empty_cache()
 
