@@ -21,10 +21,11 @@ namespace psk {
 constexpr int ROT_THREADS = 256;
 constexpr int ROT_WARPS = ROT_THREADS / 32;
 constexpr int ROT_MAX_DIM = 512;
-// CTAs an SM of the kernels with four pairs a lane (by their registers) and
-// steps in flight, the best of those tried at [16384, 32 + 4, 64] bf16: forward
-// 4 and 2 36.2 us (3 and 3 36.8, 4 and 3 38.2), backward 2 65.9 (3 74.8, spilled).
-constexpr int ROT_FWD_CTAS = 4, ROT_BWD_CTAS = 2, ROT_AHEAD = 2;
+// CTAs an SM, by registers: of the forward with four pairs a lane and two or
+// four heads a team at once, and of the rest.
+template <int TY, int SUB>
+constexpr int ROT_FWD_CTAS = TY == PSK_BF16 && SUB == 2 ? 3 : 2;
+constexpr int ROT_BWD_CTAS = 2;
 constexpr int ROT_MAX_BLOCKS = 4 * NOMINAL_SMS;      // CTAs of the backward, at most
 
 struct RotSide {
@@ -331,9 +332,10 @@ __global__ void __launch_bounds__(ROT_THREADS, 2) rotary_any_backward_kernel(con
 // arithmetic; memory is accessed 8 or 16 bytes at a time and pairs that are
 // neighbours come apart as they are widened.  Cosines, sines and scales stand
 // in shared memory by pair.  Both kernels walk a token's heads step after step
-// (a step: one head a team) and have the next steps' loads under way while one
-// is worked on, across tokens too.  Four pairs a lane rather than eight halve
-// its registers, and twice the warps hide the latencies of a short pass.
+// (a step: one head a team, in the forward up to four) and have the next steps'
+// loads under way while one is worked on, across tokens too.  Four pairs a lane
+// rather than eight halve its registers, and the warps that this admits hide the
+// latencies of a short pass.
 
 template <int TY, int NP>
 struct RotRaw {
@@ -481,9 +483,10 @@ __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 // below 2^31 bytes.
 struct RotWalk {
   const char* base;
-  uint32_t offset, step, token;
-  __device__ __forceinline__ RotWalk(const void* p, int64_t ts, int64_t hs, int slot, int slots, int column, int size)
-      : base((const char*)p), offset(((uint32_t)hs * slot + column) * size), step((uint32_t)hs * slots * size),
+  uint32_t offset, sub, step, token;       // sub: between the heads of one step
+  __device__ __forceinline__ RotWalk(const void* p, int64_t ts, int64_t hs, int slot, int slots, int column, int size,
+                                     int subs = 1)
+      : base((const char*)p), offset(((uint32_t)hs * slot + column) * size), sub((uint32_t)hs * slots * size), step(sub * subs),
         token((uint32_t)ts * size) {}
   __device__ __forceinline__ const char* at(uint32_t t, int i) const {
     return base + (uint64_t)t * token + (offset + i * step);
@@ -499,21 +502,28 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 
 // The scale is folded into a token's cosines and sines, once for all its
 // heads, so a head's pass is a sum of squares, y = r (x p + x' q) with x' the
-// pair's other member, and its loads and stores.  AHEAD steps are in flight.
-template <bool NEIGH, int TY, int NP>
-__global__ void __launch_bounds__(ROT_THREADS, NP == 4 ? ROT_FWD_CTAS : 2) rotary_kernel(const __grid_constant__ RotParams P, int team) {
+// pair's other member, and its loads and stores.  A team works on SUB heads at
+// once (a step's bookkeeping serves them all, and their chains of dependent
+// operations overlap) while the next AHEAD steps' loads are under way.
+template <bool NEIGH, int TY, int NP, int SUB>
+__global__ void __launch_bounds__(ROT_THREADS, ROT_FWD_CTAS<TY, SUB>) rotary_kernel(const __grid_constant__ RotParams P, int team) {
   __shared__ __align__(16) RotTables T;
-  constexpr int SIZE = TY == PSK_BF16 ? 2 : 4, AHEAD = NP == 8 && TY == PSK_F32 ? 1 : ROT_AHEAD;
+  constexpr int SIZE = TY == PSK_BF16 ? 2 : 4, AHEAD = NP == 8 && TY == PSK_BF16 ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slots = 32 / team, slot = lane / team;
   const RotLane<NEIGH, NP> G(lane % team, P);
   // steps of both sides, and those in which this lane's team has a head
-  const int nq = (P.side[0].heads + slots - 1) / slots, nk = (P.side[1].heads + slots - 1) / slots;
-  const int lq = (P.side[0].heads - slot + slots - 1) / slots, lk = (P.side[1].heads - slot + slots - 1) / slots;
+  const int nq = (P.side[0].heads + SUB * slots - 1) / (SUB * slots), nk = (P.side[1].heads + SUB * slots - 1) / (SUB * slots);
+  int lq[SUB], lk[SUB];
+#pragma unroll
+  for (int j = 0; j < SUB; ++j) {
+    lq[j] = (P.side[0].heads - slot - j * slots + SUB * slots - 1) / (SUB * slots);
+    lk[j] = (P.side[1].heads - slot - j * slots + SUB * slots - 1) / (SUB * slots);
+  }
   const uint32_t jump = gridDim.x * ROT_WARPS, units = (uint32_t)P.tokens * P.chunks;
   const auto walk = [&](int sd, bool y) {
     const RotSide& S = P.side[sd];
-    return y ? RotWalk(S.y, S.yt, S.yh, slot, slots, G.first[0], SIZE) : RotWalk(S.x, S.xt, S.xh, slot, slots, G.first[0], SIZE);
+    return y ? RotWalk(S.y, S.yt, S.yh, slot, slots, G.first[0], SIZE, SUB) : RotWalk(S.x, S.xt, S.xh, slot, slots, G.first[0], SIZE, SUB);
   };
   const RotWalk Xq = walk(0, false), Xk = walk(1, false), Yq = walk(0, true), Yk = walk(1, true);
   // What is fetched next: step `fi` of unit `fu` (token `ft`), a unit being a
@@ -529,11 +539,18 @@ __global__ void __launch_bounds__(ROT_THREADS, NP == 4 ? ROT_FWD_CTAS : 2) rotar
       fend = fi + P.per < nq + nk ? fi + P.per : nq + nk;
     }
   };
-  RotRaw<TY, NP> raw[AHEAD];
-  const auto fetch = [&](RotRaw<TY, NP>& o) {
+  RotRaw<TY, NP> raw[AHEAD][SUB];
+  const auto fetch = [&](RotRaw<TY, NP> (&o)[SUB]) {
     if (fu >= units) return;
-    if (fi < nq) G.load(Xq.at(ft, fi), fi < lq, o);
-    else G.load(Xk.at(ft, fi - nq), fi - nq < lk, o);
+    if (fi < nq) {
+      const char* p = Xq.at(ft, fi);
+#pragma unroll
+      for (int j = 0; j < SUB; ++j) G.load(p + (uint32_t)(j * Xq.sub), fi < lq[j], o[j]);
+    } else {
+      const char* p = Xk.at(ft, fi - nq);
+#pragma unroll
+      for (int j = 0; j < SUB; ++j) G.load(p + (uint32_t)(j * Xk.sub), fi - nq < lk[j], o[j]);
+    }
     if (++fi == fend) fu += jump, enter();
   };
   enter();
@@ -550,8 +567,9 @@ __global__ void __launch_bounds__(ROT_THREADS, NP == 4 ? ROT_FWD_CTAS : 2) rotar
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
       if (u >= units) break;
-      RotPairs<NP> v;
-      G.widen(raw[j], v);
+      RotPairs<NP> v[SUB];
+#pragma unroll
+      for (int h = 0; h < SUB; ++h) G.widen(raw[j][h], v[h]);
       fetch(raw[j]);
       if (fresh) {
         if (P.chunks == 1) token = u, i = 0, end = nq + nk;
@@ -573,24 +591,42 @@ __global__ void __launch_bounds__(ROT_THREADS, NP == 4 ? ROT_FWD_CTAS : 2) rotar
           qa[m] = __fmul2_rn(gb[m], make_float2(-s[m].x, -s[m].y)), qb[m] = __fmul2_rn(ga[m], s[m]);
         }
       }
-      float2 r = splat(1.0f);
+      float2 r[SUB];
+#pragma unroll
+      for (int h = 0; h < SUB; ++h) r[h] = splat(1.0f);
       if (P.rms) {
-        float2 sum = splat(0.0f);
+        float sums[SUB];
 #pragma unroll
-        for (int m = 0; m < NP / 2; ++m) sum = __ffma2_rn(v.a[m], v.a[m], __ffma2_rn(v.b[m], v.b[m], sum));
-        r = splat(rsqrt_approx(fmaf(team_sum(sum.x + sum.y, team), P.inv_dim, P.eps)));
-      }
-      RotPairs<NP> y;
+        for (int h = 0; h < SUB; ++h) {
+          float2 sum = splat(0.0f);
 #pragma unroll
-      for (int m = 0; m < NP / 2; ++m) {
-        const float2 a = __fmul2_rn(v.a[m], r), b = __fmul2_rn(v.b[m], r);
-        y.a[m] = __fmul2_rn(a, pa[m]), y.b[m] = __fmul2_rn(b, pb[m]);
-        if (G.turns) y.a[m] = __ffma2_rn(b, qa[m], y.a[m]), y.b[m] = __ffma2_rn(a, qb[m], y.b[m]);
+          for (int m = 0; m < NP / 2; ++m) sum = __ffma2_rn(v[h].a[m], v[h].a[m], __ffma2_rn(v[h].b[m], v[h].b[m], sum));
+          sums[h] = sum.x + sum.y;
+        }
+        for (int o = team >> 1; o > 0; o >>= 1)
+#pragma unroll
+          for (int h = 0; h < SUB; ++h) sums[h] += __shfl_xor_sync(0xFFFFFFFFu, sums[h], o);
+#pragma unroll
+        for (int h = 0; h < SUB; ++h) r[h] = splat(rsqrt_approx(fmaf(sums[h], P.inv_dim, P.eps)));
       }
+#pragma unroll
+      for (int h = 0; h < SUB; ++h)
+#pragma unroll
+        for (int m = 0; m < NP / 2; ++m) {
+          const float2 a = __fmul2_rn(v[h].a[m], r[h]), b = __fmul2_rn(v[h].b[m], r[h]);
+          v[h].a[m] = __fmul2_rn(a, pa[m]), v[h].b[m] = __fmul2_rn(b, pb[m]);
+          if (G.turns) v[h].a[m] = __ffma2_rn(b, qa[m], v[h].a[m]), v[h].b[m] = __ffma2_rn(a, qb[m], v[h].b[m]);
+        }
       if (keys) {
-        if (i - nq < lk) G.template store<TY>((char*)Yk.at(token, i - nq), y);
-      } else if (i < lq) {
-        G.template store<TY>((char*)Yq.at(token, i), y);
+        char* p = (char*)Yk.at(token, i - nq);
+#pragma unroll
+        for (int h = 0; h < SUB; ++h)
+          if (i - nq < lk[h]) G.template store<TY>(p + (uint32_t)(h * Yk.sub), v[h]);
+      } else {
+        char* p = (char*)Yq.at(token, i);
+#pragma unroll
+        for (int h = 0; h < SUB; ++h)
+          if (i < lq[h]) G.template store<TY>(p + (uint32_t)(h * Yq.sub), v[h]);
       }
       if (++i == end) u += jump, fresh = true;
     }
@@ -895,7 +931,13 @@ extern "C" int psk_qk_norm_rotary(const void* q, const void* k, int32_t xt, int6
                    heads_near(out[0]) && heads_near(out[1]) && heads_vec(in[0]) && heads_vec(in[1]) && heads_vec(out[0]) && heads_vec(out[1]);
   cudaStream_t s = (cudaStream_t)stream;
   const bool fast = vec && xt == yt;
-  const int team = rot_team(P, fast ? np : rot_pairs<2>(P, [](auto NG) { return (int)NG.value; })), slots = 32 / team, per_sm = !fast ? 3 : np == 4 ? ROT_FWD_CTAS : 2;
+  const int team = rot_team(P, fast ? np : rot_pairs<2>(P, [](auto NG) { return (int)NG.value; })), teams = 32 / team;
+  // Heads a team takes at once: two, or four of bf16 where no more of them are
+  // left empty ([4096, 32 + 8, 128] bf16: one 21.8 us, two 18.9, four 15.4;
+  // [16384, 4 + 1, 256] 19.5, 18.7, 21.7; [16384, 32 + 4, 64] f32 64, 50).
+  const auto padded = [&](int64_t n) { return ((hq + n - 1) / n + (hk + n - 1) / n) * n; };
+  const int subs = !fast || np == 8 ? 1 : xt == PSK_BF16 && padded(4 * teams) <= padded(2 * teams) ? 4 : 2;
+  const int slots = teams * subs, per_sm = !fast || (xt == PSK_BF16 && subs == 2) ? 3 : 2;
   const int64_t steps = (hq + slots - 1) / slots + (hk + slots - 1) / slots;
   const int64_t most = (int64_t)device_sm_count() * per_sm, warps = most * ROT_WARPS;
   // A token's heads go to one warp where tokens alone fill the GPU, else to several.
@@ -908,8 +950,9 @@ extern "C" int psk_qk_norm_rotary(const void* q, const void* k, int32_t xt, int6
   if (fast)
     with_dtype(xt, [&](auto TY) {
       return with_bool(P.neighbours != 0, [&](auto N) {
-        if (np == 4) rotary_kernel<N.value, TY.value, 4><<<grid, ROT_THREADS, 0, s>>>(P, team);
-        else rotary_kernel<N.value, TY.value, 8><<<grid, ROT_THREADS, 0, s>>>(P, team);
+        if (subs == 1) rotary_kernel<N.value, TY.value, 8, 1><<<grid, ROT_THREADS, 0, s>>>(P, team);
+        else if (subs == 2) rotary_kernel<N.value, TY.value, 4, 2><<<grid, ROT_THREADS, 0, s>>>(P, team);
+        else rotary_kernel<N.value, PSK_BF16, 4, 4><<<grid, ROT_THREADS, 0, s>>>(P, team);
         return 0;
       });
     });
