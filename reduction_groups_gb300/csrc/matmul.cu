@@ -1023,14 +1023,17 @@ static int launch_shape(const MMCall* calls, const MMColumnSums* sums, cudaStrea
 }
 
 // CTAs that share a tile of 128 columns and `rows` rows: what fills the SMs
-// once, two blocks of the summed axis each at least; four at most beyond eight
-// tiles, because few clusters of eight such CTAs find their place at one time
-// (512 x 2048 x 512, 16 tiles: 12.6 us by eight, 7.2 by four; the gradients of
-// 16384 x 128 x 128, 1 and 128: 32.5 and 42.2).
+// once, two blocks of the summed axis each at least, as long as all clusters
+// find their place at one time: of eight CTAs up to eight tiles (512 x 2048 x
+// 512, 16 tiles: 12.6 us by eight, 7.2 by four; the gradients of 16384 x 128 x
+// 128, 1 and 128: 32.5 and 42.2), of four up to 36 (768 x 2048 x 768, 36: 8.6 us,
+// by three 9.1; 2432 x 2048 x 256, 38: 15.0 and 9.1), of three up to 42 (1280 x
+// 4096 x 512, 40: 12.4 us, by two 15.8; the gradients of 2000 x 304 x 2000, 48:
+// 35.1 and 20.4).
 static int split_of(const MMCall& C, int rows) {
   const int64_t tiles = ((C.n + 127) / 128) * ((C.m + rows - 1) / rows) * C.matrices, blocks = (C.k + MM_BK - 1) / MM_BK;
   int64_t split = device_sm_count() / tiles;
-  const int64_t most = tiles <= 8 ? 8 : 4;
+  const int64_t most = tiles <= 8 ? 8 : tiles <= 36 ? 4 : tiles <= 42 ? 3 : 2;
   split = split < 1 ? 1 : split > most ? most : split;
   while (split > 1 && blocks < 2 * split) --split;
   return (int)split;
@@ -1078,18 +1081,30 @@ static int launch_split(const MMCall& C, const MMColumnSums* sums, cudaStream_t 
   return check_launch("matrix product kernel of few tiles");
 }
 
-// Rows of the split kernel's tile for a product (0: it gains nothing).
+// Rows of the split kernel's tile for a product of planes (0: it gains nothing):
+// 64 or 128, by the time of the blocks that one CTA takes in turn, 20 and 23 by
+// measure (1 x 1024 x 1024's update 300 us by 64, 215 by 128; 509 x 771 x 1003's
+// gradients, with both in one launch 35, apart 29; 300 x 3000 x 400 the same).
+static int split_rows_sum(const MMCall& C) {
+  const int64_t blocks = (C.k + MM_BK - 1) / MM_BK;
+  const int s64 = split_of(C, 64), s128 = split_of(C, 128);
+  const bool wide = (blocks + s128 - 1) / s128 * 23 < (blocks + s64 - 1) / s64 * 20;
+  return (wide ? s128 : s64) < 2 ? 0 : wide ? 128 : 64;
+}
+
+// The same of any product.
 static int split_rows(const MMCall& C) {
   if (C.ortho) {
     // Of f32 results wherever they can (1 x 512 x 512, five steps: 201 us, 111);
     // else, where both triangles are more tiles than one, if a tile's summed axis
     // shrinks by 12 blocks at least (8 x 64 x 4096 162 us, 92; 1 x 512 x 1024 105,
     // 97; by 8 or less 1 x 1024 x 1024 132, 150, and 1 x 512 x 512 95, 101).
-    const int rows = C.pairs > 1 || C.m <= 64 ? 64 : 128, split = split_of(C, rows);
+    if (!C.e.to || C.pairs > 1) return C.e.to ? split_rows_sum(C) : 0;
+    const int rows = C.m <= 64 ? 64 : 128, split = split_of(C, rows);
     const int64_t blocks = (C.k + MM_BK - 1) / MM_BK;
-    return C.e.to && split >= 2 && (C.pairs > 1 || blocks - blocks / split >= 12) ? rows : 0;
+    return split >= 2 && blocks - blocks / split >= 12 ? rows : 0;
   }
-  if (C.pairs > 1) return split_of(C, 64) >= 2 ? 64 : 0;
+  if (C.pairs > 1) return split_rows_sum(C);
   // (the rows' operand is read along the summed axis, or in boxes of 64 rows)
   if (C.m <= 64) return C.m > 32 || !C.a.k_inner ? 64 : C.m > 16 ? 32 : 16;
   return split_of(C, 128) >= 2 ? 128 : 0;
@@ -1132,8 +1147,9 @@ int mm_launch(const MMCall* calls, int count, const MMColumnSums* sums, cudaStre
   if (count == 2) {
     // One launch where one kernel serves both, their tiles together fill the SMs
     // once at most, and the longer tile takes less than the two launches with
-    // their summed axes shared among CTAs ([509, 771] x [771, 1003] f32: 78 us as
-    // two unshared ones, 40 as one; 16384 x 128 x 128 bf16: 106 us as one).
+    // their summed axes shared among CTAs (2000 x 304 x 2000 bf16: 20 us as one, 35
+    // as two by threes; 509 x 771 x 1003 f32: 78 as two unshared ones, 35 as one,
+    // 29 as two shared; 16384 x 128 x 128 bf16: 106 as one, 33 as two shared).
     // More tiles run better one product after the other (8192 x 2048 x 5632: 252
     // us, together 275).
     int64_t tiles = 0, longest = 0, apart = 0;
@@ -1164,7 +1180,7 @@ int mm_launch(const MMCall* calls, int count, const MMColumnSums* sums, cudaStre
   if (C.ortho) {
     switch (split_rows(C)) {
       case 64: return sum ? launch_split<64, true, true>(C, sums, stream) : launch_split<64, false, true>(C, sums, stream);
-      case 128: return launch_split<128, false, true>(C, sums, stream);
+      case 128: return sum ? launch_split<128, true, true>(C, sums, stream) : launch_split<128, false, true>(C, sums, stream);
       default: break;
     }
     return sum ? launch_kind<MM_ORTHO, true>(calls, sums, stream) : launch_kind<MM_ORTHO, false>(calls, sums, stream);
@@ -1173,7 +1189,7 @@ int mm_launch(const MMCall* calls, int count, const MMColumnSums* sums, cudaStre
     case 16: return launch_split<16, false>(C, sums, stream);
     case 32: return launch_split<32, false>(C, sums, stream);
     case 64: return sum ? launch_split<64, true>(C, sums, stream) : launch_split<64, false>(C, sums, stream);
-    case 128: return launch_split<128, false>(C, sums, stream);
+    case 128: return sum ? launch_split<128, true>(C, sums, stream) : launch_split<128, false>(C, sums, stream);
     default: break;
   }
   if (sum) return launch_kind<MM_ANY, true>(calls, sums, stream);
