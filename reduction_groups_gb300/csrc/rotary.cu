@@ -444,6 +444,10 @@ struct RotLane {
 template <bool NEIGH>
 __device__ __forceinline__ void rot_tables(RotTables& T, const RotParams& P) {
   const int half = P.rot / 2, pairs = P.dim / 2;
+  // A team of more lanes than the head has groups reads scales past its pairs:
+  // zeros, for whatever an earlier kernel left there times zero may be NaN.
+  for (int j = pairs + threadIdx.x; j < ROT_MAX_DIM / 2; j += ROT_THREADS)
+    T.gamma[0][0][j] = T.gamma[0][1][j] = T.gamma[1][0][j] = T.gamma[1][1][j] = 0.0f;
   for (int j = threadIdx.x; j < pairs; j += ROT_THREADS) {
     if (j < half) {
       const float f = P.tokens ? P.freqs[j] : 0.0f;
