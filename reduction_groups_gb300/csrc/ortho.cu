@@ -207,10 +207,17 @@ __global__ void __launch_bounds__(256) ortho_copy_kernel(const __grid_constant__
   }
 }
 
+// Offsets from the workspace's first 32-byte boundary, and the bytes that hold
+// them behind any 16-byte one.
 struct OrthoLayout {
   uint64_t sums, factors, table, x0, x1, a, b, bytes;
   int64_t xsize, asize;         // elements of one plane
 };
+// The planes' rows go by 32 bytes at a time.
+constexpr uint64_t ORTHO_ALIGN = 32;
+static char* ortho_base(void* workspace) {
+  return (char*)(((uintptr_t)workspace + ORTHO_ALIGN - 1) / ORTHO_ALIGN * ORTHO_ALIGN);
+}
 
 static int64_t ortho_up16(int64_t v) { return (v + 15) / 16 * 16; }      // rows of whole 32-byte sectors
 
@@ -232,7 +239,7 @@ static OrthoLayout ortho_layout(int32_t leaves, int64_t rows, int64_t cols, int3
   L.x1 = take((uint64_t)leaves * ORTHO_PARTS * L.xsize * 2);
   L.a = take((uint64_t)leaves * planes * L.asize * 2);
   L.b = take((uint64_t)leaves * planes * L.asize * 2);
-  L.bytes = at;
+  L.bytes = at + ORTHO_ALIGN - 16;
   return L;
 }
 
@@ -342,14 +349,15 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
   if (ortho_is_small(rows, cols)) {
     const char* copies = nullptr;
     if (crossed) {                       // every x is read before the first y is written
-      copies = (const char*)workspace + L.x0;
-      ortho_copy_kernel<<<n_leaves, 256, 0, s>>>(T, (int)rows, (int)cols, xt, (char*)workspace + L.x0);
+      char* to = ortho_base(workspace) + L.x0;
+      copies = to;
+      ortho_copy_kernel<<<n_leaves, 256, 0, s>>>(T, (int)rows, (int)cols, xt, to);
       rc = check_launch("orthogonalisation's copies");
       if (rc) return rc;
     }
     return ortho_small_launch(leaves, copies, n_leaves, rows, cols, xt, yt, coefficients, steps, eps, scale, s);
   }
-  char* ws = (char*)workspace;
+  char* ws = ortho_base(workspace);
   OrthoShape S{};
   S.rows = rows, S.cols = cols;
   S.tall = rows > cols;
