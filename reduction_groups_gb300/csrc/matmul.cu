@@ -851,6 +851,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid
         if (lane == 0) mbar_arrive(&acc_empty[buf]);
       }
       // (all of them: the ring is another's until every warp has its last sums)
+      __syncwarp();
       named_barrier(1, SPLIT_THREADS - 64);
       if (ok) {
 #pragma unroll
@@ -871,7 +872,6 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid
       fence_before();
     }
   }
-  __syncwarp();
   cluster_sync_all();
   fence_after();
   if (warp == 1) tmem_free<1>(tmem, S::TMEM_COLS);
