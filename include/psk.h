@@ -534,9 +534,12 @@ int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int64_t cols, 
  * The products of a sum are exact (an f32 operand enters as three bf16 parts,
  * products of parts below 2^-24 of the largest left out) and added in f32: by
  * the tensor core, which truncates (at most 17 f32 steps of the sum so far for
- * each 16 terms), and with an f32 operand every 256 terms by one rounded
- * addition.  The order is fixed by the sizes, types, the rows' alignment and
- * the device's SMs.  z, act and the residual's sum are f32; y and z are rounded
+ * each 16 terms; one on average), and with an f32 operand every 256 terms by
+ * one rounded addition, with bf16 operands every 1024 where the result (y or z)
+ * is f32 and the sum longer than 2048 terms, or it is longer than 65536: an f32
+ * result of bf16 operands is off by about 2.4e-6 of the sum of its terms'
+ * magnitudes at most.  The order is fixed by the sizes, types, the rows'
+ * alignment and the device's SMs.  z, act and the residual's sum are f32; y and z are rounded
  * once.  PSK_ACT_GELU is z Phi(z), its negative tail included to 2^-20 of its
  * value, where x, w, y, z, bias and residual are all bf16 to 2^-16; at
  * z = +-inf an activation is its limit.  A row of
@@ -566,8 +569,8 @@ int psk_linear(const void* x, int32_t xt, int64_t ldx, const void* w, int32_t wt
  * accumulate != 0, dw and dbias are added to (micro-batches that share a
  * leaf): RN(dw + sum).  act'(z) is f32 to 2^-20 absolutely, dz is formed in
  * f32; a product of bf16 ct, bf16 operand and bf16 result takes it rounded to
- * bf16, any other to f32's accuracy.  act' of relu at 0 is 0.  rows == 0 gives dw = 0 and dbias = 0
- * (accumulating: unchanged).  No overlap of what is written with anything
+ * bf16, any other to f32's accuracy.  Sums are taken as psk_linear's.  act' of
+ * relu at 0 is 0.  rows == 0 gives dw = 0 and dbias = 0 (accumulating: unchanged).  No overlap of what is written with anything
  * else.  rows, out <= 2^25, in < 2^31 - 1024.  workspace as for psk_linear,
  * psk_linear_backward_workspace bytes for the same arguments. */
 int psk_linear_backward_workspace(const void* ct, int32_t ct_t, int64_t ldc, const void* x, int32_t xt, int64_t ldx,

@@ -34,8 +34,13 @@
 
 namespace psk {
 
+// How a tile's sum is taken (SUM): whole, in one accumulator; by pieces of the
+// summed axis, which the epilogue's warps add up in registers; or by pieces of
+// the products of several planes, the smaller ones in an accumulator beside.
+constexpr int MM_WHOLE = 0, MM_PIECES = 1, MM_PARTS = 2;
+
 // Warps of the epilogue: sixteen, or eight where each keeps its sums in registers.
-template <bool SUM>
+template <int SUM>
 struct MMWarps {
   static constexpr int EPI = SUM ? 8 : 16, THREADS = 128 + 32 * EPI;
 };
@@ -47,7 +52,7 @@ struct MMProblem {
   int64_t m, n;
   int32_t kblocks, pairs, planes_a, planes_b;
   int32_t chunk;                           // blocks of the summed axis that one accumulator takes
-  int32_t na, nb;                          // planes of A and B in a stage (one each but with SUM)
+  int32_t na, nb;                          // planes of A and B in a stage (one each but with MM_PARTS)
   int32_t a_k, b_k, tiles_m, tiles_n, tiles, symmetric;      // tiles: of one matrix
   uint8_t pa[8], pb[8];
 };
@@ -392,24 +397,26 @@ __device__ __forceinline__ void column_sums(const MMColumnSums& J, int64_t first
 
 // KIND: an activation with every matrix in bf16, 32-byte aligned rows and n a
 // multiple of 16; MM_ANY: the linear layer with any types; MM_ORTHO.
-template <int CG, int BN, int KIND, bool SUM>
+template <int CG, int BN, int KIND, int SUM>
 struct MMShape {
+  static constexpr bool PARTS = SUM == MM_PARTS;
   static constexpr int BM = 128 * CG;
   static constexpr int B_ROWS = BN / CG;                        // of B's tile in one CTA
   static constexpr int B_BYTES = B_ROWS * MM_BK * 2;
   static constexpr int STAGE = MM_A_BYTES + B_BYTES;            // of one plane each
   static constexpr int TURN = KIND == MM_ANY ? MMWarps<SUM>::EPI * 32 * 17 * 4 : 0;     // of the epilogue
   static constexpr int STAGES = (225 * 1024 - TURN) / STAGE < 8 ? (225 * 1024 - TURN) / STAGE : 8;
-  static constexpr int RING = SUM ? (225 * 1024 - TURN) / 1024 * 1024 : STAGES * STAGE;
+  static constexpr int RING = PARTS ? (225 * 1024 - TURN) / 1024 * 1024 : STAGES * STAGE;
   static constexpr int SMEM = RING + TURN + 1024;               // and what aligns the ring to 1024 bytes
-  // Columns of one accumulator: with SUM the last product of planes has its own,
-  // beside that of the others.
-  static constexpr int ACC = SUM ? 2 * BN : BN;
+  // Columns of one accumulator: the last product of planes has its own, beside
+  // that of the others.
+  static constexpr int ACC = PARTS ? 2 * BN : BN;
 };
 
-template <int CG, int BN, int KIND, bool SUM, int COUNT>
+template <int CG, int BN, int KIND, int SUM, int COUNT>
 __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __grid_constant__ MMParams G) {
   using S = MMShape<CG, BN, KIND, SUM>;
+  constexpr bool PARTS = S::PARTS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[S::STAGES], empty[S::STAGES], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
@@ -418,8 +425,8 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int32_t first = blockIdx.x / CG, step = gridDim.x / CG;
   const int32_t total = G.total;
-  const int stages = SUM ? G.stages : S::STAGES;
-  const uint32_t slot_bytes = SUM ? G.slot_bytes : S::STAGE;
+  const int stages = PARTS ? G.stages : S::STAGES;
+  const uint32_t slot_bytes = PARTS ? G.slot_bytes : S::STAGE;
 
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < S::STAGES; ++i) {
@@ -454,7 +461,7 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
       const int q = COUNT == 2 && t >= G.split;
       const MMProblem& P = G.q[q];
       const Tile tile = tile_at<S::BM / BN>(P, q ? t - G.split : t);
-      const int na = SUM ? P.na : 1, nb = SUM ? P.nb : 1;
+      const int na = PARTS ? P.na : 1, nb = PARTS ? P.nb : 1;
       const int32_t am = tile.tm * S::BM + (int32_t)rank * 128;
       const int32_t bn = tile.tn * BN + (int32_t)rank * S::B_ROWS;
       for (int32_t kb = 0; kb < P.kblocks; ++kb) {
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
       const uint32_t idesc = (1u << 4) | (G.f16 ? 0u : (1u << 7) | (1u << 10)) | (P.a_k ? 0u : 1u << 15) |
                              (P.b_k ? 0u : 1u << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(S::BM >> 4) << 24);
       const uint32_t a_step = (P.a_k ? 32u : 2048u) >> 4, b_step = (P.b_k ? 32u : 2048u) >> 4;
-      const int32_t b_first = (SUM ? P.na : 1) * MM_A_BYTES;
+      const int32_t b_first = (PARTS ? P.na : 1) * MM_A_BYTES;
       for (int32_t k = 0; ok && k < P.kblocks; k += P.chunk, ++n) {
         const int buf = n & 1;
         if (!mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1)) {
@@ -519,13 +526,13 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
           }
           fence_after();
           const uint32_t at = ring + slot * slot_bytes;
-          for (int p = 0; p < (SUM ? P.pairs : 1); ++p) {
-            const uint32_t a = at + (SUM ? P.pa[p] : 0) * MM_A_BYTES, b = at + b_first + (SUM ? P.pb[p] : 0) * S::B_BYTES;
+          for (int p = 0; p < (PARTS ? P.pairs : 1); ++p) {
+            const uint32_t a = at + (PARTS ? P.pa[p] : 0) * MM_A_BYTES, b = at + b_first + (PARTS ? P.pb[p] : 0) * S::B_BYTES;
             const uint64_t da = operand_desc(a, MM_A_BYTES / 2), db = operand_desc(b, 64 * MM_BK * 2);
 #pragma unroll
             for (int j = 0; j < MM_BK / 16; ++j)
-              mma_16<CG>(SUM && p + 1 < P.pairs ? d + BN : d, da + (uint64_t)(j * a_step), db + (uint64_t)(j * b_step), idesc,
-                         (i | j) != 0 || (SUM && p > 0 && p + 1 < P.pairs));
+              mma_16<CG>(PARTS && p + 1 < P.pairs ? d + BN : d, da + (uint64_t)(j * a_step), db + (uint64_t)(j * b_step), idesc,
+                         (i | j) != 0 || (PARTS && p > 0 && p + 1 < P.pairs));
           }
           mma_commit<CG>(&empty[slot]);
           if (++slot == stages) slot = 0, ++round;
@@ -556,6 +563,10 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
       bool ok = true;
       if constexpr (SUM) {
         float sum[COLS];
+        if constexpr (!PARTS) {
+#pragma unroll
+          for (int i = 0; i < COLS; ++i) sum[i] = 0.0f;
+        }
         for (int32_t k = 0; k < P.kblocks; k += P.chunk, ++n) {
           const int buf = n & 1;
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[buf], (n >> 1) & 1));
@@ -563,11 +574,18 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
           fence_after();
 #pragma unroll
           for (int c = 0; c < COLS; c += 16) {
-            float v[16], w[16];
-            tmem_load16(mine + buf * S::ACC + BN + c, w);
-            tmem_load16(mine + buf * S::ACC + c, v);
+            float v[16];
+            if constexpr (PARTS) {
+              float w[16];
+              tmem_load16(mine + buf * S::ACC + BN + c, w);
+              tmem_load16(mine + buf * S::ACC + c, v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[c + i] = k ? sum[c + i] + (v[i] + w[i]) : v[i] + w[i];
+              for (int i = 0; i < 16; ++i) sum[c + i] = k ? sum[c + i] + (v[i] + w[i]) : v[i] + w[i];
+            } else {
+              tmem_load16(mine + buf * S::ACC + c, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[c + i] += v[i];
+            }
           }
           fence_before();
           __syncwarp();
@@ -634,13 +652,14 @@ __global__ void __launch_bounds__(MMWarps<SUM>::THREADS, 1) mm_kernel(const __gr
 // other way round, 128 columns of the second operand as the tensor core's rows
 // and BN rows of the first as its N: for few rows of x the weights' bytes are
 // the time, and lanes hold neighbouring columns of y.
-template <int BN, bool SUM>
+template <int BN, int SUM>
 struct SplitShape {
+  static constexpr bool PARTS = SUM == MM_PARTS;
   static constexpr int B_BYTES = BN * MM_BK * 2, STAGE = MM_A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN < 128 ? 8 : 6;                // with SUM as many as the planes leave room for
-  static constexpr int RING = SUM ? 224 * 1024 : STAGES * STAGE;
+  static constexpr int STAGES = BN < 128 ? 8 : 6;                // with planes as many as they leave room for
+  static constexpr int RING = PARTS ? 224 * 1024 : STAGES * STAGE;
   static constexpr int SMEM = RING + 1024;
-  static constexpr int ACC = SUM ? 2 * BN : BN, BUFS = SUM ? 2 : 1;
+  static constexpr int ACC = PARTS ? 2 * BN : BN, BUFS = SUM ? 2 : 1;
   static constexpr int TMEM_COLS = BUFS * ACC < 32 ? 32 : BUFS * ACC;
 };
 constexpr int SPLIT_THREADS = 320;
@@ -708,9 +727,10 @@ __device__ __forceinline__ void ortho_row4(const MMEpilogue& E, int32_t matrix, 
   }
 }
 
-template <int BN, bool SUM, bool ORTHO>
+template <int BN, int SUM, bool ORTHO>
 __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid_constant__ SplitParams G) {
   using S = SplitShape<BN, SUM>;
+  constexpr bool PARTS = S::PARTS;
   const MMProblem& P = G.q;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[S::STAGES], empty[S::STAGES], acc_full[2], acc_empty[2], drain;
@@ -722,8 +742,8 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid
   const int32_t tc = tile / G.row_tiles, tr = tile - tc * G.row_tiles;
   const int32_t za = matrix * P.planes_a, zb = matrix * P.planes_b;
   const int32_t k0 = (int32_t)((int64_t)P.kblocks * rank / split), k1 = (int32_t)((int64_t)P.kblocks * (rank + 1) / split);
-  const int stages = SUM ? G.stages : S::STAGES, na = SUM ? P.na : 1, nb = SUM ? P.nb : 1;
-  const uint32_t slot_bytes = SUM ? G.slot_bytes : S::STAGE;
+  const int stages = PARTS ? G.stages : S::STAGES, na = PARTS ? P.na : 1, nb = PARTS ? P.nb : 1;
+  const uint32_t slot_bytes = PARTS ? G.slot_bytes : S::STAGE;
   const int32_t chunk = SUM ? P.chunk : P.kblocks;
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < S::STAGES; ++i) {
@@ -802,10 +822,10 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid
         }
         fence_after();
         const uint32_t at = ring + s * slot_bytes;
-        for (int p = 0; p < (SUM ? P.pairs : 1); ++p) {
-          const bool small = SUM && p + 1 < P.pairs;
-          const uint64_t da = operand_desc(at + (SUM ? P.pa[p] : 0) * MM_A_BYTES, MM_A_BYTES / 2);
-          const uint64_t db = operand_desc(at + na * MM_A_BYTES + (SUM ? P.pb[p] : 0) * S::B_BYTES, 64 * MM_BK * 2);
+        for (int p = 0; p < (PARTS ? P.pairs : 1); ++p) {
+          const bool small = PARTS && p + 1 < P.pairs;
+          const uint64_t da = operand_desc(at + (PARTS ? P.pa[p] : 0) * MM_A_BYTES, MM_A_BYTES / 2);
+          const uint64_t db = operand_desc(at + na * MM_A_BYTES + (PARTS ? P.pb[p] : 0) * S::B_BYTES, 64 * MM_BK * 2);
 #pragma unroll
           for (int j = 0; j < MM_BK / 16; ++j)
             mma_16<1>(small ? d + BN : d, da + (uint64_t)(j * a_step), db + (uint64_t)(j * b_step), idesc,
@@ -830,6 +850,10 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid
     const uint32_t mine = tmem + ((uint32_t)row << 16);
     if constexpr (SUM) {
       float sum[MINE * 16];
+      if constexpr (!PARTS) {
+#pragma unroll
+        for (int j = 0; j < MINE * 16; ++j) sum[j] = 0.0f;
+      }
       bool ok = true;
       int n = 0;
       for (int32_t k = k0; k < k1; k += chunk, ++n) {
@@ -839,12 +863,20 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid
         fence_after();
 #pragma unroll
         for (int c = 0; c < MINE; ++c) {
-          float v[16], w[16];
+          float v[16];
           const int at = (share + 2 * c) * 16;
-          tmem_load16(mine + buf * S::ACC + BN + at, w);
-          tmem_load16(mine + buf * S::ACC + at, v);
+          if (at >= BN) break;             // (of 16 columns the second four warps have none)
+          if constexpr (PARTS) {
+            float w[16];
+            tmem_load16(mine + buf * S::ACC + BN + at, w);
+            tmem_load16(mine + buf * S::ACC + at, v);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) sum[16 * c + j] = n ? sum[16 * c + j] + (v[j] + w[j]) : v[j] + w[j];
+            for (int j = 0; j < 16; ++j) sum[16 * c + j] = n ? sum[16 * c + j] + (v[j] + w[j]) : v[j] + w[j];
+          } else {
+            tmem_load16(mine + buf * S::ACC + at, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[16 * c + j] += v[j];
+          }
         }
         fence_before();
         __syncwarp();
@@ -855,7 +887,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) mm_split_kernel(const __grid
       named_barrier(1, SPLIT_THREADS - 64);
       if (ok) {
 #pragma unroll
-        for (int c = 0; c < MINE; ++c)
+        for (int c = 0; c < MINE && (share + 2 * c) * 16 < BN; ++c)
 #pragma unroll
           for (int j = 0; j < 16; ++j) part[((share + 2 * c) * 16 + j) * SPLIT_ROW + row + lane] = sum[16 * c + j];
       }
@@ -951,20 +983,37 @@ static int encode_operand(CUtensorMap* map, const MMOperand& o, int64_t matrices
   return PSK_OK;
 }
 
-// Blocks of the summed axis that one accumulator takes where the sum is an
-// f32 operand's: the tensor core's additions truncate (an f32 result of 2048
-// terms is off by 1e-5 of its size, of 65536 by 2e-4), so every 256 terms the
-// accumulator is added to a register with one rounding instead.  And the small
-// products of planes have an accumulator of their own: added into the large
-// one, each would truncate it again (1.5e-6 of the result's size, apart 1.5e-7).
-constexpr int MM_SUM_BLOCKS = 4;
+// Blocks of the summed axis that one accumulator takes where the sum is taken
+// by pieces: the tensor core's additions truncate, always to one side (terms of
+// one sign: 2048 are off by 2.4e-6 of their sum, 8192 by 9e-6, 65536 by up to
+// 3.4e-4), so the accumulator is added to a register with one rounding instead.
+// With an f32 operand every 256 terms; and the small products of planes have an
+// accumulator of their own: added into the large one, each would truncate it
+// again (1.5e-6 of the result's size, apart 1.5e-7).  bf16 operands every 1024
+// terms, which keeps f32 results to 1e-6 at any length and hides the last piece's
+// epilogue behind the next tile's products (16384 x 2048 x 5632, f32 result, in
+// pieces of 256 terms 453 us, 512 391, 1024 301, 2048 285, whole 231).
+constexpr int MM_SUM_BLOCKS = 4, MM_PIECE_BLOCKS = 16;
+
+// By pieces go the sums of f32 operands; those of bf16 ones above 2048 terms
+// (that one CTA takes) whose result is stored in f32 (8192 x 2048 x 5632's
+// gradients with an f32 dw 286 us for 270, off by 1e-6 instead of 9e-6); and
+// those so long that truncations would come near bf16's rounding of the result
+// (half a step is 2e-3 to 4e-3).
+constexpr int64_t MM_WHOLE_F32 = 2048, MM_WHOLE_BF16 = 65536;
+static int sum_of(const MMCall& C, int64_t terms) {
+  if (C.pairs > 1) return MM_PARTS;
+  const bool f32 = !C.ortho && (C.e.yt == PSK_F32 || (C.e.z && C.e.zt == PSK_F32));
+  return terms > (f32 ? MM_WHOLE_F32 : MM_WHOLE_BF16) ? MM_PIECES : MM_WHOLE;
+}
+static int piece_of(int sum) { return sum == MM_PARTS ? MM_SUM_BLOCKS : MM_PIECE_BLOCKS; }
 
 // Absent, or bf16 rows that begin on 32-byte boundaries.
 static bool rows_32(const void* p, int32_t dt, int64_t ld) {
   return !p || (dt == PSK_BF16 && (uintptr_t)p % 32 == 0 && ld % 16 == 0);
 }
 
-template <int CG, int BN, int KIND, bool SUM, int COUNT>
+template <int CG, int BN, int KIND, int SUM, int COUNT>
 static int launch_shape(const MMCall* calls, const MMColumnSums* sums, cudaStream_t stream) {
   using S = MMShape<CG, BN, KIND, SUM>;
   MMParams G{};
@@ -978,7 +1027,7 @@ static int launch_shape(const MMCall* calls, const MMColumnSums* sums, cudaStrea
     P.e = C.e;
     P.m = C.m, P.n = C.n;
     P.kblocks = (int32_t)((C.k + MM_BK - 1) / MM_BK), P.pairs = C.pairs;
-    P.chunk = SUM ? MM_SUM_BLOCKS : P.kblocks;
+    P.chunk = sum_of(C, C.k) == MM_WHOLE ? P.kblocks : piece_of(SUM);
     P.planes_a = C.a.planes, P.planes_b = C.b.planes;
     P.a_k = C.a.k_inner, P.b_k = C.b.k_inner;
     for (int i = 0; i < C.pairs; ++i) {
@@ -1039,7 +1088,7 @@ static int split_of(const MMCall& C, int rows) {
   return (int)split;
 }
 
-template <int BN, bool SUM, bool ORTHO = false>
+template <int BN, int SUM, bool ORTHO = false>
 static int launch_split(const MMCall& C, const MMColumnSums* sums, cudaStream_t stream) {
   using S = SplitShape<BN, SUM>;
   SplitParams G{};
@@ -1049,7 +1098,7 @@ static int launch_split(const MMCall& C, const MMColumnSums* sums, cudaStream_t 
   if (rc) return rc;
   P.e = C.e;
   P.m = C.n, P.n = C.m;
-  P.kblocks = (int32_t)((C.k + MM_BK - 1) / MM_BK), P.chunk = MM_SUM_BLOCKS, P.pairs = C.pairs;
+  P.kblocks = (int32_t)((C.k + MM_BK - 1) / MM_BK), P.chunk = piece_of(SUM), P.pairs = C.pairs;
   P.a_k = C.b.k_inner, P.b_k = C.a.k_inner, P.planes_a = C.b.planes, P.planes_b = C.a.planes;
   for (int i = 0; i < C.pairs; ++i) {
     P.pa[i] = C.pb[i], P.pb[i] = C.pa[i];
@@ -1115,11 +1164,11 @@ static int split_rows(const MMCall& C) {
 // take about 0.34 us of a pair and 0.30 us of one CTA, whose 128 columns are
 // bound by shared memory (operands read and filled in: 2048^3 16.8 and 24.3 us,
 // 512 x 2048 x 5632 15.9 and 23.8, 1024^3 11.4 and 9.0, 128 x 2048 x 5632 15.6
-// and 13.4).  With SUM always the latter: two accumulators of 256 columns would
+// and 13.4).  With planes always the latter: two accumulators of 256 columns would
 // leave no second pair of them, and pairs on 256 x 128 gain nothing (4096 x 2048
 // x 2048 f32 199 us, single ones 195).  The update's products take 128 x 64 where
 // those still fit the SMs once (512 x 512, five steps: 114 us, 95).
-template <int KIND, bool SUM>
+template <int KIND, int SUM>
 static int launch_kind(const MMCall* calls, const MMColumnSums* sums, cudaStream_t stream) {
   const MMCall& C = calls[0];
   const int64_t sms = device_sm_count(), pairs = sms / 2;
@@ -1127,11 +1176,11 @@ static int launch_kind(const MMCall* calls, const MMColumnSums* sums, cudaStream
     const int64_t tm = (C.m + side - 1) / side, tn = (C.n + side - 1) / side;
     return ((C.symmetric ? tm * (tm + 1) / 2 : tm * tn) * C.matrices + units - 1) / units;
   };
-  if constexpr (!SUM)
+  if constexpr (SUM == MM_WHOLE || (SUM == MM_PIECES && KIND == MM_ANY))
     if (pairs > 0 && waves(256, pairs) * 34 < waves(128, sms) * 30)
-      return launch_shape<2, 256, KIND, false, 1>(calls, sums, stream);
-  if constexpr (KIND == MM_ORTHO && !SUM)
-    if (waves(128, 1) * 2 <= sms) return launch_shape<1, 64, KIND, false, 1>(calls, sums, stream);
+      return launch_shape<2, 256, KIND, SUM, 1>(calls, sums, stream);
+  if constexpr (KIND == MM_ORTHO && SUM == MM_WHOLE)
+    if (waves(128, 1) * 2 <= sms) return launch_shape<1, 64, KIND, MM_WHOLE, 1>(calls, sums, stream);
   return launch_shape<1, 128, KIND, SUM, 1>(calls, sums, stream);
 }
 
@@ -1141,10 +1190,35 @@ static bool is_wide(const MMCall& C) {
          rows_32(E.bias, E.bt, 0);
 }
 
+// rows: split_rows' answer.
+template <int SUM>
+static int launch_one(const MMCall* calls, int rows, const MMColumnSums* sums, cudaStream_t stream) {
+  const MMCall& C = calls[0];
+  if (C.ortho) {
+    if (rows == 64) return launch_split<64, SUM, true>(C, sums, stream);
+    if (rows == 128) return launch_split<128, SUM, true>(C, sums, stream);
+    return launch_kind<MM_ORTHO, SUM>(calls, sums, stream);
+  }
+  if constexpr (SUM != MM_PARTS) {
+    if (rows == 16) return launch_split<16, SUM>(C, sums, stream);
+    if (rows == 32) return launch_split<32, SUM>(C, sums, stream);
+  }
+  if (rows == 64) return launch_split<64, SUM>(C, sums, stream);
+  if (rows == 128) return launch_split<128, SUM>(C, sums, stream);
+  if constexpr (SUM == MM_WHOLE)
+    if (is_wide(C)) switch (C.e.act) {
+        case ACT_RELU: return launch_kind<ACT_RELU, SUM>(calls, sums, stream);
+        case ACT_GELU: return launch_kind<ACT_GELU, SUM>(calls, sums, stream);
+        case ACT_SILU: return launch_kind<ACT_SILU, SUM>(calls, sums, stream);
+        default: return launch_kind<ACT_NONE, SUM>(calls, sums, stream);
+      }
+  return launch_kind<MM_ANY, SUM>(calls, sums, stream);
+}
+
 int mm_launch(const MMCall* calls, int count, const MMColumnSums* sums, cudaStream_t stream) {
   const MMCall& C = calls[0];
-  const bool sum = C.pairs > 1, wide = !sum && is_wide(C);
   if (count == 2) {
+    const int sum = sum_of(C, C.k), other = sum_of(calls[1], calls[1].k);
     // One launch where one kernel serves both, their tiles together fill the SMs
     // once at most, and the longer tile takes less than the two launches with
     // their summed axes shared among CTAs (2000 x 304 x 2000 bf16: 20 us as one, 35
@@ -1161,9 +1235,10 @@ int mm_launch(const MMCall* calls, int count, const MMColumnSums* sums, cudaStre
       longest = longest > blocks ? longest : blocks;
       apart += blocks / (rows ? split_of(D, rows) : 1);
     }
+    const bool parts = sum == MM_PARTS, whole = sum == MM_WHOLE && other == MM_WHOLE, wide = whole && is_wide(C);
     // a launch more costs what eight blocks take, with planes three
-    if (tiles > device_sm_count() || longest > apart + (sum ? 3 : 8) || (calls[1].pairs > 1) != sum ||
-        (!sum && is_wide(calls[1]) != wide)) {
+    if (tiles > device_sm_count() || longest > apart + (parts ? 3 : 8) || (other == MM_PARTS) != parts ||
+        (whole && is_wide(calls[1]) != wide)) {
       const int rc = mm_launch(calls, 1, sums, stream);
       return rc ? rc : mm_launch(calls + 1, 1, nullptr, stream);
     }
@@ -1171,34 +1246,17 @@ int mm_launch(const MMCall* calls, int count, const MMColumnSums* sums, cudaStre
       const MMCall turned[2] = {calls[1], calls[0]};
       return mm_launch(turned, 2, sums, stream);
     }
+    if (parts) return launch_shape<1, 128, MM_ANY, MM_PARTS, 2>(calls, sums, stream);
+    if (!whole) return launch_shape<1, 128, MM_ANY, MM_PIECES, 2>(calls, sums, stream);
+    if (!wide) return launch_shape<1, 128, MM_ANY, MM_WHOLE, 2>(calls, sums, stream);
+    return launch_shape<1, 128, ACT_NONE, MM_WHOLE, 2>(calls, sums, stream);
   }
-  if (count == 2) {
-    if (sum) return launch_shape<1, 128, MM_ANY, true, 2>(calls, sums, stream);
-    if (!wide) return launch_shape<1, 128, MM_ANY, false, 2>(calls, sums, stream);
-    return launch_shape<1, 128, ACT_NONE, false, 2>(calls, sums, stream);
-  }
-  if (C.ortho) {
-    switch (split_rows(C)) {
-      case 64: return sum ? launch_split<64, true, true>(C, sums, stream) : launch_split<64, false, true>(C, sums, stream);
-      case 128: return sum ? launch_split<128, true, true>(C, sums, stream) : launch_split<128, false, true>(C, sums, stream);
-      default: break;
-    }
-    return sum ? launch_kind<MM_ORTHO, true>(calls, sums, stream) : launch_kind<MM_ORTHO, false>(calls, sums, stream);
-  }
-  switch (split_rows(C)) {
-    case 16: return launch_split<16, false>(C, sums, stream);
-    case 32: return launch_split<32, false>(C, sums, stream);
-    case 64: return sum ? launch_split<64, true>(C, sums, stream) : launch_split<64, false>(C, sums, stream);
-    case 128: return sum ? launch_split<128, true>(C, sums, stream) : launch_split<128, false>(C, sums, stream);
-    default: break;
-  }
-  if (sum) return launch_kind<MM_ANY, true>(calls, sums, stream);
-  if (!wide) return launch_kind<MM_ANY, false>(calls, sums, stream);
-  switch (C.e.act) {
-    case ACT_RELU: return launch_kind<ACT_RELU, false>(calls, sums, stream);
-    case ACT_GELU: return launch_kind<ACT_GELU, false>(calls, sums, stream);
-    case ACT_SILU: return launch_kind<ACT_SILU, false>(calls, sums, stream);
-    default: return launch_kind<ACT_NONE, false>(calls, sums, stream);
+  const int rows = split_rows(C);
+  const int64_t blocks = (C.k + MM_BK - 1) / MM_BK, split = rows ? split_of(C, rows) : 1;
+  switch (sum_of(C, split == 1 ? C.k : (blocks + split - 1) / split * MM_BK)) {
+    case MM_PARTS: return launch_one<MM_PARTS>(calls, rows, sums, stream);
+    case MM_PIECES: return launch_one<MM_PIECES>(calls, rows, sums, stream);
+    default: return launch_one<MM_WHOLE>(calls, rows, sums, stream);
   }
 }
 
