@@ -624,9 +624,10 @@ int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves, int64_t ro
  *   (u_a, u_b) -> (u_a cos - u_b sin, u_b cos + u_a sin),
  * a = j, b = j + rot / 2 (PSK_PAIRS_HALVES) or a = 2 j, b = 2 j + 1
  * (PSK_PAIRS_NEIGHBOURS); columns from rot on do not turn.  positions: DEVICE,
- * PSK_I32 or PSK_I64, any sign; freqs: rot / 2 f32, radians a position.  The
- * angle is the exact product reduced to a turn with an error of 2^-62 a
- * position.  Arithmetic in f32, one rounding to yt; the squares of a head are
+ * PSK_I32 or PSK_I64, any sign; freqs: rot / 2 f32, radians a position, any
+ * sign.  The angle is the exact product reduced to a turn with an error of 2^-62
+ * of one a position, for frequencies of up to 2^40 (beyond, it is finite but
+ * need not be that angle).  Arithmetic in f32, one rounding to yt; the squares of a head are
  * expected within f32's range (|x| below 2^59, and eps above 0 or |x| above
  * 2^-60).  Without turning columns positions and freqs may be NULL.  yq may be q and yk k in
  * place (same type and strides); no other overlap.  hq or hk may be 0.  dim

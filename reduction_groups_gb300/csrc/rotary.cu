@@ -49,12 +49,17 @@ struct RotParams {
 };
 
 // f / 2 pi as a fraction of 2^64 (mod 1): the quotient as a pair of doubles.
+// Of |f|, whose fraction of a turn is exact (of a small negative one it would
+// be 1 - a little, rounded to 2^-53), and negated in integers.  L is off by
+// 2^-110, so up to 2^40 radians the fraction is off by about a step of 2^-64.
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
   const double H = 0.15915494309189535, L = -9.839338337591243e-18;
-  const double x = (double)f;
+  const double x = fabs((double)f);
   const double hi = x * H, lo = fma(x, H, -hi) + x * L;
   const double frac = hi - floor(hi);
-  return __double2ull_rd(frac * 18446744073709551616.0) + (uint64_t)__double2ll_rn(lo * 18446744073709551616.0);
+  const uint64_t turn =
+      __double2ull_rd(frac * 18446744073709551616.0) + (uint64_t)__double2ll_rn(lo * 18446744073709551616.0);
+  return f < 0.0f ? 0 - turn : turn;
 }
 
 struct RotTable {
