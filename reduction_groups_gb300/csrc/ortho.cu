@@ -55,7 +55,7 @@ struct OrthoShape {
   int32_t xt, tall, blocks, leaves;
   double eps;
   double* sums;                 // [leaf][block]
-  float* factors;               // [leaf]
+  float2* factors;              // [leaf]: two, applied one after the other
   MMLeaf* table;
   uint16_t* x;                  // [leaf][part][m][ldn]
 };
@@ -64,7 +64,7 @@ struct OrthoShape {
 // of a row, which are on their way at once, 64 bits beyond.  Warps take such
 // pieces in turn (whole rows left few warps at work: 18 of [145, 4299] 58 us).
 // A share whose squares leave f32 (elements above 2^60 or so) is taken again
-// times 2^-64.
+// times 2^-80, which leaves room for 2^32 squares of the largest f32.
 constexpr int ORTHO_PIECE = 1024;
 
 template <int XT, bool VEC>
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(256) ortho_sum_kernel(const __grid_constant__ 
     const int64_t r = i / across, c = (i - r * across) * ORTHO_PIECE;
     const float s = ortho_share<XT, VEC>(x, r * ld, c, S.cols, lane, 1.0f);
     if (s > 3.4028234663852886e38f)
-      total += (double)ortho_share<XT, VEC>(x, r * ld, c, S.cols, lane, 5.421010862427522e-20f) * 3.402823669209385e38;
+      total += (double)ortho_share<XT, VEC>(x, r * ld, c, S.cols, lane, 8.271806125530277e-25f) * 1.461501637330903e48;
     else total += (double)s;
   }
 #pragma unroll
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(256) ortho_factor_kernel(const __grid_constant
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   if (lane == 0) {
-    S.factors[leaf] = (float)((double)ORTHO_SCALE / (sqrt(s) + S.eps));
+    S.factors[leaf] = ortho_factors((double)ORTHO_SCALE / (sqrt(s) + S.eps));
     S.table[leaf] = MMLeaf{T.y[leaf], T.ldy[leaf], T.vec[leaf]};
   }
 }
@@ -175,12 +175,12 @@ __global__ void __launch_bounds__(256) ortho_begin_kernel(const __grid_constant_
     const int64_t left = S.cols - c;
     load8<XT, VEC>(x, r * ld + c, r < S.rows && left > 0 ? (left < 8 ? (int)left : 8) : 0, v[h]);
   }
-  const float f = S.factors[leaf];
+  const float2 f = S.factors[leaf];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      v[h][k] *= f;
+      v[h][k] = v[h][k] * f.x * f.y;
       if constexpr (TALL) tile[g + k][i + 32 * h] = v[h][k];
     }
   if constexpr (TALL) __syncthreads();
@@ -233,7 +233,7 @@ static OrthoLayout ortho_layout(int32_t leaves, int64_t rows, int64_t cols, int3
     return o;
   };
   L.sums = take((uint64_t)leaves * ORTHO_SUM_BLOCKS * 8);
-  L.factors = take((uint64_t)leaves * 4);
+  L.factors = take((uint64_t)leaves * 8);
   L.table = take((uint64_t)leaves * sizeof(MMLeaf));
   L.x0 = take((uint64_t)leaves * ORTHO_PARTS * L.xsize * 2);
   L.x1 = take((uint64_t)leaves * ORTHO_PARTS * L.xsize * 2);
@@ -368,7 +368,7 @@ extern "C" int psk_orthogonalize(const psk_ortho_leaf* leaves, int32_t n_leaves,
   const int64_t blocks = (rows * ((cols + ORTHO_PIECE - 1) / ORTHO_PIECE) + 15) / 16;     // two pieces a warp at least
   S.blocks = (int32_t)(blocks < ORTHO_SUM_BLOCKS ? blocks : ORTHO_SUM_BLOCKS);
   S.eps = eps;
-  S.sums = (double*)(ws + L.sums), S.factors = (float*)(ws + L.factors);
+  S.sums = (double*)(ws + L.sums), S.factors = (float2*)(ws + L.factors);
   S.table = (MMLeaf*)(ws + L.table), S.x = (uint16_t*)(ws + L.x0);
   bool vec = cols % 8 == 0;
   for (int i = 0; i < n_leaves; ++i) vec = vec && rows_vec8(leaves[i].x, xt, leaves[i].ldx, rows);

@@ -114,19 +114,19 @@ __global__ void __launch_bounds__(OS_THREADS, 1)
   for (uint32_t i = threadIdx.x; i < 2 * x_plane / 16; i += OS_THREADS) ((uint4*)xs)[i] = make_uint4(0, 0, 0, 0);
   float s = 0.0f, big = 0.0f;
   os_each(P, x, ldx, [&](int, int, float v) {
-    // squares that would leave f32 are taken times 2^-128
+    // squares that would leave f32 are taken times 2^-160 (64 of the largest: 2^102)
     const bool over = fabsf(v) > 1.1e15f;
-    const float u = over ? v * 5.421010862427522e-20f : 0.0f, w = over ? 0.0f : v;
+    const float u = over ? v * 8.271806125530277e-25f : 0.0f, w = over ? 0.0f : v;
     big = fmaf(u, u, big), s = fmaf(w, w, s);
   });
-  double total = (double)s + (double)big * 3.402823669209385e38;
+  double total = (double)s + (double)big * 1.461501637330903e48;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
   if (lane == 0) part[warp] = total;
   __syncthreads();
   total = 0.0;
   for (int w = 0; w < OS_THREADS / 32; ++w) total += part[w];
-  const float f = (float)(1024.0 / (sqrt(total) + P.eps));
+  const float2 f = ortho_factors(1024.0 / (sqrt(total) + P.eps));
   // Where element (row, column) of the leaf stands in X.
   const auto at = [&](int lr, int lc) {
     const int r = P.tall ? lc : lr, c = P.tall ? lr : lc;
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(OS_THREADS, 1)
   };
   os_each(P, x, ldx, [&](int lr, int lc, float v) {
     if (lr >= P.rows || lc >= P.cols) return;
-    const float t = v * f;
+    const float t = v * f.x * f.y;
     const uint32_t w = f32x2_to_f16x2(t, 0.0f);
     char* q = at(lr, lc);
     *(uint16_t*)q = (uint16_t)w;
