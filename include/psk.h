@@ -540,9 +540,10 @@ int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int64_t cols, 
  * result of bf16 operands is off by about 2.4e-6 of the sum of its terms'
  * magnitudes at most.  The order is fixed by the sizes, types, the rows'
  * alignment and the device's SMs.  z, act and the residual's sum are f32; y and z are rounded
- * once.  PSK_ACT_GELU is z Phi(z), its negative tail included to 2^-20 of its
- * value, where x, w, y, z, bias and residual are all bf16 to 2^-16; at
- * z = +-inf an activation is its limit.  A row of
+ * once.  PSK_ACT_GELU is z Phi(z) and PSK_ACT_SILU z / (1 + exp(-z)), their
+ * negative tails included to 2^-20 of their value, where x, w, y, z, bias and
+ * residual are all bf16 to 2^-16 (values below 2^-126 may be 0); at z = +-inf
+ * an activation is its limit.  A row of
  * x or a column of w that holds an infinity or a NaN gives infinities or NaNs
  * in its own row or column of z (NaN also where the exact sum is infinite, if
  * an operand is f32).

@@ -93,6 +93,18 @@ __device__ __forceinline__ float2 sigmoid(float2 z) {
   return rcp_pair(__fadd2_rn(pair_of(1.0f), e));
 }
 
+// silu far below zero, z exp(z) with the exponential in two halves: as one it
+// would leave ex2's range (2^-126) where the product is still in f32's.
+__device__ __forceinline__ float silu_far(float z) {
+  z = max_nan(z, -120.0f);
+  const float a = z * 0.72134751081466675f;                               // log2(e) / 2
+  const float al = fmaf(z, 9.62981494545545e-9f, fmaf(z, 0.72134751081466675f, -a));
+  float h = ex2_approx(a);
+  h = fmaf(h, al * 0.69314718f, h);
+  return z * h * h;
+}
+constexpr float SILU_FAR = -64.0f;         // from here on 1 / (1 + exp(-z)) is exp(z) (act_all looks for such z)
+
 template <int ACT, bool FINE>
 __device__ __forceinline__ float2 act_value(float2 z) {
   if constexpr (ACT == ACT_RELU) return make_float2(max_nan(z.x, 0.0f), max_nan(z.y, 0.0f));

@@ -167,6 +167,17 @@ __device__ __forceinline__ void turn16(float* v, int lane) {
 template <int ACT, bool FINE, int N>
 __device__ __forceinline__ void act_all(float* v) {
   if constexpr (ACT != ACT_NONE) {
+    if constexpr (ACT == ACT_SILU) {       // one test for all: values this far out are rare
+      float low = v[0];
+#pragma unroll
+      for (int k = 1; k < N; ++k) low = fminf(low, v[k]);
+      if (low < SILU_FAR) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          v[k] = v[k] < SILU_FAR ? silu_far(v[k]) : act_value<ACT, FINE>(make_float2(v[k], v[k])).x;
+        return;
+      }
+    }
 #pragma unroll
     for (int k = 0; k < N; k += 2) {
       const float2 a = act_value<ACT, FINE>(make_float2(v[k], v[k + 1]));
