@@ -40,3 +40,15 @@ def test_gaussian_matrices(rows, cols, dtype):
     for x, y in zip(xs, ys):
         want = _definition(x)
         assert float((y.double() - want).norm() / want.norm()) <= limit
+
+
+@pytest.mark.parametrize("co", [[(7.9, 0.0, 0.0), (0.1, 0.0, 0.0)], [(-7.9, 0.0, 0.0), (1.0, -1.0 / 64, 0.0)],
+                                [(2.5, 0.0, 0.0), (0.5, 0.25, 1.5)]])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 50), (1, 700), (2, 200)])
+def test_singular_values_up_to_the_stated_limit(co, rows, cols):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import reduction_groups_gb300 as R
+    from tests.test_gpu_orthogonalize import _run
+
+    _run(R, 2, rows, cols, "f32", "f32", len(co), co)
