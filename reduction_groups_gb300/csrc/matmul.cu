@@ -17,8 +17,14 @@
 //
 // f32 operands come as planes of 16-bit parts; the launch lists the products
 // of planes to be added, the smallest first: a stage holds every plane of its
-// part of the summed axis, each product of planes goes into the same
-// accumulator.
+// part of the summed axis, the products of planes but the last go into an
+// accumulator of their own.
+//
+// The tensor core's additions truncate, so sums of f32 operands, and long ones
+// of 16-bit operands, leave their accumulators piece by piece and are added up
+// in the epilogue warps' registers (MM_PARTS, MM_PIECES; [8192, 4096] x 4096,
+// f32 result, by pieces: 188 us under ncu, tensor pipe 63 % of cycles, as with
+// whole sums of bf16 results).
 //
 // Every wait is bounded: a role that gives up records it in the device status
 // and leaves its loop, all meet at the end of the kernel.
