@@ -32,6 +32,8 @@ static int current_device() {
   return dev;
 }
 
+void bind_context() { cudaSetDevice(current_device()); }
+
 int device_sm_count() {
   static int cache[PSK_MAX_DEVICES] = {};
   const int dev = current_device();

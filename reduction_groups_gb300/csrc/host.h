@@ -15,6 +15,9 @@ int check_launch(const char* what);
 // thread).
 constexpr int PSK_MAX_DEVICES = 64;
 int device_sm_count();
+// Make the current device's context the calling thread's, for driver calls: a
+// host thread's first runtime call that needs one would do it.
+void bind_context();
 // Raise `kernel`'s dynamic shared-memory limit to `bytes` on the current
 // device, once per device; `done` is the call site's per-device flag array.
 void smem_limit_once(const void* kernel, int bytes, bool* done);
