@@ -596,8 +596,8 @@ int psk_linear_backward(const void* ct, int32_t ct_t, int64_t ldc, const void* x
  * take one part of each factor, for f32 two; the iteration amplifies their
  * roundings.  Five steps of (3.4445, -4.7750, 2.0315), Gaussian matrices,
  * relative to ||y||: stored in bf16, y is off by 5e-3 at most where the shorter
- * side is 64 or more (2e-3 at 2048; 1.7e-3 of each is the storage's) and by up
- * to 2e-2 for shorter ones; in f32 by 1e-5 at most.  Coefficients that drive an
+ * side is 64 or more (2e-3 at 2048; 1.7e-3 of each is the storage's), by 1e-2
+ * from 8 on and up to 3e-2 below; in f32 by 1e-5 at most, by up to 1e-4 below 8.  Coefficients that drive an
  * element of X, X X^T or b X X^T + c (X X^T)^2 to 63 or beyond (a singular value
  * of X to 7.9) overflow.  The norm's squares are f32: elements
  * below 2^-63 may count as 0 in it, and ||G||_F + eps of at least 2^-100 is
