@@ -16,10 +16,11 @@
 // the products take the first part, and A and B one part.  The iteration
 // amplifies their roundings: beside bf16's own rounding (1.7e-3 of the result's
 // size) a Gaussian matrix is off by 1.1e-3 (4096 x 4096) to 3.7e-3 (64 x 192),
-// shorter sides below 64 by up to 1e-2, below 8 by up to 3e-2; a few strong directions over noise by 2e-4 to
-// 2.4e-3 at the same sizes.  (X in one part: 3e-3 to 4e-3 where two give 3e-4 to
-// 1e-3.)  For a result stored in f32 A and B are two parts as well and every
-// product three products of parts: off by 1e-6 to 5e-6 (below 8 by up to 7e-5).
+// shorter sides below 64 by up to 1e-2, below 8 by up to 3e-2; one of a few
+// strong directions over noise by 2e-4 (4096 x 4096) to 2.4e-3 (64 x 192).  (X in
+// one part: 3e-3 to 4e-3 where two give 3e-4 to 1e-3.)  For a result stored in
+// f32 A and B are two parts as well and every product three products of parts:
+// off by 1e-6 to 5e-6 (below 8 by up to 7e-5).
 #include <algorithm>
 #include <vector>
 
