@@ -534,7 +534,7 @@ int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int64_t cols, 
  * The products of a sum are exact (an f32 operand enters as three bf16 parts,
  * products of parts below 2^-24 of the largest left out) and added in f32: by
  * the tensor core, which truncates (at most 17 f32 steps of the sum so far for
- * each 16 terms; one on average), and with an f32 operand every 256 terms by
+ * each 16 terms), and with an f32 operand every 256 terms by
  * one rounded addition, with bf16 operands every 1024 where the result (y or z)
  * is f32 and the sum longer than 2048 terms, or it is longer than 65536: an f32
  * result of bf16 operands is off by about 2.4e-6 of the sum of its terms'
