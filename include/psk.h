@@ -534,12 +534,12 @@ int psk_policy_loss(const void* logits, int32_t lt, int64_t rows, int64_t cols, 
  * The products of a sum are exact (an f32 operand enters as three bf16 parts,
  * products of parts below 2^-24 of the largest left out) and added in f32: by
  * the tensor core, which truncates (at most 17 f32 steps of the sum so far for
- * each 16 terms), and with an f32 operand every 256 terms by
- * one rounded addition, with bf16 operands every 1024 where the result (y or z)
- * is f32 and the sum longer than 2048 terms, or it is longer than 65536: an f32
- * result of bf16 operands is off by about 2.4e-6 of the sum of its terms'
- * magnitudes at most.  The order is fixed by the sizes, types, the rows'
- * alignment and the device's SMs.  z, act and the residual's sum are f32; y and z are rounded
+ * each 16 terms), and with an f32 operand every 256 terms by one rounded
+ * addition, with bf16 operands every 1024 where the result (y or z) is f32 and
+ * the sum longer than 2048 terms, or it is longer than 65536 (measured, f32
+ * results of bf16 terms of one sign: off by up to 3.3e-6 of their sum at 2048
+ * terms, by about 1e-6 beyond).  The order is fixed by the sizes, types, the
+ * rows' alignment and the device's SMs.  z, act and the residual's sum are f32; y and z are rounded
  * once.  PSK_ACT_GELU is z Phi(z) and PSK_ACT_SILU z / (1 + exp(-z)), their
  * negative tails included to 2^-20 of their value, where x, w, y, z, bias and
  * residual are all bf16 to 2^-16 (values below 2^-126 may be 0); at z = +-inf
